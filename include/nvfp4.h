@@ -62,7 +62,8 @@ enum nvfp4_mode {
     NVFP4_MODE_SOAR = 3
 };
 
-enum nvfp4_dtype { NVFP4_DTYPE_BF16 = 0, NVFP4_DTYPE_F32 = 1 };
+/* MXFP8 is a form of activations (the layer operators below); no entry point of the quantiser takes it. */
+enum nvfp4_dtype { NVFP4_DTYPE_BF16 = 0, NVFP4_DTYPE_F32 = 1, NVFP4_DTYPE_MXFP8 = 2 };
 
 /* How the SOAR search picks each candidate's two E4M3 reconstruct scales Delta_d (SOAR page, decoupled
  * search: "the two E4M3 values nearest the current value"). CJSO: the pair around the unrounded CJSO
@@ -83,7 +84,8 @@ enum nvfp4_error {
     NVFP4_ERR_TOO_LARGE = -5,   /* nvfp4_quantize_noalloc: the call needs more scratch than its fixed
                                    device array holds */
     NVFP4_ERR_UNSUPPORTED = -6  /* nvfp4_matmul / nvfp4_matmul_ex on a capturing stream with a shape
-                                   that takes the 128 x 128 or 256 x 128 output tiles */
+                                   that takes the 128 x 128 or 256 x 128 output tiles; a layer operator on
+                                   a capturing stream that needs scratch and was given none */
 };
 
 /* In-band status bits, written to nvfp4_stats_t.status by the device. */
@@ -289,6 +291,54 @@ int nvfp4_gptq(const void *W, int dtype, int64_t rows, int64_t cols, const doubl
 
 /* Device scratch one nvfp4_gptq call needs (0 for an invalid shape). */
 size_t nvfp4_gptq_workspace_bytes(int64_t rows, int64_t cols);
+
+/* ------------------------------------------------------------------------------------ layer operators
+ *
+ * What a layer computes around its NVFP4 products, forward and backward.
+ *
+ * All of them: device pointers, row-major; `ld*` is the number of elements from a row of an operand to the
+ * next (>= its columns; not looked at for fewer than two rows), the outputs are contiguous. Pointers are
+ * aligned to their element; rows need no more alignment than that (16-byte aligned rows are fastest). rows = 0
+ * is allowed: nothing is written but the column sums (dweight, dbias), which are zeros. rows <= 2^23 and
+ * rows * columns < 2^35 (else NVFP4_ERR_SHAPE). Outputs may not overlap inputs unless a call says so. Sums
+ * and statistics are binary32, in an order that does not depend on timing; each output is rounded once.
+ * Nothing is allocated when `workspace` (256-byte aligned) is given or none is needed; without it scratch
+ * is taken from a stream-ordered pool, except on a capturing stream (NVFP4_ERR_UNSUPPORTED).
+ *
+ * MXFP8 ([rows][cols] code bytes and [rows][ceil(cols/32)] scale bytes): blocks of 32 consecutive columns
+ * (the last may be shorter); a code is E4M3, a scale byte b is 2^(b-127) (E8M0), and a value is their
+ * product. The scale written is the smallest power of two, 2^-127 at least, with max|v| <= 448 * scale, so
+ * nothing saturates and a value is within half an E4M3 step. Zeros: b = 0. A block holding a NaN or an infinity:
+ * b = 255, codes 0x7F, and all its values read as NaN. */
+
+/* MXFP8 codes and scales of x (dtype bf16 or fp32, [rows][cols], any cols >= 1), as activations are kept in
+ * between a forward and a backward pass; and the values back, rounded to bf16 or fp32 (both hold every value
+ * whose scale is at least 2^-117). */
+int nvfp4_mxfp8_quantize(const void *x, int64_t ldx, int dtype, int64_t rows, int64_t cols, uint8_t *codes,
+                         uint8_t *scales, void *stream);
+int nvfp4_mxfp8_dequantize(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t rows, int64_t cols,
+                           void *y, int y_dtype, void *stream);
+
+/* Root-mean-square norm with the residual's addition: h = x + residual, y = h * (mean(h^2) + eps)^(-1/2) *
+ * weight over each row of cols >= 1 columns. x, residual and sum_out have `dtype` (bf16 or fp32), weight [cols]
+ * has weight_dtype. sum_out gets h rounded to dtype (y is computed from h unrounded) and may be `residual`
+ * itself (contiguous); residual and sum_out are both given or both NULL (then h = x). y is bf16, fp32 or
+ * MXFP8 (y_dtype; y_scales for MXFP8 alone, else NULL). eps >= 0. */
+int nvfp4_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight, int dtype,
+                   int weight_dtype, int64_t rows, int64_t cols, float eps, void *sum_out, void *y,
+                   uint8_t *y_scales, int y_dtype, void *stream);
+
+/* Gradient of nvfp4_rms_norm at h, given dy at y and (nullable) dh at h from its other uses:
+ *   dx = q * (weight dy) - h q^3 mean(weight dy h) + dh with q = (mean(h^2) + eps)^(-1/2): the gradient at x
+ *        and at the residual alike, of `dtype` (bf16 or fp32), as dy and dh;
+ *   dweight [cols] fp32 = the sum over rows of dy h q.
+ * h is of `dtype` (h_dtype equal to it, h_scales NULL) or MXFP8 (a checkpoint of it). Scratch:
+ * nvfp4_rms_norm_grad_workspace_bytes. */
+int nvfp4_rms_norm_grad(const void *dy, int64_t lddy, const void *h, int64_t ldh, const uint8_t *h_scales,
+                        int h_dtype, const void *weight, const void *dh, int64_t lddh, int dtype,
+                        int weight_dtype, int64_t rows, int64_t cols, float eps, void *dx, float *dweight,
+                        void *workspace, size_t workspace_bytes, void *stream);
+size_t nvfp4_rms_norm_grad_workspace_bytes(int64_t rows, int64_t cols);
 
 /* Text of an nvfp4_error value. */
 const char *nvfp4_status_string(int status);

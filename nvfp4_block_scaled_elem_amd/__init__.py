@@ -86,6 +86,18 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_gptq.restype = i32
         L.nvfp4_gptq_workspace_bytes.argtypes = [i64, i64]
         L.nvfp4_gptq_workspace_bytes.restype = ctypes.c_size_t
+        sz, f32 = ctypes.c_size_t, ctypes.c_float
+        L.nvfp4_rms_norm.argtypes = [vp, i64, vp, i64, vp, i32, i32, i64, i64, f32, vp, vp, vp, i32, vp]
+        L.nvfp4_rms_norm.restype = i32
+        L.nvfp4_rms_norm_grad.argtypes = [vp, i64, vp, i64, vp, i32, vp, vp, i64, i32, i32, i64, i64, f32, vp, vp, vp,
+                                          sz, vp]
+        L.nvfp4_rms_norm_grad.restype = i32
+        L.nvfp4_rms_norm_grad_workspace_bytes.argtypes = [i64, i64]
+        L.nvfp4_rms_norm_grad_workspace_bytes.restype = sz
+        L.nvfp4_mxfp8_quantize.argtypes = [vp, i64, i32, i64, i64, vp, vp, vp]
+        L.nvfp4_mxfp8_quantize.restype = i32
+        L.nvfp4_mxfp8_dequantize.argtypes = [vp, i64, vp, i64, i64, vp, i32, vp]
+        L.nvfp4_mxfp8_dequantize.restype = i32
         L.nvfp4_status_string.argtypes = [i32]
         L.nvfp4_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -368,3 +380,7 @@ def matmul(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, alpha: to
                                      workspace.numel() * workspace.element_size() if workspace is not None else 0,
                                      _stream_ptr(stream, dev)))
     return Y
+
+
+from .layer import (dequantize_mxfp8, quantize_mxfp8, rms_norm, rms_norm_grad,  # noqa: E402
+                    rms_norm_grad_workspace_bytes)

@@ -346,7 +346,7 @@ NVFP4_API const char *nvfp4_status_string(int status) {
         case NVFP4_ERR_WORKSPACE: return "workspace too small";
         case NVFP4_ERR_HIP: return "HIP launch or allocation failed";
         case NVFP4_ERR_TOO_LARGE: return "the call needs more scratch than the library's fixed device array holds";
-        case NVFP4_ERR_UNSUPPORTED: return "not supported under stream capture for this shape (128 x 128 or 256 x 128 product tiles)";
+        case NVFP4_ERR_UNSUPPORTED: return "not supported under stream capture: a product of 128 x 128 or 256 x 128 tiles, or a layer operator without the workspace it needs";
         default: return "unknown status";
     }
 }

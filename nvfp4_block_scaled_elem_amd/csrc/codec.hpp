@@ -125,6 +125,27 @@ __device__ __forceinline__ uint32_t e2m1_soft(float x) {
     return (i != 0u && __builtin_signbit(x)) ? (i | 8u) : i;
 }
 
+// 8 codes (one dword) and their scale value -> 8 dequantised weights (without alpha) as bf16 pairs.
+__device__ __forceinline__ uint4 dequant8(uint32_t c, float dv) {
+    const f32x2 q0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0);
+    const f32x2 q1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
+    const f32x2 q2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2);
+    const f32x2 q3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
+    // q*dv is exact and has at most 6 significant bits: its high 16 bits are the bf16 value. The byte
+    // permute takes bytes 2, 3 of a*dv (selectors 2, 3: the second operand) and of b*dv (6, 7: the first).
+    auto pair = [&](float a, float b) {
+        return __builtin_amdgcn_perm(__float_as_uint(b * dv), __float_as_uint(a * dv), 0x07060302u);
+    };
+    return make_uint4(pair(q0.x, q0.y), pair(q1.x, q1.y), pair(q2.x, q2.y), pair(q3.x, q3.y));
+}
+
+// Round binary32 to bf16 (nearest, ties to even; infinities stay, a NaN stays a quiet NaN).
+__device__ __forceinline__ uint16_t to_bf16(float f) {
+    const uint32_t u = __float_as_uint(f);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);
+    return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+}
+
 // ------------------------------------------------------------------------------- reciprocal
 
 // fl(1/s), the correctly rounded binary32 reciprocal, for any s. For 2^-125 <= s < 2^125 it is formed
@@ -139,6 +160,19 @@ __device__ __forceinline__ float recip_rn(float s) {
     const bool fast = s >= 0x1p-125f && s < 0x1p125f;
     if (__builtin_amdgcn_ballot_w64(!fast) != 0) return fast ? r : 1.0f / s;
     return r;
+}
+
+// --------------------------------------------------------------------------------- wave sum
+
+// Wave sum on the VALU (DPP; the total ends in lane 63).
+__device__ __forceinline__ float wave_sum_f32(float x) {
+    x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0xB1, 0xF, 0xF, false));
+    x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x4E, 0xF, 0xF, false));
+    x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x141, 0xF, 0xF, false));
+    x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x140, 0xF, 0xF, false));
+    x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x142, 0xA, 0xF, false));
+    x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x143, 0xC, 0xF, false));
+    return x;
 }
 
 // ------------------------------------------------------------------------ exact double-double

@@ -53,27 +53,6 @@ struct TileCfg {
 };
 constexpr int kLdsStride = kBK + 8;  // bf16 per LDS row: the padding spreads the rows a wave reads over the banks
 
-// 8 codes (one dword) and their scale value -> 8 dequantised weights (without alpha) as bf16 pairs.
-__device__ __forceinline__ uint4 dequant8(uint32_t c, float dv) {
-    const f32x2 q0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 0);
-    const f32x2 q1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 1);
-    const f32x2 q2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 2);
-    const f32x2 q3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c, 1.0f, 3);
-    // q*dv is exact and has at most 6 significant bits: its high 16 bits are the bf16 value. The byte
-    // permute takes bytes 2, 3 of a*dv (selectors 2, 3: the second operand) and of b*dv (6, 7: the first).
-    auto pair = [&](float a, float b) {
-        return __builtin_amdgcn_perm(__float_as_uint(b * dv), __float_as_uint(a * dv), 0x07060302u);
-    };
-    return make_uint4(pair(q0.x, q0.y), pair(q1.x, q1.y), pair(q2.x, q2.y), pair(q3.x, q3.y));
-}
-
-// Round binary32 to bf16 (nearest, ties to even; infinities stay, a NaN stays a quiet NaN).
-__device__ __forceinline__ uint16_t to_bf16(float f) {
-    const uint32_t u = __float_as_uint(f);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);
-    return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
-}
-
 template <bool OUTF32>
 __device__ __forceinline__ void store_y(void *Y, int64_t idx, float v) {
     if (OUTF32)
@@ -386,17 +365,6 @@ __global__ __launch_bounds__(kSkinnyThreads) void k_w4a16_skinny(const uint16_t 
 #endif
 constexpr int kGemvThreads = NVFP4_GEMV_THREADS;
 constexpr int kGemvMaxM = NVFP4_GEMV_MAX_M;
-
-// Wave sum on the VALU (DPP; the total ends in lane 63).
-__device__ __forceinline__ float wave_sum_f32(float x) {
-    x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0xB1, 0xF, 0xF, false));
-    x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x4E, 0xF, 0xF, false));
-    x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x141, 0xF, 0xF, false));
-    x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x140, 0xF, 0xF, false));
-    x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x142, 0xA, 0xF, false));
-    x += __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), 0x143, 0xC, 0xF, false));
-    return x;
-}
 
 // Each wave owns kGemvRows consecutive rows n (one by default: with 16 waves per work-group the most
 // loads are in flight) and, before anything else, requests all of their codes and scales (lane l takes

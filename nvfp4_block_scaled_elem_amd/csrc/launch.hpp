@@ -117,6 +117,31 @@ hipError_t launch_stats(const void *W, bool f32, int64_t nblk, const uint8_t *co
 size_t gptq_workspace_bytes(int64_t rows, int64_t cols);
 hipError_t launch_gptq(const void *W, bool f32, int64_t rows, int64_t cols, const double *H, double percdamp,
                        uint8_t *codes, uint8_t *scales, float *alpha, void *workspace, hipStream_t stream);
+// ---- layer operators (norm_kernels.hip) ----
+
+enum { kOutBf16 = 0, kOutF32 = 1, kOutMx = 2 };
+// One call of the norm (x, r = residual or null, h = their sum, y) or of its gradient (x = h plain or
+// MXFP8, dy, r = the gradient at h or null, y = dx). ld*: elements between rows; h, y and every scale array are
+// contiguous.
+struct NormArgs {
+    const void *x, *r, *w, *dy;
+    const uint8_t *xs;  // gradient: scale bytes of an MXFP8 h
+    void *y, *h;
+    uint8_t *ys;  // norm: scale bytes of an MXFP8 y
+    int64_t rows, cols, ldx, ldr, lddy;
+    float eps;
+    int w_f32, out;
+};
+hipError_t launch_rms_norm(const NormArgs &p, bool f32, hipStream_t stream);
+size_t rms_norm_grad_workspace(int64_t rows, int64_t cols);
+hipError_t launch_rms_norm_grad(const NormArgs &p, bool f32, bool mx, float *dw, float *ws, hipStream_t stream);
+// out[c] = sum of part[r][c] over r < rows, in a fixed order (zeros for no rows).
+hipError_t launch_column_sum(const float *part, int64_t rows, int64_t cols, float *out, hipStream_t stream);
+hipError_t launch_mx_quantize(const void *x, bool f32, int64_t rows, int64_t cols, int64_t ldx, uint8_t *codes,
+                              uint8_t *scales, hipStream_t stream);
+hipError_t launch_mx_dequantize(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t rows, int64_t cols,
+                                void *y, bool f32, hipStream_t stream);
+
 hipError_t launch_dequant(const uint8_t *codes, const uint8_t *scales, const float *alpha, int64_t nblk, void *out,
                           bool out_f32, hipStream_t stream);
 

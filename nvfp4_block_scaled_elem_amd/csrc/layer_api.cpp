@@ -1,0 +1,134 @@
+// C ABI of the layer operators (declared in include/nvfp4.h): argument checks on the host, scratch, launches.
+//
+// Kernels per call (all on the caller's stream):
+//   nvfp4_rms_norm        : k_rms_norm, or k_rms_norm_long beyond 16384 columns
+//   nvfp4_rms_norm_grad   : k_rms_norm_grad -> k_column_sum (beyond 16384 columns: k_rms_norm_grad_long ->
+//                           k_rms_norm_dw_long -> k_column_sum)
+//   nvfp4_mxfp8_quantize / nvfp4_mxfp8_dequantize : one kernel each
+#include <hip/hip_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include "launch.hpp"
+
+#define NVFP4_API extern "C" __attribute__((visibility("default")))
+
+namespace {
+
+using nvfp4::NormArgs;
+
+// 2^35 elements, and 2^23 rows: a row's 256 threads then stay below 2^32 threads per grid.
+constexpr int64_t kMaxElems = (int64_t)1 << 35;
+constexpr int64_t kMaxRows = (int64_t)1 << 23;
+
+bool aligned(const void *p, unsigned a) { return ((uintptr_t)p & (a - 1)) == 0; }
+bool plain_dtype(int t) { return t == NVFP4_DTYPE_BF16 || t == NVFP4_DTYPE_F32; }
+unsigned width(int t) { return t == NVFP4_DTYPE_BF16 ? 2u : t == NVFP4_DTYPE_F32 ? 4u : 1u; }
+
+// NVFP4_OK for a [rows][cols] operand of rows >= 0 with `ld` elements between rows.
+int check_shape(int64_t rows, int64_t cols) {
+    if (rows < 0 || cols <= 0) return NVFP4_ERR_INVALID_ARG;
+    const int64_t padded = (cols + 31) / 32 * 32;
+    if (rows > kMaxRows || padded > kMaxElems || (rows > 0 && padded >= kMaxElems / rows)) return NVFP4_ERR_SHAPE;
+    return NVFP4_OK;
+}
+
+int status(hipError_t e) { return e == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP; }
+
+// Scratch of a call: the caller's workspace, or stream-ordered memory given back on the same stream. The
+// library does not allocate on a capturing stream.
+template <typename F>
+int with_scratch(void *workspace, size_t workspace_bytes, size_t need, hipStream_t st, F &&run) {
+    if (need == 0) return status(run(nullptr));
+    if (workspace) return workspace_bytes < need ? (int)NVFP4_ERR_WORKSPACE : status(run(workspace));
+    hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(st, &cs) != hipSuccess) return NVFP4_ERR_HIP;
+    if (cs != hipStreamCaptureStatusNone) return NVFP4_ERR_UNSUPPORTED;
+    void *ws = nullptr;
+    if (hipMallocAsync(&ws, need, st) != hipSuccess) return NVFP4_ERR_HIP;
+    const hipError_t e = run(ws);
+    if (hipFreeAsync(ws, st) != hipSuccess) return NVFP4_ERR_HIP;
+    return status(e);
+}
+
+}  // namespace
+
+NVFP4_API int nvfp4_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight,
+                             int dtype, int weight_dtype, int64_t rows, int64_t cols, float eps, void *sum_out,
+                             void *y, uint8_t *y_scales, int y_dtype, void *stream) {
+    if (!plain_dtype(dtype) || !plain_dtype(weight_dtype)) return NVFP4_ERR_INVALID_ARG;
+    if (!plain_dtype(y_dtype) && y_dtype != NVFP4_DTYPE_MXFP8) return NVFP4_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || !(eps < INFINITY)) return NVFP4_ERR_INVALID_ARG;
+    const int c = check_shape(rows, cols);
+    if (c != NVFP4_OK) return c;
+    if (rows == 0) return NVFP4_OK;
+    if (!x || !weight || !y || (residual != nullptr) != (sum_out != nullptr) ||
+        (y_dtype == NVFP4_DTYPE_MXFP8) != (y_scales != nullptr))
+        return NVFP4_ERR_INVALID_ARG;
+    if ((rows > 1 && ldx < cols) || (residual && rows > 1 && ldr < cols)) return NVFP4_ERR_INVALID_ARG;
+    const unsigned a = width(dtype);
+    if (!aligned(x, a) || !aligned(residual, a) || !aligned(sum_out, a) || !aligned(weight, width(weight_dtype)) ||
+        !aligned(y, width(y_dtype)))
+        return NVFP4_ERR_INVALID_ARG;
+    NormArgs p = {};
+    p.x = x, p.r = residual, p.w = weight, p.y = y, p.h = sum_out, p.ys = y_scales;
+    p.rows = rows, p.cols = cols, p.ldx = ldx, p.ldr = residual ? ldr : 0, p.eps = eps;
+    p.w_f32 = weight_dtype == NVFP4_DTYPE_F32;
+    p.out = y_dtype == NVFP4_DTYPE_MXFP8 ? nvfp4::kOutMx : y_dtype == NVFP4_DTYPE_F32 ? nvfp4::kOutF32 : nvfp4::kOutBf16;
+    return status(nvfp4::launch_rms_norm(p, dtype == NVFP4_DTYPE_F32, static_cast<hipStream_t>(stream)));
+}
+
+NVFP4_API size_t nvfp4_rms_norm_grad_workspace_bytes(int64_t rows, int64_t cols) {
+    return check_shape(rows, cols) == NVFP4_OK ? nvfp4::rms_norm_grad_workspace(rows, cols) : 0;
+}
+
+NVFP4_API int nvfp4_rms_norm_grad(const void *dy, int64_t lddy, const void *h, int64_t ldh, const uint8_t *h_scales,
+                                  int h_dtype, const void *weight, const void *dh, int64_t lddh, int dtype,
+                                  int weight_dtype, int64_t rows, int64_t cols, float eps, void *dx, float *dweight,
+                                  void *workspace, size_t workspace_bytes, void *stream) {
+    if (!plain_dtype(dtype) || !plain_dtype(weight_dtype)) return NVFP4_ERR_INVALID_ARG;
+    if (h_dtype != dtype && h_dtype != NVFP4_DTYPE_MXFP8) return NVFP4_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || !(eps < INFINITY)) return NVFP4_ERR_INVALID_ARG;
+    const int c = check_shape(rows, cols);
+    if (c != NVFP4_OK) return c;
+    const bool mx = h_dtype == NVFP4_DTYPE_MXFP8;
+    if (!dweight || !aligned(dweight, 4) || !aligned(workspace, 256)) return NVFP4_ERR_INVALID_ARG;
+    if (rows > 0) {
+        if (!dy || !h || !weight || !dx || mx != (h_scales != nullptr)) return NVFP4_ERR_INVALID_ARG;
+        if (rows > 1 && (lddy < cols || ldh < cols || (dh && lddh < cols))) return NVFP4_ERR_INVALID_ARG;
+        const unsigned a = width(dtype);
+        if (!aligned(dy, a) || !aligned(dh, a) || !aligned(dx, a) || !aligned(h, width(h_dtype)) ||
+            !aligned(weight, width(weight_dtype)))
+            return NVFP4_ERR_INVALID_ARG;
+    }
+    NormArgs p = {};
+    p.x = h, p.r = dh, p.w = weight, p.dy = dy, p.xs = h_scales, p.y = dx;
+    p.rows = rows, p.cols = cols, p.ldx = ldh, p.ldr = dh ? lddh : 0, p.lddy = lddy, p.eps = eps;
+    p.w_f32 = weight_dtype == NVFP4_DTYPE_F32;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return with_scratch(workspace, workspace_bytes, nvfp4::rms_norm_grad_workspace(rows, cols), st, [&](void *ws) {
+        return nvfp4::launch_rms_norm_grad(p, dtype == NVFP4_DTYPE_F32, mx, dweight, static_cast<float *>(ws), st);
+    });
+}
+
+NVFP4_API int nvfp4_mxfp8_quantize(const void *x, int64_t ldx, int dtype, int64_t rows, int64_t cols, uint8_t *codes,
+                                   uint8_t *scales, void *stream) {
+    if (!plain_dtype(dtype)) return NVFP4_ERR_INVALID_ARG;
+    const int c = check_shape(rows, cols);
+    if (c != NVFP4_OK) return c;
+    if (rows == 0) return NVFP4_OK;
+    if (!x || !codes || !scales || (rows > 1 && ldx < cols) || !aligned(x, width(dtype))) return NVFP4_ERR_INVALID_ARG;
+    return status(nvfp4::launch_mx_quantize(x, dtype == NVFP4_DTYPE_F32, rows, cols, ldx, codes, scales,
+                                            static_cast<hipStream_t>(stream)));
+}
+
+NVFP4_API int nvfp4_mxfp8_dequantize(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t rows,
+                                     int64_t cols, void *y, int y_dtype, void *stream) {
+    if (!plain_dtype(y_dtype)) return NVFP4_ERR_INVALID_ARG;
+    const int c = check_shape(rows, cols);
+    if (c != NVFP4_OK) return c;
+    if (rows == 0) return NVFP4_OK;
+    if (!codes || !scales || !y || (rows > 1 && ldc < cols) || !aligned(y, width(y_dtype))) return NVFP4_ERR_INVALID_ARG;
+    return status(nvfp4::launch_mx_dequantize(codes, ldc, scales, rows, cols, y, y_dtype == NVFP4_DTYPE_F32,
+                                              static_cast<hipStream_t>(stream)));
+}

@@ -1,0 +1,200 @@
+"""Layer operators: what a layer computes around its NVFP4 products, forward and backward (C ABI: the layer
+operators of ``include/nvfp4.h``). Marshalling only, like the rest of the binding.
+
+    h8, s = rms_norm(X, w, residual=R, out_dtype="mxfp8")       # s = X + R, h8 = (codes, scales)
+    dX, dw = rms_norm_grad(dY, s, w, dS=dS)
+    kept = quantize_mxfp8(A)                                    # an activation kept in 8 bits ...
+    A_hat = dequantize_mxfp8(*kept)                             # ... and read back
+
+An MXFP8 tensor is a pair (codes, scales): codes [rows, cols] ``torch.float8_e4m3fn`` and scales
+[rows, ceil(cols / 32)] ``torch.float8_e8m0fnu``, a power of two per 32 consecutive columns (uint8 tensors
+of the same bits are accepted too). Operands may have any row stride >= their columns; outputs are
+contiguous and are allocated on the call's stream: ``stream``, or the current stream of the operands' device.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import DTYPES, NVFP4Error, _check, _check_buffer, lib
+
+MXFP8 = "mxfp8"
+_MX = 2  # NVFP4_DTYPE_MXFP8
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+_SCALES = (torch.float8_e8m0fnu, torch.uint8)
+
+
+def _run(dev, stream, call):
+    """``call(raw stream)`` with the operands' device current, and the call's stream current where one is given
+    (so that outputs and scratch are allocated on it)."""
+    if stream is None:
+        if torch.cuda.current_device() == dev.index:
+            return call(torch.cuda.current_stream().cuda_stream)
+        with torch.cuda.device(dev):
+            return call(torch.cuda.current_stream().cuda_stream)
+    if stream.device != dev:
+        raise NVFP4Error(f"the stream is on {stream.device}, the operands on {dev}")
+    with torch.cuda.stream(stream):
+        return call(stream.cuda_stream)
+
+
+def _rows(t, name, dtypes, dev=None, shape=None):
+    """Checks a 2-D operand with unit column stride; returns the elements between its rows."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or not t.is_cuda or t.dtype not in dtypes:
+        raise NVFP4Error(f"{name} must be a 2-D CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
+    if dev is not None and t.device != dev:
+        raise NVFP4Error(f"{name} must be on {dev}")
+    rows, cols = t.shape
+    if shape is not None and (rows, cols) != shape:
+        raise NVFP4Error(f"{name} must be {list(shape)}, got {[rows, cols]}")
+    if rows < 2:
+        if cols > 1 and rows and t.stride(1) != 1:
+            raise NVFP4Error(f"{name} must have unit column stride")
+        return cols
+    s0, s1 = t.stride()
+    if (s1 != 1 and cols > 1) or s0 < cols:
+        raise NVFP4Error(f"{name} must have unit column stride and rows that do not overlap")
+    return s0
+
+
+def _mx_pair(t, name, dev=None, shape=None):
+    """Checks an MXFP8 pair; returns (codes, scales, elements between the codes' rows)."""
+    if not isinstance(t, (tuple, list)) or len(t) != 2:
+        raise NVFP4Error(f"{name} must be a pair (codes, scales)")
+    codes, scales = t
+    ld = _rows(codes, f"{name}'s codes", _CODES, dev, shape)
+    rows, cols = codes.shape
+    nb = -(-cols // 32)
+    if (not isinstance(scales, torch.Tensor) or scales.dtype not in _SCALES or scales.device != codes.device
+            or tuple(scales.shape) != (rows, nb) or not scales.is_contiguous()):
+        raise NVFP4Error(f"{name}'s scales must be a contiguous [{rows}, {nb}] E8M0 tensor beside its codes")
+    return codes, scales, ld
+
+
+def _vector(t, name, n, dev, dtypes=DTYPES):
+    if (not isinstance(t, torch.Tensor) or t.dtype not in dtypes or t.device != dev or tuple(t.shape) != (n,)
+            or not t.is_contiguous()):
+        raise NVFP4Error(f"{name} must be a contiguous [{n}] bf16 or fp32 tensor on {dev}")
+
+
+def _output(t, name, shape, dtype, dev):
+    if t is not None and (not isinstance(t, torch.Tensor) or tuple(t.shape) != shape or t.dtype != dtype
+                          or t.device != dev or not t.is_contiguous()):
+        raise NVFP4Error(f"{name} must be a contiguous {list(shape)} {dtype} tensor on {dev}")
+
+
+def _new_mx(rows, cols, dev):
+    return (torch.empty((rows, cols), dtype=torch.float8_e4m3fn, device=dev),
+            torch.empty((rows, -(-cols // 32)), dtype=torch.float8_e8m0fnu, device=dev))
+
+
+def _ptr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _space(workspace, need, dev):
+    """(the scratch tensor or None, its bytes): the caller's, checked, or one allocated on the call's stream."""
+    if workspace is not None:
+        _check_buffer(workspace, "workspace", need, dev)
+        return workspace, workspace.numel() * workspace.element_size()
+    return (torch.empty(need, dtype=torch.uint8, device=dev), need) if need else (None, 0)
+
+
+def quantize_mxfp8(X: torch.Tensor, *, stream=None):
+    """MXFP8 (codes, scales) of ``X`` ([rows, cols] bf16 or fp32 CUDA tensor): per 32 consecutive columns the
+    smallest power-of-two scale under which nothing saturates, and the nearest E4M3 codes (ties to even)."""
+    ld = _rows(X, "X", DTYPES)
+    rows, cols = X.shape
+    dev = X.device
+
+    def call(st):
+        codes, scales = _new_mx(rows, cols, dev)
+        _check(lib().nvfp4_mxfp8_quantize(X.data_ptr(), ld, DTYPES[X.dtype], rows, cols, codes.data_ptr(),
+                                          scales.data_ptr(), st))
+        return codes, scales
+
+    return _run(dev, stream, call)
+
+
+def dequantize_mxfp8(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bfloat16, *, stream=None) -> torch.Tensor:
+    """The values of an MXFP8 tensor as bf16 or fp32."""
+    codes, scales, ld = _mx_pair((codes, scales), "the tensor")
+    if dtype not in DTYPES:
+        raise NVFP4Error("dtype must be bf16 or fp32")
+    rows, cols = codes.shape
+    dev = codes.device
+
+    def call(st):
+        out = torch.empty((rows, cols), dtype=dtype, device=dev)
+        _check(lib().nvfp4_mxfp8_dequantize(codes.data_ptr(), ld, scales.data_ptr(), rows, cols, out.data_ptr(),
+                                            DTYPES[dtype], st))
+        return out
+
+    return _run(dev, stream, call)
+
+
+def rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *, residual=None, out_dtype=None,
+             sum_out=None, stream=None):
+    """Root-mean-square norm of ``X`` ([rows, cols] bf16 or fp32) over its rows: Y = h / sqrt(mean(h^2) + eps) *
+    weight with h = X, or X + residual. Y is of X's dtype, of ``out_dtype`` (bf16 or fp32), or an MXFP8 pair
+    (``out_dtype="mxfp8"``). Returns Y, or (Y, h) where a ``residual`` (X's shape and dtype) is given: h rounded to
+    X's dtype, in ``sum_out`` if given (which may be a contiguous ``residual``)."""
+    ldx = _rows(X, "X", DTYPES)
+    rows, cols = X.shape
+    dev = X.device
+    _vector(weight, "weight", cols, dev)
+    out_dtype = X.dtype if out_dtype is None else out_dtype
+    if out_dtype != MXFP8 and out_dtype not in DTYPES:
+        raise NVFP4Error('out_dtype must be bf16, fp32 or "mxfp8"')
+    if residual is None and sum_out is not None:
+        raise NVFP4Error("sum_out needs a residual")
+    ldr = 0 if residual is None else _rows(residual, "residual", (X.dtype,), dev, (rows, cols))
+    _output(sum_out, "sum_out", (rows, cols), X.dtype, dev)
+
+    def call(st):
+        if out_dtype == MXFP8:
+            Y = _new_mx(rows, cols, dev)
+            y, ys, yt = Y[0].data_ptr(), Y[1].data_ptr(), _MX
+        else:
+            Y = torch.empty((rows, cols), dtype=out_dtype, device=dev)
+            y, ys, yt = Y.data_ptr(), None, DTYPES[out_dtype]
+        h = sum_out
+        if residual is not None and h is None:
+            h = torch.empty((rows, cols), dtype=X.dtype, device=dev)
+        _check(lib().nvfp4_rms_norm(X.data_ptr(), ldx, _ptr(residual), ldr, weight.data_ptr(), DTYPES[X.dtype],
+                                    DTYPES[weight.dtype], rows, cols, eps, _ptr(h), y, ys, yt, st))
+        return Y if residual is None else (Y, h)
+
+    return _run(dev, stream, call)
+
+
+def rms_norm_grad_workspace_bytes(rows: int, cols: int) -> int:
+    return int(lib().nvfp4_rms_norm_grad_workspace_bytes(rows, cols))
+
+
+def rms_norm_grad(dY: torch.Tensor, S, weight: torch.Tensor, eps: float = 1e-6, *, dS=None, workspace=None,
+                  stream=None):
+    """Gradients of ``rms_norm``: ``dY`` at its output, ``S`` the h it normed (of dY's dtype, or an MXFP8 pair: a
+    checkpoint of it), ``dS`` (nullable, dY's dtype) the gradient at h from its other uses. Returns (dX,
+    dweight): dX of dY's dtype, the gradient at X and at the residual alike, and dweight [cols] fp32."""
+    lddy = _rows(dY, "dY", DTYPES)
+    rows, cols = dY.shape
+    dev = dY.device
+    if isinstance(S, (tuple, list)):
+        h, hs, ldh = _mx_pair(S, "S", dev, (rows, cols))
+        ht = _MX
+    else:
+        ldh = _rows(S, "S", (dY.dtype,), dev, (rows, cols))
+        h, hs, ht = S, None, DTYPES[dY.dtype]
+    _vector(weight, "weight", cols, dev)
+    ldds = 0 if dS is None else _rows(dS, "dS", (dY.dtype,), dev, (rows, cols))
+
+    def call(st):
+        dX = torch.empty((rows, cols), dtype=dY.dtype, device=dev)
+        dw = torch.empty(cols, dtype=torch.float32, device=dev)
+        ws, nbytes = _space(workspace, rms_norm_grad_workspace_bytes(rows, cols), dev)
+        _check(lib().nvfp4_rms_norm_grad(dY.data_ptr(), lddy, h.data_ptr(), ldh, _ptr(hs), ht, weight.data_ptr(),
+                                         _ptr(dS), ldds, DTYPES[dY.dtype], DTYPES[weight.dtype], rows, cols, eps,
+                                         dX.data_ptr(), dw.data_ptr(), _ptr(ws), nbytes, st))
+        return dX, dw
+
+    return _run(dev, stream, call)
