@@ -340,6 +340,82 @@ int nvfp4_rms_norm_grad(const void *dy, int64_t lddy, const void *h, int64_t ldh
                         void *workspace, size_t workspace_bytes, void *stream);
 size_t nvfp4_rms_norm_grad_workspace_bytes(int64_t rows, int64_t cols);
 
+/* What a product applies to z: nothing; silu(z) = z / (1 + e^-z); gelu(z) = z / (1 + e^-v) with v = 2 sqrt(2/pi) (z +
+ * 0.044715 z^3), the tanh form. */
+enum nvfp4_activation { NVFP4_ACT_NONE = 0, NVFP4_ACT_SILU = 1, NVFP4_ACT_GELU = 2 };
+
+/* The product of nvfp4_matmul with the rest of a layer's projection in its epilogue:
+ *   z [M][N] = alpha * (x Wq^T) + bias, Wq = e2m1(code) * e4m3(scale) of the weights [N][K];
+ *   y [M][N] = act(z) + residual, or, gated (with an activation, N even, F = N / 2),
+ *   y [M][F] = act(z[:, :F]) * z[:, F:] + residual: rows 0 .. F-1 of the weights are the gate.
+ * x is bf16 or MXFP8 [M][K]; bias [N] and residual (as y) bf16 or fp32, NULL for none; y bf16 or fp32; z, kept
+ * for the gradient, bf16 or MXFP8 (z_scales), NULL if not (gated and MXFP8: F % 32 == 0). K % 16 == 0; K, N
+ * <= 2^21. codes 8-byte aligned. residual may be y itself (contiguous, of y's type).
+ * Arithmetic: as nvfp4_matmul (exact products, fp32 sums), then fp32 and one rounding per output. Values of
+ * an MXFP8 x below 2^-126 may count as zero. */
+typedef struct nvfp4_linear_args {
+    const void *x;
+    int64_t ldx;
+    const uint8_t *x_scales; /* MXFP8 x alone, else NULL */
+    int x_dtype;             /* NVFP4_DTYPE_BF16 or _MXFP8 */
+    int64_t M, K, N;
+    const uint8_t *codes;
+    const uint8_t *scales;
+    const float *alpha;
+    const void *bias;
+    int bias_dtype;
+    int activation; /* enum nvfp4_activation */
+    int gated;      /* 0 or 1 */
+    const void *residual;
+    int64_t ldr;
+    int residual_dtype;
+    void *y;
+    int y_dtype;
+    void *z;
+    uint8_t *z_scales; /* MXFP8 z alone, else NULL */
+    int z_dtype;       /* NVFP4_DTYPE_BF16 or _MXFP8 */
+    void *workspace;   /* nvfp4_linear_workspace_bytes */
+    size_t workspace_bytes;
+    void *stream;
+} nvfp4_linear_args_t;
+
+int nvfp4_linear(const nvfp4_linear_args_t *args);
+
+/* Scratch of one nvfp4_linear call (fp32 sums where K is split over work-groups; often 0). z_dtype: the form
+ * in which z is kept, NVFP4_DTYPE_BF16 also where it is not. */
+size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int gated, int z_dtype);
+
+/* Gradient of nvfp4_linear, given dy (bf16, as y) at y; the residual's gradient is dy itself, the weights are
+ * frozen:
+ *   dz [M][N] bf16 = dy act'(z), or gated (dy * up * act'(gate), dy * act(gate)) for z = (gate, up);
+ *   dx [M][K] bf16 = alpha * (dz Wq), of dz as rounded (the products are exact, the sums fp32);
+ *   dbias [N] fp32 = the sum over rows of dz unrounded (NULL: not formed).
+ * z is what nvfp4_linear kept, bf16 or MXFP8 (contiguous scales). activation = none: z and dz are NULL and
+ * dz = dy. Scratch: the decoded weights and partial sums, nvfp4_linear_grad_workspace_bytes. */
+typedef struct nvfp4_linear_grad_args {
+    const void *dy;
+    int64_t lddy;
+    const void *z;
+    int64_t ldz;
+    const uint8_t *z_scales; /* MXFP8 z alone, else NULL */
+    int z_dtype;
+    int64_t M, K, N;
+    const uint8_t *codes;
+    const uint8_t *scales;
+    const float *alpha;
+    int activation;
+    int gated;
+    void *dx;
+    void *dz;
+    float *dbias;
+    void *workspace;
+    size_t workspace_bytes;
+    void *stream;
+} nvfp4_linear_grad_args_t;
+
+int nvfp4_linear_grad(const nvfp4_linear_grad_args_t *args);
+size_t nvfp4_linear_grad_workspace_bytes(int64_t M, int64_t K, int64_t N, int gated, int with_dbias);
+
 /* Text of an nvfp4_error value. */
 const char *nvfp4_status_string(int status);
 

@@ -98,6 +98,13 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_mxfp8_quantize.restype = i32
         L.nvfp4_mxfp8_dequantize.argtypes = [vp, i64, vp, i64, i64, vp, i32, vp]
         L.nvfp4_mxfp8_dequantize.restype = i32
+        L.nvfp4_linear.argtypes = [vp]
+        L.nvfp4_linear.restype = i32
+        L.nvfp4_linear_grad.argtypes = [vp]
+        L.nvfp4_linear_grad.restype = i32
+        for name in ("nvfp4_linear_workspace_bytes", "nvfp4_linear_grad_workspace_bytes"):
+            getattr(L, name).argtypes = [i64, i64, i64, i32, i32]
+            getattr(L, name).restype = sz
         L.nvfp4_status_string.argtypes = [i32]
         L.nvfp4_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -382,5 +389,5 @@ def matmul(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, alpha: to
     return Y
 
 
-from .layer import (dequantize_mxfp8, quantize_mxfp8, rms_norm, rms_norm_grad,  # noqa: E402
-                    rms_norm_grad_workspace_bytes)
+from .layer import (dequantize_mxfp8, linear, linear_grad, linear_grad_workspace_bytes,  # noqa: E402
+                    linear_workspace_bytes, quantize_mxfp8, rms_norm, rms_norm_grad, rms_norm_grad_workspace_bytes)

@@ -142,6 +142,45 @@ hipError_t launch_mx_quantize(const void *x, bool f32, int64_t rows, int64_t col
 hipError_t launch_mx_dequantize(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t rows, int64_t cols,
                                 void *y, bool f32, hipStream_t stream);
 
+// ---- products with an epilogue, and their gradients (linear_kernels.hip) ----
+
+enum { kActNone = 0, kActSilu = 1, kActGelu = 2 };
+enum { kKeepNone = 0, kKeepBf16 = 1, kKeepMx = 2 };
+// A product x [M][L] times the weights [N][L]^T with its epilogue; F = N / 2 output columns if gated, else N.
+struct LinArgs {
+    const void *x;
+    const uint8_t *xs;  // scale bytes of an MXFP8 x
+    const uint8_t *codes, *scales;
+    const uint16_t *wt;  // decoded weights in fragment order (the gradient), or null
+    const float *alpha;
+    const void *bias, *res;
+    void *y, *z;
+    uint8_t *zs;
+    float *part;  // fp32 sums of the K slices, or null
+    int64_t M, L, N, F, ldx, ldr, kslice;
+    unsigned tiles, tiles_m, tiles_n;
+    int x_mx, bias_f32, res_f32, y_f32, act, gated, keep;
+};
+struct LinGradArgs {
+    const uint16_t *dy;
+    const void *z;
+    const uint8_t *zs;
+    uint16_t *dz;
+    int64_t M, N, F, lddy, ldz;
+    int z_mx, act, gated;
+};
+struct LinPlan {
+    int mt;  // tiles of 32 rows of X per work-group; 0: the skinny kernel
+    int64_t tiles_m, tiles_n, slices, kslice;
+    size_t part_bytes;
+};
+LinPlan plan_linear(int64_t M, int64_t K, int64_t N, bool gated, int keep);
+// `part` holds the plan's part_bytes when it splits K.
+hipError_t launch_linear(const LinArgs &p, float *part, hipStream_t stream);
+size_t linear_grad_workspace(int64_t M, int64_t K, int64_t N, int64_t F, bool bias);
+hipError_t launch_linear_grad(const LinGradArgs &g, const uint8_t *codes, const uint8_t *scales, const float *alpha,
+                              int64_t K, void *dx, float *dbias, void *ws, hipStream_t stream);
+
 hipError_t launch_dequant(const uint8_t *codes, const uint8_t *scales, const float *alpha, int64_t nblk, void *out,
                           bool out_f32, hipStream_t stream);
 

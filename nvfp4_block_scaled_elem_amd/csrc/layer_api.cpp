@@ -5,6 +5,9 @@
 //   nvfp4_rms_norm_grad   : k_rms_norm_grad -> k_column_sum (beyond 16384 columns: k_rms_norm_grad_long ->
 //                           k_rms_norm_dw_long -> k_column_sum)
 //   nvfp4_mxfp8_quantize / nvfp4_mxfp8_dequantize : one kernel each
+//   nvfp4_linear          : k_lin_skinny, or k_lin_tile (-> k_lin_reduce where K is split)
+//   nvfp4_linear_grad     : (k_lin_dz with an activation or dbias; -> k_column_sum with dbias) -> k_lin_transpose ->
+//                           k_lin_tile (-> k_lin_reduce)
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -28,8 +31,9 @@ unsigned width(int t) { return t == NVFP4_DTYPE_BF16 ? 2u : t == NVFP4_DTYPE_F32
 // NVFP4_OK for a [rows][cols] operand of rows >= 0 with `ld` elements between rows.
 int check_shape(int64_t rows, int64_t cols) {
     if (rows < 0 || cols <= 0) return NVFP4_ERR_INVALID_ARG;
+    if (rows > kMaxRows || cols >= kMaxElems) return NVFP4_ERR_SHAPE;
     const int64_t padded = (cols + 31) / 32 * 32;
-    if (rows > kMaxRows || padded > kMaxElems || (rows > 0 && padded >= kMaxElems / rows)) return NVFP4_ERR_SHAPE;
+    if (rows > 0 && padded >= kMaxElems / rows) return NVFP4_ERR_SHAPE;
     return NVFP4_OK;
 }
 
@@ -131,4 +135,97 @@ NVFP4_API int nvfp4_mxfp8_dequantize(const uint8_t *codes, int64_t ldc, const ui
     if (!codes || !scales || !y || (rows > 1 && ldc < cols) || !aligned(y, width(y_dtype))) return NVFP4_ERR_INVALID_ARG;
     return status(nvfp4::launch_mx_dequantize(codes, ldc, scales, rows, cols, y, y_dtype == NVFP4_DTYPE_F32,
                                               static_cast<hipStream_t>(stream)));
+}
+
+namespace {
+
+constexpr int64_t kMaxSide = (int64_t)1 << 21;  // K and N of a product: grids stay below 65536 along y
+
+// The shapes of a product [M][K] x [N][K]^T, gated or not.
+int check_product(int64_t M, int64_t K, int64_t N, int activation, int gated) {
+    if (M < 0 || K <= 0 || N <= 0) return NVFP4_ERR_INVALID_ARG;
+    if (activation < NVFP4_ACT_NONE || activation > NVFP4_ACT_GELU) return NVFP4_ERR_INVALID_ARG;
+    if (gated != 0 && (gated != 1 || activation == NVFP4_ACT_NONE)) return NVFP4_ERR_INVALID_ARG;
+    if (K % 16 != 0 || (gated && N % 2 != 0) || K > kMaxSide || N > kMaxSide) return NVFP4_ERR_SHAPE;
+    const int c = check_shape(M, K);
+    return c != NVFP4_OK ? c : check_shape(M, N);
+}
+
+}  // namespace
+
+NVFP4_API size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int gated, int z_dtype) {
+    if (check_product(M, K, N, gated ? NVFP4_ACT_SILU : NVFP4_ACT_NONE, gated) != NVFP4_OK || M == 0) return 0;
+    return nvfp4::plan_linear(M, K, N, gated != 0, z_dtype == NVFP4_DTYPE_MXFP8 ? nvfp4::kKeepMx : nvfp4::kKeepNone)
+        .part_bytes;
+}
+
+NVFP4_API int nvfp4_linear(const nvfp4_linear_args_t *a) {
+    if (!a) return NVFP4_ERR_INVALID_ARG;
+    const int c = check_product(a->M, a->K, a->N, a->activation, a->gated);
+    if (c != NVFP4_OK) return c;
+    const int64_t F = a->gated ? a->N / 2 : a->N;
+    const bool xmx = a->x_dtype == NVFP4_DTYPE_MXFP8, zmx = a->z_dtype == NVFP4_DTYPE_MXFP8;
+    if ((!xmx && a->x_dtype != NVFP4_DTYPE_BF16) || !plain_dtype(a->y_dtype)) return NVFP4_ERR_INVALID_ARG;
+    if (a->z && !zmx && a->z_dtype != NVFP4_DTYPE_BF16) return NVFP4_ERR_INVALID_ARG;
+    if ((a->bias && !plain_dtype(a->bias_dtype)) || (a->residual && !plain_dtype(a->residual_dtype)))
+        return NVFP4_ERR_INVALID_ARG;
+    if (a->z && zmx && a->gated && F % 32 != 0) return NVFP4_ERR_SHAPE;
+    if (!aligned(a->workspace, 256)) return NVFP4_ERR_INVALID_ARG;
+    if (a->M == 0) return NVFP4_OK;
+    if (!a->x || !a->codes || !a->scales || !a->alpha || !a->y || xmx != (a->x_scales != nullptr) ||
+        (a->z && zmx) != (a->z_scales != nullptr))
+        return NVFP4_ERR_INVALID_ARG;
+    if (a->M > 1 && (a->ldx < a->K || (a->residual && a->ldr < F))) return NVFP4_ERR_INVALID_ARG;
+    if (!aligned(a->x, width(a->x_dtype)) || !aligned(a->codes, 8) || !aligned(a->alpha, 4) ||
+        !aligned(a->y, width(a->y_dtype)) || (a->bias && !aligned(a->bias, width(a->bias_dtype))) ||
+        (a->residual && !aligned(a->residual, width(a->residual_dtype))) || (a->z && !aligned(a->z, width(a->z_dtype))))
+        return NVFP4_ERR_INVALID_ARG;
+    nvfp4::LinArgs p = {};
+    p.x = a->x, p.xs = a->x_scales, p.x_mx = xmx, p.ldx = a->ldx;
+    p.codes = a->codes, p.scales = a->scales, p.alpha = a->alpha;
+    p.bias = a->bias, p.bias_f32 = a->bias_dtype == NVFP4_DTYPE_F32;
+    p.res = a->residual, p.res_f32 = a->residual_dtype == NVFP4_DTYPE_F32, p.ldr = a->residual ? a->ldr : 0;
+    p.y = a->y, p.y_f32 = a->y_dtype == NVFP4_DTYPE_F32;
+    p.z = a->z, p.zs = a->z_scales, p.keep = !a->z ? nvfp4::kKeepNone : zmx ? nvfp4::kKeepMx : nvfp4::kKeepBf16;
+    p.M = a->M, p.L = a->K, p.N = a->N, p.F = F, p.act = a->activation, p.gated = a->gated;
+    if (a->M == 1) p.ldx = a->K;
+    hipStream_t st = static_cast<hipStream_t>(a->stream);
+    const size_t need = nvfp4::plan_linear(p.M, p.L, p.N, p.gated, p.keep).part_bytes;
+    return with_scratch(a->workspace, a->workspace_bytes, need, st,
+                        [&](void *ws) { return nvfp4::launch_linear(p, static_cast<float *>(ws), st); });
+}
+
+NVFP4_API size_t nvfp4_linear_grad_workspace_bytes(int64_t M, int64_t K, int64_t N, int gated, int with_dbias) {
+    if (check_product(M, K, N, gated ? NVFP4_ACT_SILU : NVFP4_ACT_NONE, gated) != NVFP4_OK) return 0;
+    return nvfp4::linear_grad_workspace(M, K, N, gated ? N / 2 : N, with_dbias != 0);
+}
+
+NVFP4_API int nvfp4_linear_grad(const nvfp4_linear_grad_args_t *a) {
+    if (!a) return NVFP4_ERR_INVALID_ARG;
+    const int c = check_product(a->M, a->K, a->N, a->activation, a->gated);
+    if (c != NVFP4_OK) return c;
+    const int64_t F = a->gated ? a->N / 2 : a->N;
+    const bool act = a->activation != NVFP4_ACT_NONE, zmx = act && a->z_dtype == NVFP4_DTYPE_MXFP8;
+    if (act && !zmx && a->z_dtype != NVFP4_DTYPE_BF16) return NVFP4_ERR_INVALID_ARG;
+    if (zmx && a->gated && F % 32 != 0) return NVFP4_ERR_SHAPE;
+    if (!aligned(a->workspace, 256) || !aligned(a->dbias, 4)) return NVFP4_ERR_INVALID_ARG;
+    if (a->M > 0) {
+        if (!a->dy || !a->codes || !a->scales || !a->alpha || !a->dx || act != (a->z != nullptr) ||
+            act != (a->dz != nullptr) || zmx != (a->z_scales != nullptr))
+            return NVFP4_ERR_INVALID_ARG;
+        if (a->M > 1 && (a->lddy < F || (act && a->ldz < a->N))) return NVFP4_ERR_INVALID_ARG;
+        if (!aligned(a->dy, 2) || !aligned(a->codes, 8) || !aligned(a->alpha, 4) || !aligned(a->dx, 2) ||
+            !aligned(a->dz, 2) || (act && !aligned(a->z, width(a->z_dtype))))
+            return NVFP4_ERR_INVALID_ARG;
+    }
+    nvfp4::LinGradArgs g = {};
+    g.dy = static_cast<const uint16_t *>(a->dy), g.lddy = a->M > 1 ? a->lddy : F;
+    g.z = a->z, g.zs = a->z_scales, g.z_mx = zmx, g.ldz = a->M > 1 ? a->ldz : a->N;
+    g.dz = static_cast<uint16_t *>(a->dz);
+    g.M = a->M, g.N = a->N, g.F = F, g.act = a->activation, g.gated = a->gated;
+    hipStream_t st = static_cast<hipStream_t>(a->stream);
+    const size_t need = nvfp4::linear_grad_workspace(a->M, a->K, a->N, F, a->dbias != nullptr);
+    return with_scratch(a->workspace, a->workspace_bytes, need, st, [&](void *ws) {
+        return nvfp4::launch_linear_grad(g, a->codes, a->scales, a->alpha, a->K, a->dx, a->dbias, ws, st);
+    });
 }

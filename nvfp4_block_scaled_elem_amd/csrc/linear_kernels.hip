@@ -1,0 +1,788 @@
+// gfx950 W4 products with the rest of a layer's projection in their epilogue, and their gradients.
+//
+// Forward: z[M][N] = alpha (X Wq^T) + bias with Wq = e2m1(code) e4m3(scale) ([N][K], exact in bf16) and X bf16 or
+// MXFP8 (mx.hpp; exact in bf16 down to 2^-133); y = act(z) + residual, or, gated, with F = N / 2,
+//     y[:, f] = act(z[:, f]) z[:, F + f] + residual[:, f].
+// act: none, silu(z) = z s(z), gelu(z) = z s(2 c (z + 0.044715 z^3)), c = sqrt(2/pi) (the tanh form), s the logistic
+// function. z may be kept, bf16 or MXFP8.
+// Gradient: dz = dy act'(z) (gated: dy u act'(g) and dy act(g) for z = (g, u)), dX = alpha (dz Wq),
+// dbias = the column sums of dz. dz is an output rounded to bf16, and dX is the product of that rounding (the
+// matrix cores take bf16; its error, 2^-9 of a term and independent between terms, is of the size of dX's
+// own rounding); dbias adds dz unrounded.
+//
+// Products are exact and summed in fp32 on the matrix cores; everything after the sum is fp32.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "codec.hpp"
+#include "launch.hpp"
+#include "mx.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+__device__ __forceinline__ int clamp_count(int64_t left, int most) {
+    return left >= most ? most : left > 0 ? (int)left : 0;
+}
+
+// ------------------------------------------------------------------------------------- activations
+
+constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+constexpr float kGeluA = 0.044715f;
+
+// 1 / (1 + e^-v): the hardware exp2 and reciprocal, each within about one unit in the last place; v itself
+// is rounded once more in v log2(e), a relative error of |v| 2^-24 in e^-v.
+__device__ __forceinline__ float logistic(float v) {
+    return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f));
+}
+
+__device__ __forceinline__ float act_value(float z, int act) {
+    if (act == kActSilu) return z * logistic(z);
+    if (act == kActGelu) return z * logistic(kGelu2C * __builtin_fmaf(kGeluA * z * z, z, z));
+    return z;
+}
+
+// act(z) and act'(z). The gelu's derivative is 0 or 1 to fp32 beyond |z| = 30; the clamp keeps z^2 finite.
+__device__ __forceinline__ float2 act_both(float z, int act) {
+    if (act == kActSilu) {
+        const float s = logistic(z);
+        return make_float2(z * s, s * __builtin_fmaf(z, 1.0f - s, 1.0f));
+    }
+    const float c = fminf(fmaxf(z, -30.0f), 30.0f);
+    const float c2 = c * c;
+    const float s = logistic(kGelu2C * __builtin_fmaf(kGeluA * c2, c, c));
+    return make_float2(z * s, __builtin_fmaf(c * s * (1.0f - s), kGelu2C * __builtin_fmaf(3.0f * kGeluA, c2, 1.0f), s));
+}
+
+// ---------------------------------------------------------------------------------------- epilogue
+
+__device__ __forceinline__ void add8(const void *b, int f32, int64_t e, int n, float v[8]) {
+    float t[8];
+    if (f32) {
+        Raw8<float> r;
+        r.load(static_cast<const float *>(b) + e, n);
+        r.get(t);
+    } else {
+        Raw8<uint16_t> r;
+        r.load(static_cast<const uint16_t *>(b) + e, n);
+        r.get(t);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] += t[i];
+}
+
+__device__ __forceinline__ void keep8(const LinArgs &p, int64_t m, int64_t col, int n, const float v[8], int lane) {
+    if (p.keep == kKeepMx)
+        mx_put8(static_cast<uint8_t *>(p.z) + m * p.N + col,
+                p.zs + m * ((p.N + kMxBlock - 1) / kMxBlock) + col / kMxBlock, v, n, lane);
+    else
+        put8(static_cast<uint16_t *>(p.z) + m * p.N + col, v, n);
+}
+
+// Everything after alpha * sum for the output columns f .. f + 7 of row m, n of them in the matrix (0: the
+// lane only takes part in its block's maximum; a quad of lanes holds 32 consecutive columns). g: z of the
+// columns; u: their gate partners.
+__device__ __forceinline__ void epilogue8(const LinArgs &p, int64_t m, int64_t f, int n, float g[8], float u[8],
+                                          int lane) {
+    if (p.bias) {
+        add8(p.bias, p.bias_f32, f, n, g);
+        if (p.gated) add8(p.bias, p.bias_f32, p.F + f, n, u);
+    }
+    if (p.keep != kKeepNone) {
+        keep8(p, m, f, n, g, lane);
+        if (p.gated) keep8(p, m, p.F + f, n, u, lane);
+    }
+    if (p.act != kActNone)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] = act_value(g[i], p.act);
+    if (p.gated)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) g[i] *= u[i];
+    if (p.res) add8(p.res, p.res_f32, m * p.ldr + f, n, g);
+    if (p.y_f32)
+        put8(static_cast<float *>(p.y) + m * p.F + f, g, n);
+    else
+        put8(static_cast<uint16_t *>(p.y) + m * p.F + f, g, n);
+}
+
+// --------------------------------------------------------------------------------------- tile kernel
+
+// The weights go straight from memory into the matrix cores' A operand: a wave owns 64 weight rows (two
+// tiles of 32), so no weight is decoded twice in a work-group and none passes through LDS. X (32 MT rows,
+// the B operand) goes through LDS, decoded to bf16 if it is MXFP8; the work-group's four waves read it all.
+//
+// v_mfma_f32_32x32x16_bf16 sums over its 16 k slots in any order, and its 32 A rows may be any rows, so
+// both are mapped to suit the memory:
+//   k: lane l (half h = l / 32) takes k = 32 h + 8 i .. + 7 of a step of 64 for product i = 0..3: 16 contiguous
+//      bytes of codes and two scale bytes per row and step; X is read from LDS with the same map.
+//   rows: slot r = 8 b + 4 h' + i' holds weight row 16 h' + 4 b + i', because the result's element e = 4 b + i'
+//      of a lane is slot 8 b + 4 h + i': a lane ends with 16 consecutive columns of one row of X.
+// Gated: the wave's first tile holds 32 rows f, the second the rows F + f.
+constexpr int kTileThreads = 256, kStep = 64;
+
+__device__ __forceinline__ int slot_row(int r) { return 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3); }
+
+// X of one step in registers, between the loads and the LDS stores.
+template <int MT, bool XMX>
+struct XStage {
+    static constexpr int kLoads = XMX ? (MT + 1) / 2 : MT;
+    uint4 v[kLoads];
+    uint32_t sb[XMX ? kLoads : 1];
+};
+
+template <int MT, bool XMX>
+__device__ __forceinline__ void x_load(XStage<MT, XMX> &S, const LinArgs &p, int64_t m0, int64_t k0, int64_t kend, int tid) {
+    const bool whole = k0 + kStep <= kend;
+    if (XMX) {  // four threads per row, 16 codes each; k0 and kend are multiples of 16
+        const int64_t k = k0 + 16 * (tid & 3);
+        const int64_t nb = (p.L + kMxBlock - 1) / kMxBlock;
+#pragma unroll
+        for (int i = 0; i < S.kLoads; ++i) {
+            const int64_t m = min(p.M - 1, m0 + (tid >> 2) + 64 * i);
+            S.v[i] = make_uint4(0u, 0u, 0u, 0u);
+            S.sb[i] = 0u;
+            if ((MT > 1 || tid < 128) && (whole || k < kend)) {
+                S.v[i] = load16(static_cast<const uint8_t *>(p.x) + m * p.ldx + k);
+                S.sb[i] = p.xs[m * nb + k / kMxBlock];
+            }
+        }
+    } else {  // eight threads per row, 8 values each
+        const int64_t k = k0 + 8 * (tid & 7);
+#pragma unroll
+        for (int i = 0; i < S.kLoads; ++i) {
+            const int64_t m = min(p.M - 1, m0 + (tid >> 3) + 32 * i);
+            const uint16_t *q = static_cast<const uint16_t *>(p.x) + m * p.ldx + k;
+            if (whole) {
+                S.v[i] = load16(q);
+            } else {
+                Raw8<uint16_t> r;
+                r.load(q, clamp_count(kend - k, 8));
+                S.v[i] = r.a;
+            }
+        }
+    }
+}
+
+// LDS rows are 64 bf16 in eight 16-byte chunks, chunk c of row r at position c ^ (r % 8): the 32 rows that a
+// wave reads at one c then cover all banks.
+__device__ __forceinline__ int x_place(int row, int chunk) { return row * kStep + ((chunk ^ (row & 7)) << 3); }
+
+template <int MT, bool XMX>
+__device__ __forceinline__ void x_store(const XStage<MT, XMX> &S, uint16_t *xs, int tid) {
+    if (XMX) {
+        if (MT == 1 && tid >= 128) return;
+#pragma unroll
+        for (int i = 0; i < S.kLoads; ++i) {
+            const int row = (tid >> 2) + 64 * i;
+            const float s = mx_scale_value(S.sb[i]);
+            const uint32_t c[4] = {S.v[i].x, S.v[i].y, S.v[i].z, S.v[i].w};
+#pragma unroll
+            for (int o = 0; o < 2; ++o) {
+                float f[8];
+                mx_decode4(c[2 * o], s, f);
+                mx_decode4(c[2 * o + 1], s, f + 4);
+                // exact in bf16: the high halves
+                auto pair = [](float a, float b) { return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u); };
+                *reinterpret_cast<uint4 *>(&xs[x_place(row, 2 * (tid & 3) + o)]) =
+                    make_uint4(pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7]));
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < S.kLoads; ++i)
+            *reinterpret_cast<uint4 *>(&xs[x_place((tid >> 3) + 32 * i, tid & 7)]) = S.v[i];
+    }
+}
+
+// A lane's weights of one step: codes and scales of its row in both tiles, or the decoded fragments.
+struct WCodes {
+    uint4 c[2];
+    uint32_t s[2];
+};
+struct WFrag {
+    uint4 v[2][4];
+};
+
+// MT: tiles of 32 rows of X. FRAG: the weights come decoded, in the order of the fragments (k_lin_transpose).
+template <int MT, bool XMX, bool FRAG>
+__global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinArgs p) {
+    constexpr int kTpr = MT >= 8 ? 2 : 1, kXHalf = 32 * MT * kStep;  // tiles per epilogue round; one X buffer
+    constexpr int kLds = 2 * kXHalf * 2 > kTpr * 32768 ? 2 * kXHalf * 2 : kTpr * 32768;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
+    uint16_t *const xs = reinterpret_cast<uint16_t *>(lds);
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r32 = lane & 31, half = lane >> 5;
+    // Work-groups go to the 8 XCDs round robin: give each XCD a contiguous run of tiles, and order the tiles
+    // in bands of four along M, so that the work-groups on an XCD share rows of X and of W in its L2.
+    const unsigned total = gridDim.x, q8 = total / 8, r8 = total % 8, xcd = blockIdx.x % 8;
+    const unsigned b = xcd * q8 + min(xcd, r8) + blockIdx.x / 8;
+    const unsigned slice = b / p.tiles, t0 = b % p.tiles;
+    const unsigned band = t0 / (4 * p.tiles_n), in = t0 % (4 * p.tiles_n);
+    const unsigned bm = min(4u, p.tiles_m - 4 * band);
+    const int64_t m0 = (int64_t)(4 * band + in % bm) * (32 * MT);
+    const int64_t tn = in / bm;
+    const int64_t kbeg = (int64_t)slice * p.kslice, kend = min(p.L, kbeg + p.kslice);
+    // first output column of the wave's tile j, and the lane's weight row in it
+    const int64_t f0 = p.gated ? tn * 128 + 32 * wave : tn * 256 + 64 * wave;
+    int64_t wrow[2];
+    if (p.gated) {
+        wrow[0] = min(p.F - 1, f0 + slot_row(r32));
+        wrow[1] = p.F + wrow[0];
+    } else {
+        wrow[0] = min(p.N - 1, f0 + slot_row(r32));
+        wrow[1] = min(p.N - 1, f0 + 32 + slot_row(r32));
+    }
+    const int64_t steps_all = (p.L + kStep - 1) / kStep, ktiles = (p.N + 31) / 32;
+
+    f32x16 acc[2][MT] = {};
+    XStage<MT, XMX> X;
+    typename std::conditional<FRAG, WFrag, WCodes>::type W, Wn;
+
+    auto w_load = [&](auto &D, int64_t k0) {
+        if constexpr (FRAG) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int64_t kt = min(ktiles - 1, f0 / 32 + j);
+                const uint16_t *q = p.wt + ((kt * steps_all + k0 / kStep) * 4) * 512 + lane * 8;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) D.v[j][i] = *reinterpret_cast<const uint4 *>(q + i * 512);
+            }
+        } else {
+            const int64_t k = k0 + 32 * half;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint8_t *c = p.codes + (wrow[j] * p.L + k) / 2, *s = p.scales + (wrow[j] * p.L + k) / 16;
+                if (k0 + kStep <= kend || k + 32 <= kend) {
+                    D.c[j] = load16(c);
+                    D.s[j] = load2b(s);
+                } else {
+                    D.c[j] = make_uint4(0u, 0u, 0u, 0u);
+                    D.s[j] = 0u;
+                    if (k < kend) {  // the row's last 16
+                        const uint2 c2 = load8b(c);
+                        D.c[j].x = c2.x, D.c[j].y = c2.y;
+                        D.s[j] = *s;
+                    }
+                }
+            }
+        }
+    };
+    auto products = [&](const uint16_t *xb) {
+        float d[2][2];
+        if constexpr (!FRAG)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) d[j][0] = e4m3_value(W.s[j] & 0x7Fu), d[j][1] = e4m3_value((W.s[j] >> 8) & 0x7Fu);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            bf16x8 a[2], x[MT];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                if constexpr (FRAG) {
+                    a[j] = __builtin_bit_cast(bf16x8, W.v[j][i]);
+                } else {
+                    const uint32_t c = i == 0 ? W.c[j].x : i == 1 ? W.c[j].y : i == 2 ? W.c[j].z : W.c[j].w;
+                    a[j] = __builtin_bit_cast(bf16x8, dequant8(c, d[j][i >> 1]));
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+                x[t] = *reinterpret_cast<const bf16x8 *>(&xb[x_place(32 * t + r32, 4 * half + i)]);
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    acc[j][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[j], x[t], acc[j][t], 0, 0, 0);
+        }
+    };
+
+    // Step s: store X of step s + 1 (loaded during step s - 1) to the other buffer, start the loads of X of step
+    // s + 2 and of the weights of s + 1, then the products of s; one barrier per step.
+    x_load<MT, XMX>(X, p, m0, kbeg, kend, tid);
+    w_load(W, kbeg);
+    x_store<MT, XMX>(X, xs, tid);
+    if (kbeg + kStep < kend) x_load<MT, XMX>(X, p, m0, kbeg + kStep, kend, tid);
+    __syncthreads();
+    int buf = 0;
+    for (int64_t k0 = kbeg; k0 < kend; k0 += kStep, buf ^= 1) {
+        if (k0 + kStep < kend) {
+            x_store<MT, XMX>(X, xs + (buf ^ 1) * kXHalf, tid);
+            w_load(Wn, k0 + kStep);
+            if (k0 + 2 * kStep < kend) x_load<MT, XMX>(X, p, m0, k0 + 2 * kStep, kend, tid);
+        }
+        products(xs + buf * kXHalf);
+        W = Wn;
+        __syncthreads();
+    }
+
+    // The sums go through LDS, kTpr tiles of 32 rows by 256 weight rows at a time, so that the epilogue works on
+    // whole rows: a thread takes eight consecutive output columns, a row's threads are consecutive. 16-byte
+    // chunk c of row r sits at c ^ (r % 8).
+    float *const es = reinterpret_cast<float *>(lds);
+    auto place = [](int row, int chunk) { return row * 256 + ((chunk ^ (row & 7)) << 2); };
+    const float alpha = p.part ? 1.0f : *p.alpha;
+    const int cols = p.gated ? 128 : 256, threads = cols / 8;  // output columns of the work-group; threads per row
+    const int fl = 8 * (tid % threads);
+    const int ch = p.gated ? 16 * (fl / 32) + (fl % 32) / 4 : fl / 4;  // the chunk of column fl
+    const int64_t f = tn * cols + fl;
+    const int nf = clamp_count(p.F - f, 8);
+#pragma unroll 1
+    for (int round = 0; round < MT / kTpr; ++round) {
+        auto dump = [&](int t, const f32x16 &a0, const f32x16 &a1) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const f32x16 &a = j ? a1 : a0;
+                    *reinterpret_cast<f32x4 *>(&es[place(32 * t + r32, 16 * wave + 8 * j + 4 * half + e / 4)]) =
+                        f32x4{a[e], a[e + 1], a[e + 2], a[e + 3]};
+                }
+        };
+#pragma unroll
+        for (int r = 0; r < MT / kTpr; ++r)  // a branch per round: the accumulators are not indexed at run time
+            if (r == round)
+#pragma unroll
+                for (int t = 0; t < kTpr; ++t) dump(t, acc[0][r * kTpr + t], acc[1][r * kTpr + t]);
+        __syncthreads();
+#pragma unroll 1
+        for (int row = tid / threads; row < 32 * kTpr; row += kTileThreads / threads) {
+            const int64_t m = m0 + 32 * kTpr * round + row;
+            const int n = m < p.M ? nf : 0;
+            float g[8], u[8] = {};
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const f32x4 v = *reinterpret_cast<const f32x4 *>(&es[place(row, ch + c)]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) g[4 * c + i] = alpha * v[i];
+                if (p.gated) {
+                    const f32x4 w = *reinterpret_cast<const f32x4 *>(&es[place(row, ch + 8 + c)]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) u[4 * c + i] = alpha * w[i];
+                }
+            }
+            if (p.part) {  // fp32 sums of this slice, without alpha
+                float *q = p.part + ((int64_t)slice * p.M + m) * p.N + f;
+                put8(q, g, n);
+                if (p.gated) put8(q + p.F, u, n);
+            } else {
+                epilogue8(p, m, f, n, g, u, lane);
+            }
+        }
+        __syncthreads();
+    }
+}
+
+constexpr int kReduceThreads = 256;
+
+// The slices' sums added in slice order, then the epilogue: eight columns per thread, rows padded to whole
+// 32-column blocks so that a quad holds a block.
+__global__ __launch_bounds__(kReduceThreads) void k_lin_reduce(LinArgs p, int slices, int64_t per_row, int64_t groups) {
+    const float alpha = *p.alpha;
+    for (int64_t i = (int64_t)blockIdx.x * kReduceThreads + threadIdx.x; i < groups;
+         i += (int64_t)gridDim.x * kReduceThreads) {
+        const int64_t m = i / per_row, f = 8 * (i - m * per_row);
+        const int n = clamp_count(p.F - f, 8);
+        float g[8] = {}, u[8] = {};
+        for (int s = 0; s < slices; ++s) {
+            const float *q = p.part + ((int64_t)s * p.M + m) * p.N + f;
+            Raw8<float> r;
+            float v[8];
+            r.load(q, n);
+            r.get(v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[e] += v[e];
+            if (p.gated) {
+                r.load(q + p.F, n);
+                r.get(v);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) u[e] += v[e];
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] *= alpha, u[e] *= alpha;
+        epilogue8(p, m, f, n, g, u, (int)(threadIdx.x & 63));
+    }
+}
+
+// -------------------------------------------------------------------------------------- skinny kernel
+
+// Few rows of X (M <= 64), bound by reading the weights once: a work-group owns 16 output columns (gated: their
+// 16 gate rows and 16 up rows), its 16 waves split K in chunks of 128 and its sums are joined through LDS
+// in wave order. Products on v_mfma_f32_16x16x32_bf16, weights as A (lane l: row l % 16, 16 bytes of codes per
+// chunk at k = 32 (l / 16)), X^T as B straight from L2.
+constexpr int kSkinnyThreads = 1024, kSkinnyWaves = kSkinnyThreads / 64;
+
+template <int MT, int NT, bool XMX>
+__global__ __launch_bounds__(kSkinnyThreads) void k_lin_skinny(LinArgs p) {
+    __shared__ float red[kSkinnyWaves][MT][256];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r16 = lane & 15, g = lane >> 4;
+    const int64_t f0 = (int64_t)blockIdx.x * 16;
+    const int64_t K = p.L, nch = (K + 127) / 128, nb = (K + kMxBlock - 1) / kMxBlock;
+    int64_t wrow[NT];
+    wrow[0] = min(p.F - 1, f0 + r16);
+    if (NT == 2) wrow[NT - 1] = p.F + wrow[0];
+    f32x4 acc[NT][MT] = {};
+    uint4 cv[NT];
+    uint32_t sv[NT];
+    auto load_w = [&](int64_t c) {
+        const int64_t k = 128 * c + 32 * g;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const uint8_t *q = p.codes + (wrow[j] * K + k) / 2, *s = p.scales + (wrow[j] * K + k) / 16;
+            cv[j] = make_uint4(0u, 0u, 0u, 0u);
+            sv[j] = 0u;
+            if (k + 32 <= K) {
+                cv[j] = load16(q);
+                sv[j] = load2b(s);
+            } else if (k < K) {  // the row's last 16
+                const uint2 c2 = load8b(q);
+                cv[j].x = c2.x, cv[j].y = c2.y;
+                sv[j] = *s;
+            }
+        }
+    };
+    int64_t c = wave;
+    if (c < nch) load_w(c);
+    for (; c < nch; c += kSkinnyWaves) {
+        uint4 cur[NT];
+        uint32_t scur[NT];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) cur[j] = cv[j], scur[j] = sv[j];
+        if (c + kSkinnyWaves < nch) load_w(c + kSkinnyWaves);
+        const int64_t k = 128 * c + 32 * g;
+        uint4 xv[MT][4];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            const int64_t m = 16 * t + r16;
+            const bool row = m < p.M;
+            if (XMX) {
+                const uint8_t *q = static_cast<const uint8_t *>(p.x) + m * p.ldx + k;
+                uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+                float s = 0.0f;
+                if (row && k < K) {
+                    a = load16(q);
+                    s = mx_scale_value(p.xs[m * nb + k / kMxBlock]);
+                    if (k + 32 <= K) b = load16(q + 16);
+                }
+                const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float f[8];
+                    mx_decode4(w[2 * i], s, f);
+                    mx_decode4(w[2 * i + 1], s, f + 4);
+                    auto pair = [](float lo, float hi) { return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u); };
+                    xv[t][i] = make_uint4(pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7]));
+                }
+            } else {
+                const uint16_t *q = static_cast<const uint16_t *>(p.x) + m * p.ldx + k;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    xv[t][i] = make_uint4(0u, 0u, 0u, 0u);
+                    if (row && k + 8 * i < K) xv[t][i] = load16(q + 8 * i);
+                }
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const float d0 = e4m3_value(scur[j] & 0x7Fu), d1 = e4m3_value((scur[j] >> 8) & 0x7Fu);
+            const uint4 w[4] = {dequant8(cur[j].x, d0), dequant8(cur[j].y, d0), dequant8(cur[j].z, d1),
+                                dequant8(cur[j].w, d1)};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[i]),
+                                                                        __builtin_bit_cast(bf16x8, xv[t][i]), acc[j][t], 0, 0, 0);
+        }
+    }
+    // Element r of lane l is weight row 4 (l / 16) + r of the tile, row 16 t + l % 16 of X. Thread tid sums output
+    // o = tid, MT * 256 of them (at most 1024).
+    float z[NT] = {};
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        if (j) __syncthreads();
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) red[wave][t][lane * 4 + r] = acc[j][t][r];
+        __syncthreads();
+        if (tid < MT * 256)
+#pragma unroll
+            for (int w = 0; w < kSkinnyWaves; ++w) z[j] += red[w][tid >> 8][tid & 255];
+    }
+    const int l = (tid >> 2) & 63;
+    const int64_t f = f0 + 4 * (l >> 4) + (tid & 3), m = 16 * (tid >> 8) + (l & 15);
+    if (tid >= MT * 256 || f >= p.F || m >= p.M) return;
+    const float alpha = *p.alpha;
+    auto scalar = [](const void *b, int f32, int64_t e) {
+        return f32 ? static_cast<const float *>(b)[e] : __uint_as_float((uint32_t)static_cast<const uint16_t *>(b)[e] << 16);
+    };
+    float a = alpha * z[0], u = NT == 2 ? alpha * z[NT - 1] : 0.0f;
+    if (p.bias) {
+        a += scalar(p.bias, p.bias_f32, f);
+        if (NT == 2) u += scalar(p.bias, p.bias_f32, p.F + f);
+    }
+    if (p.keep == kKeepBf16) {
+        uint16_t *q = static_cast<uint16_t *>(p.z) + m * p.N + f;
+        q[0] = to_bf16(a);
+        if (NT == 2) q[p.F] = to_bf16(u);
+    }
+    a = act_value(a, p.act);
+    if (NT == 2) a *= u;
+    if (p.res) a += scalar(p.res, p.res_f32, m * p.ldr + f);
+    if (p.y_f32)
+        static_cast<float *>(p.y)[m * p.F + f] = a;
+    else
+        static_cast<uint16_t *>(p.y)[m * p.F + f] = to_bf16(a);
+}
+
+// ------------------------------------------------------------------------------------------ gradient
+
+// Weights decoded to bf16 and transposed, in the order in which k_lin_tile's lanes read them: 32 columns k (a
+// tile of the product's rows) by 64 rows n (a step of its sum) make 4 KB, [i][lane][8]: lane's column is
+// slot_row(lane % 32), its rows 32 (lane / 32) + 8 i + 0..7. A work-group takes 64 rows by 256 columns, a thread
+// 8 x 8 of them: eight dwords of codes, whose decoded values are paired along n as they are packed. Rows
+// past N are zeros.
+__global__ __launch_bounds__(256) void k_lin_transpose(const uint8_t *__restrict__ codes,
+                                                     const uint8_t *__restrict__ scales, int64_t N, int64_t K,
+                                                     uint16_t *__restrict__ wt) {
+    const int64_t step = blockIdx.y, steps = gridDim.y;
+    const int kg = threadIdx.x & 31, ng = threadIdx.x >> 5;
+    const int64_t k0 = (int64_t)blockIdx.x * 256 + 8 * kg, n0 = step * kStep + 8 * ng;
+    if (k0 >= K) return;  // K % 16 == 0: the eight columns are in or out
+    uint32_t c[8], sb[8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        c[r] = sb[r] = 0u;
+        if (n0 + r < N) {
+            const int64_t e = (n0 + r) * K + k0;
+            c[r] = *reinterpret_cast<const uint32_t *>(codes + e / 2);
+            sb[r] = scales[e / 16];
+        }
+    }
+    float v[8][8];
+#pragma unroll
+    for (int r = 0; r < 8; ++r) {
+        const float d = e4m3_value(sb[r] & 0x7Fu);
+        const f32x2 q0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[r], 1.0f, 0);
+        const f32x2 q1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[r], 1.0f, 1);
+        const f32x2 q2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[r], 1.0f, 2);
+        const f32x2 q3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(c[r], 1.0f, 3);
+        v[r][0] = q0.x * d, v[r][1] = q0.y * d, v[r][2] = q1.x * d, v[r][3] = q1.y * d;
+        v[r][4] = q2.x * d, v[r][5] = q2.y * d, v[r][6] = q3.x * d, v[r][7] = q3.y * d;
+    }
+    auto pair = [](float a, float b) { return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u); };
+    const int64_t tile = (k0 / 32 * steps + step) * 4 + (ng & 3);
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk) {
+        const int o = (int)(k0 & 31) + kk;  // column o of the tile sits in slot 8 b + 4 h' + i', o = 16 h' + 4 b + i'
+        const int slot = 8 * ((o >> 2) & 3) + 4 * (o >> 4) + (o & 3);
+        *reinterpret_cast<uint4 *>(wt + tile * 512 + (32 * (ng >> 2) + slot) * 8) =
+            make_uint4(pair(v[0][kk], v[1][kk]), pair(v[2][kk], v[3][kk]), pair(v[4][kk], v[5][kk]), pair(v[6][kk], v[7][kk]));
+    }
+}
+
+// dz of eight columns per thread, and its column sums over the work-group's chunk of rows (waves take every
+// fourth row; their sums are joined in wave order). act = none: the sums of dy alone.
+template <bool ZMX>
+__global__ __launch_bounds__(256) void k_lin_dz(LinGradArgs p, int64_t chunk, float *__restrict__ part) {
+    __shared__ float red[2][4][64 * 8];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int64_t f = 8 * ((int64_t)blockIdx.x * 64 + lane);
+    const int n = clamp_count(p.F - f, 8);
+    const int64_t r0 = (int64_t)blockIdx.y * chunk, r1 = min(p.M, r0 + chunk);
+    const int64_t nb = (p.N + kMxBlock - 1) / kMxBlock;
+    auto z8 = [&](int64_t m, int64_t col, float v[8]) {
+        if (ZMX) {
+            RawMx8 r;
+            r.load(static_cast<const uint8_t *>(p.z) + m * p.ldz + col, p.zs + m * nb + col / kMxBlock, n);
+            r.get(v);
+        } else {
+            Raw8<uint16_t> r;
+            r.load(static_cast<const uint16_t *>(p.z) + m * p.ldz + col, n);
+            r.get(v);
+        }
+    };
+    float sg[8] = {}, su[8] = {};
+    if (n > 0)
+        for (int64_t m = r0 + wave; m < r1; m += 4) {
+            float dy[8], g[8], u[8];
+            Raw8<uint16_t> r;
+            r.load(p.dy + m * p.lddy + f, n);
+            r.get(dy);
+            if (p.act == kActNone) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sg[i] += dy[i];
+                continue;
+            }
+            z8(m, f, g);
+            if (p.gated) z8(m, p.F + f, u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 a = act_both(g[i], p.act);
+                if (p.gated) {
+                    g[i] = dy[i] * u[i] * a.y;
+                    u[i] = dy[i] * a.x;
+                    su[i] += u[i];
+                } else {
+                    g[i] = dy[i] * a.y;
+                }
+                sg[i] += g[i];
+            }
+            put8(p.dz + m * p.N + f, g, n);
+            if (p.gated) put8(p.dz + m * p.N + p.F + f, u, n);
+        }
+    if (!part) return;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) red[0][wave][8 * lane + i] = sg[i], red[1][wave][8 * lane + i] = su[i];
+    __syncthreads();
+    for (int o = threadIdx.x; o < 512; o += 256) {
+        const int64_t col = (int64_t)blockIdx.x * 512 + o;
+        if (col >= p.F) continue;
+        float *q = part + (int64_t)blockIdx.y * p.N + col;
+        q[0] = ((red[0][0][o] + red[0][1][o]) + red[0][2][o]) + red[0][3][o];
+        if (p.gated) q[p.F] = ((red[1][0][o] + red[1][1][o]) + red[1][2][o]) + red[1][3][o];
+    }
+}
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Tile height and K split of the tile kernel for an [M] x [F] output over a sum of length L.
+LinPlan plan_tile(int64_t M, int64_t L, int64_t F, int64_t N, bool gated) {
+    LinPlan p = {};
+    const int64_t tn = ceil_div(F, gated ? 128 : 256);
+    auto tiles = [&](int mt) { return ceil_div(M, 32 * mt) * tn; };
+    p.mt = tiles(8) >= 200 ? 8 : tiles(4) >= 256 ? 4 : M > 32 ? 2 : 1;
+    p.tiles_n = tn;
+    p.tiles_m = ceil_div(M, 32 * p.mt);
+    const int64_t steps = ceil_div(L, kStep), all = p.tiles_m * tn;
+    int64_t want = all >= 256 ? 1 : std::min<int64_t>(ceil_div(512, all), steps / 4);
+    while (want > 1 && want * M * N * (int64_t)sizeof(float) > ((int64_t)1 << 30)) --want;
+    want = std::max<int64_t>(want, 1);
+    p.kslice = ceil_div(steps, want) * kStep;
+    p.slices = ceil_div(L, p.kslice);
+    if (p.slices > 1) p.part_bytes = (size_t)(p.slices * M * N) * sizeof(float);
+    return p;
+}
+
+template <bool XMX, bool FRAG>
+hipError_t tile_launch(LinArgs p, const LinPlan &plan, hipStream_t st) {
+    p.tiles_n = (unsigned)plan.tiles_n, p.tiles_m = (unsigned)plan.tiles_m;
+    p.tiles = (unsigned)(plan.tiles_n * plan.tiles_m);
+    p.kslice = plan.kslice;
+    const dim3 grid((unsigned)(p.tiles * plan.slices)), block(kTileThreads);
+    switch (plan.mt) {
+        case 1: hipLaunchKernelGGL((k_lin_tile<1, XMX, FRAG>), grid, block, 0, st, p); break;
+        case 2: hipLaunchKernelGGL((k_lin_tile<2, XMX, FRAG>), grid, block, 0, st, p); break;
+        case 4: hipLaunchKernelGGL((k_lin_tile<4, XMX, FRAG>), grid, block, 0, st, p); break;
+        default: hipLaunchKernelGGL((k_lin_tile<8, XMX, FRAG>), grid, block, 0, st, p); break;
+    }
+    hipError_t err = hipGetLastError();
+    if (err == hipSuccess && plan.slices > 1) {
+        const int64_t per_row = ceil_div(p.F, kMxBlock) * 4, groups = p.M * per_row;
+        const dim3 rg((unsigned)std::min<int64_t>(ceil_div(groups, kReduceThreads), 4096));
+        hipLaunchKernelGGL(k_lin_reduce, rg, dim3(kReduceThreads), 0, st, p, (int)plan.slices, per_row, groups);
+        err = hipGetLastError();
+    }
+    return err;
+}
+
+template <int NT, bool XMX>
+hipError_t skinny_launch(const LinArgs &p, hipStream_t st) {
+    const dim3 grid((unsigned)ceil_div(p.F, 16)), block(kSkinnyThreads);
+    switch ((p.M + 15) / 16) {
+        case 1: hipLaunchKernelGGL((k_lin_skinny<1, NT, XMX>), grid, block, 0, st, p); break;
+        case 2: hipLaunchKernelGGL((k_lin_skinny<2, NT, XMX>), grid, block, 0, st, p); break;
+        case 3: hipLaunchKernelGGL((k_lin_skinny<3, NT, XMX>), grid, block, 0, st, p); break;
+        default: hipLaunchKernelGGL((k_lin_skinny<4, NT, XMX>), grid, block, 0, st, p); break;
+    }
+    return hipGetLastError();
+}
+
+struct GradPlan {
+    LinPlan tile;
+    int64_t chunk, chunks;
+    size_t wt_bytes, sum_bytes;
+};
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+GradPlan plan_grad(int64_t M, int64_t K, int64_t N, int64_t F, bool bias) {
+    GradPlan g = {};
+    g.tile = plan_tile(M, N, K, K, false);
+    g.wt_bytes = align256((size_t)(ceil_div(K, 32) * ceil_div(N, kStep)) * 4096);
+    g.chunk = std::max<int64_t>(bias ? 16 : 4, ceil_div(M * ceil_div(F, 512), 2048));
+    g.chunk = std::max(g.chunk, ceil_div(M, 65535));
+    g.chunks = ceil_div(M, g.chunk);
+    g.sum_bytes = bias ? align256((size_t)(g.chunks * N) * sizeof(float)) : 0;
+    return g;
+}
+
+}  // namespace
+
+LinPlan plan_linear(int64_t M, int64_t K, int64_t N, bool gated, int keep) {
+    if (M <= 64 && keep != kKeepMx) {
+        LinPlan p = {};
+        p.slices = 1;
+        return p;  // mt = 0: the skinny kernel
+    }
+    return plan_tile(M, K, gated ? N / 2 : N, N, gated);
+}
+
+hipError_t launch_linear(const LinArgs &args, float *part, hipStream_t stream) {
+    const LinPlan plan = plan_linear(args.M, args.L, args.N, args.gated, args.keep);
+    LinArgs p = args;
+    if (plan.mt == 0) {
+        if (p.gated) return p.x_mx ? skinny_launch<2, true>(p, stream) : skinny_launch<2, false>(p, stream);
+        return p.x_mx ? skinny_launch<1, true>(p, stream) : skinny_launch<1, false>(p, stream);
+    }
+    p.part = plan.slices > 1 ? part : nullptr;
+    return p.x_mx ? tile_launch<true, false>(p, plan, stream) : tile_launch<false, false>(p, plan, stream);
+}
+
+size_t linear_grad_workspace(int64_t M, int64_t K, int64_t N, int64_t F, bool bias) {
+    if (M == 0) return 0;
+    const GradPlan g = plan_grad(M, K, N, F, bias);
+    return g.wt_bytes + g.sum_bytes + g.tile.part_bytes;
+}
+
+hipError_t launch_linear_grad(const LinGradArgs &g, const uint8_t *codes, const uint8_t *scales, const float *alpha,
+                              int64_t K, void *dx, float *dbias, void *ws, hipStream_t stream) {
+    if (g.M == 0) return dbias ? launch_column_sum(nullptr, 0, g.N, dbias, stream) : hipSuccess;
+    const GradPlan plan = plan_grad(g.M, K, g.N, g.F, dbias != nullptr);
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    uint16_t *wt = reinterpret_cast<uint16_t *>(base);
+    float *sums = reinterpret_cast<float *>(base + plan.wt_bytes);
+    float *part = reinterpret_cast<float *>(base + plan.wt_bytes + plan.sum_bytes);
+    hipError_t err = hipSuccess;
+    if (g.act != kActNone || dbias) {
+        const dim3 grid((unsigned)ceil_div(g.F, 512), (unsigned)plan.chunks);
+        if (g.z_mx)
+            hipLaunchKernelGGL(k_lin_dz<true>, grid, dim3(256), 0, stream, g, plan.chunk, dbias ? sums : nullptr);
+        else
+            hipLaunchKernelGGL(k_lin_dz<false>, grid, dim3(256), 0, stream, g, plan.chunk, dbias ? sums : nullptr);
+        err = hipGetLastError();
+        if (err == hipSuccess && dbias) err = launch_column_sum(sums, plan.chunks, g.N, dbias, stream);
+    }
+    if (err != hipSuccess) return err;
+    const dim3 grid((unsigned)ceil_div(K, 256), (unsigned)ceil_div(g.N, kStep));
+    hipLaunchKernelGGL(k_lin_transpose, grid, dim3(256), 0, stream, codes, scales, g.N, K, wt);
+    err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    LinArgs p = {};
+    p.x = g.act == kActNone ? g.dy : g.dz;
+    p.ldx = g.act == kActNone ? g.lddy : g.N;
+    p.M = g.M, p.L = g.N, p.N = K, p.F = K;
+    p.alpha = alpha;
+    p.y = dx;
+    p.wt = wt;
+    p.part = plan.tile.slices > 1 ? part : nullptr;
+    return tile_launch<false, true>(p, plan.tile, stream);
+}
+
+}  // namespace nvfp4

@@ -3,6 +3,8 @@ operators of ``include/nvfp4.h``). Marshalling only, like the rest of the bindin
 
     h8, s = rms_norm(X, w, residual=R, out_dtype="mxfp8")       # s = X + R, h8 = (codes, scales)
     dX, dw = rms_norm_grad(dY, s, w, dS=dS)
+    Y, Z = linear(h8, *W, activation="silu", gated=True, keep="mxfp8")   # W = quantize(...)'s codes, scales, alpha
+    dX, dZ, _ = linear_grad(dY, *W, Z=Z, activation="silu", gated=True)
     kept = quantize_mxfp8(A)                                    # an activation kept in 8 bits ...
     A_hat = dequantize_mxfp8(*kept)                             # ... and read back
 
@@ -13,6 +15,8 @@ contiguous and are allocated on the call's stream: ``stream``, or the current st
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import DTYPES, NVFP4Error, _check, _check_buffer, lib
@@ -21,6 +25,33 @@ MXFP8 = "mxfp8"
 _MX = 2  # NVFP4_DTYPE_MXFP8
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 _SCALES = (torch.float8_e8m0fnu, torch.uint8)
+
+
+ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2}  # enum nvfp4_activation
+
+
+class _LinearArgs(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("x_scales", ctypes.c_void_p), ("x_dtype", ctypes.c_int),
+        ("M", ctypes.c_int64), ("K", ctypes.c_int64), ("N", ctypes.c_int64), ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p), ("alpha", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+        ("bias_dtype", ctypes.c_int), ("activation", ctypes.c_int), ("gated", ctypes.c_int),
+        ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64), ("residual_dtype", ctypes.c_int),
+        ("y", ctypes.c_void_p), ("y_dtype", ctypes.c_int), ("z", ctypes.c_void_p), ("z_scales", ctypes.c_void_p),
+        ("z_dtype", ctypes.c_int), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class _LinearGradArgs(ctypes.Structure):
+    _fields_ = [
+        ("dy", ctypes.c_void_p), ("lddy", ctypes.c_int64), ("z", ctypes.c_void_p), ("ldz", ctypes.c_int64),
+        ("z_scales", ctypes.c_void_p), ("z_dtype", ctypes.c_int), ("M", ctypes.c_int64), ("K", ctypes.c_int64),
+        ("N", ctypes.c_int64), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("alpha", ctypes.c_void_p),
+        ("activation", ctypes.c_int), ("gated", ctypes.c_int), ("dx", ctypes.c_void_p), ("dz", ctypes.c_void_p),
+        ("dbias", ctypes.c_void_p), ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
+        ("stream", ctypes.c_void_p),
+    ]
 
 
 def _run(dev, stream, call):
@@ -196,5 +227,117 @@ def rms_norm_grad(dY: torch.Tensor, S, weight: torch.Tensor, eps: float = 1e-6, 
                                          _ptr(dS), ldds, DTYPES[dY.dtype], DTYPES[weight.dtype], rows, cols, eps,
                                          dX.data_ptr(), dw.data_ptr(), _ptr(ws), nbytes, st))
         return dX, dw
+
+    return _run(dev, stream, call)
+
+
+def _weights(codes, scales, alpha, dev, K=None):
+    """Checks NVFP4 weights as ``quantize`` returns them; returns (N, K)."""
+    if codes.dim() != 2 or (K is not None and 2 * codes.shape[1] != K) or codes.shape[1] % 8:
+        raise NVFP4Error("codes must be [N, K/2] with K % 16 == 0")
+    N, K = codes.shape[0], 2 * codes.shape[1]
+    _check_buffer(codes, "codes", N * K // 2, dev, torch.uint8)
+    _check_buffer(scales, "scales", N * K // 16, dev, torch.uint8)
+    _check_buffer(alpha, "alpha", 4, dev, torch.float32)
+    return N, K
+
+
+def _activation(activation, gated, N):
+    if activation not in ACTIVATIONS:
+        raise NVFP4Error('activation must be None, "silu" or "gelu"')
+    if gated and (activation is None or N % 2):
+        raise NVFP4Error("a gated product needs an activation and an even number of weight rows")
+    return N // 2 if gated else N
+
+
+def linear_workspace_bytes(M: int, K: int, N: int, gated: bool = False, keep=None) -> int:
+    return int(lib().nvfp4_linear_workspace_bytes(M, K, N, int(gated), _MX if keep == MXFP8 else 0))
+
+
+def linear(X, codes: torch.Tensor, scales: torch.Tensor, alpha: torch.Tensor, *, bias=None, activation=None,
+           gated: bool = False, residual=None, out_dtype=torch.bfloat16, keep=None, out=None, workspace=None,
+           stream=None):
+    """Product with NVFP4 weights (codes [N, K/2], scales [N, K/16], alpha [1], as ``quantize`` returns them) and
+    the rest of a projection in its epilogue: Z = alpha * (X @ Wq.T) + bias and Y = act(Z) + residual, or, gated
+    with F = N // 2, Y = act(Z[:, :F]) * Z[:, F:] + residual. ``X`` is [M, K] bf16 or an MXFP8 pair; ``activation`` None,
+    "silu" or "gelu" (tanh form); ``bias`` [N] and ``residual`` (Y's shape) bf16 or fp32; Y is of ``out_dtype``, in
+    ``out`` if given (contiguous; it may be the residual itself). ``keep`` (None, torch.bfloat16 or "mxfp8") asks
+    for Z too, [M, N] in that form, for ``linear_grad`` (gated and "mxfp8": F % 32 == 0). Returns Y, or (Y, Z)."""
+    if isinstance(X, (tuple, list)):
+        x, xs, ldx = _mx_pair(X, "X")
+        xt = _MX
+    else:
+        ldx = _rows(X, "X", (torch.bfloat16,))
+        x, xs, xt = X, None, 0
+    M, K = x.shape
+    dev = x.device
+    N, K = _weights(codes, scales, alpha, dev, K)
+    F = _activation(activation, gated, N)
+    if out_dtype not in DTYPES:
+        raise NVFP4Error("out_dtype must be bf16 or fp32")
+    if keep not in (None, torch.bfloat16, MXFP8):
+        raise NVFP4Error('keep must be None, torch.bfloat16 or "mxfp8"')
+    if bias is not None:
+        _vector(bias, "bias", N, dev)
+    ldr = 0 if residual is None else _rows(residual, "residual", DTYPES, dev, (M, F))
+    _output(out, "out", (M, F), out_dtype, dev)
+
+    def call(st):
+        Y = torch.empty((M, F), dtype=out_dtype, device=dev) if out is None else out
+        Z, z, zs = None, None, None
+        if keep == MXFP8:
+            Z = _new_mx(M, N, dev)
+            z, zs = Z[0].data_ptr(), Z[1].data_ptr()
+        elif keep is not None:
+            Z = torch.empty((M, N), dtype=keep, device=dev)
+            z = Z.data_ptr()
+        ws, nbytes = _space(workspace, linear_workspace_bytes(M, K, N, gated, keep), dev)
+        a = _LinearArgs(x.data_ptr(), ldx, _ptr(xs), xt, M, K, N, codes.data_ptr(), scales.data_ptr(), alpha.data_ptr(),
+                        _ptr(bias), 0 if bias is None else DTYPES[bias.dtype], ACTIVATIONS[activation], int(gated),
+                        _ptr(residual), ldr, 0 if residual is None else DTYPES[residual.dtype], Y.data_ptr(),
+                        DTYPES[out_dtype], z, zs, _MX if keep == MXFP8 else 0, _ptr(ws), nbytes, st)
+        _check(lib().nvfp4_linear(ctypes.byref(a)))
+        return Y if keep is None else (Y, Z)
+
+    return _run(dev, stream, call)
+
+
+def linear_grad_workspace_bytes(M: int, K: int, N: int, gated: bool = False, bias: bool = False) -> int:
+    return int(lib().nvfp4_linear_grad_workspace_bytes(M, K, N, int(gated), int(bias)))
+
+
+def linear_grad(dY: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, alpha: torch.Tensor, *, Z=None,
+                activation=None, gated: bool = False, bias: bool = False, workspace=None, stream=None):
+    """Gradients of ``linear`` for ``dY`` (bf16, Y's shape) at its output, with ``Z`` as it kept it (bf16 or an MXFP8
+    pair; None without an activation). Returns (dX, dZ, dbias): dX [M, K] bf16; dZ [M, N] bf16, the gradient at Z
+    (None without an activation, where it is dY); dbias [N] fp32 where ``bias`` is true, else None. The residual's
+    gradient is dY; the weights are frozen."""
+    lddy = _rows(dY, "dY", (torch.bfloat16,))
+    dev = dY.device
+    N, K = _weights(codes, scales, alpha, dev)
+    F = _activation(activation, gated, N)
+    M = dY.shape[0]
+    if dY.shape[1] != F:
+        raise NVFP4Error(f"dY must be [M, {F}]")
+    if (Z is None) != (activation is None):
+        raise NVFP4Error("Z is needed with an activation, and only there")
+    z, zs, ldz, zt = None, None, 0, 0
+    if isinstance(Z, (tuple, list)):
+        z, zs, ldz = _mx_pair(Z, "Z", dev, (M, N))
+        zt = _MX
+    elif Z is not None:
+        ldz = _rows(Z, "Z", (torch.bfloat16,), dev, (M, N))
+        z = Z
+
+    def call(st):
+        dX = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
+        dZ = None if activation is None else torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+        db = torch.empty(N, dtype=torch.float32, device=dev) if bias else None
+        ws, nbytes = _space(workspace, linear_grad_workspace_bytes(M, K, N, gated, bias), dev)
+        a = _LinearGradArgs(dY.data_ptr(), lddy, _ptr(z), ldz, _ptr(zs), zt, M, K, N, codes.data_ptr(),
+                            scales.data_ptr(), alpha.data_ptr(), ACTIVATIONS[activation], int(gated), dX.data_ptr(),
+                            _ptr(dZ), _ptr(db), _ptr(ws), nbytes, st)
+        _check(lib().nvfp4_linear_grad(ctypes.byref(a)))
+        return dX, dZ, db
 
     return _run(dev, stream, call)
