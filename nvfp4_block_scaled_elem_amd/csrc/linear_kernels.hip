@@ -128,6 +128,9 @@ __device__ __forceinline__ void epilogue8(const LinArgs &p, int64_t m, int64_t f
 // Gated: the wave's first tile holds 32 rows f, the second the rows F + f.
 constexpr int kTileThreads = 256, kStep = 64;
 
+// Instruction classes of the scheduling groups.
+constexpr int kValu = 0x002, kMfma = 0x008, kVmemRead = 0x020, kDsRead = 0x100, kDsWrite = 0x200;
+
 __device__ __forceinline__ int slot_row(int r) { return 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3); }
 
 // X of one step in registers, between the loads and the LDS stores.
@@ -138,9 +141,10 @@ struct XStage {
     uint32_t sb[XMX ? kLoads : 1];
 };
 
-template <int MT, bool XMX>
+// WHOLE: the step lies inside the slice (else its k are masked).
+template <int MT, bool XMX, bool WHOLE>
 __device__ __forceinline__ void x_load(XStage<MT, XMX> &S, const LinArgs &p, int64_t m0, int64_t k0, int64_t kend, int tid) {
-    const bool whole = k0 + kStep <= kend;
+    const bool whole = WHOLE || k0 + kStep <= kend;
     if (XMX) {  // four threads per row, 16 codes each; k0 and kend are multiples of 16
         const int64_t k = k0 + 16 * (tid & 3);
         const int64_t nb = (p.L + kMxBlock - 1) / kMxBlock;
@@ -241,11 +245,13 @@ __global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinA
     }
     const int64_t steps_all = (p.L + kStep - 1) / kStep, ktiles = (p.N + 31) / 32;
 
+    using Weights = typename std::conditional<FRAG, WFrag, WCodes>::type;
     f32x16 acc[2][MT] = {};
     XStage<MT, XMX> X;
-    typename std::conditional<FRAG, WFrag, WCodes>::type W, Wn;
+    Weights W[2];
+    bf16x8 A[2][2], B[2][MT];  // the fragments of one phase and of the next (A: decoded weights alone)
 
-    auto w_load = [&](auto &D, int64_t k0) {
+    auto w_load = [&](auto whole, Weights &D, int64_t k0) __attribute__((always_inline)) {
         if constexpr (FRAG) {
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
@@ -259,7 +265,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinA
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const uint8_t *c = p.codes + (wrow[j] * p.L + k) / 2, *s = p.scales + (wrow[j] * p.L + k) / 16;
-                if (k0 + kStep <= kend || k + 32 <= kend) {
+                if (whole.value || k + 32 <= kend) {
                     D.c[j] = load16(c);
                     D.s[j] = load2b(s);
                 } else {
@@ -274,52 +280,104 @@ __global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinA
             }
         }
     };
-    auto products = [&](const uint16_t *xb) {
-        float d[2][2];
-        if constexpr (!FRAG)
+    auto a_frag = [&](bf16x8 (&D)[2], const Weights &w, int i) __attribute__((always_inline)) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) d[j][0] = e4m3_value(W.s[j] & 0x7Fu), d[j][1] = e4m3_value((W.s[j] >> 8) & 0x7Fu);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            bf16x8 a[2], x[MT];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                if constexpr (FRAG) {
-                    a[j] = __builtin_bit_cast(bf16x8, W.v[j][i]);
-                } else {
-                    const uint32_t c = i == 0 ? W.c[j].x : i == 1 ? W.c[j].y : i == 2 ? W.c[j].z : W.c[j].w;
-                    a[j] = __builtin_bit_cast(bf16x8, dequant8(c, d[j][i >> 1]));
-                }
+        for (int j = 0; j < 2; ++j) {
+            if constexpr (!FRAG) {
+                const uint32_t c = i == 0 ? w.c[j].x : i == 1 ? w.c[j].y : i == 2 ? w.c[j].z : w.c[j].w;
+                D[j] = __builtin_bit_cast(bf16x8, dequant8(c, e4m3_value((w.s[j] >> (i >= 2 ? 8 : 0)) & 0x7Fu)));
             }
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-                x[t] = *reinterpret_cast<const bf16x8 *>(&xb[x_place(32 * t + r32, 4 * half + i)]);
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    acc[j][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[j], x[t], acc[j][t], 0, 0, 0);
         }
     };
-
-    // Step s: store X of step s + 1 (loaded during step s - 1) to the other buffer, start the loads of X of step
-    // s + 2 and of the weights of s + 1, then the products of s; one barrier per step.
-    x_load<MT, XMX>(X, p, m0, kbeg, kend, tid);
-    w_load(W, kbeg);
-    x_store<MT, XMX>(X, xs, tid);
-    if (kbeg + kStep < kend) x_load<MT, XMX>(X, p, m0, kbeg + kStep, kend, tid);
-    __syncthreads();
-    int buf = 0;
-    for (int64_t k0 = kbeg; k0 < kend; k0 += kStep, buf ^= 1) {
-        if (k0 + kStep < kend) {
-            x_store<MT, XMX>(X, xs + (buf ^ 1) * kXHalf, tid);
-            w_load(Wn, k0 + kStep);
-            if (k0 + 2 * kStep < kend) x_load<MT, XMX>(X, p, m0, k0 + 2 * kStep, kend, tid);
+    auto b_frag = [&](bf16x8 (&D)[MT], int buf, int i) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+            D[t] = *reinterpret_cast<const bf16x8 *>(&xs[buf * kXHalf + x_place(32 * t + r32, 4 * half + i)]);
+    };
+    auto products = [&](const Weights &w, int i) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                bf16x8 a;
+                if constexpr (FRAG)
+                    a = __builtin_bit_cast(bf16x8, w.v[j][i]);
+                else
+                    a = A[i & 1][j];
+                acc[j][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, B[i & 1][t], acc[j][t], 0, 0, 0);
+            }
+    };
+    // Step s from buffer s % 2, in four phases. At its start the fragments of phase 0 are formed, and X of step
+    // s + 1 is in registers or on its way (loaded during step s - 1). Phase i forms the fragments of phase i + 1
+    // while the matrix cores work on its own. Coded weights are loaded two steps ahead, in phase 3, over those
+    // whose last use was in phase 2; decoded ones one step ahead, in phase 0. The one barrier stands before
+    // the last phase: by then every wave has stored X of step s + 1 (in phase 0) and has read all of buffer s % 2,
+    // so that phase 3 can read ahead from the other buffer and step s + 1 can store into this one.
+    // One wave per SIMD (MT = 8) hides nothing behind another wave, so the order inside a phase is asked for:
+    // LDS reads (and weights decoded) between the first products, stores and loads between the rest.
+    auto step = [&](int buf, Weights &w, Weights &next, auto &&store, auto &&load_x, auto &&load_w)
+                    __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i == 3) __syncthreads();
+            b_frag(B[(i + 1) & 1], i < 3 ? buf : buf ^ 1, (i + 1) & 3);
+            a_frag(A[(i + 1) & 1], i < 3 ? w : next, (i + 1) & 3);
+            if (i == 0) store();
+            if (i == 1) load_x();
+            if (i == (FRAG ? 0 : 3)) load_w(FRAG ? next : w);
+            products(w, i);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+                if (!FRAG) __builtin_amdgcn_sched_group_barrier(kValu, 40 / MT, 0);
+            }
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
+                if (i == 0 && XMX) __builtin_amdgcn_sched_group_barrier(kValu, 16, 0);
+                if (i == 0) __builtin_amdgcn_sched_group_barrier(kDsWrite, 1, 0);
+                if (i == 1 || i == (FRAG ? 0 : 3)) __builtin_amdgcn_sched_group_barrier(kVmemRead, 1, 0);
+            }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        products(xs + buf * kXHalf);
-        W = Wn;
-        __syncthreads();
+    };
+    constexpr int kAhead = FRAG ? 1 : 2;  // steps by which the weights are loaded ahead
+
+    constexpr std::true_type kWhole;
+    constexpr std::false_type kMasked;
+    x_load<MT, XMX, false>(X, p, m0, kbeg, kend, tid);
+    w_load(kMasked, W[0], kbeg);
+    x_store<MT, XMX>(X, xs, tid);
+    if (kbeg + kStep < kend) {
+        x_load<MT, XMX, false>(X, p, m0, kbeg + kStep, kend, tid);
+        if (!FRAG) w_load(kMasked, W[1], kbeg + kStep);
     }
+    __syncthreads();
+    b_frag(B[0], 0, 0);
+    a_frag(A[0], W[0], 0);
+    // Two whole steps per turn without a branch, as long as everything they load lies inside the slice, W[s % 2]
+    // holding the weights of step s; the last steps with masks.
+    int64_t k0 = kbeg;
+    for (; k0 + 4 * kStep <= kend; k0 += 2 * kStep) {
+#pragma unroll
+        for (int b2 = 0; b2 < 2; ++b2)
+            step(b2, W[b2], W[b2 ^ 1],
+                 [&]() __attribute__((always_inline)) { x_store<MT, XMX>(X, xs + (b2 ^ 1) * kXHalf, tid); },
+                 [&]() __attribute__((always_inline)) { x_load<MT, XMX, true>(X, p, m0, k0 + (b2 + 2) * kStep, kend, tid); },
+                 [&](Weights &D) __attribute__((always_inline)) { w_load(kWhole, D, k0 + (b2 + kAhead) * kStep); });
+    }
+#pragma unroll 1
+    for (int buf = 0; k0 < kend; k0 += kStep, buf ^= 1) {
+        Weights after = W[1];
+        step(buf, W[0], W[1],
+             [&]() __attribute__((always_inline)) { if (k0 + kStep < kend) x_store<MT, XMX>(X, xs + (buf ^ 1) * kXHalf, tid); },
+             [&]() __attribute__((always_inline)) { if (k0 + 2 * kStep < kend) x_load<MT, XMX, false>(X, p, m0, k0 + 2 * kStep, kend, tid); },
+             [&](Weights &) __attribute__((always_inline)) { if (k0 + kAhead * kStep < kend) w_load(kMasked, FRAG ? W[1] : after, k0 + kAhead * kStep); });
+        W[0] = W[1];
+        if (!FRAG) W[1] = after;
+    }
+    __syncthreads();  // the last phase has read ahead; what it read is not used
 
     // The sums go through LDS, kTpr tiles of 32 rows by 256 weight rows at a time, so that the epilogue works on
     // whole rows: a thread takes eight consecutive output columns, a row's threads are consecutive. 16-byte
