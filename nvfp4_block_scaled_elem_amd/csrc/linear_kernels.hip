@@ -33,6 +33,14 @@ __device__ __forceinline__ int clamp_count(int64_t left, int most) {
     return left >= most ? most : left > 0 ? (int)left : 0;
 }
 
+// A barrier that orders LDS alone: __syncthreads also waits until the work-group's stores to global memory have
+// been acknowledged, which nothing here depends on.
+__device__ __forceinline__ void lds_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // ------------------------------------------------------------------------------------- activations
 
 constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
@@ -64,53 +72,128 @@ __device__ __forceinline__ float2 act_both(float z, int act) {
 
 // ---------------------------------------------------------------------------------------- epilogue
 
-__device__ __forceinline__ void add8(const void *b, int f32, int64_t e, int n, float v[8]) {
-    float t[8];
-    if (f32) {
-        Raw8<float> r;
-        r.load(static_cast<const float *>(b) + e, n);
-        r.get(t);
-    } else {
-        Raw8<uint16_t> r;
-        r.load(static_cast<const uint16_t *>(b) + e, n);
-        r.get(t);
+// Eight values of a row of bias or residual (bf16 or fp32), n of them in the matrix; the rest read as zeros.
+// WHOLE, here and below: n is 0 or 8 (the output's columns are a multiple of eight), which leaves one vector
+// access behind a mask; else the end of a row is taken element by element.
+template <bool WHOLE>
+struct RawAny {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const void *q, int f32, int64_t e, int n) {
+        a = b = make_uint4(0u, 0u, 0u, 0u);
+        if (WHOLE && n == 0) return;
+        if (f32) {
+            Raw8<float> r;
+            r.load(static_cast<const float *>(q) + e, WHOLE ? 8 : n);
+            a = r.a, b = r.b;
+        } else {
+            Raw8<uint16_t> r;
+            r.load(static_cast<const uint16_t *>(q) + e, WHOLE ? 8 : n);
+            a = r.a;
+        }
     }
+    __device__ __forceinline__ void get(int f32, float v[8]) const {
+        const uint32_t d[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] += t[i];
+        for (int i = 0; i < 8; ++i)
+            v[i] = f32 ? __uint_as_float(d[i]) : i & 1 ? bf16_hi(d[i >> 1]) : bf16_lo(d[i >> 1]);
+    }
+};
+
+template <bool WHOLE, typename T>
+__device__ __forceinline__ void put(T *q, const float v[8], int n) {
+    if (!WHOLE)
+        put8(q, v, n);
+    else if (n > 0)
+        put8(q, v, 8);
 }
 
-__device__ __forceinline__ void keep8(const LinArgs &p, int64_t m, int64_t col, int n, const float v[8], int lane) {
-    if (p.keep == kKeepMx)
-        mx_put8(static_cast<uint8_t *>(p.z) + m * p.N + col,
-                p.zs + m * ((p.N + kMxBlock - 1) / kMxBlock) + col / kMxBlock, v, n, lane);
-    else
-        put8(static_cast<uint16_t *>(p.z) + m * p.N + col, v, n);
+// What an epilogue does. Plain (y = alpha * sum in bf16, nothing else: the gradient's product, projections without
+// extras) is a kernel of its own, since a work-group's epilogue is not overlapped with anything where one fills a
+// CU; the others look at the call's arguments as they go.
+enum { kEpiPlain = 0, kEpiFull = 1, kEpiGated = 2 };
+
+// bias of the output columns f .. f + 7 and of their gate partners (zeros without a bias).
+template <int EPI, bool WHOLE>
+__device__ __forceinline__ void load_bias(const LinArgs &p, int64_t f, int n, float bg[8], float bu[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) bg[i] = bu[i] = 0.0f;
+    if (EPI == kEpiPlain || !p.bias) return;
+    RawAny<WHOLE> r;
+    r.load(p.bias, p.bias_f32, f, n);
+    r.get(p.bias_f32, bg);
+    if (EPI == kEpiGated) {
+        r.load(p.bias, p.bias_f32, p.F + f, n);
+        r.get(p.bias_f32, bu);
+    }
 }
 
-// Everything after alpha * sum for the output columns f .. f + 7 of row m, n of them in the matrix (0: the
-// lane only takes part in its block's maximum; a quad of lanes holds 32 consecutive columns). g: z of the
-// columns; u: their gate partners.
-__device__ __forceinline__ void epilogue8(const LinArgs &p, int64_t m, int64_t f, int n, float g[8], float u[8],
-                                          int lane) {
-    if (p.bias) {
-        add8(p.bias, p.bias_f32, f, n, g);
-        if (p.gated) add8(p.bias, p.bias_f32, p.F + f, n, u);
-    }
-    if (p.keep != kKeepNone) {
-        keep8(p, m, f, n, g, lane);
-        if (p.gated) keep8(p, m, p.F + f, n, u, lane);
-    }
-    if (p.act != kActNone)
+// Everything after alpha * sum for the output columns f .. f + 7 of R rows m, m + dm, ..., n[r] of which columns are in
+// the matrix (0: the lane only takes part in its block's maximum; a quad of lanes holds 32 consecutive columns).
+// g: alpha * sum of the columns; u: of their gate partners; res: the residual's values, requested by the caller
+// ahead. Row by row inside each step, so that a step's branches are taken once for all rows.
+template <int EPI, bool WHOLE, int R>
+__device__ __forceinline__ void epilogue(const LinArgs &p, int64_t m, int64_t dm, int64_t f, const int n[R], float g[R][8],
+                                         float u[R][8], const float bg[8], const float bu[8],
+                                         const RawAny<WHOLE> res[R], int lane) {
+    if (EPI == kEpiPlain) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] = act_value(g[i], p.act);
-    if (p.gated)
+        for (int r = 0; r < R; ++r) put<WHOLE>(static_cast<uint16_t *>(p.y) + (m + r * dm) * p.F + f, g[r], n[r]);
+        return;
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) g[i] *= u[i];
-    if (p.res) add8(p.res, p.res_f32, m * p.ldr + f, n, g);
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            g[r][i] += bg[i];
+            if (EPI == kEpiGated) u[r][i] += bu[i];
+        }
+    if (p.keep == kKeepMx) {
+        const int64_t nb = (p.N + kMxBlock - 1) / kMxBlock;
+        uint8_t *z = static_cast<uint8_t *>(p.z);
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int64_t row = m + r * dm, e = row * p.N + f, s = row * nb + f / kMxBlock;
+            mx_put8<WHOLE>(z + e, p.zs + s, g[r], n[r], lane);
+            if (EPI == kEpiGated) mx_put8<WHOLE>(z + e + p.F, p.zs + s + p.F / kMxBlock, u[r], n[r], lane);
+        }
+    } else if (p.keep == kKeepBf16) {
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            uint16_t *z = static_cast<uint16_t *>(p.z) + (m + r * dm) * p.N + f;
+            put<WHOLE>(z, g[r], n[r]);
+            if (EPI == kEpiGated) put<WHOLE>(z + p.F, u[r], n[r]);
+        }
+    }
+    if (p.act == kActSilu) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[r][i] = act_value(g[r][i], kActSilu);
+    } else if (p.act == kActGelu) {
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[r][i] = act_value(g[r][i], kActGelu);
+    }
+    if (EPI == kEpiGated)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[r][i] *= u[r][i];
+    if (p.res)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            float v[8];
+            res[r].get(p.res_f32, v);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[r][i] += v[i];
+        }
     if (p.y_f32)
-        put8(static_cast<float *>(p.y) + m * p.F + f, g, n);
+#pragma unroll
+        for (int r = 0; r < R; ++r) put<WHOLE>(static_cast<float *>(p.y) + (m + r * dm) * p.F + f, g[r], n[r]);
     else
-        put8(static_cast<uint16_t *>(p.y) + m * p.F + f, g, n);
+#pragma unroll
+        for (int r = 0; r < R; ++r) put<WHOLE>(static_cast<uint16_t *>(p.y) + (m + r * dm) * p.F + f, g[r], n[r]);
 }
 
 // --------------------------------------------------------------------------------------- tile kernel
@@ -141,34 +224,51 @@ struct XStage {
     uint32_t sb[XMX ? kLoads : 1];
 };
 
+// Where a thread reads X: byte offsets from the first row and k of the work-group's tile, which are uniform (rows
+// past the last read the last: the API keeps ld below 2^23, so 32 bits hold them).
+template <int MT, bool XMX>
+struct XAddr {
+    static constexpr int kLoads = XStage<MT, XMX>::kLoads;
+    const uint8_t *x, *xs;  // row m0, k = 0
+    uint32_t off[kLoads], soff[XMX ? kLoads : 1];
+    int kk;  // the thread's first k in a step
+    __device__ __forceinline__ XAddr(const LinArgs &p, int64_t m0, int tid) {
+        const int last = (int)min((int64_t)(32 * MT - 1), p.M - 1 - m0);
+        const int64_t nb = (p.L + kMxBlock - 1) / kMxBlock;
+        x = static_cast<const uint8_t *>(p.x) + m0 * p.ldx * (XMX ? 1 : 2);
+        xs = XMX ? p.xs + m0 * nb : nullptr;
+        kk = XMX ? 16 * (tid & 3) : 8 * (tid & 7);
+#pragma unroll
+        for (int i = 0; i < kLoads; ++i) {
+            const int row = min(last, XMX ? (tid >> 2) + 64 * i : (tid >> 3) + 32 * i);
+            off[i] = (uint32_t)row * (uint32_t)p.ldx * (XMX ? 1u : 2u) + (uint32_t)kk * (XMX ? 1u : 2u);
+            if (XMX) soff[i] = (uint32_t)row * (uint32_t)nb + (uint32_t)(kk / kMxBlock);
+        }
+    }
+};
+
 // WHOLE: the step lies inside the slice (else its k are masked).
 template <int MT, bool XMX, bool WHOLE>
-__device__ __forceinline__ void x_load(XStage<MT, XMX> &S, const LinArgs &p, int64_t m0, int64_t k0, int64_t kend, int tid) {
-    const bool whole = WHOLE || k0 + kStep <= kend;
+__device__ __forceinline__ void x_load(XStage<MT, XMX> &S, const XAddr<MT, XMX> &q, int64_t k0, int64_t kend, int tid) {
+    const uint8_t *x = q.x + k0 * (XMX ? 1 : 2);
     if (XMX) {  // four threads per row, 16 codes each; k0 and kend are multiples of 16
-        const int64_t k = k0 + 16 * (tid & 3);
-        const int64_t nb = (p.L + kMxBlock - 1) / kMxBlock;
+        const uint8_t *xs = q.xs + k0 / kMxBlock;
 #pragma unroll
         for (int i = 0; i < S.kLoads; ++i) {
-            const int64_t m = min(p.M - 1, m0 + (tid >> 2) + 64 * i);
-            S.v[i] = make_uint4(0u, 0u, 0u, 0u);
-            S.sb[i] = 0u;
-            if ((MT > 1 || tid < 128) && (whole || k < kend)) {
-                S.v[i] = load16(static_cast<const uint8_t *>(p.x) + m * p.ldx + k);
-                S.sb[i] = p.xs[m * nb + k / kMxBlock];
+            if (!WHOLE) S.v[i] = make_uint4(0u, 0u, 0u, 0u), S.sb[i] = 0u;
+            if ((MT > 1 || tid < 128) && (WHOLE || k0 + q.kk < kend)) {
+                S.v[i] = load16(x + q.off[i]);
+                S.sb[i] = xs[q.soff[i]];
             }
         }
     } else {  // eight threads per row, 8 values each
-        const int64_t k = k0 + 8 * (tid & 7);
 #pragma unroll
         for (int i = 0; i < S.kLoads; ++i) {
-            const int64_t m = min(p.M - 1, m0 + (tid >> 3) + 32 * i);
-            const uint16_t *q = static_cast<const uint16_t *>(p.x) + m * p.ldx + k;
-            if (whole) {
-                S.v[i] = load16(q);
+            if (WHOLE || k0 + kStep <= kend) {
+                S.v[i] = load16(x + q.off[i]);
             } else {
                 Raw8<uint16_t> r;
-                r.load(q, clamp_count(kend - k, 8));
+                r.load(reinterpret_cast<const uint16_t *>(x + q.off[i]), clamp_count(kend - k0 - q.kk, 8));
                 S.v[i] = r.a;
             }
         }
@@ -216,13 +316,15 @@ struct WFrag {
 };
 
 // MT: tiles of 32 rows of X. FRAG: the weights come decoded, in the order of the fragments (k_lin_transpose).
-template <int MT, bool XMX, bool FRAG>
+template <int MT, bool XMX, bool FRAG, int EPI>
 __global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinArgs p) {
     constexpr int kTpr = MT >= 8 ? 2 : 1, kXHalf = 32 * MT * kStep;  // tiles per epilogue round; one X buffer
     constexpr int kLds = 2 * kXHalf * 2 > kTpr * 32768 ? 2 * kXHalf * 2 : kTpr * 32768;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
     uint16_t *const xs = reinterpret_cast<uint16_t *>(lds);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r32 = lane & 31, half = lane >> 5;
+    constexpr bool kGated = EPI == kEpiGated;
+    const int tid = threadIdx.x, lane = tid & 63, r32 = lane & 31, half = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // Work-groups go to the 8 XCDs round robin: give each XCD a contiguous run of tiles, and order the tiles
     // in bands of four along M, so that the work-groups on an XCD share rows of X and of W in its L2.
     const unsigned total = gridDim.x, q8 = total / 8, r8 = total % 8, xcd = blockIdx.x % 8;
@@ -233,48 +335,51 @@ __global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinA
     const int64_t m0 = (int64_t)(4 * band + in % bm) * (32 * MT);
     const int64_t tn = in / bm;
     const int64_t kbeg = (int64_t)slice * p.kslice, kend = min(p.L, kbeg + p.kslice);
-    // first output column of the wave's tile j, and the lane's weight row in it
-    const int64_t f0 = p.gated ? tn * 128 + 32 * wave : tn * 256 + 64 * wave;
-    int64_t wrow[2];
-    if (p.gated) {
-        wrow[0] = min(p.F - 1, f0 + slot_row(r32));
-        wrow[1] = p.F + wrow[0];
-    } else {
-        wrow[0] = min(p.N - 1, f0 + slot_row(r32));
-        wrow[1] = min(p.N - 1, f0 + 32 + slot_row(r32));
-    }
+    // The wave's weight rows: tile j starts at row w0[j] (uniform) and the lane's row is so many bytes of codes and
+    // of scales further; rows past the last read the last.
+    const int64_t f0 = kGated ? tn * 128 + 32 * wave : tn * 256 + 64 * wave;
     const int64_t steps_all = (p.L + kStep - 1) / kStep, ktiles = (p.N + 31) / 32;
+    int64_t w0[2];
+    uint32_t woff[2], wsoff[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int64_t first = kGated ? min(p.F - 1, f0) : min(p.N - 1, f0 + 32 * j);
+        const int row = (int)min((int64_t)slot_row(r32), (kGated ? p.F : p.N) - 1 - first);
+        w0[j] = first + (kGated && j ? p.F : 0);
+        woff[j] = (uint32_t)row * (uint32_t)(p.L / 2) + 16u * half;
+        wsoff[j] = (uint32_t)row * (uint32_t)(p.L / 16) + 2u * half;
+    }
 
     using Weights = typename std::conditional<FRAG, WFrag, WCodes>::type;
     f32x16 acc[2][MT] = {};
-    XStage<MT, XMX> X;
+    // X is loaded two steps ahead of its use, one (with half the registers) where two work-groups share a CU.
+    constexpr int kSets = MT >= 8 ? 2 : 1;
+    XStage<MT, XMX> X[kSets];
+    const XAddr<MT, XMX> xa(p, m0, tid);
     Weights W[2];
     bf16x8 A[2][2], B[2][MT];  // the fragments of one phase and of the next (A: decoded weights alone)
 
     auto w_load = [&](auto whole, Weights &D, int64_t k0) __attribute__((always_inline)) {
-        if constexpr (FRAG) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < 2; ++j) {
+            if constexpr (FRAG) {
                 const int64_t kt = min(ktiles - 1, f0 / 32 + j);
-                const uint16_t *q = p.wt + ((kt * steps_all + k0 / kStep) * 4) * 512 + lane * 8;
+                const uint8_t *q = reinterpret_cast<const uint8_t *>(p.wt) + ((kt * steps_all + k0 / kStep) * 4096);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) D.v[j][i] = *reinterpret_cast<const uint4 *>(q + i * 512);
-            }
-        } else {
-            const int64_t k = k0 + 32 * half;
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint8_t *c = p.codes + (wrow[j] * p.L + k) / 2, *s = p.scales + (wrow[j] * p.L + k) / 16;
+                for (int i = 0; i < 4; ++i) D.v[j][i] = load16(q + (uint32_t)(lane * 16) + i * 1024);
+            } else {
+                const uint8_t *c = p.codes + (w0[j] * p.L + k0) / 2, *s = p.scales + (w0[j] * p.L + k0) / 16;
+                const int64_t k = k0 + 32 * half;
                 if (whole.value || k + 32 <= kend) {
-                    D.c[j] = load16(c);
-                    D.s[j] = load2b(s);
+                    D.c[j] = load16(c + woff[j]);
+                    D.s[j] = load2b(s + wsoff[j]);
                 } else {
                     D.c[j] = make_uint4(0u, 0u, 0u, 0u);
                     D.s[j] = 0u;
                     if (k < kend) {  // the row's last 16
-                        const uint2 c2 = load8b(c);
+                        const uint2 c2 = load8b(c + woff[j]);
                         D.c[j].x = c2.x, D.c[j].y = c2.y;
-                        D.s[j] = *s;
+                        D.s[j] = s[wsoff[j]];
                     }
                 }
             }
@@ -307,8 +412,8 @@ __global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinA
                 acc[j][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, B[i & 1][t], acc[j][t], 0, 0, 0);
             }
     };
-    // Step s from buffer s % 2, in four phases. At its start the fragments of phase 0 are formed, and X of step
-    // s + 1 is in registers or on its way (loaded during step s - 1). Phase i forms the fragments of phase i + 1
+    // Step s from buffer s % 2, in four phases. At its start the fragments of phase 0 are formed, and X of the next
+    // kSets steps is in registers or on its way. Phase i forms the fragments of phase i + 1
     // while the matrix cores work on its own. Coded weights are loaded two steps ahead, in phase 3, over those
     // whose last use was in phase 2; decoded ones one step ahead, in phase 0. The one barrier stands before
     // the last phase: by then every wave has stored X of step s + 1 (in phase 0) and has read all of buffer s % 2,
@@ -319,7 +424,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinA
                     __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (i == 3) __syncthreads();
+            if (i == 3) lds_barrier();
             b_frag(B[(i + 1) & 1], i < 3 ? buf : buf ^ 1, (i + 1) & 3);
             a_frag(A[(i + 1) & 1], i < 3 ? w : next, (i + 1) & 3);
             if (i == 0) store();
@@ -346,38 +451,44 @@ __global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinA
 
     constexpr std::true_type kWhole;
     constexpr std::false_type kMasked;
-    x_load<MT, XMX, false>(X, p, m0, kbeg, kend, tid);
+    x_load<MT, XMX, false>(X[0], xa, kbeg, kend, tid);
     w_load(kMasked, W[0], kbeg);
-    x_store<MT, XMX>(X, xs, tid);
     if (kbeg + kStep < kend) {
-        x_load<MT, XMX, false>(X, p, m0, kbeg + kStep, kend, tid);
+        if (kSets == 2) x_load<MT, XMX, false>(X[kSets - 1], xa, kbeg + kStep, kend, tid);
         if (!FRAG) w_load(kMasked, W[1], kbeg + kStep);
     }
-    __syncthreads();
+    x_store<MT, XMX>(X[0], xs, tid);
+    if (kbeg + kSets * kStep < kend) x_load<MT, XMX, false>(X[0], xa, kbeg + kSets * kStep, kend, tid);
+    lds_barrier();
     b_frag(B[0], 0, 0);
     a_frag(A[0], W[0], 0);
+    // Nothing in flight at the loop's entry: its waits then count the loads of its own turns alone.
+    __builtin_amdgcn_s_waitcnt(0);
     // Two whole steps per turn without a branch, as long as everything they load lies inside the slice, W[s % 2]
-    // holding the weights of step s; the last steps with masks.
+    // holding the weights of step s and X[s % kSets] its X or the next one's of its kind; the last steps with masks.
     int64_t k0 = kbeg;
-    for (; k0 + 4 * kStep <= kend; k0 += 2 * kStep) {
+    for (; k0 + (kSets + 3) * kStep <= kend; k0 += 2 * kStep) {
 #pragma unroll
         for (int b2 = 0; b2 < 2; ++b2)
             step(b2, W[b2], W[b2 ^ 1],
-                 [&]() __attribute__((always_inline)) { x_store<MT, XMX>(X, xs + (b2 ^ 1) * kXHalf, tid); },
-                 [&]() __attribute__((always_inline)) { x_load<MT, XMX, true>(X, p, m0, k0 + (b2 + 2) * kStep, kend, tid); },
+                 [&]() __attribute__((always_inline)) { x_store<MT, XMX>(X[(b2 ^ 1) & (kSets - 1)], xs + (b2 ^ 1) * kXHalf, tid); },
+                 [&]() __attribute__((always_inline)) { x_load<MT, XMX, true>(X[(b2 ^ 1) & (kSets - 1)], xa, k0 + (b2 + 1 + kSets) * kStep, kend, tid); },
                  [&](Weights &D) __attribute__((always_inline)) { w_load(kWhole, D, k0 + (b2 + kAhead) * kStep); });
     }
 #pragma unroll 1
     for (int buf = 0; k0 < kend; k0 += kStep, buf ^= 1) {
         Weights after = W[1];
         step(buf, W[0], W[1],
-             [&]() __attribute__((always_inline)) { if (k0 + kStep < kend) x_store<MT, XMX>(X, xs + (buf ^ 1) * kXHalf, tid); },
-             [&]() __attribute__((always_inline)) { if (k0 + 2 * kStep < kend) x_load<MT, XMX, false>(X, p, m0, k0 + 2 * kStep, kend, tid); },
+             [&]() __attribute__((always_inline)) { if (k0 + kStep < kend) x_store<MT, XMX>(X[kSets - 1], xs + (buf ^ 1) * kXHalf, tid); },
+             [&]() __attribute__((always_inline)) {
+                 if (kSets == 2) X[kSets - 1] = X[0];
+                 if (k0 + (1 + kSets) * kStep < kend) x_load<MT, XMX, false>(X[0], xa, k0 + (1 + kSets) * kStep, kend, tid);
+             },
              [&](Weights &) __attribute__((always_inline)) { if (k0 + kAhead * kStep < kend) w_load(kMasked, FRAG ? W[1] : after, k0 + kAhead * kStep); });
         W[0] = W[1];
         if (!FRAG) W[1] = after;
     }
-    __syncthreads();  // the last phase has read ahead; what it read is not used
+    lds_barrier();  // the last phase has read ahead; what it read is not used
 
     // The sums go through LDS, kTpr tiles of 32 rows by 256 weight rows at a time, so that the epilogue works on
     // whole rows: a thread takes eight consecutive output columns, a row's threads are consecutive. 16-byte
@@ -385,14 +496,59 @@ __global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinA
     float *const es = reinterpret_cast<float *>(lds);
     auto place = [](int row, int chunk) { return row * 256 + ((chunk ^ (row & 7)) << 2); };
     const float alpha = p.part ? 1.0f : *p.alpha;
-    const int cols = p.gated ? 128 : 256, threads = cols / 8;  // output columns of the work-group; threads per row
+    constexpr int cols = kGated ? 128 : 256, threads = cols / 8;  // output columns of the work-group; threads per row
+    constexpr int stride = kTileThreads / threads;  // a thread's rows are so far apart
     const int fl = 8 * (tid % threads);
-    const int ch = p.gated ? 16 * (fl / 32) + (fl % 32) / 4 : fl / 4;  // the chunk of column fl
+    const int ch = kGated ? 16 * (fl / 32) + (fl % 32) / 4 : fl / 4;    // the chunk of column fl
     const int64_t f = tn * cols + fl;
     const int nf = clamp_count(p.F - f, 8);
+    // A thread's rows of a round, up to four at a time: with one work-group per CU nothing else hides the latency
+    // of their LDS reads and residuals.
+    constexpr int kMine = 32 * kTpr / stride;
+    auto rows_out = [&](auto whole, int round) __attribute__((always_inline)) {
+        constexpr bool kWholeRow = decltype(whole)::value;
+        constexpr int kRows = !kWholeRow ? 1 : kMine < 4 ? kMine : 4;
+        float bg[8], bu[8];
+        load_bias<EPI, kWholeRow>(p, f, p.part ? 0 : nf, bg, bu);
+#pragma unroll 1
+        for (int row = tid / threads; row < 32 * kTpr; row += kRows * stride) {
+            const int64_t m = m0 + 32 * kTpr * round + row;
+            int n[kRows];
+            RawAny<kWholeRow> res[kRows];
+            float g[kRows][8], u[kRows][8];
+#pragma unroll
+            for (int r = 0; r < kRows; ++r) n[r] = m + r * stride < p.M ? nf : 0;
+            if (EPI != kEpiPlain && p.res && !p.part)
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) res[r].load(p.res, p.res_f32, (m + r * stride) * p.ldr + f, n[r]);
+#pragma unroll
+            for (int r = 0; r < kRows; ++r)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const f32x4 v = *reinterpret_cast<const f32x4 *>(&es[place(row + r * stride, ch + c)]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) g[r][4 * c + i] = alpha * v[i];
+                    if (kGated) {
+                        const f32x4 w = *reinterpret_cast<const f32x4 *>(&es[place(row + r * stride, ch + 8 + c)]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) u[r][4 * c + i] = alpha * w[i];
+                    }
+                }
+            if (p.part) {  // fp32 sums of this slice, without alpha
+#pragma unroll
+                for (int r = 0; r < kRows; ++r) {
+                    float *q = p.part + ((int64_t)slice * p.M + m + r * stride) * p.N + f;
+                    put<kWholeRow>(q, g[r], n[r]);
+                    if (kGated) put<kWholeRow>(q + p.F, u[r], n[r]);
+                }
+            } else {
+                epilogue<EPI, kWholeRow, kRows>(p, m, stride, f, n, g, u, bg, bu, res, lane);
+            }
+        }
+    };
 #pragma unroll 1
     for (int round = 0; round < MT / kTpr; ++round) {
-        auto dump = [&](int t, const f32x16 &a0, const f32x16 &a1) {
+        auto dump = [&](int t, const f32x16 &a0, const f32x16 &a1) __attribute__((always_inline)) {
 #pragma unroll
             for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -407,32 +563,12 @@ __global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinA
             if (r == round)
 #pragma unroll
                 for (int t = 0; t < kTpr; ++t) dump(t, acc[0][r * kTpr + t], acc[1][r * kTpr + t]);
-        __syncthreads();
-#pragma unroll 1
-        for (int row = tid / threads; row < 32 * kTpr; row += kTileThreads / threads) {
-            const int64_t m = m0 + 32 * kTpr * round + row;
-            const int n = m < p.M ? nf : 0;
-            float g[8], u[8] = {};
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const f32x4 v = *reinterpret_cast<const f32x4 *>(&es[place(row, ch + c)]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) g[4 * c + i] = alpha * v[i];
-                if (p.gated) {
-                    const f32x4 w = *reinterpret_cast<const f32x4 *>(&es[place(row, ch + 8 + c)]);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) u[4 * c + i] = alpha * w[i];
-                }
-            }
-            if (p.part) {  // fp32 sums of this slice, without alpha
-                float *q = p.part + ((int64_t)slice * p.M + m) * p.N + f;
-                put8(q, g, n);
-                if (p.gated) put8(q + p.F, u, n);
-            } else {
-                epilogue8(p, m, f, n, g, u, lane);
-            }
-        }
-        __syncthreads();
+        lds_barrier();
+        if (p.F % 8 == 0)
+            rows_out(kWhole, round);
+        else
+            rows_out(kMasked, round);
+        lds_barrier();
     }
 }
 
@@ -440,31 +576,36 @@ constexpr int kReduceThreads = 256;
 
 // The slices' sums added in slice order, then the epilogue: eight columns per thread, rows padded to whole
 // 32-column blocks so that a quad holds a block.
+template <int EPI, bool WHOLE>
 __global__ __launch_bounds__(kReduceThreads) void k_lin_reduce(LinArgs p, int slices, int64_t per_row, int64_t groups) {
     const float alpha = *p.alpha;
     for (int64_t i = (int64_t)blockIdx.x * kReduceThreads + threadIdx.x; i < groups;
          i += (int64_t)gridDim.x * kReduceThreads) {
         const int64_t m = i / per_row, f = 8 * (i - m * per_row);
-        const int n = clamp_count(p.F - f, 8);
-        float g[8] = {}, u[8] = {};
+        const int n[1] = {clamp_count(p.F - f, 8)};
+        RawAny<WHOLE> res[1];
+        float g[1][8] = {}, u[1][8] = {}, bg[8], bu[8];
+        if (EPI != kEpiPlain && p.res) res[0].load(p.res, p.res_f32, m * p.ldr + f, n[0]);
+        load_bias<EPI, WHOLE>(p, f, n[0], bg, bu);
+#pragma unroll 4
         for (int s = 0; s < slices; ++s) {
             const float *q = p.part + ((int64_t)s * p.M + m) * p.N + f;
-            Raw8<float> r;
+            RawAny<WHOLE> r;
             float v[8];
-            r.load(q, n);
-            r.get(v);
+            r.load(q, 1, 0, n[0]);
+            r.get(1, v);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] += v[e];
-            if (p.gated) {
-                r.load(q + p.F, n);
-                r.get(v);
+            for (int e = 0; e < 8; ++e) g[0][e] += v[e];
+            if (EPI == kEpiGated) {
+                r.load(q + p.F, 1, 0, n[0]);
+                r.get(1, v);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) u[e] += v[e];
+                for (int e = 0; e < 8; ++e) u[0][e] += v[e];
             }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] *= alpha, u[e] *= alpha;
-        epilogue8(p, m, f, n, g, u, (int)(threadIdx.x & 63));
+        for (int e = 0; e < 8; ++e) g[0][e] *= alpha, u[0][e] *= alpha;
+        epilogue<EPI, WHOLE, 1>(p, m, 0, f, n, g, u, bg, bu, res, (int)(threadIdx.x & 63));
     }
 }
 
@@ -729,26 +870,39 @@ LinPlan plan_tile(int64_t M, int64_t L, int64_t F, int64_t N, bool gated) {
     return p;
 }
 
-template <bool XMX, bool FRAG>
-hipError_t tile_launch(LinArgs p, const LinPlan &plan, hipStream_t st) {
-    p.tiles_n = (unsigned)plan.tiles_n, p.tiles_m = (unsigned)plan.tiles_m;
-    p.tiles = (unsigned)(plan.tiles_n * plan.tiles_m);
-    p.kslice = plan.kslice;
+template <bool XMX, bool FRAG, int EPI>
+hipError_t tile_launch_as(const LinArgs &p, const LinPlan &plan, hipStream_t st) {
     const dim3 grid((unsigned)(p.tiles * plan.slices)), block(kTileThreads);
     switch (plan.mt) {
-        case 1: hipLaunchKernelGGL((k_lin_tile<1, XMX, FRAG>), grid, block, 0, st, p); break;
-        case 2: hipLaunchKernelGGL((k_lin_tile<2, XMX, FRAG>), grid, block, 0, st, p); break;
-        case 4: hipLaunchKernelGGL((k_lin_tile<4, XMX, FRAG>), grid, block, 0, st, p); break;
-        default: hipLaunchKernelGGL((k_lin_tile<8, XMX, FRAG>), grid, block, 0, st, p); break;
+        case 1: hipLaunchKernelGGL((k_lin_tile<1, XMX, FRAG, EPI>), grid, block, 0, st, p); break;
+        case 2: hipLaunchKernelGGL((k_lin_tile<2, XMX, FRAG, EPI>), grid, block, 0, st, p); break;
+        case 4: hipLaunchKernelGGL((k_lin_tile<4, XMX, FRAG, EPI>), grid, block, 0, st, p); break;
+        default: hipLaunchKernelGGL((k_lin_tile<8, XMX, FRAG, EPI>), grid, block, 0, st, p); break;
     }
     hipError_t err = hipGetLastError();
     if (err == hipSuccess && plan.slices > 1) {
         const int64_t per_row = ceil_div(p.F, kMxBlock) * 4, groups = p.M * per_row;
         const dim3 rg((unsigned)std::min<int64_t>(ceil_div(groups, kReduceThreads), 4096));
-        hipLaunchKernelGGL(k_lin_reduce, rg, dim3(kReduceThreads), 0, st, p, (int)plan.slices, per_row, groups);
+        if (p.F % 8 == 0)
+            hipLaunchKernelGGL((k_lin_reduce<EPI, true>), rg, dim3(kReduceThreads), 0, st, p, (int)plan.slices, per_row, groups);
+        else
+            hipLaunchKernelGGL((k_lin_reduce<EPI, false>), rg, dim3(kReduceThreads), 0, st, p, (int)plan.slices, per_row, groups);
         err = hipGetLastError();
     }
     return err;
+}
+
+template <bool XMX, bool FRAG>
+hipError_t tile_launch(LinArgs p, const LinPlan &plan, hipStream_t st) {
+    p.tiles_n = (unsigned)plan.tiles_n, p.tiles_m = (unsigned)plan.tiles_m;
+    p.tiles = (unsigned)(plan.tiles_n * plan.tiles_m);
+    p.kslice = plan.kslice;
+    if constexpr (!FRAG) {
+        if (p.gated) return tile_launch_as<XMX, FRAG, kEpiGated>(p, plan, st);
+        if (p.bias || p.res || p.act != kActNone || p.keep != kKeepNone || p.y_f32)
+            return tile_launch_as<XMX, FRAG, kEpiFull>(p, plan, st);
+    }
+    return tile_launch_as<XMX, FRAG, kEpiPlain>(p, plan, st);
 }
 
 template <int NT, bool XMX>

@@ -167,15 +167,17 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t m) {
 
 // The lane's eight values (n of them in the row, 0..8) of a 32-value block held by a quad, to memory: codes
 // at `codes`, the block's scale byte by the quad's first lane at `scale`.
+// WHOLE: n is 0 or 8.
+template <bool WHOLE = false>
 __device__ __forceinline__ void mx_put8(uint8_t *codes, uint8_t *scale, const float v[8], int n, int lane) {
     float w[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = i < n ? v[i] : 0.0f;  // past the row: no part in the maximum
+    for (int i = 0; i < 8; ++i) w[i] = (WHOLE ? n > 0 : i < n) ? v[i] : 0.0f;  // past the row: no part in the maximum
     const uint32_t sb = mx_scale_byte(quad_max(amax8(w)));
     const uint2 c = mx_encode8(w, sb);
     if (n >= 8) {
         store8b(codes, c);
-    } else {
+    } else if (!WHOLE) {
 #pragma unroll
         for (int i = 0; i < 7; ++i)
             if (i < n) codes[i] = (uint8_t)((i < 4 ? c.x : c.y) >> (8 * (i & 3)));
