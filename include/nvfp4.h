@@ -350,7 +350,7 @@ enum nvfp4_activation { NVFP4_ACT_NONE = 0, NVFP4_ACT_SILU = 1, NVFP4_ACT_GELU =
  *   y [M][F] = act(z[:, :F]) * z[:, F:] + residual: rows 0 .. F-1 of the weights are the gate.
  * x is bf16 or MXFP8 [M][K]; bias [N] and residual (as y) bf16 or fp32, NULL for none; y bf16 or fp32; z, kept
  * for the gradient, bf16 or MXFP8 (z_scales), NULL if not (gated and MXFP8: F % 32 == 0). K % 16 == 0; K, N
- * <= 2^21. codes 8-byte aligned. residual may be y itself (contiguous, of y's type).
+ * <= 2^21, ldx < 2^23 (else NVFP4_ERR_SHAPE). codes 8-byte aligned. residual may be y itself (contiguous, of y's type).
  * Arithmetic: as nvfp4_matmul (exact products, fp32 sums), then fp32 and one rounding per output. Values of
  * an MXFP8 x below 2^-126 may count as zero. */
 typedef struct nvfp4_linear_args {
@@ -381,7 +381,8 @@ typedef struct nvfp4_linear_args {
 
 int nvfp4_linear(const nvfp4_linear_args_t *args);
 
-/* Scratch of one nvfp4_linear call (fp32 sums where K is split over work-groups; often 0). z_dtype: the form
+/* Scratch of one nvfp4_linear call (fp32 sums where K is split over work-groups; the decoded weights for many
+ * rows; 0 for few). z_dtype: the form
  * in which z is kept, NVFP4_DTYPE_BF16 also where it is not. */
 size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int gated, int z_dtype);
 
@@ -391,7 +392,7 @@ size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int gated, 
  *   dx [M][K] bf16 = alpha * (dz Wq), of dz as rounded (the products are exact, the sums fp32);
  *   dbias [N] fp32 = the sum over rows of dz unrounded (NULL: not formed).
  * z is what nvfp4_linear kept, bf16 or MXFP8 (contiguous scales). activation = none: z and dz are NULL and
- * dz = dy. Scratch: the decoded weights and partial sums, nvfp4_linear_grad_workspace_bytes. */
+ * dz = dy. lddy < 2^23. Scratch: the decoded weights and partial sums, nvfp4_linear_grad_workspace_bytes. */
 typedef struct nvfp4_linear_grad_args {
     const void *dy;
     int64_t lddy;

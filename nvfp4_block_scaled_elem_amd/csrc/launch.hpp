@@ -172,11 +172,12 @@ struct LinGradArgs {
 struct LinPlan {
     int mt;  // tiles of 32 rows of X per work-group; 0: the skinny kernel
     int64_t tiles_m, tiles_n, slices, kslice;
-    size_t part_bytes;
+    size_t part_bytes;  // fp32 sums of the K slices (0: K is not split)
+    size_t wt_bytes;    // decoded weights (0: decoded in the product); not both
 };
 LinPlan plan_linear(int64_t M, int64_t K, int64_t N, bool gated, int keep);
-// `part` holds the plan's part_bytes when it splits K.
-hipError_t launch_linear(const LinArgs &p, float *part, hipStream_t stream);
+// `ws` holds the plan's part_bytes or wt_bytes.
+hipError_t launch_linear(const LinArgs &p, void *ws, hipStream_t stream);
 size_t linear_grad_workspace(int64_t M, int64_t K, int64_t N, int64_t F, bool bias);
 hipError_t launch_linear_grad(const LinGradArgs &g, const uint8_t *codes, const uint8_t *scales, const float *alpha,
                               int64_t K, void *dx, float *dbias, void *ws, hipStream_t stream);

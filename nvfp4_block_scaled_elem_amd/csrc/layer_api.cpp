@@ -5,7 +5,7 @@
 //   nvfp4_rms_norm_grad   : k_rms_norm_grad -> k_column_sum (beyond 16384 columns: k_rms_norm_grad_long ->
 //                           k_rms_norm_dw_long -> k_column_sum)
 //   nvfp4_mxfp8_quantize / nvfp4_mxfp8_dequantize : one kernel each
-//   nvfp4_linear          : k_lin_skinny, or k_lin_tile (-> k_lin_reduce where K is split)
+//   nvfp4_linear          : k_lin_skinny, or (k_lin_decode ->) k_lin_tile (-> k_lin_reduce where K is split)
 //   nvfp4_linear_grad     : (k_lin_dz with an activation or dbias; -> k_column_sum with dbias) -> k_lin_transpose ->
 //                           k_lin_tile (-> k_lin_reduce)
 #include <hip/hip_runtime.h>
@@ -139,6 +139,7 @@ NVFP4_API int nvfp4_mxfp8_dequantize(const uint8_t *codes, int64_t ldc, const ui
 
 namespace {
 
+constexpr int64_t kMaxLd = (int64_t)1 << 23;    // a product's X: 256 rows of it stay below 2^32 bytes
 constexpr int64_t kMaxSide = (int64_t)1 << 21;  // K and N of a product: grids stay below 65536 along y
 
 // The shapes of a product [M][K] x [N][K]^T, gated or not.
@@ -155,8 +156,9 @@ int check_product(int64_t M, int64_t K, int64_t N, int activation, int gated) {
 
 NVFP4_API size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int gated, int z_dtype) {
     if (check_product(M, K, N, gated ? NVFP4_ACT_SILU : NVFP4_ACT_NONE, gated) != NVFP4_OK || M == 0) return 0;
-    return nvfp4::plan_linear(M, K, N, gated != 0, z_dtype == NVFP4_DTYPE_MXFP8 ? nvfp4::kKeepMx : nvfp4::kKeepNone)
-        .part_bytes;
+    const nvfp4::LinPlan plan =
+        nvfp4::plan_linear(M, K, N, gated != 0, z_dtype == NVFP4_DTYPE_MXFP8 ? nvfp4::kKeepMx : nvfp4::kKeepNone);
+    return plan.part_bytes + plan.wt_bytes;
 }
 
 NVFP4_API int nvfp4_linear(const nvfp4_linear_args_t *a) {
@@ -176,6 +178,7 @@ NVFP4_API int nvfp4_linear(const nvfp4_linear_args_t *a) {
         (a->z && zmx) != (a->z_scales != nullptr))
         return NVFP4_ERR_INVALID_ARG;
     if (a->M > 1 && (a->ldx < a->K || (a->residual && a->ldr < F))) return NVFP4_ERR_INVALID_ARG;
+    if (a->M > 1 && a->ldx >= kMaxLd) return NVFP4_ERR_SHAPE;
     if (!aligned(a->x, width(a->x_dtype)) || !aligned(a->codes, 8) || !aligned(a->alpha, 4) ||
         !aligned(a->y, width(a->y_dtype)) || (a->bias && !aligned(a->bias, width(a->bias_dtype))) ||
         (a->residual && !aligned(a->residual, width(a->residual_dtype))) || (a->z && !aligned(a->z, width(a->z_dtype))))
@@ -190,9 +193,9 @@ NVFP4_API int nvfp4_linear(const nvfp4_linear_args_t *a) {
     p.M = a->M, p.L = a->K, p.N = a->N, p.F = F, p.act = a->activation, p.gated = a->gated;
     if (a->M == 1) p.ldx = a->K;
     hipStream_t st = static_cast<hipStream_t>(a->stream);
-    const size_t need = nvfp4::plan_linear(p.M, p.L, p.N, p.gated, p.keep).part_bytes;
-    return with_scratch(a->workspace, a->workspace_bytes, need, st,
-                        [&](void *ws) { return nvfp4::launch_linear(p, static_cast<float *>(ws), st); });
+    const nvfp4::LinPlan plan = nvfp4::plan_linear(p.M, p.L, p.N, p.gated, p.keep);
+    return with_scratch(a->workspace, a->workspace_bytes, plan.part_bytes + plan.wt_bytes, st,
+                        [&](void *ws) { return nvfp4::launch_linear(p, ws, st); });
 }
 
 NVFP4_API size_t nvfp4_linear_grad_workspace_bytes(int64_t M, int64_t K, int64_t N, int gated, int with_dbias) {
@@ -214,6 +217,7 @@ NVFP4_API int nvfp4_linear_grad(const nvfp4_linear_grad_args_t *a) {
             act != (a->dz != nullptr) || zmx != (a->z_scales != nullptr))
             return NVFP4_ERR_INVALID_ARG;
         if (a->M > 1 && (a->lddy < F || (act && a->ldz < a->N))) return NVFP4_ERR_INVALID_ARG;
+        if (a->M > 1 && a->lddy >= kMaxLd) return NVFP4_ERR_SHAPE;
         if (!aligned(a->dy, 2) || !aligned(a->codes, 8) || !aligned(a->alpha, 4) || !aligned(a->dx, 2) ||
             !aligned(a->dz, 2) || (act && !aligned(a->z, width(a->z_dtype))))
             return NVFP4_ERR_INVALID_ARG;

@@ -88,7 +88,7 @@ def linear_args(**kw):
     (dict(z_scales=FAKE), INVALID), (dict(gated=1, activation=1, N=96, z=FAKE, z_scales=FAKE, z_dtype=2), SHAPE),
     (dict(codes=FAKE + 4), INVALID), (dict(alpha=FAKE + 2), INVALID), (dict(x=FAKE + 1), INVALID),
     (dict(y=FAKE + 1), INVALID), (dict(workspace=FAKE + 16), INVALID), (dict(K=(1 << 21) + 16), SHAPE),
-    (dict(N=(1 << 21) + 1), SHAPE), (dict(M=1 << 20, K=1 << 16, ldx=1 << 16), SHAPE), (dict(M=0), OK),
+    (dict(N=(1 << 21) + 1), SHAPE), (dict(ldx=1 << 23), SHAPE), (dict(M=1 << 20, K=1 << 16, ldx=1 << 16), SHAPE), (dict(M=0), OK),
     (dict(M=100, K=4096, ldx=4096, workspace=FAKE, workspace_bytes=256), WORKSPACE),
 ])
 def test_linear_rejects(L, kw, err):
@@ -114,7 +114,7 @@ WITH_Z = dict(activation=1, z=FAKE, ldz=64, dz=FAKE)
     (dict(WITH_Z, z_dtype=2), INVALID), (dict(WITH_Z, z=FAKE + 1), INVALID), (dict(gated=1), INVALID),
     (dict(WITH_Z, gated=1, N=96, z_dtype=2, z_scales=FAKE), SHAPE), (dict(WITH_Z, gated=1, N=63), SHAPE),
     (dict(dbias=FAKE + 2), INVALID), (dict(workspace=FAKE + 16), INVALID), (dict(dy=FAKE + 1), INVALID),
-    (dict(codes=FAKE + 4), INVALID), (dict(), WORKSPACE), (dict(WITH_Z), WORKSPACE), (dict(M=0), OK),
+    (dict(lddy=1 << 23), SHAPE), (dict(codes=FAKE + 4), INVALID), (dict(), WORKSPACE), (dict(WITH_Z), WORKSPACE), (dict(M=0), OK),
 ])
 def test_linear_grad_rejects(L, kw, err):
     assert L.nvfp4_linear_grad(ctypes.byref(grad_args(**kw))) == err
