@@ -314,13 +314,25 @@ struct WCodes {
 struct WFrag {
     uint4 v[2][4];
 };
+// A wave's codes of two steps (64 rows of 64 bytes) and their scales (8 bytes a row) between memory and LDS. A lane
+// needs 16 bytes of each of two rows per step, and a load of just those touches 32 lines for 1 KB: four times the
+// address cycles of whole rows, which four lanes read together here.
+struct WStage {
+    uint4 c[4];
+    uint2 s;
+};
+constexpr int kWaveCodes = 64 * 64, kWaveScales = 64 * 8;  // LDS bytes of a wave
+
+// 16-byte chunk q (0..3) of row r of a wave's codes.
+__device__ __forceinline__ int w_place(int r, int q) { return r * 64 + ((q ^ ((r >> 2) & 3)) << 4); }
 
 // MT: tiles of 32 rows of X. FRAG: the weights come decoded, in the order of the fragments (k_lin_decode,
 // k_lin_transpose): coalesced and without the decoding, a step of a 256 x 256 tile takes 1.43 us instead of 1.70.
 template <int MT, bool XMX, bool FRAG, int EPI>
-__global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinArgs p) {
+__global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinArgs p) {
     constexpr int kTpr = MT >= 8 ? 2 : 1, kXHalf = 32 * MT * kStep;  // tiles per epilogue round; one X buffer
-    constexpr int kLds = 2 * kXHalf * 2 > kTpr * 32768 ? 2 * kXHalf * 2 : kTpr * 32768;
+    constexpr int kLdsX = 2 * kXHalf * 2, kLdsLoop = kLdsX + (FRAG ? 0 : 4 * (kWaveCodes + kWaveScales));
+    constexpr int kLds = kLdsLoop > kTpr * 32768 ? kLdsLoop : kTpr * 32768;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
     uint16_t *const xs = reinterpret_cast<uint16_t *>(lds);
     constexpr bool kGated = EPI == kEpiGated;
@@ -336,55 +348,71 @@ __global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinA
     const int64_t m0 = (int64_t)(4 * band + in % bm) * (32 * MT);
     const int64_t tn = in / bm;
     const int64_t kbeg = (int64_t)slice * p.kslice, kend = min(p.L, kbeg + p.kslice);
-    // The wave's weight rows: tile j starts at row w0[j] (uniform) and the lane's row is so many bytes of codes and
-    // of scales further; rows past the last read the last.
+    const int64_t kfull = kbeg + (kend - kbeg) / (2 * kStep) * (2 * kStep);  // the end of its whole pairs of steps
     const int64_t f0 = kGated ? tn * 128 + 32 * wave : tn * 256 + 64 * wave;
     const int64_t steps_all = (p.L + kStep - 1) / kStep, ktiles = (p.F + 31) / 32;  // FRAG; F = N unless gated
+    // The wave's weight rows: tile j starts at row w0[j] (uniform) and has `rows[j]` of them; rows past the last
+    // read the last.
     int64_t w0[2];
-    uint32_t woff[2], wsoff[2];
+    int rows[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
         const int64_t first = kGated ? min(p.F - 1, f0) : min(p.N - 1, f0 + 32 * j);
-        const int row = (int)min((int64_t)slot_row(r32), (kGated ? p.F : p.N) - 1 - first);
+        rows[j] = (int)min((int64_t)32, (kGated ? p.F : p.N) - first);
         w0[j] = first + (kGated && j ? p.F : 0);
-        woff[j] = (uint32_t)row * (uint32_t)(p.L / 2) + 16u * half;
-        wsoff[j] = (uint32_t)row * (uint32_t)(p.L / 16) + 2u * half;
     }
 
     using Weights = typename std::conditional<FRAG, WFrag, WCodes>::type;
     f32x16 acc[2][MT] = {};
-    // X is loaded two steps ahead of its use, one (with half the registers) where two work-groups share a CU.
-    constexpr int kSets = MT >= 8 ? 2 : 1;
+    // X is loaded one step ahead of its store, two where a step is short.
+    constexpr int kSets = MT >= 8 ? 1 : 2;
     XStage<MT, XMX> X[kSets];
     const XAddr<MT, XMX> xa(p, m0, tid);
     Weights W[2];
+    WStage S;
     bf16x8 A[2][2], B[2][MT];  // the fragments of one phase and of the next (A: decoded weights alone)
 
-    auto w_load = [&](auto whole, Weights &D, int64_t k0) __attribute__((always_inline)) {
+    // The stage's codes: load i takes rows 16 i + lane / 4 of the wave's 64, chunk lane % 4; its scales: row lane.
+    uint32_t soff[4], sscale = 0u;
+    uint8_t *const wl = lds + kLdsX + wave * (kWaveCodes + kWaveScales);
+    if constexpr (!FRAG) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            if constexpr (FRAG) {
+        for (int i = 0; i < 4; ++i) {
+            const int row = min(slot_row((16 * i + (lane >> 2)) & 31), rows[i >> 1] - 1);
+            soff[i] = (uint32_t)row * (uint32_t)(p.L / 2) + 16u * (lane & 3);
+        }
+        // relative to w0[0]: at most N L / 16 <= 2^31 bytes
+        sscale = (uint32_t)(((half ? w0[1] - w0[0] : 0) + min(slot_row(r32), (half ? rows[1] : rows[0]) - 1)) * (p.L / 16));
+    }
+    auto stage_load = [&](int64_t k0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) S.c[i] = load16(p.codes + (w0[i >> 1] * p.L + k0) / 2 + soff[i]);
+        S.s = load8b(p.scales + (w0[0] * p.L + k0) / 16 + sscale);
+    };
+    auto stage_store = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(wl + w_place(16 * i + (lane >> 2), lane & 3)) = S.c[i];
+        *reinterpret_cast<uint2 *>(wl + kWaveCodes + 8 * lane) = S.s;
+    };
+    // The lane's codes and scales of step `odd` of the stored pair. Only the wave itself writes and reads them, in
+    // order.
+    auto stage_read = [&](Weights &D, int odd) __attribute__((always_inline)) {
+        if constexpr (!FRAG)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                D.c[j] = *reinterpret_cast<const uint4 *>(wl + w_place(32 * j + r32, 2 * odd + half));
+                D.s[j] = *reinterpret_cast<const uint16_t *>(wl + kWaveCodes + 8 * (32 * j + r32) + 4 * odd + 2 * half);
+            }
+    };
+    auto frag_load = [&](Weights &D, int64_t k0) __attribute__((always_inline)) {
+        if constexpr (FRAG)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
                 const int64_t kt = kGated ? min(ktiles - 1, f0 / 32) + j * ktiles : min(ktiles - 1, f0 / 32 + j);
                 const uint8_t *q = reinterpret_cast<const uint8_t *>(p.wt) + ((kt * steps_all + k0 / kStep) * 4096);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) D.v[j][i] = load16(q + (uint32_t)(lane * 16) + i * 1024);
-            } else {
-                const uint8_t *c = p.codes + (w0[j] * p.L + k0) / 2, *s = p.scales + (w0[j] * p.L + k0) / 16;
-                const int64_t k = k0 + 32 * half;
-                if (whole.value || k + 32 <= kend) {
-                    D.c[j] = load16(c + woff[j]);
-                    D.s[j] = load2b(s + wsoff[j]);
-                } else {
-                    D.c[j] = make_uint4(0u, 0u, 0u, 0u);
-                    D.s[j] = 0u;
-                    if (k < kend) {  // the row's last 16
-                        const uint2 c2 = load8b(c + woff[j]);
-                        D.c[j].x = c2.x, D.c[j].y = c2.y;
-                        D.s[j] = s[wsoff[j]];
-                    }
-                }
             }
-        }
     };
     auto a_frag = [&](bf16x8 (&D)[2], const Weights &w, int i) __attribute__((always_inline)) {
 #pragma unroll
@@ -400,7 +428,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinA
         for (int t = 0; t < MT; ++t)
             D[t] = *reinterpret_cast<const bf16x8 *>(&xs[buf * kXHalf + x_place(32 * t + r32, 4 * half + i)]);
     };
-    auto products = [&](const Weights &w, int i) __attribute__((always_inline)) {
+    auto products = [&](const Weights &w, int i, int at) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < MT; ++t)
 #pragma unroll
@@ -409,29 +437,40 @@ __global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinA
                 if constexpr (FRAG)
                     a = __builtin_bit_cast(bf16x8, w.v[j][i]);
                 else
-                    a = A[i & 1][j];
-                acc[j][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, B[i & 1][t], acc[j][t], 0, 0, 0);
+                    a = A[at][j];
+                acc[j][t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, B[at][t], acc[j][t], 0, 0, 0);
             }
     };
-    // Step s from buffer s % 2, in four phases. At its start the fragments of phase 0 are formed, and X of the next
-    // kSets steps is in registers or on its way. Phase i forms the fragments of phase i + 1
-    // while the matrix cores work on its own. Coded weights are loaded two steps ahead, in phase 3, over those
-    // whose last use was in phase 2; decoded ones one step ahead, in phase 0. The one barrier stands before
-    // the last phase: by then every wave has stored X of step s + 1 (in phase 0) and has read all of buffer s % 2,
-    // so that phase 3 can read ahead from the other buffer and step s + 1 can store into this one.
+    // Step `odd` of a pair, from X buffer `odd`, in four phases. At its start the fragments of phase 0 are formed and
+    // X of the next kSets steps is in registers or on its way. Phase i forms the fragments of phase i + 1 while the
+    // matrix cores work on its own. X: stored in phase 0 for the next step, loaded in phase 1 for the one kSets later.
+    // Codes: a pair is stored in phase 0 of the odd step (every read of the pair before has been issued) and
+    // loaded in phase 1 for the pair after; the lane's own are read in phase 2 for the next step. Decoded weights
+    // are loaded in phase 0 for the next step. The one barrier stands before the last phase: by then every
+    // wave has stored X of the next step and has read all of this one's, so that phase 3 can read ahead from the other
+    // buffer and the next step can store into this one. What is loaded past the last whole pair is that pair again.
     // One wave per SIMD (MT = 8) hides nothing behind another wave, so the order inside a phase is asked for:
     // LDS reads (and weights decoded) between the first products, stores and loads between the rest.
-    auto step = [&](int buf, Weights &w, Weights &next, auto &&store, auto &&load_x, auto &&load_w)
-                    __attribute__((always_inline)) {
+    auto step = [&](auto parity, int64_t k0) __attribute__((always_inline)) {
+        constexpr int odd = decltype(parity)::value;
+        constexpr int kPairWork = !FRAG && odd ? 2 : 1;  // the odd step moves the codes too
+        Weights &w = W[odd], &next = W[odd ^ 1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i == 3) lds_barrier();
-            b_frag(B[(i + 1) & 1], i < 3 ? buf : buf ^ 1, (i + 1) & 3);
+            b_frag(B[(i + 1) & 1], i < 3 ? odd : odd ^ 1, (i + 1) & 3);
             a_frag(A[(i + 1) & 1], i < 3 ? w : next, (i + 1) & 3);
-            if (i == 0) store();
-            if (i == 1) load_x();
-            if (i == (FRAG ? 0 : 3)) load_w(FRAG ? next : w);
-            products(w, i);
+            if (i == 0) {
+                x_store<MT, XMX>(X[(odd ^ 1) & (kSets - 1)], xs + (odd ^ 1) * kXHalf, tid);
+                if (!FRAG && odd) stage_store();
+                frag_load(next, min(k0 + kStep, kfull - kStep));
+            }
+            if (i == 1) {
+                x_load<MT, XMX, true>(X[(odd ^ 1) & (kSets - 1)], xa, min(k0 + (1 + kSets) * kStep, kfull - kStep), kend, tid);
+                if (!FRAG && odd) stage_load(min(k0 + 3 * kStep, kfull - 2 * kStep));
+            }
+            if (i == 2) stage_read(next, odd ^ 1);
+            products(w, i, i & 1);
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
@@ -442,54 +481,68 @@ __global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinA
             for (int t = 0; t < MT; ++t) {
                 __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
                 if (i == 0 && XMX) __builtin_amdgcn_sched_group_barrier(kValu, 16, 0);
-                if (i == 0) __builtin_amdgcn_sched_group_barrier(kDsWrite, 1, 0);
-                if (i == 1 || i == (FRAG ? 0 : 3)) __builtin_amdgcn_sched_group_barrier(kVmemRead, 1, 0);
+                if (i == 0) __builtin_amdgcn_sched_group_barrier(kDsWrite, kPairWork, 0);
+                if (i == 2 && !FRAG) __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
+                if (i == 1 || (i == 0 && FRAG)) __builtin_amdgcn_sched_group_barrier(kVmemRead, kPairWork, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    constexpr int kAhead = FRAG ? 1 : 2;  // steps by which the weights are loaded ahead
 
-    constexpr std::true_type kWhole;
-    constexpr std::false_type kMasked;
-    x_load<MT, XMX, false>(X[0], xa, kbeg, kend, tid);
-    w_load(kMasked, W[0], kbeg);
-    if (kbeg + kStep < kend) {
-        if (kSets == 2) x_load<MT, XMX, false>(X[kSets - 1], xa, kbeg + kStep, kend, tid);
-        if (!FRAG) w_load(kMasked, W[1], kbeg + kStep);
-    }
-    x_store<MT, XMX>(X[0], xs, tid);
-    if (kbeg + kSets * kStep < kend) x_load<MT, XMX, false>(X[0], xa, kbeg + kSets * kStep, kend, tid);
-    lds_barrier();
-    b_frag(B[0], 0, 0);
-    a_frag(A[0], W[0], 0);
-    // Nothing in flight at the loop's entry: its waits then count the loads of its own turns alone.
-    __builtin_amdgcn_s_waitcnt(0);
-    // Two whole steps per turn without a branch, as long as everything they load lies inside the slice, W[s % 2]
-    // holding the weights of step s and X[s % kSets] its X or the next one's of its kind; the last steps with masks.
-    int64_t k0 = kbeg;
-    for (; k0 + (kSets + 3) * kStep <= kend; k0 += 2 * kStep) {
-#pragma unroll
-        for (int b2 = 0; b2 < 2; ++b2)
-            step(b2, W[b2], W[b2 ^ 1],
-                 [&]() __attribute__((always_inline)) { x_store<MT, XMX>(X[(b2 ^ 1) & (kSets - 1)], xs + (b2 ^ 1) * kXHalf, tid); },
-                 [&]() __attribute__((always_inline)) { x_load<MT, XMX, true>(X[(b2 ^ 1) & (kSets - 1)], xa, k0 + (b2 + 1 + kSets) * kStep, kend, tid); },
-                 [&](Weights &D) __attribute__((always_inline)) { w_load(kWhole, D, k0 + (b2 + kAhead) * kStep); });
-    }
+    if (kfull > kbeg) {
+        x_load<MT, XMX, true>(X[0], xa, kbeg, kend, tid);
+        if (!FRAG) stage_load(kbeg);
+        frag_load(W[0], kbeg);
+        x_store<MT, XMX>(X[0], xs, tid);
+        if (!FRAG) {
+            stage_store();
+            stage_load(min(kbeg + 2 * kStep, kfull - 2 * kStep));
+        }
+        x_load<MT, XMX, true>(X[kSets - 1], xa, kbeg + kStep, kend, tid);
+        if (kSets == 2) x_load<MT, XMX, true>(X[0], xa, min(kbeg + 2 * kStep, kfull - kStep), kend, tid);
+        lds_barrier();
+        b_frag(B[0], 0, 0);
+        stage_read(W[0], 0);
+        a_frag(A[0], W[0], 0);
+        // Nothing in flight at the loop's entry: its waits then count the loads of its own turns alone.
+        __builtin_amdgcn_s_waitcnt(0);
 #pragma unroll 1
-    for (int buf = 0; k0 < kend; k0 += kStep, buf ^= 1) {
-        Weights after = W[1];
-        step(buf, W[0], W[1],
-             [&]() __attribute__((always_inline)) { if (k0 + kStep < kend) x_store<MT, XMX>(X[kSets - 1], xs + (buf ^ 1) * kXHalf, tid); },
-             [&]() __attribute__((always_inline)) {
-                 if (kSets == 2) X[kSets - 1] = X[0];
-                 if (k0 + (1 + kSets) * kStep < kend) x_load<MT, XMX, false>(X[0], xa, k0 + (1 + kSets) * kStep, kend, tid);
-             },
-             [&](Weights &) __attribute__((always_inline)) { if (k0 + kAhead * kStep < kend) w_load(kMasked, FRAG ? W[1] : after, k0 + kAhead * kStep); });
-        W[0] = W[1];
-        if (!FRAG) W[1] = after;
+        for (int64_t k0 = kbeg; k0 < kfull; k0 += 2 * kStep) {
+            step(std::integral_constant<int, 0>{}, k0);
+            step(std::integral_constant<int, 1>{}, k0 + kStep);
+        }
+        lds_barrier();
     }
-    lds_barrier();  // the last phase has read ahead; what it read is not used
+    // The slice's last, fewer than 128 k, with masks and one step at a time.
+#pragma unroll 1
+    for (int64_t k0 = kfull; k0 < kend; k0 += kStep) {
+        x_load<MT, XMX, false>(X[0], xa, k0, kend, tid);
+        frag_load(W[0], k0);
+        if constexpr (!FRAG)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int64_t k = k0 + 32 * half, e = (w0[j] + min(slot_row(r32), rows[j] - 1)) * p.L + k;
+                W[0].c[j] = make_uint4(0u, 0u, 0u, 0u);
+                W[0].s[j] = 0u;
+                if (k + 32 <= kend) {
+                    W[0].c[j] = load16(p.codes + e / 2);
+                    W[0].s[j] = load2b(p.scales + e / 16);
+                } else if (k < kend) {  // the row's last 16
+                    const uint2 c2 = load8b(p.codes + e / 2);
+                    W[0].c[j].x = c2.x, W[0].c[j].y = c2.y;
+                    W[0].s[j] = p.scales[e / 16];
+                }
+            }
+        x_store<MT, XMX>(X[0], xs, tid);
+        lds_barrier();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            b_frag(B[0], 0, i);
+            a_frag(A[0], W[0], i);
+            products(W[0], i, 0);
+        }
+        lds_barrier();
+    }
 
     // The sums go through LDS, kTpr tiles of 32 rows by 256 weight rows at a time, so that the epilogue works on
     // whole rows: a thread takes eight consecutive output columns, a row's threads are consecutive. 16-byte
@@ -566,9 +619,9 @@ __global__ __launch_bounds__(kTileThreads, MT >= 8 ? 1 : 2) void k_lin_tile(LinA
                 for (int t = 0; t < kTpr; ++t) dump(t, acc[0][r * kTpr + t], acc[1][r * kTpr + t]);
         lds_barrier();
         if (p.F % 8 == 0)
-            rows_out(kWhole, round);
+            rows_out(std::true_type{}, round);
         else
-            rows_out(kMasked, round);
+            rows_out(std::false_type{}, round);
         lds_barrier();
     }
 }
@@ -901,22 +954,52 @@ __global__ __launch_bounds__(256) void k_lin_dz(LinGradArgs p, int64_t chunk, fl
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Tile height and K split of the tile kernel for an [M] x [F] output over a sum of length L.
-LinPlan plan_tile(int64_t M, int64_t L, int64_t F, int64_t N, bool gated) {
-    LinPlan p = {};
-    const int64_t tn = ceil_div(F, gated ? 128 : 256);
-    auto tiles = [&](int mt) { return ceil_div(M, 32 * mt) * tn; };
-    p.mt = tiles(8) >= 200 ? 8 : tiles(4) >= 256 ? 4 : M > 32 ? 2 : 1;
-    p.tiles_n = tn;
-    p.tiles_m = ceil_div(M, 32 * p.mt);
-    const int64_t steps = ceil_div(L, kStep), all = p.tiles_m * tn;
-    int64_t want = all >= 256 ? 1 : std::min<int64_t>(ceil_div(512, all), steps / 4);
-    while (want > 1 && want * M * N * (int64_t)sizeof(float) > ((int64_t)1 << 30)) --want;
-    want = std::max<int64_t>(want, 1);
-    p.kslice = ceil_div(steps, want) * kStep;
-    p.slices = ceil_div(L, p.kslice);
-    if (p.slices > 1) p.part_bytes = (size_t)(p.slices * M * N) * sizeof(float);
-    return p;
+// Tile height and K split of the tile kernel for an [M] x [F] output over a sum of length L: the least of the times
+// that these measurements add up to (us on an MI355X; weights coded, or decoded before: `frag`). A step of 64 k
+// costs, with one work-group per CU and with two (heights 1 and 2; the taller take a CU each):
+//   height (of 32 rows)   1            2            4      8
+//   coded                 0.60 / 0.97  0.71 / 1.26  1.00   1.55
+//   decoded               0.38 / 0.74  0.51 / 0.97  0.80   1.43
+// on top of 7, 9, 14 and 15 per work-group (launch, first loads, epilogue), and slices of K cost 4 and 8 bytes per
+// sum at 4 TB/s.
+LinPlan plan_tile(int64_t M, int64_t L, int64_t F, int64_t N, bool gated, bool frag) {
+    static constexpr int kHeights[4] = {1, 2, 4, 8};
+    static constexpr double kAlone[2][4] = {{0.60, 0.71, 1.00, 1.55}, {0.38, 0.51, 0.80, 1.43}};
+    static constexpr double kPaired[2][2] = {{0.97, 1.26}, {0.74, 0.97}};
+    static constexpr double kFixed[4] = {7.0, 9.0, 14.0, 15.0};
+    const int64_t tn = ceil_div(F, gated ? 128 : 256), pairs = ceil_div(L, 2 * kStep);
+    LinPlan best = {};
+    double least = 0.0;
+    for (int h = 0; h < 4; ++h) {
+        const int64_t tm = ceil_div(M, 32 * kHeights[h]);
+        for (int64_t want = 1; want <= 16 && want <= pairs; ++want) {
+            const int64_t per = ceil_div(pairs, want), slices = ceil_div(pairs, per);
+            if (slices != want) continue;
+            const double sums = (double)slices * (double)M * (double)N;
+            if (slices > 1 && sums * sizeof(float) > (double)((int64_t)1 << 30)) break;
+            const int64_t groups = tm * tn * slices;
+            const double steps = 2.0 * (double)per, alone = kFixed[h] + steps * kAlone[frag][h];
+            double t;
+            if (h < 2) {
+                const double paired = kFixed[h] + steps * kPaired[frag][h];
+                const int64_t rest = groups % 512;
+                t = (double)(groups / 512) * paired + (rest > 256 ? paired : rest > 0 ? alone : 0.0);
+            } else {
+                t = (double)ceil_div(groups, 256) * alone;
+            }
+            if (slices > 1) t += 4.0 + sums * 8.0 / 4.0e6;
+            if (best.mt == 0 || t < least) {
+                least = t;
+                best.mt = kHeights[h];
+                best.tiles_n = tn;
+                best.tiles_m = tm;
+                best.slices = slices;
+                best.kslice = per * 2 * kStep;
+                best.part_bytes = slices > 1 ? (size_t)(slices * M * N) * sizeof(float) : 0;
+            }
+        }
+    }
+    return best;
 }
 
 template <bool XMX, bool FRAG, int EPI>
@@ -978,7 +1061,7 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 GradPlan plan_grad(int64_t M, int64_t K, int64_t N, int64_t F, bool bias) {
     GradPlan g = {};
-    g.tile = plan_tile(M, N, K, K, false);
+    g.tile = plan_tile(M, N, K, K, false, true);
     g.wt_bytes = align256((size_t)(ceil_div(K, 32) * ceil_div(N, kStep)) * 4096);
     g.chunk = std::max<int64_t>(bias ? 16 : 4, ceil_div(M * ceil_div(F, 512), 2048));
     g.chunk = std::max(g.chunk, ceil_div(M, 65535));
@@ -999,7 +1082,7 @@ LinPlan plan_linear(int64_t M, int64_t K, int64_t N, bool gated, int keep) {
         p.slices = 1;
         return p;  // mt = 0: the skinny kernel
     }
-    LinPlan p = plan_tile(M, K, gated ? N / 2 : N, N, gated);
+    LinPlan p = plan_tile(M, K, gated ? N / 2 : N, N, gated, false);
     if (M >= kDecodeFirstRows && p.mt == 8 && p.slices == 1)
         p.wt_bytes = (size_t)(ceil_div(gated ? N / 2 : N, 32) * (gated ? 2 : 1) * ceil_div(K, kStep)) * 4096;
     return p;
