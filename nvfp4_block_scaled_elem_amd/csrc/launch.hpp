@@ -151,7 +151,7 @@ struct LinArgs {
     const void *x;
     const uint8_t *xs;  // scale bytes of an MXFP8 x
     const uint8_t *codes, *scales;
-    const uint16_t *wt;  // decoded weights in fragment order (the gradient), or null
+    const uint16_t *wt;  // an operand in fragment order (decoded weights, or X for the skinny kernel), or null
     const float *alpha;
     const void *bias, *res;
     void *y, *z;
@@ -173,10 +173,10 @@ struct LinPlan {
     int mt;  // tiles of 32 rows of X per work-group; 0: the skinny kernel
     int64_t tiles_m, tiles_n, slices, kslice;
     size_t part_bytes;  // fp32 sums of the K slices (0: K is not split)
-    size_t wt_bytes;    // decoded weights (0: decoded in the product); not both
+    size_t frag_bytes;  // an operand in fragment order: X for the skinny kernel, the weights for many rows; not both
 };
 LinPlan plan_linear(int64_t M, int64_t K, int64_t N, bool gated, int keep);
-// `ws` holds the plan's part_bytes or wt_bytes.
+// `ws` holds the plan's part_bytes or frag_bytes.
 hipError_t launch_linear(const LinArgs &p, void *ws, hipStream_t stream);
 size_t linear_grad_workspace(int64_t M, int64_t K, int64_t N, int64_t F, bool bias);
 hipError_t launch_linear_grad(const LinGradArgs &g, const uint8_t *codes, const uint8_t *scales, const float *alpha,

@@ -666,86 +666,149 @@ __global__ __launch_bounds__(kReduceThreads) void k_lin_reduce(LinArgs p, int sl
 // -------------------------------------------------------------------------------------- skinny kernel
 
 // Few rows of X (M <= 64), bound by reading the weights once: a work-group owns 16 output columns (gated: their
-// 16 gate rows and 16 up rows), its 16 waves split K in chunks of 128 and its sums are joined through LDS
-// in wave order. Products on v_mfma_f32_16x16x32_bf16, weights as A (lane l: row l % 16, 16 bytes of codes per
-// chunk at k = 32 (l / 16)), X^T as B straight from L2.
-constexpr int kSkinnyThreads = 1024, kSkinnyWaves = kSkinnyThreads / 64;
+// 16 gate rows and 16 up rows), its waves split K in chunks of 128 (wave w takes chunks w, w + WAVES, ...) and its
+// sums are joined through LDS in wave order. Products on v_mfma_f32_16x16x32_bf16, weights as A: lane l has row
+// l % 16 and, for product i = 0..3 of a chunk, k = 32 (l / 16) + 8 i .. + 7; X^T as B with the same map.
+// Neighbouring lanes of an operand are rows apart in memory, and a load of 64 scattered 16-byte pieces takes four
+// times the address cycles of a contiguous one (they, not the bytes, bound the kernel when both operands were
+// loaded so: 24 x 22016 x 4096 gated in 35 us). So a wave reads its chunk of codes in whole 64-byte pieces and
+// turns it in LDS, and X comes in fragment order, written by k_lin_xfrag, or, up to kDirectRows rows, straight
+// from memory: so few lanes cost little, and a launch is saved.
+constexpr int kSkinnyMaxM = 64, kDirectRows = 8;
+constexpr int kChunk = 128, kChunkLds = 16 * 64 + 16 * 8;  // k per chunk; LDS bytes of a tile's codes and scales
 
-template <int MT, int NT, bool XMX>
-__global__ __launch_bounds__(kSkinnyThreads) void k_lin_skinny(LinArgs p) {
-    __shared__ float red[kSkinnyWaves][MT][256];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, r16 = lane & 15, g = lane >> 4;
+// X in the order in which k_lin_skinny's lanes read it: per chunk and tile of 16 rows 4 KB, [i][lane][8]. Rows past M
+// and k past K are zeros. A work-group writes one chunk of one tile.
+template <bool XMX>
+__global__ __launch_bounds__(256) void k_lin_xfrag(LinArgs p, uint16_t *__restrict__ out) {
+    const int lane = threadIdx.x & 63, i = threadIdx.x >> 6;
+    const int64_t m = 16 * (int64_t)blockIdx.y + (lane & 15), k = kChunk * (int64_t)blockIdx.x + 32 * (lane >> 4) + 8 * i;
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (m < p.M && k < p.L) {  // K % 16 == 0: the eight are in or out
+        if (XMX) {
+            RawMx8 r;
+            r.load(static_cast<const uint8_t *>(p.x) + m * p.ldx + k, p.xs + m * ((p.L + kMxBlock - 1) / kMxBlock) + k / kMxBlock, 8);
+            float f[8];
+            r.get(f);
+            v = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+        } else {
+            v = load16(static_cast<const uint16_t *>(p.x) + m * p.ldx + k);
+        }
+    }
+    reinterpret_cast<uint4 *>(out)[((int64_t)blockIdx.x * gridDim.y + blockIdx.y) * 256 + threadIdx.x] = v;
+}
+
+// MT: tiles of 16 rows of X; NT: 2 if gated. XF: X in fragment order (p.wt's place in LinArgs holds it), else direct,
+// MT = 1.
+template <int MT, int NT, bool XF, bool XMX, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void k_lin_skinny(LinArgs p) {
+    // each wave's chunk of codes and scales; afterwards each wave's sums
+    constexpr int kStage = WAVES * NT * kChunkLds, kSums = WAVES * MT * 1024;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kStage > kSums ? kStage : kSums];
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t f0 = (int64_t)blockIdx.x * 16;
-    const int64_t K = p.L, nch = (K + 127) / 128, nb = (K + kMxBlock - 1) / kMxBlock;
-    int64_t wrow[NT];
-    wrow[0] = min(p.F - 1, f0 + r16);
-    if (NT == 2) wrow[NT - 1] = p.F + wrow[0];
+    const int64_t K = p.L, nch = (K + kChunk - 1) / kChunk, nb = (K + kMxBlock - 1) / kMxBlock;
+    uint8_t *const wl = lds + wave * NT * kChunkLds;
+    // codes: the lane loads row lane / 4, 16 bytes lane % 4; scales: row lane % 16, its 8 bytes
+    const int64_t crow = min(p.F - 1, f0 + (lane >> 2)), srow = min(p.F - 1, f0 + r16);
     f32x4 acc[NT][MT] = {};
-    uint4 cv[NT];
-    uint32_t sv[NT];
-    auto load_w = [&](int64_t c) {
-        const int64_t k = 128 * c + 32 * g;
+    uint4 cv[2][NT];
+    uint2 sv[2][NT];
+    const uint8_t *pc[NT], *ps[NT];  // of the wave's first chunk
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+        pc[j] = p.codes + ((crow + j * p.F) * K + kChunk * wave + 32 * (lane & 3)) / 2;
+        ps[j] = p.scales + ((srow + j * p.F) * K + kChunk * wave) / 16;
+    }
+    auto load_w = [&](uint4 (&c)[NT], uint2 (&s)[NT], int64_t ch) __attribute__((always_inline)) {
+        const int64_t by = (ch - wave) * (kChunk / 16);  // uniform
+        if ((ch + 1) * kChunk <= K) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                c[j] = load16(pc[j] + 8 * by);
+                if (lane < 16) s[j] = load8b(ps[j] + by);
+            }
+            return;
+        }
+        const int64_t kc = kChunk * ch + 32 * (lane & 3), ks = kChunk * ch;
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const uint8_t *q = p.codes + (wrow[j] * K + k) / 2, *s = p.scales + (wrow[j] * K + k) / 16;
-            cv[j] = make_uint4(0u, 0u, 0u, 0u);
-            sv[j] = 0u;
-            if (k + 32 <= K) {
-                cv[j] = load16(q);
-                sv[j] = load2b(s);
-            } else if (k < K) {  // the row's last 16
-                const uint2 c2 = load8b(q);
-                cv[j].x = c2.x, cv[j].y = c2.y;
-                sv[j] = *s;
+            c[j] = make_uint4(0u, 0u, 0u, 0u);
+            s[j] = make_uint2(0u, 0u);
+            if (kc + 32 <= K) {
+                c[j] = load16(pc[j] + 8 * by);
+            } else if (kc < K) {  // the row's last 16
+                const uint2 d = load8b(pc[j] + 8 * by);
+                c[j].x = d.x, c[j].y = d.y;
             }
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (ks + 16 * e < K) (e < 4 ? s[j].x : s[j].y) |= (uint32_t)ps[j][by + e] << (8 * (e & 3));
         }
     };
-    int64_t c = wave;
-    if (c < nch) load_w(c);
-    for (; c < nch; c += kSkinnyWaves) {
-        uint4 cur[NT];
-        uint32_t scur[NT];
-#pragma unroll
-        for (int j = 0; j < NT; ++j) cur[j] = cv[j], scur[j] = sv[j];
-        if (c + kSkinnyWaves < nch) load_w(c + kSkinnyWaves);
-        const int64_t k = 128 * c + 32 * g;
+    auto chunk = [&](const uint4 (&c)[NT], const uint2 (&s)[NT], int64_t ch) __attribute__((always_inline)) {
+        const int64_t k = kChunk * ch + 32 * g;
         uint4 xv[MT][4];
+        if constexpr (XF) {
+            const uint4 *q = reinterpret_cast<const uint4 *>(p.wt) + ch * MT * 256 + lane;
 #pragma unroll
-        for (int t = 0; t < MT; ++t) {
-            const int64_t m = 16 * t + r16;
-            const bool row = m < p.M;
-            if (XMX) {
-                const uint8_t *q = static_cast<const uint8_t *>(p.x) + m * p.ldx + k;
-                uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
-                float s = 0.0f;
-                if (row && k < K) {
-                    a = load16(q);
-                    s = mx_scale_value(p.xs[m * nb + k / kMxBlock]);
-                    if (k + 32 <= K) b = load16(q + 16);
-                }
-                const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+            for (int t = 0; t < MT; ++t)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float f[8];
-                    mx_decode4(w[2 * i], s, f);
-                    mx_decode4(w[2 * i + 1], s, f + 4);
-                    auto pair = [](float lo, float hi) { return __builtin_amdgcn_perm(__float_as_uint(hi), __float_as_uint(lo), 0x07060302u); };
-                    xv[t][i] = make_uint4(pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7]));
-                }
-            } else {
-                const uint16_t *q = static_cast<const uint16_t *>(p.x) + m * p.ldx + k;
+                for (int i = 0; i < 4; ++i) xv[t][i] = q[t * 256 + i * 64];
+        } else {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    xv[t][i] = make_uint4(0u, 0u, 0u, 0u);
-                    if (row && k + 8 * i < K) xv[t][i] = load16(q + 8 * i);
+            for (int i = 0; i < 4; ++i) xv[0][i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r16 < p.M) {
+                if constexpr (XMX) {
+                    const uint8_t *q = static_cast<const uint8_t *>(p.x) + r16 * p.ldx + k;
+                    uint4 a = make_uint4(0u, 0u, 0u, 0u), b = a;
+                    float sc = 0.0f;
+                    if ((ch + 1) * kChunk <= K) {
+                        a = load16(q);
+                        b = load16(q + 16);
+                        sc = mx_scale_value(p.xs[r16 * nb + k / kMxBlock]);
+                    } else if (k < K) {
+                        a = load16(q);
+                        sc = mx_scale_value(p.xs[r16 * nb + k / kMxBlock]);
+                        if (k + 32 <= K) b = load16(q + 16);
+                    }
+                    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        float f[8];
+                        mx_decode4(w[2 * i], sc, f);
+                        mx_decode4(w[2 * i + 1], sc, f + 4);
+                        xv[0][i] = make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]), pack_bf16(f[6], f[7]));
+                    }
+                } else {
+                    const uint16_t *q = static_cast<const uint16_t *>(p.x) + r16 * p.ldx + k;
+                    if ((ch + 1) * kChunk <= K) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) xv[0][i] = load16(q + 8 * i);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (k + 8 * i < K) xv[0][i] = load16(q + 8 * i);
+                    }
                 }
             }
         }
+        // Only the wave itself writes and reads its part of LDS, in order. A row's 64 bytes are four pieces, piece q at
+        // q ^ (row / 4 % 4).
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
-            const float d0 = e4m3_value(scur[j] & 0x7Fu), d1 = e4m3_value((scur[j] >> 8) & 0x7Fu);
-            const uint4 w[4] = {dequant8(cur[j].x, d0), dequant8(cur[j].y, d0), dequant8(cur[j].z, d1),
-                                dequant8(cur[j].w, d1)};
+            uint8_t *const q = wl + j * kChunkLds;
+            *reinterpret_cast<uint4 *>(q + w_place(lane >> 2, lane & 3)) = c[j];
+            if (lane < 16) *reinterpret_cast<uint2 *>(q + 1024 + 8 * lane) = s[j];
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const uint8_t *const q = wl + j * kChunkLds;
+            const uint4 cur = *reinterpret_cast<const uint4 *>(q + w_place(r16, g));
+            const uint32_t sb = *reinterpret_cast<const uint16_t *>(q + 1024 + 8 * r16 + 2 * g);
+            const float d0 = e4m3_value(sb & 0x7Fu), d1 = e4m3_value((sb >> 8) & 0x7Fu);
+            const uint4 w[4] = {dequant8(cur.x, d0), dequant8(cur.y, d0), dequant8(cur.z, d1), dequant8(cur.w, d1)};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -753,46 +816,67 @@ __global__ __launch_bounds__(kSkinnyThreads) void k_lin_skinny(LinArgs p) {
                     acc[j][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[i]),
                                                                         __builtin_bit_cast(bf16x8, xv[t][i]), acc[j][t], 0, 0, 0);
         }
+    };
+    // two chunks' weights in flight
+    int64_t c = wave;
+    if (c < nch) load_w(cv[0], sv[0], c);
+    if (c + WAVES < nch) load_w(cv[1], sv[1], c + WAVES);
+#pragma unroll 1
+    for (; c < nch; c += 2 * WAVES) {
+        chunk(cv[0], sv[0], c);
+        if (c + 2 * WAVES < nch) load_w(cv[0], sv[0], c + 2 * WAVES);
+        if (c + WAVES >= nch) break;
+        chunk(cv[1], sv[1], c + WAVES);
+        if (c + 3 * WAVES < nch) load_w(cv[1], sv[1], c + 3 * WAVES);
     }
-    // Element r of lane l is weight row 4 (l / 16) + r of the tile, row 16 t + l % 16 of X. Thread tid sums output
-    // o = tid, MT * 256 of them (at most 1024).
-    float z[NT] = {};
+    __syncthreads();  // the sums take the place of the codes
+    float (*const red)[MT][256] = reinterpret_cast<float (*)[MT][256]>(lds);
+    // Element r of lane l is weight row 4 (l / 16) + r of the tile, row 16 t + l % 16 of X. A thread sums the outputs
+    // o = tid, tid + 64 WAVES, ... of MT * 256.
+    constexpr int kMine = (MT * 256 + 64 * WAVES - 1) / (64 * WAVES);
+    float z[NT][kMine] = {};
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
         if (j) __syncthreads();
 #pragma unroll
         for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int r = 0; r < 4; ++r) red[wave][t][lane * 4 + r] = acc[j][t][r];
+            *reinterpret_cast<f32x4 *>(&red[wave][t][lane * 4]) = acc[j][t];
         __syncthreads();
-        if (tid < MT * 256)
 #pragma unroll
-            for (int w = 0; w < kSkinnyWaves; ++w) z[j] += red[w][tid >> 8][tid & 255];
+        for (int q = 0; q < kMine; ++q) {
+            const int o = tid + 64 * WAVES * q;
+            if (o < MT * 256)
+#pragma unroll
+                for (int w = 0; w < WAVES; ++w) z[j][q] += red[w][o >> 8][o & 255];
+        }
     }
-    const int l = (tid >> 2) & 63;
-    const int64_t f = f0 + 4 * (l >> 4) + (tid & 3), m = 16 * (tid >> 8) + (l & 15);
-    if (tid >= MT * 256 || f >= p.F || m >= p.M) return;
     const float alpha = *p.alpha;
     auto scalar = [](const void *b, int f32, int64_t e) {
         return f32 ? static_cast<const float *>(b)[e] : __uint_as_float((uint32_t)static_cast<const uint16_t *>(b)[e] << 16);
     };
-    float a = alpha * z[0], u = NT == 2 ? alpha * z[NT - 1] : 0.0f;
-    if (p.bias) {
-        a += scalar(p.bias, p.bias_f32, f);
-        if (NT == 2) u += scalar(p.bias, p.bias_f32, p.F + f);
+#pragma unroll
+    for (int q = 0; q < kMine; ++q) {
+        const int o = tid + 64 * WAVES * q, l = (o >> 2) & 63;
+        const int64_t f = f0 + 4 * (l >> 4) + (o & 3), m = 16 * (o >> 8) + (l & 15);
+        if (o >= MT * 256 || f >= p.F || m >= p.M) continue;
+        float a = alpha * z[0][q], u = NT == 2 ? alpha * z[NT - 1][q] : 0.0f;
+        if (p.bias) {
+            a += scalar(p.bias, p.bias_f32, f);
+            if (NT == 2) u += scalar(p.bias, p.bias_f32, p.F + f);
+        }
+        if (p.keep == kKeepBf16) {
+            uint16_t *e = static_cast<uint16_t *>(p.z) + m * p.N + f;
+            e[0] = to_bf16(a);
+            if (NT == 2) e[p.F] = to_bf16(u);
+        }
+        a = act_value(a, p.act);
+        if (NT == 2) a *= u;
+        if (p.res) a += scalar(p.res, p.res_f32, m * p.ldr + f);
+        if (p.y_f32)
+            static_cast<float *>(p.y)[m * p.F + f] = a;
+        else
+            static_cast<uint16_t *>(p.y)[m * p.F + f] = to_bf16(a);
     }
-    if (p.keep == kKeepBf16) {
-        uint16_t *q = static_cast<uint16_t *>(p.z) + m * p.N + f;
-        q[0] = to_bf16(a);
-        if (NT == 2) q[p.F] = to_bf16(u);
-    }
-    a = act_value(a, p.act);
-    if (NT == 2) a *= u;
-    if (p.res) a += scalar(p.res, p.res_f32, m * p.ldr + f);
-    if (p.y_f32)
-        static_cast<float *>(p.y)[m * p.F + f] = a;
-    else
-        static_cast<uint16_t *>(p.y)[m * p.F + f] = to_bf16(a);
 }
 
 // ------------------------------------------------------------------------------------------ gradient
@@ -1040,16 +1124,46 @@ hipError_t tile_launch(LinArgs p, const LinPlan &plan, hipStream_t st) {
     return tile_launch_as<XMX, FRAG, kEpiPlain>(p, plan, st);
 }
 
-template <int NT, bool XMX>
-hipError_t skinny_launch(const LinArgs &p, hipStream_t st) {
-    const dim3 grid((unsigned)ceil_div(p.F, 16)), block(kSkinnyThreads);
-    switch ((p.M + 15) / 16) {
-        case 1: hipLaunchKernelGGL((k_lin_skinny<1, NT, XMX>), grid, block, 0, st, p); break;
-        case 2: hipLaunchKernelGGL((k_lin_skinny<2, NT, XMX>), grid, block, 0, st, p); break;
-        case 3: hipLaunchKernelGGL((k_lin_skinny<3, NT, XMX>), grid, block, 0, st, p); break;
-        default: hipLaunchKernelGGL((k_lin_skinny<4, NT, XMX>), grid, block, 0, st, p); break;
+template <int NT, int WAVES>
+hipError_t skinny_launch_as(LinArgs p, void *ws, hipStream_t st) {
+    const dim3 grid((unsigned)ceil_div(p.F, 16)), block(64 * WAVES);
+    if (p.M <= kDirectRows) {
+        if (p.x_mx)
+            hipLaunchKernelGGL((k_lin_skinny<1, NT, false, true, WAVES>), grid, block, 0, st, p);
+        else
+            hipLaunchKernelGGL((k_lin_skinny<1, NT, false, false, WAVES>), grid, block, 0, st, p);
+        return hipGetLastError();
+    }
+    const int64_t mt = ceil_div(p.M, 16);
+    const dim3 xgrid((unsigned)ceil_div(p.L, kChunk), (unsigned)mt);
+    if (p.x_mx)
+        hipLaunchKernelGGL(k_lin_xfrag<true>, xgrid, dim3(256), 0, st, p, static_cast<uint16_t *>(ws));
+    else
+        hipLaunchKernelGGL(k_lin_xfrag<false>, xgrid, dim3(256), 0, st, p, static_cast<uint16_t *>(ws));
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    p.wt = static_cast<const uint16_t *>(ws);
+    if (mt == 1)
+        hipLaunchKernelGGL((k_lin_skinny<1, NT, true, false, WAVES>), grid, block, 0, st, p);
+    else if (mt == 2)
+        hipLaunchKernelGGL((k_lin_skinny<2, NT, true, false, WAVES>), grid, block, 0, st, p);
+    else if constexpr (NT == 1 || WAVES == 8) {  // skinny_launch gives six tiles and more to 8 waves
+        if (mt == 3)
+            hipLaunchKernelGGL((k_lin_skinny<3, NT, true, false, WAVES>), grid, block, 0, st, p);
+        else
+            hipLaunchKernelGGL((k_lin_skinny<4, NT, true, false, WAVES>), grid, block, 0, st, p);
     }
     return hipGetLastError();
+}
+
+// Waves per work-group: 16 while the work-groups are few (one or two a CU), so that enough loads are in flight; 8
+// where there are more, which spend less on joining their sums (M = 1: 4096 x 4096 5.0 us with 16, 5.3 with 8;
+// 22016 x 4096 gated 19.5 and 14.9), and where the accumulators of six or more tiles would not fit the
+// registers of 16 (M = 64, 22016 x 4096 gated: 71 and 31 us).
+template <int NT>
+hipError_t skinny_launch(const LinArgs &p, void *ws, hipStream_t st) {
+    return ceil_div(p.F, 16) > 512 || NT * ceil_div(p.M, 16) >= 6 ? skinny_launch_as<NT, 8>(p, ws, st)
+                                                                 : skinny_launch_as<NT, 16>(p, ws, st);
 }
 
 struct GradPlan {
@@ -1077,14 +1191,15 @@ GradPlan plan_grad(int64_t M, int64_t K, int64_t N, int64_t F, bool bias) {
 constexpr int64_t kDecodeFirstRows = 2560;
 
 LinPlan plan_linear(int64_t M, int64_t K, int64_t N, bool gated, int keep) {
-    if (M <= 64 && keep != kKeepMx) {
+    if (M <= kSkinnyMaxM && keep != kKeepMx) {  // mt = 0: the skinny kernel
         LinPlan p = {};
         p.slices = 1;
-        return p;  // mt = 0: the skinny kernel
+        if (M > kDirectRows) p.frag_bytes = (size_t)(ceil_div(K, kChunk) * ceil_div(M, 16)) * 4096;
+        return p;
     }
     LinPlan p = plan_tile(M, K, gated ? N / 2 : N, N, gated, false);
     if (M >= kDecodeFirstRows && p.mt == 8 && p.slices == 1)
-        p.wt_bytes = (size_t)(ceil_div(gated ? N / 2 : N, 32) * (gated ? 2 : 1) * ceil_div(K, kStep)) * 4096;
+        p.frag_bytes = (size_t)(ceil_div(gated ? N / 2 : N, 32) * (gated ? 2 : 1) * ceil_div(K, kStep)) * 4096;
     return p;
 }
 
@@ -1092,10 +1207,9 @@ hipError_t launch_linear(const LinArgs &args, void *ws, hipStream_t stream) {
     const LinPlan plan = plan_linear(args.M, args.L, args.N, args.gated, args.keep);
     LinArgs p = args;
     if (plan.mt == 0) {
-        if (p.gated) return p.x_mx ? skinny_launch<2, true>(p, stream) : skinny_launch<2, false>(p, stream);
-        return p.x_mx ? skinny_launch<1, true>(p, stream) : skinny_launch<1, false>(p, stream);
+        return p.gated ? skinny_launch<2>(p, ws, stream) : skinny_launch<1>(p, ws, stream);
     }
-    if (plan.wt_bytes) {
+    if (plan.frag_bytes) {
         p.wt = static_cast<uint16_t *>(ws);
         const dim3 grid((unsigned)ceil_div(ceil_div(p.F, 32), 4), (unsigned)ceil_div(ceil_div(p.L, kStep), 4), p.gated ? 2 : 1);
         hipLaunchKernelGGL(k_lin_decode, grid, dim3(256), 0, stream, p.codes, p.scales, p.F, p.L, static_cast<uint16_t *>(ws));
