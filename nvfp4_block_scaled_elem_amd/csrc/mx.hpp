@@ -47,6 +47,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
 
 // ------------------------------------------------------------------------- eight values of a row
 
+// A value the compiler has to take as new: what was computed from it before is computed again from it after, and
+// not kept in registers meanwhile.
+__device__ __forceinline__ void renew(uint32_t &v) { asm volatile("" : "+v"(v)); }
+__device__ __forceinline__ void renew(uint4 &v) { renew(v.x), renew(v.y), renew(v.z), renew(v.w); }
+
 // Eight consecutive values as they lie in memory: bf16 (one 16-byte load) or fp32 (two).
 template <typename T>
 struct Raw8;
@@ -70,6 +75,7 @@ struct Raw8<uint16_t> {
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[2 * i] = bf16_lo(d[i]), v[2 * i + 1] = bf16_hi(d[i]);
     }
+    __device__ __forceinline__ void again() { renew(a); }
 };
 template <>
 struct Raw8<float> {
@@ -92,6 +98,7 @@ struct Raw8<float> {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(d[i]);
     }
+    __device__ __forceinline__ void again() {}  // the values are what lies in memory
 };
 
 // The first n (0..8) of eight values, rounded once to the memory's type.
@@ -206,6 +213,7 @@ struct RawMx8 {
         mx_decode4(c.x, s, v);
         mx_decode4(c.y, s, v + 4);
     }
+    __device__ __forceinline__ void again() { renew(c.x), renew(c.y), renew(sb); }
 };
 
 }  // namespace nvfp4

@@ -234,7 +234,9 @@ __global__ __launch_bounds__(ROWT < 256 ? 256 : ROWT) void k_rms_norm_grad(NormA
             if (p.r) dv[v].load(static_cast<const T *>(p.r) + row * p.ldr + e, n);
         }
     };
-    fetch(group);
+    // the next row in flight, unless its registers are needed (fp32 rows of 16 KB and more)
+    constexpr bool kAhead = !(ROWT == 1024 && sizeof(T) == 4);
+    if (kAhead) fetch(group);
     float w[VPT][8], dw[VPT][8];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
@@ -245,31 +247,42 @@ __global__ __launch_bounds__(ROWT < 256 ? 256 : ROWT) void k_rms_norm_grad(NormA
     }
     int turn = 0;
     for (int64_t row = group; row < p.rows; row += groups, turn ^= 1) {
-        float h[VPT][8], g[VPT][8], d[VPT][8], ss = 0.0f, gh = 0.0f;
+        if (!kAhead) fetch(row);
+        RawH8<T, MX> h0[VPT];
+        Raw8<T> g0[VPT], d0[VPT];
+        float ss = 0.0f, gh = 0.0f;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            hv[v].get(h[v]);
-            gv[v].get(g[v]);
-            if (p.r) dv[v].get(d[v]);
+            h0[v] = hv[v], g0[v] = gv[v], d0[v] = dv[v];
+            float h[8], g[8];
+            h0[v].get(h);
+            g0[v].get(g);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                ss = __builtin_fmaf(h[v][i], h[v][i], ss);
-                gh = __builtin_fmaf(g[v][i] * w[v][i], h[v][i], gh);
+                ss = __builtin_fmaf(h[i], h[i], ss);
+                gh = __builtin_fmaf(g[i] * w[v][i], h[i], gh);
             }
         }
-        if (row + groups < p.rows) fetch(row + groups);
+        if (kAhead && row + groups < p.rows) fetch(row + groups);
         const float2 s = group_sum2<ROWT>(ss, gh, slot[turn], tid);
         const float q = rms_rcp(s.x, p.cols, p.eps);
         const float c = q * q * (s.y / (float)p.cols);
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             const int64_t e = 8 * (int64_t)(v * ROWT + tid);
-            float o[8];
+            float h[8], g[8], d[8], o[8];
+            if (ROWT == 1024) {  // 128 registers a thread: the row stays in its memory form over the reduction
+                h0[v].again();
+                g0[v].again();
+            }
+            h0[v].get(h);
+            g0[v].get(g);
+            if (p.r) d0[v].get(d);
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                o[i] = q * __builtin_fmaf(-h[v][i], c, g[v][i] * w[v][i]);
-                if (p.r) o[i] += d[v][i];
-                dw[v][i] = __builtin_fmaf(g[v][i], h[v][i] * q, dw[v][i]);
+                o[i] = q * __builtin_fmaf(-h[i], c, g[i] * w[v][i]);
+                if (p.r) o[i] += d[i];
+                dw[v][i] = __builtin_fmaf(g[i], h[i] * q, dw[v][i]);
             }
             put8(static_cast<T *>(p.y) + row * p.cols + e, o, valid8(p.cols, e));
         }
@@ -352,21 +365,27 @@ __global__ __launch_bounds__(256) void k_rms_norm_dw_long(NormArgs p, const floa
     put8(part + (int64_t)blockIdx.y * p.cols + e, dw, n);
 }
 
-// out[c] = sum over `rows` rows of part[.][c], in a fixed order: a work-group takes 64 columns, its four
-// waves every fourth row each, and their sums are added in wave order. No rows: zeros.
-__global__ __launch_bounds__(256) void k_column_sum(const float *__restrict__ part, int64_t rows, int64_t cols,
+// out[c] = sum over `rows` rows of part[.][c], in a fixed order: a work-group takes 32 columns, its 32 half-waves
+// every 32nd row each, and their sums are added in that order (1024 x 4096: 3.5 us; with 64 columns and four
+// waves, 64 work-groups, 11 us). No rows: zeros.
+__global__ __launch_bounds__(1024) void k_column_sum(const float *__restrict__ part, int64_t rows, int64_t cols,
                                                     float *__restrict__ out) {
-    __shared__ float s[4][64];
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + lane;
+    __shared__ float s[32][32];
+    const int lane = threadIdx.x & 31, h = threadIdx.x >> 5;
+    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float a = 0.0f;
     if (c < cols) {
 #pragma unroll 8
-        for (int64_t r = wave; r < rows; r += 4) a += part[r * cols + c];
+        for (int64_t r = h; r < rows; r += 32) a += part[r * cols + c];
     }
-    s[wave][lane] = a;
+    s[h][lane] = a;
     __syncthreads();
-    if (wave == 0 && c < cols) out[c] = ((s[0][lane] + s[1][lane]) + s[2][lane]) + s[3][lane];
+    if (h == 0 && c < cols) {
+        float t = s[0][lane];
+#pragma unroll
+        for (int i = 1; i < 32; ++i) t += s[i][lane];
+        out[c] = t;
+    }
 }
 
 // --------------------------------------------------------------------------------------------- codec
@@ -422,19 +441,21 @@ NormConfig norm_config(int64_t rows, int64_t cols) {
 NormConfig norm_grad_config(int64_t cols) {
     const int64_t v = (cols + 7) / 8;
     if (v <= 64) return {64, 1};
+    if (v <= 128) return {64, 2};
     if (v <= 256) return {256, 1};
     if (v <= 512) return {256, 2};
     if (v <= 1024) return {512, 2};
     return v <= 2048 ? NormConfig{1024, 2} : NormConfig{0, 0};
 }
 
-constexpr int64_t kGradThreads = 2048 * 256;  // threads the gradient's groups fill: eight waves per SIMD
 constexpr int64_t kLongChunk = 64;            // rows per partial sum of k_rms_norm_dw_long
 
 int64_t norm_grad_groups(int64_t rows, int64_t cols) {
     const NormConfig c = norm_grad_config(cols);
     if (c.vpt == 0) return (rows + kLongChunk - 1) / kLongChunk;
-    return std::min(rows, std::max<int64_t>(1, kGradThreads / 2 / c.rowt));
+    // As many groups as keep the card's loads in flight; each writes a row of partial sums, so no more (8192 x 4096: 512
+    // groups 39 us, 1024 43; 20000 x 1000, a wave each: 2048 groups 31 us, 1024 38, 4096 39).
+    return std::min<int64_t>(rows, c.rowt == 64 ? 4096 / c.vpt : c.rowt == 256 ? 1024 / c.vpt : 256);
 }
 
 template <typename T>
@@ -471,6 +492,7 @@ hipError_t norm_grad_dispatch(const NormArgs &p, float *dw, float *ws, hipStream
         done = true;                                                                                           \
     }
     NVFP4_NORM_GRAD(64, 1)
+    NVFP4_NORM_GRAD(64, 2)
     NVFP4_NORM_GRAD(256, 1)
     NVFP4_NORM_GRAD(256, 2)
     NVFP4_NORM_GRAD(512, 2)
@@ -489,7 +511,7 @@ hipError_t norm_grad_dispatch(const NormArgs &p, float *dw, float *ws, hipStream
 }  // namespace
 
 hipError_t launch_column_sum(const float *part, int64_t rows, int64_t cols, float *out, hipStream_t stream) {
-    hipLaunchKernelGGL(k_column_sum, dim3((unsigned)((cols + 63) / 64)), dim3(256), 0, stream, part, rows, cols, out);
+    hipLaunchKernelGGL(k_column_sum, dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, stream, part, rows, cols, out);
     return hipGetLastError();
 }
 
