@@ -382,9 +382,9 @@ typedef struct nvfp4_linear_args {
 int nvfp4_linear(const nvfp4_linear_args_t *args);
 
 /* Scratch of one nvfp4_linear call (x rearranged for 9 to 64 rows; fp32 sums where K is split over work-groups;
- * the decoded weights for many rows; 0 for up to 8 rows). z_dtype: the form
+ * an MXFP8 x decoded beyond; the decoded weights for many rows; 0 for up to 8 rows unless z is MXFP8). z_dtype: the form
  * in which z is kept, NVFP4_DTYPE_BF16 also where it is not. */
-size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int gated, int z_dtype);
+size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int x_dtype, int gated, int z_dtype);
 
 /* Gradient of nvfp4_linear, given dy (bf16, as y) at y; the residual's gradient is dy itself, the weights are
  * frozen:

@@ -102,9 +102,10 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_linear.restype = i32
         L.nvfp4_linear_grad.argtypes = [vp]
         L.nvfp4_linear_grad.restype = i32
-        for name in ("nvfp4_linear_workspace_bytes", "nvfp4_linear_grad_workspace_bytes"):
-            getattr(L, name).argtypes = [i64, i64, i64, i32, i32]
-            getattr(L, name).restype = sz
+        L.nvfp4_linear_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i32]
+        L.nvfp4_linear_workspace_bytes.restype = sz
+        L.nvfp4_linear_grad_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+        L.nvfp4_linear_grad_workspace_bytes.restype = sz
         L.nvfp4_status_string.argtypes = [i32]
         L.nvfp4_status_string.restype = ctypes.c_char_p
         _lib = L

@@ -5,7 +5,7 @@
 //   nvfp4_rms_norm_grad   : k_rms_norm_grad -> k_column_sum (beyond 16384 columns: k_rms_norm_grad_long ->
 //                           k_rms_norm_dw_long -> k_column_sum)
 //   nvfp4_mxfp8_quantize / nvfp4_mxfp8_dequantize : one kernel each
-//   nvfp4_linear          : (k_lin_xfrag ->) k_lin_skinny, or (k_lin_decode ->) k_lin_tile (-> k_lin_reduce where K is split)
+//   nvfp4_linear          : (k_lin_xfrag ->) k_lin_skinny, or (k_mx_dequantize ->) (k_lin_decode ->) k_lin_tile (-> k_lin_reduce where K is split)
 //   nvfp4_linear_grad     : (k_lin_dz with an activation or dbias; -> k_column_sum with dbias) -> k_lin_transpose ->
 //                           k_lin_tile (-> k_lin_reduce)
 #include <hip/hip_runtime.h>
@@ -154,11 +154,11 @@ int check_product(int64_t M, int64_t K, int64_t N, int activation, int gated) {
 
 }  // namespace
 
-NVFP4_API size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int gated, int z_dtype) {
+NVFP4_API size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int x_dtype, int gated, int z_dtype) {
     if (check_product(M, K, N, gated ? NVFP4_ACT_SILU : NVFP4_ACT_NONE, gated) != NVFP4_OK || M == 0) return 0;
     const nvfp4::LinPlan plan =
-        nvfp4::plan_linear(M, K, N, gated != 0, z_dtype == NVFP4_DTYPE_MXFP8 ? nvfp4::kKeepMx : nvfp4::kKeepNone);
-    return plan.part_bytes + plan.frag_bytes;
+        nvfp4::plan_linear(M, K, N, x_dtype == NVFP4_DTYPE_MXFP8, gated != 0, z_dtype == NVFP4_DTYPE_MXFP8 ? nvfp4::kKeepMx : nvfp4::kKeepNone);
+    return plan.x_bytes + plan.part_bytes + plan.frag_bytes;
 }
 
 NVFP4_API int nvfp4_linear(const nvfp4_linear_args_t *a) {
@@ -193,8 +193,8 @@ NVFP4_API int nvfp4_linear(const nvfp4_linear_args_t *a) {
     p.M = a->M, p.L = a->K, p.N = a->N, p.F = F, p.act = a->activation, p.gated = a->gated;
     if (a->M == 1) p.ldx = a->K;
     hipStream_t st = static_cast<hipStream_t>(a->stream);
-    const nvfp4::LinPlan plan = nvfp4::plan_linear(p.M, p.L, p.N, p.gated, p.keep);
-    return with_scratch(a->workspace, a->workspace_bytes, plan.part_bytes + plan.frag_bytes, st,
+    const nvfp4::LinPlan plan = nvfp4::plan_linear(p.M, p.L, p.N, p.x_mx, p.gated, p.keep);
+    return with_scratch(a->workspace, a->workspace_bytes, plan.x_bytes + plan.part_bytes + plan.frag_bytes, st,
                         [&](void *ws) { return nvfp4::launch_linear(p, ws, st); });
 }
 

@@ -199,8 +199,8 @@ __device__ __forceinline__ void epilogue(const LinArgs &p, int64_t m, int64_t dm
 // --------------------------------------------------------------------------------------- tile kernel
 
 // The weights go straight from memory into the matrix cores' A operand: a wave owns 64 weight rows (two
-// tiles of 32), so no weight is decoded twice in a work-group and none passes through LDS. X (32 MT rows,
-// the B operand) goes through LDS, decoded to bf16 if it is MXFP8; the work-group's four waves read it all.
+// tiles of 32), so no weight is decoded twice in a work-group. X (32 MT rows of bf16, the B operand) goes through
+// LDS; the work-group's four waves read it all.
 //
 // v_mfma_f32_32x32x16_bf16 sums over its 16 k slots in any order, and its 32 A rows may be any rows, so
 // both are mapped to suit the memory:
@@ -217,60 +217,39 @@ constexpr int kValu = 0x002, kMfma = 0x008, kVmemRead = 0x020, kDsRead = 0x100, 
 __device__ __forceinline__ int slot_row(int r) { return 16 * ((r >> 2) & 1) + 4 * (r >> 3) + (r & 3); }
 
 // X of one step in registers, between the loads and the LDS stores.
-template <int MT, bool XMX>
+template <int MT>
 struct XStage {
-    static constexpr int kLoads = XMX ? (MT + 1) / 2 : MT;
-    uint4 v[kLoads];
-    uint32_t sb[XMX ? kLoads : 1];
+    uint4 v[MT];
 };
 
-// Where a thread reads X: byte offsets from the first row and k of the work-group's tile, which are uniform (rows
-// past the last read the last: the API keeps ld below 2^23, so 32 bits hold them).
-template <int MT, bool XMX>
+// Where a thread reads X (eight threads per row, 8 values each): byte offsets from the first row and k of the
+// work-group's tile, which are uniform (rows past the last read the last: the API keeps ld below 2^23, so 32 bits
+// hold them).
+template <int MT>
 struct XAddr {
-    static constexpr int kLoads = XStage<MT, XMX>::kLoads;
-    const uint8_t *x, *xs;  // row m0, k = 0
-    uint32_t off[kLoads], soff[XMX ? kLoads : 1];
-    int kk;  // the thread's first k in a step
+    const uint8_t *x;  // row m0, k = 0
+    uint32_t off[MT];
     __device__ __forceinline__ XAddr(const LinArgs &p, int64_t m0, int tid) {
         const int last = (int)min((int64_t)(32 * MT - 1), p.M - 1 - m0);
-        const int64_t nb = (p.L + kMxBlock - 1) / kMxBlock;
-        x = static_cast<const uint8_t *>(p.x) + m0 * p.ldx * (XMX ? 1 : 2);
-        xs = XMX ? p.xs + m0 * nb : nullptr;
-        kk = XMX ? 16 * (tid & 3) : 8 * (tid & 7);
+        x = static_cast<const uint8_t *>(p.x) + m0 * p.ldx * 2;
 #pragma unroll
-        for (int i = 0; i < kLoads; ++i) {
-            const int row = min(last, XMX ? (tid >> 2) + 64 * i : (tid >> 3) + 32 * i);
-            off[i] = (uint32_t)row * (uint32_t)p.ldx * (XMX ? 1u : 2u) + (uint32_t)kk * (XMX ? 1u : 2u);
-            if (XMX) soff[i] = (uint32_t)row * (uint32_t)nb + (uint32_t)(kk / kMxBlock);
-        }
+        for (int i = 0; i < MT; ++i)
+            off[i] = (uint32_t)min(last, (tid >> 3) + 32 * i) * (uint32_t)p.ldx * 2u + 16u * (uint32_t)(tid & 7);
     }
 };
 
 // WHOLE: the step lies inside the slice (else its k are masked).
-template <int MT, bool XMX, bool WHOLE>
-__device__ __forceinline__ void x_load(XStage<MT, XMX> &S, const XAddr<MT, XMX> &q, int64_t k0, int64_t kend, int tid) {
-    const uint8_t *x = q.x + k0 * (XMX ? 1 : 2);
-    if (XMX) {  // four threads per row, 16 codes each; k0 and kend are multiples of 16
-        const uint8_t *xs = q.xs + k0 / kMxBlock;
+template <int MT, bool WHOLE>
+__device__ __forceinline__ void x_load(XStage<MT> &S, const XAddr<MT> &q, int64_t k0, int64_t kend, int tid) {
+    const uint8_t *x = q.x + k0 * 2;
 #pragma unroll
-        for (int i = 0; i < S.kLoads; ++i) {
-            if (!WHOLE) S.v[i] = make_uint4(0u, 0u, 0u, 0u), S.sb[i] = 0u;
-            if ((MT > 1 || tid < 128) && (WHOLE || k0 + q.kk < kend)) {
-                S.v[i] = load16(x + q.off[i]);
-                S.sb[i] = xs[q.soff[i]];
-            }
-        }
-    } else {  // eight threads per row, 8 values each
-#pragma unroll
-        for (int i = 0; i < S.kLoads; ++i) {
-            if (WHOLE || k0 + kStep <= kend) {
-                S.v[i] = load16(x + q.off[i]);
-            } else {
-                Raw8<uint16_t> r;
-                r.load(reinterpret_cast<const uint16_t *>(x + q.off[i]), clamp_count(kend - k0 - q.kk, 8));
-                S.v[i] = r.a;
-            }
+    for (int i = 0; i < MT; ++i) {
+        if (WHOLE || k0 + kStep <= kend) {
+            S.v[i] = load16(x + q.off[i]);
+        } else {
+            Raw8<uint16_t> r;
+            r.load(reinterpret_cast<const uint16_t *>(x + q.off[i]), clamp_count(kend - k0 - 8 * (tid & 7), 8));
+            S.v[i] = r.a;
         }
     }
 }
@@ -279,31 +258,10 @@ __device__ __forceinline__ void x_load(XStage<MT, XMX> &S, const XAddr<MT, XMX> 
 // wave reads at one c then cover all banks.
 __device__ __forceinline__ int x_place(int row, int chunk) { return row * kStep + ((chunk ^ (row & 7)) << 3); }
 
-template <int MT, bool XMX>
-__device__ __forceinline__ void x_store(const XStage<MT, XMX> &S, uint16_t *xs, int tid) {
-    if (XMX) {
-        if (MT == 1 && tid >= 128) return;
+template <int MT>
+__device__ __forceinline__ void x_store(const XStage<MT> &S, uint16_t *xs, int tid) {
 #pragma unroll
-        for (int i = 0; i < S.kLoads; ++i) {
-            const int row = (tid >> 2) + 64 * i;
-            const float s = mx_scale_value(S.sb[i]);
-            const uint32_t c[4] = {S.v[i].x, S.v[i].y, S.v[i].z, S.v[i].w};
-#pragma unroll
-            for (int o = 0; o < 2; ++o) {
-                float f[8];
-                mx_decode4(c[2 * o], s, f);
-                mx_decode4(c[2 * o + 1], s, f + 4);
-                // exact in bf16: the high halves
-                auto pair = [](float a, float b) { return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u); };
-                *reinterpret_cast<uint4 *>(&xs[x_place(row, 2 * (tid & 3) + o)]) =
-                    make_uint4(pair(f[0], f[1]), pair(f[2], f[3]), pair(f[4], f[5]), pair(f[6], f[7]));
-            }
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < S.kLoads; ++i)
-            *reinterpret_cast<uint4 *>(&xs[x_place((tid >> 3) + 32 * i, tid & 7)]) = S.v[i];
-    }
+    for (int i = 0; i < MT; ++i) *reinterpret_cast<uint4 *>(&xs[x_place((tid >> 3) + 32 * i, tid & 7)]) = S.v[i];
 }
 
 // A lane's weights of one step: codes and scales of its row in both tiles, or the decoded fragments.
@@ -328,7 +286,7 @@ __device__ __forceinline__ int w_place(int r, int q) { return r * 64 + ((q ^ ((r
 
 // MT: tiles of 32 rows of X. FRAG: the weights come decoded, in the order of the fragments (k_lin_decode,
 // k_lin_transpose): coalesced and without the decoding, a step of a 256 x 256 tile takes 1.43 us instead of 1.70.
-template <int MT, bool XMX, bool FRAG, int EPI>
+template <int MT, bool FRAG, int EPI>
 __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinArgs p) {
     constexpr int kTpr = MT >= 8 ? 2 : 1, kXHalf = 32 * MT * kStep;  // tiles per epilogue round; one X buffer
     constexpr int kLdsX = 2 * kXHalf * 2, kLdsLoop = kLdsX + (FRAG ? 0 : 4 * (kWaveCodes + kWaveScales));
@@ -346,7 +304,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
     const unsigned band = t0 / (4 * p.tiles_n), in = t0 % (4 * p.tiles_n);
     const unsigned bm = min(4u, p.tiles_m - 4 * band);
     const int64_t m0 = (int64_t)(4 * band + in % bm) * (32 * MT);
-    const int64_t tn = in / bm;
+    const int64_t tn = p.tn0 + in / bm;
     const int64_t kbeg = (int64_t)slice * p.kslice, kend = min(p.L, kbeg + p.kslice);
     const int64_t kfull = kbeg + (kend - kbeg) / (2 * kStep) * (2 * kStep);  // the end of its whole pairs of steps
     const int64_t f0 = kGated ? tn * 128 + 32 * wave : tn * 256 + 64 * wave;
@@ -366,8 +324,8 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
     f32x16 acc[2][MT] = {};
     // X is loaded one step ahead of its store, two where a step is short.
     constexpr int kSets = MT >= 8 ? 1 : 2;
-    XStage<MT, XMX> X[kSets];
-    const XAddr<MT, XMX> xa(p, m0, tid);
+    XStage<MT> X[kSets];
+    const XAddr<MT> xa(p, m0, tid);
     Weights W[2];
     WStage S;
     bf16x8 A[2][2], B[2][MT];  // the fragments of one phase and of the next (A: decoded weights alone)
@@ -461,12 +419,12 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
             b_frag(B[(i + 1) & 1], i < 3 ? odd : odd ^ 1, (i + 1) & 3);
             a_frag(A[(i + 1) & 1], i < 3 ? w : next, (i + 1) & 3);
             if (i == 0) {
-                x_store<MT, XMX>(X[(odd ^ 1) & (kSets - 1)], xs + (odd ^ 1) * kXHalf, tid);
+                x_store<MT>(X[(odd ^ 1) & (kSets - 1)], xs + (odd ^ 1) * kXHalf, tid);
                 if (!FRAG && odd) stage_store();
                 frag_load(next, min(k0 + kStep, kfull - kStep));
             }
             if (i == 1) {
-                x_load<MT, XMX, true>(X[(odd ^ 1) & (kSets - 1)], xa, min(k0 + (1 + kSets) * kStep, kfull - kStep), kend, tid);
+                x_load<MT, true>(X[(odd ^ 1) & (kSets - 1)], xa, min(k0 + (1 + kSets) * kStep, kfull - kStep), kend, tid);
                 if (!FRAG && odd) stage_load(min(k0 + 3 * kStep, kfull - 2 * kStep));
             }
             if (i == 2) stage_read(next, odd ^ 1);
@@ -480,7 +438,6 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-                if (i == 0 && XMX) __builtin_amdgcn_sched_group_barrier(kValu, 16, 0);
                 if (i == 0) __builtin_amdgcn_sched_group_barrier(kDsWrite, kPairWork, 0);
                 if (i == 2 && !FRAG) __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
                 if (i == 1 || (i == 0 && FRAG)) __builtin_amdgcn_sched_group_barrier(kVmemRead, kPairWork, 0);
@@ -490,16 +447,16 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
     };
 
     if (kfull > kbeg) {
-        x_load<MT, XMX, true>(X[0], xa, kbeg, kend, tid);
+        x_load<MT, true>(X[0], xa, kbeg, kend, tid);
         if (!FRAG) stage_load(kbeg);
         frag_load(W[0], kbeg);
-        x_store<MT, XMX>(X[0], xs, tid);
+        x_store<MT>(X[0], xs, tid);
         if (!FRAG) {
             stage_store();
             stage_load(min(kbeg + 2 * kStep, kfull - 2 * kStep));
         }
-        x_load<MT, XMX, true>(X[kSets - 1], xa, kbeg + kStep, kend, tid);
-        if (kSets == 2) x_load<MT, XMX, true>(X[0], xa, min(kbeg + 2 * kStep, kfull - kStep), kend, tid);
+        x_load<MT, true>(X[kSets - 1], xa, kbeg + kStep, kend, tid);
+        if (kSets == 2) x_load<MT, true>(X[0], xa, min(kbeg + 2 * kStep, kfull - kStep), kend, tid);
         lds_barrier();
         b_frag(B[0], 0, 0);
         stage_read(W[0], 0);
@@ -516,7 +473,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
     // The slice's last, fewer than 128 k, with masks and one step at a time.
 #pragma unroll 1
     for (int64_t k0 = kfull; k0 < kend; k0 += kStep) {
-        x_load<MT, XMX, false>(X[0], xa, k0, kend, tid);
+        x_load<MT, false>(X[0], xa, k0, kend, tid);
         frag_load(W[0], k0);
         if constexpr (!FRAG)
 #pragma unroll
@@ -533,7 +490,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
                     W[0].s[j] = p.scales[e / 16];
                 }
             }
-        x_store<MT, XMX>(X[0], xs, tid);
+        x_store<MT>(X[0], xs, tid);
         lds_barrier();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -1037,6 +994,7 @@ __global__ __launch_bounds__(256) void k_lin_dz(LinGradArgs p, int64_t chunk, fl
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Tile height and K split of the tile kernel for an [M] x [F] output over a sum of length L: the least of the times
 // that these measurements add up to (us on an MI355X; weights coded, or decoded before: `frag`). A step of 64 k
@@ -1083,24 +1041,49 @@ LinPlan plan_tile(int64_t M, int64_t L, int64_t F, int64_t N, bool gated, bool f
             }
         }
     }
+    // The last round of the tallest tiles, if it has too few of them: its columns in tiles of half the height, which
+    // take 65 us where a round of the tallest takes 107 (K = 4096).
+    if (best.mt == 8 && best.slices == 1 && best.tiles_m * best.tiles_n > 256 && best.tiles_m <= 256) {
+        const int64_t whole = best.tiles_m * best.tiles_n / 256 * 256 / best.tiles_m;  // columns of the whole rounds
+        const int64_t last = best.tiles_n - whole;
+        if (last > 0 && last * ceil_div(M, 128) <= 256) best.last_tiles_n = last;
+    }
     return best;
 }
 
-template <bool XMX, bool FRAG, int EPI>
-hipError_t tile_launch_as(const LinArgs &p, const LinPlan &plan, hipStream_t st) {
-    const dim3 grid((unsigned)(p.tiles * plan.slices)), block(kTileThreads);
-    if constexpr (FRAG && (XMX || EPI != kEpiPlain)) {  // the forward with weights decoded first: tall tiles alone
-        if (plan.mt != 8) return hipErrorInvalidValue;
-        hipLaunchKernelGGL((k_lin_tile<8, XMX, FRAG, EPI>), grid, block, 0, st, p);
+template <bool FRAG, int EPI>
+hipError_t tile_launch_height(const LinArgs &p, int mt, int64_t slices, hipStream_t st) {
+    const dim3 grid((unsigned)(p.tiles * slices)), block(kTileThreads);
+    if constexpr (FRAG && EPI != kEpiPlain) {  // the forward with weights decoded first: tall tiles alone
+        if (mt == 4)
+            hipLaunchKernelGGL((k_lin_tile<4, FRAG, EPI>), grid, block, 0, st, p);
+        else if (mt == 8)
+            hipLaunchKernelGGL((k_lin_tile<8, FRAG, EPI>), grid, block, 0, st, p);
+        else
+            return hipErrorInvalidValue;
     } else {
-        switch (plan.mt) {
-            case 1: hipLaunchKernelGGL((k_lin_tile<1, XMX, FRAG, EPI>), grid, block, 0, st, p); break;
-            case 2: hipLaunchKernelGGL((k_lin_tile<2, XMX, FRAG, EPI>), grid, block, 0, st, p); break;
-            case 4: hipLaunchKernelGGL((k_lin_tile<4, XMX, FRAG, EPI>), grid, block, 0, st, p); break;
-            default: hipLaunchKernelGGL((k_lin_tile<8, XMX, FRAG, EPI>), grid, block, 0, st, p); break;
+        switch (mt) {
+            case 1: hipLaunchKernelGGL((k_lin_tile<1, FRAG, EPI>), grid, block, 0, st, p); break;
+            case 2: hipLaunchKernelGGL((k_lin_tile<2, FRAG, EPI>), grid, block, 0, st, p); break;
+            case 4: hipLaunchKernelGGL((k_lin_tile<4, FRAG, EPI>), grid, block, 0, st, p); break;
+            default: hipLaunchKernelGGL((k_lin_tile<8, FRAG, EPI>), grid, block, 0, st, p); break;
         }
     }
-    hipError_t err = hipGetLastError();
+    return hipGetLastError();
+}
+
+template <bool FRAG, int EPI>
+hipError_t tile_launch_as(LinArgs p, const LinPlan &plan, hipStream_t st) {
+    auto columns = [&](int mt, int64_t first, int64_t count) {
+        const int64_t tm = ceil_div(p.M, 32 * mt);
+        p.tn0 = first, p.tiles_n = (unsigned)count, p.tiles_m = (unsigned)tm, p.tiles = (unsigned)(tm * count);
+        return tile_launch_height<FRAG, EPI>(p, mt, plan.slices, st);
+    };
+    if (plan.last_tiles_n > 0) {
+        const hipError_t err = columns(8, 0, plan.tiles_n - plan.last_tiles_n);
+        return err != hipSuccess ? err : columns(4, plan.tiles_n - plan.last_tiles_n, plan.last_tiles_n);
+    }
+    hipError_t err = columns(plan.mt, 0, plan.tiles_n);
     if (err == hipSuccess && plan.slices > 1) {
         const int64_t per_row = ceil_div(p.F, kMxBlock) * 4, groups = p.M * per_row;
         const dim3 rg((unsigned)std::min<int64_t>(ceil_div(groups, kReduceThreads), 4096));
@@ -1113,15 +1096,13 @@ hipError_t tile_launch_as(const LinArgs &p, const LinPlan &plan, hipStream_t st)
     return err;
 }
 
-template <bool XMX, bool FRAG>
+template <bool FRAG>
 hipError_t tile_launch(LinArgs p, const LinPlan &plan, hipStream_t st) {
-    p.tiles_n = (unsigned)plan.tiles_n, p.tiles_m = (unsigned)plan.tiles_m;
-    p.tiles = (unsigned)(plan.tiles_n * plan.tiles_m);
     p.kslice = plan.kslice;
-    if (p.gated) return tile_launch_as<XMX, FRAG, kEpiGated>(p, plan, st);
+    if (p.gated) return tile_launch_as<FRAG, kEpiGated>(p, plan, st);
     if (p.bias || p.res || p.act != kActNone || p.keep != kKeepNone || p.y_f32)
-        return tile_launch_as<XMX, FRAG, kEpiFull>(p, plan, st);
-    return tile_launch_as<XMX, FRAG, kEpiPlain>(p, plan, st);
+        return tile_launch_as<FRAG, kEpiFull>(p, plan, st);
+    return tile_launch_as<FRAG, kEpiPlain>(p, plan, st);
 }
 
 template <int NT, int WAVES>
@@ -1171,7 +1152,6 @@ struct GradPlan {
     int64_t chunk, chunks;
     size_t wt_bytes, sum_bytes;
 };
-size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 GradPlan plan_grad(int64_t M, int64_t K, int64_t N, int64_t F, bool bias) {
     GradPlan g = {};
@@ -1190,7 +1170,7 @@ GradPlan plan_grad(int64_t M, int64_t K, int64_t N, int64_t F, bool bias) {
 // about 2300 rows of X (4096 x 4096 weights: see the figures at the plan's test of M).
 constexpr int64_t kDecodeFirstRows = 2560;
 
-LinPlan plan_linear(int64_t M, int64_t K, int64_t N, bool gated, int keep) {
+LinPlan plan_linear(int64_t M, int64_t K, int64_t N, bool x_mx, bool gated, int keep) {
     if (M <= kSkinnyMaxM && keep != kKeepMx) {  // mt = 0: the skinny kernel
         LinPlan p = {};
         p.slices = 1;
@@ -1198,27 +1178,35 @@ LinPlan plan_linear(int64_t M, int64_t K, int64_t N, bool gated, int keep) {
         return p;
     }
     LinPlan p = plan_tile(M, K, gated ? N / 2 : N, N, gated, false);
+    if (x_mx) p.x_bytes = align256((size_t)(M * K) * 2);
     if (M >= kDecodeFirstRows && p.mt == 8 && p.slices == 1)
         p.frag_bytes = (size_t)(ceil_div(gated ? N / 2 : N, 32) * (gated ? 2 : 1) * ceil_div(K, kStep)) * 4096;
     return p;
 }
 
 hipError_t launch_linear(const LinArgs &args, void *ws, hipStream_t stream) {
-    const LinPlan plan = plan_linear(args.M, args.L, args.N, args.gated, args.keep);
+    const LinPlan plan = plan_linear(args.M, args.L, args.N, args.x_mx, args.gated, args.keep);
     LinArgs p = args;
     if (plan.mt == 0) {
         return p.gated ? skinny_launch<2>(p, ws, stream) : skinny_launch<1>(p, ws, stream);
     }
+    uint8_t *base = static_cast<uint8_t *>(ws);
+    if (plan.x_bytes) {  // an MXFP8 X is decoded once, not by every work-group that reads it
+        const hipError_t err = launch_mx_dequantize(static_cast<const uint8_t *>(p.x), p.ldx, p.xs, p.M, p.L, base, false, stream);
+        if (err != hipSuccess) return err;
+        p.x = base, p.ldx = p.L, p.x_mx = 0;
+        base += plan.x_bytes;
+    }
     if (plan.frag_bytes) {
-        p.wt = static_cast<uint16_t *>(ws);
+        p.wt = reinterpret_cast<uint16_t *>(base);
         const dim3 grid((unsigned)ceil_div(ceil_div(p.F, 32), 4), (unsigned)ceil_div(ceil_div(p.L, kStep), 4), p.gated ? 2 : 1);
-        hipLaunchKernelGGL(k_lin_decode, grid, dim3(256), 0, stream, p.codes, p.scales, p.F, p.L, static_cast<uint16_t *>(ws));
+        hipLaunchKernelGGL(k_lin_decode, grid, dim3(256), 0, stream, p.codes, p.scales, p.F, p.L, reinterpret_cast<uint16_t *>(base));
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
-        return p.x_mx ? tile_launch<true, true>(p, plan, stream) : tile_launch<false, true>(p, plan, stream);
+        return tile_launch<true>(p, plan, stream);
     }
-    p.part = plan.slices > 1 ? static_cast<float *>(ws) : nullptr;
-    return p.x_mx ? tile_launch<true, false>(p, plan, stream) : tile_launch<false, false>(p, plan, stream);
+    p.part = plan.slices > 1 ? reinterpret_cast<float *>(base) : nullptr;
+    return tile_launch<false>(p, plan, stream);
 }
 
 size_t linear_grad_workspace(int64_t M, int64_t K, int64_t N, int64_t F, bool bias) {
@@ -1258,7 +1246,7 @@ hipError_t launch_linear_grad(const LinGradArgs &g, const uint8_t *codes, const 
     p.y = dx;
     p.wt = wt;
     p.part = plan.tile.slices > 1 ? part : nullptr;
-    return tile_launch<false, true>(p, plan.tile, stream);
+    return tile_launch<true>(p, plan.tile, stream);
 }
 
 }  // namespace nvfp4

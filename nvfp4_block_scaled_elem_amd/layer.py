@@ -257,8 +257,8 @@ def _activation(activation, gated, N):
     return N // 2 if gated else N
 
 
-def linear_workspace_bytes(M: int, K: int, N: int, gated: bool = False, keep=None) -> int:
-    return int(lib().nvfp4_linear_workspace_bytes(M, K, N, int(gated), _MX if keep == MXFP8 else 0))
+def linear_workspace_bytes(M: int, K: int, N: int, gated: bool = False, keep=None, x_mxfp8: bool = False) -> int:
+    return int(lib().nvfp4_linear_workspace_bytes(M, K, N, _MX if x_mxfp8 else 0, int(gated), _MX if keep == MXFP8 else 0))
 
 
 def linear(X, codes: torch.Tensor, scales: torch.Tensor, alpha: torch.Tensor, *, bias=None, activation=None,
@@ -298,7 +298,7 @@ def linear(X, codes: torch.Tensor, scales: torch.Tensor, alpha: torch.Tensor, *,
         elif keep is not None:
             Z = torch.empty((M, N), dtype=keep, device=dev)
             z = Z.data_ptr()
-        ws, nbytes = _space(workspace, linear_workspace_bytes(M, K, N, gated, keep), dev)
+        ws, nbytes = _space(workspace, linear_workspace_bytes(M, K, N, gated, keep, xt == _MX), dev)
         a = _LinearArgs(x.data_ptr(), ldx, _ptr(xs), xt, M, K, N, codes.data_ptr(), scales.data_ptr(), alpha.data_ptr(),
                         _ptr(bias), 0 if bias is None else DTYPES[bias.dtype], ACTIVATIONS[activation], int(gated),
                         _ptr(residual), ldr, 0 if residual is None else DTYPES[residual.dtype], Y.data_ptr(),

@@ -125,10 +125,11 @@ def test_null_arguments(L):
 
 
 def test_workspace_sizes(L):
-    assert L.nvfp4_linear_workspace_bytes(1, 4096, 4096, 0, 0) == 0
-    assert L.nvfp4_linear_workspace_bytes(0, 4096, 4096, 0, 0) == 0
-    assert L.nvfp4_linear_workspace_bytes(4, 100, 64, 0, 0) == 0  # no such product
-    assert L.nvfp4_linear_workspace_bytes(100, 4096, 64, 0, 0) > 0
+    assert L.nvfp4_linear_workspace_bytes(1, 4096, 4096, 0, 0, 0) == 0
+    assert L.nvfp4_linear_workspace_bytes(0, 4096, 4096, 0, 0, 0) == 0
+    assert L.nvfp4_linear_workspace_bytes(4, 100, 64, 0, 0, 0) == 0  # no such product
+    assert L.nvfp4_linear_workspace_bytes(100, 4096, 64, 0, 0, 0) > 0
+    assert L.nvfp4_linear_workspace_bytes(100, 96, 64, 2, 0, 0) >= 2 * 100 * 96  # an MXFP8 X, decoded
     # the decoded weights, and a partial sum of the bias per chunk of rows
     assert L.nvfp4_linear_grad_workspace_bytes(4096, 4096, 4096, 0, 0) >= 2 * 4096 * 4096
     assert (L.nvfp4_linear_grad_workspace_bytes(64, 96, 64, 0, 1) > L.nvfp4_linear_grad_workspace_bytes(64, 96, 64, 0, 0))
