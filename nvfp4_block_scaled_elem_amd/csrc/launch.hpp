@@ -173,6 +173,7 @@ struct LinGradArgs {
 struct LinPlan {
     int mt;  // tiles of 32 rows of X per work-group; 0: the skinny kernel
     int64_t tiles_m, tiles_n, slices, kslice;
+    double us;             // estimated
     int64_t last_tiles_n;  // of the tiles_n columns of tiles (mt 8), the last ones run at half the height
     size_t part_bytes;  // fp32 sums of the K slices (0: K is not split)
     size_t x_bytes;     // an MXFP8 X decoded for the tile kernel

@@ -284,12 +284,34 @@ constexpr int kWaveCodes = 64 * 64, kWaveScales = 64 * 8;  // LDS bytes of a wav
 // 16-byte chunk q (0..3) of row r of a wave's codes.
 __device__ __forceinline__ int w_place(int r, int q) { return r * 64 + ((q ^ ((r >> 2) & 3)) << 4); }
 
-// MT: tiles of 32 rows of X. FRAG: the weights come decoded, in the order of the fragments (k_lin_decode,
-// k_lin_transpose): coalesced and without the decoding, a step of a 256 x 256 tile takes 1.43 us instead of 1.70.
-template <int MT, bool FRAG, int EPI>
+// Where the weights come from.
+//   kSrcCodes: as stored, the sum running along their rows (the forward).
+//   kSrcFrag: decoded beforehand, in the order of the fragments (k_lin_decode, k_lin_transpose): coalesced and
+//     without the decoding, a step of a 256 x 256 tile takes 1.43 us instead of 1.55.
+//   kSrcTurn: as stored, the sum running along their columns (the gradient): a wave decodes its 64 columns of 64
+//     weight rows, pairs the values along the sum, and turns them into fragments in LDS. What a decoding pass
+//     before would write and read again (four bytes a weight) is saved; the work is repeated for every tile of
+//     rows of X.
+enum { kSrcCodes = 0, kSrcFrag = 1, kSrcTurn = 2 };
+
+// kSrcTurn: the codes of 8 weight rows by 8 columns per lane (lane = 8 (rows / 8) + columns / 8), and the scale bytes
+// of the wave's 64 columns for row `lane`.
+struct TStage {
+    uint32_t c[8];
+    uint32_t s;
+};
+constexpr int kTurnFrags = 8192, kTurnLds = kTurnFrags + 4 * 64;  // LDS bytes of a wave: fragments, scales
+// 16-byte piece u (32 half + slot) of product i and column tile j. The pieces that eight lanes write at once are 4 or 8
+// apart: the swizzle puts them in different banks, and keeps eight consecutive ones in different banks.
+__device__ __forceinline__ int turn_place(int j, int i, int u) { return (((j * 4 + i) * 64) + ((u ^ ((u >> 3) & 7)) ^ j)) * 16; }
+
+// MT: tiles of 32 rows of X.
+template <int MT, int SRC, int EPI>
 __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinArgs p) {
     constexpr int kTpr = MT >= 8 ? 2 : 1, kXHalf = 32 * MT * kStep;  // tiles per epilogue round; one X buffer
-    constexpr int kLdsX = 2 * kXHalf * 2, kLdsLoop = kLdsX + (FRAG ? 0 : 4 * (kWaveCodes + kWaveScales));
+    constexpr bool kCodes = SRC == kSrcCodes, kFrag = SRC == kSrcFrag, kTurn = SRC == kSrcTurn;
+    constexpr int kWaveLds = kCodes ? kWaveCodes + kWaveScales : kTurn ? kTurnLds : 0;
+    constexpr int kLdsX = 2 * kXHalf * 2, kLdsLoop = kLdsX + 4 * kWaveLds;
     constexpr int kLds = kLdsLoop > kTpr * 32768 ? kLdsLoop : kTpr * 32768;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kLds];
     uint16_t *const xs = reinterpret_cast<uint16_t *>(lds);
@@ -308,7 +330,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
     const int64_t kbeg = (int64_t)slice * p.kslice, kend = min(p.L, kbeg + p.kslice);
     const int64_t kfull = kbeg + (kend - kbeg) / (2 * kStep) * (2 * kStep);  // the end of its whole pairs of steps
     const int64_t f0 = kGated ? tn * 128 + 32 * wave : tn * 256 + 64 * wave;
-    const int64_t steps_all = (p.L + kStep - 1) / kStep, ktiles = (p.F + 31) / 32;  // FRAG; F = N unless gated
+    const int64_t steps_all = (p.L + kStep - 1) / kStep, ktiles = (p.F + 31) / 32;  // kFrag; F = N unless gated
     // The wave's weight rows: tile j starts at row w0[j] (uniform) and has `rows[j]` of them; rows past the last
     // read the last.
     int64_t w0[2];
@@ -320,7 +342,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
         w0[j] = first + (kGated && j ? p.F : 0);
     }
 
-    using Weights = typename std::conditional<FRAG, WFrag, WCodes>::type;
+    using Weights = typename std::conditional<kCodes, WCodes, WFrag>::type;
     f32x16 acc[2][MT] = {};
     // X is loaded one step ahead of its store, two where a step is short.
     constexpr int kSets = MT >= 8 ? 1 : 2;
@@ -332,8 +354,8 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
 
     // The stage's codes: load i takes rows 16 i + lane / 4 of the wave's 64, chunk lane % 4; its scales: row lane.
     uint32_t soff[4], sscale = 0u;
-    uint8_t *const wl = lds + kLdsX + wave * (kWaveCodes + kWaveScales);
-    if constexpr (!FRAG) {
+    uint8_t *const wl = lds + kLdsX + wave * kWaveLds;
+    if constexpr (kCodes) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int row = min(slot_row((16 * i + (lane >> 2)) & 31), rows[i >> 1] - 1);
@@ -355,7 +377,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
     // The lane's codes and scales of step `odd` of the stored pair. Only the wave itself writes and reads them, in
     // order.
     auto stage_read = [&](Weights &D, int odd) __attribute__((always_inline)) {
-        if constexpr (!FRAG)
+        if constexpr (kCodes)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 D.c[j] = *reinterpret_cast<const uint4 *>(wl + w_place(32 * j + r32, 2 * odd + half));
@@ -363,7 +385,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
             }
     };
     auto frag_load = [&](Weights &D, int64_t k0) __attribute__((always_inline)) {
-        if constexpr (FRAG)
+        if constexpr (kFrag)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int64_t kt = kGated ? min(ktiles - 1, f0 / 32) + j * ktiles : min(ktiles - 1, f0 / 32 + j);
@@ -372,12 +394,82 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
                 for (int i = 0; i < 4; ++i) D.v[j][i] = load16(q + (uint32_t)(lane * 16) + i * 1024);
             }
     };
+    // kSrcTurn: the wave's 64 columns start at cb; lanes past the last column read it again, and the scale bytes start at
+    // block sb / 16 (F >= 64), so that every read lies inside a row.
+    TStage T[2];
+    const int kg = lane & 7, ng = lane >> 3;
+    const int64_t cb = kTurn ? min(f0, p.F - 16) : 0, sb = kTurn ? min(cb, p.F - 64) : 0;
+    const int kgc = kTurn ? (int)min((int64_t)kg, (p.F - cb) / 8 - 1) : 0;
+    const uint32_t toff = kTurn ? (uint32_t)ng * 8u * (uint32_t)(p.F / 2) + 4u * kgc : 0u;
+    const int tblock = kTurn ? (int)((cb - sb) / 16) + (kgc >> 1) : 0;
+    auto turn_load = [&](auto whole, TStage &D, int64_t n0) __attribute__((always_inline)) {
+        if constexpr (kTurn) {
+            const uint8_t *c = p.codes + (n0 * p.F + cb) / 2;
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                D.c[r] = 0u;
+                if (whole.value || n0 + 8 * ng + r < kend)
+                    D.c[r] = load4(c + (int64_t)r * (p.F / 2) + toff);
+            }
+            D.s = 0u;
+            if (whole.value || n0 + lane < kend) D.s = load4(p.scales + (n0 * p.F + sb) / 16 + (uint32_t)lane * (uint32_t)(p.F / 16));
+        }
+    };
+    float td[8];
+    auto turn_scales = [&](const TStage &D) __attribute__((always_inline)) {
+        if constexpr (kTurn) {
+            uint8_t *const q = wl + kTurnFrags;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) q[64 * b + lane] = (uint8_t)(D.s >> (8 * b));
+            const uint2 s = *reinterpret_cast<const uint2 *>(q + 64 * tblock + 8 * ng);
+            const uint32_t w[2] = {s.x & 0x7F7F7F7Fu, s.y & 0x7F7F7F7Fu};
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const f32x2 a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], false), b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w[i], true);
+                td[4 * i] = a.x, td[4 * i + 1] = a.y, td[4 * i + 2] = b.x, td[4 * i + 3] = b.y;
+            }
+        }
+    };
+    // Columns 2 CP and 2 CP + 1 of the lane's eight, as fragment pieces of eight rows each.
+    auto turn_columns = [&](const TStage &D, auto pair) __attribute__((always_inline)) {
+        if constexpr (kTurn) {
+            constexpr int CP = decltype(pair)::value;
+            float v[2][8];
+#pragma unroll
+            for (int r = 0; r < 8; ++r) {
+                const f32x2 q = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(D.c[r], 1.0f, CP);
+                v[0][r] = q.x * td[r], v[1][r] = q.y * td[r];
+            }
+            auto two = [](float x, float y) { return __builtin_amdgcn_perm(__float_as_uint(y), __float_as_uint(x), 0x07060302u); };
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int o = 8 * (kg & 3) + 2 * CP + e, slot = 8 * ((o >> 2) & 3) + 4 * (o >> 4) + (o & 3);
+                *reinterpret_cast<uint4 *>(wl + turn_place(kg >> 2, ng & 3, 32 * (ng >> 2) + slot)) =
+                    make_uint4(two(v[e][0], v[e][1]), two(v[e][2], v[e][3]), two(v[e][4], v[e][5]), two(v[e][6], v[e][7]));
+            }
+        }
+    };
+    auto turn_read = [&](Weights &D) __attribute__((always_inline)) {
+        if constexpr (kTurn)
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) D.v[j][i] = *reinterpret_cast<const uint4 *>(wl + turn_place(j, i, lane));
+    };
+    auto turn_all = [&](const TStage &D) __attribute__((always_inline)) {
+        turn_scales(D);
+        turn_columns(D, std::integral_constant<int, 0>{});
+        turn_columns(D, std::integral_constant<int, 1>{});
+        turn_columns(D, std::integral_constant<int, 2>{});
+        turn_columns(D, std::integral_constant<int, 3>{});
+    };
     auto a_frag = [&](bf16x8 (&D)[2], const Weights &w, int i) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            if constexpr (!FRAG) {
+            if constexpr (kCodes) {
                 const uint32_t c = i == 0 ? w.c[j].x : i == 1 ? w.c[j].y : i == 2 ? w.c[j].z : w.c[j].w;
-                D[j] = __builtin_bit_cast(bf16x8, dequant8(c, e4m3_value((w.s[j] >> (i >= 2 ? 8 : 0)) & 0x7Fu)));
+                const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8((int)(w.s[j] & 0x7F7Fu), false);  // both scales
+                D[j] = __builtin_bit_cast(bf16x8, dequant8(c, i < 2 ? d.x : d.y));
             }
         }
     };
@@ -392,7 +484,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 bf16x8 a;
-                if constexpr (FRAG)
+                if constexpr (!kCodes)
                     a = __builtin_bit_cast(bf16x8, w.v[j][i]);
                 else
                     a = A[at][j];
@@ -404,14 +496,15 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
     // matrix cores work on its own. X: stored in phase 0 for the next step, loaded in phase 1 for the one kSets later.
     // Codes: a pair is stored in phase 0 of the odd step (every read of the pair before has been issued) and
     // loaded in phase 1 for the pair after; the lane's own are read in phase 2 for the next step. Decoded weights
-    // are loaded in phase 0 for the next step. The one barrier stands before the last phase: by then every
+    // are loaded in phase 0 for the next step; turned ones are formed in phases 0 to 2 from codes loaded two steps
+    // before, and read back in phase 3. The one barrier stands before the last phase: by then every
     // wave has stored X of the next step and has read all of this one's, so that phase 3 can read ahead from the other
     // buffer and the next step can store into this one. What is loaded past the last whole pair is that pair again.
     // One wave per SIMD (MT = 8) hides nothing behind another wave, so the order inside a phase is asked for:
     // LDS reads (and weights decoded) between the first products, stores and loads between the rest.
     auto step = [&](auto parity, int64_t k0) __attribute__((always_inline)) {
         constexpr int odd = decltype(parity)::value;
-        constexpr int kPairWork = !FRAG && odd ? 2 : 1;  // the odd step moves the codes too
+        constexpr int kPairWork = kCodes && odd ? 2 : 1;  // the odd step moves the codes too
         Weights &w = W[odd], &next = W[odd ^ 1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -420,27 +513,37 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
             a_frag(A[(i + 1) & 1], i < 3 ? w : next, (i + 1) & 3);
             if (i == 0) {
                 x_store<MT>(X[(odd ^ 1) & (kSets - 1)], xs + (odd ^ 1) * kXHalf, tid);
-                if (!FRAG && odd) stage_store();
+                if (kCodes && odd) stage_store();
                 frag_load(next, min(k0 + kStep, kfull - kStep));
+                turn_scales(T[odd ^ 1]);
+                turn_columns(T[odd ^ 1], std::integral_constant<int, 0>{});
             }
             if (i == 1) {
                 x_load<MT, true>(X[(odd ^ 1) & (kSets - 1)], xa, min(k0 + (1 + kSets) * kStep, kfull - kStep), kend, tid);
-                if (!FRAG && odd) stage_load(min(k0 + 3 * kStep, kfull - 2 * kStep));
+                if (kCodes && odd) stage_load(min(k0 + 3 * kStep, kfull - 2 * kStep));
+                turn_columns(T[odd ^ 1], std::integral_constant<int, 1>{});
+                turn_columns(T[odd ^ 1], std::integral_constant<int, 2>{});
             }
-            if (i == 2) stage_read(next, odd ^ 1);
+            if (i == 2) {
+                stage_read(next, odd ^ 1);
+                turn_columns(T[odd ^ 1], std::integral_constant<int, 3>{});
+                turn_load(std::true_type{}, T[odd ^ 1], min(k0 + 3 * kStep, kfull - kStep));
+            }
+            if (i == 3) turn_read(next);
             products(w, i, i & 1);
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
                 __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
-                if (!FRAG) __builtin_amdgcn_sched_group_barrier(kValu, 40 / MT, 0);
+                if (!kFrag) __builtin_amdgcn_sched_group_barrier(kValu, 40 / MT, 0);
             }
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
                 __builtin_amdgcn_sched_group_barrier(kMfma, 1, 0);
                 if (i == 0) __builtin_amdgcn_sched_group_barrier(kDsWrite, kPairWork, 0);
-                if (i == 2 && !FRAG) __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
-                if (i == 1 || (i == 0 && FRAG)) __builtin_amdgcn_sched_group_barrier(kVmemRead, kPairWork, 0);
+                if (kTurn && i > 0 && i < 3) __builtin_amdgcn_sched_group_barrier(kDsWrite, 1, 0);
+                if ((i == 2 && kCodes) || (i == 3 && kTurn)) __builtin_amdgcn_sched_group_barrier(kDsRead, 1, 0);
+                if (i == 1 || (i == 0 && kFrag) || (i == 2 && kTurn)) __builtin_amdgcn_sched_group_barrier(kVmemRead, kPairWork, 0);
             }
             __builtin_amdgcn_sched_barrier(0);
         }
@@ -448,10 +551,17 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
 
     if (kfull > kbeg) {
         x_load<MT, true>(X[0], xa, kbeg, kend, tid);
-        if (!FRAG) stage_load(kbeg);
+        if (kCodes) stage_load(kbeg);
+        turn_load(std::true_type{}, T[0], kbeg);
+        turn_load(std::true_type{}, T[1], kbeg + kStep);
         frag_load(W[0], kbeg);
         x_store<MT>(X[0], xs, tid);
-        if (!FRAG) {
+        if (kTurn) {
+            turn_all(T[0]);
+            turn_load(std::true_type{}, T[0], min(kbeg + 2 * kStep, kfull - kStep));
+            turn_read(W[0]);
+        }
+        if (kCodes) {
             stage_store();
             stage_load(min(kbeg + 2 * kStep, kfull - 2 * kStep));
         }
@@ -475,7 +585,12 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
     for (int64_t k0 = kfull; k0 < kend; k0 += kStep) {
         x_load<MT, false>(X[0], xa, k0, kend, tid);
         frag_load(W[0], k0);
-        if constexpr (!FRAG)
+        if (kTurn) {
+            turn_load(std::false_type{}, T[0], k0);
+            turn_all(T[0]);
+            turn_read(W[0]);
+        }
+        if constexpr (kCodes)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 const int64_t k = k0 + 32 * half, e = (w0[j] + min(slot_row(r32), rows[j] - 1)) * p.L + k;
@@ -997,21 +1112,21 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Tile height and K split of the tile kernel for an [M] x [F] output over a sum of length L: the least of the times
-// that these measurements add up to (us on an MI355X; weights coded, or decoded before: `frag`). A step of 64 k
-// costs, with one work-group per CU and with two (heights 1 and 2; the taller take a CU each):
+// that these measurements add up to (us on an MI355X). A step of 64 k costs, with one work-group per CU and with
+// two (heights 1 and 2; the taller take a CU each), by where the weights come from:
 //   height (of 32 rows)   1            2            4      8
-//   coded                 0.60 / 0.97  0.71 / 1.26  1.00   1.55
-//   decoded               0.38 / 0.74  0.51 / 0.97  0.80   1.43
-// on top of 7, 9, 14 and 15 per work-group (launch, first loads, epilogue), and slices of K cost 4 and 8 bytes per
+//   as stored             0.62 / 0.96  0.75 / 1.27  1.00   1.55
+//   decoded before        0.38 / 0.74  0.51 / 0.97  0.80   1.43
+//   turned                0.83 / 1.09  0.85 / 1.35  1.09   1.75
+// on top of 6, 8, 13 and 15 per work-group (launch, first loads, epilogue), and slices of K cost 4 and 8 bytes per
 // sum at 4 TB/s.
-LinPlan plan_tile(int64_t M, int64_t L, int64_t F, int64_t N, bool gated, bool frag) {
+LinPlan plan_tile(int64_t M, int64_t L, int64_t F, int64_t N, bool gated, int src) {
     static constexpr int kHeights[4] = {1, 2, 4, 8};
-    static constexpr double kAlone[2][4] = {{0.60, 0.71, 1.00, 1.55}, {0.38, 0.51, 0.80, 1.43}};
-    static constexpr double kPaired[2][2] = {{0.97, 1.26}, {0.74, 0.97}};
-    static constexpr double kFixed[4] = {7.0, 9.0, 14.0, 15.0};
+    static constexpr double kAlone[3][4] = {{0.62, 0.75, 1.00, 1.55}, {0.38, 0.51, 0.80, 1.43}, {0.83, 0.85, 1.09, 1.75}};
+    static constexpr double kPaired[3][2] = {{0.96, 1.27}, {0.74, 0.97}, {1.09, 1.35}};
+    static constexpr double kFixed[4] = {6.0, 8.0, 13.0, 15.0};
     const int64_t tn = ceil_div(F, gated ? 128 : 256), pairs = ceil_div(L, 2 * kStep);
     LinPlan best = {};
-    double least = 0.0;
     for (int h = 0; h < 4; ++h) {
         const int64_t tm = ceil_div(M, 32 * kHeights[h]);
         for (int64_t want = 1; want <= 16 && want <= pairs; ++want) {
@@ -1020,18 +1135,18 @@ LinPlan plan_tile(int64_t M, int64_t L, int64_t F, int64_t N, bool gated, bool f
             const double sums = (double)slices * (double)M * (double)N;
             if (slices > 1 && sums * sizeof(float) > (double)((int64_t)1 << 30)) break;
             const int64_t groups = tm * tn * slices;
-            const double steps = 2.0 * (double)per, alone = kFixed[h] + steps * kAlone[frag][h];
+            const double steps = 2.0 * (double)per, alone = kFixed[h] + steps * kAlone[src][h];
             double t;
             if (h < 2) {
-                const double paired = kFixed[h] + steps * kPaired[frag][h];
+                const double paired = kFixed[h] + steps * kPaired[src][h];
                 const int64_t rest = groups % 512;
                 t = (double)(groups / 512) * paired + (rest > 256 ? paired : rest > 0 ? alone : 0.0);
             } else {
                 t = (double)ceil_div(groups, 256) * alone;
             }
             if (slices > 1) t += 4.0 + sums * 8.0 / 4.0e6;
-            if (best.mt == 0 || t < least) {
-                least = t;
+            if (best.mt == 0 || t < best.us) {
+                best.us = t;
                 best.mt = kHeights[h];
                 best.tiles_n = tn;
                 best.tiles_m = tm;
@@ -1046,38 +1161,44 @@ LinPlan plan_tile(int64_t M, int64_t L, int64_t F, int64_t N, bool gated, bool f
     if (best.mt == 8 && best.slices == 1 && best.tiles_m * best.tiles_n > 256 && best.tiles_m <= 256) {
         const int64_t whole = best.tiles_m * best.tiles_n / 256 * 256 / best.tiles_m;  // columns of the whole rounds
         const int64_t last = best.tiles_n - whole;
-        if (last > 0 && last * ceil_div(M, 128) <= 256) best.last_tiles_n = last;
+        if (last > 0 && last * ceil_div(M, 128) <= 256) {
+            best.last_tiles_n = last;
+            best.us -= (kFixed[3] - kFixed[2]) + 2.0 * (double)pairs * (kAlone[src][3] - kAlone[src][2]);
+        }
     }
     return best;
 }
 
-template <bool FRAG, int EPI>
+// What decoding the weights before costs, in us: 2.56 bytes a weight at 4.4 TB/s, and a launch.
+double decode_us(int64_t N, int64_t K) { return 3.0 + (double)N * (double)K * (2.5625 / 4.4e6); }
+
+template <int SRC, int EPI>
 hipError_t tile_launch_height(const LinArgs &p, int mt, int64_t slices, hipStream_t st) {
     const dim3 grid((unsigned)(p.tiles * slices)), block(kTileThreads);
-    if constexpr (FRAG && EPI != kEpiPlain) {  // the forward with weights decoded first: tall tiles alone
+    if constexpr (SRC == kSrcFrag && EPI != kEpiPlain) {  // the forward of many rows: tall tiles alone
         if (mt == 4)
-            hipLaunchKernelGGL((k_lin_tile<4, FRAG, EPI>), grid, block, 0, st, p);
+            hipLaunchKernelGGL((k_lin_tile<4, SRC, EPI>), grid, block, 0, st, p);
         else if (mt == 8)
-            hipLaunchKernelGGL((k_lin_tile<8, FRAG, EPI>), grid, block, 0, st, p);
+            hipLaunchKernelGGL((k_lin_tile<8, SRC, EPI>), grid, block, 0, st, p);
         else
             return hipErrorInvalidValue;
     } else {
         switch (mt) {
-            case 1: hipLaunchKernelGGL((k_lin_tile<1, FRAG, EPI>), grid, block, 0, st, p); break;
-            case 2: hipLaunchKernelGGL((k_lin_tile<2, FRAG, EPI>), grid, block, 0, st, p); break;
-            case 4: hipLaunchKernelGGL((k_lin_tile<4, FRAG, EPI>), grid, block, 0, st, p); break;
-            default: hipLaunchKernelGGL((k_lin_tile<8, FRAG, EPI>), grid, block, 0, st, p); break;
+            case 1: hipLaunchKernelGGL((k_lin_tile<1, SRC, EPI>), grid, block, 0, st, p); break;
+            case 2: hipLaunchKernelGGL((k_lin_tile<2, SRC, EPI>), grid, block, 0, st, p); break;
+            case 4: hipLaunchKernelGGL((k_lin_tile<4, SRC, EPI>), grid, block, 0, st, p); break;
+            default: hipLaunchKernelGGL((k_lin_tile<8, SRC, EPI>), grid, block, 0, st, p); break;
         }
     }
     return hipGetLastError();
 }
 
-template <bool FRAG, int EPI>
+template <int SRC, int EPI>
 hipError_t tile_launch_as(LinArgs p, const LinPlan &plan, hipStream_t st) {
     auto columns = [&](int mt, int64_t first, int64_t count) {
         const int64_t tm = ceil_div(p.M, 32 * mt);
         p.tn0 = first, p.tiles_n = (unsigned)count, p.tiles_m = (unsigned)tm, p.tiles = (unsigned)(tm * count);
-        return tile_launch_height<FRAG, EPI>(p, mt, plan.slices, st);
+        return tile_launch_height<SRC, EPI>(p, mt, plan.slices, st);
     };
     if (plan.last_tiles_n > 0) {
         const hipError_t err = columns(8, 0, plan.tiles_n - plan.last_tiles_n);
@@ -1096,13 +1217,15 @@ hipError_t tile_launch_as(LinArgs p, const LinPlan &plan, hipStream_t st) {
     return err;
 }
 
-template <bool FRAG>
+template <int SRC>
 hipError_t tile_launch(LinArgs p, const LinPlan &plan, hipStream_t st) {
     p.kslice = plan.kslice;
-    if (p.gated) return tile_launch_as<FRAG, kEpiGated>(p, plan, st);
-    if (p.bias || p.res || p.act != kActNone || p.keep != kKeepNone || p.y_f32)
-        return tile_launch_as<FRAG, kEpiFull>(p, plan, st);
-    return tile_launch_as<FRAG, kEpiPlain>(p, plan, st);
+    if constexpr (SRC != kSrcTurn) {
+        if (p.gated) return tile_launch_as<SRC, kEpiGated>(p, plan, st);
+        if (p.bias || p.res || p.act != kActNone || p.keep != kKeepNone || p.y_f32)
+            return tile_launch_as<SRC, kEpiFull>(p, plan, st);
+    }
+    return tile_launch_as<SRC, kEpiPlain>(p, plan, st);
 }
 
 template <int NT, int WAVES>
@@ -1149,14 +1272,20 @@ hipError_t skinny_launch(const LinArgs &p, void *ws, hipStream_t st) {
 
 struct GradPlan {
     LinPlan tile;
+    bool turn;  // the weights turned in the product, not decoded before
     int64_t chunk, chunks;
     size_t wt_bytes, sum_bytes;
 };
 
 GradPlan plan_grad(int64_t M, int64_t K, int64_t N, int64_t F, bool bias) {
     GradPlan g = {};
-    g.tile = plan_tile(M, N, K, K, false, true);
-    g.wt_bytes = align256((size_t)(ceil_div(K, 32) * ceil_div(N, kStep)) * 4096);
+    g.tile = plan_tile(M, N, K, K, false, kSrcFrag);
+    if (K >= 64) {  // kSrcTurn's reads of 64 columns' scales
+        const LinPlan turned = plan_tile(M, N, K, K, false, kSrcTurn);
+        g.turn = turned.us < g.tile.us + decode_us(N, K);
+        if (g.turn) g.tile = turned;
+    }
+    g.wt_bytes = g.turn ? 0 : align256((size_t)(ceil_div(K, 32) * ceil_div(N, kStep)) * 4096);
     g.chunk = std::max<int64_t>(bias ? 16 : 4, ceil_div(M * ceil_div(F, 512), 2048));
     g.chunk = std::max(g.chunk, ceil_div(M, 65535));
     g.chunks = ceil_div(M, g.chunk);
@@ -1166,10 +1295,6 @@ GradPlan plan_grad(int64_t M, int64_t K, int64_t N, int64_t F, bool bias) {
 
 }  // namespace
 
-// Decoding the weights first costs 2.56 bytes of traffic per weight and saves 0.27 us per step and tile: it pays from
-// about 2300 rows of X (4096 x 4096 weights: see the figures at the plan's test of M).
-constexpr int64_t kDecodeFirstRows = 2560;
-
 LinPlan plan_linear(int64_t M, int64_t K, int64_t N, bool x_mx, bool gated, int keep) {
     if (M <= kSkinnyMaxM && keep != kKeepMx) {  // mt = 0: the skinny kernel
         LinPlan p = {};
@@ -1177,10 +1302,16 @@ LinPlan plan_linear(int64_t M, int64_t K, int64_t N, bool x_mx, bool gated, int 
         if (M > kDirectRows) p.frag_bytes = (size_t)(ceil_div(K, kChunk) * ceil_div(M, 16)) * 4096;
         return p;
     }
-    LinPlan p = plan_tile(M, K, gated ? N / 2 : N, N, gated, false);
+    const int64_t F = gated ? N / 2 : N;
+    LinPlan p = plan_tile(M, K, F, N, gated, kSrcCodes);
+    if (M > 1024) {  // the decoding is paid back by many tiles of rows (4096 x 4096 weights: from about 2300 rows) or not at all
+        const LinPlan q = plan_tile(M, K, F, N, gated, kSrcFrag);
+        if (q.mt >= 4 && q.slices == 1 && q.us + decode_us(N, K) < p.us) {
+            p = q;
+            p.frag_bytes = (size_t)(ceil_div(F, 32) * (gated ? 2 : 1) * ceil_div(K, kStep)) * 4096;
+        }
+    }
     if (x_mx) p.x_bytes = align256((size_t)(M * K) * 2);
-    if (M >= kDecodeFirstRows && p.mt == 8 && p.slices == 1)
-        p.frag_bytes = (size_t)(ceil_div(gated ? N / 2 : N, 32) * (gated ? 2 : 1) * ceil_div(K, kStep)) * 4096;
     return p;
 }
 
@@ -1203,10 +1334,10 @@ hipError_t launch_linear(const LinArgs &args, void *ws, hipStream_t stream) {
         hipLaunchKernelGGL(k_lin_decode, grid, dim3(256), 0, stream, p.codes, p.scales, p.F, p.L, reinterpret_cast<uint16_t *>(base));
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
-        return tile_launch<true>(p, plan, stream);
+        return tile_launch<kSrcFrag>(p, plan, stream);
     }
     p.part = plan.slices > 1 ? reinterpret_cast<float *>(base) : nullptr;
-    return tile_launch<false>(p, plan, stream);
+    return tile_launch<kSrcCodes>(p, plan, stream);
 }
 
 size_t linear_grad_workspace(int64_t M, int64_t K, int64_t N, int64_t F, bool bias) {
@@ -1234,19 +1365,21 @@ hipError_t launch_linear_grad(const LinGradArgs &g, const uint8_t *codes, const 
         if (err == hipSuccess && dbias) err = launch_column_sum(sums, plan.chunks, g.N, dbias, stream);
     }
     if (err != hipSuccess) return err;
-    const dim3 grid((unsigned)ceil_div(K, 256), (unsigned)ceil_div(g.N, kStep));
-    hipLaunchKernelGGL(k_lin_transpose, grid, dim3(256), 0, stream, codes, scales, g.N, K, wt);
-    err = hipGetLastError();
-    if (err != hipSuccess) return err;
+    if (!plan.turn) {
+        const dim3 grid((unsigned)ceil_div(K, 256), (unsigned)ceil_div(g.N, kStep));
+        hipLaunchKernelGGL(k_lin_transpose, grid, dim3(256), 0, stream, codes, scales, g.N, K, wt);
+        err = hipGetLastError();
+        if (err != hipSuccess) return err;
+    }
     LinArgs p = {};
     p.x = g.act == kActNone ? g.dy : g.dz;
     p.ldx = g.act == kActNone ? g.lddy : g.N;
     p.M = g.M, p.L = g.N, p.N = K, p.F = K;
     p.alpha = alpha;
     p.y = dx;
-    p.wt = wt;
+    p.wt = wt, p.codes = codes, p.scales = scales;
     p.part = plan.tile.slices > 1 ? part : nullptr;
-    return tile_launch<true>(p, plan.tile, stream);
+    return plan.turn ? tile_launch<kSrcTurn>(p, plan.tile, stream) : tile_launch<kSrcFrag>(p, plan.tile, stream);
 }
 
 }  // namespace nvfp4

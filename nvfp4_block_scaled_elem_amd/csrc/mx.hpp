@@ -25,6 +25,7 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef u32x4 u32x4_any __attribute__((aligned(1)));
 typedef u32x2 u32x2_any __attribute__((aligned(1)));
 typedef uint16_t u16_any __attribute__((aligned(1)));
+typedef uint32_t u32_any __attribute__((aligned(1)));
 
 __device__ __forceinline__ uint4 load16(const void *p) {
     const u32x4 v = *static_cast<const u32x4_any *>(p);
@@ -34,6 +35,7 @@ __device__ __forceinline__ uint2 load8b(const void *p) {
     const u32x2 v = *static_cast<const u32x2_any *>(p);
     return make_uint2(v.x, v.y);
 }
+__device__ __forceinline__ uint32_t load4(const void *p) { return *static_cast<const u32_any *>(p); }
 __device__ __forceinline__ uint32_t load2b(const void *p) { return *static_cast<const u16_any *>(p); }
 __device__ __forceinline__ void store16(void *p, uint4 v) {
     *static_cast<u32x4_any *>(p) = u32x4{v.x, v.y, v.z, v.w};

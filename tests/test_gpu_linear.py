@@ -359,7 +359,7 @@ def test_refusals():
         lambda: nv.linear_grad(dy, *W, Z=z[:3], activation="silu"),
         lambda: nv.linear_grad(dy, *W, Z=z, activation="silu", gated=True),
         lambda: nv.linear_grad(dy, *W, Z=z.float(), activation="silu"),
-        lambda: nv.linear_grad(dy, *W, workspace=torch.empty(256, dtype=torch.uint8, device="cuda")),
+        lambda: nv.linear_grad(dy, *W, bias=True, workspace=torch.empty(16, dtype=torch.uint8, device="cuda")),
         lambda: nv.linear(rand(1, 100, 96), *make_weights(64, 96), keep="mxfp8", activation="silu",
                           workspace=torch.empty(0, dtype=torch.uint8)),
     ]

@@ -114,7 +114,7 @@ WITH_Z = dict(activation=1, z=FAKE, ldz=64, dz=FAKE)
     (dict(WITH_Z, z_dtype=2), INVALID), (dict(WITH_Z, z=FAKE + 1), INVALID), (dict(gated=1), INVALID),
     (dict(WITH_Z, gated=1, N=96, z_dtype=2, z_scales=FAKE), SHAPE), (dict(WITH_Z, gated=1, N=63), SHAPE),
     (dict(dbias=FAKE + 2), INVALID), (dict(workspace=FAKE + 16), INVALID), (dict(dy=FAKE + 1), INVALID),
-    (dict(lddy=1 << 23), SHAPE), (dict(codes=FAKE + 4), INVALID), (dict(), WORKSPACE), (dict(WITH_Z), WORKSPACE), (dict(M=0), OK),
+    (dict(lddy=1 << 23), SHAPE), (dict(codes=FAKE + 4), INVALID), (dict(K=48), WORKSPACE), (dict(WITH_Z, K=48), WORKSPACE), (dict(M=0), OK),
 ])
 def test_linear_grad_rejects(L, kw, err):
     assert L.nvfp4_linear_grad(ctypes.byref(grad_args(**kw))) == err
