@@ -773,7 +773,9 @@ __global__ __launch_bounds__(256) void k_lin_xfrag(LinArgs p, uint16_t *__restri
 // MT: tiles of 16 rows of X; NT: 2 if gated. XF: X in fragment order (p.wt's place in LinArgs holds it), else direct,
 // MT = 1.
 template <int MT, int NT, bool XF, bool XMX, int WAVES>
-__global__ __launch_bounds__(64 * WAVES) void k_lin_skinny(LinArgs p) {
+__global__ __launch_bounds__(64 * WAVES)
+__attribute__((amdgpu_waves_per_eu(NT * MT <= 4 ? 4 : 1)))  // 128 registers where the accumulators leave room
+void k_lin_skinny(LinArgs p) {
     // each wave's chunk of codes and scales; afterwards each wave's sums
     constexpr int kStage = WAVES * NT * kChunkLds, kSums = WAVES * MT * 1024;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kStage > kSums ? kStage : kSums];
@@ -879,8 +881,8 @@ __global__ __launch_bounds__(64 * WAVES) void k_lin_skinny(LinArgs p) {
             const uint8_t *const q = wl + j * kChunkLds;
             const uint4 cur = *reinterpret_cast<const uint4 *>(q + w_place(r16, g));
             const uint32_t sb = *reinterpret_cast<const uint16_t *>(q + 1024 + 8 * r16 + 2 * g);
-            const float d0 = e4m3_value(sb & 0x7Fu), d1 = e4m3_value((sb >> 8) & 0x7Fu);
-            const uint4 w[4] = {dequant8(cur.x, d0), dequant8(cur.y, d0), dequant8(cur.z, d1), dequant8(cur.w, d1)};
+            const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8((int)(sb & 0x7F7Fu), false);  // both scales
+            const uint4 w[4] = {dequant8(cur.x, d.x), dequant8(cur.y, d.x), dequant8(cur.z, d.y), dequant8(cur.w, d.y)};
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll

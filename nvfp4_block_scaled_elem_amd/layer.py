@@ -193,11 +193,11 @@ def rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *, residu
             Y = _new_mx(rows, cols, dev)
             y, ys, yt = Y[0].data_ptr(), Y[1].data_ptr(), _MX
         else:
-            Y = torch.empty(X.shape, dtype=out_dtype, device=dev)
+            Y = torch.empty_like(X, dtype=out_dtype, memory_format=torch.contiguous_format)
             y, ys, yt = Y.data_ptr(), None, DTYPES[out_dtype]
         h = sum_out
         if residual is not None and h is None:
-            h = torch.empty(X.shape, dtype=X.dtype, device=dev)
+            h = torch.empty_like(X, memory_format=torch.contiguous_format)
         _check(lib().nvfp4_rms_norm(X.data_ptr(), ldx, _ptr(residual), ldr, weight.data_ptr(), DTYPES[X.dtype],
                                     DTYPES[weight.dtype], rows, cols, eps, _ptr(h), y, ys, yt, st))
         return Y if residual is None else (Y, h)
@@ -227,7 +227,7 @@ def rms_norm_grad(dY: torch.Tensor, S, weight: torch.Tensor, eps: float = 1e-6, 
     ldds = 0 if dS is None else _rows(dS, "dS", (dY.dtype,), dev, (rows, cols))
 
     def call(st):
-        dX = torch.empty((rows, cols), dtype=dY.dtype, device=dev)
+        dX = torch.empty_like(dY, memory_format=torch.contiguous_format)
         dw = torch.empty(cols, dtype=torch.float32, device=dev)
         ws, nbytes = _space(workspace, rms_norm_grad_workspace_bytes(rows, cols), dev)
         _check(lib().nvfp4_rms_norm_grad(dY.data_ptr(), lddy, h.data_ptr(), ldh, _ptr(hs), ht, weight.data_ptr(),
@@ -242,7 +242,12 @@ def _weights(codes, scales, alpha, dev, K=None):
     """Checks NVFP4 weights as ``quantize`` returns them; returns (N, K)."""
     if codes.dim() != 2 or (K is not None and 2 * codes.shape[1] != K) or codes.shape[1] % 8:
         raise NVFP4Error("codes must be [N, K/2] with K % 16 == 0")
-    N, K = codes.shape[0], 2 * codes.shape[1]
+    N, half = codes.shape
+    K = 2 * half
+    if (codes.device == scales.device == alpha.device == dev and codes.dtype == scales.dtype == torch.uint8
+            and alpha.dtype == torch.float32 and scales.numel() >= N * half // 8 and alpha.numel() >= 1
+            and codes.is_contiguous() and scales.is_contiguous() and alpha.is_contiguous()):
+        return N, K
     _check_buffer(codes, "codes", N * K // 2, dev, torch.uint8)
     _check_buffer(scales, "scales", N * K // 16, dev, torch.uint8)
     _check_buffer(alpha, "alpha", 4, dev, torch.float32)
