@@ -116,6 +116,38 @@ def test_gated_linear_matches_binary64(m, n, k, act):
             check(got, y, ey)
 
 
+MANY = [(9000, 4352, 2064), (12300, 4352, 1040)]  # weights decoded first; more than a round of tall tiles
+
+
+@pytest.mark.parametrize("m,n,k", MANY)
+def test_many_rows(m, n, k):
+    """The forms for many rows of X (the weights decoded before the product, the last columns of tiles at half the
+    height), forward plain, with every extra and gated, and the gradient; each output against binary64."""
+    W = make_weights(n, k)
+    Wv, alpha = ref.weights(*W[:2]), float(W[2])
+    X = rand(1, m, k)
+    assert nv.linear_workspace_bytes(m, k, n) >= 2 * n * k  # decoded weights
+    say(f"many M={m} N={n} K={k}")
+    y, z, ey, ez = ref.linear(X.double(), *W)
+    check(nv.linear(X, *W), y, ey)
+    bias, res = rand(2, n), rand(3, m, n)
+    y, z, ey, ez = ref.linear(X.double(), *W, bias=bias, act="gelu", res=res)
+    got, Z = nv.linear(X, *W, bias=bias, activation="gelu", residual=res, keep="mxfp8")
+    check(got, y, ey)
+    check_kept(Z, z, ez)
+    del y, z, ey, ez, got, Z
+    x8 = nv.quantize_mxfp8(X)
+    y, z, ey, ez = ref.linear(ref.value(x8), *W, act="silu", gated=True)
+    got, Z = nv.linear(x8, *W, activation="silu", gated=True, keep=BF16)
+    check(got, y, ey)
+    check(Z, z, ez)
+    del y, z, ey, ez, got, Z
+    dy = rand(4, m, n)
+    dX, _, db = nv.linear_grad(dy, *W, bias=True)
+    check(dX, alpha * (dy.double() @ Wv), ref.product_error(dy.double(), Wv.T, alpha, n))
+    assert ((db.double() - dy.double().sum(0)).abs() <= (m + 8) * ref.U * dy.double().abs().sum(0)).all()
+
+
 @pytest.mark.parametrize("n,k", [(96, 64), (200, 176), (256, 512), (300, 1040)])
 def test_one_hot_rows_are_exact(n, k):
     """X = I, repeated: each output is one weight times alpha, rounded once."""
@@ -335,6 +367,58 @@ def test_layer_on_streams_and_in_graphs():
                 assert all(torch.equal(a, b) for a, b in zip(h, eager))
                 layer(x, r, wn, W1, W2, dy)  # eager work between replays
         torch.cuda.synchronize()
+
+
+def test_many_rows_in_graphs():
+    """Captured calls of the tall tiles, the decoding before them and the split sums give the eager results on every
+    replay."""
+    for m, n, k in ((2600, 4352, 1040), (12300, 4352, 1040), (700, 512, 2048)):
+        W = make_weights(n, k)
+        x, dy = rand(1, m, k), rand(2, m, n)
+        work = lambda: (nv.linear(x, *W), nv.linear_grad(dy, *W)[0])  # noqa: E731
+        eager = work()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held = work()
+        for _ in range(3):
+            for t in held:
+                t.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(held, eager))
+            work()
+        torch.cuda.synchronize()
+
+
+def test_offsets_past_32_bits():
+    """X, Y, dY and dX of more than 2^31 values: the last rows equal those of a call of their own."""
+    m, k, n = 525_000, 4112, 48
+    W = make_weights(n, k)
+    x = torch.zeros(m, k, dtype=BF16, device="cuda")
+    x[-300:] = rand(1, 300, k)
+    assert x.numel() > 2 ** 31
+    y = nv.linear(x, *W)
+    want, _, ey, _ = ref.linear(x[-300:].double(), *W)
+    check(y[-300:], want, ey)
+    assert (y[:-300] == 0).all()
+    dy = torch.zeros(m, n, dtype=BF16, device="cuda")
+    dy[-300:] = rand(2, 300, n)
+    dX, _, _ = nv.linear_grad(dy, *W)
+    Wv, alpha = ref.weights(*W[:2]), float(W[2])
+    d = dy[-300:].double()
+    check(dX[-300:], alpha * (d @ Wv), ref.product_error(d, Wv.T, alpha, n))
+    del dX, y, dy
+    s8 = nv.quantize_mxfp8(x)
+    q, b = ref.mx_quantize(x[-300:].double())
+    assert torch.equal(s8[0][-300:].double(), q) and torch.equal(u8(s8[1])[-300:], b)
+    h, s = nv.rms_norm(x, torch.ones(k, device="cuda"), 1e-3, residual=x, out_dtype="mxfp8")
+    h1, s1 = nv.rms_norm(x[-300:], torch.ones(k, device="cuda"), 1e-3, residual=x[-300:], out_dtype="mxfp8")
+    assert torch.equal(s[-300:], s1) and torch.equal(u8(h[0])[-300:], u8(h1[0])) and torch.equal(u8(h[1])[-300:], u8(h1[1]))
+    del h, s
+    dx, dw = nv.rms_norm_grad(x, s8, torch.ones(k, device="cuda"), 1e-3)
+    dx1, dw1 = nv.rms_norm_grad(x[-300:], (s8[0][-300:], s8[1][-300:]), torch.ones(k, device="cuda"), 1e-3)
+    assert torch.equal(dx[-300:], dx1) and torch.allclose(dw, dw1, rtol=1e-4, atol=1e-4)
 
 
 def test_refusals():
