@@ -254,9 +254,10 @@ __device__ __forceinline__ void x_load(XStage<MT> &S, const XAddr<MT> &q, int64_
     }
 }
 
-// LDS rows are 64 bf16 in eight 16-byte chunks, chunk c of row r at position c ^ (r % 8): the 32 rows that a
-// wave reads at one c then cover all banks.
-__device__ __forceinline__ int x_place(int row, int chunk) { return row * kStep + ((chunk ^ (row & 7)) << 3); }
+// LDS rows are 64 bf16 in eight 16-byte chunks, chunk c of row r at position c ^ (r / 2 % 8). Two rows span the 64
+// banks; the 16 lanes that read one c of 16 rows at once then meet no bank twice (with r % 8 there were two rows
+// to a bank and four more cycles a read; LDS does not bound the kernel: 1 % of its time).
+__device__ __forceinline__ int x_place(int row, int chunk) { return row * kStep + ((chunk ^ ((row >> 1) & 7)) << 3); }
 
 template <int MT>
 __device__ __forceinline__ void x_store(const XStage<MT> &S, uint16_t *xs, int tid) {
@@ -287,7 +288,7 @@ __device__ __forceinline__ int w_place(int r, int q) { return r * 64 + ((q ^ ((r
 // Where the weights come from.
 //   kSrcCodes: as stored, the sum running along their rows (the forward).
 //   kSrcFrag: decoded beforehand, in the order of the fragments (k_lin_decode, k_lin_transpose): coalesced and
-//     without the decoding, a step of a 256 x 256 tile takes 1.43 us instead of 1.55.
+//     without the decoding, a step of a 256 x 256 tile takes 1.47 us instead of 1.66.
 //   kSrcTurn: as stored, the sum running along their columns (the gradient): a wave decodes its 64 columns of 64
 //     weight rows, pairs the values along the sum, and turns them into fragments in LDS. What a decoding pass
 //     before would write and read again (four bytes a weight) is saved; the work is repeated for every tile of
@@ -618,9 +619,9 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
 
     // The sums go through LDS, kTpr tiles of 32 rows by 256 weight rows at a time, so that the epilogue works on
     // whole rows: a thread takes eight consecutive output columns, a row's threads are consecutive. 16-byte
-    // chunk c of row r sits at c ^ (r % 8).
+    // chunk c of row r sits at c ^ (r % 16).
     float *const es = reinterpret_cast<float *>(lds);
-    auto place = [](int row, int chunk) { return row * 256 + ((chunk ^ (row & 7)) << 2); };
+    auto place = [](int row, int chunk) { return row * 256 + ((chunk ^ (row & 15)) << 2); };
     const float alpha = p.part ? 1.0f : *p.alpha;
     constexpr int cols = kGated ? 128 : 256, threads = cols / 8;  // output columns of the work-group; threads per row
     constexpr int stride = kTileThreads / threads;  // a thread's rows are so far apart
@@ -690,7 +691,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
 #pragma unroll
                 for (int t = 0; t < kTpr; ++t) dump(t, acc[0][r * kTpr + t], acc[1][r * kTpr + t]);
         lds_barrier();
-        if (p.F % 8 == 0)
+        if (p.F % 8 == 0 || (tn + 1) * cols <= p.F)  // no column group of the tile ends inside the eight
             rows_out(std::true_type{}, round);
         else
             rows_out(std::false_type{}, round);
@@ -1117,14 +1118,14 @@ size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 // that these measurements add up to (us on an MI355X). A step of 64 k costs, with one work-group per CU and with
 // two (heights 1 and 2; the taller take a CU each), by where the weights come from:
 //   height (of 32 rows)   1            2            4      8
-//   as stored             0.62 / 0.96  0.75 / 1.27  1.00   1.55
-//   decoded before        0.38 / 0.74  0.51 / 0.97  0.80   1.43
-//   turned                0.83 / 1.09  0.85 / 1.35  1.09   1.75
+//   as stored             0.62 / 0.96  0.75 / 1.27  1.00   1.66
+//   decoded before        0.38 / 0.74  0.51 / 0.97  0.80   1.47
+//   turned                0.83 / 1.09  0.85 / 1.35  1.09   1.78
 // on top of 6, 8, 13 and 15 per work-group (launch, first loads, epilogue), and slices of K cost 4 and 8 bytes per
 // sum at 4 TB/s.
 LinPlan plan_tile(int64_t M, int64_t L, int64_t F, int64_t N, bool gated, int src) {
     static constexpr int kHeights[4] = {1, 2, 4, 8};
-    static constexpr double kAlone[3][4] = {{0.62, 0.75, 1.00, 1.55}, {0.38, 0.51, 0.80, 1.43}, {0.83, 0.85, 1.09, 1.75}};
+    static constexpr double kAlone[3][4] = {{0.62, 0.75, 1.00, 1.66}, {0.38, 0.51, 0.80, 1.47}, {0.83, 0.85, 1.09, 1.78}};
     static constexpr double kPaired[3][2] = {{0.96, 1.27}, {0.74, 0.97}, {1.09, 1.35}};
     static constexpr double kFixed[4] = {6.0, 8.0, 13.0, 15.0};
     const int64_t tn = ceil_div(F, gated ? 128 : 256), pairs = ceil_div(L, 2 * kStep);
@@ -1159,7 +1160,7 @@ LinPlan plan_tile(int64_t M, int64_t L, int64_t F, int64_t N, bool gated, int sr
         }
     }
     // The last round of the tallest tiles, if it has too few of them: its columns in tiles of half the height, which
-    // take 65 us where a round of the tallest takes 107 (K = 4096).
+    // take 64 us where a round of the tallest takes 109 (decoded, K = 4096).
     if (best.mt == 8 && best.slices == 1 && best.tiles_m * best.tiles_n > 256 && best.tiles_m <= 256) {
         const int64_t whole = best.tiles_m * best.tiles_n / 256 * 256 / best.tiles_m;  // columns of the whole rounds
         const int64_t last = best.tiles_n - whole;
