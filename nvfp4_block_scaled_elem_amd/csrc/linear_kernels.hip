@@ -382,7 +382,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
                 D.c[j] = *reinterpret_cast<const uint4 *>(wl + w_place(32 * j + r32, 2 * odd + half));
-                D.s[j] = *reinterpret_cast<const uint16_t *>(wl + kWaveCodes + 8 * (32 * j + r32) + 4 * odd + 2 * half);
+                D.s[j] = *reinterpret_cast<const u16_lds *>(wl + kWaveCodes + 8 * (32 * j + r32) + 4 * odd + 2 * half);
             }
     };
     auto frag_load = [&](Weights &D, int64_t k0) __attribute__((always_inline)) {
@@ -881,7 +881,7 @@ void k_lin_skinny(LinArgs p) {
         for (int j = 0; j < NT; ++j) {
             const uint8_t *const q = wl + j * kChunkLds;
             const uint4 cur = *reinterpret_cast<const uint4 *>(q + w_place(r16, g));
-            const uint32_t sb = *reinterpret_cast<const uint16_t *>(q + 1024 + 8 * r16 + 2 * g);
+            const uint32_t sb = *reinterpret_cast<const u16_lds *>(q + 1024 + 8 * r16 + 2 * g);
             const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8((int)(sb & 0x7F7Fu), false);  // both scales
             const uint4 w[4] = {dequant8(cur.x, d.x), dequant8(cur.y, d.x), dequant8(cur.z, d.y), dequant8(cur.w, d.y)};
 #pragma unroll

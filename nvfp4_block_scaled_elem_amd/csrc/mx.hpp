@@ -22,10 +22,11 @@ constexpr int kMxBlock = 32;
 // of odd length costs masks at its end only.
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef u32x4 u32x4_any __attribute__((aligned(1)));
-typedef u32x2 u32x2_any __attribute__((aligned(1)));
-typedef uint16_t u16_any __attribute__((aligned(1)));
-typedef uint32_t u32_any __attribute__((aligned(1)));
+typedef u32x4 u32x4_any __attribute__((aligned(1), may_alias));
+typedef u32x2 u32x2_any __attribute__((aligned(1), may_alias));
+typedef uint16_t u16_any __attribute__((aligned(1), may_alias));
+typedef uint32_t u32_any __attribute__((aligned(1), may_alias));
+typedef uint16_t u16_lds __attribute__((may_alias));  // two scale bytes of those that a wave has stored in LDS as dwords
 
 __device__ __forceinline__ uint4 load16(const void *p) {
     const u32x4 v = *static_cast<const u32x4_any *>(p);
