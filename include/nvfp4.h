@@ -300,10 +300,12 @@ size_t nvfp4_gptq_workspace_bytes(int64_t rows, int64_t cols);
  * next (>= its columns; not looked at for fewer than two rows), the outputs are contiguous. Pointers are
  * aligned to their element; rows need no more alignment than that (16-byte aligned rows are fastest). rows = 0
  * is allowed: nothing is written but the column sums (dweight, dbias), which are zeros. rows <= 2^23 and
- * rows * columns < 2^35 (else NVFP4_ERR_SHAPE). Outputs may not overlap inputs unless a call says so. Sums
+ * rows * columns < 2^35 for every operand, weights among them (else NVFP4_ERR_SHAPE). Outputs may not overlap inputs unless a call says so. Sums
  * and statistics are binary32, in an order that does not depend on timing; each output is rounded once.
  * Nothing is allocated when `workspace` (256-byte aligned) is given or none is needed; without it scratch
- * is taken from a stream-ordered pool, except on a capturing stream (NVFP4_ERR_UNSUPPORTED).
+ * is taken from a stream-ordered pool, except on a capturing stream (NVFP4_ERR_UNSUPPORTED). A call writes what
+ * it reads of its workspace, so calls and captured graphs may share one if they run one after the other; calls
+ * or replays that may overlap need one each.
  *
  * MXFP8 ([rows][cols] code bytes and [rows][ceil(cols/32)] scale bytes): blocks of 32 consecutive columns
  * (the last may be shorter); a code is E4M3, a scale byte b is 2^(b-127) (E8M0), and a value is their
@@ -323,7 +325,9 @@ int nvfp4_mxfp8_dequantize(const uint8_t *codes, int64_t ldc, const uint8_t *sca
  * weight over each row of cols >= 1 columns. x, residual and sum_out have `dtype` (bf16 or fp32), weight [cols]
  * has weight_dtype. sum_out gets h rounded to dtype (y is computed from h unrounded) and may be `residual`
  * itself (contiguous); residual and sum_out are both given or both NULL (then h = x). y is bf16, fp32 or
- * MXFP8 (y_dtype; y_scales for MXFP8 alone, else NULL). eps >= 0. */
+ * MXFP8 (y_dtype; y_scales for MXFP8 alone, else NULL). eps >= 0. Squares are binary32: where a row's sum of them
+ * overflows (|h| from 1.8e19 on), y is 0 (and the gradient's dx may be NaN), and where it vanishes beside eps = 0,
+ * y is not finite. */
 int nvfp4_rms_norm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight, int dtype,
                    int weight_dtype, int64_t rows, int64_t cols, float eps, void *sum_out, void *y,
                    uint8_t *y_scales, int y_dtype, void *stream);

@@ -142,14 +142,16 @@ namespace {
 constexpr int64_t kMaxLd = (int64_t)1 << 23;    // a product's X: 256 rows of it stay below 2^32 bytes
 constexpr int64_t kMaxSide = (int64_t)1 << 21;  // K and N of a product: grids stay below 65536 along y
 
-// The shapes of a product [M][K] x [N][K]^T, gated or not.
+// The shapes of a product [M][K] x [N][K]^T, gated or not. The weights are held to the bound of every operand: the
+// kernels' 32-bit offsets of scale bytes and their grids rest on it.
 int check_product(int64_t M, int64_t K, int64_t N, int activation, int gated) {
     if (M < 0 || K <= 0 || N <= 0) return NVFP4_ERR_INVALID_ARG;
     if (activation < NVFP4_ACT_NONE || activation > NVFP4_ACT_GELU) return NVFP4_ERR_INVALID_ARG;
     if (gated != 0 && (gated != 1 || activation == NVFP4_ACT_NONE)) return NVFP4_ERR_INVALID_ARG;
     if (K % 16 != 0 || (gated && N % 2 != 0) || K > kMaxSide || N > kMaxSide) return NVFP4_ERR_SHAPE;
-    const int c = check_shape(M, K);
-    return c != NVFP4_OK ? c : check_shape(M, N);
+    for (const int c : {check_shape(M, K), check_shape(M, N), check_shape(N, K)})
+        if (c != NVFP4_OK) return c;
+    return NVFP4_OK;
 }
 
 }  // namespace

@@ -277,3 +277,16 @@ def test_refusals():
         with pytest.raises(nv.NVFP4Error):
             call()
             say(f"call {i} was not refused")
+
+
+def test_rms_norm_squares_past_binary32():
+    """The sum of a row's squares overflows: its y is 0, and the rows beside it are what they are alone."""
+    x = rand(12, 3, 1000)
+    x[1] = torch.finfo(BF16).min
+    w, dy = torch.ones(1000, device="cuda"), rand(13, 3, 1000)
+    y = nv.rms_norm(x, w, EPS)
+    assert (y[1] == 0).all()
+    check_y(y[::2], ref.rms_norm(x[::2], w, EPS)[0], 1000)
+    dx, dw = nv.rms_norm_grad(dy, x, w, EPS)
+    alone = nv.rms_norm_grad(dy[:1], x[:1], w, EPS)[0], nv.rms_norm_grad(dy[2:], x[2:], w, EPS)[0]
+    assert torch.equal(dx[:1], alone[0]) and torch.equal(dx[2:], alone[1])

@@ -159,3 +159,13 @@ def test_binding_refuses_cpu_tensors():
                  lambda: nv.dequantize_mxfp8(x.to(torch.float8_e4m3fn), x[:, :2])):
         with pytest.raises(nv.NVFP4Error):
             call()
+
+
+def test_weights_are_bounded(L):
+    """2^35 weights: refused by the products, like any operand of that size."""
+    lin = layer._LinearArgs(x=FAKE, M=1, K=1 << 20, N=1 << 15, codes=FAKE, scales=FAKE, alpha=FAKE, y=FAKE)
+    grad = layer._LinearGradArgs(dy=FAKE, M=1, K=1 << 20, N=1 << 15, codes=FAKE, scales=FAKE, alpha=FAKE, dx=FAKE)
+    assert L.nvfp4_linear(ctypes.byref(lin)) == SHAPE and L.nvfp4_linear_grad(ctypes.byref(grad)) == SHAPE
+    assert L.nvfp4_linear_workspace_bytes(100, 1 << 20, 1 << 15, 0, 0, 0) == 0
+    assert L.nvfp4_linear_workspace_bytes(100, 1 << 20, (1 << 15) - 16, 0, 0, 0) > 0
+    assert L.nvfp4_linear_grad_workspace_bytes(100, 1 << 20, 1 << 15, 0, 0) == 0
