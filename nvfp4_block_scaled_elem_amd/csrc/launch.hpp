@@ -156,9 +156,10 @@ struct LinArgs {
     const void *bias, *res;
     void *y, *z;
     uint8_t *zs;
-    float *part;  // fp32 sums of the K slices, or null
+    float *part;  // fp32 sums of the K slices; null in a launch that does not split K
     int64_t M, L, N, F, ldx, ldr, kslice;
     int64_t tn0;  // first column tile of a launch
+    int64_t part_f0, part_f, part_n;  // the output columns that part holds: first and number; values per row
     unsigned tiles, tiles_m, tiles_n;
     int x_mx, bias_f32, res_f32, y_f32, act, gated, keep;
 };
@@ -170,17 +171,21 @@ struct LinGradArgs {
     int64_t M, N, F, lddy, ldz;
     int z_mx, act, gated;
 };
+// Columns of the tile kernel's tiles that one launch takes.
+struct TileCut {
+    int mt;  // tiles of 32 rows of X per work-group
+    int64_t tiles_n, slices, kslice;
+    double us;  // estimated
+};
 struct LinPlan {
-    int mt;  // tiles of 32 rows of X per work-group; 0: the skinny kernel
-    int64_t tiles_m, tiles_n, slices, kslice;
-    double us;             // estimated
-    int64_t last_tiles_n;  // of the tiles_n columns of tiles (mt 8), the last ones run at half the height
-    size_t part_bytes;  // fp32 sums of the K slices (0: K is not split)
-    size_t x_bytes;     // an MXFP8 X decoded for the tile kernel
-    size_t frag_bytes;  // an operand in fragment order: X for the skinny kernel, the weights for many rows
+    TileCut main, rest;  // rest.mt = 0: all columns in main; main.mt = 0: the skinny kernel
+    double us;           // estimated
+    size_t x_bytes;      // an MXFP8 X decoded for the tile kernel
+    size_t frag_bytes;   // an operand in fragment order: X for the skinny kernel, the weights for many rows
+    size_t part_bytes;   // fp32 sums of the K slices (0: K is not split)
 };
 LinPlan plan_linear(int64_t M, int64_t K, int64_t N, bool x_mx, bool gated, int keep);
-// `ws` holds the plan's x_bytes, then its part_bytes or frag_bytes (never both).
+// `ws` holds the plan's x_bytes, then its frag_bytes, then its part_bytes.
 hipError_t launch_linear(const LinArgs &p, void *ws, hipStream_t stream);
 size_t linear_grad_workspace(int64_t M, int64_t K, int64_t N, int64_t F, bool bias);
 hipError_t launch_linear_grad(const LinGradArgs &g, const uint8_t *codes, const uint8_t *scales, const float *alpha,

@@ -664,9 +664,9 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
             if (p.part) {  // fp32 sums of this slice, without alpha
 #pragma unroll
                 for (int r = 0; r < kRows; ++r) {
-                    float *q = p.part + ((int64_t)slice * p.M + m + r * stride) * p.N + f;
+                    float *q = p.part + ((int64_t)slice * p.M + m + r * stride) * p.part_n + (f - p.part_f0);
                     put<kWholeRow>(q, g[r], n[r]);
-                    if (kGated) put<kWholeRow>(q + p.F, u[r], n[r]);
+                    if (kGated) put<kWholeRow>(q + p.part_f, u[r], n[r]);
                 }
             } else {
                 epilogue<EPI, kWholeRow, kRows>(p, m, stride, f, n, g, u, bg, bu, res, lane);
@@ -708,7 +708,7 @@ __global__ __launch_bounds__(kReduceThreads) void k_lin_reduce(LinArgs p, int sl
     const float alpha = *p.alpha;
     for (int64_t i = (int64_t)blockIdx.x * kReduceThreads + threadIdx.x; i < groups;
          i += (int64_t)gridDim.x * kReduceThreads) {
-        const int64_t m = i / per_row, f = 8 * (i - m * per_row);
+        const int64_t m = i / per_row, fp = 8 * (i - m * per_row), f = p.part_f0 + fp;
         const int n[1] = {clamp_count(p.F - f, 8)};
         RawAny<WHOLE> res[1];
         float g[1][8] = {}, u[1][8] = {}, bg[8], bu[8];
@@ -716,7 +716,7 @@ __global__ __launch_bounds__(kReduceThreads) void k_lin_reduce(LinArgs p, int sl
         load_bias<EPI, WHOLE>(p, f, n[0], bg, bu);
 #pragma unroll 4
         for (int s = 0; s < slices; ++s) {
-            const float *q = p.part + ((int64_t)s * p.M + m) * p.N + f;
+            const float *q = p.part + ((int64_t)s * p.M + m) * p.part_n + fp;
             RawAny<WHOLE> r;
             float v[8];
             r.load(q, 1, 0, n[0]);
@@ -724,7 +724,7 @@ __global__ __launch_bounds__(kReduceThreads) void k_lin_reduce(LinArgs p, int sl
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[0][e] += v[e];
             if (EPI == kEpiGated) {
-                r.load(q + p.F, 1, 0, n[0]);
+                r.load(q + p.part_f, 1, 0, n[0]);
                 r.get(1, v);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) u[0][e] += v[e];
@@ -964,8 +964,7 @@ __global__ __launch_bounds__(256) void k_lin_decode(const uint8_t *__restrict__ 
                                                   int64_t F, int64_t K, uint16_t *__restrict__ wt) {
     const int lane = threadIdx.x & 63, half = lane >> 5;
     const int64_t ktiles = (F + 31) / 32, steps = (K + kStep - 1) / kStep;
-    const int64_t kt = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6), s0 = (int64_t)blockIdx.y * 4;
-    if (kt >= ktiles) return;
+    const int64_t kt = blockIdx.x, s0 = (int64_t)blockIdx.y * 16 + 4 * (threadIdx.x >> 6);
     const int64_t row = 32 * kt + slot_row(lane & 31), up = blockIdx.z;
     const int64_t e0 = (row + up * F) * K;
     uint4 c[4];
@@ -1114,61 +1113,75 @@ __global__ __launch_bounds__(256) void k_lin_dz(LinGradArgs p, int64_t chunk, fl
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-// Tile height and K split of the tile kernel for an [M] x [F] output over a sum of length L: the least of the times
-// that these measurements add up to (us on an MI355X). A step of 64 k costs, with one work-group per CU and with
-// two (heights 1 and 2; the taller take a CU each), by where the weights come from:
+// What a launch of the tile kernel takes, in us, as measured on an MI355X. A step of 64 k costs, with one work-group
+// per CU and with two (heights 1 and 2; the taller take a CU each), by where the weights come from:
 //   height (of 32 rows)   1            2            4      8
 //   as stored             0.62 / 0.96  0.75 / 1.27  1.00   1.66
 //   decoded before        0.38 / 0.74  0.51 / 0.97  0.80   1.47
 //   turned                0.83 / 1.09  0.85 / 1.35  1.09   1.78
 // on top of 6, 8, 13 and 15 per work-group (launch, first loads, epilogue), and slices of K cost 4 and 8 bytes per
 // sum at 4 TB/s.
-LinPlan plan_tile(int64_t M, int64_t L, int64_t F, int64_t N, bool gated, int src) {
-    static constexpr int kHeights[4] = {1, 2, 4, 8};
+constexpr int kHeights[4] = {1, 2, 4, 8};
+constexpr double kFixed[4] = {6.0, 8.0, 13.0, 15.0};
+constexpr double kLaunch = 3.0;  // a launch more
+
+double tile_us(int src, int h, int64_t groups, double steps) {
     static constexpr double kAlone[3][4] = {{0.62, 0.75, 1.00, 1.66}, {0.38, 0.51, 0.80, 1.47}, {0.83, 0.85, 1.09, 1.78}};
     static constexpr double kPaired[3][2] = {{0.96, 1.27}, {0.74, 0.97}, {1.09, 1.35}};
-    static constexpr double kFixed[4] = {6.0, 8.0, 13.0, 15.0};
-    const int64_t tn = ceil_div(F, gated ? 128 : 256), pairs = ceil_div(L, 2 * kStep);
-    LinPlan best = {};
-    for (int h = 0; h < 4; ++h) {
+    const double alone = kFixed[h] + steps * kAlone[src][h];
+    if (h >= 2) return (double)ceil_div(groups, 256) * alone;
+    const double paired = kFixed[h] + steps * kPaired[src][h];
+    const int64_t rest = groups % 512;
+    return (double)(groups / 512) * paired + (rest > 256 ? paired : rest > 0 ? alone : 0.0);
+}
+
+// The height (kHeights[h0] at least) and the K split of the least estimated time for `tn` columns of tiles, whose
+// sums have n values a row.
+TileCut cut_tiles(int64_t M, int64_t L, int64_t tn, int64_t n, int src, int h0) {
+    const int64_t pairs = ceil_div(L, 2 * kStep);
+    TileCut best = {};
+    for (int h = h0; h < 4; ++h) {
         const int64_t tm = ceil_div(M, 32 * kHeights[h]);
         for (int64_t want = 1; want <= 16 && want <= pairs; ++want) {
-            const int64_t per = ceil_div(pairs, want), slices = ceil_div(pairs, per);
-            if (slices != want) continue;
-            const double sums = (double)slices * (double)M * (double)N;
-            if (slices > 1 && sums * sizeof(float) > (double)((int64_t)1 << 30)) break;
-            const int64_t groups = tm * tn * slices;
-            const double steps = 2.0 * (double)per, alone = kFixed[h] + steps * kAlone[src][h];
-            double t;
-            if (h < 2) {
-                const double paired = kFixed[h] + steps * kPaired[src][h];
-                const int64_t rest = groups % 512;
-                t = (double)(groups / 512) * paired + (rest > 256 ? paired : rest > 0 ? alone : 0.0);
-            } else {
-                t = (double)ceil_div(groups, 256) * alone;
-            }
-            if (slices > 1) t += 4.0 + sums * 8.0 / 4.0e6;
-            if (best.mt == 0 || t < best.us) {
-                best.us = t;
-                best.mt = kHeights[h];
-                best.tiles_n = tn;
-                best.tiles_m = tm;
-                best.slices = slices;
-                best.kslice = per * 2 * kStep;
-                best.part_bytes = slices > 1 ? (size_t)(slices * M * N) * sizeof(float) : 0;
-            }
+            const int64_t per = ceil_div(pairs, want);
+            if (ceil_div(pairs, per) != want) continue;
+            const double sums = (double)want * (double)M * (double)n;
+            if (want > 1 && sums * sizeof(float) > (double)((int64_t)1 << 30)) break;
+            double t = tile_us(src, h, tm * tn * want, 2.0 * (double)per);
+            if (want > 1) t += 4.0 + sums * 8.0 / 4.0e6;
+            if (best.mt == 0 || t < best.us) best = {kHeights[h], tn, want, per * 2 * kStep, t};
         }
     }
-    // The last round of the tallest tiles, if it has too few of them: its columns in tiles of half the height, which
-    // take 64 us where a round of the tallest takes 109 (decoded, K = 4096).
-    if (best.mt == 8 && best.slices == 1 && best.tiles_m * best.tiles_n > 256 && best.tiles_m <= 256) {
-        const int64_t whole = best.tiles_m * best.tiles_n / 256 * 256 / best.tiles_m;  // columns of the whole rounds
-        const int64_t last = best.tiles_n - whole;
-        if (last > 0 && last * ceil_div(M, 128) <= 256) {
-            best.last_tiles_n = last;
-            best.us -= (kFixed[3] - kFixed[2]) + 2.0 * (double)pairs * (kAlone[src][3] - kAlone[src][2]);
+    return best;
+}
+
+// The tiles of an [M] x [F] output over a sum of length L: all columns of tiles alike, or, where the last round of
+// work-groups would be short, the columns of the whole rounds and the rest of them as launches of their own, the
+// rest lower or with K split (3000 x 11008 x 4096 is 516 of the tallest tiles: 325 us with the third round's in half the
+// height, 249 us with 504 of them in two rounds and the last column's K split; 1500 x 11008 x 4096: 203 and 132 us).
+LinPlan plan_tile(int64_t M, int64_t L, int64_t F, int64_t N, bool gated, int src, int h0 = 0) {
+    const int64_t cols = gated ? 128 : 256, tn = ceil_div(F, cols), per_col = gated ? 2 : 1;
+    const double steps = 2.0 * (double)ceil_div(L, 2 * kStep);
+    LinPlan best = {};
+    best.main = cut_tiles(M, L, tn, N, src, h0);
+    best.us = best.main.us;
+    for (int h = h0; h < 4; ++h) {
+        const int64_t tm = ceil_div(M, 32 * kHeights[h]);
+        for (int64_t slots = 256; slots <= (h < 2 ? 512 : 256); slots *= 2) {
+            const int64_t whole = tm * tn / slots * slots / tm;  // columns of the whole rounds
+            if (whole == 0 || whole == tn) continue;
+            const double us = kLaunch + tile_us(src, h, tm * whole, steps);
+            if (us >= best.us) continue;
+            const TileCut rest = cut_tiles(M, L, tn - whole, (F - whole * cols) * per_col, src, h0);
+            if (us + rest.us >= best.us) continue;
+            best.us = us + rest.us;
+            best.main = {kHeights[h], whole, 1, ceil_div(L, 2 * kStep) * 2 * kStep, us};
+            best.rest = rest;
         }
     }
+    const int64_t rest_n = (F - (best.rest.mt ? best.main.tiles_n * cols : 0)) * per_col;
+    const TileCut &split = best.rest.mt ? best.rest : best.main;  // where there is a rest, K is whole before it
+    best.part_bytes = split.slices > 1 ? align256((size_t)(split.slices * M * rest_n) * sizeof(float)) : 0;
     return best;
 }
 
@@ -1196,33 +1209,38 @@ hipError_t tile_launch_height(const LinArgs &p, int mt, int64_t slices, hipStrea
     return hipGetLastError();
 }
 
+// The columns of tiles [first, first + cut.tiles_n), and the sum of their slices where K is split.
 template <int SRC, int EPI>
-hipError_t tile_launch_as(LinArgs p, const LinPlan &plan, hipStream_t st) {
-    auto columns = [&](int mt, int64_t first, int64_t count) {
-        const int64_t tm = ceil_div(p.M, 32 * mt);
-        p.tn0 = first, p.tiles_n = (unsigned)count, p.tiles_m = (unsigned)tm, p.tiles = (unsigned)(tm * count);
-        return tile_launch_height<SRC, EPI>(p, mt, plan.slices, st);
-    };
-    if (plan.last_tiles_n > 0) {
-        const hipError_t err = columns(8, 0, plan.tiles_n - plan.last_tiles_n);
-        return err != hipSuccess ? err : columns(4, plan.tiles_n - plan.last_tiles_n, plan.last_tiles_n);
-    }
-    hipError_t err = columns(plan.mt, 0, plan.tiles_n);
-    if (err == hipSuccess && plan.slices > 1) {
-        const int64_t per_row = ceil_div(p.F, kMxBlock) * 4, groups = p.M * per_row;
+hipError_t tile_launch_cut(LinArgs p, const TileCut &cut, int64_t first, hipStream_t st) {
+    constexpr int64_t cols = EPI == kEpiGated ? 128 : 256;
+    const int64_t tm = ceil_div(p.M, 32 * cut.mt);
+    p.tn0 = first, p.tiles_n = (unsigned)cut.tiles_n, p.tiles_m = (unsigned)tm, p.tiles = (unsigned)(tm * cut.tiles_n);
+    p.kslice = cut.kslice;
+    p.part_f0 = first * cols;
+    p.part_f = std::min(p.F, (first + cut.tiles_n) * cols) - p.part_f0;
+    p.part_n = EPI == kEpiGated ? 2 * p.part_f : p.part_f;
+    if (cut.slices == 1) p.part = nullptr;
+    hipError_t err = tile_launch_height<SRC, EPI>(p, cut.mt, cut.slices, st);
+    if (err == hipSuccess && cut.slices > 1) {
+        const int64_t per_row = ceil_div(p.part_f, kMxBlock) * 4, groups = p.M * per_row;
         const dim3 rg((unsigned)std::min<int64_t>(ceil_div(groups, kReduceThreads), 4096));
         if (p.F % 8 == 0)
-            hipLaunchKernelGGL((k_lin_reduce<EPI, true>), rg, dim3(kReduceThreads), 0, st, p, (int)plan.slices, per_row, groups);
+            hipLaunchKernelGGL((k_lin_reduce<EPI, true>), rg, dim3(kReduceThreads), 0, st, p, (int)cut.slices, per_row, groups);
         else
-            hipLaunchKernelGGL((k_lin_reduce<EPI, false>), rg, dim3(kReduceThreads), 0, st, p, (int)plan.slices, per_row, groups);
+            hipLaunchKernelGGL((k_lin_reduce<EPI, false>), rg, dim3(kReduceThreads), 0, st, p, (int)cut.slices, per_row, groups);
         err = hipGetLastError();
     }
     return err;
 }
 
+template <int SRC, int EPI>
+hipError_t tile_launch_as(const LinArgs &p, const LinPlan &plan, hipStream_t st) {
+    const hipError_t err = tile_launch_cut<SRC, EPI>(p, plan.main, 0, st);
+    return err != hipSuccess || plan.rest.mt == 0 ? err : tile_launch_cut<SRC, EPI>(p, plan.rest, plan.main.tiles_n, st);
+}
+
 template <int SRC>
-hipError_t tile_launch(LinArgs p, const LinPlan &plan, hipStream_t st) {
-    p.kslice = plan.kslice;
+hipError_t tile_launch(const LinArgs &p, const LinPlan &plan, hipStream_t st) {
     if constexpr (SRC != kSrcTurn) {
         if (p.gated) return tile_launch_as<SRC, kEpiGated>(p, plan, st);
         if (p.bias || p.res || p.act != kActNone || p.keep != kKeepNone || p.y_f32)
@@ -1299,17 +1317,16 @@ GradPlan plan_grad(int64_t M, int64_t K, int64_t N, int64_t F, bool bias) {
 }  // namespace
 
 LinPlan plan_linear(int64_t M, int64_t K, int64_t N, bool x_mx, bool gated, int keep) {
-    if (M <= kSkinnyMaxM && keep != kKeepMx) {  // mt = 0: the skinny kernel
+    if (M <= kSkinnyMaxM && keep != kKeepMx) {  // main.mt = 0: the skinny kernel
         LinPlan p = {};
-        p.slices = 1;
         if (M > kDirectRows) p.frag_bytes = (size_t)(ceil_div(K, kChunk) * ceil_div(M, 16)) * 4096;
         return p;
     }
     const int64_t F = gated ? N / 2 : N;
     LinPlan p = plan_tile(M, K, F, N, gated, kSrcCodes);
     if (M > 1024) {  // the decoding is paid back by many tiles of rows (4096 x 4096 weights: from about 2300 rows) or not at all
-        const LinPlan q = plan_tile(M, K, F, N, gated, kSrcFrag);
-        if (q.mt >= 4 && q.slices == 1 && q.us + decode_us(N, K) < p.us) {
+        const LinPlan q = plan_tile(M, K, F, N, gated, kSrcFrag, 2);
+        if (q.us + decode_us(N, K) < p.us) {
             p = q;
             p.frag_bytes = (size_t)(ceil_div(F, 32) * (gated ? 2 : 1) * ceil_div(K, kStep)) * 4096;
         }
@@ -1321,7 +1338,7 @@ LinPlan plan_linear(int64_t M, int64_t K, int64_t N, bool x_mx, bool gated, int 
 hipError_t launch_linear(const LinArgs &args, void *ws, hipStream_t stream) {
     const LinPlan plan = plan_linear(args.M, args.L, args.N, args.x_mx, args.gated, args.keep);
     LinArgs p = args;
-    if (plan.mt == 0) {
+    if (plan.main.mt == 0) {
         return p.gated ? skinny_launch<2>(p, ws, stream) : skinny_launch<1>(p, ws, stream);
     }
     uint8_t *base = static_cast<uint8_t *>(ws);
@@ -1333,13 +1350,14 @@ hipError_t launch_linear(const LinArgs &args, void *ws, hipStream_t stream) {
     }
     if (plan.frag_bytes) {
         p.wt = reinterpret_cast<uint16_t *>(base);
-        const dim3 grid((unsigned)ceil_div(ceil_div(p.F, 32), 4), (unsigned)ceil_div(ceil_div(p.L, kStep), 4), p.gated ? 2 : 1);
+        const dim3 grid((unsigned)ceil_div(p.F, 32), (unsigned)ceil_div(p.L, 16 * kStep), p.gated ? 2 : 1);
         hipLaunchKernelGGL(k_lin_decode, grid, dim3(256), 0, stream, p.codes, p.scales, p.F, p.L, reinterpret_cast<uint16_t *>(base));
         const hipError_t err = hipGetLastError();
         if (err != hipSuccess) return err;
+        p.part = reinterpret_cast<float *>(base + plan.frag_bytes);
         return tile_launch<kSrcFrag>(p, plan, stream);
     }
-    p.part = plan.slices > 1 ? reinterpret_cast<float *>(base) : nullptr;
+    p.part = reinterpret_cast<float *>(base);
     return tile_launch<kSrcCodes>(p, plan, stream);
 }
 
@@ -1381,7 +1399,7 @@ hipError_t launch_linear_grad(const LinGradArgs &g, const uint8_t *codes, const 
     p.alpha = alpha;
     p.y = dx;
     p.wt = wt, p.codes = codes, p.scales = scales;
-    p.part = plan.tile.slices > 1 ? part : nullptr;
+    p.part = part;
     return plan.turn ? tile_launch<kSrcTurn>(p, plan.tile, stream) : tile_launch<kSrcFrag>(p, plan.tile, stream);
 }
 

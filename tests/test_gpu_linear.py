@@ -175,6 +175,60 @@ def test_one_hot_gradients_are_exact(n, k):
         assert torch.equal(nv.linear_grad(dy, *W)[0], want[at[:m]])
 
 
+# One more column of tiles than whole rounds of work-groups take: it runs by itself, with K split. Columns that end
+# inside a tile and inside eight, gated or not; weights as stored and decoded first.
+REST = [(1500, 10843, 1040, False), (1500, 10944, 1040, False), (1500, 10944, 1040, True), (1500, 10946, 1040, True),
+        (2050, 3984, 2064, False)]
+
+
+@pytest.mark.parametrize("m,n,k,gated", REST)
+def test_last_columns_alone(m, n, k, gated):
+    F = n // 2 if gated else n
+    W = make_weights(n, k)
+    say(f"rest M={m} N={n} K={k} {gated}")
+    X, bias, res = rand(1, m, k), rand(2, n), rand(3, m, F)
+    act = "silu" if gated else None
+    y, z, ey, ez = ref.linear(X.double(), *W, act=act, gated=gated)
+    check(nv.linear(X, *W, activation=act, gated=gated), y, ey)
+    y, z, ey, ez = ref.linear(X.double(), *W, bias=bias, act="gelu", gated=gated, res=res)
+    for keep in (BF16, "mxfp8"):
+        if keep == "mxfp8" and gated and F % 32:
+            continue
+        got, Z = nv.linear(X, *W, bias=bias, activation="gelu", gated=gated, residual=res, keep=keep)
+        check(got, y, ey)
+        check_kept(Z, z, ez) if keep == "mxfp8" else check(Z, z, ez)
+    need = nv.linear_workspace_bytes(m, k, n, gated)
+    assert need > 0
+    space = torch.full((need + 512,), 0x5A, dtype=torch.uint8, device="cuda")  # a call stays inside its workspace
+    off = -space.data_ptr() % 256
+    again = nv.linear(X, *W, bias=bias, activation="gelu", gated=gated, residual=res, workspace=space[off:off + need])
+    assert torch.equal(again, got) and (space[off + need:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("m,n,k", [(1500, 2064, 10992), (4100, 272, 4128)])
+def test_last_columns_alone_gradient(m, n, k):
+    W = make_weights(n, k)
+    Wv, alpha = ref.weights(*W[:2]), float(W[2])
+    dy = rand(4, m, n)
+    say(f"rest gradient M={m} N={n} K={k}")
+    dX, _, db = nv.linear_grad(dy, *W, bias=True)
+    check(dX, alpha * (dy.double() @ Wv), ref.product_error(dy.double(), Wv.T, alpha, n))
+    assert ((db.double() - dy.double().sum(0)).abs() <= (m + 8) * ref.U * dy.double().abs().sum(0)).all()
+    x, held = rand(5, m, k), None
+    work = lambda: (nv.linear(x, *W), nv.linear_grad(dy, *W)[0])  # noqa: E731
+    eager = work()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        held = work()
+    for _ in range(3):
+        for t in held:
+            t.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(held, eager))
+        work()
+
+
 GRADS = [(1, 256, 1024), (1, 1, 16), (5, 7, 48), (33, 130, 272), (64, 64, 2064), (100, 1001, 176), (300, 520, 96),
          (130, 4100, 528), (32800, 80, 256), (51300, 48, 208), (300, 112, 25600), (2100, 64, 6400)]
 
