@@ -156,10 +156,10 @@ struct LinArgs {
     const void *bias, *res;
     void *y, *z;
     uint8_t *zs;
-    float *part;  // fp32 sums of the K slices; null in a launch that does not split K
+    float *part;  // fp32 sums of the K slices, where column 0 would be; null in a launch that does not split K
     int64_t M, L, N, F, ldx, ldr, kslice;
     int64_t tn0;  // first column tile of a launch
-    int64_t part_f0, part_f, part_n;  // the output columns that part holds: first and number; values per row
+    int64_t part_n;  // values per row of part (gated: its gate columns, then as many up columns)
     unsigned tiles, tiles_m, tiles_n;
     int x_mx, bias_f32, res_f32, y_f32, act, gated, keep;
 };

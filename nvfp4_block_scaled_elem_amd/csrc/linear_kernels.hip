@@ -664,9 +664,9 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
             if (p.part) {  // fp32 sums of this slice, without alpha
 #pragma unroll
                 for (int r = 0; r < kRows; ++r) {
-                    float *q = p.part + ((int64_t)slice * p.M + m + r * stride) * p.part_n + (f - p.part_f0);
+                    float *q = p.part + ((int64_t)slice * p.M + m + r * stride) * p.part_n + f;
                     put<kWholeRow>(q, g[r], n[r]);
-                    if (kGated) put<kWholeRow>(q + p.part_f, u[r], n[r]);
+                    if (kGated) put<kWholeRow>(q + p.part_n / 2, u[r], n[r]);
                 }
             } else {
                 epilogue<EPI, kWholeRow, kRows>(p, m, stride, f, n, g, u, bg, bu, res, lane);
@@ -704,11 +704,11 @@ constexpr int kReduceThreads = 256;
 // The slices' sums added in slice order, then the epilogue: eight columns per thread, rows padded to whole
 // 32-column blocks so that a quad holds a block.
 template <int EPI, bool WHOLE>
-__global__ __launch_bounds__(kReduceThreads) void k_lin_reduce(LinArgs p, int slices, int64_t per_row, int64_t groups) {
+__global__ __launch_bounds__(kReduceThreads) void k_lin_reduce(LinArgs p, int slices, int64_t f0, int64_t per_row, int64_t groups) {
     const float alpha = *p.alpha;
     for (int64_t i = (int64_t)blockIdx.x * kReduceThreads + threadIdx.x; i < groups;
          i += (int64_t)gridDim.x * kReduceThreads) {
-        const int64_t m = i / per_row, fp = 8 * (i - m * per_row), f = p.part_f0 + fp;
+        const int64_t m = i / per_row, f = f0 + 8 * (i - m * per_row);
         const int n[1] = {clamp_count(p.F - f, 8)};
         RawAny<WHOLE> res[1];
         float g[1][8] = {}, u[1][8] = {}, bg[8], bu[8];
@@ -716,7 +716,7 @@ __global__ __launch_bounds__(kReduceThreads) void k_lin_reduce(LinArgs p, int sl
         load_bias<EPI, WHOLE>(p, f, n[0], bg, bu);
 #pragma unroll 4
         for (int s = 0; s < slices; ++s) {
-            const float *q = p.part + ((int64_t)s * p.M + m) * p.part_n + fp;
+            const float *q = p.part + ((int64_t)s * p.M + m) * p.part_n + f;
             RawAny<WHOLE> r;
             float v[8];
             r.load(q, 1, 0, n[0]);
@@ -724,7 +724,7 @@ __global__ __launch_bounds__(kReduceThreads) void k_lin_reduce(LinArgs p, int sl
 #pragma unroll
             for (int e = 0; e < 8; ++e) g[0][e] += v[e];
             if (EPI == kEpiGated) {
-                r.load(q + p.part_f, 1, 0, n[0]);
+                r.load(q + p.part_n / 2, 1, 0, n[0]);
                 r.get(1, v);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) u[0][e] += v[e];
@@ -1216,18 +1216,17 @@ hipError_t tile_launch_cut(LinArgs p, const TileCut &cut, int64_t first, hipStre
     const int64_t tm = ceil_div(p.M, 32 * cut.mt);
     p.tn0 = first, p.tiles_n = (unsigned)cut.tiles_n, p.tiles_m = (unsigned)tm, p.tiles = (unsigned)(tm * cut.tiles_n);
     p.kslice = cut.kslice;
-    p.part_f0 = first * cols;
-    p.part_f = std::min(p.F, (first + cut.tiles_n) * cols) - p.part_f0;
-    p.part_n = EPI == kEpiGated ? 2 * p.part_f : p.part_f;
-    if (cut.slices == 1) p.part = nullptr;
+    const int64_t f0 = first * cols, f = std::min(p.F, (first + cut.tiles_n) * cols) - f0;
+    p.part_n = EPI == kEpiGated ? 2 * f : f;
+    p.part = cut.slices > 1 ? p.part - f0 : nullptr;
     hipError_t err = tile_launch_height<SRC, EPI>(p, cut.mt, cut.slices, st);
     if (err == hipSuccess && cut.slices > 1) {
-        const int64_t per_row = ceil_div(p.part_f, kMxBlock) * 4, groups = p.M * per_row;
+        const int64_t per_row = ceil_div(f, kMxBlock) * 4, groups = p.M * per_row;
         const dim3 rg((unsigned)std::min<int64_t>(ceil_div(groups, kReduceThreads), 4096));
         if (p.F % 8 == 0)
-            hipLaunchKernelGGL((k_lin_reduce<EPI, true>), rg, dim3(kReduceThreads), 0, st, p, (int)cut.slices, per_row, groups);
+            hipLaunchKernelGGL((k_lin_reduce<EPI, true>), rg, dim3(kReduceThreads), 0, st, p, (int)cut.slices, f0, per_row, groups);
         else
-            hipLaunchKernelGGL((k_lin_reduce<EPI, false>), rg, dim3(kReduceThreads), 0, st, p, (int)cut.slices, per_row, groups);
+            hipLaunchKernelGGL((k_lin_reduce<EPI, false>), rg, dim3(kReduceThreads), 0, st, p, (int)cut.slices, f0, per_row, groups);
         err = hipGetLastError();
     }
     return err;
