@@ -505,3 +505,37 @@ def test_refusals():
         with pytest.raises(nv.NVFP4Error):
             call()
             say(f"call {i} was not refused")
+
+
+def test_graphs_that_share_a_workspace():
+    """Calls captured into two graphs with one workspace, replayed in turn: each writes what it reads of it."""
+    m, n, k = 700, 512, 2048  # K split forward and backward
+    W = make_weights(n, k)
+    x, dy, w = rand(1, m, k), rand(2, m, n), torch.ones(k, device="cuda")
+    need = max(nv.linear_workspace_bytes(m, k, n), nv.linear_grad_workspace_bytes(m, k, n, bias=True),
+               nv.rms_norm_grad_workspace_bytes(m, k))
+    assert nv.linear_workspace_bytes(m, k, n) > 0
+    space = torch.empty(need, dtype=torch.uint8, device="cuda")
+
+    def work(scale):
+        a, b = x * scale, dy * scale
+        return (nv.linear(a, *W, workspace=space), *nv.linear_grad(b, *W, bias=True, workspace=space)[::2],
+                *nv.rms_norm_grad(a, x, w, workspace=space))
+
+    graphs = []
+    for scale in (1.0, -3.0):
+        eager = work(scale)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            held = work(scale)
+        graphs.append((g, held, eager))
+    for _ in range(3):
+        for g, held, eager in graphs:
+            for t in held:
+                t.zero_()
+            g.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(held, eager))
+        work(2.0)
+    torch.cuda.synchronize()
