@@ -395,8 +395,8 @@ size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int x_dtype
  *   dz [M][N] bf16 = dy act'(z), or gated (dy * up * act'(gate), dy * act(gate)) for z = (gate, up);
  *   dx [M][K] bf16 = alpha * (dz Wq), of dz as rounded (the products are exact, the sums fp32);
  *   dbias [N] fp32 = the sum over rows of dz unrounded (NULL: not formed).
- * z is what nvfp4_linear kept, bf16 or MXFP8 (contiguous scales). activation = none: z and dz are NULL and
- * dz = dy. lddy < 2^23. Scratch: the decoded weights and partial sums, nvfp4_linear_grad_workspace_bytes. */
+ * act' of a NaN or an infinity in z is NaN. z is what nvfp4_linear kept, bf16 or MXFP8 (contiguous scales).
+ * activation = none: z and dz are NULL and dz = dy. lddy < 2^23. Scratch: the decoded weights and partial sums, nvfp4_linear_grad_workspace_bytes. */
 typedef struct nvfp4_linear_grad_args {
     const void *dy;
     int64_t lddy;

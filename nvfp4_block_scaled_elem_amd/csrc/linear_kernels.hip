@@ -58,7 +58,9 @@ __device__ __forceinline__ float act_value(float z, int act) {
     return z;
 }
 
-// act(z) and act'(z). The gelu's derivative is 0 or 1 to fp32 beyond |z| = 30; the clamp keeps z^2 finite.
+// act(z) and act'(z). The gelu's derivative is 0 or 1 to fp32 beyond |z| = 30; the clamp keeps z^2 finite. The clamp
+// would take a NaN or an infinity for a number: z - z, 0 for every finite z, makes its slope the NaN that the formulas
+// give (an infinity's is inf * 0).
 __device__ __forceinline__ float2 act_both(float z, int act) {
     if (act == kActSilu) {
         const float s = logistic(z);
@@ -67,7 +69,8 @@ __device__ __forceinline__ float2 act_both(float z, int act) {
     const float c = fminf(fmaxf(z, -30.0f), 30.0f);
     const float c2 = c * c;
     const float s = logistic(kGelu2C * __builtin_fmaf(kGeluA * c2, c, c));
-    return make_float2(z * s, __builtin_fmaf(c * s * (1.0f - s), kGelu2C * __builtin_fmaf(3.0f * kGeluA, c2, 1.0f), s));
+    const float slope = __builtin_fmaf(c * s * (1.0f - s), kGelu2C * __builtin_fmaf(3.0f * kGeluA, c2, 1.0f), s);
+    return make_float2(z * s, slope + (z - z));
 }
 
 // ---------------------------------------------------------------------------------------- epilogue
