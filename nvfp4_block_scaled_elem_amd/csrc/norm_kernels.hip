@@ -367,12 +367,13 @@ __global__ __launch_bounds__(256) void k_rms_norm_dw_long(NormArgs p, const floa
 
 // out[c] = sum over `rows` rows of part[.][c], in a fixed order: a work-group takes 32 columns, its 32 half-waves
 // every 32nd row each, and their sums are added in that order (1024 x 4096: 3.5 us; with 64 columns and four
-// waves, 64 work-groups, 11 us). No rows: zeros.
+// waves, 64 work-groups, 11 us). No rows: zeros. The grid's x and y count the groups of 32 columns together: a dimension
+// holds fewer than 2^32 threads, 2^27 columns.
 __global__ __launch_bounds__(1024) void k_column_sum(const float *__restrict__ part, int64_t rows, int64_t cols,
                                                     float *__restrict__ out) {
     __shared__ float s[32][32];
     const int lane = threadIdx.x & 31, h = threadIdx.x >> 5;
-    const int64_t c = (int64_t)blockIdx.x * 32 + lane;
+    const int64_t c = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 32 + lane;
     float a = 0.0f;
     if (c < cols) {
 #pragma unroll 8
@@ -449,6 +450,7 @@ NormConfig norm_grad_config(int64_t cols) {
 }
 
 constexpr int64_t kLongChunk = 64;            // rows per partial sum of k_rms_norm_dw_long
+constexpr int64_t kSumGridX = (int64_t)1 << 16;  // most work-groups of k_column_sum along x
 
 int64_t norm_grad_groups(int64_t rows, int64_t cols) {
     const NormConfig c = norm_grad_config(cols);
@@ -511,7 +513,9 @@ hipError_t norm_grad_dispatch(const NormArgs &p, float *dw, float *ws, hipStream
 }  // namespace
 
 hipError_t launch_column_sum(const float *part, int64_t rows, int64_t cols, float *out, hipStream_t stream) {
-    hipLaunchKernelGGL(k_column_sum, dim3((unsigned)((cols + 31) / 32)), dim3(1024), 0, stream, part, rows, cols, out);
+    const int64_t blocks = (cols + 31) / 32, y = (blocks + kSumGridX - 1) / kSumGridX;
+    const dim3 grid((unsigned)((blocks + y - 1) / y), (unsigned)y);
+    hipLaunchKernelGGL(k_column_sum, grid, dim3(1024), 0, stream, part, rows, cols, out);
     return hipGetLastError();
 }
 

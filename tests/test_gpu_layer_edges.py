@@ -78,3 +78,18 @@ def test_gradient_far_from_zero(act):
     err = dy.double().abs() * (2.0 ** -22 * slope.abs() + small + ref.TINY * (1 + z.double().abs()))
     want = dy.double() * slope
     assert ((dZ.double() - want).abs() <= err + want.abs() * ref.HALF[BF16]).all()
+
+
+def test_weight_gradient_of_very_long_rows():
+    """More than 2^27 columns: dweight's last columns too. The sum of a row's squares has paths of cols / 1024 additions
+    (layer_ref.norm_depth), each off by 2^-24 of it."""
+    cols = (1 << 27) + 40
+    say(f"rms_norm_grad 1 x {cols}")
+    dy, h, w = rand(5, 1, cols), rand(6, 1, cols), rand(7, cols) + 1
+    dx, dw = nv.rms_norm_grad(dy, h, w, 1e-6)
+    rx, rw, ex, ew = ref.rms_norm_grad(dy, h, w, 1e-6)
+    assert ((dw.double() - rw).abs() <= ew + rw.abs() * ref.U).all()
+    assert ((dx.double() - rx).abs() <= ex + rx.abs() * ref.HALF[BF16]).all()
+    del rx, rw, ex, ew, dx, dw
+    _, none = nv.rms_norm_grad(dy[:0], h[:0], w, 1e-6)
+    assert none.shape == (cols,) and (none == 0).all()
