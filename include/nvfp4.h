@@ -299,9 +299,10 @@ size_t nvfp4_gptq_workspace_bytes(int64_t rows, int64_t cols);
  * All of them: device pointers, row-major; `ld*` is the number of elements from a row of an operand to the
  * next (>= its columns; not looked at for fewer than two rows), the outputs are contiguous. Pointers are
  * aligned to their element; rows need no more alignment than that (16-byte aligned rows are fastest). rows = 0
- * is allowed: nothing is written but the column sums (dweight, dbias), which are zeros. rows <= 2^23 and
- * rows * columns < 2^35 for every operand, weights among them (else NVFP4_ERR_SHAPE). Outputs may not overlap inputs unless a call says so. Sums
- * and statistics are binary32, in an order that does not depend on timing; each output is rounded once.
+ * is allowed: nothing is written but the column sums (dweight, dbias), which are zeros. rows <= 2^23 and, with
+ * columns rounded up to 32, rows * columns <= 2^35 - 2^11 for every operand, weights among them (else
+ * NVFP4_ERR_SHAPE). Outputs may not overlap inputs unless a call says so. Sums and statistics are binary32, in
+ * an order that does not depend on timing; each output is rounded once.
  * Nothing is allocated when `workspace` (256-byte aligned) is given or none is needed; without it scratch
  * is taken from a stream-ordered pool, except on a capturing stream (NVFP4_ERR_UNSUPPORTED). A call writes what
  * it reads of its workspace, so calls and captured graphs may share one if they run one after the other; calls

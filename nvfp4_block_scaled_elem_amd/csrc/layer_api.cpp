@@ -20,8 +20,9 @@ namespace {
 
 using nvfp4::NormArgs;
 
-// 2^35 elements, and 2^23 rows: a row's 256 threads then stay below 2^32 threads per grid.
-constexpr int64_t kMaxElems = (int64_t)1 << 35;
+// Fewer than 2^32 threads per dimension of a grid: 2^23 rows of 256 threads, and 2^35 - 2^11 elements (rows counted in whole
+// blocks of 32) by eight per thread in work-groups of 256.
+constexpr int64_t kMaxElems = ((int64_t)1 << 35) - ((int64_t)1 << 11);
 constexpr int64_t kMaxRows = (int64_t)1 << 23;
 
 bool aligned(const void *p, unsigned a) { return ((uintptr_t)p & (a - 1)) == 0; }
@@ -31,9 +32,8 @@ unsigned width(int t) { return t == NVFP4_DTYPE_BF16 ? 2u : t == NVFP4_DTYPE_F32
 // NVFP4_OK for a [rows][cols] operand of rows >= 0 with `ld` elements between rows.
 int check_shape(int64_t rows, int64_t cols) {
     if (rows < 0 || cols <= 0) return NVFP4_ERR_INVALID_ARG;
-    if (rows > kMaxRows || cols >= kMaxElems) return NVFP4_ERR_SHAPE;
-    const int64_t padded = (cols + 31) / 32 * 32;
-    if (rows > 0 && padded >= kMaxElems / rows) return NVFP4_ERR_SHAPE;
+    if (rows > kMaxRows || cols > kMaxElems) return NVFP4_ERR_SHAPE;
+    if (rows * ((cols + 31) / 32 * 32) > kMaxElems) return NVFP4_ERR_SHAPE;
     return NVFP4_OK;
 }
 
