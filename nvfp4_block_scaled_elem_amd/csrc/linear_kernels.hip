@@ -41,6 +41,14 @@ __device__ __forceinline__ void lds_barrier() {
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// Between what a wave's lanes store in LDS and what other lanes of it load there, or store over it: the hardware keeps a
+// wave's LDS accesses in order, this keeps the compiler from reordering them. No instruction.
+__device__ __forceinline__ void wave_handover() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
 // ------------------------------------------------------------------------------------- activations
 
 constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
@@ -378,8 +386,8 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
         for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(wl + w_place(16 * i + (lane >> 2), lane & 3)) = S.c[i];
         *reinterpret_cast<uint2 *>(wl + kWaveCodes + 8 * lane) = S.s;
     };
-    // The lane's codes and scales of step `odd` of the stored pair. Only the wave itself writes and reads them, in
-    // order.
+    // The lane's codes and scales of step `odd` of the stored pair. Only the wave itself writes and reads them: a
+    // wave_handover, or a barrier that stands there anyway, lies between.
     auto stage_read = [&](Weights &D, int odd) __attribute__((always_inline)) {
         if constexpr (kCodes)
 #pragma unroll
@@ -425,6 +433,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
             uint8_t *const q = wl + kTurnFrags;
 #pragma unroll
             for (int b = 0; b < 4; ++b) q[64 * b + lane] = (uint8_t)(D.s >> (8 * b));
+            wave_handover();
             const uint2 s = *reinterpret_cast<const uint2 *>(q + 64 * tblock + 8 * ng);
             const uint32_t w[2] = {s.x & 0x7F7F7F7Fu, s.y & 0x7F7F7F7Fu};
 #pragma unroll
@@ -513,6 +522,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             if (i == 3) lds_barrier();
+            if ((kTurn && i == 0) || (kCodes && odd && i == 2)) wave_handover();
             b_frag(B[(i + 1) & 1], i < 3 ? odd : odd ^ 1, (i + 1) & 3);
             a_frag(A[(i + 1) & 1], i < 3 ? w : next, (i + 1) & 3);
             if (i == 0) {
@@ -563,6 +573,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
         if (kTurn) {
             turn_all(T[0]);
             turn_load(std::true_type{}, T[0], min(kbeg + 2 * kStep, kfull - kStep));
+            wave_handover();
             turn_read(W[0]);
         }
         if (kCodes) {
@@ -592,6 +603,7 @@ __global__ __launch_bounds__(kTileThreads, MT >= 4 ? 1 : 2) void k_lin_tile(LinA
         if (kTurn) {
             turn_load(std::false_type{}, T[0], k0);
             turn_all(T[0]);
+            wave_handover();
             turn_read(W[0]);
         }
         if constexpr (kCodes)
@@ -872,14 +884,16 @@ void k_lin_skinny(LinArgs p) {
                 }
             }
         }
-        // Only the wave itself writes and reads its part of LDS, in order. A row's 64 bytes are four pieces, piece q at
+        // Only the wave itself writes and reads its part of LDS. A row's 64 bytes are four pieces, piece q at
         // q ^ (row / 4 % 4).
+        wave_handover();
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             uint8_t *const q = wl + j * kChunkLds;
             *reinterpret_cast<uint4 *>(q + w_place(lane >> 2, lane & 3)) = c[j];
             if (lane < 16) *reinterpret_cast<uint2 *>(q + 1024 + 8 * lane) = s[j];
         }
+        wave_handover();
 #pragma unroll
         for (int j = 0; j < NT; ++j) {
             const uint8_t *const q = wl + j * kChunkLds;
