@@ -12,6 +12,10 @@ An MXFP8 tensor is a pair (codes, scales): codes [rows, cols] ``torch.float8_e4m
 [rows, ceil(cols / 32)] ``torch.float8_e8m0fnu``, a power of two per 32 consecutive columns (uint8 tensors
 of the same bits are accepted too). Operands may have any row stride >= their columns; outputs are
 contiguous and are allocated on the call's stream: ``stream``, or the current stream of the operands' device.
+
+No call records an autograd graph: the gradients are calls of their own, for a program's own backward pass or
+inside a ``torch.autograd.Function``. Where grad mode is on, an operand that requires a gradient is refused, since
+its gradient would be lost without a word; ``torch.no_grad()`` or ``detach()`` says that none is wanted.
 """
 from __future__ import annotations
 
@@ -25,7 +29,6 @@ MXFP8 = "mxfp8"
 _MX = 2  # NVFP4_DTYPE_MXFP8
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 _SCALES = (torch.float8_e8m0fnu, torch.uint8)
-
 
 
 def _raw_stream(index: int) -> int:
@@ -125,6 +128,15 @@ def _new_mx(rows, cols, dev):
             torch.empty((rows, -(-cols // 32)), dtype=torch.float8_e8m0fnu, device=dev))
 
 
+def _no_graph(*operands):
+    if torch.is_grad_enabled():
+        for t in operands:
+            if t is not None and t.requires_grad:
+                raise NVFP4Error("the layer operators record no autograd graph: call them under torch.no_grad() or in a "
+                                 "torch.autograd.Function, with detached operands, and their gradients by rms_norm_grad "
+                                 "and linear_grad")
+
+
 def _ptr(t):
     return None if t is None else t.data_ptr()
 
@@ -141,6 +153,7 @@ def quantize_mxfp8(X: torch.Tensor, *, stream=None):
     """MXFP8 (codes, scales) of ``X`` ([rows, cols] bf16 or fp32 CUDA tensor): per 32 consecutive columns the
     smallest power-of-two scale under which nothing saturates, and the nearest E4M3 codes (ties to even)."""
     ld = _rows(X, "X", DTYPES)
+    _no_graph(X)
     rows, cols = X.shape
     dev = X.device
 
@@ -156,6 +169,7 @@ def quantize_mxfp8(X: torch.Tensor, *, stream=None):
 def dequantize_mxfp8(codes: torch.Tensor, scales: torch.Tensor, dtype=torch.bfloat16, *, stream=None) -> torch.Tensor:
     """The values of an MXFP8 tensor as bf16 or fp32."""
     codes, scales, ld = _mx_pair((codes, scales), "the tensor")
+    _no_graph(codes)
     if dtype not in DTYPES:
         raise NVFP4Error("dtype must be bf16 or fp32")
     rows, cols = codes.shape
@@ -187,6 +201,7 @@ def rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *, residu
         raise NVFP4Error("sum_out needs a residual")
     ldr = 0 if residual is None else _rows(residual, "residual", (X.dtype,), dev, (rows, cols))
     _output(sum_out, "sum_out", (rows, cols), X.dtype, dev)
+    _no_graph(X, weight, residual)
 
     def call(st):
         if out_dtype == MXFP8:
@@ -225,6 +240,7 @@ def rms_norm_grad(dY: torch.Tensor, S, weight: torch.Tensor, eps: float = 1e-6, 
         h, hs, ht = S, None, DTYPES[dY.dtype]
     _vector(weight, "weight", cols, dev)
     ldds = 0 if dS is None else _rows(dS, "dS", (dY.dtype,), dev, (rows, cols))
+    _no_graph(dY, h, weight, dS)
 
     def call(st):
         dX = torch.empty_like(dY, memory_format=torch.contiguous_format)
@@ -293,6 +309,7 @@ def linear(X, codes: torch.Tensor, scales: torch.Tensor, alpha: torch.Tensor, *,
         _vector(bias, "bias", N, dev)
     ldr = 0 if residual is None else _rows(residual, "residual", DTYPES, dev, (M, F))
     _output(out, "out", (M, F), out_dtype, dev)
+    _no_graph(x, alpha, bias, residual)
 
     def call(st):
         Y = torch.empty((M, F), dtype=out_dtype, device=dev) if out is None else out
@@ -340,6 +357,7 @@ def linear_grad(dY: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, alp
     elif Z is not None:
         ldz = _rows(Z, "Z", (torch.bfloat16,), dev, (M, N))
         z = Z
+    _no_graph(dY, alpha, z)
 
     def call(st):
         dX = torch.empty((M, K), dtype=torch.bfloat16, device=dev)
