@@ -311,12 +311,13 @@ size_t nvfp4_gptq_workspace_bytes(int64_t rows, int64_t cols);
  * MXFP8 ([rows][cols] code bytes and [rows][ceil(cols/32)] scale bytes): blocks of 32 consecutive columns
  * (the last may be shorter); a code is E4M3, a scale byte b is 2^(b-127) (E8M0), and a value is their
  * product. The scale written is the smallest power of two, 2^-127 at least, with max|v| <= 448 * scale, so
- * nothing saturates and a value is within half an E4M3 step. Zeros: b = 0. A block holding a NaN or an infinity:
+ * nothing saturates and a value is within half an E4M3 step (from 1.9375 * 2^127 on that is 2^128, which reads as
+ * an infinity). Zeros: b = 0. A block holding a NaN or an infinity:
  * b = 255, codes 0x7F, and all its values read as NaN. */
 
 /* MXFP8 codes and scales of x (dtype bf16 or fp32, [rows][cols], any cols >= 1), as activations are kept in
  * between a forward and a backward pass; and the values back, rounded to bf16 or fp32 (both hold every value
- * whose scale is at least 2^-117). */
+ * below 2^128 whose scale is at least 2^-117). */
 int nvfp4_mxfp8_quantize(const void *x, int64_t ldx, int dtype, int64_t rows, int64_t cols, uint8_t *codes,
                          uint8_t *scales, void *stream);
 int nvfp4_mxfp8_dequantize(const uint8_t *codes, int64_t ldc, const uint8_t *scales, int64_t rows, int64_t cols,
@@ -350,7 +351,8 @@ size_t nvfp4_rms_norm_grad_workspace_bytes(int64_t rows, int64_t cols);
 enum nvfp4_activation { NVFP4_ACT_NONE = 0, NVFP4_ACT_SILU = 1, NVFP4_ACT_GELU = 2 };
 
 /* The product of nvfp4_matmul with the rest of a layer's projection in its epilogue:
- *   z [M][N] = alpha * (x Wq^T) + bias, Wq = e2m1(code) * e4m3(scale) of the weights [N][K];
+ *   z [M][N] = alpha * (x Wq^T) + bias, Wq = e2m1(code) * e4m3(scale) of the weights [N][K] (scale bytes 0x00 .. 0x7E,
+ *   as the quantiser writes them);
  *   y [M][N] = act(z) + residual, or, gated (with an activation, N even, F = N / 2),
  *   y [M][F] = act(z[:, :F]) * z[:, F:] + residual: rows 0 .. F-1 of the weights are the gate.
  * x is bf16 or MXFP8 [M][K]; bias [N] and residual (as y) bf16 or fp32, NULL for none; y bf16 or fp32; z, kept
@@ -397,7 +399,8 @@ size_t nvfp4_linear_workspace_bytes(int64_t M, int64_t K, int64_t N, int x_dtype
  *   dx [M][K] bf16 = alpha * (dz Wq), of dz as rounded (the products are exact, the sums fp32);
  *   dbias [N] fp32 = the sum over rows of dz unrounded (NULL: not formed).
  * act' of a NaN or an infinity in z is NaN. z is what nvfp4_linear kept, bf16 or MXFP8 (contiguous scales).
- * activation = none: z and dz are NULL and dz = dy. lddy < 2^23. Scratch: the decoded weights and partial sums, nvfp4_linear_grad_workspace_bytes. */
+ * activation = none: z and dz are NULL and dz = dy. lddy < 2^23. Scratch: nvfp4_linear_grad_workspace_bytes (the weights
+ * decoded where that is the faster way, the bias's partial sums, fp32 sums where N is split over work-groups). */
 typedef struct nvfp4_linear_grad_args {
     const void *dy;
     int64_t lddy;

@@ -5,9 +5,10 @@
 //   nvfp4_rms_norm_grad   : k_rms_norm_grad -> k_column_sum (beyond 16384 columns: k_rms_norm_grad_long ->
 //                           k_rms_norm_dw_long -> k_column_sum)
 //   nvfp4_mxfp8_quantize / nvfp4_mxfp8_dequantize : one kernel each
-//   nvfp4_linear          : (k_lin_xfrag ->) k_lin_skinny, or (k_mx_dequantize ->) (k_lin_decode ->) k_lin_tile (-> k_lin_reduce where K is split)
-//   nvfp4_linear_grad     : (k_lin_dz with an activation or dbias; -> k_column_sum with dbias) -> k_lin_transpose ->
-//                           k_lin_tile (-> k_lin_reduce)
+//   nvfp4_linear          : (k_lin_xfrag ->) k_lin_skinny, or (k_mx_dequantize ->) (k_lin_decode ->) tiles
+//   nvfp4_linear_grad     : (k_lin_dz with an activation or dbias; -> k_column_sum with dbias) -> (k_lin_transpose ->) tiles
+//     tiles: k_lin_tile (-> k_lin_reduce where K is split), once or, the last columns by themselves, twice. Without
+//     k_lin_decode and k_lin_transpose the weights are decoded in k_lin_tile, whichever is estimated to take less.
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>

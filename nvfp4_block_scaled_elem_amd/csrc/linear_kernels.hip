@@ -7,8 +7,9 @@
 // function. z may be kept, bf16 or MXFP8.
 // Gradient: dz = dy act'(z) (gated: dy u act'(g) and dy act(g) for z = (g, u)), dX = alpha (dz Wq),
 // dbias = the column sums of dz. dz is an output rounded to bf16, and dX is the product of that rounding (the
-// matrix cores take bf16; its error, 2^-9 of a term and independent between terms, is of the size of dX's
-// own rounding); dbias adds dz unrounded.
+// matrix cores take bf16; its error, at most 2^-8 of a term and independent between terms, is of the size of dX's
+// own rounding: together 0.0023 of dX's norm, where a product of dz in fp32 has 0.0017. dz whole, in two bf16 parts,
+// would double the matrix cores' work); dbias adds dz unrounded.
 //
 // Products are exact and summed in fp32 on the matrix cores; everything after the sum is fp32.
 #include <hip/hip_runtime.h>
@@ -120,7 +121,8 @@ __device__ __forceinline__ void put(T *q, const float v[8], int n) {
 
 // What an epilogue does. Plain (y = alpha * sum in bf16, nothing else: the gradient's product, projections without
 // extras) is a kernel of its own, since a work-group's epilogue is not overlapped with anything where one fills a
-// CU; the others look at the call's arguments as they go.
+// CU; the others look at the call's arguments as they go. The full one of the 256-row tile, four rows of sums and
+// residuals at a time, needs 27 registers more than there are (112 bytes of scratch a thread).
 enum { kEpiPlain = 0, kEpiFull = 1, kEpiGated = 2 };
 
 // bias of the output columns f .. f + 7 and of their gate partners (zeros without a bias).
@@ -267,7 +269,9 @@ __device__ __forceinline__ void x_load(XStage<MT> &S, const XAddr<MT> &q, int64_
 
 // LDS rows are 64 bf16 in eight 16-byte chunks, chunk c of row r at position c ^ (r / 2 % 8). Two rows span the 64
 // banks; the 16 lanes that read one c of 16 rows at once then meet no bank twice (with r % 8 there were two rows
-// to a bank and four more cycles a read; LDS does not bound the kernel: 1 % of its time).
+// to a bank and four more cycles a read; LDS does not bound the kernel: 1 % of its time). That is X's reads; the
+// epilogue's and the codes' accesses do conflict: conflict cycles are a tenth of the LDS instructions in the 256-row
+// tile, 0.4 of them in the 32-row one.
 __device__ __forceinline__ int x_place(int row, int chunk) { return row * kStep + ((chunk ^ ((row >> 1) & 7)) << 3); }
 
 template <int MT>
@@ -790,7 +794,10 @@ __global__ __launch_bounds__(256) void k_lin_xfrag(LinArgs p, uint16_t *__restri
 // MT = 1.
 template <int MT, int NT, bool XF, bool XMX, int WAVES>
 __global__ __launch_bounds__(64 * WAVES)
-__attribute__((amdgpu_waves_per_eu(NT * MT <= 4 ? 4 : 1)))  // 128 registers where the accumulators leave room
+// Four waves a SIMD, 128 registers, to four tiles of sums. The forms of four tiles need 2 (gated) and 4 registers more
+// and spill them, which costs less than a wave: 24 x 22016 x 4096 gated 22.0 us, 24.6 without the bound (64 x 4096 x 4096,
+// 16 waves: 13.0 both).
+__attribute__((amdgpu_waves_per_eu(NT * MT <= 4 ? 4 : 1)))
 void k_lin_skinny(LinArgs p) {
     // each wave's chunk of codes and scales; afterwards each wave's sums
     constexpr int kStage = WAVES * NT * kChunkLds, kSums = WAVES * MT * 1024;
@@ -1333,7 +1340,11 @@ GradPlan plan_grad(int64_t M, int64_t K, int64_t N, int64_t F, bool bias) {
 }  // namespace
 
 LinPlan plan_linear(int64_t M, int64_t K, int64_t N, bool x_mx, bool gated, int keep) {
-    if (M <= kSkinnyMaxM && keep != kKeepMx) {  // main.mt = 0: the skinny kernel
+    // The skinny kernel (main.mt = 0) to the most rows that it has tiles for: there it is still ahead of the tile kernel
+    // (4096 x 4096: 64 rows 13.0 us, 65 rows in tiles 20.3; gated 22016 x 4096, 64 rows: 33.6 and 40.4). Its epilogue has no 32
+    // columns of a row together, so a z kept in MXFP8 takes the tile kernel (gated 22016 x 4096, 1 row: 27.1 us, with z
+    // in bf16 15.7; 24 rows: 29.9 and 22.5).
+    if (M <= kSkinnyMaxM && keep != kKeepMx) {
         LinPlan p = {};
         if (M > kDirectRows) p.frag_bytes = (size_t)(ceil_div(K, kChunk) * ceil_div(M, 16)) * 4096;
         return p;

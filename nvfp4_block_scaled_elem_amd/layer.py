@@ -290,7 +290,9 @@ def linear(X, codes: torch.Tensor, scales: torch.Tensor, alpha: torch.Tensor, *,
     with F = N // 2, Y = act(Z[:, :F]) * Z[:, F:] + residual. ``X`` is [M, K] bf16 or an MXFP8 pair; ``activation`` None,
     "silu" or "gelu" (tanh form); ``bias`` [N] and ``residual`` (Y's shape) bf16 or fp32; Y is of ``out_dtype``, in
     ``out`` if given (contiguous; it may be the residual itself). ``keep`` (None, torch.bfloat16 or "mxfp8") asks
-    for Z too, [M, N] in that form, for ``linear_grad`` (gated and "mxfp8": F % 32 == 0). Returns Y, or (Y, Z)."""
+    for Z too, [M, N] in that form, for ``linear_grad`` (gated and "mxfp8": F % 32 == 0). Returns Y, or (Y, Z). Without
+    any of these it is ``matmul``'s product by other kernels: faster for 2 to 64 rows and for thousands, slower for most
+    one-row products and some of a few hundred rows."""
     if isinstance(X, (tuple, list)):
         x, xs, ldx = _mx_pair(X, "X")
         xt = _MX
@@ -338,9 +340,9 @@ def linear_grad_workspace_bytes(M: int, K: int, N: int, gated: bool = False, bia
 def linear_grad(dY: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, alpha: torch.Tensor, *, Z=None,
                 activation=None, gated: bool = False, bias: bool = False, workspace=None, stream=None):
     """Gradients of ``linear`` for ``dY`` (bf16, Y's shape) at its output, with ``Z`` as it kept it (bf16 or an MXFP8
-    pair; None without an activation). Returns (dX, dZ, dbias): dX [M, K] bf16; dZ [M, N] bf16, the gradient at Z
-    (None without an activation, where it is dY); dbias [N] fp32 where ``bias`` is true, else None. The residual's
-    gradient is dY; the weights are frozen."""
+    pair; None without an activation). Returns (dX, dZ, dbias): dZ [M, N] bf16, the gradient at Z (None without an
+    activation, where it is dY); dX [M, K] bf16, the product of dZ as rounded; dbias [N] fp32 where ``bias`` is true,
+    else None, of dZ unrounded. The residual's gradient is dY; the weights are frozen."""
     lddy = _rows(dY, "dY", (torch.bfloat16,))
     dev = dY.device
     N, K = _weights(codes, scales, alpha, dev)
