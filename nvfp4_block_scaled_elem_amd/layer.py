@@ -14,8 +14,8 @@ of the same bits are accepted too). Operands may have any row stride >= their co
 contiguous and are allocated on the call's stream: ``stream``, or the current stream of the operands' device.
 
 No call records an autograd graph: the gradients are calls of their own, for a program's own backward pass or
-inside a ``torch.autograd.Function``. Where grad mode is on, an operand that requires a gradient is refused, since
-its gradient would be lost without a word; ``torch.no_grad()`` or ``detach()`` says that none is wanted.
+inside a ``torch.autograd.Function``. Where grad mode is on, an operand or a given output that requires a gradient is
+refused, since its gradient would be lost without a word; ``torch.no_grad()`` or ``detach()`` says that none is wanted.
 """
 from __future__ import annotations
 
@@ -201,7 +201,7 @@ def rms_norm(X: torch.Tensor, weight: torch.Tensor, eps: float = 1e-6, *, residu
         raise NVFP4Error("sum_out needs a residual")
     ldr = 0 if residual is None else _rows(residual, "residual", (X.dtype,), dev, (rows, cols))
     _output(sum_out, "sum_out", (rows, cols), X.dtype, dev)
-    _no_graph(X, weight, residual)
+    _no_graph(X, weight, residual, sum_out)
 
     def call(st):
         if out_dtype == MXFP8:
@@ -311,7 +311,7 @@ def linear(X, codes: torch.Tensor, scales: torch.Tensor, alpha: torch.Tensor, *,
         _vector(bias, "bias", N, dev)
     ldr = 0 if residual is None else _rows(residual, "residual", DTYPES, dev, (M, F))
     _output(out, "out", (M, F), out_dtype, dev)
-    _no_graph(x, alpha, bias, residual)
+    _no_graph(x, alpha, bias, residual, out)
 
     def call(st):
         Y = torch.empty((M, F), dtype=out_dtype, device=dev) if out is None else out

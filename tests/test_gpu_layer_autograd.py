@@ -37,6 +37,17 @@ def test_operands_that_require_gradients_are_refused():
             call()
 
 
+def test_outputs_that_require_gradients_are_refused():
+    W = nv.quantize(rand(21, 64, 96, std=0.05), "4o6")
+    x, w = rand(22, 4, 96), rand(23, 96)
+    for call in (lambda: nv.linear(x, *W, out=rand(24, 4, 64).requires_grad_()),
+                 lambda: nv.rms_norm(x, w, residual=x, sum_out=rand(25, 4, 96).requires_grad_())):
+        with pytest.raises(nv.NVFP4Error, match="autograd"):
+            call()
+        with torch.no_grad():
+            call()
+
+
 class Projection(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, wn, codes, scales, alpha):
