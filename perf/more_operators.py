@@ -45,29 +45,29 @@ def _moe(name, tokens, experts, top_k, width, inner, act="silu", gated=True, sco
 def listed():
     return [
         # one token of a decoding step: the positions of its query and key heads
-        _rotary("rotary, one token", 1, 40, 128),
+        _rotary("rotary: one token", 1, 40, 128),
         # a prompt with images: three axes (time, height, width)
-        _rotary("rotary, images", 8191, 40, 128, axes=3),
+        _rotary("rotary: images", 8191, 40, 128, axes=3),
         # a decoding step of a batch: a token of each sequence goes into the cache
-        _append("cache, a token each", 64, 8, 128, 1, 100, 8000),
+        _append("cache: a token each", 64, 8, 128, 1, 100, 8000),
         # prompts of odd lengths, some after earlier turns, go into the cache
-        _append("cache, prompts", 5, 8, 128, 3001, 0, 700),
+        _append("cache: prompts", 5, 8, 128, 3001, 0, 700),
         # a decoding step of one user's long conversation
-        _attention("attention, one sequence", 1, 32, 8, 128, 1, 7999, 7999),
+        _attention("attention: one sequence", 1, 32, 8, 128, 1, 7999, 7999),
         # a decoding step of a batch of conversations of very different lengths
-        _attention("attention, batch", 64, 32, 8, 128, 1, 300, 16000),
+        _attention("attention: batch", 64, 32, 8, 128, 1, 300, 16000),
         # a few drafted tokens of each sequence are verified: seven query heads to a key head of 64
-        _attention("attention, drafts", 16, 28, 4, 64, 6, 500, 5000),
+        _attention("attention: drafts", 16, 28, 4, 64, 6, 500, 5000),
         # prompts of odd lengths, one after an earlier turn
-        _attention("attention, prompts", 2, 32, 8, 128, 5003, 0, 3333),
+        _attention("attention: prompts", 2, 32, 8, 128, 5003, 0, 3333),
         # a token through a layer of many small experts
-        _moe("experts, one token", 1, 128, 8, 2048, 768),
+        _moe("experts: one token", 1, 128, 8, 2048, 768),
         # a small decoding batch through the same kind of layer, the experts' sum added to the residual stream
-        _moe("experts, small batch", 8, 64, 6, 4096, 1408, scoring="sigmoid", residual=True),
+        _moe("experts: small batch", 8, 64, 6, 4096, 1408, scoring="sigmoid", residual=True),
         # a short batch through a layer of few wide experts
-        _moe("experts, wide", 33, 8, 2, 4096, 14336),
+        _moe("experts: wide", 33, 8, 2, 4096, 14336),
         # a larger decoding batch
-        _moe("experts, batch", 150, 128, 8, 2048, 768, act="gelu", normalize=False, logits="bf16"),
+        _moe("experts: batch", 150, 128, 8, 2048, 768, act="gelu", normalize=False, logits="bf16"),
     ]
 
 
