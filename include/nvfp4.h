@@ -425,6 +425,90 @@ typedef struct nvfp4_linear_grad_args {
 int nvfp4_linear_grad(const nvfp4_linear_grad_args_t *args);
 size_t nvfp4_linear_grad_workspace_bytes(int64_t M, int64_t K, int64_t N, int gated, int with_dbias);
 
+/* ------------------------------------------------------- rotary positions, a cache in 8 bits, attention
+ *
+ * What a decoder layer computes between its products. Errors, streams, scratch and alignment as for the layer
+ * operators above; tokens <= 2^23, heads <= 65535. */
+
+/* Rotary positions: for each token t and head, with (a, b) = (x[j], x[j + R/2]), j < R/2,
+ *   y[j] = a cos w - b sin w, y[j + R/2] = b cos w + a sin w, w = positions[axis(j)][t] * base^(-2j/R);
+ * columns from R on are copied. R = 2 * (sections[0] + ... + sections[axes - 1]) <= dim, and axis(j) is the one in whose
+ * section j lies (sections of consecutive pairs, 1 <= axes <= 4). inverse = 1 turns back (w negated): the gradient of
+ * the call with inverse = 0, and the other way round. x and y are bf16 or fp32 (`dtype`) with `xs`, `ys` elements from
+ * token to token and `xh`, `yh` from head to head (not looked at for one token or head); y may be x itself with the same
+ * strides, and may not overlap it otherwise. positions: int32 or, with positions64 = 1, int64, `tokens` per axis. Angles
+ * are binary64, sines and cosines binary32, y is rounded once. dim <= 256, base > 0 and finite. */
+typedef struct nvfp4_rotary_args {
+    const void *x;
+    int64_t xs, xh;
+    void *y;
+    int64_t ys, yh;
+    int dtype;
+    int64_t tokens;
+    int heads, dim;
+    const void *positions;
+    int positions64;
+    int axes;
+    int sections[4];
+    double base;
+    int inverse;
+    void *stream;
+} nvfp4_rotary_args_t;
+
+int nvfp4_rotary(const nvfp4_rotary_args_t *args);
+
+/* A paged cache of keys and values in 8 bits: `pages` pages of 64 tokens for each of kv_heads heads, dim columns (dim % 16
+ * == 0, dim <= 256).
+ *   k_codes  [pages][kv_heads][64][dim]   E4M3
+ *   v_codes  [pages][kv_heads][dim][64]   E4M3, the tokens of a column side by side
+ *   k_scales, v_scales [pages][kv_heads]  E8M0 (as MXFP8): one power of two per page and head
+ * Token t of sequence s is slot t % 64 of page table[s][t / 64] (table: int32, `ldt` elements from sequence to
+ * sequence, `width` blocks each). lengths [seqs]: tokens of each sequence, those of the call among them. starts
+ * [seqs + 1]: the rows starts[s] .. starts[s + 1] - 1 of the call's operands are the last tokens of sequence s; NULL: row
+ * s is the one new token of sequence s (tokens == seqs). Rows in front of starts[0] and behind starts[seqs] are of no
+ * sequence: not read, and their outputs not written. Codes and outputs 16-byte aligned.
+ * lengths, starts and table are device data and not checked on the host. A page outside the cache holds nothing: its
+ * tokens are not written and not attended to; a length beyond 64 * width counts as that. The pages that a call
+ * writes to must be of one sequence only, once; pages that are only read may be shared.
+ *
+ * Writing: per block of 64 tokens and head, for keys and values apart, the scale is the smallest power of two (2^-127 at
+ * least) with max|x| <= 448 * scale over the block's new tokens, and not below the scale it has where it holds
+ * earlier tokens of the sequence (slots in front of the new ones): their codes are then rounded to the new scale, which is
+ * exact for codes that stay at or above 2^-6 in magnitude. Codes are the nearest, ties to even. Slots behind the
+ * sequence's end stay as they are. A NaN or an infinity in a block gives scale byte 255 and codes 0x7F: all its tokens read
+ * as NaN, until a sequence begins in the block anew. */
+typedef struct nvfp4_kv_cache {
+    uint8_t *k_codes, *v_codes;
+    uint8_t *k_scales, *v_scales;
+    int64_t pages;
+    int kv_heads, dim;
+} nvfp4_kv_cache_t;
+
+typedef struct nvfp4_sequences {
+    const int32_t *table;
+    int64_t ldt;
+    const int32_t *lengths;
+    const int32_t *starts; /* nullable */
+    int seqs, width;
+} nvfp4_sequences_t;
+
+/* k, v: [tokens][kv_heads][dim] bf16 or fp32 with their strides (unit columns). */
+int nvfp4_kv_append(const nvfp4_kv_cache_t *cache, const nvfp4_sequences_t *seqs, const void *k, int64_t k_token,
+                    int64_t k_head, const void *v, int64_t v_token, int64_t v_head, int dtype, int64_t tokens,
+                    void *stream);
+
+/* Attention of q [tokens][heads][dim] (bf16, its strides; heads a multiple of kv_heads, head i on key/value head i /
+ * (heads / kv_heads)) over the cache: out [tokens][heads][dim] bf16, contiguous,
+ *   out = sum_t softmax_t(scale * q . k_t) v_t
+ * over the tokens t that a row sees: with causal = 1 row i of a sequence's n rows sees its first length - n + i + 1
+ * tokens, with causal = 0 all `length`. A row that sees none gives zeros; one that sees a token of a block with scale byte
+ * 255 gives NaN. Products with q are exact, sums fp32, probabilities are rounded to bf16 before they are multiplied with
+ * the values. Values of the cache below 2^-126 may count as zero. Scratch: nvfp4_attention_workspace_bytes. */
+int nvfp4_attention(const nvfp4_kv_cache_t *cache, const nvfp4_sequences_t *seqs, const void *q, int64_t q_token,
+                    int64_t q_head, int heads, int64_t tokens, float scale, int causal, void *out, void *workspace,
+                    size_t workspace_bytes, void *stream);
+size_t nvfp4_attention_workspace_bytes(int64_t tokens, int seqs, int width, int heads, int kv_heads, int dim);
+
 /* Text of an nvfp4_error value. */
 const char *nvfp4_status_string(int status);
 

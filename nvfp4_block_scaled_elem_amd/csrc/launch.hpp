@@ -191,6 +191,58 @@ size_t linear_grad_workspace(int64_t M, int64_t K, int64_t N, int64_t F, bool bi
 hipError_t launch_linear_grad(const LinGradArgs &g, const uint8_t *codes, const uint8_t *scales, const float *alpha,
                               int64_t K, void *dx, float *dbias, void *ws, hipStream_t stream);
 
+// ---- rotary positions and the cache in 8 bits (cache_kernels.hip, attention_kernels.hip) ----
+
+constexpr int kRotaryAxes = 4, kRotaryPairs = 512, kMaxHeadDim = 256;
+struct RotaryArgs {
+    const void *x, *pos;
+    void *y;
+    int64_t xs, xh, ys, yh;  // elements between tokens and between heads
+    int64_t tokens, pos_ld;  // pos_ld: positions of an axis
+    int heads, dim, half;    // half: pairs
+    int pass;                // pieces of 8 columns behind the rotated ones to copy (0 in place)
+    int end[kRotaryAxes];    // the pair behind the axis's last
+    int pos64, inverse;
+    double c_hi, c_lo;       // log2 of the ratio of neighbouring pairs' frequencies; j c_hi is exact
+    int per, heads_per;      // tokens and heads of a work-group (set by the launcher)
+};
+hipError_t launch_rotary(const RotaryArgs &p, bool f32, hipStream_t stream);
+
+// The sequences of a call (cache.hpp): starts null: token s is the one new token of sequence s.
+struct SeqArgs {
+    const int *table, *lengths, *starts;
+    int64_t ldt;
+    int seqs, width, tokens, pages;
+};
+struct AppendArgs {
+    SeqArgs seq;
+    const void *k, *v;
+    int64_t ks, kh, vs, vh;  // elements between tokens and between heads
+    uint8_t *k_codes, *v_codes, *k_scales, *v_scales;
+    int heads, dim;
+};
+hipError_t launch_kv_append(const AppendArgs &p, bool f32, hipStream_t stream);
+struct AttnArgs {
+    SeqArgs seq;
+    const uint16_t *q;
+    int64_t qs, qh;  // elements between tokens and between heads
+    const uint8_t *k_codes, *v_codes, *k_scales, *v_scales;
+    uint16_t *out;
+    float *part, *part_ml;  // parts of tiles that several work-groups share: outputs; (maximum, sum)
+    float scale2;           // the scores' factor, in powers of two
+    int kv_heads, group, dim, causal;
+    int pieces, groups;  // set by the launcher
+};
+struct AttnPlan {
+    bool rows;       // rows over the waves; else blocks over the work-groups
+    int rt, size;    // tiles of 16 rows of a wave; rows of a piece
+    int64_t pieces;  // their numbers are below this
+    int groups;      // work-groups of a head (blocks over them)
+    size_t part_bytes, ml_bytes;
+};
+AttnPlan plan_attention(int64_t tokens, int seqs, int width, int kv_heads, int group, int dim);
+hipError_t launch_attention(const AttnArgs &p, void *ws, hipStream_t stream);
+
 hipError_t launch_dequant(const uint8_t *codes, const uint8_t *scales, const float *alpha, int64_t nblk, void *out,
                           bool out_f32, hipStream_t stream);
 

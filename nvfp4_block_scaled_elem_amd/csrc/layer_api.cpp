@@ -13,22 +13,22 @@
 #include <math.h>
 #include <stdint.h>
 
+#include "host.hpp"
 #include "launch.hpp"
-
-#define NVFP4_API extern "C" __attribute__((visibility("default")))
 
 namespace {
 
 using nvfp4::NormArgs;
+using nvfp4::aligned;
+using nvfp4::plain_dtype;
+using nvfp4::status;
+using nvfp4::width;
+using nvfp4::with_scratch;
 
 // Fewer than 2^32 threads per dimension of a grid: 2^23 rows of 256 threads, and 2^35 - 2^11 elements (rows counted in whole
 // blocks of 32) by eight per thread in work-groups of 256.
 constexpr int64_t kMaxElems = ((int64_t)1 << 35) - ((int64_t)1 << 11);
 constexpr int64_t kMaxRows = (int64_t)1 << 23;
-
-bool aligned(const void *p, unsigned a) { return ((uintptr_t)p & (a - 1)) == 0; }
-bool plain_dtype(int t) { return t == NVFP4_DTYPE_BF16 || t == NVFP4_DTYPE_F32; }
-unsigned width(int t) { return t == NVFP4_DTYPE_BF16 ? 2u : t == NVFP4_DTYPE_F32 ? 4u : 1u; }
 
 // NVFP4_OK for a [rows][cols] operand of rows >= 0 with `ld` elements between rows.
 int check_shape(int64_t rows, int64_t cols) {
@@ -36,24 +36,6 @@ int check_shape(int64_t rows, int64_t cols) {
     if (rows > kMaxRows || cols > kMaxElems) return NVFP4_ERR_SHAPE;
     if (rows * ((cols + 31) / 32 * 32) > kMaxElems) return NVFP4_ERR_SHAPE;
     return NVFP4_OK;
-}
-
-int status(hipError_t e) { return e == hipSuccess ? NVFP4_OK : NVFP4_ERR_HIP; }
-
-// Scratch of a call: the caller's workspace, or stream-ordered memory given back on the same stream. The
-// library does not allocate on a capturing stream.
-template <typename F>
-int with_scratch(void *workspace, size_t workspace_bytes, size_t need, hipStream_t st, F &&run) {
-    if (need == 0) return status(run(nullptr));
-    if (workspace) return workspace_bytes < need ? (int)NVFP4_ERR_WORKSPACE : status(run(workspace));
-    hipStreamCaptureStatus cs = hipStreamCaptureStatusNone;
-    if (hipStreamIsCapturing(st, &cs) != hipSuccess) return NVFP4_ERR_HIP;
-    if (cs != hipStreamCaptureStatusNone) return NVFP4_ERR_UNSUPPORTED;
-    void *ws = nullptr;
-    if (hipMallocAsync(&ws, need, st) != hipSuccess) return NVFP4_ERR_HIP;
-    const hipError_t e = run(ws);
-    if (hipFreeAsync(ws, st) != hipSuccess) return NVFP4_ERR_HIP;
-    return status(e);
 }
 
 }  // namespace

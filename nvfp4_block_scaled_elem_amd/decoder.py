@@ -1,0 +1,222 @@
+"""A decoder layer's operators between its products: rotary positions, a paged cache of keys and values in 8 bits,
+and attention over it (C ABI: ``include/nvfp4.h``). Marshalling only, like the rest of the binding.
+
+    rotary(qk, positions, out=qk)                                # qk: the query and key heads of a product, in place
+    cache = kv_cache(pages, kv_heads, dim)                       # codes and scales, all zeros
+    kv_append(cache, K, V, table, lengths)                       # a token of each sequence, or, with starts, several
+    O = attention(Q, cache, table, lengths)                      # of the same tokens' queries
+
+Streams, scratch and autograd are as for the layer operators (``layer.py``): outputs are allocated on the call's stream, and
+where grad mode is on an operand that requires a gradient is refused. ``rotary``'s gradient is ``rotary`` with
+``inverse=True``; the cache is for serving, and its attention has no gradient.
+
+Sequences: ``table`` [seqs, width] int32 holds the pages of each, 64 tokens a page; ``lengths`` [seqs] int32 their tokens, those
+of the call among them; with ``starts`` [seqs + 1] int32 the rows starts[s] .. starts[s + 1] - 1 of the operands are the last
+tokens of sequence s, without it row s is the one new token of sequence s. They are device data and not looked at by
+the host: pages outside the cache are left out, rows of no sequence are neither read nor written. The pages that ``kv_append``
+writes to must belong to one sequence each; pages that are only read may be shared.
+"""
+from __future__ import annotations
+
+import collections
+import ctypes
+
+import torch
+
+from . import DTYPES, NVFP4Error, _check, lib
+from .layer import _no_graph, _ptr, _run, _space
+
+PAGE = 64  # tokens of a page
+KVCache = collections.namedtuple("KVCache", "k v k_scales v_scales")
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+_SCALES = (torch.float8_e8m0fnu, torch.uint8)
+_AXES = 4
+
+
+class _RotaryArgs(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("xs", ctypes.c_int64), ("xh", ctypes.c_int64), ("y", ctypes.c_void_p),
+        ("ys", ctypes.c_int64), ("yh", ctypes.c_int64), ("dtype", ctypes.c_int), ("tokens", ctypes.c_int64),
+        ("heads", ctypes.c_int), ("dim", ctypes.c_int), ("positions", ctypes.c_void_p), ("positions64", ctypes.c_int),
+        ("axes", ctypes.c_int), ("sections", ctypes.c_int * _AXES), ("base", ctypes.c_double), ("inverse", ctypes.c_int),
+        ("stream", ctypes.c_void_p),
+    ]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+        ("v_scales", ctypes.c_void_p), ("pages", ctypes.c_int64), ("kv_heads", ctypes.c_int), ("dim", ctypes.c_int),
+    ]
+
+
+class _Sequences(ctypes.Structure):
+    _fields_ = [
+        ("table", ctypes.c_void_p), ("ldt", ctypes.c_int64), ("lengths", ctypes.c_void_p), ("starts", ctypes.c_void_p),
+        ("seqs", ctypes.c_int), ("width", ctypes.c_int),
+    ]
+
+
+def _heads(t, name, dtypes, dev=None, shape=None):
+    """Checks a [tokens, heads, dim] operand with unit column stride; returns its token and head strides."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3 or not t.is_cuda or t.dtype not in dtypes:
+        raise NVFP4Error(f"{name} must be a [tokens, heads, dim] CUDA tensor of {' or '.join(str(d) for d in dtypes)}")
+    if dev is not None and t.device != dev:
+        raise NVFP4Error(f"{name} must be on {dev}")
+    tokens, heads, dim = t.shape
+    if shape is not None and (tokens, heads, dim) != shape:
+        raise NVFP4Error(f"{name} must be {list(shape)}, got {[tokens, heads, dim]}")
+    st, sh, sc = t.stride()
+    if (sc != 1 and dim > 1) or (heads > 1 and sh < dim) or (tokens > 1 and st < dim):
+        raise NVFP4Error(f"{name} must have unit column stride and rows that do not overlap")
+    return st, sh
+
+
+def rotary(x: torch.Tensor, positions: torch.Tensor, *, sections=None, base: float = 10000.0, inverse: bool = False,
+           out=None, stream=None) -> torch.Tensor:
+    """Rotary positions of ``x`` ([tokens, heads, dim] bf16 or fp32): with R = 2 * sum(sections) <= dim, columns j and j +
+    R/2 are turned by the angle positions[axis(j)] * base^(-2j/R), columns from R on pass. ``positions`` is [tokens] or
+    [axes, tokens] (up to four axes) int32 or int64, contiguous; ``sections`` the number of consecutive pairs of each axis
+    (None: one axis, all dim // 2 pairs). Angles are binary64, so far positions lose nothing. ``inverse`` turns back:
+    the gradient. Returns y, in ``out`` if given: x itself (in place), or a contiguous tensor."""
+    xs, xh = _heads(x, "x", DTYPES)
+    tokens, heads, dim = x.shape
+    dev = x.device
+    if (not isinstance(positions, torch.Tensor) or positions.dtype not in (torch.int32, torch.int64) or positions.device != dev
+            or positions.dim() not in (1, 2) or positions.shape[-1] != tokens or not positions.is_contiguous()):
+        raise NVFP4Error(f"positions must be a contiguous [{tokens}] or [axes, {tokens}] int32 or int64 tensor on {dev}")
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if sections is None:
+        sections = (dim // 2,)
+        if dim % 2:
+            raise NVFP4Error("an odd dim needs sections")
+    if not 1 <= axes <= _AXES or len(sections) != axes:
+        raise NVFP4Error(f"sections must give the pairs of each of {axes} axes (at most {_AXES})")
+    if any(n < 0 for n in sections) or not 0 < 2 * sum(sections) <= dim:
+        raise NVFP4Error(f"the sections must be of one to {dim // 2} pairs together")
+    if out is not None:
+        if not isinstance(out, torch.Tensor) or out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
+            raise NVFP4Error(f"out must be a {[tokens, heads, dim]} {x.dtype} tensor on {dev}")
+        if out.data_ptr() == x.data_ptr():
+            if out.stride() != x.stride():
+                raise NVFP4Error("out may be x itself, not another view of its memory")
+            if tokens > 1 and heads > 1 and xs < (heads - 1) * xh + dim and xh < (tokens - 1) * xs + dim:
+                raise NVFP4Error("in place, the rows of x may not overlap")
+        elif not out.is_contiguous():
+            raise NVFP4Error("out must be contiguous or x itself")
+    _no_graph(x, out)
+
+    def call(st):
+        y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+        ys, yh, _ = y.stride()
+        a = _RotaryArgs(x.data_ptr(), xs, xh, y.data_ptr(), ys, yh, DTYPES[x.dtype], tokens, heads, dim, positions.data_ptr(),
+                        int(positions.dtype == torch.int64), axes, (ctypes.c_int * _AXES)(*sections), base, int(inverse), st)
+        _check(lib().nvfp4_rotary(ctypes.byref(a)))
+        return y
+
+    return _run(dev, stream, call)
+
+
+def kv_cache(pages: int, kv_heads: int, dim: int, device="cuda") -> KVCache:
+    """An empty cache: k [pages, kv_heads, 64, dim] and v [pages, kv_heads, dim, 64] E4M3 codes (zeros), k_scales and
+    v_scales [pages, kv_heads] E8M0, one power of two per page and head. dim % 16 == 0, dim <= 256."""
+    if pages < 0 or kv_heads <= 0 or dim <= 0 or dim % 16 or dim > 256:
+        raise NVFP4Error("a cache has at least one head, and a dim that is a multiple of 16 up to 256")
+    def zeros(*shape):
+        return torch.zeros(shape, dtype=torch.uint8, device=device)
+    return KVCache(zeros(pages, kv_heads, PAGE, dim).view(_CODES[0]), zeros(pages, kv_heads, dim, PAGE).view(_CODES[0]),
+                   zeros(pages, kv_heads).view(_SCALES[0]), zeros(pages, kv_heads).view(_SCALES[0]))
+
+
+def _cache(cache, dev):
+    """Checks a cache; returns its C form, heads and dim."""
+    if not isinstance(cache, (tuple, list)) or len(cache) != 4 or not all(isinstance(t, torch.Tensor) for t in cache):
+        raise NVFP4Error("the cache must be (k, v, k_scales, v_scales), as kv_cache makes it")
+    k, v, ks, vs = cache
+    if k.dim() != 4 or k.shape[2] != PAGE:
+        raise NVFP4Error(f"the cache's k must be [pages, kv_heads, {PAGE}, dim]")
+    pages, heads, _, dim = k.shape
+    if v.shape != (pages, heads, dim, PAGE) or ks.shape != (pages, heads) or vs.shape != (pages, heads):
+        raise NVFP4Error(f"the cache's v must be {[pages, heads, dim, PAGE]} and its scales {[pages, heads]}")
+    for t, dtypes in ((k, _CODES), (v, _CODES), (ks, _SCALES), (vs, _SCALES)):
+        if t.device != dev or t.dtype not in dtypes or not t.is_contiguous():
+            raise NVFP4Error(f"the cache's codes must be contiguous E4M3 and its scales contiguous E8M0 tensors on {dev}")
+    return _Cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, heads, dim), heads, dim
+
+
+def _ints(t, name, n, dev):
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != dev or tuple(t.shape) != (n,)
+            or not t.is_contiguous()):
+        raise NVFP4Error(f"{name} must be a contiguous [{n}] int32 tensor on {dev}")
+
+
+def _sequences(table, lengths, starts, tokens, dev):
+    if (not isinstance(table, torch.Tensor) or table.dim() != 2 or table.dtype != torch.int32 or table.device != dev
+            or (table.shape[1] > 1 and table.stride(1) != 1) or (table.shape[0] > 1 and table.stride(0) < table.shape[1])):
+        raise NVFP4Error(f"table must be a [seqs, width] int32 tensor with unit column stride on {dev}")
+    seqs, width = table.shape
+    _ints(lengths, "lengths", seqs, dev)
+    if starts is not None:
+        _ints(starts, "starts", seqs + 1, dev)
+    elif tokens != seqs:
+        raise NVFP4Error(f"without starts there is one token for each of the {seqs} sequences, got {tokens}")
+    if tokens and seqs and not width:
+        raise NVFP4Error("the table has no columns")
+    return _Sequences(table.data_ptr(), table.stride(0), lengths.data_ptr(), _ptr(starts), seqs, width)
+
+
+def kv_append(cache, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor, starts=None, *,
+              stream=None):
+    """Writes the keys and values ``K`` and ``V`` ([tokens, kv_heads, dim], bf16 or fp32) of the sequences' last tokens
+    into the cache, and returns it. Per block of 64 tokens and head the scale is the smallest power of two under which
+    nothing saturates; where a block already holds tokens of the sequence it does not fall, and their codes are
+    rounded to the new one if it grows."""
+    kt, kh = _heads(K, "K", DTYPES)
+    dev = K.device
+    vt, vh = _heads(V, "V", (K.dtype,), dev, tuple(K.shape))
+    c, heads, dim = _cache(cache, dev)
+    tokens = K.shape[0]
+    if K.shape[1:] != (heads, dim):
+        raise NVFP4Error(f"K must be [tokens, {heads}, {dim}], as the cache")
+    q = _sequences(table, lengths, starts, tokens, dev)
+    _no_graph(K, V)
+
+    def call(st):
+        _check(lib().nvfp4_kv_append(ctypes.byref(c), ctypes.byref(q), K.data_ptr(), kt, kh, V.data_ptr(), vt, vh,
+                                     DTYPES[K.dtype], tokens, st))
+        return cache
+
+    return _run(dev, stream, call)
+
+
+def attention_workspace_bytes(tokens: int, seqs: int, width: int, heads: int, kv_heads: int, dim: int) -> int:
+    return int(lib().nvfp4_attention_workspace_bytes(tokens, seqs, width, heads, kv_heads, dim))
+
+
+def attention(Q: torch.Tensor, cache, table: torch.Tensor, lengths: torch.Tensor, starts=None, *, scale=None,
+              causal: bool = True, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """Attention of ``Q`` ([tokens, heads, dim] bf16; heads a multiple of the cache's) over the cache: softmax(scale * Q
+    K^T) V over the tokens that a row sees, [tokens, heads, dim] bf16, in ``out`` if given (contiguous). ``causal``: row i of
+    a sequence's n sees its first length - n + i + 1 tokens; else all of them (the cached states of an encoder). ``scale``
+    None: dim^-0.5. A row that sees no token gives zeros; one that sees a block written with a NaN or an infinity
+    gives NaN."""
+    qt, qh = _heads(Q, "Q", (torch.bfloat16,))
+    dev = Q.device
+    c, kv_heads, dim = _cache(cache, dev)
+    tokens, heads, qdim = Q.shape
+    if qdim != dim or heads % kv_heads or not heads:
+        raise NVFP4Error(f"Q must be [tokens, heads, {dim}] with a multiple of {kv_heads} heads")
+    q = _sequences(table, lengths, starts, tokens, dev)
+    if out is not None and (not isinstance(out, torch.Tensor) or out.shape != Q.shape or out.dtype != torch.bfloat16
+                            or out.device != dev or not out.is_contiguous()):
+        raise NVFP4Error(f"out must be a contiguous {list(Q.shape)} bf16 tensor on {dev}")
+    _no_graph(Q, out)
+
+    def call(st):
+        O = torch.empty(Q.shape, dtype=torch.bfloat16, device=dev) if out is None else out
+        ws, nbytes = _space(workspace, attention_workspace_bytes(tokens, q.seqs, q.width, heads, kv_heads, dim), dev)
+        _check(lib().nvfp4_attention(ctypes.byref(c), ctypes.byref(q), Q.data_ptr(), qt, qh, heads, tokens,
+                                     dim ** -0.5 if scale is None else scale, int(causal), O.data_ptr(), _ptr(ws), nbytes, st))
+        return O
+
+    return _run(dev, stream, call)
