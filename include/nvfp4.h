@@ -509,6 +509,47 @@ int nvfp4_attention(const nvfp4_kv_cache_t *cache, const nvfp4_sequences_t *seqs
                     size_t workspace_bytes, void *stream);
 size_t nvfp4_attention_workspace_bytes(int64_t tokens, int seqs, int width, int heads, int kv_heads, int dim);
 
+/* A layer of experts with NVFP4 weights for a few tokens, whole: for token t with logits l[t][0 .. experts - 1]
+ *   its top_k largest logits choose experts, equal ones by the lower index; an expert of logit -inf is never chosen,
+ *   so a token may have fewer, or none (then y = residual, or zeros);
+ *   w = softmax(l) over all experts, or the logistic function of l (NVFP4_SCORE_SIGMOID), of the chosen; with
+ *   normalize = 1 divided by their sum over the chosen;
+ *   h = act(z), z = alpha1_e (x Wq1_e^T), or, gated, act(z[:inner]) * z[inner:], rounded to bf16;
+ *   y = residual + sum over the chosen of w alpha2_e (h Wq2_e^T), fp32 sums, rounded once to bf16.
+ * A NaN among a token's logits is chosen first and makes NaN of its y. x [tokens][width] bf16; logits [tokens][experts] bf16
+ * or fp32 with `ldl`; up: the experts' [inner, or gated 2 inner][width] weights one after the other, as the quantiser writes
+ * them (codes, scales, and one alpha per expert); down: [width][inner]; residual (nullable) as y, with `ldr`, may be y
+ * itself (contiguous). width, inner % 16 == 0 and <= 2^21, experts <= 512, top_k <= min(32, experts), tokens * top_k <= 8192,
+ * ldx, ldl, ldr < 2^31, an expert's weights below 2^31 values (else NVFP4_ERR_SHAPE). Codes 8-byte aligned. No expert's
+ * weights are read that no token chose. Scratch: nvfp4_moe_workspace_bytes. */
+enum nvfp4_scoring { NVFP4_SCORE_SOFTMAX = 0, NVFP4_SCORE_SIGMOID = 1 };
+typedef struct nvfp4_moe_args {
+    const void *x;
+    int64_t ldx;
+    const void *logits;
+    int64_t ldl;
+    int logits_dtype; /* NVFP4_DTYPE_BF16 or _F32 */
+    int64_t tokens, width, inner;
+    int experts, top_k;
+    const uint8_t *up_codes, *up_scales;
+    const float *up_alpha;
+    const uint8_t *down_codes, *down_scales;
+    const float *down_alpha;
+    int activation; /* enum nvfp4_activation */
+    int gated;
+    int scoring; /* enum nvfp4_scoring */
+    int normalize;
+    const void *residual;
+    int64_t ldr;
+    void *y;
+    void *workspace;
+    size_t workspace_bytes;
+    void *stream;
+} nvfp4_moe_args_t;
+
+int nvfp4_moe(const nvfp4_moe_args_t *args);
+size_t nvfp4_moe_workspace_bytes(int64_t tokens, int64_t width, int64_t inner, int experts, int top_k);
+
 /* Text of an nvfp4_error value. */
 const char *nvfp4_status_string(int status);
 

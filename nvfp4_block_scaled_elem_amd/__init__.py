@@ -114,6 +114,10 @@ def lib() -> ctypes.CDLL:
         L.nvfp4_attention.restype = i32
         L.nvfp4_attention_workspace_bytes.argtypes = [i64, i32, i32, i32, i32, i32]
         L.nvfp4_attention_workspace_bytes.restype = sz
+        L.nvfp4_moe.argtypes = [vp]
+        L.nvfp4_moe.restype = i32
+        L.nvfp4_moe_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+        L.nvfp4_moe_workspace_bytes.restype = sz
         L.nvfp4_status_string.argtypes = [i32]
         L.nvfp4_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -400,4 +404,5 @@ def matmul(X: torch.Tensor, codes: torch.Tensor, scales: torch.Tensor, alpha: to
 
 from .layer import (dequantize_mxfp8, linear, linear_grad, linear_grad_workspace_bytes,  # noqa: E402
                     linear_workspace_bytes, quantize_mxfp8, rms_norm, rms_norm_grad, rms_norm_grad_workspace_bytes)
-from .decoder import KVCache, attention, attention_workspace_bytes, kv_append, kv_cache, rotary  # noqa: E402
+from .decoder import (KVCache, attention, attention_workspace_bytes, kv_append, kv_cache, moe,  # noqa: E402
+                      moe_workspace_bytes, rotary)

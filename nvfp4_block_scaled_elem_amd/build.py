@@ -15,7 +15,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libnvfp4.so")
 SOURCES = ["quant_kernels.hip", "soar_kernel.hip", "gemm_kernels.hip", "gptq_kernels.hip", "norm_kernels.hip",
-           "linear_kernels.hip", "cache_kernels.hip", "attention_kernels.hip", "api.cpp", "layer_api.cpp", "decoder_api.cpp", "noalloc.hip"]
+           "linear_kernels.hip", "cache_kernels.hip", "attention_kernels.hip", "moe_kernels.hip", "api.cpp", "layer_api.cpp", "decoder_api.cpp", "noalloc.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [

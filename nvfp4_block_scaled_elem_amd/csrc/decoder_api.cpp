@@ -5,6 +5,7 @@
 //   nvfp4_rotary    : k_rotary
 //   nvfp4_kv_append : k_kv_append
 //   nvfp4_attention : k_attn_rows, or k_attn_split -> k_attn_join
+//   nvfp4_moe       : k_moe_route -> k_moe_product (up) -> k_moe_product (down) -> k_moe_sum
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -147,4 +148,60 @@ NVFP4_API int nvfp4_attention(const nvfp4_kv_cache_t *c, const nvfp4_sequences_t
     const nvfp4::AttnPlan plan = nvfp4::plan_attention(tokens, s->seqs, s->width, c->kv_heads, p.group, c->dim);
     return with_scratch(workspace, workspace_bytes, plan.part_bytes + plan.ml_bytes, st,
                         [&](void *ws) { return nvfp4::launch_attention(p, ws, st); });
+}
+
+namespace {
+
+constexpr int64_t kMaxSide = (int64_t)1 << 21;  // of an expert's products
+
+int check_experts(int64_t tokens, int64_t width, int64_t inner, int experts, int top_k) {
+    if (tokens < 0 || width <= 0 || inner <= 0 || experts <= 0 || top_k <= 0) return NVFP4_ERR_INVALID_ARG;
+    if (width % 16 != 0 || inner % 16 != 0 || width > kMaxSide || inner > kMaxSide) return NVFP4_ERR_SHAPE;
+    if (experts > nvfp4::kMoeMaxExperts || top_k > nvfp4::kMoeMaxTopK || top_k > experts) return NVFP4_ERR_SHAPE;
+    if (tokens > nvfp4::kMoeMaxPairs || tokens * top_k > nvfp4::kMoeMaxPairs) return NVFP4_ERR_SHAPE;
+    if (2 * width * inner >= ((int64_t)1 << 31)) return NVFP4_ERR_SHAPE;
+    // work-groups of 512 threads: one for 16 rows of each chosen expert
+    if ((width > inner ? width : inner) / 16 * experts >= ((int64_t)1 << 23)) return NVFP4_ERR_SHAPE;
+    return NVFP4_OK;
+}
+
+}  // namespace
+
+NVFP4_API size_t nvfp4_moe_workspace_bytes(int64_t tokens, int64_t width, int64_t inner, int experts, int top_k) {
+    if (check_experts(tokens, width, inner, experts, top_k) != NVFP4_OK || tokens == 0) return 0;
+    return nvfp4::moe_workspace(tokens, width, inner, top_k);
+}
+
+NVFP4_API int nvfp4_moe(const nvfp4_moe_args_t *a) {
+    if (!a) return NVFP4_ERR_INVALID_ARG;
+    const int c = check_experts(a->tokens, a->width, a->inner, a->experts, a->top_k);
+    if (c != NVFP4_OK) return c;
+    if (!plain_dtype(a->logits_dtype) || a->activation < NVFP4_ACT_NONE || a->activation > NVFP4_ACT_GELU ||
+        (a->gated != 0 && (a->gated != 1 || a->activation == NVFP4_ACT_NONE)) || (a->normalize != 0 && a->normalize != 1) ||
+        (a->scoring != NVFP4_SCORE_SOFTMAX && a->scoring != NVFP4_SCORE_SIGMOID) || !aligned(a->workspace, 256))
+        return NVFP4_ERR_INVALID_ARG;
+    if (a->tokens == 0) return NVFP4_OK;
+    if (!a->x || !a->logits || !a->up_codes || !a->up_scales || !a->up_alpha || !a->down_codes || !a->down_scales ||
+        !a->down_alpha || !a->y)
+        return NVFP4_ERR_INVALID_ARG;
+    if (a->tokens > 1 && (a->ldx < a->width || a->ldl < a->experts || (a->residual && a->ldr < a->width)))
+        return NVFP4_ERR_INVALID_ARG;
+    if (a->tokens > 1 && (a->ldx >= ((int64_t)1 << 31) || a->ldl >= ((int64_t)1 << 31) || (a->residual && a->ldr >= ((int64_t)1 << 31))))
+        return NVFP4_ERR_SHAPE;
+    if (!aligned(a->x, 2) || !aligned(a->logits, width(a->logits_dtype)) || !aligned(a->up_codes, 8) || !aligned(a->down_codes, 8) ||
+        !aligned(a->up_alpha, 4) || !aligned(a->down_alpha, 4) || !aligned(a->residual, 2) || !aligned(a->y, 2))
+        return NVFP4_ERR_INVALID_ARG;
+    nvfp4::MoeArgs p = {};
+    p.x = a->x, p.logits = a->logits, p.logits_f32 = a->logits_dtype == NVFP4_DTYPE_F32;
+    p.up = {a->up_codes, a->up_scales, a->up_alpha};
+    p.down = {a->down_codes, a->down_scales, a->down_alpha};
+    p.res = static_cast<const uint16_t *>(a->residual), p.y = static_cast<uint16_t *>(a->y);
+    p.tokens = a->tokens, p.width = a->width, p.inner = a->inner;
+    p.ldx = a->tokens > 1 ? a->ldx : a->width, p.ldl = a->tokens > 1 ? a->ldl : a->experts;
+    p.ldr = a->tokens > 1 ? a->ldr : a->width;
+    p.experts = a->experts, p.top_k = a->top_k, p.act = a->activation, p.gated = a->gated;
+    p.sigmoid = a->scoring == NVFP4_SCORE_SIGMOID, p.normalize = a->normalize;
+    hipStream_t st = static_cast<hipStream_t>(a->stream);
+    return with_scratch(a->workspace, a->workspace_bytes, nvfp4::moe_workspace(p.tokens, p.width, p.inner, p.top_k), st,
+                        [&](void *ws) { return nvfp4::launch_moe(p, ws, st); });
 }

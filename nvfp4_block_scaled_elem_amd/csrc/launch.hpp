@@ -243,6 +243,30 @@ struct AttnPlan {
 AttnPlan plan_attention(int64_t tokens, int seqs, int width, int kv_heads, int group, int dim);
 hipError_t launch_attention(const AttnArgs &p, void *ws, hipStream_t stream);
 
+// ---- experts (moe_kernels.hip) ----
+
+constexpr int kMoeMaxExperts = 512, kMoeMaxPairs = 8192, kMoeMaxTopK = 32;
+struct MoeWeights {
+    const uint8_t *codes, *scales;
+    const float *alpha;  // per expert
+};
+struct MoeArgs {
+    const void *x, *logits;
+    MoeWeights up, down;
+    const uint16_t *res;
+    uint16_t *y;
+    int64_t tokens, width, inner, ldx, ldl, ldr;
+    int experts, top_k, act, gated, sigmoid, normalize, logits_f32;
+    // scratch, set by the launcher: of each pair (token, choice) the expert (-1: none), its weight, the activations between
+    // the products, its part of y
+    int *ids;
+    float *weights;
+    uint16_t *h;
+    float *z;
+};
+size_t moe_workspace(int64_t tokens, int64_t width, int64_t inner, int top_k);
+hipError_t launch_moe(const MoeArgs &p, void *ws, hipStream_t stream);
+
 hipError_t launch_dequant(const uint8_t *codes, const uint8_t *scales, const float *alpha, int64_t nblk, void *out,
                           bool out_f32, hipStream_t stream);
 

@@ -1,0 +1,346 @@
+// gfx950 layer of experts with NVFP4 weights, for a few tokens.
+//
+// For token t with logits l[t][0..E-1]: its top_k largest logits choose experts (equal ones by the lower index; -inf
+// never), weighted by p = softmax(l) over all experts or the logistic function s(l), divided by their sum where
+// they are normalised:
+//     y[t] = residual[t] + sum_j w_j alpha2_e (W2_e h_j),  h_j = act(alpha1_e W1_e x_t)
+// (gated: act of the first `inner` rows of W1_e x times the others). Weights are those of the product kernels, e2m1(code)
+// e4m3(scale), exact in bf16; x is bf16; sums are fp32 on the matrix cores; h is rounded to bf16, which the second
+// product takes (its error, 2^-9 of a term, is of the size of y's own rounding).
+//
+// Bound by reading the chosen experts' weights, each once however many tokens chose it.
+//   k_moe_route: experts and weights of each token.
+//   k_moe_product, twice: a work-group has 16 weight rows (gated: 16 gate rows and their 16 up rows) of one chosen
+//     expert and the pairs (token, choice) that chose it, 16 at a time as the columns of v_mfma_f32_16x16x32_bf16; its waves
+//     split the sum and are joined through LDS in wave order.
+//   k_moe_sum: y from the pairs' parts.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "act.hpp"
+#include "codec.hpp"
+#include "launch.hpp"
+#include "mx.hpp"
+
+namespace nvfp4 {
+
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kWaves = 8, kThreads = 64 * kWaves;
+constexpr float kLog2e = 1.4426950408889634f;
+
+// ------------------------------------------------------------------------------------------- routing
+
+// A logit's place in the order: larger is first, 0 (-inf) never; NaN before all numbers, so that it is chosen and
+// shows. -0 is 0.
+__device__ __forceinline__ uint32_t order_key(float l) {
+    if (l == -__builtin_inff()) return 0u;
+    const uint32_t b = __float_as_uint(l + 0.0f);
+    if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
+    return v;
+}
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
+    return v;
+}
+
+// The experts of token t, by one wave: lane j < top_k gets choice j (-1: none) and its weight. Lane l holds the logits
+// l, l + 64, ...
+__device__ __forceinline__ void route(const MoeArgs &p, int64_t t, int &id, float &w) {
+    constexpr int kMost = kMoeMaxExperts / 64;
+    const int lane = threadIdx.x & 63;
+    float l[kMost];
+    uint32_t key[kMost];
+#pragma unroll
+    for (int r = 0; r < kMost; ++r) {
+        const int e = lane + 64 * r;
+        l[r] = -__builtin_inff();
+        if (e < p.experts)
+            l[r] = p.logits_f32 ? static_cast<const float *>(p.logits)[t * p.ldl + e]
+                                : __uint_as_float((uint32_t)static_cast<const uint16_t *>(p.logits)[t * p.ldl + e] << 16);
+        key[r] = order_key(l[r]);
+    }
+    float all = 0.0f, top = 0.0f;
+    if (!p.sigmoid) {
+        uint32_t k = 0u;
+#pragma unroll
+        for (int r = 0; r < kMost; ++r) k = max(k, key[r]);
+        k = wave_max(k);
+        top = k == 0xFFFFFFFFu ? __builtin_nanf("") : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+        if (!p.normalize) {
+#pragma unroll
+            for (int r = 0; r < kMost; ++r) all += key[r] ? __builtin_amdgcn_exp2f((l[r] - top) * kLog2e) : 0.0f;
+            all = wave_sum(all);
+        }
+    }
+    id = -1;
+    float mine = 0.0f;
+    for (int j = 0; j < p.top_k; ++j) {
+        uint32_t k = 0u;
+#pragma unroll
+        for (int r = 0; r < kMost; ++r) k = max(k, key[r]);
+        k = wave_max(k);
+        if (k == 0u) break;
+        bool found = false;
+#pragma unroll
+        for (int r = 0; r < kMost; ++r) {  // the lowest index: e = lane + 64 r
+            const uint64_t who = __ballot(key[r] == k);
+            if (!found && who) {
+                found = true;
+                const int first = __ffsll((unsigned long long)who) - 1;
+                const float v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(l[r]), first));
+                if (lane == j) id = 64 * r + first, mine = v;
+                if (lane == first) key[r] = 0u;
+            }
+        }
+    }
+    // softmax: e^(l - top); logistic function: e^min(l, 0) / (1 + e^-|l|), against the largest where they are normalised
+    // (all of them may be below the smallest number).
+    float e = 0.0f;
+    if (!p.sigmoid) {
+        e = id >= 0 ? __builtin_amdgcn_exp2f((mine - top) * kLog2e) : 0.0f;
+    } else {
+        float m = 0.0f;
+        if (p.normalize) {
+            m = id >= 0 ? fminf(mine, 0.0f) : -__builtin_inff();
+#pragma unroll
+            for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k));
+            if (m == -__builtin_inff()) m = 0.0f;
+        }
+        const float low = mine < 0.0f ? mine : 0.0f;
+        e = id >= 0 ? __builtin_amdgcn_exp2f((low - m) * kLog2e) / (1.0f + __builtin_amdgcn_exp2f(-fabsf(mine) * kLog2e)) : 0.0f;
+    }
+    if (p.normalize) all = wave_sum(e);
+    w = p.normalize || !p.sigmoid ? e / all : e;
+}
+
+__global__ __launch_bounds__(256) void k_moe_route(MoeArgs p) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+    if (t >= p.tokens) return;
+    int id;
+    float w;
+    route(p, t, id, w);
+    if (lane < p.top_k) p.ids[t * p.top_k + lane] = id, p.weights[t * p.top_k + lane] = w;
+}
+
+// ------------------------------------------------------------------------------------------- products
+
+constexpr int kChunk = 128, kChunkLds = 16 * 64 + 16 * 8;  // k per chunk; LDS bytes of 16 rows' codes and scales
+
+// 16-byte piece q (0..3) of row r of a chunk's codes in LDS: the 16 lanes that read one q of 16 rows meet no bank twice.
+__device__ __forceinline__ int code_place(int r, int q) { return r * 64 + ((q ^ ((r >> 2) & 3)) << 4); }
+
+// The chosen experts in order: the number `nth` of them (-1: there are not so many), and its pairs into `list`. By the whole
+// work-group; `seen` has a word per expert.
+__device__ __forceinline__ int take_expert(const MoeArgs &p, int nth, int *seen, uint16_t *list, int *count) {
+    const int tid = threadIdx.x, lane = tid & 63, pairs = (int)p.tokens * p.top_k;
+    for (int e = tid; e < p.experts; e += kThreads) seen[e] = 0;
+    if (tid == 0) *count = 0;
+    __syncthreads();
+    for (int i = tid; i < pairs; i += kThreads) {
+        const int e = p.ids[i];
+        if (e >= 0) seen[e] = 1;
+    }
+    __syncthreads();
+    int before = 0, mine = -1;
+    for (int e0 = 0; e0 < p.experts && mine < 0; e0 += 64) {
+        uint64_t who = __ballot(e0 + lane < p.experts && seen[e0 + lane]);
+        const int n = __popcll(who);
+        if (before + n > nth) {
+            for (int k = before; k < nth; ++k) who &= who - 1;
+            mine = e0 + __ffsll((unsigned long long)who) - 1;
+        }
+        before += n;
+    }
+    if (mine < 0) return -1;
+    // The pairs' order in the list decides their column alone, which no result depends on.
+    for (int i = tid; i < pairs; i += kThreads)
+        if (p.ids[i] == mine) list[atomicAdd(count, 1)] = (uint16_t)i;
+    __syncthreads();
+    return mine;
+}
+
+// NT: 2 if gated. SECOND: the product with W2, else with W1.
+template <int NT, bool SECOND>
+__global__ __launch_bounds__(kThreads) void k_moe_product(MoeArgs p, int tiles) {
+    constexpr int kStage = kWaves * NT * kChunkLds, kSums = kWaves * NT * 1024;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kStage > kSums ? kStage : kSums];
+    __shared__ int seen[kMoeMaxExperts];
+    __shared__ uint16_t list[kMoeMaxPairs];
+    __shared__ int count;
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int expert = take_expert(p, blockIdx.x / tiles, seen, list, &count);
+    if (expert < 0) return;
+    const int64_t K = SECOND ? p.inner : p.width, F = SECOND ? p.width : p.inner;
+    const int64_t f0 = (int64_t)(blockIdx.x % tiles) * 16, nch = (K + kChunk - 1) / kChunk;
+    const MoeWeights &W = SECOND ? p.down : p.up;
+    const uint8_t *codes = W.codes + expert * (NT * F * (K / 2)), *scales = W.scales + expert * (NT * F * (K / 16));
+    const float alpha = W.alpha[expert];
+    const uint16_t *x = SECOND ? p.h : static_cast<const uint16_t *>(p.x);
+    const int64_t ldx = SECOND ? p.inner : p.ldx;
+    uint8_t *const wl = lds + wave * NT * kChunkLds;
+    const int64_t crow = min(F - 1, f0 + (lane >> 2)), srow = min(F - 1, f0 + r16);
+    const int pairs = count;
+    for (int c0 = 0; c0 < pairs; c0 += 16) {
+        const int pair = c0 + r16 < pairs ? list[c0 + r16] : -1;
+        const uint16_t *xr = x + (int64_t)(SECOND ? max(pair, 0) : max(pair, 0) / p.top_k) * ldx;
+        f32x4 acc[NT] = {};
+        uint4 cv[NT];
+        uint2 sv[NT];
+        auto load_w = [&](int64_t ch) __attribute__((always_inline)) {
+            const int64_t kc = kChunk * ch + 32 * (lane & 3), ks = kChunk * ch;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const uint8_t *c = codes + ((crow + j * F) * K + kc) / 2, *s = scales + ((srow + j * F) * K + ks) / 16;
+                cv[j] = make_uint4(0u, 0u, 0u, 0u);
+                sv[j] = make_uint2(0u, 0u);
+                if (kc + 32 <= K) {
+                    cv[j] = load16(c);
+                } else if (kc < K) {  // the row's last 16
+                    const uint2 d = load8b(c);
+                    cv[j].x = d.x, cv[j].y = d.y;
+                }
+                if (lane >= 16) continue;
+                if (ks + kChunk <= K) {
+                    sv[j] = load8b(s);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (ks + 16 * e < K) (e < 4 ? sv[j].x : sv[j].y) |= (uint32_t)s[e] << (8 * (e & 3));
+                }
+            }
+        };
+        int64_t ch = wave;
+        if (ch < nch) load_w(ch);
+#pragma unroll 1
+        for (; ch < nch; ch += kWaves) {
+            const int64_t k = kChunk * ch + 32 * g;
+            uint4 xv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                xv[i] = make_uint4(0u, 0u, 0u, 0u);
+                if (pair >= 0 && k + 8 * i < K) xv[i] = load16(xr + k + 8 * i);
+            }
+            wave_handover();
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                uint8_t *const q = wl + j * kChunkLds;
+                *reinterpret_cast<uint4 *>(q + code_place(lane >> 2, lane & 3)) = cv[j];
+                if (lane < 16) *reinterpret_cast<uint2 *>(q + 1024 + 8 * lane) = sv[j];
+            }
+            wave_handover();
+            if (ch + kWaves < nch) load_w(ch + kWaves);
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const uint8_t *const q = wl + j * kChunkLds;
+                const uint4 cur = *reinterpret_cast<const uint4 *>(q + code_place(r16, g));
+                const uint32_t sb = *reinterpret_cast<const u16_lds *>(q + 1024 + 8 * r16 + 2 * g);
+                const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8((int)(sb & 0x7F7Fu), false);  // both scales
+                const uint4 w[4] = {dequant8(cur.x, d.x), dequant8(cur.y, d.x), dequant8(cur.z, d.y), dequant8(cur.w, d.y)};
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    acc[j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w[i]),
+                                                                     __builtin_bit_cast(bf16x8, xv[i]), acc[j], 0, 0, 0);
+            }
+        }
+        __syncthreads();  // the sums take the place of the codes
+        float *const red = reinterpret_cast<float *>(lds);
+#pragma unroll
+        for (int j = 0; j < NT; ++j) *reinterpret_cast<f32x4 *>(&red[(wave * NT + j) * 256 + lane * 4]) = acc[j];
+        __syncthreads();
+        // Element r of lane l is weight row 4 (l / 16) + r of the tile, pair l % 16 of the list's sixteen.
+        if (tid < 256) {
+            float z[NT] = {};
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) z[j] += red[(w * NT + j) * 256 + tid];
+            const int l = tid >> 2;
+            const int64_t f = f0 + 4 * (l >> 4) + (tid & 3);
+            if (f < F && c0 + (l & 15) < pairs) {
+                const int q = list[c0 + (l & 15)];
+                if (SECOND) {
+                    p.z[q * F + f] = p.weights[q] * (alpha * z[0]);
+                } else {
+                    float a = act_value(alpha * z[0], p.act);
+                    if (NT == 2) a *= alpha * z[NT - 1];
+                    p.h[q * F + f] = to_bf16(a);
+                }
+            }
+        }
+        __syncthreads();
+    }
+}
+
+// y of eight columns of a token per thread: the parts in the order of the choices.
+__global__ __launch_bounds__(256) void k_moe_sum(MoeArgs p, int per) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, t = i / per, c = 8 * (i % per);
+    if (t >= p.tokens) return;
+    float v[8] = {};
+    if (p.res) {
+        Raw8<uint16_t> r;
+        r.load(p.res + t * p.ldr + c, 8);
+        r.get(v);
+    }
+    for (int j = 0; j < p.top_k; ++j) {
+        const int64_t q = t * p.top_k + j;
+        if (p.ids[q] < 0) break;
+        float z[8];
+        Raw8<float> r;
+        r.load(p.z + q * p.width + c, 8);
+        r.get(z);
+#pragma unroll
+        for (int k = 0; k < 8; ++k) v[k] += z[k];
+    }
+    put8(p.y + t * p.width + c, v, 8);
+}
+
+size_t round256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace
+
+// ids, weights, h, z
+size_t moe_workspace(int64_t tokens, int64_t width, int64_t inner, int top_k) {
+    const size_t pairs = (size_t)(tokens * top_k);
+    return 2 * round256(4 * pairs) + round256(2 * pairs * inner) + round256(4 * pairs * width);
+}
+
+hipError_t launch_moe(const MoeArgs &a, void *ws, hipStream_t st) {
+    MoeArgs p = a;
+    const size_t pairs = (size_t)(p.tokens * p.top_k);
+    uint8_t *at = static_cast<uint8_t *>(ws);
+    p.ids = reinterpret_cast<int *>(at), at += round256(4 * pairs);
+    p.weights = reinterpret_cast<float *>(at), at += round256(4 * pairs);
+    p.h = reinterpret_cast<uint16_t *>(at), at += round256(2 * pairs * p.inner);
+    p.z = reinterpret_cast<float *>(at);
+    hipLaunchKernelGGL(k_moe_route, dim3((unsigned)((p.tokens + 3) / 4)), dim3(256), 0, st, p);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    const int64_t chosen = std::min<int64_t>(p.experts, (int64_t)pairs);
+    const int t1 = (int)((p.inner + 15) / 16), t2 = (int)((p.width + 15) / 16);
+    if (p.gated)
+        hipLaunchKernelGGL((k_moe_product<2, false>), dim3((unsigned)(chosen * t1)), dim3(kThreads), 0, st, p, t1);
+    else
+        hipLaunchKernelGGL((k_moe_product<1, false>), dim3((unsigned)(chosen * t1)), dim3(kThreads), 0, st, p, t1);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    hipLaunchKernelGGL((k_moe_product<1, true>), dim3((unsigned)(chosen * t2)), dim3(kThreads), 0, st, p, t2);
+    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    const int per = (int)(p.width / 8);
+    hipLaunchKernelGGL(k_moe_sum, dim3((unsigned)((p.tokens * per + 255) / 256)), dim3(256), 0, st, p, per);
+    return hipGetLastError();
+}
+
+}  // namespace nvfp4

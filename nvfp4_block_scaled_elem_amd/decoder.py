@@ -1,14 +1,15 @@
-"""A decoder layer's operators between its products: rotary positions, a paged cache of keys and values in 8 bits,
-and attention over it (C ABI: ``include/nvfp4.h``). Marshalling only, like the rest of the binding.
+"""A decoder layer's operators beside its products: rotary positions, a paged cache of keys and values in 8 bits and
+attention over it, and a layer of experts (C ABI: ``include/nvfp4.h``). Marshalling only, like the rest of the binding.
 
     rotary(qk, positions, out=qk)                                # qk: the query and key heads of a product, in place
     cache = kv_cache(pages, kv_heads, dim)                       # codes and scales, all zeros
     kv_append(cache, K, V, table, lengths)                       # a token of each sequence, or, with starts, several
     O = attention(Q, cache, table, lengths)                      # of the same tokens' queries
+    Y = moe(X, logits, up, down, top_k)                          # up, down: stacked (codes, scales, alphas) of the experts
 
 Streams, scratch and autograd are as for the layer operators (``layer.py``): outputs are allocated on the call's stream, and
 where grad mode is on an operand that requires a gradient is refused. ``rotary``'s gradient is ``rotary`` with
-``inverse=True``; the cache is for serving, and its attention has no gradient.
+``inverse=True``; the cache is for serving, and its attention has no gradient, nor has the experts' layer for few tokens.
 
 Sequences: ``table`` [seqs, width] int32 holds the pages of each, 64 tokens a page; ``lengths`` [seqs] int32 their tokens, those
 of the call among them; with ``starts`` [seqs + 1] int32 the rows starts[s] .. starts[s + 1] - 1 of the operands are the last
@@ -24,7 +25,7 @@ import ctypes
 import torch
 
 from . import DTYPES, NVFP4Error, _check, lib
-from .layer import _no_graph, _ptr, _run, _space
+from .layer import ACTIVATIONS, _no_graph, _output, _ptr, _rows, _run, _space
 
 PAGE = 64  # tokens of a page
 KVCache = collections.namedtuple("KVCache", "k v k_scales v_scales")
@@ -218,5 +219,86 @@ def attention(Q: torch.Tensor, cache, table: torch.Tensor, lengths: torch.Tensor
         _check(lib().nvfp4_attention(ctypes.byref(c), ctypes.byref(q), Q.data_ptr(), qt, qh, heads, tokens,
                                      dim ** -0.5 if scale is None else scale, int(causal), O.data_ptr(), _ptr(ws), nbytes, st))
         return O
+
+    return _run(dev, stream, call)
+
+
+class _MoeArgs(ctypes.Structure):
+    _fields_ = [
+        ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("logits", ctypes.c_void_p), ("ldl", ctypes.c_int64),
+        ("logits_dtype", ctypes.c_int), ("tokens", ctypes.c_int64), ("width", ctypes.c_int64), ("inner", ctypes.c_int64),
+        ("experts", ctypes.c_int), ("top_k", ctypes.c_int), ("up_codes", ctypes.c_void_p), ("up_scales", ctypes.c_void_p),
+        ("up_alpha", ctypes.c_void_p), ("down_codes", ctypes.c_void_p), ("down_scales", ctypes.c_void_p),
+        ("down_alpha", ctypes.c_void_p), ("activation", ctypes.c_int), ("gated", ctypes.c_int), ("scoring", ctypes.c_int),
+        ("normalize", ctypes.c_int), ("residual", ctypes.c_void_p), ("ldr", ctypes.c_int64), ("y", ctypes.c_void_p),
+        ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t), ("stream", ctypes.c_void_p),
+    ]
+
+
+SCORING = {"softmax": 0, "sigmoid": 1}  # enum nvfp4_scoring
+
+
+def _experts(W, name, experts, dev, rows=None, cols=None):
+    """Checks stacked NVFP4 weights (codes [experts, rows, cols/2], scales [experts, rows, cols/16], alphas [experts]);
+    returns (rows, cols)."""
+    if not isinstance(W, (tuple, list)) or len(W) != 3 or not all(isinstance(t, torch.Tensor) for t in W):
+        raise NVFP4Error(f"{name} must be (codes, scales, alphas)")
+    codes, scales, alphas = W
+    if codes.dim() != 3 or codes.shape[0] != experts or codes.shape[2] % 8:
+        raise NVFP4Error(f"{name}'s codes must be [{experts}, rows, cols/2] with cols % 16 == 0")
+    n, k = codes.shape[1], 2 * codes.shape[2]
+    if (rows is not None and n != rows) or (cols is not None and k != cols):
+        raise NVFP4Error(f"{name} must be {experts} matrices of {[rows, cols]}, got {[n, k]}")
+    if scales.shape != (experts, n, k // 16) or alphas.shape != (experts,):
+        raise NVFP4Error(f"{name}'s scales must be {[experts, n, k // 16]} and its alphas [{experts}]")
+    for t, dtype in ((codes, torch.uint8), (scales, torch.uint8), (alphas, torch.float32)):
+        if t.dtype != dtype or t.device != dev or not t.is_contiguous():
+            raise NVFP4Error(f"{name} must be contiguous uint8 codes and scales and float32 alphas on {dev}")
+    return n, k
+
+
+def moe_workspace_bytes(tokens: int, width: int, inner: int, experts: int, top_k: int) -> int:
+    return int(lib().nvfp4_moe_workspace_bytes(tokens, width, inner, experts, top_k))
+
+
+def moe(X: torch.Tensor, logits: torch.Tensor, up, down, top_k: int, *, activation="silu", gated: bool = True,
+        scoring: str = "softmax", normalize: bool = True, residual=None, out=None, workspace=None, stream=None):
+    """A layer of experts for a few tokens (tokens * top_k <= 8192): each token's ``top_k`` largest ``logits`` ([tokens,
+    experts] bf16 or fp32; equal ones by the lower index, -inf never) choose its experts, weighted by their ``softmax`` over
+    all experts or the ``sigmoid``, with ``normalize`` divided by their sum; Y = residual + sum of weight * W2 act(W1 x),
+    gated act(gate) * up, [tokens, width] bf16, in ``out`` if given (contiguous; it may be the residual). ``X`` is [tokens,
+    width] bf16; ``up`` and ``down`` are the experts' NVFP4 weights stacked, as ``quantize`` returns them for each: codes
+    [experts, N, K/2], scales [experts, N, K/16], alphas [experts], with (N, K) = (inner, or gated 2 * inner with the
+    gate's rows first, width) and (width, inner). The activations between the products are rounded to bf16. A token of
+    no experts (all logits -inf) gives its residual, or zeros."""
+    ldx = _rows(X, "X", (torch.bfloat16,))
+    tokens, width = X.shape
+    dev = X.device
+    ldl = _rows(logits, "logits", DTYPES, dev)
+    if logits.shape[0] != tokens:
+        raise NVFP4Error(f"logits must be [{tokens}, experts]")
+    experts = logits.shape[1]
+    if activation not in ACTIVATIONS or (gated and activation is None):
+        raise NVFP4Error('activation must be None (not gated), "silu" or "gelu"')
+    if scoring not in SCORING:
+        raise NVFP4Error('scoring must be "softmax" or "sigmoid"')
+    n, _ = _experts(up, "up", experts, dev, None, width)
+    if gated and n % 2:
+        raise NVFP4Error("gated experts have an even number of rows")
+    inner = n // 2 if gated else n
+    _experts(down, "down", experts, dev, width, inner)
+    ldr = 0 if residual is None else _rows(residual, "residual", (torch.bfloat16,), dev, (tokens, width))
+    _output(out, "out", (tokens, width), torch.bfloat16, dev)
+    _no_graph(X, logits, up[2], down[2], residual, out)
+
+    def call(st):
+        Y = torch.empty((tokens, width), dtype=torch.bfloat16, device=dev) if out is None else out
+        ws, nbytes = _space(workspace, moe_workspace_bytes(tokens, width, inner, experts, top_k), dev)
+        a = _MoeArgs(X.data_ptr(), ldx, logits.data_ptr(), ldl, DTYPES[logits.dtype], tokens, width, inner, experts, top_k,
+                     up[0].data_ptr(), up[1].data_ptr(), up[2].data_ptr(), down[0].data_ptr(), down[1].data_ptr(),
+                     down[2].data_ptr(), ACTIVATIONS[activation], int(gated), SCORING[scoring], int(normalize),
+                     _ptr(residual), ldr, Y.data_ptr(), _ptr(ws), nbytes, st)
+        _check(lib().nvfp4_moe(ctypes.byref(a)))
+        return Y
 
     return _run(dev, stream, call)

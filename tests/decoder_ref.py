@@ -107,3 +107,45 @@ def attention(q, cache, table, spans, scale, causal):
             o[(seen & nan[g]).any(1)] = math.nan
             out[first:first + n, h], err[first:first + n, h] = o, e
     return out, err
+
+
+# ------------------------------------------------------------------------------------------- experts
+
+def route(logits, top_k, sigmoid, normalize):
+    """(chosen [tokens, experts] bool, weights, their relative error): the binary32 exponential of a difference d of
+    logits is off by |d| 2^-23 (d and d log2(e) rounded) and a few units; sums of up to 512 terms in six steps."""
+    l = logits.double()
+    T, E = l.shape
+    lower = torch.arange(E, device=l.device)
+    before = ((l[:, None, :] > l[:, :, None]) | ((l[:, None, :] == l[:, :, None]) & (lower[None, :] < lower[:, None]))).sum(-1)
+    chosen = (before < top_k) & (l > -math.inf)
+    p = torch.sigmoid(l) if sigmoid else torch.softmax(l.masked_fill(~(l > -math.inf).any(1)[:, None], 0.0), -1)
+    if normalize:
+        e = torch.where(chosen, p, 0.0)
+        p = e / e.sum(1, keepdim=True).clamp_min(1e-300)
+    top = l.amax(1, keepdim=True).clamp_min(-1e30)
+    err = 2.0 ** -19 + 2.0 ** -21 * torch.nan_to_num((top - l).abs() + l.abs(), 0, 0, 0)
+    return chosen, torch.where(chosen, p, 0.0), err
+
+
+def moe(x, logits, up, down, top_k, act, gated, sigmoid, normalize, res=None):
+    """(y, a bound of the error before y's own rounding): the first product and its activation as in layer_ref.linear,
+    a half step of bf16 on h, the second product's sums, the weights."""
+    chosen, w, ew = route(logits, top_k, sigmoid, normalize)
+    y = torch.zeros(x.shape, dtype=F64, device=x.device) if res is None else res.double()
+    err = ref.U * y.abs()
+    total = torch.zeros_like(y)
+    for e in range(logits.shape[1]):
+        mine = chosen[:, e].nonzero()[:, 0]
+        if len(mine) == 0:
+            continue
+        h, _, eh, _ = ref.linear(x[mine].double(), up[0][e], up[1][e], up[2][e], act=act, gated=gated)
+        eh = eh + (h.abs() + eh) * ref.HALF[torch.bfloat16]
+        W, alpha = ref.weights(down[0][e], down[1][e]), float(down[2][e])
+        o = alpha * (h @ W.T)
+        eo = alpha * (eh @ W.abs().T) + ref.product_error(h.abs() + eh, W, alpha, h.shape[1])
+        share = w[mine, e, None]
+        y[mine] += share * o
+        total[mine] += (share * o).abs()
+        err[mine] += share * (eo + (ew[mine, e, None] + 4 * ref.U) * (o.abs() + eo))
+    return y, err + (top_k + 1) * ref.U * total

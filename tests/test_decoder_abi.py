@@ -113,7 +113,8 @@ def test_attention_rejects(L):
 
 
 @pytest.mark.parametrize("name,struct", [("nvfp4_rotary_args_t", decoder._RotaryArgs), ("nvfp4_kv_cache_t", decoder._Cache),
-                                         ("nvfp4_sequences_t", decoder._Sequences)])
+                                         ("nvfp4_sequences_t", decoder._Sequences),
+                                         ("nvfp4_moe_args_t", decoder._MoeArgs)])
 def test_struct_layouts(tmp_path, name, struct):
     cc = shutil.which("gcc") or shutil.which("cc")
     if cc is None:
@@ -136,3 +137,35 @@ def test_binding_refuses_cpu_tensors():
                  lambda: nv.attention(x, (x, x, x, x), i.view(4, 1), i)):
         with pytest.raises(nv.NVFP4Error):
             call()
+
+
+@pytest.mark.parametrize("kw,err", [
+    (dict(x=None), INVALID), (dict(logits=None), INVALID), (dict(up_codes=None), INVALID), (dict(up_scales=None), INVALID),
+    (dict(up_alpha=None), INVALID), (dict(down_codes=None), INVALID), (dict(down_scales=None), INVALID),
+    (dict(down_alpha=None), INVALID), (dict(y=None), INVALID), (dict(tokens=-1), INVALID), (dict(width=0), INVALID),
+    (dict(inner=0), INVALID), (dict(experts=0), INVALID), (dict(top_k=0), INVALID), (dict(width=72), SHAPE),
+    (dict(inner=40), SHAPE), (dict(width=(1 << 21) + 16), SHAPE), (dict(inner=(1 << 21) + 16), SHAPE), (dict(experts=513), SHAPE),
+    (dict(top_k=9), SHAPE), (dict(experts=64, top_k=33), SHAPE), (dict(tokens=4097), SHAPE), (dict(tokens=1 << 40), SHAPE),
+    (dict(width=1 << 16, inner=1 << 14, ldx=1 << 16), SHAPE), (dict(ldx=63), INVALID), (dict(ldl=7), INVALID),
+    (dict(residual=FAKE, ldr=63), INVALID), (dict(ldx=1 << 31), SHAPE), (dict(ldl=1 << 31), SHAPE),
+    (dict(residual=FAKE, ldr=1 << 31), SHAPE), (dict(logits_dtype=2), INVALID), (dict(activation=3), INVALID),
+    (dict(activation=0), INVALID), (dict(gated=2), INVALID), (dict(normalize=2), INVALID), (dict(scoring=2), INVALID),
+    (dict(workspace=FAKE + 16), INVALID), (dict(x=FAKE + 1), INVALID), (dict(logits=FAKE + 1), INVALID),
+    (dict(logits=FAKE + 2, logits_dtype=1), INVALID), (dict(up_codes=FAKE + 4), INVALID), (dict(down_codes=FAKE + 4), INVALID),
+    (dict(up_alpha=FAKE + 2), INVALID), (dict(down_alpha=FAKE + 2), INVALID), (dict(y=FAKE + 1), INVALID),
+    (dict(residual=FAKE + 1, ldr=64), INVALID), (dict(workspace=FAKE, workspace_bytes=256), WORKSPACE), (dict(tokens=0), OK),
+    (dict(tokens=0, x=None), OK),
+])
+def test_moe_rejects(L, kw, err):
+    a = decoder._MoeArgs(x=FAKE, ldx=64, logits=FAKE, ldl=8, tokens=4, width=64, inner=32, experts=8, top_k=2, up_codes=FAKE,
+                         up_scales=FAKE, up_alpha=FAKE, down_codes=FAKE, down_scales=FAKE, down_alpha=FAKE, activation=1,
+                         gated=1, y=FAKE)
+    for k, v in kw.items():
+        setattr(a, k, v)
+    assert L.nvfp4_moe(ctypes.byref(a)) == err
+    assert L.nvfp4_moe(None) == INVALID
+
+
+def test_moe_workspace(L):
+    assert L.nvfp4_moe_workspace_bytes(4, 64, 32, 8, 2) > 0 and L.nvfp4_moe_workspace_bytes(0, 64, 32, 8, 2) == 0
+    assert L.nvfp4_moe_workspace_bytes(4, 72, 32, 8, 2) == 0
