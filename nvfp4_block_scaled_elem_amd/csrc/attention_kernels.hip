@@ -24,6 +24,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "act.hpp"
 #include "cache.hpp"
@@ -65,8 +66,25 @@ __device__ __forceinline__ float row_sum(float v) {
     return __uint_as_float(b.x) + __uint_as_float(b.y);
 }
 
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) v += __shfl_xor(v, k);
+    return v;
+}
+
 // e^(a - b) in powers of two, 0 for a = -inf whatever b.
 __device__ __forceinline__ float weight(float a, float b) { return a == kNegInf ? 0.0f : __builtin_amdgcn_exp2f(a - b); }
+
+// Masks the bytes of the first n of 16 tokens.
+__device__ __forceinline__ u32x4 tokens_kept(int n) {
+    u32x4 keep;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        const int k = n - 4 * w;
+        keep[w] = k >= 4 ? ~0u : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
+    }
+    return keep;
+}
 
 // What a wave carries for its 16 RT rows: per lane the maximum (of the row), the sum (of the lane's tokens), the output.
 template <int KS, int RT>
@@ -76,19 +94,29 @@ struct Rows {
     int lim[RT];  // tokens that the lane's row sees (0: no such row)
 };
 
-// KS: head sizes to 64 KS. RT: tiles of 16 rows. The wave takes blocks b0, b0 + step, ... below b1 of sequence s. `safe`:
-// the tokens that every row of the wave sees (blocks below need no mask).
-template <int KS, int RT>
+// LDS bytes of a wave's block: K's rows with an odd number of 16-byte pieces from one to the next and four pieces more per 16
+// rows, so that the sixteen lanes that read one piece of the tokens 16 a + 4 t + j meet no bank twice; V's tiles of 16 columns.
+template <int KS>
+constexpr int kWaveK = 64 * (64 * KS + 16) + 4 * 64;
+template <int KS>
+constexpr int kWaveLds = kWaveK<KS> + 4096 * KS;
+
+// KS: head sizes to 64 KS; FULL: 64 KS itself (else what is past dim is read from inside it: K's meet zeros of q, V's
+// sums are not stored). RT: tiles of 16 rows. The wave takes blocks b0, b0 + step, ... below b1 of sequence s. `safe`:
+// the tokens that every row of the wave sees (blocks below need no mask). `wl`: the wave's kWaveLds bytes.
+//
+// A block's codes are read whole, 1 KB a load: lanes that read an operand's pieces where they lie are rows apart, which takes
+// four times the address cycles. They are turned in LDS, where only the wave itself writes and reads, and the next
+// block's loads are in flight meanwhile.
+template <int KS, int RT, bool FULL>
 __device__ __forceinline__ void attend(const AttnArgs &p, const Seq &q, int s, int64_t h, int b0, int b1, int step, int safe,
-                                       const bf16x8 (&Q)[RT][2 * KS], Rows<KS, RT> &R) {
+                                       const bf16x8 (&Q)[RT][2 * KS], Rows<KS, RT> &R, uint8_t *wl) {
     const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
-    const int dim = p.dim;
-    const int64_t page_bytes = (int64_t)kPage * dim;
+    const int dim = FULL ? 64 * KS : p.dim, per = dim / 16;  // 16-byte pieces of a token; loads of a block's K, and of its V
     const int count = b1 > b0 ? (b1 - b0 + step - 1) / step : 0;
     if (count == 0) return;
-    // byte offsets of the lane's pieces in a (page, head)
-    const int koff = (16 * (r16 >> 2) + (r16 & 3)) * dim + 16 * g;  // + 4 t dim + 64 i
-    const int voff = r16 * kPage + 16 * g;                          // + 1024 d
+    const int pitch = dim + (per & 1 ? 0 : 16);
+    uint8_t *const wv = wl + kWaveK<KS>;
     // Pages and scales of 64 of the wave's blocks, one a lane.
     int page = -1;
     uint32_t scales = 0u;
@@ -103,27 +131,21 @@ __device__ __forceinline__ void attend(const AttnArgs &p, const Seq &q, int s, i
     // Page i; a page that is not there, or one of NaNs, is read as page 0 and left out.
     auto base_of = [&](int i) __attribute__((always_inline)) {
         const int pg = __builtin_amdgcn_readlane(page, i & 63);
-        return ((int64_t)max(pg, 0) * p.kv_heads + h) * page_bytes;
+        return ((int64_t)max(pg, 0) * p.kv_heads + h) * (kPage * dim);
     };
-    uint4 kc[4][KS], vc[4 * KS];
+    u32x4 kc[4 * KS], vc[4 * KS];
+    const uint32_t loff = 16u * (uint32_t)lane;
     auto load_k = [&](int64_t base) __attribute__((always_inline)) {
         const uint8_t *c = p.k_codes + base;
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
-#pragma unroll
-            for (int i = 0; i < KS; ++i)
-                if (64 * i + 16 * g < dim) kc[t][i] = *reinterpret_cast<const uint4 *>(c + koff + 4 * t * dim + 64 * i);
+        for (int i = 0; i < 4 * KS; ++i) kc[i] = *reinterpret_cast<const u32x4 *>(c + 1024 * (FULL ? i : min(i, per - 1)) + loff);
     };
     auto load_v = [&](int64_t base) __attribute__((always_inline)) {
         const uint8_t *c = p.v_codes + base;
 #pragma unroll
-        for (int d = 0; d < 4 * KS; ++d)
-            if (16 * d < dim) vc[d] = *reinterpret_cast<const uint4 *>(c + voff + 1024 * d);
+        for (int i = 0; i < 4 * KS; ++i) vc[i] = *reinterpret_cast<const u32x4 *>(c + 1024 * (FULL ? i : min(i, per - 1)) + loff);
     };
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-        for (int i = 0; i < KS; ++i) kc[t][i] = make_uint4(0u, 0u, 0u, 0u);  // columns past dim stay zeros
+    auto k_place = [&](int token, int c) __attribute__((always_inline)) { return token * pitch + 64 * (token >> 4) + 16 * c; };
     look_up(0);
     int64_t base = base_of(0);
     load_k(base);
@@ -139,26 +161,42 @@ __device__ __forceinline__ void attend(const AttnArgs &p, const Seq &q, int s, i
         if (nan) poison = min(poison, t0);
         if (((i + 1) & 63) == 0) look_up(i + 1);
         const int64_t next = base_of(i + 1 < count ? i + 1 : i);
-        if (!live) {
-            load_k(next);
-            load_v(next);
-            continue;
+        const float kscale = mx_scale_value(ke), vscale = live ? mx_scale_value(ve) : 1.0f;
+        wave_handover();
+#pragma unroll
+        for (int k = 0; k < 4 * KS; ++k) {
+            const int e = 64 * (FULL ? k : min(k, per - 1)) + lane;
+            *reinterpret_cast<u32x4 *>(wl + k_place(e / per, e % per)) = kc[k];
         }
-        const float kscale = mx_scale_value(ke), vscale = mx_scale_value(ve);
+        load_k(next);
+        wave_handover();
         f32x4 S[RT][4] = {};
 #pragma unroll
-        for (int t = 0; t < 4; ++t)
+        for (int t = 0; t < 4; ++t) {
+            __builtin_amdgcn_sched_barrier(0);  // tile by tile: operands of all tiles at once take more registers than there are
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-                const bf16x8 a = operand8(kc[t][k].x, kc[t][k].y, kscale), b = operand8(kc[t][k].z, kc[t][k].w, kscale);
+                const int piece = FULL ? 4 * k + g : min(4 * k + g, per - 1);
+                const u32x4 c = *reinterpret_cast<const u32x4 *>(wl + k_place(16 * (r16 >> 2) + 4 * t + (r16 & 3), piece));
+                const bf16x8 a = operand8(c.x, c.y, kscale), b = operand8(c.z, c.w, kscale);
 #pragma unroll
                 for (int r = 0; r < RT; ++r) {
                     S[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, Q[r][2 * k], S[r][t], 0, 0, 0);
                     S[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, Q[r][2 * k + 1], S[r][t], 0, 0, 0);
                 }
             }
-        load_k(next);
-        const bool mask = t0 + kPage > safe;
+        }
+        __builtin_amdgcn_sched_barrier(0);
+        if (t0 + kPage > q.len || !live) {  // codes behind the end may be any bytes
+            const u32x4 keep = tokens_kept(live ? q.len - t0 - 16 * (lane & 3) : 0);
+#pragma unroll
+            for (int d = 0; d < 4 * KS; ++d) vc[d] &= keep;
+        }
+        // Piece u of column d of a tile at u ^ (d / 4 % 4).
+#pragma unroll
+        for (int d = 0; d < 4 * KS; ++d) *reinterpret_cast<u32x4 *>(wv + 1024 * d + (lane >> 2) * 64 + 16 * ((lane ^ (lane >> 4)) & 3)) = vc[d];
+        load_v(next);
+        const bool mask = t0 + kPage > safe || !live;
         bool more = false;
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -167,12 +205,12 @@ __device__ __forceinline__ void attend(const AttnArgs &p, const Seq &q, int s, i
             for (int t = 0; t < 4; ++t)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    float v = S[r][t][j] * p.scale2;
-                    if (mask) v = t0 + 16 * g + 4 * t + j < R.lim[r] ? v : kNegInf;
+                    float v = S[r][t][j];
+                    if (mask) v = live && t0 + 16 * g + 4 * t + j < R.lim[r] ? v : kNegInf;
                     S[r][t][j] = v;
                     top = fmaxf(top, v);
                 }
-            more |= top > R.m[r] + 8.0f;
+            more |= top > R.m[r] + p.slack;
         }
         if (__any(more)) {
 #pragma unroll
@@ -183,35 +221,24 @@ __device__ __forceinline__ void attend(const AttnArgs &p, const Seq &q, int s, i
 #pragma unroll
                     for (int j = 0; j < 4; ++j) top = fmaxf(top, S[r][t][j]);
                 const float m = row_max(fmaxf(top, R.m[r]));
-                const float w = weight(R.m[r], m);
+                const float w = R.m[r] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((R.m[r] - m) * p.scale2);
                 R.m[r] = m;
                 R.l[r] *= w;
 #pragma unroll
                 for (int d = 0; d < 4 * KS; ++d) R.o[r][d] *= w;
             }
         }
-        if (t0 + kPage > q.len) {  // codes behind the end may be any bytes
-            const int n = q.len - t0 - 16 * g;
-            uint32_t keep[4];
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-                const int k = n - 4 * w;
-                keep[w] = k >= 4 ? 0xFFFFFFFFu : k <= 0 ? 0u : (1u << (8 * k)) - 1u;
-            }
-#pragma unroll
-            for (int d = 0; d < 4 * KS; ++d) vc[d].x &= keep[0], vc[d].y &= keep[1], vc[d].z &= keep[2], vc[d].w &= keep[3];
-        }
         bf16x8 P[RT][2];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-            const float m = R.m[r] == kNegInf ? 0.0f : R.m[r];
+            const float m = (R.m[r] == kNegInf ? 0.0f : -R.m[r]) * p.scale2;
             uint32_t w[8];
 #pragma unroll
             for (int t = 0; t < 4; ++t) {
                 float e[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    e[j] = __builtin_amdgcn_exp2f(S[r][t][j] - m);
+                    e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[r][t][j], p.scale2, m));
                     R.l[r] += e[j];
                 }
                 w[2 * t] = pack_bf16(e[0], e[1]);
@@ -220,17 +247,18 @@ __device__ __forceinline__ void attend(const AttnArgs &p, const Seq &q, int s, i
             P[r][0] = __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
             P[r][1] = __builtin_bit_cast(bf16x8, u32x4{w[4], w[5], w[6], w[7]});
         }
+        wave_handover();
 #pragma unroll
-        for (int d = 0; d < 4 * KS; ++d)
-            if (16 * d < dim) {
-                const bf16x8 a = operand8(vc[d].x, vc[d].y, vscale), b = operand8(vc[d].z, vc[d].w, vscale);
+        for (int d = 0; d < 4 * KS; ++d) {
+            if (d % 2 == 0) __builtin_amdgcn_sched_barrier(0);
+            const u32x4 c = *reinterpret_cast<const u32x4 *>(wv + 1024 * d + r16 * 64 + 16 * ((g ^ (r16 >> 2)) & 3));
+            const bf16x8 a = operand8(c.x, c.y, vscale), b = operand8(c.z, c.w, vscale);
 #pragma unroll
-                for (int r = 0; r < RT; ++r) {
-                    R.o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, P[r][0], R.o[r][d], 0, 0, 0);
-                    R.o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, P[r][1], R.o[r][d], 0, 0, 0);
-                }
+            for (int r = 0; r < RT; ++r) {
+                R.o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, P[r][0], R.o[r][d], 0, 0, 0);
+                R.o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b, P[r][1], R.o[r][d], 0, 0, 0);
             }
-        load_v(next);
+        }
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -239,7 +267,7 @@ __device__ __forceinline__ void attend(const AttnArgs &p, const Seq &q, int s, i
 
 // The lane's rows row0 + 16 r + l % 16 of the sequence: their queries as operands, and what they see. Returns the
 // tokens that all of the wave's rows see.
-template <int KS, int RT>
+template <int KS, int RT, bool FULL>
 __device__ __forceinline__ int take_rows(const AttnArgs &p, const Seq &q, int64_t h, int row0, bf16x8 (&Q)[RT][2 * KS], Rows<KS, RT> &R) {
     const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
     int safe = 0x7FFFFFFF;
@@ -254,7 +282,8 @@ __device__ __forceinline__ int take_rows(const AttnArgs &p, const Seq &q, int64_
         for (int k = 0; k < 2 * KS; ++k) {
             const int c = 64 * (k >> 1) + 16 * g + 8 * (k & 1);
             u32x4 v = {0u, 0u, 0u, 0u};
-            if (in && c < p.dim) v = *reinterpret_cast<const u32x4_any *>(x + c);
+            if (in && (FULL || c < p.dim)) v = *reinterpret_cast<const u32x4_any *>(x + c);
+            v ^= p.flip;  // a negative scale: -q, exact
             Q[r][k] = __builtin_bit_cast(bf16x8, v);
         }
         R.m[r] = kNegInf, R.l[r] = 0.0f;
@@ -270,42 +299,257 @@ __device__ __forceinline__ uint16_t *out_row(const AttnArgs &p, const Seq &q, in
     return p.out + ((int64_t)(q.first + row / p.group) * p.kv_heads * p.group + h * p.group + row % p.group) * p.dim;
 }
 
-// Rows over the waves: a work-group takes 64 RT rows of a sequence and head, a wave 16 RT of them, over all blocks that
-// they see. For prompts: bound by the matrix cores and the exponentials. The waves read the same blocks at nearly
-// the same time, mostly from the first-level cache.
-template <int KS, int RT>
-__global__ __launch_bounds__(kAttnThreads) void k_attn_rows(AttnArgs p) {
-    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    constexpr int kRows = 16 * RT * kWaves;
+// Rows over the waves, for prompts: a work-group takes 64 RT rows of a sequence and head, a wave 16 RT of them, over all
+// blocks that they see. Bound by the matrix cores and the exponentials, so a block's codes are decoded once per
+// work-group: into LDS, in the order of the operands (every read is 1 KB in lane order), while the block before is
+// computed. With 64 rows a wave, an operand read feeds four matrix instructions, and LDS is busy half the time they take.
+//
+// Slot m of key tile t holds token 16 t + m; a lane then ends with the scores of the tokens 16 t + 4 g + j, and V's
+// operand u takes tokens 32 u + 4 g + j and 32 u + 16 + 4 g + j, j = 0..3, as k = 8 g .. + 7.
+//
+// Per block b: the scores of block b + 1 are multiplied while the probabilities of b are computed, and V of b is
+// multiplied while the codes of K of b + 2 and V of b + 1 are decoded: K runs a block ahead of V, each in two buffers.
+template <int KS, int RT, bool FULL>
+__global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_attn_rows(AttnArgs p) {
+    constexpr int kRows = 16 * RT * kWaves, kHalf = 64 * 64 * KS * 2;  // LDS bytes of a block's K or V
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    uint8_t *const lds_k = lds, *const lds_v = lds + 2 * kHalf;
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // The heads run fastest over the grid, so that a head's blocks stay in one XCD's L2; the last pieces of a
     // sequence, which see the most, go first.
     const int64_t h = blockIdx.x % p.kv_heads;
     const int piece = p.pieces - 1 - (int)(blockIdx.x / p.kv_heads);
     const int s = piece_sequence(p.seq, piece, p.group, kRows, 1);
     const Seq q = sequence(p.seq, s);
-    const int row0 = (piece - piece_base(p.seq, s, p.group, kRows, 1)) * kRows + 16 * RT * wave;
-    if (row0 >= q.n * p.group || row0 < 0) return;
+    const int first = (piece - piece_base(p.seq, s, p.group, kRows, 1)) * kRows;
+    if (first >= q.n * p.group || first < 0) return;
+    const int row0 = first + 16 * RT * wave, dim = FULL ? 64 * KS : p.dim;
     bf16x8 Q[RT][2 * KS];
     Rows<KS, RT> R;
-    const int safe = take_rows<KS, RT>(p, q, h, row0, Q, R);
-    int most = 0;
+    const int safe = take_rows<KS, RT, FULL>(p, q, h, row0, Q, R);
+    int most = 0;  // tokens that some row of the wave sees
 #pragma unroll
     for (int r = 0; r < RT; ++r) most = max(most, R.lim[r]);
 #pragma unroll
     for (int k = 1; k < 64; k <<= 1) most = max(most, __shfl_xor(most, k));
     most = __builtin_amdgcn_readfirstlane(most);
-    attend<KS, RT>(p, q, s, h, 0, (most + kPage - 1) / kPage, 1, safe, Q, R);
+    const int last_tok = min(q.n, (first + kRows - 1) / p.group + 1);  // behind the work-group's last row
+    const int reach = p.causal ? min(max(q.len - q.n + last_tok, 0), q.len) : q.len;
+    const int count = (reach + kPage - 1) / kPage;
+
+    // Pages and scales of 64 blocks, one a lane.
+    int page = -1;
+    uint32_t scales = 0u;
+    auto look_up = [&](int i0) __attribute__((always_inline)) {
+        page = -1, scales = 0u;
+        if (i0 + lane < count) page = page_of(p.seq, s, i0 + lane);
+        if (page >= 0) {
+            const int64_t at = (int64_t)page * p.kv_heads + h;
+            scales = (uint32_t)p.k_scales[at] | (uint32_t)p.v_scales[at] << 8;
+        }
+    };
+    // What the wave knows of a block: whether it is there, and its scales (looked up 64 at a time, from `ahead` on).
+    struct Block {
+        int64_t base;
+        float ks, vs;
+        int live;
+    };
+    int poison = 0x7FFFFFFF, ahead = 0;
+    auto block_of = [&](int b) __attribute__((always_inline)) {
+        if (b >= ahead && b < count) look_up(b), ahead = b + 64;  // b == ahead
+        const int pg = __builtin_amdgcn_readlane(page, b & 63);
+        const uint32_t sc = (uint32_t)__builtin_amdgcn_readlane((int)scales, b & 63);
+        const bool nan = (sc & 255u) == 255u || (sc >> 8) == 255u;
+        Block B;
+        B.live = b < count && pg >= 0 && !nan;
+        if (b < count && nan) poison = min(poison, b * kPage);
+        B.base = ((int64_t)max(pg, 0) * p.kv_heads + h) * (kPage * dim);
+        B.ks = B.live ? mx_scale_value(sc & 255u) : 1.0f, B.vs = B.live ? mx_scale_value(sc >> 8) : 1.0f;
+        return B;
+    };
+    // A thread's codes of a block: KS pieces of 16 of K (row e / (dim / 16)) and of V (row e / 4), e = tid + 256 i.
+    const int per = dim / 16, pieces = kPage * per;
+    u32x4 kraw[KS], vraw[KS];
+    Block kb, vb;  // of the raw pieces
+    auto load_k = [&](int b) __attribute__((always_inline)) {
+        kb = block_of(b);
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+            const int e = tid + kAttnThreads * i;
+            kraw[i] = u32x4{0u, 0u, 0u, 0u};
+            if (kb.live && (FULL || e < pieces)) kraw[i] = *reinterpret_cast<const u32x4 *>(p.k_codes + kb.base + 16 * e);
+        }
+    };
+    auto load_v = [&](int b, const Block &B) __attribute__((always_inline)) {
+        vb = B;
+        const int n = q.len - b * kPage - 16 * (tid & 3);  // tokens of the piece in front of the end
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+            const int e = tid + kAttnThreads * i;
+            vraw[i] = u32x4{0u, 0u, 0u, 0u};
+            if (vb.live && (FULL || e < pieces)) vraw[i] = *reinterpret_cast<const u32x4 *>(p.v_codes + vb.base + 16 * e);
+        }
+        if (n < 16) {  // codes behind the end may be any bytes
+            const u32x4 keep = tokens_kept(n);
+#pragma unroll
+            for (int i = 0; i < KS; ++i) vraw[i] &= keep;
+        }
+    };
+    // Piece c = 4 i + g of a token: k = 64 i + 16 g .. + 15, the operands 2 i and 2 i + 1 of the token's tile, at lane
+    // (token % 16) ^ c within the sixteen of g: the eight pieces of a row meet no bank twice.
+    auto store_k = [&](int b) __attribute__((always_inline)) {
+        uint8_t *const to = lds_k + (b & 1) * kHalf;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+            const int e = tid + kAttnThreads * i, token = e / per, c = e % per;
+            if (!FULL && e >= pieces) continue;
+            uint8_t *at = to + ((((token >> 4) * 2 * KS + 2 * (c >> 2)) * 64) + 16 * (c & 3) + ((token & 15) ^ c)) * 16;
+            *reinterpret_cast<bf16x8 *>(at) = operand8(kraw[i].x, kraw[i].y, kb.ks);
+            *reinterpret_cast<bf16x8 *>(at + 1024) = operand8(kraw[i].z, kraw[i].w, kb.ks);
+        }
+    };
+    auto store_v = [&](int b) __attribute__((always_inline)) {
+        uint8_t *const to = lds_v + (b & 1) * kHalf;
+#pragma unroll
+        for (int i = 0; i < KS; ++i) {
+            const int e = tid + kAttnThreads * i, d = e >> 2, c = e & 3;  // column; 16 tokens
+            if (!FULL && e >= pieces) continue;
+            uint8_t *at = to + (((d >> 4) * 2 + (c >> 1)) * 64 + (d & 15)) * 16 + 8 * (c & 1);
+            const u32x4 a = __builtin_bit_cast(u32x4, operand8(vraw[i].x, vraw[i].y, vb.vs));
+            const u32x4 b4 = __builtin_bit_cast(u32x4, operand8(vraw[i].z, vraw[i].w, vb.vs));
+            *reinterpret_cast<u32x2 *>(at) = u32x2{a.x, a.y};
+            *reinterpret_cast<u32x2 *>(at + 256) = u32x2{a.z, a.w};
+            *reinterpret_cast<u32x2 *>(at + 512) = u32x2{b4.x, b4.y};
+            *reinterpret_cast<u32x2 *>(at + 768) = u32x2{b4.z, b4.w};
+        }
+    };
+    auto scores = [&](int b, f32x4 (&S)[RT][4]) __attribute__((always_inline)) {
+        const uint8_t *const from = lds_k + (b & 1) * kHalf;
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) S[r][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < 2 * KS; ++k) {
+            const int c = 4 * (k >> 1) + g;
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const bf16x8 a = *reinterpret_cast<const bf16x8 *>(from + ((t * 2 * KS + k) * 64 + 16 * g + (r16 ^ c)) * 16);
+#pragma unroll
+                for (int r = 0; r < RT; ++r) S[r][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, Q[r][k], S[r][t], 0, 0, 0);
+            }
+        }
+    };
+    if (!FULL) {  // columns past dim: zeros that no block overwrites
+        for (int e = tid; e < 4 * kHalf / 16; e += kAttnThreads) reinterpret_cast<u32x4 *>(lds)[e] = u32x4{0u, 0u, 0u, 0u};
+        __syncthreads();
+    }
+    f32x4 S[RT][4];
+    int live = 0, live1 = 0;  // of the blocks b and b + 1
+    if (count > 0) {
+        load_k(0);
+        live = kb.live;
+        const Block b0 = kb;
+        load_v(0, b0);
+        store_k(0);
+        store_v(0);
+        load_k(1);
+        live1 = kb.live;
+        store_k(1);
+        load_v(1, kb);
+        load_k(2);
+        __syncthreads();
+        scores(0, S);
+        __syncthreads();
+    }
+#pragma unroll 1
+    for (int b = 0; b < count; ++b) {
+        const int t0 = b * kPage;
+        // The maximum that exponents are taken against, raised where a score is far above it.
+        if (t0 + kPage > safe || !live) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+                for (int t = 0; t < 4; ++t)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        S[r][t][j] = live && t0 + 16 * t + 4 * g + j < R.lim[r] ? S[r][t][j] : kNegInf;
+        }
+        bool more = false;
+        float top[RT];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            top[r] = kNegInf;
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top[r] = fmaxf(top[r], S[r][t][j]);
+            more |= top[r] > R.m[r] + p.slack;
+        }
+        if (__any(more)) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r) {
+                const float m = row_max(fmaxf(top[r], R.m[r]));
+                const float w = R.m[r] == kNegInf ? 0.0f : __builtin_amdgcn_exp2f((R.m[r] - m) * p.scale2);
+                R.m[r] = m;
+                R.l[r] *= w;
+#pragma unroll
+                for (int d = 0; d < 4 * KS; ++d) R.o[r][d] *= w;
+            }
+        }
+        f32x4 S1[RT][4];
+        scores(b + 1, S1);  // (of a block that is not there: never looked at)
+        bf16x8 P[RT][2];
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+            const float m = (R.m[r] == kNegInf ? 0.0f : -R.m[r]) * p.scale2;
+            uint32_t w[8];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                float e[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    e[j] = __builtin_amdgcn_exp2f(__builtin_fmaf(S[r][t][j], p.scale2, m));
+                    R.l[r] += e[j];
+                }
+                w[2 * t] = pack_bf16(e[0], e[1]);
+                w[2 * t + 1] = pack_bf16(e[2], e[3]);
+            }
+            P[r][0] = __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]});
+            P[r][1] = __builtin_bit_cast(bf16x8, u32x4{w[4], w[5], w[6], w[7]});
+        }
+        const uint8_t *const from = lds_v + (b & 1) * kHalf;
+#pragma unroll
+        for (int d = 0; d < 4 * KS; ++d)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const bf16x8 a = *reinterpret_cast<const bf16x8 *>(from + ((d * 2 + u) * 64 + lane) * 16);
+#pragma unroll
+                for (int r = 0; r < RT; ++r) R.o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, P[r][u], R.o[r][d], 0, 0, 0);
+            }
+        store_v(b + 1);
+        store_k(b + 2);
+        const Block next = kb;
+        load_v(b + 2, next);
+        live = live1, live1 = next.live;
+        load_k(b + 3);
+        lds_barrier();
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int t = 0; t < 4; ++t) S[r][t] = S1[r][t];
+    }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        const float l = row_sum(R.l[r]);
+        const float l = row_sum(R.lim[r] > poison ? __builtin_nanf("") : R.l[r]);
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int row = row0 + 16 * r + r16;
         if (row >= q.n * p.group) continue;
         uint16_t *o = out_row(p, q, h, row) + 4 * g;
 #pragma unroll
         for (int d = 0; d < 4 * KS; ++d)
-            if (16 * d < p.dim) {
+            if (FULL || 16 * d < p.dim) {
                 const f32x4 v = R.o[r][d] * inv;
                 *reinterpret_cast<uint2 *>(o + 16 * d) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
             }
@@ -328,51 +572,51 @@ struct Share {
 __device__ __forceinline__ int tiles_of(const AttnArgs &p, const Seq &q, int size) { return (q.n * p.group + size - 1) / size; }
 __device__ __forceinline__ int blocks_of(const Seq &q) { return (q.len + kPage - 1) / kPage; }
 
-// The list's length, and the sequence in whose part block `u` lies, with the part's begin. By whole waves.
-__device__ __forceinline__ uint32_t list_total(const AttnArgs &p, int size) {
-    const int lane = threadIdx.x & 63;
-    uint32_t sum = 0u;
-    for (int s = lane; s < p.seq.seqs; s += 64) {
-        const Seq q = sequence(p.seq, s);
-        sum += (uint32_t)(tiles_of(p, q, size) * blocks_of(q));
-    }
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) sum += (uint32_t)__shfl_xor((int)sum, k);
-    return (uint32_t)__builtin_amdgcn_readfirstlane((int)sum);
-}
-
-__device__ __forceinline__ int list_find(const AttnArgs &p, int size, uint32_t u, uint32_t &begin) {
-    const int lane = threadIdx.x & 63;
-    uint32_t before = 0u;
-    for (int s0 = 0; s0 < p.seq.seqs; s0 += 64) {
-        uint32_t mine = 0u;
+// 64 sequences, one a lane, with the blocks (of all their tiles) in front of them in the list. By whole waves.
+struct Window {
+    int s0;
+    Seq q;
+    uint32_t mine, upto, before;  // the lane's blocks; those of the window up to and with it; those before the window
+    __device__ __forceinline__ void load(const AttnArgs &p, int size, int from, uint32_t front) {
+        const int lane = threadIdx.x & 63;
+        s0 = from, before = front, mine = 0u, q = Seq{0, 0, 0};
         if (s0 + lane < p.seq.seqs) {
-            const Seq q = sequence(p.seq, s0 + lane);
+            q = sequence(p.seq, s0 + lane);
             mine = (uint32_t)(tiles_of(p, q, size) * blocks_of(q));
         }
-        uint32_t upto = mine;
+        upto = mine;
 #pragma unroll
         for (int k = 1; k < 64; k <<= 1) {
             const uint32_t v = (uint32_t)__shfl_up((int)upto, k);
             if (lane >= k) upto += v;
         }
-        const uint64_t past = __ballot(before + upto > u);
-        if (past) {
-            const int first = __ffsll((unsigned long long)past) - 1;
-            begin = before + (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), first);
-            return s0 + first;
-        }
-        before += (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
     }
-    begin = before;
-    return p.seq.seqs;
+    __device__ __forceinline__ uint32_t total() const { return before + (uint32_t)__builtin_amdgcn_readlane((int)upto, 63); }
+    __device__ __forceinline__ Seq seq(int s) const {
+        return Seq{__builtin_amdgcn_readlane(q.first, s - s0), __builtin_amdgcn_readlane(q.n, s - s0), __builtin_amdgcn_readlane(q.len, s - s0)};
+    }
+    __device__ __forceinline__ uint32_t begin(int s) const {
+        return before + (uint32_t)__builtin_amdgcn_readlane((int)(upto - mine), s - s0);
+    }
+};
+
+// The first window, and the list's length.
+__device__ __forceinline__ uint32_t list_total(const AttnArgs &p, int size, Window &w) {
+    w.load(p, size, 0, 0u);
+    uint32_t sum = w.total();
+    for (int s0 = 64; s0 < p.seq.seqs; s0 += 64) {
+        Window v;
+        v.load(p, size, s0, sum);
+        sum = v.total();
+    }
+    return sum;
 }
 
-__device__ __forceinline__ Share share_of(const AttnArgs &p, int size) {
+__device__ __forceinline__ Share share_of(const AttnArgs &p, uint32_t total) {
     Share sh;
-    sh.total = list_total(p, size);
+    sh.total = total;
     // Not less than a block for each wave of a work-group.
-    sh.groups = max(1u, min((uint32_t)p.groups, (sh.total + kWaves - 1) / kWaves));
+    sh.groups = max(1u, min((uint32_t)p.groups, (total + kWaves - 1) / kWaves));
     return sh;
 }
 
@@ -381,45 +625,43 @@ __device__ __forceinline__ int64_t part_place(const AttnArgs &p, int64_t h, uint
     return h * (p.groups + p.pieces) + j + piece;
 }
 
-template <int KS, int RT>
-__global__ __launch_bounds__(kAttnThreads) void k_attn_split(AttnArgs p) {
+template <int KS, int RT, bool FULL>
+__global__ __launch_bounds__(kAttnThreads, RT * KS <= 2 ? 2 : 1) void k_attn_split(AttnArgs p) {
     constexpr int kRows = 16 * RT, kDim = 64 * KS;
-    __shared__ float lds_o[kWaves][16][kDim + 4];
+    // each wave's block; afterwards each wave's sums
+    constexpr int kStage = kWaves * kWaveLds<KS>, kSums = kWaves * 16 * (kDim + 4) * 4;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kStage > kSums ? kStage : kSums];
     __shared__ float lds_m[kWaves][16], lds_l[kWaves][16];
+    float (*const lds_o)[16][kDim + 4] = reinterpret_cast<float (*)[16][kDim + 4]>(lds);
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t h = blockIdx.x % p.kv_heads;
     const uint32_t j = blockIdx.x / p.kv_heads;
-    const Share sh = share_of(p, kRows);
+    Window w;
+    const Share sh = share_of(p, list_total(p, kRows, w));
     if (j >= sh.groups || sh.total == 0u) return;
     uint32_t u = sh.begin(j);
     const uint32_t end = sh.begin(j + 1);
-    if (u >= end) return;
-    uint32_t at;
-    int s = list_find(p, kRows, u, at);
-    while (u < end && s < p.seq.seqs) {
-        const Seq q = sequence(p.seq, s);
-        const uint32_t nb = (uint32_t)blocks_of(q), mine = nb * (uint32_t)tiles_of(p, q, kRows);
-        if (u >= at + mine) {
-            at += mine;
-            ++s;
-            continue;
-        }
+    while (u < end) {
+        while (u >= w.total()) w.load(p, kRows, w.s0 + 64, w.total());
+        const int s = w.s0 + __ffsll((unsigned long long)__ballot(w.before + w.upto > u)) - 1;
+        const Seq q = w.seq(s);
+        const uint32_t nb = (uint32_t)blocks_of(q), at = w.begin(s);
         const int tile = (int)((u - at) / nb), b0 = (int)((u - at) % nb), b1 = (int)min(nb, b0 + (end - u));
         u += b1 - b0;
         const int row0 = tile * kRows, rows = min(kRows, q.n * p.group - row0);
         bf16x8 Q[RT][2 * KS];
         Rows<KS, RT> R;
-        const int safe = take_rows<KS, RT>(p, q, h, row0, Q, R);
-        attend<KS, RT>(p, q, s, h, b0 + wave, b1, kWaves, safe, Q, R);
+        const int safe = take_rows<KS, RT, FULL>(p, q, h, row0, Q, R);
+        attend<KS, RT, FULL>(p, q, s, h, b0 + wave, b1, kWaves, safe, Q, R, lds + wave * kWaveLds<KS>);
         const bool whole = b0 == 0 && b1 == (int)nb;
         const int64_t place = part_place(p, h, j, piece_base(p.seq, s, p.group, kRows, 1) + tile);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             const float l = row_sum(R.l[r]);
             if (16 * r >= rows) break;
-            __syncthreads();  // the tile before has been read
-            if (g == 0) lds_m[wave][r16] = R.m[r], lds_l[wave][r16] = l;
+            __syncthreads();  // the blocks, or the tile before, have been read
+            if (g == 0) lds_m[wave][r16] = R.m[r] * p.scale2, lds_l[wave][r16] = l;
 #pragma unroll
             for (int d = 0; d < 4 * KS; ++d) *reinterpret_cast<f32x4 *>(&lds_o[wave][r16][16 * d + 4 * g]) = R.o[r][d];
             __syncthreads();
@@ -461,79 +703,88 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_split(AttnArgs p) {
     }
 }
 
-// The tiles whose blocks lie in several shares, and the rows of sequences of no tokens (zeros): a wave takes a row.
+// The tiles whose blocks lie in several shares, and the rows of sequences of no tokens (zeros). A work-group takes a row,
+// its waves every fourth part, joined in wave order.
 __global__ __launch_bounds__(kAttnThreads) void k_attn_join(AttnArgs p, int size) {
+    __shared__ float lds_o[kWaves][kMaxHeadDim], lds_l[kWaves];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t h = blockIdx.x % p.kv_heads;
-    const int piece = (int)(blockIdx.x / p.kv_heads);
+    const int piece = (int)(blockIdx.x / p.kv_heads), row = (int)blockIdx.y;  // of the tile
+    Window w;
+    const uint32_t total = list_total(p, size, w);
     const int s = piece_sequence(p.seq, piece, p.group, size, 1);
-    const Seq q = sequence(p.seq, s);
-    const int base = piece_base(p.seq, s, p.group, size, 1), tile = piece - base;
-    const int row = (int)blockIdx.y * kWaves + wave;  // of the tile
-    if (tile < 0 || tile >= tiles_of(p, q, size) || row >= size || tile * size + row >= q.n * p.group) return;
+    while (s >= w.s0 + 64) w.load(p, size, w.s0 + 64, w.total());
+    const Seq q = w.seq(s);
+    const int tile = piece - piece_base(p.seq, s, p.group, size, 1);
+    if (tile < 0 || tile >= tiles_of(p, q, size) || tile * size + row >= q.n * p.group) return;
     uint16_t *o = out_row(p, q, h, tile * size + row);
     const int c = 4 * lane;
     const uint32_t nb = (uint32_t)blocks_of(q);
     if (nb == 0u) {
-        if (c < p.dim) *reinterpret_cast<uint2 *>(o + c) = make_uint2(0u, 0u);
+        if (wave == 0 && c < p.dim) *reinterpret_cast<uint2 *>(o + c) = make_uint2(0u, 0u);
         return;
     }
-    const Share sh = share_of(p, size);
-    uint32_t before = 0u;  // blocks of the sequences before s
-    for (int i = lane; i < s; i += 64) {
-        const Seq e = sequence(p.seq, i);
-        before += (uint32_t)(tiles_of(p, e, size) * blocks_of(e));
-    }
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) before += (uint32_t)__shfl_xor((int)before, k);
-    before = (uint32_t)__builtin_amdgcn_readfirstlane((int)before);
-    const uint32_t u0 = before + (uint32_t)tile * nb;
+    const Share sh = share_of(p, total);
+    const uint32_t u0 = w.begin(s) + (uint32_t)tile * nb;
     const uint32_t j0 = sh.owner(u0), j1 = sh.owner(u0 + nb - 1);
     if (j0 == j1) return;
+    const int parts = (int)(j1 - j0 + 1);
     const int64_t at = part_place(p, h, j0, piece) * size + row;
     float m = kNegInf;
-    for (uint32_t j = j0 + lane; j <= j1; j += 64) m = fmaxf(m, p.part_ml[(at + (int64_t)(j - j0) * size) * 2]);
+    for (int k = lane; k < parts; k += 64) m = fmaxf(m, p.part_ml[(at + (int64_t)k * size) * 2]);
 #pragma unroll
     for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k));
     float sum = 0.0f;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    const int parts = (int)(j1 - j0 + 1);
-#pragma unroll 8
-    for (int k = 0; k < parts; ++k) {
-        const int64_t e = at + (int64_t)k * size;
-        const float w = weight(p.part_ml[2 * e], m), l = p.part_ml[2 * e + 1];
-        sum += l == 0.0f ? 0.0f : w * l;
-        if (c < p.dim) v += *reinterpret_cast<const f32x4 *>(p.part + e * p.dim + c) * w;
+    for (int k0 = 0; k0 < parts; k0 += 256) {  // 64 parts of the wave, one a lane
+        const int k = k0 + 4 * lane + wave;
+        float f = 0.0f;
+        if (k < parts) {
+            const float *ml = p.part_ml + (at + (int64_t)k * size) * 2;
+            f = weight(ml[0], m);
+            sum += ml[1] == 0.0f ? 0.0f : f * ml[1];
+        }
+        const int here = min(64, (parts - k0 - wave + 3) / kWaves);
+        const float *o4 = p.part + (at + (int64_t)(k0 + wave) * size) * p.dim + min(c, p.dim - 4);
+        for (int i = 0; i < here; ++i)
+            v += *reinterpret_cast<const f32x4 *>(o4 + (int64_t)i * 4 * size * p.dim) *
+                 __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f), i));
     }
+    sum = wave_sum(sum);
+    if (c < p.dim) *reinterpret_cast<f32x4 *>(&lds_o[wave][c]) = v;
+    if (lane == 0) lds_l[wave] = sum;
+    __syncthreads();
+    if (wave != 0 || c >= p.dim) return;
+    sum = 0.0f, v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < kWaves; ++k) sum += lds_l[k], v += *reinterpret_cast<const f32x4 *>(&lds_o[k][c]);
     v *= sum == 0.0f ? 0.0f : 1.0f / sum;
-    if (c < p.dim) *reinterpret_cast<uint2 *>(o + c) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+    *reinterpret_cast<uint2 *>(o + c) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
 
-template <int KS>
+template <int KS, bool FULL>
 void split(const AttnArgs &p, int rt, hipStream_t st) {
     const dim3 grid((unsigned)(p.groups * p.kv_heads)), block(kAttnThreads);
     if constexpr (KS <= 2)
         if (rt == 4) {
-            hipLaunchKernelGGL((k_attn_split<KS, 4>), grid, block, 0, st, p);
+            hipLaunchKernelGGL((k_attn_split<KS, 4, FULL>), grid, block, 0, st, p);
             return;
         }
     if (rt >= 2)
-        hipLaunchKernelGGL((k_attn_split<KS, 2>), grid, block, 0, st, p);
+        hipLaunchKernelGGL((k_attn_split<KS, 2, FULL>), grid, block, 0, st, p);
     else
-        hipLaunchKernelGGL((k_attn_split<KS, 1>), grid, block, 0, st, p);
+        hipLaunchKernelGGL((k_attn_split<KS, 1, FULL>), grid, block, 0, st, p);
 }
 
-template <int KS>
+template <int KS, bool FULL>
 void rows(const AttnArgs &p, hipStream_t st) {
     const dim3 grid((unsigned)((int64_t)p.pieces * p.kv_heads)), block(kAttnThreads);
-    if constexpr (KS <= 2)
-        hipLaunchKernelGGL((k_attn_rows<KS, 2>), grid, block, 0, st, p);
-    else
-        hipLaunchKernelGGL((k_attn_rows<KS, 1>), grid, block, 0, st, p);
+    constexpr size_t lds = 4 * 64 * 64 * KS * 2;
+    hipLaunchKernelGGL((k_attn_rows<KS, KS <= 2 ? 4 : 2, FULL>), grid, block, lds, st, p);
 }
 
-int rows_tiles(int ks) { return ks <= 2 ? 2 : 1; }
+int rows_tiles(int ks) { return ks <= 2 ? 4 : 2; }
 
 }  // namespace
 
@@ -543,7 +794,7 @@ AttnPlan plan_attention(int64_t tokens, int seqs, int width, int kv_heads, int g
     const int64_t all = tokens * group, mean = seqs ? (all + seqs - 1) / seqs : 0;  // rows of a head; of a sequence
     const int big = 64 * rows_tiles(ks);
     // Rows over the waves where that makes work for the whole GPU, else blocks over the work-groups.
-    if (mean > 64 && (all / big) * kv_heads >= 512) {
+    if (mean > 64 && (all / big) * kv_heads >= 256) {
         plan.rows = true;
         plan.size = big;
         plan.pieces = all / big + seqs;
@@ -568,15 +819,30 @@ hipError_t launch_attention(const AttnArgs &a, void *ws, hipStream_t st) {
     p.pieces = (int)plan.pieces, p.groups = plan.groups;
     p.part = static_cast<float *>(ws);
     p.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + plan.part_bytes);
-    const int ks = (p.dim + 63) / 64;
-    if (plan.rows) {
-        ks == 1 ? rows<1>(p, st) : ks == 2 ? rows<2>(p, st) : ks == 3 ? rows<3>(p, st) : rows<4>(p, st);
-        return hipGetLastError();
+    // The sizes most heads have, and forms for any other.
+    auto run = [&](auto ks, auto full) {
+        if (plan.rows)
+            rows<ks.value, full.value>(p, st);
+        else
+            split<ks.value, full.value>(p, plan.rt, st);
+    };
+    using std::integral_constant;
+    using Full = std::true_type;
+    using Part = std::false_type;
+    switch (p.dim) {
+        case 64: run(integral_constant<int, 1>{}, Full{}); break;
+        case 128: run(integral_constant<int, 2>{}, Full{}); break;
+        case 256: run(integral_constant<int, 4>{}, Full{}); break;
+        default:
+            if (p.dim < 64) run(integral_constant<int, 1>{}, Part{});
+            else if (p.dim < 128) run(integral_constant<int, 2>{}, Part{});
+            else if (p.dim <= 192) run(integral_constant<int, 3>{}, Part{});
+            else run(integral_constant<int, 4>{}, Part{});
     }
-    ks == 1 ? split<1>(p, plan.rt, st) : ks == 2 ? split<2>(p, plan.rt, st) : ks == 3 ? split<3>(p, plan.rt, st) : split<4>(p, plan.rt, st);
+    if (plan.rows) return hipGetLastError();
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const int most = p.seq.starts ? plan.size : std::min(plan.size, p.group);  // rows of a tile
-    const dim3 grid((unsigned)((int64_t)p.pieces * p.kv_heads), (unsigned)((most + kWaves - 1) / kWaves));
+    const dim3 grid((unsigned)((int64_t)p.pieces * p.kv_heads), (unsigned)most);
     hipLaunchKernelGGL(k_attn_join, grid, dim3(kAttnThreads), 0, st, p, plan.size);
     return hipGetLastError();
 }

@@ -134,7 +134,7 @@ NVFP4_API int nvfp4_attention(const nvfp4_kv_cache_t *c, const nvfp4_sequences_t
     if (e != NVFP4_OK) return e;
     e = check_plan(tokens, s->seqs, s->width, heads, c->kv_heads, c->dim);
     if (e != NVFP4_OK) return e;
-    if ((causal != 0 && causal != 1) || !(fabsf(scale) < INFINITY) || !aligned(workspace, 256)) return NVFP4_ERR_INVALID_ARG;
+    if ((causal != 0 && causal != 1) || !(fabsf(scale) < 1e30f) || !(fabsf(scale) > 1e-30f) || !aligned(workspace, 256)) return NVFP4_ERR_INVALID_ARG;
     if (tokens == 0 || s->seqs == 0) return NVFP4_OK;
     if (!q || !out || !aligned(q, 2) || !aligned(out, 16)) return NVFP4_ERR_INVALID_ARG;
     if ((tokens > 1 && q_token < c->dim) || (heads > 1 && q_head < c->dim)) return NVFP4_ERR_INVALID_ARG;
@@ -142,7 +142,8 @@ NVFP4_API int nvfp4_attention(const nvfp4_kv_cache_t *c, const nvfp4_sequences_t
     p.seq = sequences(c, s, tokens);
     p.q = static_cast<const uint16_t *>(q), p.qs = q_token, p.qh = q_head;
     p.k_codes = c->k_codes, p.v_codes = c->v_codes, p.k_scales = c->k_scales, p.v_scales = c->v_scales;
-    p.out = static_cast<uint16_t *>(out), p.scale2 = (float)((double)scale * 1.4426950408889634);
+    p.out = static_cast<uint16_t *>(out), p.scale2 = (float)(fabs((double)scale) * 1.4426950408889634);
+    p.slack = 8.0f / p.scale2, p.flip = scale < 0.0f ? 0x80008000u : 0u;
     p.kv_heads = c->kv_heads, p.group = heads / c->kv_heads, p.dim = c->dim, p.causal = causal;
     hipStream_t st = static_cast<hipStream_t>(stream);
     const nvfp4::AttnPlan plan = nvfp4::plan_attention(tokens, s->seqs, s->width, c->kv_heads, p.group, c->dim);

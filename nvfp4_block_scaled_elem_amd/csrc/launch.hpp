@@ -229,7 +229,8 @@ struct AttnArgs {
     const uint8_t *k_codes, *v_codes, *k_scales, *v_scales;
     uint16_t *out;
     float *part, *part_ml;  // parts of tiles that several work-groups share: outputs; (maximum, sum)
-    float scale2;           // the scores' factor, in powers of two
+    float scale2, slack;    // the scores' factor (positive) in powers of two; 8 / scale2
+    uint32_t flip;          // of two bf16: the signs, for a negative factor
     int kv_heads, group, dim, causal;
     int pieces, groups;  // set by the launcher
 };
