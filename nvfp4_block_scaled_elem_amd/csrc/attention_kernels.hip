@@ -310,7 +310,7 @@ __device__ __forceinline__ uint16_t *out_row(const AttnArgs &p, const Seq &q, in
 // Per block b: the scores of block b + 1 are multiplied while the probabilities of b are computed, and V of b is
 // multiplied while the codes of K of b + 2 and V of b + 1 are decoded: K runs a block ahead of V, each in two buffers.
 template <int KS, int RT, bool FULL>
-__global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(1, 1))) void k_attn_rows(AttnArgs p) {
+__global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(AttnArgs p) {
     constexpr int kRows = 16 * RT * kWaves, kHalf = 64 * 64 * KS * 2;  // LDS bytes of a block's K or V
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     uint8_t *const lds_k = lds, *const lds_v = lds + 2 * kHalf;
@@ -445,28 +445,22 @@ __global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(1,
         for (int e = tid; e < 4 * kHalf / 16; e += kAttnThreads) reinterpret_cast<u32x4 *>(lds)[e] = u32x4{0u, 0u, 0u, 0u};
         __syncthreads();
     }
-    f32x4 S[RT][4];
-    int live = 0, live1 = 0;  // of the blocks b and b + 1
+    int live = 0;  // of the block that is computed
     if (count > 0) {
         load_k(0);
+        load_v(0, kb);
         live = kb.live;
-        const Block b0 = kb;
-        load_v(0, b0);
         store_k(0);
         store_v(0);
         load_k(1);
-        live1 = kb.live;
-        store_k(1);
         load_v(1, kb);
-        load_k(2);
-        __syncthreads();
-        scores(0, S);
-        __syncthreads();
+        lds_barrier();
     }
 #pragma unroll 1
     for (int b = 0; b < count; ++b) {
         const int t0 = b * kPage;
-        // The maximum that exponents are taken against, raised where a score is far above it.
+        f32x4 S[RT][4];
+        scores(b, S);
         if (t0 + kPage > safe || !live) {
 #pragma unroll
             for (int r = 0; r < RT; ++r)
@@ -476,6 +470,7 @@ __global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(1,
                     for (int j = 0; j < 4; ++j)
                         S[r][t][j] = live && t0 + 16 * t + 4 * g + j < R.lim[r] ? S[r][t][j] : kNegInf;
         }
+        // The maximum that exponents are taken against, raised where a score is far above it.
         bool more = false;
         float top[RT];
 #pragma unroll
@@ -498,8 +493,6 @@ __global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(1,
                 for (int d = 0; d < 4 * KS; ++d) R.o[r][d] *= w;
             }
         }
-        f32x4 S1[RT][4];
-        scores(b + 1, S1);  // (of a block that is not there: never looked at)
         bf16x8 P[RT][2];
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
@@ -528,17 +521,12 @@ __global__ __launch_bounds__(kAttnThreads) __attribute__((amdgpu_waves_per_eu(1,
 #pragma unroll
                 for (int r = 0; r < RT; ++r) R.o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, P[r][u], R.o[r][d], 0, 0, 0);
             }
+        store_k(b + 1);
         store_v(b + 1);
-        store_k(b + 2);
-        const Block next = kb;
-        load_v(b + 2, next);
-        live = live1, live1 = next.live;
-        load_k(b + 3);
+        live = kb.live;
+        load_k(b + 2);
+        load_v(b + 2, kb);
         lds_barrier();
-#pragma unroll
-        for (int r = 0; r < RT; ++r)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) S[r][t] = S1[r][t];
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -781,10 +769,9 @@ template <int KS, bool FULL>
 void rows(const AttnArgs &p, hipStream_t st) {
     const dim3 grid((unsigned)((int64_t)p.pieces * p.kv_heads)), block(kAttnThreads);
     constexpr size_t lds = 4 * 64 * 64 * KS * 2;
-    hipLaunchKernelGGL((k_attn_rows<KS, KS <= 2 ? 4 : 2, FULL>), grid, block, lds, st, p);
+    hipLaunchKernelGGL((k_attn_rows<KS, 2, FULL>), grid, block, lds, st, p);
 }
 
-int rows_tiles(int ks) { return ks <= 2 ? 4 : 2; }
 
 }  // namespace
 
@@ -792,7 +779,7 @@ AttnPlan plan_attention(int64_t tokens, int seqs, int width, int kv_heads, int g
     AttnPlan plan = {};
     const int ks = (dim + 63) / 64;
     const int64_t all = tokens * group, mean = seqs ? (all + seqs - 1) / seqs : 0;  // rows of a head; of a sequence
-    const int big = 64 * rows_tiles(ks);
+    const int big = 128;
     // Rows over the waves where that makes work for the whole GPU, else blocks over the work-groups.
     if (mean > 64 && (all / big) * kv_heads >= 256) {
         plan.rows = true;
