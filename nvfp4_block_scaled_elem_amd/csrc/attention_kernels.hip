@@ -377,23 +377,15 @@ __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(Att
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
             const int e = tid + kAttnThreads * i;
-            kraw[i] = u32x4{0u, 0u, 0u, 0u};
-            if (kb.live && (FULL || e < pieces)) kraw[i] = *reinterpret_cast<const u32x4 *>(p.k_codes + kb.base + 16 * e);
+            kraw[i] = *reinterpret_cast<const u32x4 *>(p.k_codes + kb.base + 16u * (uint32_t)(FULL ? e : min(e, pieces - 1)));
         }
     };
-    auto load_v = [&](int b, const Block &B) __attribute__((always_inline)) {
-        vb = B;
-        const int n = q.len - b * kPage - 16 * (tid & 3);  // tokens of the piece in front of the end
+    auto load_v = [&]() __attribute__((always_inline)) {
+        vb = kb;
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
             const int e = tid + kAttnThreads * i;
-            vraw[i] = u32x4{0u, 0u, 0u, 0u};
-            if (vb.live && (FULL || e < pieces)) vraw[i] = *reinterpret_cast<const u32x4 *>(p.v_codes + vb.base + 16 * e);
-        }
-        if (n < 16) {  // codes behind the end may be any bytes
-            const u32x4 keep = tokens_kept(n);
-#pragma unroll
-            for (int i = 0; i < KS; ++i) vraw[i] &= keep;
+            vraw[i] = *reinterpret_cast<const u32x4 *>(p.v_codes + vb.base + 16u * (uint32_t)(FULL ? e : min(e, pieces - 1)));
         }
     };
     // Piece c = 4 i + g of a token: k = 64 i + 16 g .. + 15, the operands 2 i and 2 i + 1 of the token's tile, at lane
@@ -411,6 +403,11 @@ __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(Att
     };
     auto store_v = [&](int b) __attribute__((always_inline)) {
         uint8_t *const to = lds_v + (b & 1) * kHalf;
+        if ((b + 1) * kPage > q.len || !vb.live) {  // codes behind the end, and of no page, may be any bytes
+            const u32x4 keep = tokens_kept(vb.live ? q.len - b * kPage - 16 * (tid & 3) : 0);
+#pragma unroll
+            for (int i = 0; i < KS; ++i) vraw[i] &= keep;
+        }
 #pragma unroll
         for (int i = 0; i < KS; ++i) {
             const int e = tid + kAttnThreads * i, d = e >> 2, c = e & 3;  // column; 16 tokens
@@ -448,12 +445,12 @@ __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(Att
     int live = 0;  // of the block that is computed
     if (count > 0) {
         load_k(0);
-        load_v(0, kb);
+        load_v();
         live = kb.live;
         store_k(0);
         store_v(0);
         load_k(1);
-        load_v(1, kb);
+        load_v();
         lds_barrier();
     }
 #pragma unroll 1
@@ -525,7 +522,7 @@ __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(Att
         store_v(b + 1);
         live = kb.live;
         load_k(b + 2);
-        load_v(b + 2, kb);
+        load_v();
         lds_barrier();
     }
 #pragma unroll
@@ -691,14 +688,18 @@ __global__ __launch_bounds__(kAttnThreads, RT * KS <= 2 ? 2 : 1) void k_attn_spl
     }
 }
 
-// The tiles whose blocks lie in several shares, and the rows of sequences of no tokens (zeros). A work-group takes a row,
-// its waves every fourth part, joined in wave order.
+// The tiles whose blocks lie in several shares, and the rows of sequences of no tokens (zeros). TOGETHER: a work-group takes a
+// row, its waves every fourth part, joined in wave order; else a wave takes a row.
+template <bool TOGETHER>
 __global__ __launch_bounds__(kAttnThreads) void k_attn_join(AttnArgs p, int size) {
-    __shared__ float lds_o[kWaves][kMaxHeadDim], lds_l[kWaves];
+    constexpr int kShare = TOGETHER ? kWaves : 1;
+    __shared__ float lds_o[TOGETHER ? kWaves : 1][TOGETHER ? kMaxHeadDim : 1], lds_l[kWaves];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int64_t h = blockIdx.x % p.kv_heads;
-    const int piece = (int)(blockIdx.x / p.kv_heads), row = (int)blockIdx.y;  // of the tile
+    const int piece = (int)(blockIdx.x / p.kv_heads), row = TOGETHER ? (int)blockIdx.y : (int)blockIdx.y * kWaves + wave;  // of the tile
+    const int turn = TOGETHER ? wave : 0;
+    if (row >= size) return;
     Window w;
     const uint32_t total = list_total(p, size, w);
     const int s = piece_sequence(p.seq, piece, p.group, size, 1);
@@ -710,7 +711,7 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_join(AttnArgs p, int size
     const int c = 4 * lane;
     const uint32_t nb = (uint32_t)blocks_of(q);
     if (nb == 0u) {
-        if (wave == 0 && c < p.dim) *reinterpret_cast<uint2 *>(o + c) = make_uint2(0u, 0u);
+        if (turn == 0 && c < p.dim) *reinterpret_cast<uint2 *>(o + c) = make_uint2(0u, 0u);
         return;
     }
     const Share sh = share_of(p, total);
@@ -725,28 +726,32 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_join(AttnArgs p, int size
     for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k));
     float sum = 0.0f;
     f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k0 = 0; k0 < parts; k0 += 256) {  // 64 parts of the wave, one a lane
-        const int k = k0 + 4 * lane + wave;
+    for (int k0 = 0; k0 < parts; k0 += 64 * kShare) {  // 64 parts of the wave, one a lane
+        const int k = k0 + kShare * lane + turn;
         float f = 0.0f;
         if (k < parts) {
             const float *ml = p.part_ml + (at + (int64_t)k * size) * 2;
             f = weight(ml[0], m);
             sum += ml[1] == 0.0f ? 0.0f : f * ml[1];
         }
-        const int here = min(64, (parts - k0 - wave + 3) / kWaves);
-        const float *o4 = p.part + (at + (int64_t)(k0 + wave) * size) * p.dim + min(c, p.dim - 4);
+        const int here = min(64, (parts - k0 - turn + kShare - 1) / kShare);
+        const float *o4 = p.part + (at + (int64_t)(k0 + turn) * size) * p.dim + min(c, p.dim - 4);
         for (int i = 0; i < here; ++i)
-            v += *reinterpret_cast<const f32x4 *>(o4 + (int64_t)i * 4 * size * p.dim) *
+            v += *reinterpret_cast<const f32x4 *>(o4 + (int64_t)i * kShare * size * p.dim) *
                  __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f), i));
     }
     sum = wave_sum(sum);
-    if (c < p.dim) *reinterpret_cast<f32x4 *>(&lds_o[wave][c]) = v;
-    if (lane == 0) lds_l[wave] = sum;
-    __syncthreads();
-    if (wave != 0 || c >= p.dim) return;
-    sum = 0.0f, v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (TOGETHER) {
+        if (c < p.dim) *reinterpret_cast<f32x4 *>(&lds_o[wave][c]) = v;
+        if (lane == 0) lds_l[wave] = sum;
+        __syncthreads();
+        if (wave != 0) return;
+        sum = 0.0f, v = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        if (c < p.dim)
 #pragma unroll
-    for (int k = 0; k < kWaves; ++k) sum += lds_l[k], v += *reinterpret_cast<const f32x4 *>(&lds_o[k][c]);
+            for (int k = 0; k < kWaves; ++k) sum += lds_l[k], v += *reinterpret_cast<const f32x4 *>(&lds_o[k][c]);
+    }
+    if (c >= p.dim) return;
     v *= sum == 0.0f ? 0.0f : 1.0f / sum;
     *reinterpret_cast<uint2 *>(o + c) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
 }
@@ -829,8 +834,13 @@ hipError_t launch_attention(const AttnArgs &a, void *ws, hipStream_t st) {
     if (plan.rows) return hipGetLastError();
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const int most = p.seq.starts ? plan.size : std::min(plan.size, p.group);  // rows of a tile
-    const dim3 grid((unsigned)((int64_t)p.pieces * p.kv_heads), (unsigned)most);
-    hipLaunchKernelGGL(k_attn_join, grid, dim3(kAttnThreads), 0, st, p, plan.size);
+    // Many parts to a tile: a work-group each row (one sequence of 8000 tokens, 31 parts: 4.4 us, 10.6 with a wave a row); else
+    // the rows' work is mostly finding their place (64 sequences, 0 to 16 parts: 6.4 us, 9.0 with a work-group a row).
+    const unsigned pieces = (unsigned)((int64_t)p.pieces * p.kv_heads);
+    if (p.groups >= 8 * (int64_t)p.pieces)
+        hipLaunchKernelGGL(k_attn_join<true>, dim3(pieces, (unsigned)most), dim3(kAttnThreads), 0, st, p, plan.size);
+    else
+        hipLaunchKernelGGL(k_attn_join<false>, dim3(pieces, (unsigned)((most + kWaves - 1) / kWaves)), dim3(kAttnThreads), 0, st, p, plan.size);
     return hipGetLastError();
 }
 

@@ -32,6 +32,7 @@ KVCache = collections.namedtuple("KVCache", "k v k_scales v_scales")
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 _SCALES = (torch.float8_e8m0fnu, torch.uint8)
 _AXES = 4
+_Sections = ctypes.c_int * _AXES
 
 
 class _RotaryArgs(ctypes.Structure):
@@ -39,7 +40,7 @@ class _RotaryArgs(ctypes.Structure):
         ("x", ctypes.c_void_p), ("xs", ctypes.c_int64), ("xh", ctypes.c_int64), ("y", ctypes.c_void_p),
         ("ys", ctypes.c_int64), ("yh", ctypes.c_int64), ("dtype", ctypes.c_int), ("tokens", ctypes.c_int64),
         ("heads", ctypes.c_int), ("dim", ctypes.c_int), ("positions", ctypes.c_void_p), ("positions64", ctypes.c_int),
-        ("axes", ctypes.c_int), ("sections", ctypes.c_int * _AXES), ("base", ctypes.c_double), ("inverse", ctypes.c_int),
+        ("axes", ctypes.c_int), ("sections", _Sections), ("base", ctypes.c_double), ("inverse", ctypes.c_int),
         ("stream", ctypes.c_void_p),
     ]
 
@@ -65,7 +66,7 @@ def _heads(t, name, dtypes, dev=None, shape=None):
     if dev is not None and t.device != dev:
         raise NVFP4Error(f"{name} must be on {dev}")
     tokens, heads, dim = t.shape
-    if shape is not None and (tokens, heads, dim) != shape:
+    if shape is not None and t.shape != shape:
         raise NVFP4Error(f"{name} must be {list(shape)}, got {[tokens, heads, dim]}")
     st, sh, sc = t.stride()
     if (sc != 1 and dim > 1) or (heads > 1 and sh < dim) or (tokens > 1 and st < dim):
@@ -93,7 +94,7 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, *, sections=None, base: flo
             raise NVFP4Error("an odd dim needs sections")
     if not 1 <= axes <= _AXES or len(sections) != axes:
         raise NVFP4Error(f"sections must give the pairs of each of {axes} axes (at most {_AXES})")
-    if any(n < 0 for n in sections) or not 0 < 2 * sum(sections) <= dim:
+    if min(sections) < 0 or not 0 < 2 * sum(sections) <= dim:
         raise NVFP4Error(f"the sections must be of one to {dim // 2} pairs together")
     if out is not None:
         if not isinstance(out, torch.Tensor) or out.shape != x.shape or out.dtype != x.dtype or out.device != dev:
@@ -108,10 +109,10 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, *, sections=None, base: flo
     _no_graph(x, out)
 
     def call(st):
-        y = torch.empty(x.shape, dtype=x.dtype, device=dev) if out is None else out
+        y = torch.empty_like(x, memory_format=torch.contiguous_format) if out is None else out
         ys, yh, _ = y.stride()
         a = _RotaryArgs(x.data_ptr(), xs, xh, y.data_ptr(), ys, yh, DTYPES[x.dtype], tokens, heads, dim, positions.data_ptr(),
-                        int(positions.dtype == torch.int64), axes, (ctypes.c_int * _AXES)(*sections), base, int(inverse), st)
+                        int(positions.dtype == torch.int64), axes, _Sections(*sections), base, int(inverse), st)
         _check(lib().nvfp4_rotary(ctypes.byref(a)))
         return y
 
@@ -131,31 +132,33 @@ def kv_cache(pages: int, kv_heads: int, dim: int, device="cuda") -> KVCache:
 
 def _cache(cache, dev):
     """Checks a cache; returns its C form, heads and dim."""
-    if not isinstance(cache, (tuple, list)) or len(cache) != 4 or not all(isinstance(t, torch.Tensor) for t in cache):
+    if not isinstance(cache, (tuple, list)) or len(cache) != 4:
         raise NVFP4Error("the cache must be (k, v, k_scales, v_scales), as kv_cache makes it")
+    for t, dtypes in zip(cache, (_CODES, _CODES, _SCALES, _SCALES)):
+        if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype not in dtypes or not t.is_contiguous():
+            raise NVFP4Error(f"the cache's codes must be contiguous E4M3 and its scales contiguous E8M0 tensors on {dev}")
     k, v, ks, vs = cache
     if k.dim() != 4 or k.shape[2] != PAGE:
         raise NVFP4Error(f"the cache's k must be [pages, kv_heads, {PAGE}, dim]")
     pages, heads, _, dim = k.shape
     if v.shape != (pages, heads, dim, PAGE) or ks.shape != (pages, heads) or vs.shape != (pages, heads):
         raise NVFP4Error(f"the cache's v must be {[pages, heads, dim, PAGE]} and its scales {[pages, heads]}")
-    for t, dtypes in ((k, _CODES), (v, _CODES), (ks, _SCALES), (vs, _SCALES)):
-        if t.device != dev or t.dtype not in dtypes or not t.is_contiguous():
-            raise NVFP4Error(f"the cache's codes must be contiguous E4M3 and its scales contiguous E8M0 tensors on {dev}")
     return _Cache(k.data_ptr(), v.data_ptr(), ks.data_ptr(), vs.data_ptr(), pages, heads, dim), heads, dim
 
 
 def _ints(t, name, n, dev):
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != dev or tuple(t.shape) != (n,)
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != dev or t.shape != (n,)
             or not t.is_contiguous()):
         raise NVFP4Error(f"{name} must be a contiguous [{n}] int32 tensor on {dev}")
 
 
 def _sequences(table, lengths, starts, tokens, dev):
-    if (not isinstance(table, torch.Tensor) or table.dim() != 2 or table.dtype != torch.int32 or table.device != dev
-            or (table.shape[1] > 1 and table.stride(1) != 1) or (table.shape[0] > 1 and table.stride(0) < table.shape[1])):
-        raise NVFP4Error(f"table must be a [seqs, width] int32 tensor with unit column stride on {dev}")
+    if not isinstance(table, torch.Tensor) or table.dim() != 2 or table.dtype != torch.int32 or table.device != dev:
+        raise NVFP4Error(f"table must be a [seqs, width] int32 tensor on {dev}")
     seqs, width = table.shape
+    ldt, unit = table.stride()
+    if (width > 1 and unit != 1) or (seqs > 1 and ldt < width):
+        raise NVFP4Error("table must have unit column stride and rows that do not overlap")
     _ints(lengths, "lengths", seqs, dev)
     if starts is not None:
         _ints(starts, "starts", seqs + 1, dev)
@@ -163,7 +166,7 @@ def _sequences(table, lengths, starts, tokens, dev):
         raise NVFP4Error(f"without starts there is one token for each of the {seqs} sequences, got {tokens}")
     if tokens and seqs and not width:
         raise NVFP4Error("the table has no columns")
-    return _Sequences(table.data_ptr(), table.stride(0), lengths.data_ptr(), _ptr(starts), seqs, width)
+    return _Sequences(table.data_ptr(), ldt, lengths.data_ptr(), _ptr(starts), seqs, width)
 
 
 def kv_append(cache, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, lengths: torch.Tensor, starts=None, *,
@@ -174,7 +177,7 @@ def kv_append(cache, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, leng
     rounded to the new one if it grows."""
     kt, kh = _heads(K, "K", DTYPES)
     dev = K.device
-    vt, vh = _heads(V, "V", (K.dtype,), dev, tuple(K.shape))
+    vt, vh = _heads(V, "V", (K.dtype,), dev, K.shape)
     c, heads, dim = _cache(cache, dev)
     tokens = K.shape[0]
     if K.shape[1:] != (heads, dim):
@@ -214,7 +217,7 @@ def attention(Q: torch.Tensor, cache, table: torch.Tensor, lengths: torch.Tensor
     _no_graph(Q, out)
 
     def call(st):
-        O = torch.empty(Q.shape, dtype=torch.bfloat16, device=dev) if out is None else out
+        O = torch.empty_like(Q, memory_format=torch.contiguous_format) if out is None else out
         ws, nbytes = _space(workspace, attention_workspace_bytes(tokens, q.seqs, q.width, heads, kv_heads, dim), dev)
         _check(lib().nvfp4_attention(ctypes.byref(c), ctypes.byref(q), Q.data_ptr(), qt, qh, heads, tokens,
                                      dim ** -0.5 if scale is None else scale, int(causal), O.data_ptr(), _ptr(ws), nbytes, st))
@@ -251,9 +254,10 @@ def _experts(W, name, experts, dev, rows=None, cols=None):
         raise NVFP4Error(f"{name} must be {experts} matrices of {[rows, cols]}, got {[n, k]}")
     if scales.shape != (experts, n, k // 16) or alphas.shape != (experts,):
         raise NVFP4Error(f"{name}'s scales must be {[experts, n, k // 16]} and its alphas [{experts}]")
-    for t, dtype in ((codes, torch.uint8), (scales, torch.uint8), (alphas, torch.float32)):
-        if t.dtype != dtype or t.device != dev or not t.is_contiguous():
-            raise NVFP4Error(f"{name} must be contiguous uint8 codes and scales and float32 alphas on {dev}")
+    if (codes.dtype != torch.uint8 or scales.dtype != torch.uint8 or alphas.dtype != torch.float32 or codes.device != dev
+            or scales.device != dev or alphas.device != dev or not codes.is_contiguous() or not scales.is_contiguous()
+            or not alphas.is_contiguous()):
+        raise NVFP4Error(f"{name} must be contiguous uint8 codes and scales and float32 alphas on {dev}")
     return n, k
 
 
@@ -292,7 +296,7 @@ def moe(X: torch.Tensor, logits: torch.Tensor, up, down, top_k: int, *, activati
     _no_graph(X, logits, up[2], down[2], residual, out)
 
     def call(st):
-        Y = torch.empty((tokens, width), dtype=torch.bfloat16, device=dev) if out is None else out
+        Y = torch.empty_like(X, memory_format=torch.contiguous_format) if out is None else out
         ws, nbytes = _space(workspace, moe_workspace_bytes(tokens, width, inner, experts, top_k), dev)
         a = _MoeArgs(X.data_ptr(), ldx, logits.data_ptr(), ldl, DTYPES[logits.dtype], tokens, width, inner, experts, top_k,
                      up[0].data_ptr(), up[1].data_ptr(), up[2].data_ptr(), down[0].data_ptr(), down[1].data_ptr(),
