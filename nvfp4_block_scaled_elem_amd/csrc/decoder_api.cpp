@@ -170,7 +170,7 @@ int check_experts(int64_t tokens, int64_t width, int64_t inner, int experts, int
 
 NVFP4_API size_t nvfp4_moe_workspace_bytes(int64_t tokens, int64_t width, int64_t inner, int experts, int top_k) {
     if (check_experts(tokens, width, inner, experts, top_k) != NVFP4_OK || tokens == 0) return 0;
-    return nvfp4::moe_workspace(tokens, width, inner, top_k);
+    return nvfp4::moe_workspace(tokens, width, inner, experts, top_k);
 }
 
 NVFP4_API int nvfp4_moe(const nvfp4_moe_args_t *a) {
@@ -203,6 +203,6 @@ NVFP4_API int nvfp4_moe(const nvfp4_moe_args_t *a) {
     p.experts = a->experts, p.top_k = a->top_k, p.act = a->activation, p.gated = a->gated;
     p.sigmoid = a->scoring == NVFP4_SCORE_SIGMOID, p.normalize = a->normalize;
     hipStream_t st = static_cast<hipStream_t>(a->stream);
-    return with_scratch(a->workspace, a->workspace_bytes, nvfp4::moe_workspace(p.tokens, p.width, p.inner, p.top_k), st,
+    return with_scratch(a->workspace, a->workspace_bytes, nvfp4::moe_workspace(p.tokens, p.width, p.inner, p.experts, p.top_k), st,
                         [&](void *ws) { return nvfp4::launch_moe(p, ws, st); });
 }

@@ -264,8 +264,9 @@ struct MoeArgs {
     float *weights;
     uint16_t *h;
     float *z;
+    int split;  // parts of z
 };
-size_t moe_workspace(int64_t tokens, int64_t width, int64_t inner, int top_k);
+size_t moe_workspace(int64_t tokens, int64_t width, int64_t inner, int experts, int top_k);
 hipError_t launch_moe(const MoeArgs &p, void *ws, hipStream_t stream);
 
 hipError_t launch_dequant(const uint8_t *codes, const uint8_t *scales, const float *alpha, int64_t nblk, void *out,

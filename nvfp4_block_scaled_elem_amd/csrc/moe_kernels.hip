@@ -145,12 +145,13 @@ __device__ __forceinline__ int code_place(int r, int q) { return r * 64 + ((q ^ 
 
 // The chosen experts in order: the number `nth` of them (-1: there are not so many), and its pairs into `list`. By the whole
 // work-group; `seen` has a word per expert.
+template <int THREADS>
 __device__ __forceinline__ int take_expert(const MoeArgs &p, int nth, int *seen, uint16_t *list, int *count) {
     const int tid = threadIdx.x, lane = tid & 63, pairs = (int)p.tokens * p.top_k;
-    for (int e = tid; e < p.experts; e += kThreads) seen[e] = 0;
+    for (int e = tid; e < p.experts; e += THREADS) seen[e] = 0;
     if (tid == 0) *count = 0;
     __syncthreads();
-    for (int i = tid; i < pairs; i += kThreads) {
+    for (int i = tid; i < pairs; i += THREADS) {
         const int e = p.ids[i];
         if (e >= 0) seen[e] = 1;
     }
@@ -167,7 +168,7 @@ __device__ __forceinline__ int take_expert(const MoeArgs &p, int nth, int *seen,
     }
     if (mine < 0) return -1;
     // The pairs' order in the list decides their column alone, which no result depends on.
-    for (int i = tid; i < pairs; i += kThreads)
+    for (int i = tid; i < pairs; i += THREADS)
         if (p.ids[i] == mine) list[atomicAdd(count, 1)] = (uint16_t)i;
     __syncthreads();
     return mine;
@@ -183,7 +184,7 @@ __global__ __launch_bounds__(kThreads) void k_moe_product(MoeArgs p, int tiles) 
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int expert = take_expert(p, blockIdx.x / tiles, seen, list, &count);
+    const int expert = take_expert<kThreads>(p, blockIdx.x / tiles, seen, list, &count);
     if (expert < 0) return;
     const int64_t K = SECOND ? p.inner : p.width, F = SECOND ? p.width : p.inner;
     const int64_t f0 = (int64_t)(blockIdx.x % tiles) * 16, nch = (K + kChunk - 1) / kChunk;
@@ -286,6 +287,180 @@ __global__ __launch_bounds__(kThreads) void k_moe_product(MoeArgs p, int tiles) 
     }
 }
 
+// Many rows: a wave owns 32 weight rows (gated: 16 gate rows and their 16 up rows) over the whole sum, and a work-group's
+// four waves share the tokens' values, which go through LDS in slices of 512 k in the order of the operand. A wave's codes
+// and scales of a slice are all in flight while the slice before is multiplied: 9 KB a wave, no barrier waits for them.
+// MT: tiles of 16 pairs at a time. SECOND: the product with W2, its sum cut into p.split parts of slices, else with W1.
+constexpr int kRowWaves = 4, kRowThreads = 64 * kRowWaves, kSlice = 512, kSliceChunks = kSlice / kChunk;
+constexpr int kWaveCodes = 2 * (1024 + 512);  // LDS bytes of a wave: a chunk's codes and a slice's scales of two tiles
+
+template <int NT, int MT, bool SECOND>
+__global__ __launch_bounds__(kRowThreads, MT == 1 ? 4 : 2) void k_moe_rows(MoeArgs p, int tiles) {
+    constexpr int kXBytes = 16 * MT * kSlice * 2, kX = kXBytes / 16 / kRowThreads;  // of a slice; pieces a thread
+    constexpr int kCols = NT == 2 ? 16 * kRowWaves : 32 * kRowWaves;
+    __shared__ __attribute__((aligned(16))) uint8_t lds_x[2][kXBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t lds_w[kRowWaves][kWaveCodes];
+    __shared__ int seen[kMoeMaxExperts];
+    __shared__ uint16_t list[kMoeMaxPairs];
+    __shared__ int count;
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int expert = take_expert<kRowThreads>(p, blockIdx.x / tiles, seen, list, &count);
+    if (expert < 0) return;
+    const int K = (int)(SECOND ? p.inner : p.width), F = (int)(SECOND ? p.width : p.inner);
+    const int f0 = (int)(blockIdx.x % tiles) * kCols + (NT == 2 ? 16 : 32) * wave;
+    const int slices = (K + kSlice - 1) / kSlice;
+    const int s_lo = SECOND ? (int)((int64_t)slices * blockIdx.y / gridDim.y) : 0;
+    const int s_hi = SECOND ? (int)((int64_t)slices * (blockIdx.y + 1) / gridDim.y) : slices;
+    const MoeWeights &W = SECOND ? p.down : p.up;
+    const float alpha = W.alpha[expert];
+    const uint16_t *x = SECOND ? p.h : static_cast<const uint16_t *>(p.x);
+    const int64_t ldx = SECOND ? p.inner : p.ldx;
+    uint8_t *const wl = lds_w[wave];
+    // Rows of the two tiles; a tile past the last is read as the last.
+    const uint8_t *codes[2], *scales[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+        const int64_t row = (int64_t)expert * NT * F + (NT == 2 ? min(f0, F - 16) + j * F : min(f0 + 16 * j, F - 16));
+        codes[j] = W.codes + row * (K / 2);
+        scales[j] = W.scales + row * (K / 16);
+    }
+    // codes: the lane loads row lane / 4, 16 bytes lane % 4 of a chunk; scales: row lane / 4, the 8 of chunk lane % 4
+    const uint32_t coff = (uint32_t)(lane >> 2) * (uint32_t)(K / 2) + 16u * (lane & 3);
+    const uint32_t soff = (uint32_t)(lane >> 2) * (uint32_t)(K / 16) + 8u * (lane & 3);
+    const int pairs = count;
+    for (int c0 = 0; c0 < pairs; c0 += 16 * MT) {
+        u32x4 cv[2][kSliceChunks], xv[kX];
+        u32x2 sv[2];
+        f32x4 acc[2][MT] = {};
+        auto load_codes = [&](int s, int c) __attribute__((always_inline)) {
+            const int k0 = kSlice * s + kChunk * c;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint8_t *at = codes[j] + k0 / 2;
+                if (k0 + kChunk <= K) {
+                    cv[j][c] = *reinterpret_cast<const u32x4_any *>(at + coff);
+                } else {
+                    const int k = k0 + 32 * (lane & 3);
+                    cv[j][c] = u32x4{0u, 0u, 0u, 0u};
+                    if (k + 32 <= K) {
+                        cv[j][c] = *reinterpret_cast<const u32x4_any *>(at + coff);
+                    } else if (k < K) {  // the row's last 16
+                        const u32x2 d = *reinterpret_cast<const u32x2_any *>(at + coff);
+                        cv[j][c] = u32x4{d.x, d.y, 0u, 0u};
+                    }
+                }
+            }
+        };
+        auto load_scales = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const uint8_t *at = scales[j] + kSlice / 16 * s;
+                if (kSlice * (s + 1) <= K) {
+                    sv[j] = *reinterpret_cast<const u32x2_any *>(at + soff);
+                } else {
+                    sv[j] = u32x2{0u, 0u};
+                    const int left = (K - kSlice * s) / 16 - 8 * (lane & 3);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        if (e < left) sv[j][e >> 2] |= (uint32_t)at[soff + e] << (8 * (e & 3));
+                }
+            }
+        };
+        // Piece e of a slice: token e / 64 of the tiles, k = 8 (e % 64) .. + 7.
+        auto load_x = [&](int s) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < kX; ++i) {
+                const int e = tid + kRowThreads * i, r = e >> 6, k = kSlice * s + 8 * (e & 63);
+                xv[i] = u32x4{0u, 0u, 0u, 0u};
+                if (c0 + r < pairs && k < K) {
+                    const int pair = list[c0 + r];
+                    xv[i] = *reinterpret_cast<const u32x4_any *>(x + (int64_t)(SECOND ? pair : pair / p.top_k) * ldx + k);
+                }
+            }
+        };
+        // In LDS: [chunk][token tile][product i][lane] pieces, token r at lane (r ^ f) + 16 g with f of the piece's place in
+        // its chunk: the sixteen pieces of a chunk that neighbouring threads write meet no bank twice.
+        auto x_place = [&](int c, int m, int i, int gg, int r) __attribute__((always_inline)) {
+            return (((c * MT + m) * 4 + i) * 64 + 16 * gg + (r ^ (4 * gg + i))) * 16;
+        };
+        if (s_lo < s_hi) {
+            load_x(s_lo);
+            load_scales(s_lo);
+#pragma unroll
+            for (int c = 0; c < kSliceChunks; ++c) load_codes(s_lo, c);
+        }
+#pragma unroll 1
+        for (int s = s_lo; s < s_hi; ++s) {
+            uint8_t *const xb = lds_x[s & 1];
+#pragma unroll
+            for (int i = 0; i < kX; ++i) {
+                const int e = tid + kRowThreads * i, r = e >> 6, q = e & 63;
+                *reinterpret_cast<u32x4 *>(xb + x_place(q >> 4, r >> 4, q & 3, (q >> 2) & 3, r & 15)) = xv[i];
+            }
+            lds_barrier();
+            const int next = min(s + 1, s_hi - 1);  // (the last slice again: nothing looks at it)
+            load_x(next);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) *reinterpret_cast<u32x2 *>(wl + 2048 + 512 * j + 8 * lane) = sv[j];
+            load_scales(next);
+#pragma unroll
+            for (int c = 0; c < kSliceChunks; ++c) {
+                wave_handover();
+#pragma unroll
+                for (int j = 0; j < 2; ++j) *reinterpret_cast<u32x4 *>(wl + 1024 * j + code_place(lane >> 2, lane & 3)) = cv[j][c];
+                load_codes(next, c);
+                wave_handover();
+                bf16x8 b[MT][4];
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) b[m][i] = *reinterpret_cast<const bf16x8 *>(xb + x_place(c, m, i, g, r16));
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const u32x4 cur = *reinterpret_cast<const u32x4 *>(wl + 1024 * j + code_place(r16, g));
+                    const uint32_t sb = *reinterpret_cast<const u16_lds *>(wl + 2048 + 512 * j + 32 * r16 + 8 * c + 2 * g);
+                    const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8((int)(sb & 0x7F7Fu), false);  // both scales
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint4 w = dequant8(cur[i], i < 2 ? d.x : d.y);
+#pragma unroll
+                        for (int m = 0; m < MT; ++m)
+                            acc[j][m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, w), b[m][i], acc[j][m], 0, 0, 0);
+                    }
+                }
+            }
+        }
+        // Element r of the lane is weight row 4 g + r of a tile, pair r16 of a tile of pairs.
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+            if (c0 + 16 * m + r16 >= pairs) continue;
+            const int64_t pair = list[c0 + 16 * m + r16];
+            if (SECOND) {
+                const float w = p.weights[pair];
+                float *z = p.z + ((int64_t)blockIdx.y * p.tokens * p.top_k + pair) * F + f0 + 4 * g;
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    if (f0 + 16 * j < F) *reinterpret_cast<f32x4 *>(z + 16 * j) = (acc[j][m] * alpha) * w;
+            } else {
+                uint16_t *h = p.h + pair * F + f0 + 4 * g;
+#pragma unroll
+                for (int j = 0; j < (NT == 2 ? 1 : 2); ++j) {
+                    if (f0 + 16 * j >= F) continue;
+                    float v[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        v[r] = act_value(alpha * acc[j][m][r], p.act);
+                        if (NT == 2) v[r] *= alpha * acc[1][m][r];
+                    }
+                    *reinterpret_cast<uint2 *>(h + 16 * j) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+                }
+            }
+        }
+        lds_barrier();  // the last slices have been read
+    }
+}
+
 // y of eight columns of a token per thread: the parts in the order of the choices.
 __global__ __launch_bounds__(256) void k_moe_sum(MoeArgs p, int per) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, t = i / per, c = 8 * (i % per);
@@ -299,24 +474,67 @@ __global__ __launch_bounds__(256) void k_moe_sum(MoeArgs p, int per) {
     for (int j = 0; j < p.top_k; ++j) {
         const int64_t q = t * p.top_k + j;
         if (p.ids[q] < 0) break;
-        float z[8];
-        Raw8<float> r;
-        r.load(p.z + q * p.width + c, 8);
-        r.get(z);
+        for (int part = 0; part < p.split; ++part) {
+            float z[8];
+            Raw8<float> r;
+            r.load(p.z + ((int64_t)part * p.tokens * p.top_k + q) * p.width + c, 8);
+            r.get(z);
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] += z[k];
+            for (int k = 0; k < 8; ++k) v[k] += z[k];
+        }
     }
     put8(p.y + t * p.width + c, v, 8);
 }
 
 size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
+// Which kernels a call takes, and how many parts the second product's sum is cut into.
+struct Plan {
+    int up_rows, down_rows, mt, split;
+};
+
+Plan plan_moe(int64_t tokens, int64_t width, int64_t inner, int experts, int top_k, bool gated) {
+    // Experts that some token chooses, if all are as likely.
+    double idle = 1.0;
+    for (int64_t t = 0; t < tokens && idle > 1e-3; ++t) idle *= 1.0 - (double)top_k / experts;
+    const double used = experts * (1.0 - idle);
+    Plan plan = {};
+    plan.mt = tokens * top_k > 12 * used ? 2 : 1;  // pairs of an expert
+    const int64_t up = (inner + (gated ? 63 : 127)) / (gated ? 64 : 128), down = (width + 127) / 128;
+    plan.up_rows = used * up >= 192;
+    plan.down_rows = used * down >= 128;
+    plan.split = 1;
+    if (plan.down_rows) {
+        const int64_t slices = (inner + kSlice - 1) / kSlice;
+        while (plan.split < 8 && 4 * plan.split <= slices && used * down * plan.split < 768) plan.split *= 2;
+    }
+    return plan;
+}
+
+template <int NT, bool SECOND>
+void product(const MoeArgs &p, int64_t chosen, bool by_rows, int mt, hipStream_t st) {
+    const int64_t F = SECOND ? p.width : p.inner;
+    if (!by_rows) {
+        const int tiles = (int)((F + 15) / 16);
+        hipLaunchKernelGGL((k_moe_product<NT, SECOND>), dim3((unsigned)(chosen * tiles)), dim3(kThreads), 0, st, p, tiles);
+        return;
+    }
+    constexpr int kCols = NT == 2 ? 16 * kRowWaves : 32 * kRowWaves;
+    const int tiles = (int)((F + kCols - 1) / kCols);
+    const dim3 grid((unsigned)(chosen * tiles), SECOND ? p.split : 1), block(kRowThreads);
+    if (mt == 1)
+        hipLaunchKernelGGL((k_moe_rows<NT, 1, SECOND>), grid, block, 0, st, p, tiles);
+    else
+        hipLaunchKernelGGL((k_moe_rows<NT, 2, SECOND>), grid, block, 0, st, p, tiles);
+}
+
 }  // namespace
 
 // ids, weights, h, z
-size_t moe_workspace(int64_t tokens, int64_t width, int64_t inner, int top_k) {
+size_t moe_workspace(int64_t tokens, int64_t width, int64_t inner, int experts, int top_k) {
     const size_t pairs = (size_t)(tokens * top_k);
-    return 2 * round256(4 * pairs) + round256(2 * pairs * inner) + round256(4 * pairs * width);
+    const size_t split = std::max(plan_moe(tokens, width, inner, experts, top_k, false).split, plan_moe(tokens, width, inner, experts, top_k, true).split);
+    return 2 * round256(4 * pairs) + round256(2 * pairs * inner) + round256(4 * split * pairs * width);
 }
 
 hipError_t launch_moe(const MoeArgs &a, void *ws, hipStream_t st) {
@@ -327,16 +545,17 @@ hipError_t launch_moe(const MoeArgs &a, void *ws, hipStream_t st) {
     p.weights = reinterpret_cast<float *>(at), at += round256(4 * pairs);
     p.h = reinterpret_cast<uint16_t *>(at), at += round256(2 * pairs * p.inner);
     p.z = reinterpret_cast<float *>(at);
+    const Plan plan = plan_moe(p.tokens, p.width, p.inner, p.experts, p.top_k, p.gated);
+    p.split = plan.split;
     hipLaunchKernelGGL(k_moe_route, dim3((unsigned)((p.tokens + 3) / 4)), dim3(256), 0, st, p);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const int64_t chosen = std::min<int64_t>(p.experts, (int64_t)pairs);
-    const int t1 = (int)((p.inner + 15) / 16), t2 = (int)((p.width + 15) / 16);
     if (p.gated)
-        hipLaunchKernelGGL((k_moe_product<2, false>), dim3((unsigned)(chosen * t1)), dim3(kThreads), 0, st, p, t1);
+        product<2, false>(p, chosen, plan.up_rows, plan.mt, st);
     else
-        hipLaunchKernelGGL((k_moe_product<1, false>), dim3((unsigned)(chosen * t1)), dim3(kThreads), 0, st, p, t1);
+        product<1, false>(p, chosen, plan.up_rows, plan.mt, st);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    hipLaunchKernelGGL((k_moe_product<1, true>), dim3((unsigned)(chosen * t2)), dim3(kThreads), 0, st, p, t2);
+    product<1, true>(p, chosen, plan.down_rows, plan.mt, st);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const int per = (int)(p.width / 8);
     hipLaunchKernelGGL(k_moe_sum, dim3((unsigned)((p.tokens * per + 255) / 256)), dim3(256), 0, st, p, per);
