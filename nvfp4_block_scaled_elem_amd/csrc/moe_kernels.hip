@@ -144,9 +144,9 @@ constexpr int kChunk = 128, kChunkLds = 16 * 64 + 16 * 8;  // k per chunk; LDS b
 __device__ __forceinline__ int code_place(int r, int q) { return r * 64 + ((q ^ ((r >> 2) & 3)) << 4); }
 
 // The chosen experts in order: the number `nth` of them (-1: there are not so many), and its pairs into `list`. By the whole
-// work-group; `seen` has a word per expert.
+// work-group; `seen` has a byte per expert.
 template <int THREADS>
-__device__ __forceinline__ int take_expert(const MoeArgs &p, int nth, int *seen, uint16_t *list, int *count) {
+__device__ __forceinline__ int take_expert(const MoeArgs &p, int nth, uint8_t *seen, uint16_t *list, int *count) {
     const int tid = threadIdx.x, lane = tid & 63, pairs = (int)p.tokens * p.top_k;
     for (int e = tid; e < p.experts; e += THREADS) seen[e] = 0;
     if (tid == 0) *count = 0;
@@ -179,8 +179,8 @@ template <int NT, bool SECOND>
 __global__ __launch_bounds__(kThreads) void k_moe_product(MoeArgs p, int tiles) {
     constexpr int kStage = kWaves * NT * kChunkLds, kSums = kWaves * NT * 1024;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kStage > kSums ? kStage : kSums];
-    __shared__ int seen[kMoeMaxExperts];
-    __shared__ uint16_t list[kMoeMaxPairs];
+    __shared__ uint8_t seen[kMoeMaxExperts];
+    extern __shared__ uint16_t list[];  // an expert's pairs: as many as tokens at most
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -300,8 +300,8 @@ __global__ __launch_bounds__(kRowThreads, MT == 1 ? 4 : 2) void k_moe_rows(MoeAr
     constexpr int kCols = NT == 2 ? 16 * kRowWaves : 32 * kRowWaves;
     __shared__ __attribute__((aligned(16))) uint8_t lds_x[2][kXBytes];
     __shared__ __attribute__((aligned(16))) uint8_t lds_w[kRowWaves][kWaveCodes];
-    __shared__ int seen[kMoeMaxExperts];
-    __shared__ uint16_t list[kMoeMaxPairs];
+    __shared__ uint8_t seen[kMoeMaxExperts];
+    extern __shared__ uint16_t list[];  // an expert's pairs: as many as tokens at most
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -326,58 +326,58 @@ __global__ __launch_bounds__(kRowThreads, MT == 1 ? 4 : 2) void k_moe_rows(MoeAr
         scales[j] = W.scales + row * (K / 16);
     }
     // codes: the lane loads row lane / 4, 16 bytes lane % 4 of a chunk; scales: row lane / 4, the 8 of chunk lane % 4
-    const uint32_t coff = (uint32_t)(lane >> 2) * (uint32_t)(K / 2) + 16u * (lane & 3);
-    const uint32_t soff = (uint32_t)(lane >> 2) * (uint32_t)(K / 16) + 8u * (lane & 3);
+    const uint32_t crow = (uint32_t)(lane >> 2) * (uint32_t)(K / 2), srow = (uint32_t)(lane >> 2) * (uint32_t)(K / 16);
     const int pairs = count;
     for (int c0 = 0; c0 < pairs; c0 += 16 * MT) {
         u32x4 cv[2][kSliceChunks], xv[kX];
         u32x2 sv[2];
         f32x4 acc[2][MT] = {};
+        // Loads past a row's end (K >= 128) are moved back inside it, and what they bring is put in its place when it is stored.
         auto load_codes = [&](int s, int c) __attribute__((always_inline)) {
-            const int k0 = kSlice * s + kChunk * c;
+            const uint32_t at = min((uint32_t)(kSlice * s + kChunk * c) / 2 + 16u * (lane & 3), (uint32_t)K / 2 - 16u) + crow;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const uint8_t *at = codes[j] + k0 / 2;
-                if (k0 + kChunk <= K) {
-                    cv[j][c] = *reinterpret_cast<const u32x4_any *>(at + coff);
-                } else {
-                    const int k = k0 + 32 * (lane & 3);
-                    cv[j][c] = u32x4{0u, 0u, 0u, 0u};
-                    if (k + 32 <= K) {
-                        cv[j][c] = *reinterpret_cast<const u32x4_any *>(at + coff);
-                    } else if (k < K) {  // the row's last 16
-                        const u32x2 d = *reinterpret_cast<const u32x2_any *>(at + coff);
-                        cv[j][c] = u32x4{d.x, d.y, 0u, 0u};
-                    }
-                }
-            }
+            for (int j = 0; j < 2; ++j) cv[j][c] = *reinterpret_cast<const u32x4_any *>(codes[j] + at);
         };
         auto load_scales = [&](int s) __attribute__((always_inline)) {
+            const uint32_t at = min((uint32_t)(kSlice / 16 * s) + 8u * (lane & 3), (uint32_t)K / 16 - 8u) + srow;
+#pragma unroll
+            for (int j = 0; j < 2; ++j) sv[j] = *reinterpret_cast<const u32x2_any *>(scales[j] + at);
+        };
+        auto store_codes = [&](int s, int c) __attribute__((always_inline)) {
+            const int k0 = kSlice * s + kChunk * c, k = k0 + 32 * (lane & 3);
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                const uint8_t *at = scales[j] + kSlice / 16 * s;
-                if (kSlice * (s + 1) <= K) {
-                    sv[j] = *reinterpret_cast<const u32x2_any *>(at + soff);
-                } else {
-                    sv[j] = u32x2{0u, 0u};
-                    const int left = (K - kSlice * s) / 16 - 8 * (lane & 3);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e)
-                        if (e < left) sv[j][e >> 2] |= (uint32_t)at[soff + e] << (8 * (e & 3));
+                u32x4 v = cv[j][c];
+                if (k0 + kChunk > K) {
+                    if (k + 32 > K) v = k < K ? u32x4{v.z, v.w, 0u, 0u} : u32x4{0u, 0u, 0u, 0u};
                 }
+                *reinterpret_cast<u32x4 *>(wl + 1024 * j + code_place(lane >> 2, lane & 3)) = v;
             }
         };
-        // Piece e of a slice: token e / 64 of the tiles, k = 8 (e % 64) .. + 7.
-        auto load_x = [&](int s) __attribute__((always_inline)) {
+        auto store_scales = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
-            for (int i = 0; i < kX; ++i) {
-                const int e = tid + kRowThreads * i, r = e >> 6, k = kSlice * s + 8 * (e & 63);
-                xv[i] = u32x4{0u, 0u, 0u, 0u};
-                if (c0 + r < pairs && k < K) {
-                    const int pair = list[c0 + r];
-                    xv[i] = *reinterpret_cast<const u32x4_any *>(x + (int64_t)(SECOND ? pair : pair / p.top_k) * ldx + k);
+            for (int j = 0; j < 2; ++j) {
+                u32x2 v = sv[j];
+                if (kSlice * (s + 1) > K) {
+                    const int past = kSlice / 16 * s + 8 * (lane & 3) - (K / 16 - 8);
+                    const uint64_t w = past >= 8 ? 0u : __builtin_bit_cast(uint64_t, v) >> (8 * max(past, 0));
+                    v = __builtin_bit_cast(u32x2, w);
                 }
+                *reinterpret_cast<u32x2 *>(wl + 2048 + 512 * j + 8 * lane) = v;
             }
+        };
+        // Piece e = tid + 256 i of a slice: token e / 64 of the tiles (a wave has one at a time), k = 8 (e % 64) .. + 7. Tokens
+        // past the last are read as the last: their columns are not stored.
+        const uint16_t *xr[kX];
+#pragma unroll
+        for (int i = 0; i < kX; ++i) {
+            const int pair = __builtin_amdgcn_readfirstlane((int)list[min(c0 + wave + kRowWaves * i, pairs - 1)]);
+            xr[i] = x + (int64_t)(SECOND ? pair : pair / p.top_k) * ldx;
+        }
+        auto load_x = [&](int s) __attribute__((always_inline)) {
+            const uint32_t at = min((uint32_t)(kSlice * s) + 8u * lane, (uint32_t)K - 8u);
+#pragma unroll
+            for (int i = 0; i < kX; ++i) xv[i] = *reinterpret_cast<const u32x4_any *>(xr[i] + at);
         };
         // In LDS: [chunk][token tile][product i][lane] pieces, token r at lane (r ^ f) + 16 g with f of the piece's place in
         // its chunk: the sixteen pieces of a chunk that neighbouring threads write meet no bank twice.
@@ -395,20 +395,21 @@ __global__ __launch_bounds__(kRowThreads, MT == 1 ? 4 : 2) void k_moe_rows(MoeAr
             uint8_t *const xb = lds_x[s & 1];
 #pragma unroll
             for (int i = 0; i < kX; ++i) {
-                const int e = tid + kRowThreads * i, r = e >> 6, q = e & 63;
-                *reinterpret_cast<u32x4 *>(xb + x_place(q >> 4, r >> 4, q & 3, (q >> 2) & 3, r & 15)) = xv[i];
+                const int r = wave + kRowWaves * i;
+                u32x4 v = xv[i];
+                if (kSlice * (s + 1) > K && kSlice * s + 8 * lane >= K) v = u32x4{0u, 0u, 0u, 0u};
+                *reinterpret_cast<u32x4 *>(xb + x_place(lane >> 4, r >> 4, lane & 3, (lane >> 2) & 3, r & 15)) = v;
             }
             lds_barrier();
             const int next = min(s + 1, s_hi - 1);  // (the last slice again: nothing looks at it)
             load_x(next);
-#pragma unroll
-            for (int j = 0; j < 2; ++j) *reinterpret_cast<u32x2 *>(wl + 2048 + 512 * j + 8 * lane) = sv[j];
+            store_scales(s);
             load_scales(next);
 #pragma unroll
             for (int c = 0; c < kSliceChunks; ++c) {
+                __builtin_amdgcn_sched_barrier(0);
                 wave_handover();
-#pragma unroll
-                for (int j = 0; j < 2; ++j) *reinterpret_cast<u32x4 *>(wl + 1024 * j + code_place(lane >> 2, lane & 3)) = cv[j][c];
+                store_codes(s, c);
                 load_codes(next, c);
                 wave_handover();
                 bf16x8 b[MT][4];
@@ -501,8 +502,8 @@ Plan plan_moe(int64_t tokens, int64_t width, int64_t inner, int experts, int top
     Plan plan = {};
     plan.mt = tokens * top_k > 12 * used ? 2 : 1;  // pairs of an expert
     const int64_t up = (inner + (gated ? 63 : 127)) / (gated ? 64 : 128), down = (width + 127) / 128;
-    plan.up_rows = used * up >= 192;
-    plan.down_rows = used * down >= 128;
+    plan.up_rows = width >= kChunk && used * up >= 192;
+    plan.down_rows = inner >= kChunk && used * down >= 128;
     plan.split = 1;
     if (plan.down_rows) {
         const int64_t slices = (inner + kSlice - 1) / kSlice;
@@ -514,18 +515,19 @@ Plan plan_moe(int64_t tokens, int64_t width, int64_t inner, int experts, int top
 template <int NT, bool SECOND>
 void product(const MoeArgs &p, int64_t chosen, bool by_rows, int mt, hipStream_t st) {
     const int64_t F = SECOND ? p.width : p.inner;
+    const size_t list = (size_t)(2 * p.tokens + 255) / 256 * 256;
     if (!by_rows) {
         const int tiles = (int)((F + 15) / 16);
-        hipLaunchKernelGGL((k_moe_product<NT, SECOND>), dim3((unsigned)(chosen * tiles)), dim3(kThreads), 0, st, p, tiles);
+        hipLaunchKernelGGL((k_moe_product<NT, SECOND>), dim3((unsigned)(chosen * tiles)), dim3(kThreads), list, st, p, tiles);
         return;
     }
     constexpr int kCols = NT == 2 ? 16 * kRowWaves : 32 * kRowWaves;
     const int tiles = (int)((F + kCols - 1) / kCols);
     const dim3 grid((unsigned)(chosen * tiles), SECOND ? p.split : 1), block(kRowThreads);
     if (mt == 1)
-        hipLaunchKernelGGL((k_moe_rows<NT, 1, SECOND>), grid, block, 0, st, p, tiles);
+        hipLaunchKernelGGL((k_moe_rows<NT, 1, SECOND>), grid, block, list, st, p, tiles);
     else
-        hipLaunchKernelGGL((k_moe_rows<NT, 2, SECOND>), grid, block, 0, st, p, tiles);
+        hipLaunchKernelGGL((k_moe_rows<NT, 2, SECOND>), grid, block, list, st, p, tiles);
 }
 
 }  // namespace
