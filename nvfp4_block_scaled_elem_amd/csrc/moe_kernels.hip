@@ -18,6 +18,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "act.hpp"
 #include "codec.hpp"
@@ -290,12 +291,13 @@ __global__ __launch_bounds__(kThreads) void k_moe_product(MoeArgs p, int tiles) 
 // Many rows: a wave owns 32 weight rows (gated: 16 gate rows and their 16 up rows) over the whole sum, and a work-group's
 // four waves share the tokens' values, which go through LDS in slices of 512 k in the order of the operand. A wave's codes
 // and scales of a slice are all in flight while the slice before is multiplied: 9 KB a wave, no barrier waits for them.
-// MT: tiles of 16 pairs at a time. SECOND: the product with W2, its sum cut into p.split parts of slices, else with W1.
+// MT: tiles of 16 pairs at a time. SECOND: the product with W2, its sum cut into p.split parts of slices, else with W1. HOLD: X
+// is at most two slices and stays where it is while the work-group goes through several column tiles, without a barrier.
 constexpr int kRowWaves = 4, kRowThreads = 64 * kRowWaves, kSlice = 512, kSliceChunks = kSlice / kChunk;
 constexpr int kWaveCodes = 2 * (1024 + 512);  // LDS bytes of a wave: a chunk's codes and a slice's scales of two tiles
 
-template <int NT, int MT, bool SECOND>
-__global__ __launch_bounds__(kRowThreads, MT == 1 ? 4 : 2) void k_moe_rows(MoeArgs p, int tiles) {
+template <int NT, int MT, bool SECOND, bool HOLD>
+__global__ __launch_bounds__(kRowThreads, MT == 1 ? 3 : 2) void k_moe_rows(MoeArgs p, int tiles, int groups) {
     constexpr int kXBytes = 16 * MT * kSlice * 2, kX = kXBytes / 16 / kRowThreads;  // of a slice; pieces a thread
     constexpr int kCols = NT == 2 ? 16 * kRowWaves : 32 * kRowWaves;
     __shared__ __attribute__((aligned(16))) uint8_t lds_x[2][kXBytes];
@@ -305,10 +307,12 @@ __global__ __launch_bounds__(kRowThreads, MT == 1 ? 4 : 2) void k_moe_rows(MoeAr
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int expert = take_expert<kRowThreads>(p, blockIdx.x / tiles, seen, list, &count);
+    const int expert = take_expert<kRowThreads>(p, blockIdx.x / groups, seen, list, &count);
     if (expert < 0) return;
     const int K = (int)(SECOND ? p.inner : p.width), F = (int)(SECOND ? p.width : p.inner);
-    const int f0 = (int)(blockIdx.x % tiles) * kCols + (NT == 2 ? 16 : 32) * wave;
+    // The work-group's column tiles: first, first + groups, ...
+    const int first = (int)(blockIdx.x % groups), turns = HOLD ? (tiles - first + groups - 1) / groups : 1;
+    auto column = [&](int turn) __attribute__((always_inline)) { return (first + turn * groups) * kCols + (NT == 2 ? 16 : 32) * wave; };
     const int slices = (K + kSlice - 1) / kSlice;
     const int s_lo = SECOND ? (int)((int64_t)slices * blockIdx.y / gridDim.y) : 0;
     const int s_hi = SECOND ? (int)((int64_t)slices * (blockIdx.y + 1) / gridDim.y) : slices;
@@ -317,14 +321,17 @@ __global__ __launch_bounds__(kRowThreads, MT == 1 ? 4 : 2) void k_moe_rows(MoeAr
     const uint16_t *x = SECOND ? p.h : static_cast<const uint16_t *>(p.x);
     const int64_t ldx = SECOND ? p.inner : p.ldx;
     uint8_t *const wl = lds_w[wave];
-    // Rows of the two tiles; a tile past the last is read as the last.
+    // Rows of the two tiles that are being loaded; a tile past the last is read as the last.
     const uint8_t *codes[2], *scales[2];
+    auto take_rows = [&](int turn) __attribute__((always_inline)) {
+        const int f0 = column(turn);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-        const int64_t row = (int64_t)expert * NT * F + (NT == 2 ? min(f0, F - 16) + j * F : min(f0 + 16 * j, F - 16));
-        codes[j] = W.codes + row * (K / 2);
-        scales[j] = W.scales + row * (K / 16);
-    }
+        for (int j = 0; j < 2; ++j) {
+            const int64_t row = (int64_t)expert * NT * F + (NT == 2 ? min(f0, F - 16) + j * F : min(f0 + 16 * j, F - 16));
+            codes[j] = W.codes + row * (K / 2);
+            scales[j] = W.scales + row * (K / 16);
+        }
+    };
     // codes: the lane loads row lane / 4, 16 bytes lane % 4 of a chunk; scales: row lane / 4, the 8 of chunk lane % 4
     const uint32_t crow = (uint32_t)(lane >> 2) * (uint32_t)(K / 2), srow = (uint32_t)(lane >> 2) * (uint32_t)(K / 16);
     const int pairs = count;
@@ -384,15 +391,7 @@ __global__ __launch_bounds__(kRowThreads, MT == 1 ? 4 : 2) void k_moe_rows(MoeAr
         auto x_place = [&](int c, int m, int i, int gg, int r) __attribute__((always_inline)) {
             return (((c * MT + m) * 4 + i) * 64 + 16 * gg + (r ^ (4 * gg + i))) * 16;
         };
-        if (s_lo < s_hi) {
-            load_x(s_lo);
-            load_scales(s_lo);
-#pragma unroll
-            for (int c = 0; c < kSliceChunks; ++c) load_codes(s_lo, c);
-        }
-#pragma unroll 1
-        for (int s = s_lo; s < s_hi; ++s) {
-            uint8_t *const xb = lds_x[s & 1];
+        auto store_x = [&](int s, uint8_t *xb) __attribute__((always_inline)) {
 #pragma unroll
             for (int i = 0; i < kX; ++i) {
                 const int r = wave + kRowWaves * i;
@@ -400,9 +399,9 @@ __global__ __launch_bounds__(kRowThreads, MT == 1 ? 4 : 2) void k_moe_rows(MoeAr
                 if (kSlice * (s + 1) > K && kSlice * s + 8 * lane >= K) v = u32x4{0u, 0u, 0u, 0u};
                 *reinterpret_cast<u32x4 *>(xb + x_place(lane >> 4, r >> 4, lane & 3, (lane >> 2) & 3, r & 15)) = v;
             }
-            lds_barrier();
-            const int next = min(s + 1, s_hi - 1);  // (the last slice again: nothing looks at it)
-            load_x(next);
+        };
+        // Slice s of the loaded codes with the X at xb, and the loads of slice `next` (of the rows taken last).
+        auto multiply = [&](int s, int next, const uint8_t *xb) __attribute__((always_inline)) {
             store_scales(s);
             load_scales(next);
 #pragma unroll
@@ -431,32 +430,72 @@ __global__ __launch_bounds__(kRowThreads, MT == 1 ? 4 : 2) void k_moe_rows(MoeAr
                     }
                 }
             }
-        }
-        // Element r of the lane is weight row 4 g + r of a tile, pair r16 of a tile of pairs.
+        };
+        auto finish = [&](int turn) __attribute__((always_inline)) {
+            const int f0 = column(turn);
+            // Element r of the lane is weight row 4 g + r of a tile, pair r16 of a tile of pairs.
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-            if (c0 + 16 * m + r16 >= pairs) continue;
-            const int64_t pair = list[c0 + 16 * m + r16];
-            if (SECOND) {
-                const float w = p.weights[pair];
-                float *z = p.z + ((int64_t)blockIdx.y * p.tokens * p.top_k + pair) * F + f0 + 4 * g;
+            for (int m = 0; m < MT; ++m) {
+                if (c0 + 16 * m + r16 >= pairs) continue;
+                const int64_t pair = list[c0 + 16 * m + r16];
+                if (SECOND) {
+                    const float w = p.weights[pair];
+                    float *z = p.z + ((int64_t)blockIdx.y * p.tokens * p.top_k + pair) * F + f0 + 4 * g;
 #pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    if (f0 + 16 * j < F) *reinterpret_cast<f32x4 *>(z + 16 * j) = (acc[j][m] * alpha) * w;
-            } else {
-                uint16_t *h = p.h + pair * F + f0 + 4 * g;
+                    for (int j = 0; j < 2; ++j)
+                        if (f0 + 16 * j < F) *reinterpret_cast<f32x4 *>(z + 16 * j) = (acc[j][m] * alpha) * w;
+                } else {
+                    uint16_t *h = p.h + pair * F + f0 + 4 * g;
 #pragma unroll
-                for (int j = 0; j < (NT == 2 ? 1 : 2); ++j) {
-                    if (f0 + 16 * j >= F) continue;
-                    float v[4];
+                    for (int j = 0; j < (NT == 2 ? 1 : 2); ++j) {
+                        if (f0 + 16 * j >= F) continue;
+                        float v[4];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        v[r] = act_value(alpha * acc[j][m][r], p.act);
-                        if (NT == 2) v[r] *= alpha * acc[1][m][r];
+                        for (int r = 0; r < 4; ++r) {
+                            v[r] = act_value(alpha * acc[j][m][r], p.act);
+                            if (NT == 2) v[r] *= alpha * acc[1][m][r];
+                        }
+                        *reinterpret_cast<uint2 *>(h + 16 * j) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
                     }
-                    *reinterpret_cast<uint2 *>(h + 16 * j) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
                 }
             }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int m = 0; m < MT; ++m) acc[j][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        };
+        take_rows(0);
+        load_x(s_lo);
+        load_scales(s_lo);
+#pragma unroll
+        for (int c = 0; c < kSliceChunks; ++c) load_codes(s_lo, c);
+        if (HOLD) {
+            store_x(s_lo, lds_x[0]);
+            if (s_hi - s_lo > 1) {
+                load_x(s_lo + 1);
+                store_x(s_lo + 1, lds_x[1]);
+            }
+            lds_barrier();
+#pragma unroll 1
+            for (int turn = 0; turn < turns; ++turn) {
+#pragma unroll 1
+                for (int s = s_lo; s < s_hi; ++s) {
+                    const bool last = s + 1 == s_hi;
+                    if (last) take_rows(min(turn + 1, turns - 1));  // (after the last tile itself again: nothing looks at it)
+                    multiply(s, last ? s_lo : s + 1, lds_x[s - s_lo]);
+                }
+                finish(turn);
+            }
+        } else {
+#pragma unroll 1
+            for (int s = s_lo; s < s_hi; ++s) {
+                store_x(s, lds_x[s & 1]);
+                lds_barrier();
+                const int next = min(s + 1, s_hi - 1);
+                load_x(next);
+                multiply(s, next, lds_x[s & 1]);
+            }
+            finish(0);
         }
         lds_barrier();  // the last slices have been read
     }
@@ -492,6 +531,7 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 // Which kernels a call takes, and how many parts the second product's sum is cut into.
 struct Plan {
     int up_rows, down_rows, mt, split;
+    int up_turns, down_turns;  // column tiles of a work-group
 };
 
 Plan plan_moe(int64_t tokens, int64_t width, int64_t inner, int experts, int top_k, bool gated) {
@@ -509,11 +549,14 @@ Plan plan_moe(int64_t tokens, int64_t width, int64_t inner, int experts, int top
         const int64_t slices = (inner + kSlice - 1) / kSlice;
         while (plan.split < 8 && 4 * plan.split <= slices && used * down * plan.split < 768) plan.split *= 2;
     }
+    // Three work-groups a CU, where X stays.
+    plan.up_turns = width <= 2 * kSlice ? (int)std::max(1.0, used * up / 768.0 + 0.5) : 1;
+    plan.down_turns = inner <= 2 * kSlice ? (int)std::max(1.0, used * down / 768.0 + 0.5) : 1;
     return plan;
 }
 
 template <int NT, bool SECOND>
-void product(const MoeArgs &p, int64_t chosen, bool by_rows, int mt, hipStream_t st) {
+void product(const MoeArgs &p, int64_t chosen, bool by_rows, int mt, int turns, hipStream_t st) {
     const int64_t F = SECOND ? p.width : p.inner;
     const size_t list = (size_t)(2 * p.tokens + 255) / 256 * 256;
     if (!by_rows) {
@@ -522,12 +565,17 @@ void product(const MoeArgs &p, int64_t chosen, bool by_rows, int mt, hipStream_t
         return;
     }
     constexpr int kCols = NT == 2 ? 16 * kRowWaves : 32 * kRowWaves;
-    const int tiles = (int)((F + kCols - 1) / kCols);
-    const dim3 grid((unsigned)(chosen * tiles), SECOND ? p.split : 1), block(kRowThreads);
-    if (mt == 1)
-        hipLaunchKernelGGL((k_moe_rows<NT, 1, SECOND>), grid, block, list, st, p, tiles);
+    const int tiles = (int)((F + kCols - 1) / kCols), groups = (tiles + turns - 1) / turns;
+    const dim3 grid((unsigned)(chosen * groups), SECOND ? p.split : 1), block(kRowThreads);
+    auto run = [&](auto mts, auto hold) {
+        hipLaunchKernelGGL((k_moe_rows<NT, mts.value, SECOND, hold.value>), grid, block, list, st, p, tiles, groups);
+    };
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
+    if (turns > 1)
+        mt == 1 ? run(One{}, std::true_type{}) : run(Two{}, std::true_type{});
     else
-        hipLaunchKernelGGL((k_moe_rows<NT, 2, SECOND>), grid, block, list, st, p, tiles);
+        mt == 1 ? run(One{}, std::false_type{}) : run(Two{}, std::false_type{});
 }
 
 }  // namespace
@@ -553,11 +601,11 @@ hipError_t launch_moe(const MoeArgs &a, void *ws, hipStream_t st) {
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const int64_t chosen = std::min<int64_t>(p.experts, (int64_t)pairs);
     if (p.gated)
-        product<2, false>(p, chosen, plan.up_rows, plan.mt, st);
+        product<2, false>(p, chosen, plan.up_rows, plan.mt, plan.up_turns, st);
     else
-        product<1, false>(p, chosen, plan.up_rows, plan.mt, st);
+        product<1, false>(p, chosen, plan.up_rows, plan.mt, plan.up_turns, st);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    product<1, true>(p, chosen, plan.down_rows, plan.mt, st);
+    product<1, true>(p, chosen, plan.down_rows, plan.mt, plan.down_turns, st);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const int per = (int)(p.width / 8);
     hipLaunchKernelGGL(k_moe_sum, dim3((unsigned)((p.tokens * per + 255) / 256)), dim3(256), 0, st, p, per);
