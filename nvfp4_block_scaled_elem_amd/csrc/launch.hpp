@@ -262,7 +262,7 @@ struct MoeArgs {
     // the products, its part of y
     int *ids;
     float *weights;
-    uint16_t *h;
+    uint16_t *h, *h_low;  // h_low: null, or what h's rounding left
     float *z;
     int split;  // parts of z
 };

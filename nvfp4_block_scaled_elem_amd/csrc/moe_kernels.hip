@@ -46,26 +46,41 @@ __device__ __forceinline__ uint32_t order_key(float l) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
+// Reductions over a wave within its rows of 16 lanes and across them (row_shr 1, 2, 4, 8, row_bcast 15, 31; a lane without a
+// source keeps `old`); lane 63 has the result.
+template <int CTRL>
+__device__ __forceinline__ uint32_t moved(uint32_t old, uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)v, CTRL, 0xF, 0xF, false);
+}
 __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v = max(v, (uint32_t)__shfl_xor((int)v, m));
-    return v;
+    v = max(v, moved<0x111>(v, v));
+    v = max(v, moved<0x112>(v, v));
+    v = max(v, moved<0x114>(v, v));
+    v = max(v, moved<0x118>(v, v));
+    v = max(v, moved<0x142>(v, v));
+    v = max(v, moved<0x143>(v, v));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 __device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int m = 1; m < 64; m <<= 1) v += __shfl_xor(v, m);
-    return v;
+    auto add = [&](uint32_t u) { v += __uint_as_float(u); };
+    add(moved<0x111>(0u, __float_as_uint(v)));
+    add(moved<0x112>(0u, __float_as_uint(v)));
+    add(moved<0x114>(0u, __float_as_uint(v)));
+    add(moved<0x118>(0u, __float_as_uint(v)));
+    add(moved<0x142>(0u, __float_as_uint(v)));
+    add(moved<0x143>(0u, __float_as_uint(v)));
+    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
 }
 
 // The experts of token t, by one wave: lane j < top_k gets choice j (-1: none) and its weight. Lane l holds the logits
-// l, l + 64, ...
-__device__ __forceinline__ void route(const MoeArgs &p, int64_t t, int &id, float &w) {
-    constexpr int kMost = kMoeMaxExperts / 64;
+// l, l + 64, ... (R of them)
+template <int R>
+__device__ __forceinline__ void route_of(const MoeArgs &p, int64_t t, int &id, float &w) {
     const int lane = threadIdx.x & 63;
-    float l[kMost];
-    uint32_t key[kMost];
+    float l[R];
+    uint32_t key[R];
 #pragma unroll
-    for (int r = 0; r < kMost; ++r) {
+    for (int r = 0; r < R; ++r) {
         const int e = lane + 64 * r;
         l[r] = -__builtin_inff();
         if (e < p.experts)
@@ -77,12 +92,12 @@ __device__ __forceinline__ void route(const MoeArgs &p, int64_t t, int &id, floa
     if (!p.sigmoid) {
         uint32_t k = 0u;
 #pragma unroll
-        for (int r = 0; r < kMost; ++r) k = max(k, key[r]);
+        for (int r = 0; r < R; ++r) k = max(k, key[r]);
         k = wave_max(k);
         top = k == 0xFFFFFFFFu ? __builtin_nanf("") : __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
         if (!p.normalize) {
 #pragma unroll
-            for (int r = 0; r < kMost; ++r) all += key[r] ? __builtin_amdgcn_exp2f((l[r] - top) * kLog2e) : 0.0f;
+            for (int r = 0; r < R; ++r) all += key[r] ? __builtin_amdgcn_exp2f((l[r] - top) * kLog2e) : 0.0f;
             all = wave_sum(all);
         }
     }
@@ -91,12 +106,12 @@ __device__ __forceinline__ void route(const MoeArgs &p, int64_t t, int &id, floa
     for (int j = 0; j < p.top_k; ++j) {
         uint32_t k = 0u;
 #pragma unroll
-        for (int r = 0; r < kMost; ++r) k = max(k, key[r]);
+        for (int r = 0; r < R; ++r) k = max(k, key[r]);
         k = wave_max(k);
         if (k == 0u) break;
         bool found = false;
 #pragma unroll
-        for (int r = 0; r < kMost; ++r) {  // the lowest index: e = lane + 64 r
+        for (int r = 0; r < R; ++r) {  // the lowest index: e = lane + 64 r
             const uint64_t who = __ballot(key[r] == k);
             if (!found && who) {
                 found = true;
@@ -115,16 +130,26 @@ __device__ __forceinline__ void route(const MoeArgs &p, int64_t t, int &id, floa
     } else {
         float m = 0.0f;
         if (p.normalize) {
-            m = id >= 0 ? fminf(mine, 0.0f) : -__builtin_inff();
-#pragma unroll
-            for (int k = 1; k < 64; k <<= 1) m = fmaxf(m, __shfl_xor(m, k));
-            if (m == -__builtin_inff()) m = 0.0f;
+            // the largest of numbers up to 0: the least of their patterns without the sign (of no number: 0x7F800000)
+            const uint32_t low = wave_max(id >= 0 ? 0x7F800000u - (__float_as_uint(fminf(mine, 0.0f)) & 0x7FFFFFFFu) : 0u);
+            m = low == 0u ? 0.0f : -__uint_as_float(0x7F800000u - low);
         }
         const float low = mine < 0.0f ? mine : 0.0f;
         e = id >= 0 ? __builtin_amdgcn_exp2f((low - m) * kLog2e) / (1.0f + __builtin_amdgcn_exp2f(-fabsf(mine) * kLog2e)) : 0.0f;
     }
     if (p.normalize) all = wave_sum(e);
     w = p.normalize || !p.sigmoid ? e / all : e;
+}
+
+__device__ __forceinline__ void route(const MoeArgs &p, int64_t t, int &id, float &w) {
+    if (p.experts <= 64)
+        route_of<1>(p, t, id, w);
+    else if (p.experts <= 128)
+        route_of<2>(p, t, id, w);
+    else if (p.experts <= 256)
+        route_of<4>(p, t, id, w);
+    else
+        route_of<kMoeMaxExperts / 64>(p, t, id, w);
 }
 
 __global__ __launch_bounds__(256) void k_moe_route(MoeArgs p) {
@@ -141,19 +166,24 @@ __global__ __launch_bounds__(256) void k_moe_route(MoeArgs p) {
 
 constexpr int kChunk = 128, kChunkLds = 16 * 64 + 16 * 8;  // k per chunk; LDS bytes of 16 rows' codes and scales
 
+// What rounding v to `hi` left; nothing of an infinity.
+__device__ __forceinline__ float rest_of(float v, float hi) {
+    return fabsf(hi) == __builtin_inff() ? 0.0f : v - hi;
+}
+
 // 16-byte piece q (0..3) of row r of a chunk's codes in LDS: the 16 lanes that read one q of 16 rows meet no bank twice.
 __device__ __forceinline__ int code_place(int r, int q) { return r * 64 + ((q ^ ((r >> 2) & 3)) << 4); }
 
 // The chosen experts in order: the number `nth` of them (-1: there are not so many), and its pairs into `list`. By the whole
 // work-group; `seen` has a byte per expert.
 template <int THREADS>
-__device__ __forceinline__ int take_expert(const MoeArgs &p, int nth, uint8_t *seen, uint16_t *list, int *count) {
+__device__ __forceinline__ int take_expert(const MoeArgs &p, const int *ids, int nth, uint8_t *seen, uint16_t *list, int *count) {
     const int tid = threadIdx.x, lane = tid & 63, pairs = (int)p.tokens * p.top_k;
     for (int e = tid; e < p.experts; e += THREADS) seen[e] = 0;
     if (tid == 0) *count = 0;
     __syncthreads();
     for (int i = tid; i < pairs; i += THREADS) {
-        const int e = p.ids[i];
+        const int e = ids[i];
         if (e >= 0) seen[e] = 1;
     }
     __syncthreads();
@@ -170,22 +200,36 @@ __device__ __forceinline__ int take_expert(const MoeArgs &p, int nth, uint8_t *s
     if (mine < 0) return -1;
     // The pairs' order in the list decides their column alone, which no result depends on.
     for (int i = tid; i < pairs; i += THREADS)
-        if (p.ids[i] == mine) list[atomicAdd(count, 1)] = (uint16_t)i;
+        if (ids[i] == mine) list[atomicAdd(count, 1)] = (uint16_t)i;
     __syncthreads();
     return mine;
 }
 
-// NT: 2 if gated. SECOND: the product with W2, else with W1.
-template <int NT, bool SECOND>
+// NT: 2 if gated. SECOND: the product with W2, else with W1. ROUTE: to eight tokens, whose experts every work-group finds by
+// itself, a wave a token (a launch saved); the first one writes them down.
+template <int NT, bool SECOND, bool ROUTE>
 __global__ __launch_bounds__(kThreads) void k_moe_product(MoeArgs p, int tiles) {
     constexpr int kStage = kWaves * NT * kChunkLds, kSums = kWaves * NT * 1024;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kStage > kSums ? kStage : kSums];
     __shared__ uint8_t seen[kMoeMaxExperts];
     extern __shared__ uint16_t list[];  // an expert's pairs: as many as tokens at most
     __shared__ int count;
+    __shared__ int route_ids[ROUTE ? kWaves * kMoeMaxTopK : 1];
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int expert = take_expert<kThreads>(p, blockIdx.x / tiles, seen, list, &count);
+    if (ROUTE) {
+        if (wave < p.tokens) {
+            int id;
+            float w;
+            route(p, wave, id, w);
+            if (lane < p.top_k) {
+                route_ids[wave * p.top_k + lane] = id;
+                if (blockIdx.x == 0) p.ids[wave * p.top_k + lane] = id, p.weights[wave * p.top_k + lane] = w;
+            }
+        }
+        __syncthreads();
+    }
+    const int expert = take_expert<kThreads>(p, ROUTE ? route_ids : p.ids, blockIdx.x / tiles, seen, list, &count);
     if (expert < 0) return;
     const int64_t K = SECOND ? p.inner : p.width, F = SECOND ? p.width : p.inner;
     const int64_t f0 = (int64_t)(blockIdx.x % tiles) * 16, nch = (K + kChunk - 1) / kChunk;
@@ -280,11 +324,146 @@ __global__ __launch_bounds__(kThreads) void k_moe_product(MoeArgs p, int tiles) 
                 } else {
                     float a = act_value(alpha * z[0], p.act);
                     if (NT == 2) a *= alpha * z[NT - 1];
-                    p.h[q * F + f] = to_bf16(a);
+                    const uint16_t hi = to_bf16(a);
+                    p.h[q * F + f] = hi;
+                    if (p.h_low) p.h_low[q * F + f] = to_bf16(rest_of(a, __uint_as_float((uint32_t)hi << 16)));
                 }
             }
         }
         __syncthreads();
+    }
+}
+
+// The second product and the sum over a token's experts together, to 16 tokens: column t of an operand is token t (zeros
+// where it did not choose the expert), so that the tokens' sums stay in place from expert to expert. A work-group has 16 rows of y;
+// its sixteen waves share the list (chosen expert, chunk of 128 k) in equal runs and are joined in wave order. h comes in
+// two bf16 parts, its rounding and what that leaves (2^-17 of h together): the matrix cores are idle anyway.
+constexpr int kDownWaves = 16, kDownThreads = 64 * kDownWaves, kDownTokens = 16;
+
+__global__ __launch_bounds__(kDownThreads) void k_moe_down(MoeArgs p) {
+    constexpr int kStage = kDownWaves * kChunkLds, kSums = kDownWaves * 1024;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kStage > kSums ? kStage : kSums];
+    __shared__ uint8_t seen[kMoeMaxExperts];
+    __shared__ uint16_t chosen[kMoeMaxExperts];            // the experts in order
+    __shared__ uint8_t choice[kMoeMaxExperts][kDownTokens];  // of expert e by token t: 1 + j, 0 if not
+    __shared__ int number;
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int pairs = (int)p.tokens * p.top_k;
+    const int64_t K = p.inner, F = p.width;
+    for (int e = tid; e < p.experts; e += kDownThreads) {
+        seen[e] = 0;
+        *reinterpret_cast<u32x4 *>(choice[e]) = u32x4{0u, 0u, 0u, 0u};
+    }
+    __syncthreads();
+    for (int i = tid; i < pairs; i += kDownThreads) {
+        const int e = p.ids[i];
+        if (e >= 0) seen[e] = 1, choice[e][i / p.top_k] = (uint8_t)(1 + i % p.top_k);
+    }
+    __syncthreads();
+    if (wave == 0) {
+        int before = 0;
+        for (int e0 = 0; e0 < p.experts; e0 += 64) {
+            const bool in = e0 + lane < p.experts && seen[e0 + lane];
+            const uint64_t who = __ballot(in);
+            if (in) chosen[before + __popcll(who & (((uint64_t)1 << lane) - 1))] = (uint16_t)(e0 + lane);
+            before += __popcll(who);
+        }
+        if (lane == 0) number = before;
+    }
+    __syncthreads();
+    const int nch = (int)((K + kChunk - 1) / kChunk), items = number * nch;
+    const int lo = (int)((int64_t)items * wave / kDownWaves), hi = (int)((int64_t)items * (wave + 1) / kDownWaves);
+    const int64_t f0 = (int64_t)blockIdx.x * 16;
+    uint8_t *const wl = lds + wave * kChunkLds;
+    struct Item {
+        u32x4 c, h[4], l[4];
+        u32x2 s;
+        float w;
+    };
+    auto load = [&](Item &it, int i) __attribute__((always_inline)) {
+        const int e = __builtin_amdgcn_readfirstlane((int)chosen[i / nch]), ch = i % nch;
+        const int64_t row = (int64_t)e * F + f0;
+        const int kc = kChunk * ch + 32 * (lane & 3), ks = kChunk * ch;
+        const uint8_t *c = p.down.codes + ((row + (lane >> 2)) * K + kc) / 2, *s = p.down.scales + ((row + r16) * K + ks) / 16;
+        it.c = u32x4{0u, 0u, 0u, 0u};
+        it.s = u32x2{0u, 0u};
+        if (kc + 32 <= K) {
+            it.c = *reinterpret_cast<const u32x4_any *>(c);
+        } else if (kc < K) {  // the row's last 16
+            const u32x2 d = *reinterpret_cast<const u32x2_any *>(c);
+            it.c = u32x4{d.x, d.y, 0u, 0u};
+        }
+        if (lane < 16) {
+            if (ks + kChunk <= K) {
+                it.s = *reinterpret_cast<const u32x2_any *>(s);
+            } else {
+#pragma unroll
+                for (int b = 0; b < 8; ++b)
+                    if (ks + 16 * b < K) it.s[b >> 2] |= (uint32_t)s[b] << (8 * (b & 3));
+            }
+        }
+        const int j = choice[e][r16];
+        it.w = 0.0f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) it.h[k] = it.l[k] = u32x4{0u, 0u, 0u, 0u};
+        if (j) {
+            const int64_t pair = r16 * p.top_k + j - 1;
+            it.w = p.weights[pair] * p.down.alpha[e];
+            const int64_t at = pair * K + kChunk * ch + 32 * g;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (kChunk * ch + 32 * g + 8 * k < K) {
+                    it.h[k] = *reinterpret_cast<const u32x4 *>(p.h + at + 8 * k);
+                    it.l[k] = *reinterpret_cast<const u32x4 *>(p.h_low + at + 8 * k);
+                }
+        }
+    };
+    f32x4 total = {0.0f, 0.0f, 0.0f, 0.0f};
+    auto multiply = [&](const Item &it) __attribute__((always_inline)) {
+        wave_handover();
+        *reinterpret_cast<u32x4 *>(wl + code_place(lane >> 2, lane & 3)) = it.c;
+        if (lane < 16) *reinterpret_cast<u32x2 *>(wl + 1024 + 8 * lane) = it.s;
+        wave_handover();
+        const u32x4 cur = *reinterpret_cast<const u32x4 *>(wl + code_place(r16, g));
+        const uint32_t sb = *reinterpret_cast<const u16_lds *>(wl + 1024 + 8 * r16 + 2 * g);
+        const f32x2 d = __builtin_amdgcn_cvt_pk_f32_fp8((int)(sb & 0x7F7Fu), false);  // both scales
+        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const bf16x8 w = __builtin_bit_cast(bf16x8, dequant8(cur[k], k < 2 ? d.x : d.y));
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, it.h[k]), acc, 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, it.l[k]), acc, 0, 0, 0);
+        }
+        // a token that did not choose the expert has zeros: its NaN or infinite weights of others stay out
+#pragma unroll
+        for (int k = 0; k < 4; ++k) total[k] = __builtin_fmaf(acc[k], it.w, total[k]);
+    };
+    Item a, b;
+    int i = lo;
+    if (i < hi) load(a, i);
+#pragma unroll 1
+    for (; i < hi; i += 2) {
+        if (i + 1 < hi) load(b, i + 1);
+        multiply(a);
+        if (i + 1 >= hi) break;
+        if (i + 2 < hi) load(a, i + 2);
+        multiply(b);
+    }
+    __syncthreads();  // the sums take the place of the codes
+    float *const red = reinterpret_cast<float *>(lds);
+    *reinterpret_cast<f32x4 *>(&red[wave * 256 + lane * 4]) = total;
+    __syncthreads();
+    if (tid < 256) {
+        // Element r of lane l is row 4 (l / 16) + r, token l % 16.
+        const int l = tid >> 2, t = l & 15;
+        const int64_t f = f0 + 4 * (l >> 4) + (tid & 3);
+        if (t < p.tokens) {
+            float y = p.res ? __uint_as_float((uint32_t)p.res[t * p.ldr + f] << 16) : 0.0f;
+#pragma unroll
+            for (int w = 0; w < kDownWaves; ++w) y += red[w * 256 + tid];
+            p.y[t * F + f] = to_bf16(y);
+        }
     }
 }
 
@@ -307,7 +486,7 @@ __global__ __launch_bounds__(kRowThreads, MT == 1 ? 3 : 2) void k_moe_rows(MoeAr
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int expert = take_expert<kRowThreads>(p, blockIdx.x / groups, seen, list, &count);
+    const int expert = take_expert<kRowThreads>(p, p.ids, blockIdx.x / groups, seen, list, &count);
     if (expert < 0) return;
     const int K = (int)(SECOND ? p.inner : p.width), F = (int)(SECOND ? p.width : p.inner);
     // The work-group's column tiles: first, first + groups, ...
@@ -455,7 +634,12 @@ __global__ __launch_bounds__(kRowThreads, MT == 1 ? 3 : 2) void k_moe_rows(MoeAr
                             v[r] = act_value(alpha * acc[j][m][r], p.act);
                             if (NT == 2) v[r] *= alpha * acc[1][m][r];
                         }
-                        *reinterpret_cast<uint2 *>(h + 16 * j) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+                        const uint2 hi = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+                        *reinterpret_cast<uint2 *>(h + 16 * j) = hi;
+                        if (p.h_low)
+                            *reinterpret_cast<uint2 *>(p.h_low + pair * F + f0 + 4 * g + 16 * j) =
+                                make_uint2(pack_bf16(rest_of(v[0], bf16_lo(hi.x)), rest_of(v[1], bf16_hi(hi.x))),
+                                           pack_bf16(rest_of(v[2], bf16_lo(hi.y)), rest_of(v[3], bf16_hi(hi.y))));
                     }
                 }
             }
@@ -511,16 +695,15 @@ __global__ __launch_bounds__(256) void k_moe_sum(MoeArgs p, int per) {
         r.load(p.res + t * p.ldr + c, 8);
         r.get(v);
     }
-    for (int j = 0; j < p.top_k; ++j) {
-        const int64_t q = t * p.top_k + j;
-        if (p.ids[q] < 0) break;
-        for (int part = 0; part < p.split; ++part) {
-            float z[8];
-            Raw8<float> r;
-            r.load(p.z + ((int64_t)part * p.tokens * p.top_k + q) * p.width + c, 8);
-            r.get(z);
+    for (int part = 0; part < p.split; ++part) {
+        const float *z = p.z + ((int64_t)part * p.tokens + t) * p.top_k * p.width + c;
+#pragma unroll 4
+        for (int j = 0; j < p.top_k; ++j) {  // (a choice that is none: what lies there is not taken)
+            const f32x4 a = *reinterpret_cast<const f32x4 *>(z + (int64_t)j * p.width);
+            const f32x4 b = *reinterpret_cast<const f32x4 *>(z + (int64_t)j * p.width + 4);
+            const bool taken = p.ids[t * p.top_k + j] >= 0;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] += z[k];
+            for (int k = 0; k < 4; ++k) v[k] += taken ? a[k] : 0.0f, v[4 + k] += taken ? b[k] : 0.0f;
         }
     }
     put8(p.y + t * p.width + c, v, 8);
@@ -530,7 +713,7 @@ size_t round256(size_t n) { return (n + 255) / 256 * 256; }
 
 // Which kernels a call takes, and how many parts the second product's sum is cut into.
 struct Plan {
-    int up_rows, down_rows, mt, split;
+    int route, up_rows, down_rows, down_sum, mt, split;  // route: a kernel of its own; down_sum: the second product with the sum
     int up_turns, down_turns;  // column tiles of a work-group
 };
 
@@ -543,7 +726,9 @@ Plan plan_moe(int64_t tokens, int64_t width, int64_t inner, int experts, int top
     plan.mt = tokens * top_k > 12 * used ? 2 : 1;  // pairs of an expert
     const int64_t up = (inner + (gated ? 63 : 127)) / (gated ? 64 : 128), down = (width + 127) / 128;
     plan.up_rows = width >= kChunk && used * up >= 192;
-    plan.down_rows = inner >= kChunk && used * down >= 128;
+    plan.down_rows = inner >= kChunk && used * down >= (tokens <= kDownTokens ? 512 : 128);
+    plan.route = tokens > kWaves || plan.up_rows;
+    plan.down_sum = tokens <= kDownTokens && !plan.down_rows;
     plan.split = 1;
     if (plan.down_rows) {
         const int64_t slices = (inner + kSlice - 1) / kSlice;
@@ -556,12 +741,18 @@ Plan plan_moe(int64_t tokens, int64_t width, int64_t inner, int experts, int top
 }
 
 template <int NT, bool SECOND>
-void product(const MoeArgs &p, int64_t chosen, bool by_rows, int mt, int turns, hipStream_t st) {
+void product(const MoeArgs &p, int64_t chosen, bool by_rows, bool apart, int mt, int turns, hipStream_t st) {
     const int64_t F = SECOND ? p.width : p.inner;
     const size_t list = (size_t)(2 * p.tokens + 255) / 256 * 256;
     if (!by_rows) {
         const int tiles = (int)((F + 15) / 16);
-        hipLaunchKernelGGL((k_moe_product<NT, SECOND>), dim3((unsigned)(chosen * tiles)), dim3(kThreads), list, st, p, tiles);
+        const dim3 grid((unsigned)(chosen * tiles));
+        if constexpr (!SECOND)
+            if (!apart) {
+                hipLaunchKernelGGL((k_moe_product<NT, false, true>), grid, dim3(kThreads), list, st, p, tiles);
+                return;
+            }
+        hipLaunchKernelGGL((k_moe_product<NT, SECOND, false>), grid, dim3(kThreads), list, st, p, tiles);
         return;
     }
     constexpr int kCols = NT == 2 ? 16 * kRowWaves : 32 * kRowWaves;
@@ -580,32 +771,39 @@ void product(const MoeArgs &p, int64_t chosen, bool by_rows, int mt, int turns, 
 
 }  // namespace
 
-// ids, weights, h, z
+// ids, weights, h, then its second part, or z
 size_t moe_workspace(int64_t tokens, int64_t width, int64_t inner, int experts, int top_k) {
     const size_t pairs = (size_t)(tokens * top_k);
     const size_t split = std::max(plan_moe(tokens, width, inner, experts, top_k, false).split, plan_moe(tokens, width, inner, experts, top_k, true).split);
-    return 2 * round256(4 * pairs) + round256(2 * pairs * inner) + round256(4 * split * pairs * width);
+    return 2 * round256(4 * pairs) + round256(2 * pairs * inner) + std::max(round256(4 * split * pairs * width), round256(2 * pairs * inner));
 }
 
 hipError_t launch_moe(const MoeArgs &a, void *ws, hipStream_t st) {
     MoeArgs p = a;
     const size_t pairs = (size_t)(p.tokens * p.top_k);
+    const Plan plan = plan_moe(p.tokens, p.width, p.inner, p.experts, p.top_k, p.gated);
     uint8_t *at = static_cast<uint8_t *>(ws);
     p.ids = reinterpret_cast<int *>(at), at += round256(4 * pairs);
     p.weights = reinterpret_cast<float *>(at), at += round256(4 * pairs);
     p.h = reinterpret_cast<uint16_t *>(at), at += round256(2 * pairs * p.inner);
     p.z = reinterpret_cast<float *>(at);
-    const Plan plan = plan_moe(p.tokens, p.width, p.inner, p.experts, p.top_k, p.gated);
+    p.h_low = plan.down_sum ? reinterpret_cast<uint16_t *>(at) : nullptr;
     p.split = plan.split;
-    hipLaunchKernelGGL(k_moe_route, dim3((unsigned)((p.tokens + 3) / 4)), dim3(256), 0, st, p);
-    if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    if (plan.route) {
+        hipLaunchKernelGGL(k_moe_route, dim3((unsigned)((p.tokens + 3) / 4)), dim3(256), 0, st, p);
+        if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+    }
     const int64_t chosen = std::min<int64_t>(p.experts, (int64_t)pairs);
     if (p.gated)
-        product<2, false>(p, chosen, plan.up_rows, plan.mt, plan.up_turns, st);
+        product<2, false>(p, chosen, plan.up_rows, plan.route, plan.mt, plan.up_turns, st);
     else
-        product<1, false>(p, chosen, plan.up_rows, plan.mt, plan.up_turns, st);
+        product<1, false>(p, chosen, plan.up_rows, plan.route, plan.mt, plan.up_turns, st);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
-    product<1, true>(p, chosen, plan.down_rows, plan.mt, plan.down_turns, st);
+    if (plan.down_sum) {
+        hipLaunchKernelGGL(k_moe_down, dim3((unsigned)(p.width / 16)), dim3(kDownThreads), 0, st, p);
+        return hipGetLastError();
+    }
+    product<1, true>(p, chosen, plan.down_rows, true, plan.mt, plan.down_turns, st);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const int per = (int)(p.width / 8);
     hipLaunchKernelGGL(k_moe_sum, dim3((unsigned)((p.tokens * per + 255) / 256)), dim3(256), 0, st, p, per);

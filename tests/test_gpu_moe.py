@@ -154,9 +154,11 @@ def test_buffers_and_reproducibility():
     z = nv.moe(x, logits, up, down, 4, residual=r, stream=side)
     side.synchronize()
     assert torch.equal(z, y)
-    # any part of the tokens gives the same rows
-    for lo, hi in ((0, 1), (3, 8), (20, 40)):
-        assert torch.equal(nv.moe(x[lo:hi], logits[lo:hi], up, down, 4, residual=r[lo:hi]), y[lo:hi])
+    # parts of the tokens, each by the kernels that its size takes
+    want, err = dref.moe(x, logits, up, down, 4, "silu", True, False, True, r)
+    check(y, want, err)
+    for lo, hi in ((0, 1), (3, 8), (3, 15), (20, 40)):
+        check(nv.moe(x[lo:hi], logits[lo:hi], up, down, 4, residual=r[lo:hi]), want[lo:hi], err[lo:hi])
     assert nv.moe(x[:0], logits[:0], up, down, 4).shape == (0, 256)
 
 
