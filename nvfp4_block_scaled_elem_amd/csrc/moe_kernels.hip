@@ -73,9 +73,9 @@ __device__ __forceinline__ float wave_sum(float v) {
 }
 
 // The experts of token t, by one wave: lane j < top_k gets choice j (-1: none) and its weight. Lane l holds the logits
-// l, l + 64, ... (R of them)
+// l, l + 64, ... (R of them). `most`: choices to make (the weights are right if all top_k are).
 template <int R>
-__device__ __forceinline__ void route_of(const MoeArgs &p, int64_t t, int &id, float &w) {
+__device__ __forceinline__ void route_of(const MoeArgs &p, int64_t t, int most, int &id, float &w) {
     const int lane = threadIdx.x & 63;
     float l[R];
     uint32_t key[R];
@@ -103,7 +103,7 @@ __device__ __forceinline__ void route_of(const MoeArgs &p, int64_t t, int &id, f
     }
     id = -1;
     float mine = 0.0f;
-    for (int j = 0; j < p.top_k; ++j) {
+    for (int j = 0; j < most; ++j) {
         uint32_t k = 0u;
 #pragma unroll
         for (int r = 0; r < R; ++r) k = max(k, key[r]);
@@ -141,15 +141,15 @@ __device__ __forceinline__ void route_of(const MoeArgs &p, int64_t t, int &id, f
     w = p.normalize || !p.sigmoid ? e / all : e;
 }
 
-__device__ __forceinline__ void route(const MoeArgs &p, int64_t t, int &id, float &w) {
+__device__ __forceinline__ void route(const MoeArgs &p, int64_t t, int most, int &id, float &w) {
     if (p.experts <= 64)
-        route_of<1>(p, t, id, w);
+        route_of<1>(p, t, most, id, w);
     else if (p.experts <= 128)
-        route_of<2>(p, t, id, w);
+        route_of<2>(p, t, most, id, w);
     else if (p.experts <= 256)
-        route_of<4>(p, t, id, w);
+        route_of<4>(p, t, most, id, w);
     else
-        route_of<kMoeMaxExperts / 64>(p, t, id, w);
+        route_of<kMoeMaxExperts / 64>(p, t, most, id, w);
 }
 
 __global__ __launch_bounds__(256) void k_moe_route(MoeArgs p) {
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(256) void k_moe_route(MoeArgs p) {
     if (t >= p.tokens) return;
     int id;
     float w;
-    route(p, t, id, w);
+    route(p, t, p.top_k, id, w);
     if (lane < p.top_k) p.ids[t * p.top_k + lane] = id, p.weights[t * p.top_k + lane] = w;
 }
 
@@ -179,6 +179,12 @@ __device__ __forceinline__ int code_place(int r, int q) { return r * 64 + ((q ^ 
 template <int THREADS>
 __device__ __forceinline__ int take_expert(const MoeArgs &p, const int *ids, int nth, uint8_t *seen, uint16_t *list, int *count) {
     const int tid = threadIdx.x, lane = tid & 63, pairs = (int)p.tokens * p.top_k;
+    if (p.tokens == 1) {  // its choices are all different
+        if (tid == 0) *count = 1, list[0] = (uint16_t)nth;
+        const int e = ids[nth];
+        __syncthreads();
+        return e;
+    }
     for (int e = tid; e < p.experts; e += THREADS) seen[e] = 0;
     if (tid == 0) *count = 0;
     __syncthreads();
@@ -221,7 +227,8 @@ __global__ __launch_bounds__(kThreads) void k_moe_product(MoeArgs p, int tiles) 
         if (wave < p.tokens) {
             int id;
             float w;
-            route(p, wave, id, w);
+            // (one token: this work-group's expert is choice blockIdx.x / tiles, and those after it are not needed)
+            route(p, wave, p.tokens == 1 && blockIdx.x ? (int)blockIdx.x / tiles + 1 : p.top_k, id, w);
             if (lane < p.top_k) {
                 route_ids[wave * p.top_k + lane] = id;
                 if (blockIdx.x == 0) p.ids[wave * p.top_k + lane] = id, p.weights[wave * p.top_k + lane] = w;
@@ -345,33 +352,46 @@ __global__ __launch_bounds__(kDownThreads) void k_moe_down(MoeArgs p) {
     __shared__ __attribute__((aligned(16))) uint8_t lds[kStage > kSums ? kStage : kSums];
     __shared__ uint8_t seen[kMoeMaxExperts];
     __shared__ uint16_t chosen[kMoeMaxExperts];            // the experts in order
-    __shared__ uint8_t choice[kMoeMaxExperts][kDownTokens];  // of expert e by token t: 1 + j, 0 if not
+    __shared__ __attribute__((aligned(16))) uint8_t choice[kMoeMaxExperts][kDownTokens];  // of expert e by token t: 1 + j, 0 if not
     __shared__ int number;
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int pairs = (int)p.tokens * p.top_k;
     const int64_t K = p.inner, F = p.width;
-    for (int e = tid; e < p.experts; e += kDownThreads) {
-        seen[e] = 0;
-        *reinterpret_cast<u32x4 *>(choice[e]) = u32x4{0u, 0u, 0u, 0u};
-    }
-    __syncthreads();
-    for (int i = tid; i < pairs; i += kDownThreads) {
-        const int e = p.ids[i];
-        if (e >= 0) seen[e] = 1, choice[e][i / p.top_k] = (uint8_t)(1 + i % p.top_k);
-    }
-    __syncthreads();
-    if (wave == 0) {
-        int before = 0;
-        for (int e0 = 0; e0 < p.experts; e0 += 64) {
-            const bool in = e0 + lane < p.experts && seen[e0 + lane];
-            const uint64_t who = __ballot(in);
-            if (in) chosen[before + __popcll(who & (((uint64_t)1 << lane) - 1))] = (uint16_t)(e0 + lane);
-            before += __popcll(who);
+    if (p.tokens == 1) {  // its choices are all different
+        if (wave == 0) {
+            const int e = lane < p.top_k ? p.ids[lane] : -1;
+            if (e >= 0) {
+                chosen[lane] = (uint16_t)e;
+                *reinterpret_cast<u32x4 *>(choice[e]) = u32x4{1u + (uint32_t)lane, 0u, 0u, 0u};
+            }
+            const int n = __popcll(__ballot(e >= 0));
+            if (lane == 0) number = n;
         }
-        if (lane == 0) number = before;
+        __syncthreads();
+    } else {
+        for (int e = tid; e < p.experts; e += kDownThreads) {
+            seen[e] = 0;
+            *reinterpret_cast<u32x4 *>(choice[e]) = u32x4{0u, 0u, 0u, 0u};
+        }
+        __syncthreads();
+        for (int i = tid; i < pairs; i += kDownThreads) {
+            const int e = p.ids[i];
+            if (e >= 0) seen[e] = 1, choice[e][i / p.top_k] = (uint8_t)(1 + i % p.top_k);
+        }
+        __syncthreads();
+        if (wave == 0) {
+            int before = 0;
+            for (int e0 = 0; e0 < p.experts; e0 += 64) {
+                const bool in = e0 + lane < p.experts && seen[e0 + lane];
+                const uint64_t who = __ballot(in);
+                if (in) chosen[before + __popcll(who & (((uint64_t)1 << lane) - 1))] = (uint16_t)(e0 + lane);
+                before += __popcll(who);
+            }
+            if (lane == 0) number = before;
+        }
+        __syncthreads();
     }
-    __syncthreads();
     const int nch = (int)((K + kChunk - 1) / kChunk), items = number * nch;
     const int lo = (int)((int64_t)items * wave / kDownWaves), hi = (int)((int64_t)items * (wave + 1) / kDownWaves);
     const int64_t f0 = (int64_t)blockIdx.x * 16;
@@ -732,7 +752,7 @@ Plan plan_moe(int64_t tokens, int64_t width, int64_t inner, int experts, int top
     plan.split = 1;
     if (plan.down_rows) {
         const int64_t slices = (inner + kSlice - 1) / kSlice;
-        while (plan.split < 8 && 4 * plan.split <= slices && used * down * plan.split < 768) plan.split *= 2;
+        while (plan.split < 8 && 4 * plan.split <= slices && used * down * plan.split < 512) plan.split *= 2;
     }
     // Three work-groups a CU, where X stays.
     plan.up_turns = width <= 2 * kSlice ? (int)std::max(1.0, used * up / 768.0 + 0.5) : 1;
