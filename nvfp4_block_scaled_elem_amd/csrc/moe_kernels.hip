@@ -174,42 +174,73 @@ __device__ __forceinline__ float rest_of(float v, float hi) {
 // 16-byte piece q (0..3) of row r of a chunk's codes in LDS: the 16 lanes that read one q of 16 rows meet no bank twice.
 __device__ __forceinline__ int code_place(int r, int q) { return r * 64 + ((q ^ ((r >> 2) & 3)) << 4); }
 
-// The chosen experts in order: the number `nth` of them (-1: there are not so many), and its pairs into `list`. By the whole
-// work-group; `seen` has a byte per expert.
+// The chosen experts in order, by a whole work-group: find() gives the number `nth` of them (-1: there are not so many), fill()
+// puts its pairs into `list`. `seen` has a byte per expert. A thread's ids are loaded at once and kept: one by one, 1200 of
+// them took 8 us of a work-group's time.
 template <int THREADS>
-__device__ __forceinline__ int take_expert(const MoeArgs &p, const int *ids, int nth, uint8_t *seen, uint16_t *list, int *count) {
-    const int tid = threadIdx.x, lane = tid & 63, pairs = (int)p.tokens * p.top_k;
-    if (p.tokens == 1) {  // its choices are all different
-        if (tid == 0) *count = 1, list[0] = (uint16_t)nth;
-        const int e = ids[nth];
-        __syncthreads();
-        return e;
-    }
-    for (int e = tid; e < p.experts; e += THREADS) seen[e] = 0;
-    if (tid == 0) *count = 0;
-    __syncthreads();
-    for (int i = tid; i < pairs; i += THREADS) {
-        const int e = ids[i];
-        if (e >= 0) seen[e] = 1;
-    }
-    __syncthreads();
-    int before = 0, mine = -1;
-    for (int e0 = 0; e0 < p.experts && mine < 0; e0 += 64) {
-        uint64_t who = __ballot(e0 + lane < p.experts && seen[e0 + lane]);
-        const int n = __popcll(who);
-        if (before + n > nth) {
-            for (int k = before; k < nth; ++k) who &= who - 1;
-            mine = e0 + __ffsll((unsigned long long)who) - 1;
+struct Pick {
+    static constexpr int kMine = 8;
+    int id[kMine];
+    int expert;
+    __device__ __forceinline__ void load(const int *ids, int i0, int pairs) {
+#pragma unroll
+        for (int u = 0; u < kMine; ++u) {
+            const int i = i0 + THREADS * u + threadIdx.x;
+            id[u] = i < pairs ? ids[i] : -1;
         }
-        before += n;
     }
-    if (mine < 0) return -1;
+    __device__ __forceinline__ int find(const MoeArgs &p, const int *ids, int nth, uint8_t *seen, int *count) {
+        const int tid = threadIdx.x, lane = tid & 63, pairs = (int)p.tokens * p.top_k;
+        if (p.tokens == 1) {  // its choices are all different
+            expert = ids[nth];
+            if (tid == 0) *count = 1;
+            return expert;
+        }
+        load(ids, 0, pairs);
+        for (int e = tid; e < (p.experts + 3) / 4; e += THREADS) reinterpret_cast<uint32_t *>(seen)[e] = 0u;
+        if (tid == 0) *count = 0;
+        __syncthreads();
+        for (int i0 = 0;;) {
+#pragma unroll
+            for (int u = 0; u < kMine; ++u)
+                if (id[u] >= 0) seen[id[u]] = 1;
+            i0 += THREADS * kMine;
+            if (i0 >= pairs) break;
+            load(ids, i0, pairs);
+        }
+        __syncthreads();
+        int before = 0;
+        expert = -1;
+        for (int e0 = 0; e0 < p.experts && expert < 0; e0 += 64) {
+            uint64_t who = __ballot(e0 + lane < p.experts && seen[e0 + lane]);
+            const int n = __popcll(who);
+            if (before + n > nth) {
+                for (int k = before; k < nth; ++k) who &= who - 1;
+                expert = e0 + __ffsll((unsigned long long)who) - 1;
+            }
+            before += n;
+        }
+        return expert;
+    }
     // The pairs' order in the list decides their column alone, which no result depends on.
-    for (int i = tid; i < pairs; i += THREADS)
-        if (ids[i] == mine) list[atomicAdd(count, 1)] = (uint16_t)i;
-    __syncthreads();
-    return mine;
-}
+    __device__ __forceinline__ void fill(const MoeArgs &p, const int *ids, int nth, uint16_t *list, int *count) {
+        const int tid = threadIdx.x, pairs = (int)p.tokens * p.top_k;
+        if (p.tokens == 1) {
+            if (tid == 0) list[0] = (uint16_t)nth;
+        } else {
+            if (pairs > THREADS * kMine) load(ids, 0, pairs);
+            for (int i0 = 0;;) {
+#pragma unroll
+                for (int u = 0; u < kMine; ++u)
+                    if (id[u] == expert) list[atomicAdd(count, 1)] = (uint16_t)(i0 + THREADS * u + tid);
+                i0 += THREADS * kMine;
+                if (i0 >= pairs) break;
+                load(ids, i0, pairs);
+            }
+        }
+        __syncthreads();
+    }
+};
 
 // NT: 2 if gated. SECOND: the product with W2, else with W1. ROUTE: to eight tokens, whose experts every work-group finds by
 // itself, a wave a token (a launch saved); the first one writes them down.
@@ -217,7 +248,7 @@ template <int NT, bool SECOND, bool ROUTE>
 __global__ __launch_bounds__(kThreads) void k_moe_product(MoeArgs p, int tiles) {
     constexpr int kStage = kWaves * NT * kChunkLds, kSums = kWaves * NT * 1024;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kStage > kSums ? kStage : kSums];
-    __shared__ uint8_t seen[kMoeMaxExperts];
+    __shared__ __attribute__((aligned(4))) uint8_t seen[kMoeMaxExperts];
     extern __shared__ uint16_t list[];  // an expert's pairs: as many as tokens at most
     __shared__ int count;
     __shared__ int route_ids[ROUTE ? kWaves * kMoeMaxTopK : 1];
@@ -236,8 +267,11 @@ __global__ __launch_bounds__(kThreads) void k_moe_product(MoeArgs p, int tiles) 
         }
         __syncthreads();
     }
-    const int expert = take_expert<kThreads>(p, ROUTE ? route_ids : p.ids, blockIdx.x / tiles, seen, list, &count);
+    const int *const ids = ROUTE ? route_ids : p.ids;
+    Pick<kThreads> pick;
+    const int expert = pick.find(p, ids, blockIdx.x / tiles, seen, &count);
     if (expert < 0) return;
+    pick.fill(p, ids, blockIdx.x / tiles, list, &count);
     const int64_t K = SECOND ? p.inner : p.width, F = SECOND ? p.width : p.inner;
     const int64_t f0 = (int64_t)(blockIdx.x % tiles) * 16, nch = (K + kChunk - 1) / kChunk;
     const MoeWeights &W = SECOND ? p.down : p.up;
@@ -501,13 +535,15 @@ __global__ __launch_bounds__(kRowThreads, MT == 1 ? 3 : 2) void k_moe_rows(MoeAr
     constexpr int kCols = NT == 2 ? 16 * kRowWaves : 32 * kRowWaves;
     __shared__ __attribute__((aligned(16))) uint8_t lds_x[2][kXBytes];
     __shared__ __attribute__((aligned(16))) uint8_t lds_w[kRowWaves][kWaveCodes];
-    __shared__ uint8_t seen[kMoeMaxExperts];
+    __shared__ __attribute__((aligned(4))) uint8_t seen[kMoeMaxExperts];
     extern __shared__ uint16_t list[];  // an expert's pairs: as many as tokens at most
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int expert = take_expert<kRowThreads>(p, p.ids, blockIdx.x / groups, seen, list, &count);
+    Pick<kRowThreads> pick;
+    const int expert = pick.find(p, p.ids, blockIdx.x / groups, seen, &count);
     if (expert < 0) return;
+    pick.fill(p, p.ids, blockIdx.x / groups, list, &count);
     const int K = (int)(SECOND ? p.inner : p.width), F = (int)(SECOND ? p.width : p.inner);
     // The work-group's column tiles: first, first + groups, ...
     const int first = (int)(blockIdx.x % groups), turns = HOLD ? (tiles - first + groups - 1) / groups : 1;
@@ -752,7 +788,7 @@ Plan plan_moe(int64_t tokens, int64_t width, int64_t inner, int experts, int top
     plan.split = 1;
     if (plan.down_rows) {
         const int64_t slices = (inner + kSlice - 1) / kSlice;
-        while (plan.split < 8 && 4 * plan.split <= slices && used * down * plan.split < 512) plan.split *= 2;
+        while (plan.split < 8 && 4 * plan.split <= slices && used * down * plan.split < 500) plan.split *= 2;
     }
     // Three work-groups a CU, where X stays.
     plan.up_turns = width <= 2 * kSlice ? (int)std::max(1.0, used * up / 768.0 + 0.5) : 1;
