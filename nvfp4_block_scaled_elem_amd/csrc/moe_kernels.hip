@@ -524,14 +524,14 @@ __global__ __launch_bounds__(kDownThreads) void k_moe_down(MoeArgs p) {
 // Many rows: a wave owns 32 weight rows (gated: 16 gate rows and their 16 up rows) over the whole sum, and a work-group's
 // four waves share the tokens' values, which go through LDS in slices of 512 k in the order of the operand. A wave's codes
 // and scales of a slice are all in flight while the slice before is multiplied: 9 KB a wave, no barrier waits for them.
-// MT: tiles of 16 pairs at a time. SECOND: the product with W2, its sum cut into p.split parts of slices, else with W1. HOLD: X
+// MOST: tiles of 16 pairs at a time. SECOND: the product with W2, its sum cut into p.split parts of slices, else with W1. HOLD: X
 // is at most two slices and stays where it is while the work-group goes through several column tiles, without a barrier.
 constexpr int kRowWaves = 4, kRowThreads = 64 * kRowWaves, kSlice = 512, kSliceChunks = kSlice / kChunk;
 constexpr int kWaveCodes = 2 * (1024 + 512);  // LDS bytes of a wave: a chunk's codes and a slice's scales of two tiles
 
-template <int NT, int MT, bool SECOND, bool HOLD>
-__global__ __launch_bounds__(kRowThreads, MT == 1 ? 3 : 2) void k_moe_rows(MoeArgs p, int tiles, int groups) {
-    constexpr int kXBytes = 16 * MT * kSlice * 2, kX = kXBytes / 16 / kRowThreads;  // of a slice; pieces a thread
+template <int NT, int MOST, bool SECOND, bool HOLD>
+__global__ __launch_bounds__(kRowThreads, 2) void k_moe_rows(MoeArgs p, int tiles, int groups) {
+    constexpr int kXBytes = 16 * MOST * kSlice * 2;  // of a slice
     constexpr int kCols = NT == 2 ? 16 * kRowWaves : 32 * kRowWaves;
     __shared__ __attribute__((aligned(16))) uint8_t lds_x[2][kXBytes];
     __shared__ __attribute__((aligned(16))) uint8_t lds_w[kRowWaves][kWaveCodes];
@@ -570,7 +570,9 @@ __global__ __launch_bounds__(kRowThreads, MT == 1 ? 3 : 2) void k_moe_rows(MoeAr
     // codes: the lane loads row lane / 4, 16 bytes lane % 4 of a chunk; scales: row lane / 4, the 8 of chunk lane % 4
     const uint32_t crow = (uint32_t)(lane >> 2) * (uint32_t)(K / 2), srow = (uint32_t)(lane >> 2) * (uint32_t)(K / 16);
     const int pairs = count;
-    for (int c0 = 0; c0 < pairs; c0 += 16 * MT) {
+    // The pairs c0 .. + 16 MT - 1 of the list.
+    auto pass = [&](auto tiles_of_pairs, int c0) __attribute__((always_inline)) {
+        constexpr int MT = tiles_of_pairs.value, kX = 16 * MT * kSlice * 2 / 16 / kRowThreads;  // tiles; pieces a thread
         u32x4 cv[2][kSliceChunks], xv[kX];
         u32x2 sv[2];
         f32x4 acc[2][MT] = {};
@@ -737,6 +739,12 @@ __global__ __launch_bounds__(kRowThreads, MT == 1 ? 3 : 2) void k_moe_rows(MoeAr
             }
             finish(0);
         }
+    };
+    for (int c0 = 0; c0 < pairs;) {
+        if (MOST == 2 && pairs - c0 > 16)
+            pass(std::integral_constant<int, MOST>{}, c0), c0 += 16 * MOST;
+        else
+            pass(std::integral_constant<int, 1>{}, c0), c0 += 16;
         lds_barrier();  // the last slices have been read
     }
 }
