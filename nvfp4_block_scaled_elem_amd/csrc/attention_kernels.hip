@@ -94,6 +94,35 @@ struct Rows {
     int lim[RT];  // tokens that the lane's row sees (0: no such row)
 };
 
+// The tokens that a row sees, more for a later one.
+__device__ __forceinline__ int seen_by(const AttnArgs &p, const Seq &q, int row) {
+    return p.causal ? min(max(q.len - q.n + row / p.group + 1, 0), q.len) : q.len;
+}
+
+// The lane's rows row0 + 16 r + l % 16 of the sequence: their queries as operands, and what they see.
+template <int KS, int RT, bool FULL>
+__device__ __forceinline__ void take_rows(const AttnArgs &p, const Seq &q, int64_t h, int row0, bf16x8 (&Q)[RT][2 * KS], Rows<KS, RT> &R) {
+    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const int row = row0 + 16 * r + r16, tok = row / p.group, sub = row % p.group;
+        const bool in = tok < q.n;
+        R.lim[r] = !in ? 0 : p.causal ? min(max(q.len - q.n + tok + 1, 0), q.len) : q.len;
+        const uint16_t *x = p.q + (int64_t)(q.first + tok) * p.qs + (h * p.group + sub) * p.qh;
+#pragma unroll
+        for (int k = 0; k < 2 * KS; ++k) {
+            const int c = 64 * (k >> 1) + 16 * g + 8 * (k & 1);
+            u32x4 v = {0u, 0u, 0u, 0u};
+            if (in && (FULL || c < p.dim)) v = *reinterpret_cast<const u32x4_any *>(x + c);
+            v ^= p.flip;  // a negative scale: -q, exact
+            Q[r][k] = __builtin_bit_cast(bf16x8, v);
+        }
+        R.m[r] = kNegInf, R.l[r] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < 4 * KS; ++d) R.o[r][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+}
+
 // LDS bytes of a wave's block: K's rows with an odd number of 16-byte pieces from one to the next and four pieces more per 16
 // rows, so that the sixteen lanes that read one piece of the tokens 16 a + 4 t + j meet no bank twice; V's tiles of 16 columns.
 template <int KS>
@@ -109,12 +138,12 @@ constexpr int kWaveLds = kWaveK<KS> + 4096 * KS;
 // four times the address cycles. They are turned in LDS, where only the wave itself writes and reads, and the next
 // block's loads are in flight meanwhile.
 template <int KS, int RT, bool FULL>
-__device__ __forceinline__ void attend(const AttnArgs &p, const Seq &q, int s, int64_t h, int b0, int b1, int step, int safe,
-                                       const bf16x8 (&Q)[RT][2 * KS], Rows<KS, RT> &R, uint8_t *wl) {
+__device__ __forceinline__ void attend(const AttnArgs &p, const Seq &q, int s, int64_t h, int row0, int b0, int b1, int step,
+                                       Rows<KS, RT> &R, uint8_t *wl) {
     const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
     const int dim = FULL ? 64 * KS : p.dim, per = dim / 16;  // 16-byte pieces of a token; loads of a block's K, and of its V
     const int count = b1 > b0 ? (b1 - b0 + step - 1) / step : 0;
-    if (count == 0) return;
+    const int safe = seen_by(p, q, row0);  // blocks below need no mask
     const int pitch = dim + (per & 1 ? 0 : 16);
     uint8_t *const wv = wl + kWaveK<KS>;
     // Pages and scales of 64 of the wave's blocks, one a lane.
@@ -147,6 +176,9 @@ __device__ __forceinline__ void attend(const AttnArgs &p, const Seq &q, int s, i
     };
     auto k_place = [&](int token, int c) __attribute__((always_inline)) { return token * pitch + 64 * (token >> 4) + 16 * c; };
     look_up(0);
+    bf16x8 Q[RT][2 * KS];
+    take_rows<KS, RT, FULL>(p, q, h, row0, Q, R);
+    if (count == 0) return;
     int64_t base = base_of(0);
     load_k(base);
     load_v(base);
@@ -265,36 +297,6 @@ __device__ __forceinline__ void attend(const AttnArgs &p, const Seq &q, int s, i
         if (R.lim[r] > poison) R.l[r] = __builtin_nanf("");
 }
 
-// The lane's rows row0 + 16 r + l % 16 of the sequence: their queries as operands, and what they see. Returns the
-// tokens that all of the wave's rows see.
-template <int KS, int RT, bool FULL>
-__device__ __forceinline__ int take_rows(const AttnArgs &p, const Seq &q, int64_t h, int row0, bf16x8 (&Q)[RT][2 * KS], Rows<KS, RT> &R) {
-    const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
-    int safe = 0x7FFFFFFF;
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        const int row = row0 + 16 * r + r16, tok = row / p.group, sub = row % p.group;
-        const bool in = tok < q.n;
-        R.lim[r] = !in ? 0 : p.causal ? min(max(q.len - q.n + tok + 1, 0), q.len) : q.len;
-        if (in) safe = min(safe, R.lim[r]);
-        const uint16_t *x = p.q + (int64_t)(q.first + tok) * p.qs + (h * p.group + sub) * p.qh;
-#pragma unroll
-        for (int k = 0; k < 2 * KS; ++k) {
-            const int c = 64 * (k >> 1) + 16 * g + 8 * (k & 1);
-            u32x4 v = {0u, 0u, 0u, 0u};
-            if (in && (FULL || c < p.dim)) v = *reinterpret_cast<const u32x4_any *>(x + c);
-            v ^= p.flip;  // a negative scale: -q, exact
-            Q[r][k] = __builtin_bit_cast(bf16x8, v);
-        }
-        R.m[r] = kNegInf, R.l[r] = 0.0f;
-#pragma unroll
-        for (int d = 0; d < 4 * KS; ++d) R.o[r][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    }
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) safe = min(safe, __shfl_xor(safe, k));
-    return __builtin_amdgcn_readfirstlane(safe);
-}
-
 __device__ __forceinline__ uint16_t *out_row(const AttnArgs &p, const Seq &q, int64_t h, int row) {
     return p.out + ((int64_t)(q.first + row / p.group) * p.kv_heads * p.group + h * p.group + row % p.group) * p.dim;
 }
@@ -327,13 +329,8 @@ __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(Att
     const int row0 = first + 16 * RT * wave, dim = FULL ? 64 * KS : p.dim;
     bf16x8 Q[RT][2 * KS];
     Rows<KS, RT> R;
-    const int safe = take_rows<KS, RT, FULL>(p, q, h, row0, Q, R);
-    int most = 0;  // tokens that some row of the wave sees
-#pragma unroll
-    for (int r = 0; r < RT; ++r) most = max(most, R.lim[r]);
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) most = max(most, __shfl_xor(most, k));
-    most = __builtin_amdgcn_readfirstlane(most);
+    const int safe = seen_by(p, q, row0);
+    take_rows<KS, RT, FULL>(p, q, h, row0, Q, R);
     const int last_tok = min(q.n, (first + kRows - 1) / p.group + 1);  // behind the work-group's last row
     const int reach = p.causal ? min(max(q.len - q.n + last_tok, 0), q.len) : q.len;
     const int count = (reach + kPage - 1) / kPage;
@@ -557,6 +554,12 @@ struct Share {
 __device__ __forceinline__ int tiles_of(const AttnArgs &p, const Seq &q, int size) { return (q.n * p.group + size - 1) / size; }
 __device__ __forceinline__ int blocks_of(const Seq &q) { return (q.len + kPage - 1) / kPage; }
 
+// row_shr and row_bcast of the rows in MASK; 0 where there is no source.
+template <int CTRL, int MASK>
+__device__ __forceinline__ uint32_t shifted(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, MASK, 0xF, false);
+}
+
 // 64 sequences, one a lane, with the blocks (of all their tiles) in front of them in the list. By whole waves.
 struct Window {
     int s0;
@@ -569,12 +572,14 @@ struct Window {
             q = sequence(p.seq, s0 + lane);
             mine = (uint32_t)(tiles_of(p, q, size) * blocks_of(q));
         }
+        // inclusive sums: within rows of 16 lanes, then row 0's over row 1 and row 2's over row 3, then the first half's
         upto = mine;
-#pragma unroll
-        for (int k = 1; k < 64; k <<= 1) {
-            const uint32_t v = (uint32_t)__shfl_up((int)upto, k);
-            if (lane >= k) upto += v;
-        }
+        upto += shifted<0x111, 0xF>(upto);
+        upto += shifted<0x112, 0xF>(upto);
+        upto += shifted<0x114, 0xF>(upto);
+        upto += shifted<0x118, 0xF>(upto);
+        upto += shifted<0x142, 0xA>(upto);
+        upto += shifted<0x143, 0xC>(upto);
     }
     __device__ __forceinline__ uint32_t total() const { return before + (uint32_t)__builtin_amdgcn_readlane((int)upto, 63); }
     __device__ __forceinline__ Seq seq(int s) const {
@@ -600,8 +605,10 @@ __device__ __forceinline__ uint32_t list_total(const AttnArgs &p, int size, Wind
 __device__ __forceinline__ Share share_of(const AttnArgs &p, uint32_t total) {
     Share sh;
     sh.total = total;
-    // Not less than a block for each wave of a work-group.
+    // Not less than a block for each wave of a work-group. Long shares go to half as many work-groups, one a CU: parts
+    // and pieces are fewer (64 sequences of 300 to 16000 tokens: 110 -> 99 us), where short ones lack loads in flight.
     sh.groups = max(1u, min((uint32_t)p.groups, (total + kWaves - 1) / kWaves));
+    if (total >= (uint32_t)p.groups * (kWaves * 8u)) sh.groups = ((uint32_t)p.groups + 1u) / 2u;
     return sh;
 }
 
@@ -635,10 +642,8 @@ __global__ __launch_bounds__(kAttnThreads, RT * KS <= 2 ? 2 : 1) void k_attn_spl
         const int tile = (int)((u - at) / nb), b0 = (int)((u - at) % nb), b1 = (int)min(nb, b0 + (end - u));
         u += b1 - b0;
         const int row0 = tile * kRows, rows = min(kRows, q.n * p.group - row0);
-        bf16x8 Q[RT][2 * KS];
         Rows<KS, RT> R;
-        const int safe = take_rows<KS, RT, FULL>(p, q, h, row0, Q, R);
-        attend<KS, RT, FULL>(p, q, s, h, b0 + wave, b1, kWaves, safe, Q, R, lds + wave * kWaveLds<KS>);
+        attend<KS, RT, FULL>(p, q, s, h, row0, b0 + wave, b1, kWaves, R, lds + wave * kWaveLds<KS>);
         const bool whole = b0 == 0 && b1 == (int)nb;
         const int64_t place = part_place(p, h, j, piece_base(p.seq, s, p.group, kRows, 1) + tile);
 #pragma unroll
