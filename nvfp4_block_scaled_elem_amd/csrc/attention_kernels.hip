@@ -331,9 +331,9 @@ __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(Att
     Rows<KS, RT> R;
     const int safe = seen_by(p, q, row0);
     take_rows<KS, RT, FULL>(p, q, h, row0, Q, R);
-    const int last_tok = min(q.n, (first + kRows - 1) / p.group + 1);  // behind the work-group's last row
-    const int reach = p.causal ? min(max(q.len - q.n + last_tok, 0), q.len) : q.len;
-    const int count = (reach + kPage - 1) / kPage;
+    // The blocks that some row of the work-group sees, or this part of them.
+    const int reach = seen_by(p, q, min(first + kRows, q.n * p.group) - 1), all = (reach + kPage - 1) / kPage;
+    const int start = (int)((int64_t)all * blockIdx.y / gridDim.y), count = (int)((int64_t)all * (blockIdx.y + 1) / gridDim.y);
 
     // Pages and scales of 64 blocks, one a lane.
     int page = -1;
@@ -352,11 +352,11 @@ __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(Att
         float ks, vs;
         int live;
     };
-    int poison = 0x7FFFFFFF, ahead = 0;
+    int poison = 0x7FFFFFFF, ahead = start;
     auto block_of = [&](int b) __attribute__((always_inline)) {
         if (b >= ahead && b < count) look_up(b), ahead = b + 64;  // b == ahead
-        const int pg = __builtin_amdgcn_readlane(page, b & 63);
-        const uint32_t sc = (uint32_t)__builtin_amdgcn_readlane((int)scales, b & 63);
+        const int pg = __builtin_amdgcn_readlane(page, (b - start) & 63);
+        const uint32_t sc = (uint32_t)__builtin_amdgcn_readlane((int)scales, (b - start) & 63);
         const bool nan = (sc & 255u) == 255u || (sc >> 8) == 255u;
         Block B;
         B.live = b < count && pg >= 0 && !nan;
@@ -440,18 +440,18 @@ __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(Att
         __syncthreads();
     }
     int live = 0;  // of the block that is computed
-    if (count > 0) {
-        load_k(0);
+    if (start < count) {
+        load_k(start);
         load_v();
         live = kb.live;
-        store_k(0);
-        store_v(0);
-        load_k(1);
+        store_k(start);
+        store_v(start);
+        load_k(start + 1);
         load_v();
         lds_barrier();
     }
 #pragma unroll 1
-    for (int b = 0; b < count; ++b) {
+    for (int b = start; b < count; ++b) {
         const int t0 = b * kPage;
         f32x4 S[RT][4];
         scores(b, S);
@@ -525,9 +525,17 @@ __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(Att
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
         const float l = row_sum(R.lim[r] > poison ? __builtin_nanf("") : R.l[r]);
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         const int row = row0 + 16 * r + r16;
         if (row >= q.n * p.group) continue;
+        if (gridDim.y > 1) {  // a part: k_attn_join adds them
+            const int64_t at = ((h * p.pieces + piece) * gridDim.y + blockIdx.y) * kRows + (row - first);
+            if (g == 0) p.part_ml[2 * at] = R.m[r] * p.scale2, p.part_ml[2 * at + 1] = l;
+#pragma unroll
+            for (int d = 0; d < 4 * KS; ++d)
+                if (FULL || 16 * d < p.dim) *reinterpret_cast<f32x4 *>(p.part + at * dim + 16 * d + 4 * g) = R.o[r][d];
+            continue;
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
         uint16_t *o = out_row(p, q, h, row) + 4 * g;
 #pragma unroll
         for (int d = 0; d < 4 * KS; ++d)
@@ -719,12 +727,16 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_join(AttnArgs p, int size
         if (turn == 0 && c < p.dim) *reinterpret_cast<uint2 *>(o + c) = make_uint2(0u, 0u);
         return;
     }
-    const Share sh = share_of(p, total);
-    const uint32_t u0 = w.begin(s) + (uint32_t)tile * nb;
-    const uint32_t j0 = sh.owner(u0), j1 = sh.owner(u0 + nb - 1);
-    if (j0 == j1) return;
-    const int parts = (int)(j1 - j0 + 1);
-    const int64_t at = part_place(p, h, j0, piece) * size + row;
+    int parts = p.parts;  // of k_attn_rows: all tiles alike
+    int64_t at = (h * p.pieces + piece) * p.parts * size + row;
+    if (parts == 0) {
+        const Share sh = share_of(p, total);
+        const uint32_t u0 = w.begin(s) + (uint32_t)tile * nb;
+        const uint32_t j0 = sh.owner(u0), j1 = sh.owner(u0 + nb - 1);
+        if (j0 == j1) return;
+        parts = (int)(j1 - j0 + 1);
+        at = part_place(p, h, j0, piece) * size + row;
+    }
     float m = kNegInf;
     for (int k = lane; k < parts; k += 64) m = fmaxf(m, p.part_ml[(at + (int64_t)k * size) * 2]);
 #pragma unroll
@@ -764,11 +776,6 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_join(AttnArgs p, int size
 template <int KS, bool FULL>
 void split(const AttnArgs &p, int rt, hipStream_t st) {
     const dim3 grid((unsigned)(p.groups * p.kv_heads)), block(kAttnThreads);
-    if constexpr (KS <= 2)
-        if (rt == 4) {
-            hipLaunchKernelGGL((k_attn_split<KS, 4, FULL>), grid, block, 0, st, p);
-            return;
-        }
     if (rt >= 2)
         hipLaunchKernelGGL((k_attn_split<KS, 2, FULL>), grid, block, 0, st, p);
     else
@@ -776,10 +783,13 @@ void split(const AttnArgs &p, int rt, hipStream_t st) {
 }
 
 template <int KS, bool FULL>
-void rows(const AttnArgs &p, hipStream_t st) {
-    const dim3 grid((unsigned)((int64_t)p.pieces * p.kv_heads)), block(kAttnThreads);
+void rows(const AttnArgs &p, int rt, hipStream_t st) {
+    const dim3 grid((unsigned)((int64_t)p.pieces * p.kv_heads), (unsigned)std::max(1, p.parts)), block(kAttnThreads);
     constexpr size_t lds = 4 * 64 * 64 * KS * 2;
-    hipLaunchKernelGGL((k_attn_rows<KS, 2, FULL>), grid, block, lds, st, p);
+    if (rt == 1)
+        hipLaunchKernelGGL((k_attn_rows<KS, 1, FULL>), grid, block, lds, st, p);
+    else
+        hipLaunchKernelGGL((k_attn_rows<KS, 2, FULL>), grid, block, lds, st, p);
 }
 
 
@@ -787,17 +797,27 @@ void rows(const AttnArgs &p, hipStream_t st) {
 
 AttnPlan plan_attention(int64_t tokens, int seqs, int width, int kv_heads, int group, int dim) {
     AttnPlan plan = {};
-    const int ks = (dim + 63) / 64;
     const int64_t all = tokens * group, mean = seqs ? (all + seqs - 1) / seqs : 0;  // rows of a head; of a sequence
-    const int big = 128;
-    // Rows over the waves where that makes work for the whole GPU, else blocks over the work-groups.
-    if (mean > 64 && (all / big) * kv_heads >= 256) {
+    // Rows over the waves from more than 32 rows of a sequence on: 16 sequences of 4000 tokens, 52 rows each: 48 us (blocks over
+    // the work-groups: 62); 30 sequences of 500 to 5000, 24 rows: 71 us (53).
+    if (mean > 32) {
         plan.rows = true;
-        plan.size = big;
-        plan.pieces = all / big + seqs;
+        plan.rt = mean > 64 ? 2 : 1;
+        plan.size = 64 * plan.rt;
+        plan.pieces = all / plan.size + seqs;
+        // Two work-groups a CU, the blocks in parts where the rows make fewer: 1024 rows over 8256 tokens in eight parts 58 us,
+        // in one 190. But not less than 16 blocks a part: 4000 rows over 1000 tokens 31 us, in two parts 50.
+        const int64_t groups = std::max<int64_t>(1, (all / plan.size + (seqs + 1) / 2) * kv_heads);
+        const int64_t parts = std::min<int64_t>({512 / groups, (width + 15) / 16, 64});
+        plan.parts = parts > 1 ? (int)parts : 0;
+        if (plan.parts) {
+            const int64_t rows = (int64_t)kv_heads * plan.pieces * plan.parts * plan.size;
+            plan.part_bytes = ((size_t)rows * dim * 4 + 255) / 256 * 256;
+            plan.ml_bytes = (size_t)rows * 8;
+        }
         return plan;
     }
-    const int rt = mean <= 16 ? 1 : mean <= 32 || ks > 2 ? 2 : 4;
+    const int rt = mean <= 16 ? 1 : 2;
     plan.rt = rt;
     plan.size = 16 * rt;
     plan.pieces = all / plan.size + seqs;
@@ -813,13 +833,13 @@ AttnPlan plan_attention(int64_t tokens, int seqs, int width, int kv_heads, int g
 hipError_t launch_attention(const AttnArgs &a, void *ws, hipStream_t st) {
     AttnArgs p = a;
     const AttnPlan plan = plan_attention(p.seq.tokens, p.seq.seqs, p.seq.width, p.kv_heads, p.group, p.dim);
-    p.pieces = (int)plan.pieces, p.groups = plan.groups;
+    p.pieces = (int)plan.pieces, p.groups = plan.groups, p.parts = plan.parts;
     p.part = static_cast<float *>(ws);
     p.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + plan.part_bytes);
     // The sizes most heads have, and forms for any other.
     auto run = [&](auto ks, auto full) {
         if (plan.rows)
-            rows<ks.value, full.value>(p, st);
+            rows<ks.value, full.value>(p, plan.rt, st);
         else
             split<ks.value, full.value>(p, plan.rt, st);
     };
@@ -836,7 +856,7 @@ hipError_t launch_attention(const AttnArgs &a, void *ws, hipStream_t st) {
             else if (p.dim <= 192) run(integral_constant<int, 3>{}, Part{});
             else run(integral_constant<int, 4>{}, Part{});
     }
-    if (plan.rows) return hipGetLastError();
+    if (plan.rows && !plan.parts) return hipGetLastError();
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const int most = p.seq.starts ? plan.size : std::min(plan.size, p.group);  // rows of a tile
     // Many parts to a tile: a work-group each row (one sequence of 8000 tokens, 31 parts: 4.4 us, 10.6 with a wave a row); else

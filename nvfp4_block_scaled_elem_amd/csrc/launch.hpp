@@ -232,13 +232,14 @@ struct AttnArgs {
     float scale2, slack;    // the scores' factor (positive) in powers of two; 8 / scale2
     uint32_t flip;          // of two bf16: the signs, for a negative factor
     int kv_heads, group, dim, causal;
-    int pieces, groups;  // set by the launcher
+    int pieces, groups, parts;  // set by the launcher
 };
 struct AttnPlan {
     bool rows;       // rows over the waves; else blocks over the work-groups
     int rt, size;    // tiles of 16 rows of a wave; rows of a piece
     int64_t pieces;  // their numbers are below this
     int groups;      // work-groups of a head (blocks over them)
+    int parts;       // of the blocks (rows over the waves; 0: all together)
     size_t part_bytes, ml_bytes;
 };
 AttnPlan plan_attention(int64_t tokens, int seqs, int width, int kv_heads, int group, int dim);
