@@ -4,6 +4,7 @@
 #include <stdint.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "cache.hpp"
 #include "codec.hpp"
@@ -18,6 +19,38 @@ constexpr int kThreads = 256;
 
 // ------------------------------------------------------------------------------------------- rotary
 
+// Raw8's bytes in plain vectors, which stay in registers when they are assigned (uint4 went through scratch).
+__device__ __forceinline__ u32x4 plain(uint4 v) { return u32x4{v.x, v.y, v.z, v.w}; }
+__device__ __forceinline__ uint4 back(u32x4 v) { return make_uint4(v.x, v.y, v.z, v.w); }
+struct Held16 {
+    u32x4 a;
+    __device__ __forceinline__ void load(const uint16_t *p, int n) {
+        Raw8<uint16_t> r;
+        r.load(p, n);
+        a = plain(r.a);
+    }
+    __device__ __forceinline__ void get(float v[8]) const {
+        Raw8<uint16_t> r;
+        r.a = back(a);
+        r.get(v);
+    }
+};
+struct Held32 {
+    u32x4 a, b;
+    __device__ __forceinline__ void load(const float *p, int n) {
+        Raw8<float> r;
+        r.load(p, n);
+        a = plain(r.a), b = plain(r.b);
+    }
+    __device__ __forceinline__ void get(float v[8]) const {
+        Raw8<float> r;
+        r.a = back(a), r.b = back(b);
+        r.get(v);
+    }
+};
+template <typename T>
+using Held = typename std::conditional<sizeof(T) == 2, Held16, Held32>::type;
+
 // y[j] = a cos t - b sin t, y[j + R/2] = b cos t + a sin t for (a, b) = (x[j], x[j + R/2]), j < R/2, with the angle
 // t = pos[axis of j] base^(-2j/R); columns from R on pass. Bound by x and y (16 bytes a thread each way).
 //
@@ -27,7 +60,8 @@ constexpr int kThreads = 256;
 //
 // A work-group takes p.per tokens and a share of the heads: its threads compute the tokens' sines and cosines once,
 // into LDS, while the first rows are on their way, and turn the heads with them.
-template <typename T>
+// WHOLE: pairs and passing columns come in whole eights.
+template <typename T, bool WHOLE>
 __global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs p) {
     __shared__ float2 cs[kRotaryPairs];
     const int tid = threadIdx.x;
@@ -37,7 +71,7 @@ __global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs p) {
     const int turned = (p.half + 7) >> 3, groups = turned + p.pass;  // pieces of 8 columns (turned: 8 pairs)
     const int items = tokens * heads * groups;
     struct Item {
-        Raw8<T> a, b;
+        Held<T> a, b;
         int t, g;
         int64_t y;
     };
@@ -47,16 +81,17 @@ __global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs p) {
         it.y = (t0 + t) * p.ys + (h0 + h) * p.yh;
         const T *x = static_cast<const T *>(p.x) + (t0 + t) * p.xs + (h0 + h) * p.xh;
         if (g < turned) {
-            const int n = min(8, p.half - 8 * g);
+            const int n = WHOLE ? 8 : min(8, p.half - 8 * g);
             it.a.load(x + 8 * g, n);
             it.b.load(x + p.half + 8 * g, n);
         } else {
             const int c = 2 * p.half + 8 * (g - turned);
-            it.a.load(x + c, min(8, p.dim - c));
+            it.a.load(x + c, WHOLE ? 8 : min(8, p.dim - c));
+            it.b = it.a;
         }
     };
     Item it;
-    if (tid < items) place(it, tid);
+    place(it, min(tid, items - 1));
     for (int e = tid; e < tokens * p.half; e += kThreads) {
         const int t = e / p.half, j = e % p.half;
         int axis = 0;
@@ -73,12 +108,12 @@ __global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs p) {
     __syncthreads();
     for (int i = tid; i < items; i += kThreads) {
         Item next;
-        if (i + kThreads < items) place(next, i + kThreads);
+        place(next, min(i + kThreads, items - 1));
         T *y = static_cast<T *>(p.y) + it.y;
         float a[8], b[8];
         it.a.get(a);
         if (it.g < turned) {
-            const int n = min(8, p.half - 8 * it.g);
+            const int n = WHOLE ? 8 : min(8, p.half - 8 * it.g);
             it.b.get(b);
             float u[8], v[8];
 #pragma unroll
@@ -91,7 +126,7 @@ __global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs p) {
             put8(y + p.half + 8 * it.g, v, n);
         } else {
             const int c = 2 * p.half + 8 * (it.g - turned);
-            put8(y + c, a, min(8, p.dim - c));
+            put8(y + c, a, WHOLE ? 8 : min(8, p.dim - c));
         }
         it = next;
     }
@@ -110,7 +145,7 @@ __global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs p) {
 // of loads length -> page -> scale.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs p) {
-    constexpr int kMost = kPage * kMaxHeadDim / 8 / kThreads;  // pieces of 8 columns of a thread
+    constexpr int kMost = kPage / 4 * kMaxHeadDim / 8 / kThreads;  // pieces, four slots of 8 columns, of a thread
     constexpr int kPitch = kPage + 4;                          // of a column's 64 codes in LDS
     __shared__ uint32_t red[kThreads / 64];
     __shared__ __attribute__((aligned(16))) uint8_t tile[kMaxHeadDim * kPitch];
@@ -138,17 +173,23 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs p) {
     uint8_t *const scale = (values ? p.v_scales : p.k_scales) + at;
     const uint32_t old = slot0 ? *scale : 0u;
 
-    const int items = n * per;
-    Raw8<T> raw[kMost];
+    // Piece e: slots 4 (slot0 / 4 + e / per) .. + 3 as far as they are the call's, columns 8 (e % per) .. + 7.
+    const int quad0 = slot0 / 4, items = ((slot0 + n - 1) / 4 - quad0 + 1) * per;
+    Raw8<T> raw[kMost][4];
     uint32_t top = 0u;
 #pragma unroll
     for (int i = 0; i < kMost; ++i) {
         const int e = tid + i * kThreads;
         if (i * kThreads < items && e < items) {
-            raw[i].load(x + (int64_t)(e / per) * xs + 8 * (e % per), 8);
-            float v[8];
-            raw[i].get(v);
-            top = max(top, amax8(v));
+            const int t = 4 * (quad0 + e / per) - slot0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) raw[i][j].load(x + (int64_t)(t + j) * xs + 8 * (e % per), t + j >= 0 && t + j < n ? 8 : 0);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float v[8];
+                raw[i][j].get(v);
+                top = max(top, amax8(v));
+            }
         }
     }
 #pragma unroll
@@ -194,17 +235,33 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs p) {
     for (int i = 0; i < kMost; ++i) {
         const int e = tid + i * kThreads;
         if (i * kThreads < items && e < items) {
-            float v[8];
-            raw[i].get(v);
-            const uint2 c = mx_encode8(v, sb);
-            const int t = e / per, d = 8 * (e % per);
-            if (!values) {
-                *reinterpret_cast<uint2 *>(codes + (slot0 + t) * dim + d) = c;
-            } else {
-                uint8_t *to = few ? codes + d * kPage + slot0 + t : tile + d * kPitch + slot0 + t;
-                const int step = few ? kPage : kPitch;
+            const int slot = 4 * (quad0 + e / per), d = 8 * (e % per);
+            uint2 c[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k) to[k * step] = (uint8_t)((k < 4 ? c.x : c.y) >> (8 * (k & 3)));
+            for (int j = 0; j < 4; ++j) {
+                float v[8];
+                raw[i][j].get(v);
+                c[j] = mx_encode8(v, sb);
+            }
+            if (!values || few) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (slot + j < slot0 || slot + j >= slot0 + n) continue;
+                    if (!values) {
+                        *reinterpret_cast<uint2 *>(codes + (slot + j) * dim + d) = c[j];
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            codes[(d + k) * kPage + slot + j] = (uint8_t)((k < 4 ? c[j].x : c[j].y) >> (8 * (k & 3)));
+                    }
+                }
+            } else {  // four slots of a column in a dword
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    auto byte_of = [&](int j) { return (k < 4 ? c[j].x : c[j].y) >> (8 * (k & 3)) & 255u; };
+                    *reinterpret_cast<uint32_t *>(tile + (d + k) * kPitch + slot) =
+                        byte_of(0) | byte_of(1) << 8 | byte_of(2) << 16 | byte_of(3) << 24;
+                }
             }
         }
     }
@@ -229,7 +286,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs p) {
 
 hipError_t launch_rotary(const RotaryArgs &a, bool f32, hipStream_t st) {
     RotaryArgs p = a;
-    p.per = (int)std::min<int64_t>(std::max(1, kThreads / std::max(p.half, 1)), 16);
+    p.per = (int)std::min<int64_t>({kRotaryPairs / p.half, 16, std::max<int64_t>(1, p.tokens)});
     const int64_t gx = (p.tokens + p.per - 1) / p.per;
     // Few tokens: their heads go to several work-groups, each with work for all its threads.
     const int64_t items = (int64_t)p.per * p.heads * ((p.half + 7) / 8 + p.pass);
@@ -237,10 +294,12 @@ hipError_t launch_rotary(const RotaryArgs &a, bool f32, hipStream_t st) {
     const int64_t gy = std::max<int64_t>(1, std::min<int64_t>(want, p.heads));
     p.heads_per = (int)((p.heads + gy - 1) / gy);
     const dim3 grid((unsigned)gx, (unsigned)((p.heads + p.heads_per - 1) / p.heads_per));
+    const bool whole = p.half % 8 == 0 && (p.dim - 2 * p.half) % 8 == 0;
+    auto run = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(kThreads), 0, st, p); };
     if (f32)
-        hipLaunchKernelGGL(k_rotary<float>, grid, dim3(kThreads), 0, st, p);
+        run(whole ? k_rotary<float, true> : k_rotary<float, false>);
     else
-        hipLaunchKernelGGL(k_rotary<uint16_t>, grid, dim3(kThreads), 0, st, p);
+        run(whole ? k_rotary<uint16_t, true> : k_rotary<uint16_t, false>);
     return hipGetLastError();
 }
 
