@@ -134,10 +134,13 @@ def _cache(cache, dev):
     """Checks a cache; returns its C form, heads and dim."""
     if not isinstance(cache, (tuple, list)) or len(cache) != 4:
         raise NVFP4Error("the cache must be (k, v, k_scales, v_scales), as kv_cache makes it")
-    for t, dtypes in zip(cache, (_CODES, _CODES, _SCALES, _SCALES)):
-        if not isinstance(t, torch.Tensor) or t.device != dev or t.dtype not in dtypes or not t.is_contiguous():
-            raise NVFP4Error(f"the cache's codes must be contiguous E4M3 and its scales contiguous E8M0 tensors on {dev}")
     k, v, ks, vs = cache
+    at = dev.index
+    if not (isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor) and isinstance(ks, torch.Tensor) and isinstance(vs, torch.Tensor)
+            and k.get_device() == v.get_device() == ks.get_device() == vs.get_device() == at and k.dtype in _CODES and v.dtype in _CODES
+            and ks.dtype in _SCALES and vs.dtype in _SCALES and k.is_contiguous() and v.is_contiguous() and ks.is_contiguous()
+            and vs.is_contiguous()):
+        raise NVFP4Error(f"the cache's codes must be contiguous E4M3 and its scales contiguous E8M0 tensors on {dev}")
     if k.dim() != 4 or k.shape[2] != PAGE:
         raise NVFP4Error(f"the cache's k must be [pages, kv_heads, {PAGE}, dim]")
     pages, heads, _, dim = k.shape
@@ -147,13 +150,13 @@ def _cache(cache, dev):
 
 
 def _ints(t, name, n, dev):
-    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != dev or t.shape != (n,)
+    if (not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.get_device() != dev.index or t.shape != (n,)
             or not t.is_contiguous()):
         raise NVFP4Error(f"{name} must be a contiguous [{n}] int32 tensor on {dev}")
 
 
 def _sequences(table, lengths, starts, tokens, dev):
-    if not isinstance(table, torch.Tensor) or table.dim() != 2 or table.dtype != torch.int32 or table.device != dev:
+    if not isinstance(table, torch.Tensor) or table.dim() != 2 or table.dtype != torch.int32 or table.get_device() != dev.index:
         raise NVFP4Error(f"table must be a [seqs, width] int32 tensor on {dev}")
     seqs, width = table.shape
     ldt, unit = table.stride()
