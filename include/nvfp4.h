@@ -503,7 +503,8 @@ int nvfp4_kv_append(const nvfp4_kv_cache_t *cache, const nvfp4_sequences_t *seqs
  * over the tokens t that a row sees: with causal = 1 row i of a sequence's n rows sees its first length - n + i + 1
  * tokens, with causal = 0 all `length`. A row that sees none gives zeros; one that sees a token of a block with scale byte
  * 255 gives NaN. Products with q are exact, sums fp32, probabilities are rounded to bf16 before they are multiplied with
- * the values. Values of the cache below 2^-126 may count as zero. 1e-30 < |scale| < 1e30. Scratch: nvfp4_attention_workspace_bytes. */
+ * the values. Values of the cache below 2^-126 may count as zero. 1e-30 < |scale| < 1e30;
+ * tokens * (heads / kv_heads)^2 < 2^32. Scratch: nvfp4_attention_workspace_bytes. */
 int nvfp4_attention(const nvfp4_kv_cache_t *cache, const nvfp4_sequences_t *seqs, const void *q, int64_t q_token,
                     int64_t q_head, int heads, int64_t tokens, float scale, int causal, void *out, void *workspace,
                     size_t workspace_bytes, void *stream);

@@ -66,10 +66,27 @@ __device__ __forceinline__ float row_sum(float v) {
     return __uint_as_float(b.x) + __uint_as_float(b.y);
 }
 
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int k = 1; k < 64; k <<= 1) v += __shfl_xor(v, k);
+// row_shr and row_bcast of the rows in MASK; 0 where there is no source.
+template <int CTRL, int MASK>
+__device__ __forceinline__ uint32_t shifted(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, MASK, 0xF, false);
+}
+
+// Inclusive sums over a wave: within rows of 16 lanes, then row 0's over row 1 and row 2's over row 3, then the first
+// half's over the second.
+template <typename T>
+__device__ __forceinline__ T sums_to(T v) {
+    v += __builtin_bit_cast(T, shifted<0x111, 0xF>(__builtin_bit_cast(uint32_t, v)));
+    v += __builtin_bit_cast(T, shifted<0x112, 0xF>(__builtin_bit_cast(uint32_t, v)));
+    v += __builtin_bit_cast(T, shifted<0x114, 0xF>(__builtin_bit_cast(uint32_t, v)));
+    v += __builtin_bit_cast(T, shifted<0x118, 0xF>(__builtin_bit_cast(uint32_t, v)));
+    v += __builtin_bit_cast(T, shifted<0x142, 0xA>(__builtin_bit_cast(uint32_t, v)));
+    v += __builtin_bit_cast(T, shifted<0x143, 0xC>(__builtin_bit_cast(uint32_t, v)));
     return v;
+}
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sums_to(v)), 63));
 }
 
 // e^(a - b) in powers of two, 0 for a = -inf whatever b.
@@ -94,9 +111,15 @@ struct Rows {
     int lim[RT];  // tokens that the lane's row sees (0: no such row)
 };
 
+// The token of a row (among the sequence's new ones): row / group by a multiplication, exact while rows * group stay
+// below 2^32 (a work-group of a short call is bound by the way to its blocks, and divisions are the longest steps on it).
+__device__ __forceinline__ int token_of(const AttnArgs &p, int row) {
+    return p.per_group ? (int)__umulhi((uint32_t)row, p.per_group) : row;
+}
+
 // The tokens that a row sees, more for a later one.
 __device__ __forceinline__ int seen_by(const AttnArgs &p, const Seq &q, int row) {
-    return p.causal ? min(max(q.len - q.n + row / p.group + 1, 0), q.len) : q.len;
+    return p.causal ? min(max(q.len - q.n + token_of(p, row) + 1, 0), q.len) : q.len;
 }
 
 // The lane's rows row0 + 16 r + l % 16 of the sequence: their queries as operands, and what they see.
@@ -105,7 +128,7 @@ __device__ __forceinline__ void take_rows(const AttnArgs &p, const Seq &q, int64
     const int lane = threadIdx.x & 63, r16 = lane & 15, g = lane >> 4;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        const int row = row0 + 16 * r + r16, tok = row / p.group, sub = row % p.group;
+        const int row = row0 + 16 * r + r16, tok = token_of(p, row), sub = row - tok * p.group;
         const bool in = tok < q.n;
         R.lim[r] = !in ? 0 : p.causal ? min(max(q.len - q.n + tok + 1, 0), q.len) : q.len;
         const uint16_t *x = p.q + (int64_t)(q.first + tok) * p.qs + (h * p.group + sub) * p.qh;
@@ -298,7 +321,8 @@ __device__ __forceinline__ void attend(const AttnArgs &p, const Seq &q, int s, i
 }
 
 __device__ __forceinline__ uint16_t *out_row(const AttnArgs &p, const Seq &q, int64_t h, int row) {
-    return p.out + ((int64_t)(q.first + row / p.group) * p.kv_heads * p.group + h * p.group + row % p.group) * p.dim;
+    const int tok = token_of(p, row);
+    return p.out + ((int64_t)(q.first + tok) * p.kv_heads * p.group + h * p.group + (row - tok * p.group)) * p.dim;
 }
 
 // Rows over the waves, for prompts: a work-group takes 64 RT rows of a sequence and head, a wave 16 RT of them, over all
@@ -322,9 +346,9 @@ __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(Att
     // sequence, which see the most, go first.
     const int64_t h = blockIdx.x % p.kv_heads;
     const int piece = p.pieces - 1 - (int)(blockIdx.x / p.kv_heads);
-    const int s = piece_sequence(p.seq, piece, p.group, kRows, 1);
+    const int s = piece_sequence(p.seq, piece, p.group, log2_of(kRows), 1);
     const Seq q = sequence(p.seq, s);
-    const int first = (piece - piece_base(p.seq, s, p.group, kRows, 1)) * kRows;
+    const int first = (piece - piece_base(p.seq, s, p.group, log2_of(kRows), 1)) * kRows;
     if (first >= q.n * p.group || first < 0) return;
     const int row0 = first + 16 * RT * wave, dim = FULL ? 64 * KS : p.dim;
     bf16x8 Q[RT][2 * KS];
@@ -553,20 +577,25 @@ __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(Att
 // share (a piece: blocks of one tile of 16 RT rows of a sequence), its waves taking every fourth block; their results
 // are joined in LDS in wave order. A tile that lies in one share is finished there, else its parts go to scratch and
 // k_attn_join adds them in order of the shares.
+//
+// Where there are at least two work-groups for each tile, a tile's blocks are padded to whole shares in the list, so that no
+// work-group has two pieces, one after the other: short calls are bound by the way through one (16 sequences of 500 to 5000
+// tokens, 21 to 42 rows: 14.3 -> 11.8 us).
 struct Share {
     uint32_t total, groups;  // blocks of the head's list; work-groups that share them
-    __device__ __forceinline__ uint32_t begin(uint32_t j) const { return (uint32_t)((uint64_t)j * total / groups); }
-    __device__ __forceinline__ uint32_t owner(uint32_t u) const { return (uint32_t)(((uint64_t)(u + 1) * groups - 1) / total); }
+    uint32_t unit, more;     // blocks of a share; the first `more` shares have one more
+    __device__ __forceinline__ uint32_t begin(uint32_t j) const { return j * unit + min(j, more); }
+    __device__ __forceinline__ uint32_t owner(uint32_t u) const {
+        const uint32_t longer = more * (unit + 1u);
+        return u < longer ? u / (unit + 1u) : more + (u - longer) / unit;
+    }
+    // of a tile's blocks in the list
+    bool whole;
+    __device__ __forceinline__ uint32_t padded(uint32_t blocks) const { return whole ? (blocks + unit - 1) / unit * unit : blocks; }
 };
 
-__device__ __forceinline__ int tiles_of(const AttnArgs &p, const Seq &q, int size) { return (q.n * p.group + size - 1) / size; }
+__device__ __forceinline__ int tiles_of(const AttnArgs &p, const Seq &q, int size) { return (q.n * p.group + size - 1) >> log2_of(size); }
 __device__ __forceinline__ int blocks_of(const Seq &q) { return (q.len + kPage - 1) / kPage; }
-
-// row_shr and row_bcast of the rows in MASK; 0 where there is no source.
-template <int CTRL, int MASK>
-__device__ __forceinline__ uint32_t shifted(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, MASK, 0xF, false);
-}
 
 // 64 sequences, one a lane, with the blocks (of all their tiles) in front of them in the list. By whole waves.
 struct Window {
@@ -580,14 +609,7 @@ struct Window {
             q = sequence(p.seq, s0 + lane);
             mine = (uint32_t)(tiles_of(p, q, size) * blocks_of(q));
         }
-        // inclusive sums: within rows of 16 lanes, then row 0's over row 1 and row 2's over row 3, then the first half's
-        upto = mine;
-        upto += shifted<0x111, 0xF>(upto);
-        upto += shifted<0x112, 0xF>(upto);
-        upto += shifted<0x114, 0xF>(upto);
-        upto += shifted<0x118, 0xF>(upto);
-        upto += shifted<0x142, 0xA>(upto);
-        upto += shifted<0x143, 0xC>(upto);
+        upto = sums_to(mine);
     }
     __device__ __forceinline__ uint32_t total() const { return before + (uint32_t)__builtin_amdgcn_readlane((int)upto, 63); }
     __device__ __forceinline__ Seq seq(int s) const {
@@ -610,13 +632,29 @@ __device__ __forceinline__ uint32_t list_total(const AttnArgs &p, int size, Wind
     return sum;
 }
 
-__device__ __forceinline__ Share share_of(const AttnArgs &p, uint32_t total) {
+// The shares, and the first window of the list as they are cut.
+__device__ __forceinline__ Share share_of(const AttnArgs &p, int size, Window &w) {
     Share sh;
-    sh.total = total;
-    // Not less than a block for each wave of a work-group. Long shares go to half as many work-groups, one a CU: parts
-    // and pieces are fewer (64 sequences of 300 to 16000 tokens: 110 -> 99 us), where short ones lack loads in flight.
-    sh.groups = max(1u, min((uint32_t)p.groups, (total + kWaves - 1) / kWaves));
-    if (total >= (uint32_t)p.groups * (kWaves * 8u)) sh.groups = ((uint32_t)p.groups + 1u) / 2u;
+    sh.total = list_total(p, size, w), sh.whole = false, sh.more = 0u;
+    // Long shares go to half as many work-groups, one a CU: parts and pieces are fewer (64 sequences of 300 to 16000 tokens:
+    // 110 -> 98 us), where short ones lack loads in flight.
+    uint32_t groups = (uint32_t)p.groups;
+    if (sh.total >= groups * (kWaves * 8u)) groups = (groups + 1u) / 2u;
+    if (p.seq.seqs > 1 && p.seq.seqs <= 64) {
+        const bool any = w.mine != 0u;
+        const uint32_t tiles = wave_sum(any ? (uint32_t)tiles_of(p, w.q, size) : 0u);
+        if (tiles > 1u && 2u * tiles <= groups) {
+            const uint32_t least = (sh.total + groups - tiles - 1u) / (groups - tiles);
+            sh.unit = (least + kWaves - 1u) / kWaves * kWaves, sh.whole = true;  // a block for each wave
+            if (any) w.mine = (uint32_t)tiles_of(p, w.q, size) * sh.padded((uint32_t)blocks_of(w.q));
+            w.upto = sums_to(w.mine);
+            sh.total = w.total(), sh.groups = groups;  // (of which the last may have none)
+            return sh;
+        }
+    }
+    // Not less than a block for each wave of a work-group.
+    sh.groups = max(1u, min(groups, (sh.total + kWaves - 1) / kWaves));
+    sh.unit = sh.total / sh.groups, sh.more = sh.total - sh.unit * sh.groups;
     return sh;
 }
 
@@ -638,22 +676,22 @@ __global__ __launch_bounds__(kAttnThreads, RT * KS <= 2 ? 2 : 1) void k_attn_spl
     const int64_t h = blockIdx.x % p.kv_heads;
     const uint32_t j = blockIdx.x / p.kv_heads;
     Window w;
-    const Share sh = share_of(p, list_total(p, kRows, w));
+    const Share sh = share_of(p, kRows, w);
     if (j >= sh.groups || sh.total == 0u) return;
     uint32_t u = sh.begin(j);
-    const uint32_t end = sh.begin(j + 1);
+    const uint32_t end = min(sh.begin(j + 1), sh.total);
     while (u < end) {
         while (u >= w.total()) w.load(p, kRows, w.s0 + 64, w.total());
         const int s = w.s0 + __ffsll((unsigned long long)__ballot(w.before + w.upto > u)) - 1;
         const Seq q = w.seq(s);
-        const uint32_t nb = (uint32_t)blocks_of(q), at = w.begin(s);
-        const int tile = (int)((u - at) / nb), b0 = (int)((u - at) % nb), b1 = (int)min(nb, b0 + (end - u));
-        u += b1 - b0;
+        const uint32_t nb = (uint32_t)blocks_of(q), in_list = sh.padded(nb), at = w.begin(s);
+        const int tile = (int)((u - at) / in_list), b0 = (int)((u - at) % in_list), b1 = (int)min(nb, b0 + (end - u));
+        u += min(in_list - b0, end - u);
         const int row0 = tile * kRows, rows = min(kRows, q.n * p.group - row0);
         Rows<KS, RT> R;
         attend<KS, RT, FULL>(p, q, s, h, row0, b0 + wave, b1, kWaves, R, lds + wave * kWaveLds<KS>);
         const bool whole = b0 == 0 && b1 == (int)nb;
-        const int64_t place = part_place(p, h, j, piece_base(p.seq, s, p.group, kRows, 1) + tile);
+        const int64_t place = part_place(p, h, j, piece_base(p.seq, s, p.group, log2_of(kRows), 1) + tile);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
             const float l = row_sum(R.l[r]);
@@ -714,11 +752,11 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_join(AttnArgs p, int size
     const int turn = TOGETHER ? wave : 0;
     if (row >= size) return;
     Window w;
-    const uint32_t total = list_total(p, size, w);
-    const int s = piece_sequence(p.seq, piece, p.group, size, 1);
+    const Share sh = share_of(p, size, w);
+    const int s = piece_sequence(p.seq, piece, p.group, log2_of(size), 1);
     while (s >= w.s0 + 64) w.load(p, size, w.s0 + 64, w.total());
     const Seq q = w.seq(s);
-    const int tile = piece - piece_base(p.seq, s, p.group, size, 1);
+    const int tile = piece - piece_base(p.seq, s, p.group, log2_of(size), 1);
     if (tile < 0 || tile >= tiles_of(p, q, size) || tile * size + row >= q.n * p.group) return;
     uint16_t *o = out_row(p, q, h, tile * size + row);
     const int c = 4 * lane;
@@ -730,8 +768,7 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_join(AttnArgs p, int size
     int parts = p.parts;  // of k_attn_rows: all tiles alike
     int64_t at = (h * p.pieces + piece) * p.parts * size + row;
     if (parts == 0) {
-        const Share sh = share_of(p, total);
-        const uint32_t u0 = w.begin(s) + (uint32_t)tile * nb;
+        const uint32_t u0 = w.begin(s) + (uint32_t)tile * sh.padded(nb);
         const uint32_t j0 = sh.owner(u0), j1 = sh.owner(u0 + nb - 1);
         if (j0 == j1) return;
         parts = (int)(j1 - j0 + 1);
@@ -834,6 +871,7 @@ hipError_t launch_attention(const AttnArgs &a, void *ws, hipStream_t st) {
     AttnArgs p = a;
     const AttnPlan plan = plan_attention(p.seq.tokens, p.seq.seqs, p.seq.width, p.kv_heads, p.group, p.dim);
     p.pieces = (int)plan.pieces, p.groups = plan.groups, p.parts = plan.parts;
+    p.per_group = p.group == 1 ? 0u : (uint32_t)(((uint64_t)1 << 32) / (uint32_t)p.group + 1u);
     p.part = static_cast<float *>(ws);
     p.part_ml = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + plan.part_bytes);
     // The sizes most heads have, and forms for any other.

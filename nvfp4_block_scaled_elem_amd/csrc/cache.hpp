@@ -45,18 +45,19 @@ __device__ __forceinline__ int page_of(const SeqArgs &a, int s, int block) {
 // The pieces of `size` rows that a call's sequences are cut into, numbered: those of sequence s, of rows_per rows a
 // token, begin at base(s) = floor(first rows_per / size) + extra s. floor(a + b) + 1 >= floor(a) + ceil(b), so with extra
 // = 1 no two pieces share a number, and no number reaches piece_bound; extra = 2 leaves room for one piece more per
-// sequence. Some numbers have no piece.
-__device__ __forceinline__ int piece_base(const SeqArgs &a, int s, int rows_per, int size, int extra) {
+// sequence. Some numbers have no piece. size = 2^log2.
+__device__ __forceinline__ int log2_of(int size) { return __ffs(size) - 1; }
+__device__ __forceinline__ int piece_base(const SeqArgs &a, int s, int rows_per, int log2, int extra) {
     const int first = a.starts ? min(max(a.starts[s], 0), a.tokens) : s;
-    return (int)((int64_t)first * rows_per / size) + extra * s;
+    return (int)((uint64_t)first * (uint32_t)rows_per >> log2) + extra * s;
 }
 
 // The last sequence whose base is not past `piece` (the bases ascend). Called by whole waves, all lanes alike.
-__device__ __forceinline__ int piece_sequence(const SeqArgs &a, int piece, int rows_per, int size, int extra) {
+__device__ __forceinline__ int piece_sequence(const SeqArgs &a, int piece, int rows_per, int log2, int extra) {
     const int lane = threadIdx.x & 63;
     int s = 0;
     for (int s0 = 0; s0 < a.seqs; s0 += 64) {
-        const bool in = s0 + lane < a.seqs && piece_base(a, s0 + lane, rows_per, size, extra) <= piece;
+        const bool in = s0 + lane < a.seqs && piece_base(a, s0 + lane, rows_per, log2, extra) <= piece;
         const int n = __popcll(__ballot(in));
         if (n) s = s0 + n - 1;
         if (n < 64) break;

@@ -154,8 +154,8 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs p) {
     const bool values = blockIdx.z != 0;
     int s = blockIdx.x, nth = 0;
     if (p.seq.starts) {
-        s = piece_sequence(p.seq, blockIdx.x, 1, kPage, 2);
-        nth = (int)blockIdx.x - piece_base(p.seq, s, 1, kPage, 2);
+        s = piece_sequence(p.seq, blockIdx.x, 1, log2_of(kPage), 2);
+        nth = (int)blockIdx.x - piece_base(p.seq, s, 1, log2_of(kPage), 2);
     }
     const Seq q = sequence(p.seq, s);
     const int begin = max(q.len - q.n, 0);  // the first new token's place; more new tokens than tokens: the first are left out

@@ -53,7 +53,10 @@ int check_plan(int64_t tokens, int seqs, int w, int heads, int kv_heads, int dim
         return NVFP4_ERR_INVALID_ARG;
     if (heads > kMaxHeads || dim % 16 != 0 || dim > nvfp4::kMaxHeadDim || tokens > kMaxTokens || seqs > kMaxTokens)
         return NVFP4_ERR_SHAPE;
-    const nvfp4::AttnPlan plan = nvfp4::plan_attention(tokens, seqs, w, kv_heads, heads / kv_heads, dim);
+    // a row's token by a multiplication of 32 bits
+    const int64_t group = heads / kv_heads;
+    if (tokens * group * group >= ((int64_t)1 << 32)) return NVFP4_ERR_SHAPE;
+    const nvfp4::AttnPlan plan = nvfp4::plan_attention(tokens, seqs, w, kv_heads, (int)group, dim);
     if (plan.pieces * kv_heads >= kMaxGroups || plan.pieces * (int64_t)w >= ((int64_t)1 << 31)) return NVFP4_ERR_SHAPE;
     return NVFP4_OK;
 }

@@ -233,6 +233,7 @@ struct AttnArgs {
     uint32_t flip;          // of two bf16: the signs, for a negative factor
     int kv_heads, group, dim, causal;
     int pieces, groups, parts;  // set by the launcher
+    uint32_t per_group;         // 2^32 / group rounded up, 0 for 1
 };
 struct AttnPlan {
     bool rows;       // rows over the waves; else blocks over the work-groups
