@@ -524,16 +524,17 @@ __global__ __launch_bounds__(kDownThreads) void k_moe_down(MoeArgs p) {
 // Many rows: a wave owns 32 weight rows (gated: 16 gate rows and their 16 up rows) over the whole sum, and a work-group's
 // four waves share the tokens' values, which go through LDS in slices of 512 k in the order of the operand. A wave's codes
 // and scales of a slice are all in flight while the slice before is multiplied: 9 KB a wave, no barrier waits for them.
-// MOST: tiles of 16 pairs at a time. SECOND: the product with W2, its sum cut into p.split parts of slices, else with W1. HOLD: X
-// is at most two slices and stays where it is while the work-group goes through several column tiles, without a barrier.
+// MOST: tiles of 16 pairs at a time. SECOND: the product with W2, its sum cut into p.split parts of slices, else with W1. HOLD (2 or
+// 4, 0: not): X is at most so many slices and stays where it is while the work-group goes through several column tiles, without
+// a barrier (150 tokens, 2048 columns: the layer 97 us, 103 with one tile a work-group).
 constexpr int kRowWaves = 4, kRowThreads = 64 * kRowWaves, kSlice = 512, kSliceChunks = kSlice / kChunk;
 constexpr int kWaveCodes = 2 * (1024 + 512);  // LDS bytes of a wave: a chunk's codes and a slice's scales of two tiles
 
-template <int NT, int MOST, bool SECOND, bool HOLD>
+template <int NT, int MOST, bool SECOND, int HOLD>
 __global__ __launch_bounds__(kRowThreads, 2) void k_moe_rows(MoeArgs p, int tiles, int groups) {
     constexpr int kXBytes = 16 * MOST * kSlice * 2;  // of a slice
     constexpr int kCols = NT == 2 ? 16 * kRowWaves : 32 * kRowWaves;
-    __shared__ __attribute__((aligned(16))) uint8_t lds_x[2][kXBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t lds_x[HOLD > 2 ? HOLD : 2][kXBytes];
     __shared__ __attribute__((aligned(16))) uint8_t lds_w[kRowWaves][kWaveCodes];
     __shared__ __attribute__((aligned(4))) uint8_t seen[kMoeMaxExperts];
     extern __shared__ uint16_t list[];  // an expert's pairs: as many as tokens at most
@@ -713,9 +714,9 @@ __global__ __launch_bounds__(kRowThreads, 2) void k_moe_rows(MoeArgs p, int tile
         for (int c = 0; c < kSliceChunks; ++c) load_codes(s_lo, c);
         if (HOLD) {
             store_x(s_lo, lds_x[0]);
-            if (s_hi - s_lo > 1) {
-                load_x(s_lo + 1);
-                store_x(s_lo + 1, lds_x[1]);
+            for (int s = s_lo + 1; s < s_hi; ++s) {
+                load_x(s);
+                store_x(s, lds_x[s - s_lo]);
             }
             lds_barrier();
 #pragma unroll 1
@@ -798,8 +799,8 @@ Plan plan_moe(int64_t tokens, int64_t width, int64_t inner, int experts, int top
         const int64_t slices = (inner + kSlice - 1) / kSlice;
         while (plan.split < 8 && 4 * plan.split <= slices && used * down * plan.split < 500) plan.split *= 2;
     }
-    // Three work-groups a CU, where X stays.
-    plan.up_turns = width <= 2 * kSlice ? (int)std::max(1.0, used * up / 768.0 + 0.5) : 1;
+    // Where X stays: two or three work-groups a CU, as many as there is LDS for.
+    plan.up_turns = width <= (plan.mt == 1 ? 4 : 2) * kSlice ? (int)std::max(1.0, used * up / 512.0 + 0.5) : 1;
     plan.down_turns = inner <= 2 * kSlice ? (int)std::max(1.0, used * down / 768.0 + 0.5) : 1;
     return plan;
 }
@@ -827,10 +828,15 @@ void product(const MoeArgs &p, int64_t chosen, bool by_rows, bool apart, int mt,
     };
     using One = std::integral_constant<int, 1>;
     using Two = std::integral_constant<int, 2>;
-    if (turns > 1)
-        mt == 1 ? run(One{}, std::true_type{}) : run(Two{}, std::true_type{});
+    using H2 = std::integral_constant<int, 2>;
+    using H4 = std::integral_constant<int, 4>;
+    const int64_t slices = ((SECOND ? p.inner : p.width) + kSlice - 1) / kSlice;
+    if (turns > 1 && slices > 2)
+        run(One{}, H4{});
+    else if (turns > 1)
+        mt == 1 ? run(One{}, H2{}) : run(Two{}, H2{});
     else
-        mt == 1 ? run(One{}, std::false_type{}) : run(Two{}, std::false_type{});
+        mt == 1 ? run(One{}, std::integral_constant<int, 0>{}) : run(Two{}, std::integral_constant<int, 0>{});
 }
 
 }  // namespace
