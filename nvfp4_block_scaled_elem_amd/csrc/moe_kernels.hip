@@ -6,14 +6,16 @@
 //     y[t] = residual[t] + sum_j w_j alpha2_e (W2_e h_j),  h_j = act(alpha1_e W1_e x_t)
 // (gated: act of the first `inner` rows of W1_e x times the others). Weights are those of the product kernels, e2m1(code)
 // e4m3(scale), exact in bf16; x is bf16; sums are fp32 on the matrix cores; h is rounded to bf16, which the second
-// product takes (its error, 2^-9 of a term, is of the size of y's own rounding).
+// product takes (its error, at most 2^-8 of a term and independent between terms, is of the size of y's own rounding: together
+// 0.0023 of y's norm, y's own 0.0017), or, for few tokens, kept in two bf16 parts.
 //
-// Bound by reading the chosen experts' weights, each once however many tokens chose it.
-//   k_moe_route: experts and weights of each token.
-//   k_moe_product, twice: a work-group has 16 weight rows (gated: 16 gate rows and their 16 up rows) of one chosen
-//     expert and the pairs (token, choice) that chose it, 16 at a time as the columns of v_mfma_f32_16x16x32_bf16; its waves
-//     split the sum and are joined through LDS in wave order.
-//   k_moe_sum: y from the pairs' parts.
+// Bound by reading the chosen experts' weights, each once however many tokens chose it; a pair is a token and one of its
+// choices, and the pairs of an expert are the columns of v_mfma_f32_16x16x32_bf16, 16 at a time.
+//   k_moe_route: experts and weights of each token; to eight tokens the first product finds them itself.
+//   first product: k_moe_product (a work-group has 16 weight rows, its waves split the sum) where there is little work,
+//     else k_moe_rows (a wave has 32 weight rows);
+//   second product: k_moe_down, the weighted sum over the experts in it, to 16 tokens and little work; else k_moe_rows or
+//     k_moe_product, and k_moe_sum.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -33,6 +35,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
+constexpr int kRouteTokens = 8;  // to so many tokens are routed inside the first product
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------------------------------------- routing
@@ -242,8 +245,24 @@ struct Pick {
     }
 };
 
-// NT: 2 if gated. SECOND: the product with W2, else with W1. ROUTE: to eight tokens, whose experts every work-group finds by
-// itself, a wave a token (a launch saved); the first one writes them down.
+// The experts of a few tokens into `ids` (LDS), a wave a token at a time, by every work-group for itself: a launch saved. The
+// first one writes them down for the kernels after it.
+template <int WAVES>
+__device__ __forceinline__ void route_here(const MoeArgs &p, int most, bool write, int *ids) {
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    for (int t = wave; t < (int)p.tokens; t += WAVES) {
+        int id;
+        float w;
+        route(p, t, most, id, w);
+        if (lane < p.top_k) {
+            ids[t * p.top_k + lane] = id;
+            if (write) p.ids[t * p.top_k + lane] = id, p.weights[t * p.top_k + lane] = w;
+        }
+    }
+    __syncthreads();
+}
+
+// NT: 2 if gated. SECOND: the product with W2, else with W1. ROUTE: to eight tokens, whose experts are found here.
 template <int NT, bool SECOND, bool ROUTE>
 __global__ __launch_bounds__(kThreads) void k_moe_product(MoeArgs p, int tiles) {
     constexpr int kStage = kWaves * NT * kChunkLds, kSums = kWaves * NT * 1024;
@@ -251,22 +270,11 @@ __global__ __launch_bounds__(kThreads) void k_moe_product(MoeArgs p, int tiles) 
     __shared__ __attribute__((aligned(4))) uint8_t seen[kMoeMaxExperts];
     extern __shared__ uint16_t list[];  // an expert's pairs: as many as tokens at most
     __shared__ int count;
-    __shared__ int route_ids[ROUTE ? kWaves * kMoeMaxTopK : 1];
+    __shared__ int route_ids[ROUTE ? kRouteTokens * kMoeMaxTopK : 1];
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    if (ROUTE) {
-        if (wave < p.tokens) {
-            int id;
-            float w;
-            // (one token: this work-group's expert is choice blockIdx.x / tiles, and those after it are not needed)
-            route(p, wave, p.tokens == 1 && blockIdx.x ? (int)blockIdx.x / tiles + 1 : p.top_k, id, w);
-            if (lane < p.top_k) {
-                route_ids[wave * p.top_k + lane] = id;
-                if (blockIdx.x == 0) p.ids[wave * p.top_k + lane] = id, p.weights[wave * p.top_k + lane] = w;
-            }
-        }
-        __syncthreads();
-    }
+    // (one token: this work-group's expert is choice blockIdx.x / tiles, and those after it are not needed)
+    if (ROUTE) route_here<kWaves>(p, p.tokens == 1 && blockIdx.x ? (int)blockIdx.x / tiles + 1 : p.top_k, blockIdx.x == 0, route_ids);
     const int *const ids = ROUTE ? route_ids : p.ids;
     Pick<kThreads> pick;
     const int expert = pick.find(p, ids, blockIdx.x / tiles, seen, &count);
@@ -526,11 +534,11 @@ __global__ __launch_bounds__(kDownThreads) void k_moe_down(MoeArgs p) {
 // and scales of a slice are all in flight while the slice before is multiplied: 9 KB a wave, no barrier waits for them.
 // MOST: tiles of 16 pairs at a time. SECOND: the product with W2, its sum cut into p.split parts of slices, else with W1. HOLD (2 or
 // 4, 0: not): X is at most so many slices and stays where it is while the work-group goes through several column tiles, without
-// a barrier (150 tokens, 2048 columns: the layer 97 us, 103 with one tile a work-group).
+// a barrier (150 tokens, 2048 columns: the layer 97 us, 103 with one tile a work-group). ROUTE: as above.
 constexpr int kRowWaves = 4, kRowThreads = 64 * kRowWaves, kSlice = 512, kSliceChunks = kSlice / kChunk;
 constexpr int kWaveCodes = 2 * (1024 + 512);  // LDS bytes of a wave: a chunk's codes and a slice's scales of two tiles
 
-template <int NT, int MOST, bool SECOND, int HOLD>
+template <int NT, int MOST, bool SECOND, int HOLD, bool ROUTE>
 __global__ __launch_bounds__(kRowThreads, 2) void k_moe_rows(MoeArgs p, int tiles, int groups) {
     constexpr int kXBytes = 16 * MOST * kSlice * 2;  // of a slice
     constexpr int kCols = NT == 2 ? 16 * kRowWaves : 32 * kRowWaves;
@@ -541,10 +549,13 @@ __global__ __launch_bounds__(kRowThreads, 2) void k_moe_rows(MoeArgs p, int tile
     __shared__ int count;
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    __shared__ int route_ids[ROUTE ? kRouteTokens * kMoeMaxTopK : 1];
+    if (ROUTE) route_here<kRowWaves>(p, p.top_k, blockIdx.x == 0, route_ids);
+    const int *const ids = ROUTE ? route_ids : p.ids;
     Pick<kRowThreads> pick;
-    const int expert = pick.find(p, p.ids, blockIdx.x / groups, seen, &count);
+    const int expert = pick.find(p, ids, blockIdx.x / groups, seen, &count);
     if (expert < 0) return;
-    pick.fill(p, p.ids, blockIdx.x / groups, list, &count);
+    pick.fill(p, ids, blockIdx.x / groups, list, &count);
     const int K = (int)(SECOND ? p.inner : p.width), F = (int)(SECOND ? p.width : p.inner);
     // The work-group's column tiles: first, first + groups, ...
     const int first = (int)(blockIdx.x % groups), turns = HOLD ? (tiles - first + groups - 1) / groups : 1;
@@ -788,12 +799,17 @@ Plan plan_moe(int64_t tokens, int64_t width, int64_t inner, int experts, int top
     for (int64_t t = 0; t < tokens && idle > 1e-3; ++t) idle *= 1.0 - (double)top_k / experts;
     const double used = experts * (1.0 - idle);
     Plan plan = {};
-    plan.mt = tokens * top_k > 12 * used ? 2 : 1;  // pairs of an expert
+    plan.mt = tokens > 16 && tokens * top_k > 12 * used ? 2 : 1;  // pairs of an expert
     const int64_t up = (inner + (gated ? 63 : 127)) / (gated ? 64 : 128), down = (width + 127) / 128;
+    // k_moe_rows where there are work-groups for most of the GPU. One token, 8 experts of 2048 x 768 (96 work-groups): the layer
+    // 26 us with it, 20 without; 8 tokens, 35 experts of 4096 x 1408 (770): the first product 47 us, 65 without.
     plan.up_rows = width >= kChunk && used * up >= 192;
+    // The same for the second product; where k_moe_down does the sum as well, from more work on: the latter layer (1120
+    // work-groups) 90 us, 102 with k_moe_down; the former (128) 21, 18 with it.
     plan.down_rows = inner >= kChunk && used * down >= (tokens <= kDownTokens ? 512 : 128);
-    plan.route = tokens > kWaves || plan.up_rows;
+    plan.route = tokens > kRouteTokens || (plan.up_rows && plan.mt == 2);
     plan.down_sum = tokens <= kDownTokens && !plan.down_rows;
+    // Parts of the second product's sum, to some 500 work-groups: 33 tokens, 8 experts of 4096 x 14336: 188 us in two, 197 in four.
     plan.split = 1;
     if (plan.down_rows) {
         const int64_t slices = (inner + kSlice - 1) / kSlice;
@@ -823,20 +839,25 @@ void product(const MoeArgs &p, int64_t chosen, bool by_rows, bool apart, int mt,
     constexpr int kCols = NT == 2 ? 16 * kRowWaves : 32 * kRowWaves;
     const int tiles = (int)((F + kCols - 1) / kCols), groups = (tiles + turns - 1) / turns;
     const dim3 grid((unsigned)(chosen * groups), SECOND ? p.split : 1), block(kRowThreads);
-    auto run = [&](auto mts, auto hold) {
-        hipLaunchKernelGGL((k_moe_rows<NT, mts.value, SECOND, hold.value>), grid, block, list, st, p, tiles, groups);
+    auto run = [&](auto mts, auto hold, auto route) {
+        hipLaunchKernelGGL((k_moe_rows<NT, mts.value, SECOND, hold.value, route.value>), grid, block, list, st, p, tiles, groups);
     };
-    using One = std::integral_constant<int, 1>;
-    using Two = std::integral_constant<int, 2>;
-    using H2 = std::integral_constant<int, 2>;
-    using H4 = std::integral_constant<int, 4>;
+    auto held = [&](auto mts, auto hold) {
+        if constexpr (SECOND || mts.value > 1)
+            run(mts, hold, std::false_type{});
+        else
+            apart ? run(mts, hold, std::false_type{}) : run(mts, hold, std::true_type{});
+    };
+    using std::integral_constant;
     const int64_t slices = ((SECOND ? p.inner : p.width) + kSlice - 1) / kSlice;
-    if (turns > 1 && slices > 2)
-        run(One{}, H4{});
+    if (mt == 2)
+        turns > 1 ? held(integral_constant<int, 2>{}, integral_constant<int, 2>{}) : held(integral_constant<int, 2>{}, integral_constant<int, 0>{});
+    else if (turns > 1 && slices > 2)
+        held(integral_constant<int, 1>{}, integral_constant<int, 4>{});
     else if (turns > 1)
-        mt == 1 ? run(One{}, H2{}) : run(Two{}, H2{});
+        held(integral_constant<int, 1>{}, integral_constant<int, 2>{});
     else
-        mt == 1 ? run(One{}, std::integral_constant<int, 0>{}) : run(Two{}, std::integral_constant<int, 0>{});
+        held(integral_constant<int, 1>{}, integral_constant<int, 0>{});
 }
 
 }  // namespace

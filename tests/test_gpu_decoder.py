@@ -298,6 +298,52 @@ def test_attention_of_prompts(lengths, new, heads, kv_heads, dim):
         check(o, want, err)
 
 
+# Some tens to hundreds of rows: rows over the waves with the blocks in parts, for each head size compiled for, 64 and 128
+# rows a work-group, tables far wider than the sequences
+PARTS = [([3000], [40], 4, 1, 128), ([2100, 65, 5000], [12, 9, 20], 8, 2, 64), ([1999], [300], 6, 3, 80), ([4444, 10], [33, 10], 3, 1, 256),
+         ([2500, 0, 700], [50, 0, 50], 5, 1, 176), ([6000], [70], 17, 1, 48)]
+
+
+@pytest.mark.parametrize("lengths,new,heads,kv_heads,dim", PARTS)
+def test_attention_in_parts(lengths, new, heads, kv_heads, dim):
+    say(f"parts {lengths} {new} {heads} {kv_heads} {dim}")
+    table, pages = layout(6, lengths, width=160)
+    cache = nv.kv_cache(pages, kv_heads, dim)
+    fill(cache, 6)
+    sp = spans(lengths, new)
+    q = rand(3, sum(new), heads, dim)
+    args = (q, cache, table, ints(lengths), starts_of(sp))
+    ws = torch.full((nv.attention_workspace_bytes(sum(new), len(new), table.shape[1], heads, kv_heads, dim),), 0xFF,
+                    dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 0
+    for causal in (True, False):
+        o = nv.attention(*args, causal=causal, workspace=ws)
+        want, err = dref.attention(q, cache, table, sp, dim ** -0.5, causal)
+        check(o, want, err)
+        assert torch.equal(nv.attention(*args, causal=causal), o)
+    u8(cache.v_scales)[int(table[0, 20]), 0] = 255
+    u8(cache.v)[int(table[0, 20]), 0] = 0x7F
+    table[0, 5] = -1
+    o = nv.attention(*args)
+    want, err = dref.attention(q, cache, table, sp, dim ** -0.5, True)
+    assert torch.isnan(want).any()
+    check(o, want, err)
+
+
+# Tiles that end inside a work-group's share, and shares of several tiles: few and many sequences
+@pytest.mark.parametrize("seqs", [2, 5, 16, 33, 64, 65, 300])
+def test_attention_shares(seqs):
+    lengths = [1 + (i * 977) % 2900 for i in range(seqs)]
+    new = [1 + (i * 5) % 4 for i in range(seqs)]
+    lengths = [max(a, b) for a, b in zip(lengths, new)]
+    cache, table = ready(8, lengths, 1, 64)
+    sp = spans(lengths, new)
+    q = rand(3, sum(new), 7, 64)
+    o = nv.attention(q, cache, table, ints(lengths), starts_of(sp))
+    want, err = dref.attention(q, cache, table, sp, 64 ** -0.5, True)
+    check(o, want, err)
+
+
 def test_attention_of_many_sequences():
     """More sequences than a wave has lanes, of very different lengths."""
     lengths = [(i * 37) % 150 for i in range(200)] + [3000]

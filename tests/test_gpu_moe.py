@@ -62,6 +62,27 @@ def test_moe_matches_binary64(tokens, count, top_k, width, inner):
         check(y, want, err)
 
 
+# The forms of the kernel for many weight rows: routing inside it (5 and 8 tokens), X of two and of four slices held over
+# column tiles, whole and with a short last slice, two tiles of pairs with a last one of either, the second product's sum in
+# parts; a last column tile that is not whole
+FORMS = [(5, 32, 4, 512, 1040), (8, 64, 6, 1040, 1408), (40, 64, 4, 2048, 1024), (40, 64, 4, 1040, 1040), (40, 64, 4, 2576, 784),
+         (40, 64, 4, 1024, 2064), (100, 4, 2, 528, 3200), (70, 4, 2, 4112, 2064), (33, 8, 2, 4096, 2064), (40, 4, 1, 4096, 4112),
+         (17, 8, 2, 4096, 8208), (16, 8, 2, 4096, 2064)]
+
+
+@pytest.mark.parametrize("tokens,count,top_k,width,inner", FORMS)
+def test_moe_of_many_rows(tokens, count, top_k, width, inner):
+    say(f"moe rows tokens={tokens} experts={count} top_k={top_k} width={width} inner={inner}")
+    x, logits, r = rand(1, tokens, width), rand(2, tokens, count, dtype=F32, std=2.0), rand(3, tokens, width)
+    logits[0, :] = -INF  # a token of no experts
+    logits[-1, 1:] = -INF  # and one of a single one
+    for gated in (True, False):
+        up, down = layer(7, count, width, inner, gated)
+        y = nv.moe(x, logits, up, down, top_k, gated=gated, residual=r)
+        want, err = dref.moe(x, logits, up, down, top_k, "silu", gated, False, True, r)
+        check(y, want, err)
+
+
 # more rows, wide sums, and weights as the quantiser writes them
 @pytest.mark.parametrize("tokens,count,top_k,width,inner", [(1, 4, 2, 4096, 1408), (6, 8, 2, 2048, 5632), (70, 12, 4, 1024, 4112)])
 def test_moe_of_quantised_weights(tokens, count, top_k, width, inner):
