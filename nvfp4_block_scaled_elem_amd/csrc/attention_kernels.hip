@@ -480,6 +480,11 @@ __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(Att
         const int t0 = b * kPage;
         f32x4 S[RT][4];
         scores(b, S);
+        store_k(b + 1);
+        store_v(b + 1);
+        const int next_live = kb.live;
+        load_k(b + 2);
+        load_v();
         if (t0 + kPage > safe || !live) {
 #pragma unroll
             for (int r = 0; r < RT; ++r)
@@ -540,11 +545,7 @@ __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(Att
 #pragma unroll
                 for (int r = 0; r < RT; ++r) R.o[r][d] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, P[r][u], R.o[r][d], 0, 0, 0);
             }
-        store_k(b + 1);
-        store_v(b + 1);
-        live = kb.live;
-        load_k(b + 2);
-        load_v();
+        live = next_live;
         lds_barrier();
     }
 #pragma unroll
