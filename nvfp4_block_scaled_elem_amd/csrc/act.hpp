@@ -1,4 +1,4 @@
-// Device-side helpers that the product kernels share: barriers that order LDS alone, and activations.
+// Device-side helpers that the kernels share: barriers that order LDS alone, sums over a wave, and activations.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -22,6 +22,31 @@ __device__ __forceinline__ void wave_handover() {
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
     __builtin_amdgcn_wave_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
+// ------------------------------------------------------------------------------------- sums over a wave
+
+// row_shr and row_bcast of the rows in MASK; 0 where there is no source.
+template <int CTRL, int MASK>
+__device__ __forceinline__ uint32_t shifted(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, MASK, 0xF, false);
+}
+
+// Inclusive sums over a wave: within rows of 16 lanes, then row 0's over row 1 and row 2's over row 3, then the first
+// half's over the second.
+template <typename T>
+__device__ __forceinline__ T sums_to(T v) {
+    v += __builtin_bit_cast(T, shifted<0x111, 0xF>(__builtin_bit_cast(uint32_t, v)));
+    v += __builtin_bit_cast(T, shifted<0x112, 0xF>(__builtin_bit_cast(uint32_t, v)));
+    v += __builtin_bit_cast(T, shifted<0x114, 0xF>(__builtin_bit_cast(uint32_t, v)));
+    v += __builtin_bit_cast(T, shifted<0x118, 0xF>(__builtin_bit_cast(uint32_t, v)));
+    v += __builtin_bit_cast(T, shifted<0x142, 0xA>(__builtin_bit_cast(uint32_t, v)));
+    v += __builtin_bit_cast(T, shifted<0x143, 0xC>(__builtin_bit_cast(uint32_t, v)));
+    return v;
+}
+template <typename T>
+__device__ __forceinline__ T wave_sum(T v) {
+    return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sums_to(v)), 63));
 }
 
 // ------------------------------------------------------------------------------------- activations

@@ -5,7 +5,8 @@
 //   nvfp4_rotary    : k_rotary
 //   nvfp4_kv_append : k_kv_append
 //   nvfp4_attention : k_attn_rows, or k_attn_split -> k_attn_join
-//   nvfp4_moe       : k_moe_route -> k_moe_product (up) -> k_moe_product (down) -> k_moe_sum
+//   nvfp4_moe       : [k_moe_route ->] k_moe_product or k_moe_rows (up) -> k_moe_down, or k_moe_product or k_moe_rows (down)
+//                     -> k_moe_sum
 #include <hip/hip_runtime.h>
 #include <math.h>
 #include <stdint.h>
@@ -165,7 +166,7 @@ int check_experts(int64_t tokens, int64_t width, int64_t inner, int experts, int
     if (tokens > nvfp4::kMoeMaxPairs || tokens * top_k > nvfp4::kMoeMaxPairs) return NVFP4_ERR_SHAPE;
     if (2 * width * inner >= ((int64_t)1 << 31)) return NVFP4_ERR_SHAPE;
     // work-groups of 512 threads: one for 16 rows of each chosen expert
-    if ((width > inner ? width : inner) / 16 * experts >= ((int64_t)1 << 23)) return NVFP4_ERR_SHAPE;
+    if ((width > inner ? width : inner) / 16 * (experts + tokens * top_k / 16) >= ((int64_t)1 << 23)) return NVFP4_ERR_SHAPE;
     return NVFP4_OK;
 }
 

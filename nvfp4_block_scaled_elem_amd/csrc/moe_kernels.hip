@@ -64,17 +64,6 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t v) {
     v = max(v, moved<0x143>(v, v));
     return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
-__device__ __forceinline__ float wave_sum(float v) {
-    auto add = [&](uint32_t u) { v += __uint_as_float(u); };
-    add(moved<0x111>(0u, __float_as_uint(v)));
-    add(moved<0x112>(0u, __float_as_uint(v)));
-    add(moved<0x114>(0u, __float_as_uint(v)));
-    add(moved<0x118>(0u, __float_as_uint(v)));
-    add(moved<0x142>(0u, __float_as_uint(v)));
-    add(moved<0x143>(0u, __float_as_uint(v)));
-    return __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(v), 63));
-}
-
 // The experts of token t, by one wave: lane j < top_k gets choice j (-1: none) and its weight. Lane l holds the logits
 // l, l + 64, ... (R of them). `most`: choices to make (the weights are right if all top_k are).
 template <int R>
@@ -177,14 +166,22 @@ __device__ __forceinline__ float rest_of(float v, float hi) {
 // 16-byte piece q (0..3) of row r of a chunk's codes in LDS: the 16 lanes that read one q of 16 rows meet no bank twice.
 __device__ __forceinline__ int code_place(int r, int q) { return r * 64 + ((q ^ ((r >> 2) & 3)) << 4); }
 
-// The chosen experts in order, by a whole work-group: find() gives the number `nth` of them (-1: there are not so many), fill()
-// puts its pairs into `list`. `seen` has a byte per expert. A thread's ids are loaded at once and kept: one by one, 1200 of
+// A work-group's pairs, by all of it: the chosen experts in order, each as often as its pairs make groups of SIZE, are a list;
+// find() takes its entry `nth` (expert -1: there are not so many), fill() puts the entry's pairs into `list`, in their
+// order, so that the entries of an expert share its pairs without a word between them. An expert that many tokens chose is then
+// several work-groups' work, not several turns of one (150 tokens, 128 experts of 2048 x 768, four of them chosen by all tokens:
+// 126 us, 260 in turns; where all are as likely 111 and 109). A thread's ids are loaded at once and kept: one by one, 1200 of
 // them took 8 us of a work-group's time.
-template <int THREADS>
+template <int THREADS, int SIZE>
 struct Pick {
-    static constexpr int kMine = 8;
+    static constexpr int kMine = 8, kWavesHere = THREADS / 64;
+    struct Lds {
+        int pairs[kMoeMaxExperts];
+        int matches[kMine * kWavesHere];
+        uint16_t list[SIZE];
+    };
     int id[kMine];
-    int expert;
+    int expert, first, n;  // the entry's expert, and its pairs first .. first + n - 1
     __device__ __forceinline__ void load(const int *ids, int i0, int pairs) {
 #pragma unroll
         for (int u = 0; u < kMine; ++u) {
@@ -192,21 +189,19 @@ struct Pick {
             id[u] = i < pairs ? ids[i] : -1;
         }
     }
-    __device__ __forceinline__ int find(const MoeArgs &p, const int *ids, int nth, uint8_t *seen, int *count) {
+    __device__ __forceinline__ void find(const MoeArgs &p, const int *ids, int nth, Lds &lds) {
         const int tid = threadIdx.x, lane = tid & 63, pairs = (int)p.tokens * p.top_k;
         if (p.tokens == 1) {  // its choices are all different
-            expert = ids[nth];
-            if (tid == 0) *count = 1;
-            return expert;
+            expert = ids[nth], first = 0, n = 1;
+            return;
         }
         load(ids, 0, pairs);
-        for (int e = tid; e < (p.experts + 3) / 4; e += THREADS) reinterpret_cast<uint32_t *>(seen)[e] = 0u;
-        if (tid == 0) *count = 0;
+        for (int e = tid; e < p.experts; e += THREADS) lds.pairs[e] = 0;
         __syncthreads();
         for (int i0 = 0;;) {
 #pragma unroll
             for (int u = 0; u < kMine; ++u)
-                if (id[u] >= 0) seen[id[u]] = 1;
+                if (id[u] >= 0) atomicAdd(&lds.pairs[id[u]], 1);
             i0 += THREADS * kMine;
             if (i0 >= pairs) break;
             load(ids, i0, pairs);
@@ -214,34 +209,51 @@ struct Pick {
         __syncthreads();
         int before = 0;
         expert = -1;
-        for (int e0 = 0; e0 < p.experts && expert < 0; e0 += 64) {
-            uint64_t who = __ballot(e0 + lane < p.experts && seen[e0 + lane]);
-            const int n = __popcll(who);
-            if (before + n > nth) {
-                for (int k = before; k < nth; ++k) who &= who - 1;
-                expert = e0 + __ffsll((unsigned long long)who) - 1;
+        for (int e0 = 0; e0 < p.experts; e0 += 64) {
+            const int count = e0 + lane < p.experts ? lds.pairs[e0 + lane] : 0, entries = (count + SIZE - 1) / SIZE;
+            const int upto = sums_to(entries);
+            const uint64_t past = __ballot(before + upto > nth);
+            if (past) {
+                const int at = __ffsll((unsigned long long)past) - 1;
+                expert = e0 + at;
+                first = (nth - before - __builtin_amdgcn_readlane(upto - entries, at)) * SIZE;
+                n = min(SIZE, __builtin_amdgcn_readlane(count, at) - first);
+                return;
             }
-            before += n;
+            before += __builtin_amdgcn_readlane(upto, 63);
         }
-        return expert;
     }
-    // The pairs' order in the list decides their column alone, which no result depends on.
-    __device__ __forceinline__ void fill(const MoeArgs &p, const int *ids, int nth, uint16_t *list, int *count) {
-        const int tid = threadIdx.x, pairs = (int)p.tokens * p.top_k;
+    __device__ __forceinline__ void fill(const MoeArgs &p, const int *ids, int nth, Lds &lds) {
+        const int tid = threadIdx.x, lane = tid & 63, pairs = (int)p.tokens * p.top_k;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         if (p.tokens == 1) {
-            if (tid == 0) list[0] = (uint16_t)nth;
-        } else {
-            if (pairs > THREADS * kMine) load(ids, 0, pairs);
-            for (int i0 = 0;;) {
-#pragma unroll
-                for (int u = 0; u < kMine; ++u)
-                    if (id[u] == expert) list[atomicAdd(count, 1)] = (uint16_t)(i0 + THREADS * u + tid);
-                i0 += THREADS * kMine;
-                if (i0 >= pairs) break;
-                load(ids, i0, pairs);
-            }
+            if (tid == 0) lds.list[0] = (uint16_t)nth;
+            __syncthreads();
+            return;
         }
-        __syncthreads();
+        if (pairs > THREADS * kMine) load(ids, 0, pairs);
+        int before = 0;  // the expert's pairs in front of i0
+        for (int i0 = 0;;) {
+            uint64_t who[kMine];
+#pragma unroll
+            for (int u = 0; u < kMine; ++u) {
+                who[u] = __ballot(id[u] == expert);
+                if (lane == 0) lds.matches[u * kWavesHere + wave] = __popcll(who[u]);
+            }
+            __syncthreads();
+            const int mine = lane < kMine * kWavesHere ? lds.matches[lane] : 0, upto = sums_to(mine);
+#pragma unroll
+            for (int u = 0; u < kMine; ++u) {
+                const int at = before - first + __builtin_amdgcn_readlane(upto - mine, u * kWavesHere + wave) +
+                               __popcll(who[u] & (((uint64_t)1 << lane) - 1));
+                if (id[u] == expert && at >= 0 && at < SIZE) lds.list[at] = (uint16_t)(i0 + THREADS * u + tid);
+            }
+            __syncthreads();
+            before += __builtin_amdgcn_readlane(upto, 63);
+            i0 += THREADS * kMine;
+            if (i0 >= pairs) break;
+            load(ids, i0, pairs);
+        }
     }
 };
 
@@ -267,19 +279,19 @@ template <int NT, bool SECOND, bool ROUTE>
 __global__ __launch_bounds__(kThreads) void k_moe_product(MoeArgs p, int tiles) {
     constexpr int kStage = kWaves * NT * kChunkLds, kSums = kWaves * NT * 1024;
     __shared__ __attribute__((aligned(16))) uint8_t lds[kStage > kSums ? kStage : kSums];
-    __shared__ __attribute__((aligned(4))) uint8_t seen[kMoeMaxExperts];
-    extern __shared__ uint16_t list[];  // an expert's pairs: as many as tokens at most
-    __shared__ int count;
+    __shared__ typename Pick<kThreads, 16>::Lds pick_lds;
+    uint16_t *const list = pick_lds.list;
     __shared__ int route_ids[ROUTE ? kRouteTokens * kMoeMaxTopK : 1];
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     // (one token: this work-group's expert is choice blockIdx.x / tiles, and those after it are not needed)
     if (ROUTE) route_here<kWaves>(p, p.tokens == 1 && blockIdx.x ? (int)blockIdx.x / tiles + 1 : p.top_k, blockIdx.x == 0, route_ids);
     const int *const ids = ROUTE ? route_ids : p.ids;
-    Pick<kThreads> pick;
-    const int expert = pick.find(p, ids, blockIdx.x / tiles, seen, &count);
+    Pick<kThreads, 16> pick;
+    pick.find(p, ids, blockIdx.x / tiles, pick_lds);
+    const int expert = pick.expert, pairs = pick.n;
     if (expert < 0) return;
-    pick.fill(p, ids, blockIdx.x / tiles, list, &count);
+    pick.fill(p, ids, blockIdx.x / tiles, pick_lds);
     const int64_t K = SECOND ? p.inner : p.width, F = SECOND ? p.width : p.inner;
     const int64_t f0 = (int64_t)(blockIdx.x % tiles) * 16, nch = (K + kChunk - 1) / kChunk;
     const MoeWeights &W = SECOND ? p.down : p.up;
@@ -289,9 +301,8 @@ __global__ __launch_bounds__(kThreads) void k_moe_product(MoeArgs p, int tiles) 
     const int64_t ldx = SECOND ? p.inner : p.ldx;
     uint8_t *const wl = lds + wave * NT * kChunkLds;
     const int64_t crow = min(F - 1, f0 + (lane >> 2)), srow = min(F - 1, f0 + r16);
-    const int pairs = count;
-    for (int c0 = 0; c0 < pairs; c0 += 16) {
-        const int pair = c0 + r16 < pairs ? list[c0 + r16] : -1;
+    {
+        const int pair = r16 < pairs ? list[r16] : -1;
         const uint16_t *xr = x + (int64_t)(SECOND ? max(pair, 0) : max(pair, 0) / p.top_k) * ldx;
         f32x4 acc[NT] = {};
         uint4 cv[NT];
@@ -366,8 +377,8 @@ __global__ __launch_bounds__(kThreads) void k_moe_product(MoeArgs p, int tiles) 
                 for (int j = 0; j < NT; ++j) z[j] += red[(w * NT + j) * 256 + tid];
             const int l = tid >> 2;
             const int64_t f = f0 + 4 * (l >> 4) + (tid & 3);
-            if (f < F && c0 + (l & 15) < pairs) {
-                const int q = list[c0 + (l & 15)];
+            if (f < F && (l & 15) < pairs) {
+                const int q = list[l & 15];
                 if (SECOND) {
                     p.z[q * F + f] = p.weights[q] * (alpha * z[0]);
                 } else {
@@ -379,7 +390,6 @@ __global__ __launch_bounds__(kThreads) void k_moe_product(MoeArgs p, int tiles) 
                 }
             }
         }
-        __syncthreads();
     }
 }
 
@@ -532,30 +542,31 @@ __global__ __launch_bounds__(kDownThreads) void k_moe_down(MoeArgs p) {
 // Many rows: a wave owns 32 weight rows (gated: 16 gate rows and their 16 up rows) over the whole sum, and a work-group's
 // four waves share the tokens' values, which go through LDS in slices of 512 k in the order of the operand. A wave's codes
 // and scales of a slice are all in flight while the slice before is multiplied: 9 KB a wave, no barrier waits for them.
-// MOST: tiles of 16 pairs at a time. SECOND: the product with W2, its sum cut into p.split parts of slices, else with W1. HOLD (2 or
-// 4, 0: not): X is at most so many slices and stays where it is while the work-group goes through several column tiles, without
-// a barrier (150 tokens, 2048 columns: the layer 97 us, 103 with one tile a work-group). ROUTE: as above.
+// MOST: tiles of 16 pairs at a time. SECOND: the product with W2, its sum cut into p.split parts of slices, else with W1. HOLD: X
+// is at most two slices and stays where it is while the work-group goes through several column tiles, without a barrier (four
+// slices, two work-groups a CU with more tiles each, gained 6 % where no expert had more than a tile of pairs and lost 8 % where
+// some had: one work-group more than fit takes a whole turn). ROUTE: as above.
 constexpr int kRowWaves = 4, kRowThreads = 64 * kRowWaves, kSlice = 512, kSliceChunks = kSlice / kChunk;
 constexpr int kWaveCodes = 2 * (1024 + 512);  // LDS bytes of a wave: a chunk's codes and a slice's scales of two tiles
 
-template <int NT, int MOST, bool SECOND, int HOLD, bool ROUTE>
+template <int NT, int MOST, bool SECOND, bool HOLD, bool ROUTE>
 __global__ __launch_bounds__(kRowThreads, 2) void k_moe_rows(MoeArgs p, int tiles, int groups) {
     constexpr int kXBytes = 16 * MOST * kSlice * 2;  // of a slice
     constexpr int kCols = NT == 2 ? 16 * kRowWaves : 32 * kRowWaves;
-    __shared__ __attribute__((aligned(16))) uint8_t lds_x[HOLD > 2 ? HOLD : 2][kXBytes];
+    __shared__ __attribute__((aligned(16))) uint8_t lds_x[2][kXBytes];
     __shared__ __attribute__((aligned(16))) uint8_t lds_w[kRowWaves][kWaveCodes];
-    __shared__ __attribute__((aligned(4))) uint8_t seen[kMoeMaxExperts];
-    extern __shared__ uint16_t list[];  // an expert's pairs: as many as tokens at most
-    __shared__ int count;
+    __shared__ typename Pick<kRowThreads, 16 * MOST>::Lds pick_lds;
+    uint16_t *const list = pick_lds.list;
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     __shared__ int route_ids[ROUTE ? kRouteTokens * kMoeMaxTopK : 1];
     if (ROUTE) route_here<kRowWaves>(p, p.top_k, blockIdx.x == 0, route_ids);
     const int *const ids = ROUTE ? route_ids : p.ids;
-    Pick<kRowThreads> pick;
-    const int expert = pick.find(p, ids, blockIdx.x / groups, seen, &count);
+    Pick<kRowThreads, 16 * MOST> pick;
+    pick.find(p, ids, blockIdx.x / groups, pick_lds);
+    const int expert = pick.expert, pairs = pick.n;
     if (expert < 0) return;
-    pick.fill(p, ids, blockIdx.x / groups, list, &count);
+    pick.fill(p, ids, blockIdx.x / groups, pick_lds);
     const int K = (int)(SECOND ? p.inner : p.width), F = (int)(SECOND ? p.width : p.inner);
     // The work-group's column tiles: first, first + groups, ...
     const int first = (int)(blockIdx.x % groups), turns = HOLD ? (tiles - first + groups - 1) / groups : 1;
@@ -581,9 +592,7 @@ __global__ __launch_bounds__(kRowThreads, 2) void k_moe_rows(MoeArgs p, int tile
     };
     // codes: the lane loads row lane / 4, 16 bytes lane % 4 of a chunk; scales: row lane / 4, the 8 of chunk lane % 4
     const uint32_t crow = (uint32_t)(lane >> 2) * (uint32_t)(K / 2), srow = (uint32_t)(lane >> 2) * (uint32_t)(K / 16);
-    const int pairs = count;
-    // The pairs c0 .. + 16 MT - 1 of the list.
-    auto pass = [&](auto tiles_of_pairs, int c0) __attribute__((always_inline)) {
+    auto pass = [&](auto tiles_of_pairs) __attribute__((always_inline)) {
         constexpr int MT = tiles_of_pairs.value, kX = 16 * MT * kSlice * 2 / 16 / kRowThreads;  // tiles; pieces a thread
         u32x4 cv[2][kSliceChunks], xv[kX];
         u32x2 sv[2];
@@ -627,7 +636,7 @@ __global__ __launch_bounds__(kRowThreads, 2) void k_moe_rows(MoeArgs p, int tile
         const uint16_t *xr[kX];
 #pragma unroll
         for (int i = 0; i < kX; ++i) {
-            const int pair = __builtin_amdgcn_readfirstlane((int)list[min(c0 + wave + kRowWaves * i, pairs - 1)]);
+            const int pair = __builtin_amdgcn_readfirstlane((int)list[min(wave + kRowWaves * i, pairs - 1)]);
             xr[i] = x + (int64_t)(SECOND ? pair : pair / p.top_k) * ldx;
         }
         auto load_x = [&](int s) __attribute__((always_inline)) {
@@ -685,8 +694,8 @@ __global__ __launch_bounds__(kRowThreads, 2) void k_moe_rows(MoeArgs p, int tile
             // Element r of the lane is weight row 4 g + r of a tile, pair r16 of a tile of pairs.
 #pragma unroll
             for (int m = 0; m < MT; ++m) {
-                if (c0 + 16 * m + r16 >= pairs) continue;
-                const int64_t pair = list[c0 + 16 * m + r16];
+                if (16 * m + r16 >= pairs) continue;
+                const int64_t pair = list[16 * m + r16];
                 if (SECOND) {
                     const float w = p.weights[pair];
                     float *z = p.z + ((int64_t)blockIdx.y * p.tokens * p.top_k + pair) * F + f0 + 4 * g;
@@ -725,9 +734,9 @@ __global__ __launch_bounds__(kRowThreads, 2) void k_moe_rows(MoeArgs p, int tile
         for (int c = 0; c < kSliceChunks; ++c) load_codes(s_lo, c);
         if (HOLD) {
             store_x(s_lo, lds_x[0]);
-            for (int s = s_lo + 1; s < s_hi; ++s) {
-                load_x(s);
-                store_x(s, lds_x[s - s_lo]);
+            if (s_hi - s_lo > 1) {
+                load_x(s_lo + 1);
+                store_x(s_lo + 1, lds_x[1]);
             }
             lds_barrier();
 #pragma unroll 1
@@ -752,13 +761,10 @@ __global__ __launch_bounds__(kRowThreads, 2) void k_moe_rows(MoeArgs p, int tile
             finish(0);
         }
     };
-    for (int c0 = 0; c0 < pairs;) {
-        if (MOST == 2 && pairs - c0 > 16)
-            pass(std::integral_constant<int, MOST>{}, c0), c0 += 16 * MOST;
-        else
-            pass(std::integral_constant<int, 1>{}, c0), c0 += 16;
-        lds_barrier();  // the last slices have been read
-    }
+    if (MOST == 2 && pairs > 16)
+        pass(std::integral_constant<int, MOST>{});
+    else
+        pass(std::integral_constant<int, 1>{});
 }
 
 // y of eight columns of a token per thread: the parts in the order of the choices.
@@ -815,32 +821,37 @@ Plan plan_moe(int64_t tokens, int64_t width, int64_t inner, int experts, int top
         const int64_t slices = (inner + kSlice - 1) / kSlice;
         while (plan.split < 8 && 4 * plan.split <= slices && used * down * plan.split < 500) plan.split *= 2;
     }
-    // Where X stays: two or three work-groups a CU, as many as there is LDS for.
-    plan.up_turns = width <= (plan.mt == 1 ? 4 : 2) * kSlice ? (int)std::max(1.0, used * up / 512.0 + 0.5) : 1;
+    // Three work-groups a CU, where X stays.
+    plan.up_turns = width <= 2 * kSlice ? (int)std::max(1.0, used * up / 768.0 + 0.5) : 1;
     plan.down_turns = inner <= 2 * kSlice ? (int)std::max(1.0, used * down / 768.0 + 0.5) : 1;
     return plan;
 }
 
+// Entries that the list of Pick has at most: a pair each, and for each expert the whole groups and one more.
+int64_t entries(const MoeArgs &p, int size) {
+    const int64_t pairs = p.tokens * p.top_k;
+    return std::min(pairs, std::min<int64_t>(p.experts, pairs) + pairs / size);
+}
+
 template <int NT, bool SECOND>
-void product(const MoeArgs &p, int64_t chosen, bool by_rows, bool apart, int mt, int turns, hipStream_t st) {
+void product(const MoeArgs &p, bool by_rows, bool apart, int mt, int turns, hipStream_t st) {
     const int64_t F = SECOND ? p.width : p.inner;
-    const size_t list = (size_t)(2 * p.tokens + 255) / 256 * 256;
     if (!by_rows) {
         const int tiles = (int)((F + 15) / 16);
-        const dim3 grid((unsigned)(chosen * tiles));
+        const dim3 grid((unsigned)(entries(p, 16) * tiles));
         if constexpr (!SECOND)
             if (!apart) {
-                hipLaunchKernelGGL((k_moe_product<NT, false, true>), grid, dim3(kThreads), list, st, p, tiles);
+                hipLaunchKernelGGL((k_moe_product<NT, false, true>), grid, dim3(kThreads), 0, st, p, tiles);
                 return;
             }
-        hipLaunchKernelGGL((k_moe_product<NT, SECOND, false>), grid, dim3(kThreads), list, st, p, tiles);
+        hipLaunchKernelGGL((k_moe_product<NT, SECOND, false>), grid, dim3(kThreads), 0, st, p, tiles);
         return;
     }
     constexpr int kCols = NT == 2 ? 16 * kRowWaves : 32 * kRowWaves;
     const int tiles = (int)((F + kCols - 1) / kCols), groups = (tiles + turns - 1) / turns;
-    const dim3 grid((unsigned)(chosen * groups), SECOND ? p.split : 1), block(kRowThreads);
+    const dim3 grid((unsigned)(entries(p, 16 * mt) * groups), SECOND ? p.split : 1), block(kRowThreads);
     auto run = [&](auto mts, auto hold, auto route) {
-        hipLaunchKernelGGL((k_moe_rows<NT, mts.value, SECOND, hold.value, route.value>), grid, block, list, st, p, tiles, groups);
+        hipLaunchKernelGGL((k_moe_rows<NT, mts.value, SECOND, hold.value, route.value>), grid, block, 0, st, p, tiles, groups);
     };
     auto held = [&](auto mts, auto hold) {
         if constexpr (SECOND || mts.value > 1)
@@ -848,16 +859,12 @@ void product(const MoeArgs &p, int64_t chosen, bool by_rows, bool apart, int mt,
         else
             apart ? run(mts, hold, std::false_type{}) : run(mts, hold, std::true_type{});
     };
-    using std::integral_constant;
-    const int64_t slices = ((SECOND ? p.inner : p.width) + kSlice - 1) / kSlice;
+    using One = std::integral_constant<int, 1>;
+    using Two = std::integral_constant<int, 2>;
     if (mt == 2)
-        turns > 1 ? held(integral_constant<int, 2>{}, integral_constant<int, 2>{}) : held(integral_constant<int, 2>{}, integral_constant<int, 0>{});
-    else if (turns > 1 && slices > 2)
-        held(integral_constant<int, 1>{}, integral_constant<int, 4>{});
-    else if (turns > 1)
-        held(integral_constant<int, 1>{}, integral_constant<int, 2>{});
+        turns > 1 ? held(Two{}, std::true_type{}) : held(Two{}, std::false_type{});
     else
-        held(integral_constant<int, 1>{}, integral_constant<int, 0>{});
+        turns > 1 ? held(One{}, std::true_type{}) : held(One{}, std::false_type{});
 }
 
 }  // namespace
@@ -884,17 +891,16 @@ hipError_t launch_moe(const MoeArgs &a, void *ws, hipStream_t st) {
         hipLaunchKernelGGL(k_moe_route, dim3((unsigned)((p.tokens + 3) / 4)), dim3(256), 0, st, p);
         if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     }
-    const int64_t chosen = std::min<int64_t>(p.experts, (int64_t)pairs);
     if (p.gated)
-        product<2, false>(p, chosen, plan.up_rows, plan.route, plan.mt, plan.up_turns, st);
+        product<2, false>(p, plan.up_rows, plan.route, plan.mt, plan.up_turns, st);
     else
-        product<1, false>(p, chosen, plan.up_rows, plan.route, plan.mt, plan.up_turns, st);
+        product<1, false>(p, plan.up_rows, plan.route, plan.mt, plan.up_turns, st);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     if (plan.down_sum) {
         hipLaunchKernelGGL(k_moe_down, dim3((unsigned)(p.width / 16)), dim3(kDownThreads), 0, st, p);
         return hipGetLastError();
     }
-    product<1, true>(p, chosen, plan.down_rows, true, plan.mt, plan.down_turns, st);
+    product<1, true>(p, plan.down_rows, true, plan.mt, plan.down_turns, st);
     if (const hipError_t e = hipGetLastError(); e != hipSuccess) return e;
     const int per = (int)(p.width / 8);
     hipLaunchKernelGGL(k_moe_sum, dim3((unsigned)((p.tokens * per + 255) / 256)), dim3(256), 0, st, p, per);
