@@ -228,7 +228,7 @@ struct Pick {
         const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
         if (p.tokens == 1) {
             if (tid == 0) lds.list[0] = (uint16_t)nth;
-            __syncthreads();
+            lds_barrier();
             return;
         }
         if (pairs > THREADS * kMine) load(ids, 0, pairs);
@@ -240,7 +240,7 @@ struct Pick {
                 who[u] = __ballot(id[u] == expert);
                 if (lane == 0) lds.matches[u * kWavesHere + wave] = __popcll(who[u]);
             }
-            __syncthreads();
+            lds_barrier();
             const int mine = lane < kMine * kWavesHere ? lds.matches[lane] : 0, upto = sums_to(mine);
 #pragma unroll
             for (int u = 0; u < kMine; ++u) {
@@ -248,7 +248,7 @@ struct Pick {
                                __popcll(who[u] & (((uint64_t)1 << lane) - 1));
                 if (id[u] == expert && at >= 0 && at < SIZE) lds.list[at] = (uint16_t)(i0 + THREADS * u + tid);
             }
-            __syncthreads();
+            lds_barrier();
             before += __builtin_amdgcn_readlane(upto, 63);
             i0 += THREADS * kMine;
             if (i0 >= pairs) break;
@@ -566,7 +566,6 @@ __global__ __launch_bounds__(kRowThreads, 2) void k_moe_rows(MoeArgs p, int tile
     pick.find(p, ids, blockIdx.x / groups, pick_lds);
     const int expert = pick.expert, pairs = pick.n;
     if (expert < 0) return;
-    pick.fill(p, ids, blockIdx.x / groups, pick_lds);
     const int K = (int)(SECOND ? p.inner : p.width), F = (int)(SECOND ? p.width : p.inner);
     // The work-group's column tiles: first, first + groups, ...
     const int first = (int)(blockIdx.x % groups), turns = HOLD ? (tiles - first + groups - 1) / groups : 1;
@@ -631,6 +630,11 @@ __global__ __launch_bounds__(kRowThreads, 2) void k_moe_rows(MoeArgs p, int tile
                 *reinterpret_cast<u32x2 *>(wl + 2048 + 512 * j + 8 * lane) = v;
             }
         };
+        take_rows(0);
+        load_scales(s_lo);
+#pragma unroll
+        for (int c = 0; c < kSliceChunks; ++c) load_codes(s_lo, c);
+        pick.fill(p, ids, blockIdx.x / groups, pick_lds);  // (the codes are on their way)
         // Piece e = tid + 256 i of a slice: token e / 64 of the tiles (a wave has one at a time), k = 8 (e % 64) .. + 7. Tokens
         // past the last are read as the last: their columns are not stored.
         const uint16_t *xr[kX];
@@ -727,11 +731,7 @@ __global__ __launch_bounds__(kRowThreads, 2) void k_moe_rows(MoeArgs p, int tile
 #pragma unroll
                 for (int m = 0; m < MT; ++m) acc[j][m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         };
-        take_rows(0);
         load_x(s_lo);
-        load_scales(s_lo);
-#pragma unroll
-        for (int c = 0; c < kSliceChunks; ++c) load_codes(s_lo, c);
         if (HOLD) {
             store_x(s_lo, lds_x[0]);
             if (s_hi - s_lo > 1) {
