@@ -130,6 +130,23 @@ def test_struct_layouts(tmp_path, name, struct):
     assert out == [ctypes.sizeof(struct)] + [getattr(struct, f).offset for f in fields]
 
 
+@pytest.mark.parametrize("args,pack", [(decoder._RotaryArgs, decoder._rotary_args), (decoder._Cache, decoder._cache_args),
+                                       (decoder._Sequences, decoder._sequences_args), (decoder._MoeArgs, decoder._moe_args)])
+def test_packed_arguments(args, pack):
+    """The bytes that the binding passes are those of the structure."""
+    values, fields = [], {}
+    for i, (name, kind) in enumerate(args._fields_):
+        v = [-2.5 * i] if kind is ctypes.c_double else [3 * i + k + 1 for k in range(4)] if kind is decoder._Sections else [1 << 20 | i]
+        values += v
+        fields[name] = kind(*v) if kind is decoder._Sections else v[0]
+    a, b = args.from_buffer_copy(pack(*values)), args(**fields)
+    for name, kind in args._fields_:
+        x, y = getattr(a, name), getattr(b, name)
+        assert list(x) == list(y) if kind is decoder._Sections else x == y, name
+    with pytest.raises(decoder.NVFP4Error):
+        pack(*(1 << 70 for _ in values))
+
+
 def test_binding_refuses_cpu_tensors():
     x = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
     i = torch.zeros(4, dtype=torch.int32)
