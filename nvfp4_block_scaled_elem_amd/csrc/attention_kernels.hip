@@ -795,10 +795,12 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_join(AttnArgs p, int size
 template <int KS, bool FULL>
 void split(const AttnArgs &p, int rt, hipStream_t st) {
     const dim3 grid((unsigned)(p.groups * p.kv_heads)), block(kAttnThreads);
-    if (rt >= 2)
-        hipLaunchKernelGGL((k_attn_split<KS, 2, FULL>), grid, block, 0, st, p);
-    else
-        hipLaunchKernelGGL((k_attn_split<KS, 1, FULL>), grid, block, 0, st, p);
+    if constexpr (KS < 4)
+        if (rt == 2) {
+            hipLaunchKernelGGL((k_attn_split<KS, 2, FULL>), grid, block, 0, st, p);
+            return;
+        }
+    hipLaunchKernelGGL((k_attn_split<KS, 1, FULL>), grid, block, 0, st, p);
 }
 
 template <int KS, bool FULL>
@@ -810,7 +812,6 @@ void rows(const AttnArgs &p, int rt, hipStream_t st) {
     else
         hipLaunchKernelGGL((k_attn_rows<KS, 2, FULL>), grid, block, lds, st, p);
 }
-
 
 }  // namespace
 
@@ -836,13 +837,20 @@ AttnPlan plan_attention(int64_t tokens, int seqs, int width, int kv_heads, int g
         }
         return plan;
     }
-    const int rt = mean <= 16 ? 1 : 2;
-    plan.rt = rt;
-    plan.size = 16 * rt;
+    // Tiles of 16 rows, or, from 17 rows on, of 32, which read a block once for all of them, but in one work-group a CU from 65
+    // columns on and with more than there are registers from 193 on. `reach`: the blocks of a share where every sequence is as long
+    // as its row of the table and has one tile. Below: tables of so many blocks, 32 and 16 rows a tile, us.
+    //   16 x 79 over 128 shares (9.9), 24 rows: 64 columns 18.6 and 16.8, 128 columns 28.2 and 21.7, 192 columns 38.8 and 34.0
+    //   8 x 126 over 64 (15.8), 32 rows: 27.4 and 28.5, 42.9 and 35.9, 61 and 71;  16 x 126 (31.5): 38 and 44, 64 and 57, 102 and 95
+    //   32 x 126 (63): 67 and 77, 119 and 169, 166 and 253;  256 columns: 64 x 126 158 and 121, 16 x 79 over 128 60 and 38
+    const int64_t shares = std::max<int64_t>(1, 512 / kv_heads), reach = (int64_t)seqs * width / shares;
+    const bool wide = mean > 16 && dim <= 192 && reach >= (dim > 64 && dim <= 128 ? 40 : 12);
+    plan.rt = wide ? 2 : 1;
+    plan.size = 16 * plan.rt;
     plan.pieces = all / plan.size + seqs;
     // Two work-groups a CU, not more than there can be blocks for.
     const int64_t most = std::max<int64_t>(1, (plan.pieces * (int64_t)width + kWaves - 1) / kWaves);
-    plan.groups = (int)std::min<int64_t>(most, std::max<int64_t>(1, 512 / kv_heads));
+    plan.groups = (int)std::min<int64_t>(most, shares);
     const int64_t parts = (int64_t)kv_heads * plan.groups * 2 * plan.size;
     plan.part_bytes = ((size_t)parts * dim * 4 + 255) / 256 * 256;
     plan.ml_bytes = (size_t)parts * 8;

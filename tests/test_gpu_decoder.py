@@ -344,6 +344,32 @@ def test_attention_shares(seqs):
     check(o, want, err)
 
 
+# Tiles of 32 rows, which a table wide enough takes, for each head size compiled for: full tiles and parts of one, blocks of NaN
+WIDE = [([900, 64, 2001, 7], [5, 7, 8, 1], 16, 4, 64), ([1300, 129], [8, 9], 24, 8, 128), ([700, 1900, 63], [3, 3, 2], 8, 1, 80),
+        ([2500, 11, 0, 640], [4, 11, 0, 5], 10, 2, 192), ([513, 300], [17, 30], 1, 1, 48), ([800, 1000], [20, 31], 2, 2, 160)]
+
+
+@pytest.mark.parametrize("lengths,new,heads,kv_heads,dim", WIDE)
+def test_attention_of_wide_tables(lengths, new, heads, kv_heads, dim):
+    say(f"wide {lengths} {new} {heads} {kv_heads} {dim}")
+    table, pages = layout(6, lengths, width=40 * 512 // kv_heads // len(lengths) + 1)
+    cache = nv.kv_cache(pages, kv_heads, dim)
+    fill(cache, 6)
+    sp = spans(lengths, new)
+    q = rand(3, sum(new), heads, dim)
+    args = (q, cache, table, ints(lengths), starts_of(sp))
+    for causal in (True, False):
+        o = nv.attention(*args, causal=causal)
+        want, err = dref.attention(q, cache, table, sp, dim ** -0.5, causal)
+        check(o, want, err)
+        assert torch.equal(nv.attention(*args, causal=causal), o)
+    u8(cache.k_scales)[int(table[0, 5]), 0] = 255
+    table[0, 2] = -1
+    want, err = dref.attention(q, cache, table, sp, dim ** -0.5, True)
+    assert torch.isnan(want).any()
+    check(nv.attention(*args), want, err)
+
+
 def test_attention_of_many_sequences():
     """More sequences than a wave has lanes, of very different lengths."""
     lengths = [(i * 37) % 150 for i in range(200)] + [3000]
