@@ -756,6 +756,12 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_join(AttnArgs p, int size
     }
     // The row in part k.
     auto place = [&](int k) __attribute__((always_inline)) { return (at + (int64_t)k * apart + (k == 0 ? apart - 1 : 0)) * size + row; };
+    // The first parts are on their way while their weights are found.
+    constexpr int kAhead = 4;
+    const float *o4 = p.part + min(c, p.dim - 4);
+    f32x4 ahead[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) ahead[i] = *reinterpret_cast<const f32x4 *>(o4 + place(min(kShare * i + turn, parts - 1)) * p.dim);
     float m = kNegInf;
     for (int k = lane; k < parts; k += 64) m = fmaxf(m, p.part_ml[2 * place(k)]);
 #pragma unroll
@@ -771,8 +777,14 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_join(AttnArgs p, int size
             sum += ml[1] == 0.0f ? 0.0f : f * ml[1];
         }
         const int here = min(64, (parts - k0 - turn + kShare - 1) / kShare);
-        const float *o4 = p.part + min(c, p.dim - 4);
-        for (int i = 0; i < here; ++i)
+        int i = 0;
+        if (k0 == 0) {
+#pragma unroll
+            for (int a = 0; a < kAhead; ++a)
+                if (a < here) v += ahead[a] * __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f), a));
+            i = kAhead;
+        }
+        for (; i < here; ++i)
             v += *reinterpret_cast<const f32x4 *>(o4 + place(k0 + kShare * i + turn) * p.dim) *
                  __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(f), i));
     }
