@@ -302,21 +302,89 @@ __device__ __forceinline__ uint16_t *out_row(const AttnArgs &p, const Seq &q, in
     return p.out + ((int64_t)(q.first + tok) * p.kv_heads * p.group + h * p.group + (row - tok * p.group)) * p.dim;
 }
 
+// LDS bytes of a work-group whose waves share the blocks: each wave's block, afterwards each wave's sums.
+template <int KS>
+constexpr int kSumsLds = kWaves * 16 * (64 * KS + 4) * 4;
+template <int KS>
+constexpr int kBlocksLds = kWaves * kWaveLds<KS> > kSumsLds<KS> ? kWaves * kWaveLds<KS> : kSumsLds<KS>;
+
+// The sums of a work-group's waves over `rows` rows of a tile from row0 on, in wave order: the output, where they are `whole`, or
+// a part of it, at the rows `at` of the scratch.
+template <int KS, int RT>
+__device__ __forceinline__ void join_waves(const AttnArgs &p, const Seq &q, int64_t h, int row0, int rows, const Rows<KS, RT> &R, bool whole,
+                                           int64_t at, uint8_t *lds, float (*lds_ml)[kWaves][16]) {
+    constexpr int kDim = 64 * KS;
+    float (*const lds_o)[16][kDim + 4] = reinterpret_cast<float (*)[16][kDim + 4]>(lds);
+    float (*const lds_m)[16] = lds_ml[0], (*const lds_l)[16] = lds_ml[1];
+    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+        const float l = row_sum(R.l[r]);
+        if (16 * r >= rows) break;
+        __syncthreads();  // the blocks, or the tile before, have been read
+        if (g == 0) lds_m[wave][r16] = R.m[r] * p.scale2, lds_l[wave][r16] = l;
+#pragma unroll
+        for (int d = 0; d < 4 * KS; ++d) *reinterpret_cast<f32x4 *>(&lds_o[wave][r16][16 * d + 4 * g]) = R.o[r][d];
+        __syncthreads();
+        // 16 threads a row, each four columns of every 64
+        const int row = tid >> 4, c0 = 4 * (tid & 15);
+        if (16 * r + row < rows) {
+            float m = kNegInf;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) m = fmaxf(m, lds_m[w][row]);
+            float f[kWaves], sum = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWaves; ++w) {
+                f[w] = weight(lds_m[w][row], m);
+                sum += lds_l[w][row] == 0.0f ? 0.0f : f[w] * lds_l[w][row];
+            }
+            const float inv = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
+            float *po = p.part + (at + 16 * r + row) * p.dim;
+            uint16_t *o = out_row(p, q, h, row0 + 16 * r + row);
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+                const int c = 64 * k + c0;
+                if (c >= p.dim) break;
+                f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int w = 0; w < kWaves; ++w) v += *reinterpret_cast<const f32x4 *>(&lds_o[w][row][c]) * f[w];
+                v *= inv;
+                if (whole)
+                    *reinterpret_cast<uint2 *>(o + c) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
+                else
+                    *reinterpret_cast<f32x4 *>(po + c) = v;
+            }
+            if (!whole && c0 == 0) {
+                float *ml = p.part_ml + (at + 16 * r + row) * 2;
+                ml[0] = m, ml[1] = sum;
+            }
+        }
+    }
+}
+
 // Rows over the waves, for prompts: a work-group takes 64 RT rows of a sequence and head, a wave 16 RT of them, over the
 // blocks that they see, or over one of gridDim.y parts of these (k_attn_join adds the parts). Bound by the matrix cores and
 // the exponentials, so a block's codes are decoded once per work-group, into LDS in the order of the operands (every read is 1
 // KB in lane order), each block in one of two buffers while the block before is computed. Two work-groups a CU, so that
 // one's exponentials run beside the other's products: 32 rows a wave in 256 registers. Prompts of 8800 tokens, 32 heads of 128:
-// 565 us, 980 TFLOP/s; 64 rows a wave, one work-group a CU: 1105 us (sums move between the two register files); eight
-// waves a work-group: 618; each wave decoding for itself: 2010. Of the 565, decoding and LDS stores take some 90, the
+// 530 us, 1.05 PFLOP/s; 64 rows a wave, one work-group a CU: 1105 us (sums move between the two register files); eight
+// waves a work-group: 618; each wave decoding for itself: 2010. Decoding and LDS stores take some 90 of them, the
 // exponentials 78.
 //
 // Slot m of key tile t holds token 16 t + m; a lane then ends with the scores of the tokens 16 t + 4 g + j, and V's
 // operand u takes tokens 32 u + 4 g + j and 32 u + 16 + 4 g + j, j = 0..3, as k = 8 g .. + 7.
+//
+// A piece of at most 16 rows, as of a single token beside prompts, takes the way of few rows instead, its blocks over the
+// waves (a prompt of 2048 tokens and 16 single ones over 32000 each: 639 -> 211 us; with 63 over 8000: 318 -> 231).
+template <int KS>
+constexpr int kRowsLds = 4 * 64 * 64 * KS * 2 > kBlocksLds<KS> ? 4 * 64 * 64 * KS * 2 : kBlocksLds<KS>;
+
 template <int KS, int RT, bool FULL>
 __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(AttnArgs p) {
     constexpr int kRows = 16 * RT * kWaves, kHalf = 64 * 64 * KS * 2;  // LDS bytes of a block's K or V
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    __shared__ float lds_ml[2][kWaves][16];
     uint8_t *const lds_k = lds, *const lds_v = lds + 2 * kHalf;
     const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -328,14 +396,22 @@ __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(Att
     const Seq q = sequence(p.seq, s);
     const int first = (piece - piece_base(p.seq, s, p.group, log2_of(kRows), 1)) * kRows;
     if (first >= q.n * p.group || first < 0) return;
+    // The blocks that some row of the work-group sees, or this part of them.
+    const int in_piece = min(kRows, q.n * p.group - first);
+    const int reach = seen_by(p, q, first + in_piece - 1), all = (reach + kPage - 1) / kPage;
+    const int start = (int)((int64_t)all * blockIdx.y / gridDim.y), count = (int)((int64_t)all * (blockIdx.y + 1) / gridDim.y);
+    const int64_t part = ((h * p.pieces + piece) * gridDim.y + blockIdx.y) * kRows;
+    if (in_piece <= 16) {
+        Rows<KS, 1> F;
+        attend<KS, 1, FULL>(p, q, s, h, first, start + wave, count, kWaves, F, lds + wave * kWaveLds<KS>);
+        join_waves<KS, 1>(p, q, h, first, in_piece, F, gridDim.y == 1, part, lds, lds_ml);
+        return;
+    }
     const int row0 = first + 16 * RT * wave, dim = FULL ? 64 * KS : p.dim;
     bf16x8 Q[RT][2 * KS];
     Rows<KS, RT> R;
     const int safe = seen_by(p, q, row0);
     take_rows<KS, RT, FULL>(p, q, h, row0, Q, R);
-    // The blocks that some row of the work-group sees, or this part of them.
-    const int reach = seen_by(p, q, min(first + kRows, q.n * p.group) - 1), all = (reach + kPage - 1) / kPage;
-    const int start = (int)((int64_t)all * blockIdx.y / gridDim.y), count = (int)((int64_t)all * (blockIdx.y + 1) / gridDim.y);
 
     // Pages and scales of 64 blocks, one a lane.
     int page = -1;
@@ -531,7 +607,7 @@ __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(Att
         const int row = row0 + 16 * r + r16;
         if (row >= q.n * p.group) continue;
         if (gridDim.y > 1) {  // a part: k_attn_join adds them
-            const int64_t at = ((h * p.pieces + piece) * gridDim.y + blockIdx.y) * kRows + (row - first);
+            const int64_t at = part + (row - first);
             if (g == 0) p.part_ml[2 * at] = R.m[r] * p.scale2, p.part_ml[2 * at + 1] = l;
 #pragma unroll
             for (int d = 0; d < 4 * KS; ++d)
@@ -645,14 +721,10 @@ __device__ __forceinline__ int64_t part_place(const AttnArgs &p, int64_t h, uint
 
 template <int KS, int RT, bool FULL>
 __global__ __launch_bounds__(kAttnThreads, RT * KS <= 2 ? 2 : 1) void k_attn_split(AttnArgs p) {
-    constexpr int kRows = 16 * RT, kDim = 64 * KS;
-    // each wave's block; afterwards each wave's sums
-    constexpr int kStage = kWaves * kWaveLds<KS>, kSums = kWaves * 16 * (kDim + 4) * 4;
-    __shared__ __attribute__((aligned(16))) uint8_t lds[kStage > kSums ? kStage : kSums];
-    __shared__ float lds_m[kWaves][16], lds_l[kWaves][16];
-    float (*const lds_o)[16][kDim + 4] = reinterpret_cast<float (*)[16][kDim + 4]>(lds);
-    const int tid = threadIdx.x, lane = tid & 63, r16 = lane & 15, g = lane >> 4;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    constexpr int kRows = 16 * RT;
+    __shared__ __attribute__((aligned(16))) uint8_t lds[kBlocksLds<KS>];
+    __shared__ float lds_ml[2][kWaves][16];
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int64_t h = blockIdx.x % p.kv_heads;
     const uint32_t j = blockIdx.x / p.kv_heads;
     Window w;
@@ -670,51 +742,7 @@ __global__ __launch_bounds__(kAttnThreads, RT * KS <= 2 ? 2 : 1) void k_attn_spl
         const int row0 = tile * kRows, rows = min(kRows, q.n * p.group - row0);
         Rows<KS, RT> R;
         attend<KS, RT, FULL>(p, q, s, h, row0, b0 + wave, b1, kWaves, R, lds + wave * kWaveLds<KS>);
-        const bool whole = b0 == 0 && b1 == (int)nb;
-        const int64_t place = part_place(p, h, j, b0 == 0);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            const float l = row_sum(R.l[r]);
-            if (16 * r >= rows) break;
-            __syncthreads();  // the blocks, or the tile before, have been read
-            if (g == 0) lds_m[wave][r16] = R.m[r] * p.scale2, lds_l[wave][r16] = l;
-#pragma unroll
-            for (int d = 0; d < 4 * KS; ++d) *reinterpret_cast<f32x4 *>(&lds_o[wave][r16][16 * d + 4 * g]) = R.o[r][d];
-            __syncthreads();
-            // 16 threads a row, each four columns of every 64
-            const int row = tid >> 4, c0 = 4 * (tid & 15);
-            if (16 * r + row < rows) {
-                float m = kNegInf;
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w) m = fmaxf(m, lds_m[w][row]);
-                float f[kWaves], sum = 0.0f;
-#pragma unroll
-                for (int w = 0; w < kWaves; ++w) {
-                    f[w] = weight(lds_m[w][row], m);
-                    sum += lds_l[w][row] == 0.0f ? 0.0f : f[w] * lds_l[w][row];
-                }
-                const float inv = whole ? (sum == 0.0f ? 0.0f : 1.0f / sum) : 1.0f;
-                float *po = p.part + (place * kRows + 16 * r + row) * p.dim;
-                uint16_t *o = out_row(p, q, h, row0 + 16 * r + row);
-#pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                    const int c = 64 * k + c0;
-                    if (c >= p.dim) break;
-                    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                    for (int w = 0; w < kWaves; ++w) v += *reinterpret_cast<const f32x4 *>(&lds_o[w][row][c]) * f[w];
-                    v *= inv;
-                    if (whole)
-                        *reinterpret_cast<uint2 *>(o + c) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
-                    else
-                        *reinterpret_cast<f32x4 *>(po + c) = v;
-                }
-                if (!whole && c0 == 0) {
-                    float *ml = p.part_ml + (place * kRows + 16 * r + row) * 2;
-                    ml[0] = m, ml[1] = sum;
-                }
-            }
-        }
+        join_waves<KS, RT>(p, q, h, row0, rows, R, b0 == 0 && b1 == (int)nb, part_place(p, h, j, b0 == 0) * kRows, lds, lds_ml);
         __syncthreads();  // LDS is free for the next piece
     }
 }
@@ -818,7 +846,7 @@ void split(const AttnArgs &p, int rt, hipStream_t st) {
 template <int KS, bool FULL>
 void rows(const AttnArgs &p, int rt, hipStream_t st) {
     const dim3 grid((unsigned)((int64_t)p.pieces * p.kv_heads), (unsigned)std::max(1, p.parts)), block(kAttnThreads);
-    constexpr size_t lds = 4 * 64 * 64 * KS * 2;
+    constexpr size_t lds = kRowsLds<KS>;
     if (rt == 1)
         hipLaunchKernelGGL((k_attn_rows<KS, 1, FULL>), grid, block, lds, st, p);
     else

@@ -298,6 +298,33 @@ def test_attention_of_prompts(lengths, new, heads, kv_heads, dim):
         check(o, want, err)
 
 
+# Prompts and single tokens in a call: pieces of few rows among those of many, whole and, where the prompts are few, in parts
+MIXED = [([2500, 800, 900, 0, 700, 1], [2200, 1, 3, 1, 600, 1], 16, 4, 128), ([1800, 640, 130], [700, 2, 1], 8, 1, 64),
+         ([500, 3000, 64], [300, 1, 1], 4, 2, 80), ([400, 1000], [300, 2], 3, 1, 256), ([700, 800, 900], [129, 65, 1], 2, 2, 192)]
+
+
+@pytest.mark.parametrize("lengths,new,heads,kv_heads,dim", MIXED)
+@pytest.mark.parametrize("width", [None, 200])
+def test_attention_of_prompts_and_single_tokens(lengths, new, heads, kv_heads, dim, width):
+    say(f"mixed {lengths} {new} {heads} {kv_heads} {dim} {width}")
+    table, pages = layout(6, lengths, width=width)
+    cache = nv.kv_cache(pages, kv_heads, dim)
+    fill(cache, 6)
+    sp = spans(lengths, new)
+    q = rand(3, sum(new), heads, dim)
+    args = (q, cache, table, ints(lengths), starts_of(sp))
+    for causal in (True, False):
+        o = nv.attention(*args, causal=causal)
+        want, err = dref.attention(q, cache, table, sp, dim ** -0.5, causal)
+        check(o, want, err)
+        assert torch.equal(nv.attention(*args, causal=causal), o)
+    u8(cache.v_scales)[int(table[1, 3 % (-(-lengths[1] // 64))]), 0] = 255
+    table[1, 0] = -1
+    want, err = dref.attention(q, cache, table, sp, dim ** -0.5, True)
+    assert torch.isnan(want).any() and not torch.isnan(want).all()
+    check(nv.attention(*args), want, err)
+
+
 # Some tens to hundreds of rows: rows over the waves with the blocks in parts, for each head size compiled for, 64 and 128
 # rows a work-group, tables far wider than the sequences
 PARTS = [([3000], [40], 4, 1, 128), ([2100, 65, 5000], [12, 9, 20], 8, 2, 64), ([1999], [300], 6, 3, 80), ([4444, 10], [33, 10], 3, 1, 256),
