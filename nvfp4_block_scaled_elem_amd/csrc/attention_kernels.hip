@@ -375,8 +375,9 @@ __device__ __forceinline__ void join_waves(const AttnArgs &p, const Seq &q, int6
 // Slot m of key tile t holds token 16 t + m; a lane then ends with the scores of the tokens 16 t + 4 g + j, and V's
 // operand u takes tokens 32 u + 4 g + j and 32 u + 16 + 4 g + j, j = 0..3, as k = 8 g .. + 7.
 //
-// A piece of at most 16 rows, as of a single token beside prompts, takes the way of few rows instead, its blocks over the
-// waves (a prompt of 2048 tokens and 16 single ones over 32000 each: 639 -> 211 us; with 63 over 8000: 318 -> 231).
+// A piece of at most 32 rows, as of a single token beside prompts, takes the way of few rows instead, 16 at a time with the
+// blocks over the waves (a prompt of 2048 tokens and 16 single ones over 32000 each: 639 -> 211 us, 16 of six tokens, 24 rows, 620 -> 399;
+// 63 single ones over 8000: 318 -> 231).
 template <int KS>
 constexpr int kRowsLds = 4 * 64 * 64 * KS * 2 > kBlocksLds<KS> ? 4 * 64 * 64 * KS * 2 : kBlocksLds<KS>;
 
@@ -401,10 +402,14 @@ __global__ __launch_bounds__(kAttnThreads, KS <= 2 ? 2 : 1) void k_attn_rows(Att
     const int reach = seen_by(p, q, first + in_piece - 1), all = (reach + kPage - 1) / kPage;
     const int start = (int)((int64_t)all * blockIdx.y / gridDim.y), count = (int)((int64_t)all * (blockIdx.y + 1) / gridDim.y);
     const int64_t part = ((h * p.pieces + piece) * gridDim.y + blockIdx.y) * kRows;
-    if (in_piece <= 16) {
-        Rows<KS, 1> F;
-        attend<KS, 1, FULL>(p, q, s, h, first, start + wave, count, kWaves, F, lds + wave * kWaveLds<KS>);
-        join_waves<KS, 1>(p, q, h, first, in_piece, F, gridDim.y == 1, part, lds, lds_ml);
+    if (in_piece <= 32) {
+#pragma unroll 1
+        for (int t = 0; t < in_piece; t += 16) {
+            Rows<KS, 1> F;
+            if (t) __syncthreads();  // the tile before has been read
+            attend<KS, 1, FULL>(p, q, s, h, first + t, start + wave, count, kWaves, F, lds + wave * kWaveLds<KS>);
+            join_waves<KS, 1>(p, q, h, first + t, min(16, in_piece - t), F, gridDim.y == 1, part + t, lds, lds_ml);
+        }
         return;
     }
     const int row0 = first + 16 * RT * wave, dim = FULL ? 64 * KS : p.dim;

@@ -299,7 +299,7 @@ def test_attention_of_prompts(lengths, new, heads, kv_heads, dim):
 
 
 # Prompts and single tokens in a call: pieces of few rows among those of many, whole and, where the prompts are few, in parts
-MIXED = [([2500, 800, 900, 0, 700, 1], [2200, 1, 3, 1, 600, 1], 16, 4, 128), ([1800, 640, 130], [700, 2, 1], 8, 1, 64),
+MIXED = [([2500, 800, 900, 0, 700, 1], [2200, 1, 3, 1, 600, 1], 16, 4, 128), ([1800, 640, 130], [700, 4, 1], 8, 1, 64),
          ([500, 3000, 64], [300, 1, 1], 4, 2, 80), ([400, 1000], [300, 2], 3, 1, 256), ([700, 800, 900], [129, 65, 1], 2, 2, 192)]
 
 
