@@ -17,6 +17,7 @@
 //   second product: k_moe_down, the weighted sum over the experts in it, to 16 tokens and little work; else k_moe_rows or
 //     k_moe_product, and k_moe_sum.
 #include <hip/hip_runtime.h>
+#include <math.h>
 #include <stdint.h>
 
 #include <algorithm>
@@ -35,7 +36,8 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kWaves = 8, kThreads = 64 * kWaves;
-constexpr int kRouteTokens = 8;  // to so many tokens are routed inside the first product
+// To so many tokens are routed inside the first product (12 tokens, 8 of 128 experts: the layer 76 us so, 68 with the kernel apart).
+constexpr int kRouteTokens = 8;
 constexpr float kLog2e = 1.4426950408889634f;
 
 // ------------------------------------------------------------------------------------------- routing
@@ -807,24 +809,27 @@ Plan plan_moe(int64_t tokens, int64_t width, int64_t inner, int experts, int top
     const double used = experts * (1.0 - idle);
     Plan plan = {};
     plan.mt = tokens > 16 && tokens * top_k > 12 * used ? 2 : 1;  // pairs of an expert
+    // Entries of the list: work-groups by column tiles (counted by experts alone: 256 tokens, 2 of 8 experts of 4096 x 1408 109 us,
+    // 77 so; 2 of 16 of 1024 x 512 41 and 27; 200 tokens, 4 of 16 of 2048 x 512 47 and 37).
+    const double lists = used * ceil(tokens * top_k / used / (16 * plan.mt));
     const int64_t up = (inner + (gated ? 63 : 127)) / (gated ? 64 : 128), down = (width + 127) / 128;
     // k_moe_rows where there are work-groups for most of the GPU. One token, 8 experts of 2048 x 768 (96 work-groups): the layer
     // 26 us with it, 20 without; 8 tokens, 35 experts of 4096 x 1408 (770): the first product 47 us, 65 without.
-    plan.up_rows = width >= kChunk && used * up >= 192;
+    plan.up_rows = width >= kChunk && lists * up >= 192;
     // The same for the second product; where k_moe_down does the sum as well, from more work on: the latter layer (1120
     // work-groups) 90 us, 102 with k_moe_down; the former (128) 21, 18 with it.
-    plan.down_rows = inner >= kChunk && used * down >= (tokens <= kDownTokens ? 512 : 128);
+    plan.down_rows = inner >= kChunk && lists * down >= (tokens <= kDownTokens ? 512 : 128);
     plan.route = tokens > kRouteTokens || (plan.up_rows && plan.mt == 2);
     plan.down_sum = tokens <= kDownTokens && !plan.down_rows;
     // Parts of the second product's sum, to some 500 work-groups: 33 tokens, 8 experts of 4096 x 14336: 188 us in two, 197 in four.
     plan.split = 1;
     if (plan.down_rows) {
         const int64_t slices = (inner + kSlice - 1) / kSlice;
-        while (plan.split < 8 && 4 * plan.split <= slices && used * down * plan.split < 500) plan.split *= 2;
+        while (plan.split < 8 && 4 * plan.split <= slices && lists * down * plan.split < 500) plan.split *= 2;
     }
     // Three work-groups a CU, where X stays.
-    plan.up_turns = width <= 2 * kSlice ? (int)std::max(1.0, used * up / 768.0 + 0.5) : 1;
-    plan.down_turns = inner <= 2 * kSlice ? (int)std::max(1.0, used * down / 768.0 + 0.5) : 1;
+    plan.up_turns = width <= 2 * kSlice ? (int)std::max(1.0, lists * up / 768.0 + 0.5) : 1;
+    plan.down_turns = inner <= 2 * kSlice ? (int)std::max(1.0, lists * down / 768.0 + 0.5) : 1;
     return plan;
 }
 

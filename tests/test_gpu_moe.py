@@ -62,12 +62,12 @@ def test_moe_matches_binary64(tokens, count, top_k, width, inner):
         check(y, want, err)
 
 
-# The forms of the kernel for many weight rows: routing inside it (5 and 8 tokens), X of two and of four slices held over
+# The forms of the kernel for many weight rows: routing inside it (5 and 8 tokens), X of two slices held over
 # column tiles, whole and with a short last slice, two tiles of pairs with a last one of either, the second product's sum in
 # parts; a last column tile that is not whole
 FORMS = [(5, 32, 4, 512, 1040), (8, 64, 6, 1040, 1408), (40, 64, 4, 2048, 1024), (40, 64, 4, 1040, 1040), (40, 64, 4, 2576, 784),
          (40, 64, 4, 1024, 2064), (100, 4, 2, 528, 3200), (70, 4, 2, 4112, 2064), (33, 8, 2, 4096, 2064), (40, 4, 1, 4096, 4112),
-         (17, 8, 2, 4096, 8208), (16, 8, 2, 4096, 2064)]
+         (17, 8, 2, 4096, 8208), (16, 8, 2, 4096, 2064), (256, 8, 2, 1040, 1408), (200, 16, 4, 528, 528), (100, 2, 2, 2064, 400)]
 
 
 @pytest.mark.parametrize("tokens,count,top_k,width,inner", FORMS)
@@ -81,6 +81,19 @@ def test_moe_of_many_rows(tokens, count, top_k, width, inner):
         y = nv.moe(x, logits, up, down, top_k, gated=gated, residual=r)
         want, err = dref.moe(x, logits, up, down, top_k, "silu", gated, False, True, r)
         check(y, want, err)
+
+
+@pytest.mark.parametrize("width,inner", [(1024, 528), (2064, 784)])
+def test_moe_of_uneven_choices(width, inner):
+    """Experts that all tokens choose, beside others that few or none do: entries of one expert in several work-groups."""
+    x, logits = rand(1, 150, width), rand(2, 150, 64, dtype=F32)
+    logits[:, 7] += 20.0
+    logits[40:, 63] += 15.0
+    logits[:, 20:40] -= 30.0
+    up, down = layer(9, 64, width, inner, True)
+    y = nv.moe(x, logits, up, down, 3, scoring="sigmoid")
+    want, err = dref.moe(x, logits, up, down, 3, "silu", True, True, True)
+    check(y, want, err)
 
 
 # more rows, wide sums, and weights as the quantiser writes them
