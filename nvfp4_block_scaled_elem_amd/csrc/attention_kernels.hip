@@ -864,8 +864,12 @@ AttnPlan plan_attention(int64_t tokens, int seqs, int width, int kv_heads, int g
     AttnPlan plan = {};
     const int64_t all = tokens * group, mean = seqs ? (all + seqs - 1) / seqs : 0;  // rows of a head; of a sequence
     // Rows over the waves from more than 32 rows of a sequence on: 16 sequences of 4000 tokens, 52 rows each: 48 us (blocks over
-    // the work-groups: 62); 30 sequences of 500 to 5000, 24 rows: 71 us (53).
-    if (mean > 32) {
+    // the work-groups: 62); 30 sequences of 500 to 5000, 24 rows: 71 us (53). And where tables are short, or not long with a
+    // work-group for each CU: a sequence is then done by one, and nothing is left to join. 8 heads of 128 on 32, one token of each of
+    //   16 sequences, tables of 16 blocks 13.2 us (blocks over the work-groups: 15.9), of 32 blocks 15.7 (15.6);
+    //   64 sequences, 16 blocks 16.6 (24.3), 64 blocks 34 (38), 128 blocks 57 (55); 256 sequences, 64 blocks 121 (131);
+    //   six tokens, 24 rows, of 64 sequences, 32 blocks 44.6 (43.4).
+    if (mean > 32 || width <= 16 || (width <= 64 && mean <= 16 && (int64_t)seqs * kv_heads >= 256)) {
         plan.rows = true;
         plan.rt = mean > 64 ? 2 : 1;
         plan.size = 64 * plan.rt;
@@ -873,7 +877,7 @@ AttnPlan plan_attention(int64_t tokens, int seqs, int width, int kv_heads, int g
         // Two work-groups a CU, the blocks in parts where the rows make fewer: 1024 rows over 8256 tokens in eight parts 58 us,
         // in one 190. But not less than 16 blocks a part: 4000 rows over 1000 tokens 31 us, in two parts 50.
         const int64_t groups = std::max<int64_t>(1, (all / plan.size + (seqs + 1) / 2) * kv_heads);
-        const int64_t parts = std::min<int64_t>({512 / groups, (width + 15) / 16, 64});
+        const int64_t parts = mean > 32 ? std::min<int64_t>({512 / groups, (width + 15) / 16, 64}) : 1;
         plan.parts = parts > 1 ? (int)parts : 0;
         if (plan.parts) {
             const int64_t rows = (int64_t)kv_heads * plan.pieces * plan.parts * plan.size;

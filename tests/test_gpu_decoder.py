@@ -233,8 +233,11 @@ def test_append_leaves_out_what_has_no_place():
 
 # ---------------------------------------------------------------------------------------- attention
 
-def ready(seed, lengths, heads, dim, extra=2):
-    table, pages = layout(seed, lengths, extra)
+SPLIT = 70  # blocks of a table that few rows take over several work-groups
+
+
+def ready(seed, lengths, heads, dim, extra=2, width=None):
+    table, pages = layout(seed, lengths, extra, width)
     cache = nv.kv_cache(pages, heads, dim)
     fill(cache, seed)
     return cache, table
@@ -260,9 +263,10 @@ ATTENTION = [
 
 @pytest.mark.parametrize("lengths,new,heads,kv_heads,dim", ATTENTION)
 @pytest.mark.parametrize("causal", [True, False])
-def test_attention_matches_binary64(lengths, new, heads, kv_heads, dim, causal):
-    say(f"attention {lengths} {new} {heads} {kv_heads} {dim} {causal}")
-    cache, table = ready(11, lengths, kv_heads, dim)
+@pytest.mark.parametrize("width", [None, SPLIT])
+def test_attention_matches_binary64(lengths, new, heads, kv_heads, dim, causal, width):
+    say(f"attention {lengths} {new} {heads} {kv_heads} {dim} {causal} {width}")
+    cache, table = ready(11, lengths, kv_heads, dim, width=width)
     sp = spans(lengths, new, first=1)
     rows = sum(new) + 3
     for std in (0.05, 2.0):  # even weights, and a few tokens that take all
@@ -360,10 +364,11 @@ def test_attention_in_parts(lengths, new, heads, kv_heads, dim):
 # Tiles that end inside a work-group's share, and shares of several tiles: few and many sequences
 @pytest.mark.parametrize("seqs", [2, 5, 16, 33, 64, 65, 300])
 def test_attention_shares(seqs):
+    """Few rows of sequences of very different lengths, over tables that take them so."""
     lengths = [1 + (i * 977) % 2900 for i in range(seqs)]
     new = [1 + (i * 5) % 4 for i in range(seqs)]
     lengths = [max(a, b) for a, b in zip(lengths, new)]
-    cache, table = ready(8, lengths, 1, 64)
+    cache, table = ready(8, lengths, 1, 64, width=SPLIT)
     sp = spans(lengths, new)
     q = rand(3, sum(new), 7, 64)
     o = nv.attention(q, cache, table, ints(lengths), starts_of(sp))
@@ -397,10 +402,11 @@ def test_attention_of_wide_tables(lengths, new, heads, kv_heads, dim):
     check(nv.attention(*args), want, err)
 
 
-def test_attention_of_many_sequences():
+@pytest.mark.parametrize("width", [None, SPLIT])
+def test_attention_of_many_sequences(width):
     """More sequences than a wave has lanes, of very different lengths."""
     lengths = [(i * 37) % 150 for i in range(200)] + [3000]
-    cache, table = ready(9, lengths, 2, 32)
+    cache, table = ready(9, lengths, 2, 32, width=width)
     q = rand(1, len(lengths), 4, 32)
     o = nv.attention(q, cache, table, ints(lengths))
     want, err = dref.attention(q, cache, table, spans(lengths, [1] * len(lengths)), 32 ** -0.5, True)
@@ -409,17 +415,18 @@ def test_attention_of_many_sequences():
     lengths = [max(a, b) for a, b in zip(lengths, new)]
     sp = spans(lengths, new)
     q = rand(2, sum(new), 4, 32)
-    cache, table = ready(10, lengths, 2, 32)
+    cache, table = ready(10, lengths, 2, 32, width=width)
     o = nv.attention(q, cache, table, ints(lengths), starts_of(sp))
     want, err = dref.attention(q, cache, table, sp, 32 ** -0.5, True)
     check(o, want, err)
 
 
 @pytest.mark.parametrize("new", [1, 30, 900])
-def test_attention_does_not_look_behind_the_end(new):
+@pytest.mark.parametrize("width", [None, SPLIT])
+def test_attention_does_not_look_behind_the_end(new, width):
     """Bytes behind a sequence's end, and pages of no sequence, may be NaN."""
     lengths, heads, dim = [1000 - 11], 8, 128
-    cache, table = ready(2, lengths, 8, dim)
+    cache, table = ready(2, lengths, 8, dim, width=width)
     sp = spans(lengths, [new])
     q = rand(3, new, 16, dim)
     args = (q, cache, table, ints(lengths), starts_of(sp))
@@ -435,10 +442,11 @@ def test_attention_does_not_look_behind_the_end(new):
 
 
 @pytest.mark.parametrize("heads,new", [(8, [1, 1]), (8, [20, 9]), (16, [700, 700])])
-def test_attention_of_blocks_of_nan(heads, new):
+@pytest.mark.parametrize("width", [None, SPLIT])
+def test_attention_of_blocks_of_nan(heads, new, width):
     """Rows that see a block of NaN are NaN, the others are what they are without it."""
     lengths, dim = [777, 700], 128
-    cache, table = ready(2, lengths, 8, dim)
+    cache, table = ready(2, lengths, 8, dim, width=width)
     u8(cache.k_scales)[int(table[0, 11]), 1] = 255
     u8(cache.k)[int(table[0, 11]), 1] = 0x7F
     u8(cache.v_scales)[int(table[1, 10]), 0] = 255  # its last block
@@ -451,8 +459,9 @@ def test_attention_of_blocks_of_nan(heads, new):
     check(o, want, err)
 
 
-def test_attention_of_queries_that_are_not_finite():
-    cache, table = ready(2, [200, 200], 1, 64)
+@pytest.mark.parametrize("width", [None, SPLIT])
+def test_attention_of_queries_that_are_not_finite(width):
+    cache, table = ready(2, [200, 200], 1, 64, width=width)
     q = rand(3, 2, 4, 64)
     clean = nv.attention(q, cache, table, ints([200, 200]))
     q[1, 2, 5] = float("nan")
@@ -463,9 +472,10 @@ def test_attention_of_queries_that_are_not_finite():
 
 
 @pytest.mark.parametrize("new", [1, 5, 600])
-def test_attention_of_sequences_without_tokens(new):
+@pytest.mark.parametrize("width", [None, SPLIT])
+def test_attention_of_sequences_without_tokens(new, width):
     """Lengths of zero, more new tokens than tokens, pages outside the cache, tables of nothing: zeros, or what is there."""
-    cache, table = ready(2, [640, 640], 8, 128)
+    cache, table = ready(2, [640, 640], 8, 128, width=width)
     q = rand(3, 2 * new, 16, 128)
     starts = ints([0, new, 2 * new])
     assert (nv.attention(q, cache, table, ints([0, -3]), starts) == 0).all()
@@ -478,8 +488,14 @@ def test_attention_of_sequences_without_tokens(new):
         o = nv.attention(q, cache, t, ints([640, 3]), starts)
         want, err = dref.attention(q, cache, t, sp, 128 ** -0.5, True)
         check(o, want, err)
-    long = nv.attention(q, cache, table, ints([1 << 30, 640]), starts, causal=False)  # counts as what the table holds
-    assert torch.equal(long, nv.attention(q, cache, table, ints([640, 640]), starts, causal=False))
+    # counts as what the table holds, pages outside the cache left out
+    long = nv.attention(q, cache, table, ints([1 << 30, 640]), starts, causal=False)
+    whole = nv.attention(q, cache, table, ints([640, 640]), starts, causal=False)
+    if width is None:
+        assert torch.equal(long, whole)
+    else:  # (other shares, another order of its sums: twice what one order's bound allows, and roundings of the same value)
+        _, err = dref.attention(q, cache, table, spans([640, 640], [new, new]), 128 ** -0.5, False)
+        assert ((long.double() - whole.double()).abs() <= 2 * err + 2 * whole.double().abs() * 2.0 ** -8).all()
 
 
 def test_attention_is_reproducible_and_takes_a_workspace():
@@ -519,11 +535,12 @@ def test_attention_with_large_offsets():
 
 # -------------------------------------------------------------------------------------------- together
 
-def test_stream_and_graph():
+@pytest.mark.parametrize("width", [None, SPLIT])
+def test_stream_and_graph(width):
     """The three calls on a stream of their own, and captured and replayed as a decoding step with growing lengths."""
     heads, kv_heads, dim, seqs = 8, 2, 64, 3
     lengths = [60, 126, 0]
-    table, pages = layout(1, [400] * seqs)
+    table, pages = layout(1, [400] * seqs, width=width)
     caches = [nv.kv_cache(pages, kv_heads, dim) for _ in range(2)]
     for c in caches:
         fill(c, 5)
