@@ -102,8 +102,11 @@ def test_attention_rejects(L):
                dict(out=FAKE + 8), dict(ws=FAKE + 16)):
         assert call(**kw) == INVALID, kw
     assert call(tokens=(1 << 23) + 1) == SHAPE and call(heads=65536) == SHAPE and call(tokens=0) == OK
-    need = L.nvfp4_attention_workspace_bytes(9, 4, 8, 4, 2, 64)
-    assert need > 0 and call(n=need - 1) == WORKSPACE
+    need = L.nvfp4_attention_workspace_bytes(9, 4, 80, 4, 2, 64)
+    long = decoder._Sequences(table=FAKE, ldt=80, lengths=FAKE, starts=FAKE, seqs=4, width=80)
+    assert need > 0
+    assert L.nvfp4_attention(cache, ctypes.byref(long), FAKE, 256, 64, 4, 9, 1.0, 1, FAKE, FAKE, need - 1, None) == WORKSPACE
+    assert L.nvfp4_attention_workspace_bytes(9, 4, 8, 4, 2, 64) == 0  # a short table: no parts
     assert L.nvfp4_attention_workspace_bytes(0, 4, 8, 4, 2, 64) == 0
     assert L.nvfp4_attention_workspace_bytes(9, 4, 8, 3, 2, 64) == 0  # no such call
     assert L.nvfp4_attention_workspace_bytes(9, 4, 8, 4, 2, 24) == 0
