@@ -557,8 +557,8 @@ def test_stream_and_graph(width):
 
     work = qkv.clone()
     side = torch.cuda.Stream()
-    side.wait_stream(torch.cuda.current_stream())
     lens += 1
+    side.wait_stream(torch.cuda.current_stream())  # for the lengths too
     step(work, caches[0], side)
     torch.cuda.current_stream().wait_stream(side)
     work.copy_(qkv)
