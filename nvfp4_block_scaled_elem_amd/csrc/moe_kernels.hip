@@ -454,6 +454,7 @@ __global__ __launch_bounds__(kDownThreads) void k_moe_down(MoeArgs p) {
         u32x4 c, h[4], l[4];
         u32x2 s;
         float w;
+        int choice;
     };
     auto load = [&](Item &it, int i) __attribute__((always_inline)) {
         const int e = __builtin_amdgcn_readfirstlane((int)chosen[i / nch]), ch = i % nch;
@@ -477,7 +478,7 @@ __global__ __launch_bounds__(kDownThreads) void k_moe_down(MoeArgs p) {
                     if (ks + 16 * b < K) it.s[b >> 2] |= (uint32_t)s[b] << (8 * (b & 3));
             }
         }
-        const int j = choice[e][r16];
+        const int j = it.choice = choice[e][r16];
         it.w = 0.0f;
 #pragma unroll
         for (int k = 0; k < 4; ++k) it.h[k] = it.l[k] = u32x4{0u, 0u, 0u, 0u};
@@ -509,9 +510,9 @@ __global__ __launch_bounds__(kDownThreads) void k_moe_down(MoeArgs p) {
             acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, it.h[k]), acc, 0, 0, 0);
             acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, __builtin_bit_cast(bf16x8, it.l[k]), acc, 0, 0, 0);
         }
-        // a token that did not choose the expert has zeros: its NaN or infinite weights of others stay out
+        // a token that did not choose the expert has zeros, and NaN where the expert's scales are NaN: not taken
 #pragma unroll
-        for (int k = 0; k < 4; ++k) total[k] = __builtin_fmaf(acc[k], it.w, total[k]);
+        for (int k = 0; k < 4; ++k) total[k] = it.choice ? __builtin_fmaf(acc[k], it.w, total[k]) : total[k];
     };
     Item a, b;
     int i = lo;
