@@ -668,6 +668,7 @@ __global__ __launch_bounds__(kRowThreads, 2) void k_moe_rows(MoeArgs p, int tile
         };
         // Slice s of the loaded codes with the X at xb, and the loads of slice `next` (of the rows taken last).
         auto multiply = [&](int s, int next, const uint8_t *xb) __attribute__((always_inline)) {
+            wave_handover();  // the slice before's scales have been read (where X is held no barrier lies between)
             store_scales(s);
             load_scales(next);
 #pragma unroll
