@@ -502,8 +502,9 @@ int nvfp4_kv_append(const nvfp4_kv_cache_t *cache, const nvfp4_sequences_t *seqs
  *   out = sum_t softmax_t(scale * q . k_t) v_t
  * over the tokens t that a row sees: with causal = 1 row i of a sequence's n rows sees its first length - n + i + 1
  * tokens, with causal = 0 all `length`. A row that sees none gives zeros; one that sees a token of a block with scale byte
- * 255 gives NaN. Products with q are exact, sums fp32, probabilities are rounded to bf16 before they are multiplied with
- * the values. Values of the cache below 2^-126 may count as zero. 1e-30 < |scale| < 1e30;
+ * 255, or any token where its q holds a NaN or an infinity, gives NaN. Products with q are exact, sums fp32, probabilities
+ * are rounded to bf16 before they are multiplied with the values. Values of the cache below 2^-126 may count as zero.
+ * 1e-30 < |scale| < 1e30, and scale * q . k has to stay below 2^126 in magnitude (it is held in fp32);
  * tokens * (heads / kv_heads)^2 < 2^32. Scratch: nvfp4_attention_workspace_bytes. */
 int nvfp4_attention(const nvfp4_kv_cache_t *cache, const nvfp4_sequences_t *seqs, const void *q, int64_t q_token,
                     int64_t q_head, int heads, int64_t tokens, float scale, int causal, void *out, void *workspace,

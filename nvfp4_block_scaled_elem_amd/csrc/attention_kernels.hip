@@ -115,6 +115,10 @@ __device__ __forceinline__ void take_rows(const AttnArgs &p, const Seq &q, int64
             u32x4 v = {0u, 0u, 0u, 0u};
             if (in && (FULL || c < p.dim)) v = *reinterpret_cast<const u32x4_any *>(x + c);
             v ^= p.flip;  // a negative scale: -q, exact
+            // An infinity is read as NaN (exponent of ones: the carry sets the quiet bit). The row is NaN either way where it sees
+            // a token, but scores that are all -inf could not be told from masked ones, which give zeros.
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] |= (((v[i] & 0x7F807F80u) + 0x00800080u) & 0x80008000u) >> 9;
             Q[r][k] = __builtin_bit_cast(bf16x8, v);
         }
         R.m[r] = kNegInf, R.l[r] = 0.0f;

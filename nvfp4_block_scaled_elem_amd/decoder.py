@@ -230,8 +230,8 @@ def attention(Q: torch.Tensor, cache, table: torch.Tensor, lengths: torch.Tensor
     """Attention of ``Q`` ([tokens, heads, dim] bf16; heads a multiple of the cache's) over the cache: softmax(scale * Q
     K^T) V over the tokens that a row sees, [tokens, heads, dim] bf16, in ``out`` if given (contiguous). ``causal``: row i of
     a sequence's n sees its first length - n + i + 1 tokens; else all of them (the cached states of an encoder). ``scale``
-    None: dim^-0.5. A row that sees no token gives zeros; one that sees a block written with a NaN or an infinity
-    gives NaN. Prompts and single tokens may come in one call."""
+    None: dim^-0.5. A row that sees no token gives zeros; one that sees a block written with a NaN or an infinity, or
+    any token where its query holds one, gives NaN. Prompts and single tokens may come in one call."""
     qt, qh = _heads(Q, "Q", (torch.bfloat16,))
     dev = Q.device
     c, kv_heads, dim = _cache(cache, dev)

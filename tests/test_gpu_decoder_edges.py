@@ -5,7 +5,9 @@ import torch
 
 import nvfp4_block_scaled_elem_amd as nv
 from tests import decoder_ref as dref
+from tests import test_gpu_decoder as dec
 from tests import test_gpu_moe as moe_of
+from tests.test_gpu_decoder import SPLIT, ints, rand, spans, starts_of, u8
 
 pytestmark = pytest.mark.gpu
 
@@ -14,6 +16,40 @@ BF16, F32 = torch.bfloat16, torch.float32
 
 def say(msg):
     print(msg, flush=True)
+
+
+# ----------------------------------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("dim", [64, 80])
+@pytest.mark.parametrize("new", [[1, 1], [5, 3], [20, 9], [600, 90]])
+@pytest.mark.parametrize("width", [None, SPLIT])
+def test_queries_of_infinities(dim, new, width):
+    """softmax of scores that are all -inf is NaN, as of any with +inf among them: a row with an infinite query is NaN where it sees
+    a token, zeros where it sees none, and the other rows are what they are without it, bit for bit."""
+    say(f"infinite queries {dim} {new} {width}")
+    lengths = [700, 90]
+    cache, table = dec.ready(12, lengths, 2, dim, width=width)
+    u8(cache.k)[:, :, :, 3] = 0x38  # all keys' column 3 is positive
+    q = rand(3, sum(new), 8, dim)
+    args = (cache, table, ints(lengths), starts_of(spans(lengths, new)))
+    for causal in (True, False):
+        clean = nv.attention(q, *args, causal=causal)
+        bad = q.clone()
+        rows = [(0, 1, -1.0), (sum(new) - 1, 6, -1.0), (new[0] - 1, 7, 1.0), (sum(new) // 2, 2, -1.0)]
+        for row, head, sign in rows:
+            bad[row, head, 3] = sign * float("inf")
+        o = nv.attention(bad, *args, causal=causal)
+        for row, head, _ in rows:
+            assert torch.isnan(o[row, head]).all(), (row, head)
+            o[row, head] = clean[row, head]
+        assert torch.equal(o, clean)
+    # rows that see none: no pages, no tokens, more new tokens than tokens
+    nowhere = torch.full_like(table, -1)
+    assert (nv.attention(bad, cache, nowhere, *args[2:]) == 0).all()
+    assert (nv.attention(bad, cache, table, ints([0, 0]), args[3]) == 0).all()
+    if new[0] > 1:
+        o = nv.attention(bad, cache, table, ints([new[0] - 1, new[1] - 1]), args[3])
+        assert (o[0] == 0).all() and (o[new[0]] == 0).all()
 
 
 # ------------------------------------------------------------------------------------------- experts
