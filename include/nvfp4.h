@@ -475,8 +475,8 @@ int nvfp4_rotary(const nvfp4_rotary_args_t *args);
  * least) with max|x| <= 448 * scale over the block's new tokens, and not below the scale it has where it holds
  * earlier tokens of the sequence (slots in front of the new ones): their codes are then rounded to the new scale, which is
  * exact for codes that stay at or above 2^-6 in magnitude. Codes are the nearest, ties to even. Slots behind the
- * sequence's end stay as they are. A NaN or an infinity in a block gives scale byte 255 and codes 0x7F: all its tokens read
- * as NaN, until a sequence begins in the block anew. */
+ * sequence's end stay as they are. A NaN or an infinity in a block, or a magnitude from 248 * 2^120 on (whose nearest code is
+ * worth 2^128), gives scale byte 255 and codes 0x7F: all its tokens read as NaN, until a sequence begins in the block anew. */
 typedef struct nvfp4_kv_cache {
     uint8_t *k_codes, *v_codes;
     uint8_t *k_scales, *v_scales;
@@ -503,7 +503,8 @@ int nvfp4_kv_append(const nvfp4_kv_cache_t *cache, const nvfp4_sequences_t *seqs
  * over the tokens t that a row sees: with causal = 1 row i of a sequence's n rows sees its first length - n + i + 1
  * tokens, with causal = 0 all `length`. A row that sees none gives zeros; one that sees a token of a block with scale byte
  * 255, or any token where its q holds a NaN or an infinity, gives NaN. Products with q are exact, sums fp32, probabilities
- * are rounded to bf16 before they are multiplied with the values. Values of the cache below 2^-126 may count as zero.
+ * are rounded to bf16 before they are multiplied with the values. Values of the cache below 2^-126 may count as zero, and
+ * sums are held of up to 2^8 times the values: length * |v| has to stay below 2^119.
  * 1e-30 < |scale| < 1e30, and scale * q . k has to stay below 2^126 in magnitude (it is held in fp32);
  * tokens * (heads / kv_heads)^2 < 2^32. Scratch: nvfp4_attention_workspace_bytes. */
 int nvfp4_attention(const nvfp4_kv_cache_t *cache, const nvfp4_sequences_t *seqs, const void *q, int64_t q_token,

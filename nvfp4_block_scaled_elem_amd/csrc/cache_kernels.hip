@@ -139,10 +139,13 @@ __global__ __launch_bounds__(kThreads) void k_rotary(RotaryArgs p) {
 //       earlier tokens, whose codes are then rounded to the new scale (exact but below 2^-6 of it);
 //   codes = E4M3(x / 2^e), nearest, ties to even. Slots behind the sequence's end stay as they are.
 // A NaN or an infinity gives the block scale byte 255 and codes 0x7F (all its tokens read as NaN), which it keeps until
-// a new sequence begins in it.
+// a new sequence begins in it. So does a magnitude from kBeyond = 248 * 2^120 on: the nearest code is 256 * 2^120 = 2^128, an infinity
+// in binary32 and bf16, whose products with the zero probabilities of rows that do not see its token would be NaN.
 //
 // Bound by x, read once (a thread keeps its values between the maximum and the codes), and, for single tokens, by the chain
 // of loads length -> page -> scale.
+constexpr uint32_t kBeyond = 0x7F780000u;
+
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs p) {
     constexpr int kMost = kPage / 4 * kMaxHeadDim / 8 / kThreads;  // pieces, four slots of 8 columns, of a thread
@@ -198,7 +201,7 @@ __global__ __launch_bounds__(kThreads) void k_kv_append(AppendArgs p) {
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kThreads / 64; ++w) top = max(top, red[w]);
-    const uint32_t sb = max(old, mx_scale_byte(top));
+    const uint32_t sb = top >= kBeyond ? 255u : max(old, mx_scale_byte(top));
     if (tid == 0) *scale = (uint8_t)sb;  // every thread has read `old` before the barrier
 
     if (slot0 && sb > old) {  // the earlier tokens' codes to the larger scale

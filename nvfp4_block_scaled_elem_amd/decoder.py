@@ -201,7 +201,8 @@ def kv_append(cache, K: torch.Tensor, V: torch.Tensor, table: torch.Tensor, leng
     """Writes the keys and values ``K`` and ``V`` ([tokens, kv_heads, dim], bf16 or fp32) of the sequences' last tokens
     into the cache, and returns it. Per block of 64 tokens and head the scale is the smallest power of two under which
     nothing saturates; where a block already holds tokens of the sequence it does not fall, and their codes are
-    rounded to the new one if it grows."""
+    rounded to the new one if it grows. A NaN, an infinity or a magnitude of 248 * 2^120 and more makes its block one of
+    NaNs."""
     kt, kh = _heads(K, "K", DTYPES)
     dev = K.device
     vt, vh = _heads(V, "V", (K.dtype,), dev, K.shape)

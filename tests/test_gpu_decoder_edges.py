@@ -52,6 +52,55 @@ def test_queries_of_infinities(dim, new, width):
         assert (o[0] == 0).all() and (o[new[0]] == 0).all()
 
 
+# ------------------------------------------------------------------------------------------- the cache
+
+def bits(pattern):
+    return torch.tensor(pattern, dtype=torch.int32).view(F32).item()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("which", [0, 1])
+def test_append_of_the_largest_values(dtype, which):
+    """248 * 2^120 is half way between the codes of 240 and 256 at scale 2^120 and goes to 256 * 2^120 = 2^128, which is no binary32 number: from
+    there on a value makes its block one of NaNs as an infinity does, below it is held."""
+    table, pages = dec.layout(3, [130])
+    below = [bits(0x7F770000)] if dtype == BF16 else [bits(0x7F770000), bits(0x7F77FFFF)]  # 247 * 2^120, and the last below 248
+    beyond = [bits(0x7F780000), bits(0x7F7F0000)] + ([] if dtype == BF16 else [bits(0x7F7FFFFF)])  # 248 and 255 * 2^120, the last
+    for value in below + [-v for v in below] + beyond + [-v for v in beyond]:
+        cache = nv.kv_cache(pages, 2, 32)
+        x = [rand(i, 130, 2, 32, dtype=dtype) for i in (1, 2)]
+        x[which][70, 1, 9] = value
+        nv.kv_append(cache, *x, table, ints([130]), ints([0, 130]))
+        page = int(table[0, 1])
+        byte, codes = u8(cache[2 + which])[page], u8(cache[which])[page, 1]
+        assert byte[0] != 255 and all((u8(s)[int(table[0, b])] != 255).all() for s in cache[2:] for b in (0, 2))
+        if abs(value) < bits(0x7F780000):
+            at = codes[6, 9] if which == 0 else codes[9, 6]
+            assert byte[1] == 247 and at == (0x77 if value > 0 else 0xF7)  # 240 * 2^120
+        else:
+            assert byte[1] == 255 and (codes == 0x7F).all()
+
+
+@pytest.mark.parametrize("new,behind", [(6, 3), (20, 10), (100, 60)])
+@pytest.mark.parametrize("width", [None, SPLIT])
+def test_rows_that_do_not_see_the_largest_values(new, behind, width):
+    """Rows whose tokens end in front of a block with such a value are what they are without it, beside rows that see it."""
+    heads, dim, length = 2, 64, 64 + behind
+    table, pages = dec.layout(3, [length], width=width)
+    q = rand(5, new, 4, dim)
+    out = []
+    for value in (1.0, bits(0x7F7F0000)):
+        cache = nv.kv_cache(pages, heads, dim)
+        K, V = rand(1, length, heads, dim), rand(2, length, heads, dim)
+        V[-1, 1, 9] = value
+        nv.kv_append(cache, K, V, table, ints([length]), ints([0, length]))
+        out.append(nv.attention(q, cache, table, ints([length]), ints([0, new])))
+    apart = new - behind  # row i sees length - new + i + 1 tokens: these at most 64
+    assert torch.equal(out[0][:apart], out[1][:apart])
+    assert torch.equal(out[0][:, :2], out[1][:, :2])  # the other key head's
+    assert torch.isnan(out[1][apart:, 2:]).all()
+
+
 # ------------------------------------------------------------------------------------------- experts
 
 @pytest.mark.parametrize("tokens", [2, 3, 8, 9, 16, 17, 40])
