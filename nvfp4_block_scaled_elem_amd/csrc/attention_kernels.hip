@@ -785,9 +785,12 @@ __global__ __launch_bounds__(kAttnThreads) void k_attn_join(AttnArgs p, int size
     int parts = p.parts, apart = 1;  // of k_attn_rows: all tiles alike, side by side
     int64_t at = (h * p.pieces + piece) * p.parts;
     if (parts == 0) {
+        // Starts that run backwards give sequences the same rows, and a list that may pass 32 bits: a place in it is then past its
+        // end, or nothing is left of it, and there are no such parts. (k_attn_split takes places below the end alone.)
+        if (sh.total == 0u) return;
         const uint32_t u0 = w.begin(s) + (uint32_t)tile * sh.padded(nb);
         const uint32_t j0 = sh.owner(u0), j1 = sh.owner(u0 + nb - 1);
-        if (j0 == j1) return;
+        if (j0 >= j1 || j1 >= sh.groups) return;
         parts = (int)(j1 - j0 + 1), apart = 2;
         at = part_place(p, h, j0, false);
     }

@@ -52,6 +52,30 @@ def test_queries_of_infinities(dim, new, width):
         assert (o[0] == 0).all() and (o[new[0]] == 0).all()
 
 
+@pytest.mark.parametrize("last", [64, 0])
+def test_starts_that_run_backwards(last):
+    """Starts that give many sequences the same rows: the blocks of all tiles are 2^32 and a few (or 2^32, which is none to 32
+    bits). What the rows get is open, but nothing beside the output is written, and the next call is right."""
+    say(f"starts that run backwards {last}")
+    seqs, tokens, width, heads, dim = 1026, 1024, 8192, 16, 16
+    cache = nv.kv_cache(4, 1, dim)
+    dec.fill(cache, 1)
+    table = torch.zeros(seqs, width, dtype=torch.int32, device="cuda")
+    lengths = [width * 64] * 1024 + [last, 0]
+    starts = [0 if i % 2 == 0 else tokens for i in range(seqs)] + [0]
+    need = nv.attention_workspace_bytes(tokens, seqs, width, heads, 1, dim)
+    ws = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    out = torch.full((tokens + 64, heads, dim), 7.0, dtype=BF16, device="cuda")
+    q = rand(2, tokens, heads, dim)
+    nv.attention(q, cache, table, ints(lengths), ints(starts), workspace=ws[:need], out=out[32:-32])
+    torch.cuda.synchronize()
+    assert (ws[need:] == 0xA5).all() and (out[:32] == 7.0).all() and (out[-32:] == 7.0).all()
+    table, lengths, q = table[:100, :SPLIT], [1 + 7 * i % 130 for i in range(100)], q[:100]
+    o = nv.attention(q, cache, table, ints(lengths))
+    want, err = dref.attention(q, cache, table, spans(lengths, [1] * 100), dim ** -0.5, True)
+    dec.check(o, want, err)
+
+
 # ------------------------------------------------------------------------------------------- the cache
 
 def bits(pattern):
