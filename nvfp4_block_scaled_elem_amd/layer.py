@@ -132,9 +132,10 @@ def _no_graph(*operands):
     if torch.is_grad_enabled():
         for t in operands:
             if t is not None and t.requires_grad:
-                raise NVFP4Error("the layer operators record no autograd graph: call them under torch.no_grad() or in a "
-                                 "torch.autograd.Function, with detached operands, and their gradients by rms_norm_grad "
-                                 "and linear_grad")
+                raise NVFP4Error("the layer and decoder operators record no autograd graph: call them under torch.no_grad() or "
+                                 "in a torch.autograd.Function, with detached operands. The gradients that there are, are "
+                                 "calls of their own: rms_norm_grad, linear_grad, and rotary with inverse=True; attention, "
+                                 "kv_append and moe have none")
 
 
 def _ptr(t):
