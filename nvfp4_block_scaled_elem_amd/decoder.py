@@ -165,8 +165,8 @@ def _cache(cache, dev):
             and ks.dtype in _SCALES and vs.dtype in _SCALES and k.is_contiguous() and v.is_contiguous() and ks.is_contiguous()
             and vs.is_contiguous()):
         raise NVFP4Error(f"the cache's codes must be contiguous E4M3 and its scales contiguous E8M0 tensors on {dev}")
-    if k.dim() != 4 or k.shape[2] != PAGE:
-        raise NVFP4Error(f"the cache's k must be [pages, kv_heads, {PAGE}, dim]")
+    if k.dim() != 4 or k.shape[2] != PAGE or not k.shape[1]:
+        raise NVFP4Error(f"the cache's k must be [pages, kv_heads, {PAGE}, dim] of at least one head")
     pages, heads, _, dim = k.shape
     if v.shape != (pages, heads, dim, PAGE) or ks.shape != (pages, heads) or vs.shape != (pages, heads):
         raise NVFP4Error(f"the cache's v must be {[pages, heads, dim, PAGE]} and its scales {[pages, heads]}")

@@ -125,6 +125,17 @@ def test_rows_that_do_not_see_the_largest_values(new, behind, width):
     assert torch.isnan(out[1][apart:, 2:]).all()
 
 
+def test_a_cache_without_heads_is_refused():
+    cache = (torch.zeros(2, 0, 64, 16, dtype=torch.uint8, device="cuda"), torch.zeros(2, 0, 16, 64, dtype=torch.uint8, device="cuda"),
+             torch.zeros(2, 0, dtype=torch.uint8, device="cuda"), torch.zeros(2, 0, dtype=torch.uint8, device="cuda"))
+    table, lengths = ints([[0]]), ints([1])
+    for heads in (0, 2):
+        with pytest.raises(nv.NVFP4Error):
+            nv.attention(rand(1, 1, heads, 16), cache, table, lengths)
+    with pytest.raises(nv.NVFP4Error):
+        nv.kv_append(cache, rand(1, 1, 0, 16), rand(1, 1, 0, 16), table, lengths)
+
+
 # ------------------------------------------------------------------------------------------- experts
 
 @pytest.mark.parametrize("tokens", [2, 3, 8, 9, 16, 17, 40])
