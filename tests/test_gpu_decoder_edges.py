@@ -52,6 +52,137 @@ def test_queries_of_infinities(dim, new, width):
         assert (o[0] == 0).all() and (o[new[0]] == 0).all()
 
 
+def held(lengths, new, heads, kv_heads, dim, width=None, bad=()):
+    """Attention of such sequences against binary64, causal and not, twice the same, and with blocks (sequence, block, key head) of
+    NaN in keys or values or, without a head, missing."""
+    table, pages = dec.layout(6, lengths, width=width)
+    cache = nv.kv_cache(pages, kv_heads, dim)
+    dec.fill(cache, 6)
+    sp = spans(lengths, new)
+    q = rand(3, sum(new), heads, dim)
+    args = (q, cache, table, ints(lengths), starts_of(sp))
+    for causal in (True, False):
+        o = nv.attention(*args, causal=causal)
+        dec.check(o, *dref.attention(q, cache, table, sp, dim ** -0.5, causal))
+        assert torch.equal(nv.attention(*args, causal=causal), o)
+    if all(n == 1 for n in new):
+        assert torch.equal(nv.attention(*args[:4]), nv.attention(*args))
+    for i, (s, block, head) in enumerate(bad):
+        if head is None:
+            table[s, block] = -1 if i % 2 else 1 << 30
+        else:
+            u8(cache[2 + i % 2])[int(table[s, block]), head] = 255
+    if bad:
+        want, err = dref.attention(q, cache, table, sp, dim ** -0.5, True)
+        assert torch.isnan(want).any()
+        dec.check(nv.attention(*args), want, err)
+
+
+# Tiles in more than 16, 64 and 256 parts, joined by a work-group or by a wave; shares of more than 256 blocks (a wave looks its pages up
+# more than once), with a work-group for each CU instead of two, padded to whole shares (two sequences) and not (five)
+FAR = [
+    ([8000], [1], 4, 1, 64, None, [(0, 101, None), (0, 120, 0)]),
+    ([20011], [2], 7, 1, 32, None, [(0, 250, None), (0, 301, 0)]),
+    ([80003], [1], 2, 1, 16, None, [(0, 700, None), (0, 1249, 0)]),
+    ([80003] + [30 + i for i in range(79)], [1] * 80, 3, 1, 16, None, [(0, 800, None), (0, 1100, 0), (40, 0, 0)]),
+    ([40000, 39001], [1, 1], 128, 64, 16, None, [(0, 290, None), (1, 600, None), (0, 300, 5), (1, 607, 63)]),
+    ([20000, 19000, 21000, 64, 18001], [1, 3, 1, 2, 1], 64, 64, 16, None, [(2, 3, None), (0, 312, 7), (4, 280, None), (2, 310, 9)]),
+    ([30000, 35000, 31, 33333], [6, 5, 3, 2], 192, 32, 32, None, [(1, 400, None), (3, 333, 31), (0, 111, 4)]),
+]
+
+
+@pytest.mark.parametrize("lengths,new,heads,kv_heads,dim,width,bad", FAR, ids=[f"{len(c[0])}x{c[0][0]}-{c[3]}x{c[4]}" for c in FAR])
+def test_attention_far(lengths, new, heads, kv_heads, dim, width, bad):
+    say(f"far {lengths[:5]} {new[:5]} {heads} {kv_heads} {dim}")
+    held(lengths, new, heads, kv_heads, dim, width, bad)
+
+
+# A single token over more than 256 blocks beside a prompt, in the kernel of many rows
+@pytest.mark.parametrize("lengths,new,heads,kv_heads,dim,width", [([500, 20000], [300, 1], 4, 1, 64, None), ([30001, 700], [2, 600], 6, 2, 128, None),
+                                                                  ([17000, 90, 400], [1, 1, 400], 2, 1, 256, 300)])
+def test_attention_far_beside_prompts(lengths, new, heads, kv_heads, dim, width):
+    say(f"far beside prompts {lengths} {new} {heads} {kv_heads} {dim}")
+    far = lengths.index(max(lengths))
+    held(lengths, new, heads, kv_heads, dim, width, [(far, 257, None), (1 - far if far < 2 else 0, 1, 0), (far, 260, kv_heads - 1)])
+
+
+# Chunks of hundreds of rows beside so many single tokens that the call goes by blocks: many tiles of a sequence among the shares, of 16
+# rows and, over wide tables, of 32
+@pytest.mark.parametrize("chunk,singles,heads,kv_heads,dim,width", [
+    (200, 40, 4, 1, 64, SPLIT), (200, 40, 4, 1, 64, 200), (301, 90, 7, 1, 80, 100), (512, 128, 4, 1, 128, 170), (100, 70, 8, 4, 256, SPLIT),
+    (250, 30, 6, 2, 192, SPLIT), (64, 70, 16, 1, 48, 100)])
+def test_attention_of_chunks_among_single_tokens(chunk, singles, heads, kv_heads, dim, width):
+    say(f"chunks {chunk} {singles} {heads} {kv_heads} {dim} {width}")
+    lengths = [20 + 61 * i % 1500 for i in range(singles)]
+    new = [1] * singles
+    lengths[singles // 2:singles // 2], new[singles // 2:singles // 2] = [chunk + 190], [chunk]
+    rows = -(-sum(new) * heads // kv_heads // len(new))
+    assert 4 < rows <= 32 and width > 64
+    held(lengths, new, heads, kv_heads, dim, width, [(singles // 2, 3, 0), (3, 1, None), (singles // 2, 1, None), (singles, 0, kv_heads - 1)])
+
+
+@pytest.mark.parametrize("lengths,new", [([900, 70, 3000], [1, 1, 1]), ([700, 64, 300], [300, 64, 2]), ([4000, 3000], [30, 50])])
+def test_attention_on_a_stream_of_its_own(lengths, new):
+    """Rotary positions, cache and attention on a stream, each result compared; scratch of the call's own and the caller's."""
+    heads, kv_heads, dim = 8, 2, 64
+    table, pages = dec.layout(1, lengths, width=SPLIT)
+    sp = spans(lengths, new)
+    qkv, pos = rand(1, sum(new), heads + 2 * kv_heads, dim), torch.arange(sum(new), device="cuda")
+    caches = [nv.kv_cache(pages, kv_heads, dim) for _ in range(2)]
+    for c in caches:
+        dec.fill(c, 5)
+    ws = torch.empty(nv.attention_workspace_bytes(sum(new), len(new), SPLIT, heads, kv_heads, dim), dtype=torch.uint8, device="cuda")
+    lens, starts = ints(lengths), starts_of(sp)
+
+    def step(cache, stream, workspace):
+        x = nv.rotary(qkv, pos, sections=(16,), stream=stream)
+        nv.kv_append(cache, x[:, heads:heads + kv_heads], x[:, heads + kv_heads:], table, lens, starts, stream=stream)
+        return x, nv.attention(x[:, :heads], cache, table, lens, starts, workspace=workspace, stream=stream)
+
+    x, o = step(caches[0], None, None)
+    want, err = dref.attention(x[:, :heads], caches[0], table, sp, dim ** -0.5, True)
+    dec.check(o, want, err)
+    side = torch.cuda.Stream()
+    for workspace in (None, ws):
+        dec.fill(caches[1], 5)
+        side.wait_stream(torch.cuda.current_stream())
+        on_side = step(caches[1], side, workspace)
+        side.synchronize()
+        assert torch.equal(on_side[0], x) and torch.equal(on_side[1], o)
+        assert all(torch.equal(u8(a), u8(b)) for a, b in zip(*caches))
+        with torch.cuda.stream(side):  # the current stream
+            again = step(caches[1], None, workspace)
+        side.synchronize()
+        assert torch.equal(again[0], x) and torch.equal(again[1], o)
+
+
+@pytest.mark.parametrize("lengths,new", [([3000, 20, 700], [1, 1, 1]), ([4000, 3000], [30, 50])])
+def test_two_graphs_share_a_workspace(lengths, new):
+    """Attention captured twice over one workspace, replayed in turn with other queries, lengths and pages."""
+    heads, kv_heads, dim, width = 8, 2, 128, SPLIT
+    cache, table = dec.ready(4, lengths, kv_heads, dim, width=width)
+    q, lens, starts = rand(1, sum(new), heads, dim), ints(lengths), starts_of(spans(lengths, new))
+    ws = torch.empty(nv.attention_workspace_bytes(sum(new), len(new), width, heads, kv_heads, dim), dtype=torch.uint8, device="cuda")
+    assert ws.numel() > 0
+    tables, outs = [table.clone(), table.flip(1).contiguous()], [torch.empty_like(q) for _ in range(2)]
+    nv.attention(q, cache, table, lens, starts, workspace=ws, out=outs[0])
+    torch.cuda.synchronize()
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for graph, t, o in zip(graphs, tables, outs):
+        with torch.cuda.graph(graph):
+            nv.attention(q, cache, t, lens, starts, workspace=ws, out=o)
+    for i in range(4):
+        q.copy_(rand(30 + i, *q.shape))
+        lens.add_(-7)
+        for graph, t, o in zip(graphs, tables, outs):
+            want = nv.attention(q, cache, t, lens, starts)
+            graph.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(o, want)
+            torch.randn(1000, device="cuda").sum().item()
+        assert not torch.equal(*outs)
+
+
 @pytest.mark.parametrize("last", [64, 0])
 def test_starts_that_run_backwards(last):
     """Starts that give many sequences the same rows: the blocks of all tiles are 2^32 and a few (or 2^32, which is none to 32
@@ -137,6 +268,24 @@ def test_a_cache_without_heads_is_refused():
 
 
 # ------------------------------------------------------------------------------------------- experts
+
+# More than 2048 pairs, which the kernel of many rows lists in several loads of its ids, to the most that there may be; experts that most
+# tokens choose beside others of few; one tile of pairs an expert and two, X held and not
+@pytest.mark.parametrize("tokens,count,top_k,width,inner", [(600, 16, 8, 256, 256), (1024, 16, 8, 128, 1040), (2047, 8, 4, 1040, 144),
+                                                            (8192, 64, 1, 256, 128), (260, 512, 31, 128, 128)])
+def test_moe_of_many_pairs(tokens, count, top_k, width, inner):
+    say(f"many pairs {tokens} {count} {top_k} {width} {inner}")
+    x, logits, r = moe_of.rand(1, tokens, width), moe_of.rand(2, tokens, count, dtype=F32), moe_of.rand(3, tokens, width)
+    logits[:, 1] += 4.0
+    logits[:, count // 2] -= 4.0
+    logits[tokens // 2] = -moe_of.INF
+    for gated in (True, False):
+        up, down = moe_of.layer(7, count, width, inner, gated)
+        y = nv.moe(x, logits, up, down, top_k, gated=gated, scoring="sigmoid", residual=r)
+        want, err = dref.moe(x, logits, up, down, top_k, "silu", gated, True, True, r)
+        moe_of.check(y, want, err)
+        assert torch.equal(nv.moe(x, logits, up, down, top_k, gated=gated, scoring="sigmoid", residual=r), y)
+
 
 @pytest.mark.parametrize("tokens", [2, 3, 8, 9, 16, 17, 40])
 @pytest.mark.parametrize("which", ["up", "down"])
