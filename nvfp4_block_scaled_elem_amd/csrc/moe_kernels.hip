@@ -821,7 +821,7 @@ Plan plan_moe(int64_t tokens, int64_t width, int64_t inner, int experts, int top
     // The same for the second product; where k_moe_down does the sum as well, from more work on: the latter layer (1120
     // work-groups) 90 us, 102 with k_moe_down; the former (128) 21, 18 with it.
     plan.down_rows = inner >= kChunk && lists * down >= (tokens <= kDownTokens ? 512 : 128);
-    plan.route = tokens > kRouteTokens || (plan.up_rows && plan.mt == 2);
+    plan.route = tokens > kRouteTokens;
     plan.down_sum = tokens <= kDownTokens && !plan.down_rows;
     // Parts of the second product's sum, to some 500 work-groups: 33 tokens, 8 experts of 4096 x 14336: 188 us in two, 197 in four.
     plan.split = 1;
