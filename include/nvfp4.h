@@ -498,7 +498,8 @@ int nvfp4_kv_append(const nvfp4_kv_cache_t *cache, const nvfp4_sequences_t *seqs
                     void *stream);
 
 /* Attention of q [tokens][heads][dim] (bf16, its strides; heads a multiple of kv_heads, head i on key/value head i /
- * (heads / kv_heads)) over the cache: out [tokens][heads][dim] bf16, contiguous,
+ * (heads / kv_heads)) over the cache: out [tokens][heads][dim] bf16, contiguous (it may be q itself, and may not overlap it
+ * otherwise),
  *   out = sum_t softmax_t(scale * q . k_t) v_t
  * over the tokens t that a row sees: with causal = 1 row i of a sequence's n rows sees its first length - n + i + 1
  * tokens, with causal = 0 all `length`. A row that sees none gives zeros; one that sees a token of a block with scale byte
@@ -522,7 +523,7 @@ size_t nvfp4_attention_workspace_bytes(int64_t tokens, int seqs, int width, int 
  * A NaN among a token's logits is chosen first and makes NaN of its y. x [tokens][width] bf16; logits [tokens][experts] bf16
  * or fp32 with `ldl`; up: the experts' [inner, or gated 2 inner][width] weights one after the other, as the quantiser writes
  * them (codes, scales, and one alpha per expert); down: [width][inner]; residual (nullable) as y, with `ldr`, may be y
- * itself (contiguous). width, inner % 16 == 0 and <= 2^21, experts <= 512, top_k <= min(32, experts), tokens * top_k <= 8192,
+ * itself (contiguous) and may not overlap it otherwise. width, inner % 16 == 0 and <= 2^21, experts <= 512, top_k <= min(32, experts), tokens * top_k <= 8192,
  * ldx, ldl, ldr < 2^31, an expert's weights below 2^31 values (else NVFP4_ERR_SHAPE). Codes 8-byte aligned. No expert's
  * weights are read that no token chose. Scratch: nvfp4_moe_workspace_bytes. */
 enum nvfp4_scoring { NVFP4_SCORE_SOFTMAX = 0, NVFP4_SCORE_SIGMOID = 1 };

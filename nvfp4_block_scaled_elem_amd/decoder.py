@@ -98,13 +98,28 @@ def _heads(t, name, dtypes, dev=None, shape=None):
     return st, sh
 
 
+def _apart(out, t, name):
+    """Refuses a contiguous output that shares memory with an operand of its shape and is not the operand itself: rows would be
+    read after others were written over them."""
+    a, b, size = t.data_ptr(), out.data_ptr(), t.element_size()
+    span = 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    if a >= b + out.numel() * size or b >= a + span * size or not out.numel() or (a == b and t.is_contiguous()):
+        return
+    begin = torch.zeros((), dtype=torch.int64)  # of each row, from the operand's first
+    for n, s in zip(t.shape[:-1], t.stride()[:-1]):
+        begin = begin[..., None] + s * torch.arange(n)
+    begin = a + begin * size
+    if ((begin < b + out.numel() * size) & (begin + t.shape[-1] * size > b)).any():
+        raise NVFP4Error(f"out may be {name} itself (contiguous), but may not share memory with it otherwise")
+
+
 def rotary(x: torch.Tensor, positions: torch.Tensor, *, sections=None, base: float = 10000.0, inverse: bool = False,
            out=None, stream=None) -> torch.Tensor:
     """Rotary positions of ``x`` ([tokens, heads, dim] bf16 or fp32): with R = 2 * sum(sections) <= dim, columns j and j +
     R/2 are turned by the angle positions[axis(j)] * base^(-2j/R), columns from R on pass. ``positions`` is [tokens] or
     [axes, tokens] (up to four axes) int32 or int64, contiguous; ``sections`` the number of consecutive pairs of each axis
     (None: one axis, all dim // 2 pairs). Angles are binary64, so far positions lose nothing. ``inverse`` turns back:
-    the gradient. Returns y, in ``out`` if given: x itself (in place), or a contiguous tensor."""
+    the gradient. Returns y, in ``out`` if given: x itself (in place), or a contiguous tensor apart from it."""
     xs, xh = _heads(x, "x", DTYPES)
     tokens, heads, dim = x.shape
     dev = x.device
@@ -130,6 +145,8 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, *, sections=None, base: flo
                 raise NVFP4Error("in place, the rows of x may not overlap")
         elif not out.is_contiguous():
             raise NVFP4Error("out must be contiguous or x itself")
+        else:
+            _apart(out, x, "x")
     _no_graph(x, out)
 
     def call(st):
@@ -229,8 +246,8 @@ def attention_workspace_bytes(tokens: int, seqs: int, width: int, heads: int, kv
 def attention(Q: torch.Tensor, cache, table: torch.Tensor, lengths: torch.Tensor, starts=None, *, scale=None,
               causal: bool = True, out=None, workspace=None, stream=None) -> torch.Tensor:
     """Attention of ``Q`` ([tokens, heads, dim] bf16; heads a multiple of the cache's) over the cache: softmax(scale * Q
-    K^T) V over the tokens that a row sees, [tokens, heads, dim] bf16, in ``out`` if given (contiguous). ``causal``: row i of
-    a sequence's n sees its first length - n + i + 1 tokens; else all of them (the cached states of an encoder). ``scale``
+    K^T) V over the tokens that a row sees, [tokens, heads, dim] bf16, in ``out`` if given (contiguous; it may be Q). ``causal``: row i
+    of a sequence's n sees its first length - n + i + 1 tokens; else all of them (the cached states of an encoder). ``scale``
     None: dim^-0.5. A row that sees no token gives zeros; one that sees a block written with a NaN or an infinity, or
     any token where its query holds one, gives NaN. Prompts and single tokens may come in one call."""
     qt, qh = _heads(Q, "Q", (torch.bfloat16,))
@@ -243,6 +260,8 @@ def attention(Q: torch.Tensor, cache, table: torch.Tensor, lengths: torch.Tensor
     if out is not None and (not isinstance(out, torch.Tensor) or out.shape != Q.shape or out.dtype != torch.bfloat16
                             or out.device != dev or not out.is_contiguous()):
         raise NVFP4Error(f"out must be a contiguous {list(Q.shape)} bf16 tensor on {dev}")
+    if out is not None:
+        _apart(out, Q, "Q")
     _no_graph(Q, out)
 
     def call(st):
@@ -326,6 +345,8 @@ def moe(X: torch.Tensor, logits: torch.Tensor, up, down, top_k: int, *, activati
     _experts(down, "down", experts, dev, width, inner)
     ldr = 0 if residual is None else _rows(residual, "residual", (torch.bfloat16,), dev, (tokens, width))
     _output(out, "out", (tokens, width), torch.bfloat16, dev)
+    if out is not None and residual is not None:
+        _apart(out, residual, "the residual")
     _no_graph(X, logits, up[2], down[2], residual, out)
 
     def call(st):

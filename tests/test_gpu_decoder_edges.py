@@ -256,6 +256,49 @@ def test_rows_that_do_not_see_the_largest_values(new, behind, width):
     assert torch.isnan(out[1][apart:, 2:]).all()
 
 
+def test_outputs_that_share_memory_with_an_operand():
+    """The operand itself is fine, and so is memory between its rows; anything else is refused."""
+    E = nv.NVFP4Error
+    buf = rand(1, 12 * 40 * 64)
+    at = lambda first, tokens, heads, stride: buf[first:first + 40 * 64 * 4].as_strided((tokens, heads, 64), (stride, 64, 1))  # noqa: E731
+    x, pos = at(64, 5, 8, 40 * 64), torch.arange(5, device="cuda")
+    for first in (0, 64 + 8, 64 + 2 * 40 * 64, 64 + 7 * 64, 64 + 4 * 40 * 64 + 7 * 64 + 63):
+        with pytest.raises(E):
+            nv.rotary(x, pos, out=buf[first:first + 5 * 8 * 64].view(5, 8, 64))
+    small = at(0, 2, 4, 40 * 64)
+    between = buf[4 * 64:4 * 64 + 2 * 4 * 64].view(2, 4, 64)  # behind the first row's heads, in front of the second's
+    y = nv.rotary(small, pos[:2])
+    assert torch.equal(nv.rotary(small, pos[:2], out=between), y)
+    want = nv.rotary(x, pos)
+    assert torch.equal(nv.rotary(x, pos, out=x), want)
+    # attention: in place over each of its kernels; the first heads of a wider product are not a contiguous output
+    for lengths, new, width in (([900, 70], [1, 1], SPLIT), ([900, 70], [1, 1], None), ([900, 70], [20, 9], SPLIT), ([2000, 300], [600, 300], None),
+                                ([5000, 64], [40, 30], 160)):
+        cache, table = dec.ready(2, lengths, 2, 64, width=width)
+        args = (cache, table, ints(lengths), starts_of(spans(lengths, new)))
+        wide = rand(3, sum(new), 12, 64)
+        q = wide[:, :8].contiguous()
+        o = nv.attention(q, *args)
+        with pytest.raises(E):
+            nv.attention(wide[:, :8], *args, out=wide.view(-1)[:q.numel()].view(q.shape))
+        assert torch.equal(nv.attention(q, *args, out=q), o) and torch.equal(q, o)
+    one = wide[:1, :8]  # a single row is the same memory whatever its stride
+    o = nv.attention(one, cache, table[:1], ints([64]))
+    assert torch.equal(nv.attention(one, cache, table[:1], ints([64]), out=wide.view(-1)[:512].view(1, 8, 64)), o)
+    # experts: the residual, and the inputs
+    up, down = moe_of.layer(1, 8, 64, 32, True)
+    for tokens in (4, 40):
+        both, logits = moe_of.rand(3, 2 * tokens, 64), moe_of.rand(2, tokens, 8, dtype=F32)
+        x = moe_of.rand(1, tokens, 64)
+        for residual, out in ((both[::2], both[:tokens]), (both[1:tokens + 1], both[:tokens]), (both[:tokens], both[1:tokens + 1])):
+            with pytest.raises(E):
+                nv.moe(x, logits, up, down, 2, residual=residual, out=out)
+        y = nv.moe(x, logits, up, down, 2, residual=both[:tokens])
+        assert torch.equal(nv.moe(x, logits, up, down, 2, residual=both[:tokens], out=both[:tokens]), y)
+        y = nv.moe(x, logits, up, down, 2)
+        assert torch.equal(nv.moe(x, logits, up, down, 2, out=x), y)
+
+
 def test_a_cache_without_heads_is_refused():
     cache = (torch.zeros(2, 0, 64, 16, dtype=torch.uint8, device="cuda"), torch.zeros(2, 0, 16, 64, dtype=torch.uint8, device="cuda"),
              torch.zeros(2, 0, dtype=torch.uint8, device="cuda"), torch.zeros(2, 0, dtype=torch.uint8, device="cuda"))
