@@ -523,9 +523,9 @@ size_t nvfp4_attention_workspace_bytes(int64_t tokens, int seqs, int width, int 
  * A NaN among a token's logits is chosen first and makes NaN of its y. x [tokens][width] bf16; logits [tokens][experts] bf16
  * or fp32 with `ldl`; up: the experts' [inner, or gated 2 inner][width] weights one after the other, as the quantiser writes
  * them (codes, scales, and one alpha per expert); down: [width][inner]; residual (nullable) as y, with `ldr`, may be y
- * itself (contiguous) and may not overlap it otherwise. width, inner % 16 == 0 and <= 2^21, experts <= 512, top_k <= min(32, experts), tokens * top_k <= 8192,
- * ldx, ldl, ldr < 2^31, an expert's weights below 2^31 values (else NVFP4_ERR_SHAPE). Codes 8-byte aligned. No expert's
- * weights are read that no token chose. Scratch: nvfp4_moe_workspace_bytes. */
+ * itself (contiguous) and may not overlap it otherwise. width, inner % 16 == 0 and <= 2^21, experts <= 512, top_k <=
+ * min(32, experts), tokens * top_k <= 8192, ldx, ldl, ldr < 2^31, an expert's weights below 2^31 values (else
+ * NVFP4_ERR_SHAPE). Codes 8-byte aligned. No expert's weights are read that no token chose. Scratch: nvfp4_moe_workspace_bytes. */
 enum nvfp4_scoring { NVFP4_SCORE_SOFTMAX = 0, NVFP4_SCORE_SIGMOID = 1 };
 typedef struct nvfp4_moe_args {
     const void *x;

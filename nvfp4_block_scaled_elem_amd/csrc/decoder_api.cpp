@@ -4,7 +4,7 @@
 // Kernels per call (all on the caller's stream):
 //   nvfp4_rotary    : k_rotary
 //   nvfp4_kv_append : k_kv_append
-//   nvfp4_attention : k_attn_rows, or k_attn_split -> k_attn_join
+//   nvfp4_attention : k_attn_rows [-> k_attn_join, where the blocks go in parts], or k_attn_split -> k_attn_join
 //   nvfp4_moe       : [k_moe_route ->] k_moe_product or k_moe_rows (up) -> k_moe_down, or k_moe_product or k_moe_rows (down)
 //                     -> k_moe_sum
 #include <hip/hip_runtime.h>

@@ -118,8 +118,9 @@ def rotary(x: torch.Tensor, positions: torch.Tensor, *, sections=None, base: flo
     """Rotary positions of ``x`` ([tokens, heads, dim] bf16 or fp32): with R = 2 * sum(sections) <= dim, columns j and j +
     R/2 are turned by the angle positions[axis(j)] * base^(-2j/R), columns from R on pass. ``positions`` is [tokens] or
     [axes, tokens] (up to four axes) int32 or int64, contiguous; ``sections`` the number of consecutive pairs of each axis
-    (None: one axis, all dim // 2 pairs). Angles are binary64, so far positions lose nothing. ``inverse`` turns back:
-    the gradient. Returns y, in ``out`` if given: x itself (in place), or a contiguous tensor apart from it."""
+    (None: one axis, all dim // 2 pairs). Angles are binary64, off by some 2^-51 of themselves: below what binary32
+    holds of a turn for positions to 2^27. ``inverse`` turns back: the gradient. Returns y, in ``out`` if given: x itself (in
+    place), or a contiguous tensor apart from it."""
     xs, xh = _heads(x, "x", DTYPES)
     tokens, heads, dim = x.shape
     dev = x.device
