@@ -55,8 +55,8 @@ using Held = typename std::conditional<sizeof(T) == 2, Held16, Held32>::type;
 // t = pos[axis of j] base^(-2j/R); columns from R on pass. Bound by x and y (16 bytes a thread each way).
 //
 // The angle is formed in binary64, in turns: base^(-2j/R) = 2^(j c) with c = c_hi + c_lo, j c_hi exact, so that
-// it is within a few 2^-53 of its value, below binary32's step of a turn's fraction for angles to 2^27; a whole number of turns is dropped exactly, and what is left, at most half
-// a turn, goes to the sine and cosine in binary32.
+// it is within a few 2^-53 of its value, which for angles to 2^27 is below binary32's step of a turn's fraction; a whole
+// number of turns is dropped exactly, and what is left, at most half a turn, goes to the sine and cosine in binary32.
 //
 // A work-group takes p.per tokens and a share of the heads: its threads compute the tokens' sines and cosines once,
 // into LDS, while the first rows are on their way, and turn the heads with them.

@@ -105,9 +105,9 @@ def _apart(out, t, name):
     span = 1 + sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
     if a >= b + out.numel() * size or b >= a + span * size or not out.numel() or (a == b and t.is_contiguous()):
         return
-    begin = torch.zeros((), dtype=torch.int64)  # of each row, from the operand's first
+    begin = torch.zeros((), dtype=torch.int64, device="cpu")  # of each row, from the operand's first
     for n, s in zip(t.shape[:-1], t.stride()[:-1]):
-        begin = begin[..., None] + s * torch.arange(n)
+        begin = begin[..., None] + s * torch.arange(n, device="cpu")
     begin = a + begin * size
     if ((begin < b + out.numel() * size) & (begin + t.shape[-1] * size > b)).any():
         raise NVFP4Error(f"out may be {name} itself (contiguous), but may not share memory with it otherwise")
@@ -247,9 +247,9 @@ def attention_workspace_bytes(tokens: int, seqs: int, width: int, heads: int, kv
 def attention(Q: torch.Tensor, cache, table: torch.Tensor, lengths: torch.Tensor, starts=None, *, scale=None,
               causal: bool = True, out=None, workspace=None, stream=None) -> torch.Tensor:
     """Attention of ``Q`` ([tokens, heads, dim] bf16; heads a multiple of the cache's) over the cache: softmax(scale * Q
-    K^T) V over the tokens that a row sees, [tokens, heads, dim] bf16, in ``out`` if given (contiguous; it may be Q). ``causal``: row i
-    of a sequence's n sees its first length - n + i + 1 tokens; else all of them (the cached states of an encoder). ``scale``
-    None: dim^-0.5. A row that sees no token gives zeros; one that sees a block written with a NaN or an infinity, or
+    K^T) V over the tokens that a row sees, [tokens, heads, dim] bf16, in ``out`` if given (contiguous; it may be Q).
+    ``causal``: row i of a sequence's n sees its first length - n + i + 1 tokens; else all of them (the cached states of an
+    encoder). ``scale`` None: dim^-0.5. A row that sees no token gives zeros; one that sees a block written with a NaN or an infinity, or
     any token where its query holds one, gives NaN. Prompts and single tokens may come in one call."""
     qt, qh = _heads(Q, "Q", (torch.bfloat16,))
     dev = Q.device
